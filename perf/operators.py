@@ -296,7 +296,7 @@ def run(s):
     if op == "gemv":
         return bpw.q4_gemm(s["handle"], s["x"], s["out"])
     if op == "experts":
-        return bpw.moe_experts(*s["handles"], s["x"], s["weights"], s["offsets"], s["slots"], s["out"])
+        return bpw.moe_experts(*s["handles"], s["x"], s["ids"], s["weights"], s["offsets"], s["slots"], s["out"])
     if op == "route":
         bpw.moe_route(s["logits"], s["ids"], s["weights"], s["offsets"], s["slots"], bias=s["bias"],
                       score=c["score"], groups=c["groups"], top_groups=c["top_groups"], renorm=c["renorm"],
