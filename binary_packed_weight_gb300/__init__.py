@@ -15,6 +15,7 @@ import os
 __all__ = [
     "load", "lib_path", "TQ2Error", "Weight", "tq2_upload", "tq2_gemm", "tq2_gemm_path", "tq2_gemm_tensor_tuned",
     "tq2_gemm_skinny_static", "tq2_gemm_grouped", "GroupedGemv", "tq2_unpack", "tq2_dequant_f16", "tq2_quantize", "blr_expand_bits", "blr_forward", "blr_backward", "blr_forward_paths", "blr_backward_paths", "blr_sign_grads",
+    "Q4Weight", "q4_upload", "q4_dequant", "q4_quantize", "q4_gemm", "moe_route", "moe_route_backward", "moe_experts",
     "device_status", "debug_wait_timeout", "PATH_AUTO", "PATH_SKINNY", "PATH_TENSOR",
 ]
 
@@ -48,6 +49,15 @@ _SIGS = {
     "blr_forward_paths": (_I, [_P, _I, _P, _P, _I64, _I64, _I64, _I64, _P]),
     "blr_backward_paths": (_I, [_P, _I, _P, _P, _P, _I64, _I64, _I64, _I64, _F, _P]),
     "blr_sign_grads": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _F, _P]),
+    "q4_upload": (_I, [_P, _P, _P, _I64, _I64, _I64, _I, ctypes.POINTER(_P), _P]),
+    "q4_free": (_I, [_P]),
+    "q4_shape": (_I, [_P, ctypes.POINTER(_I64), ctypes.POINTER(_I64), ctypes.POINTER(_I64), ctypes.POINTER(_I)]),
+    "q4_dequant": (_I, [_P, _P, _P]),
+    "q4_quantize": (_I, [_P, _I, _I64, _I64, _I, _P, _P, _P, _P]),
+    "q4_gemm": (_I, [_P, _P, _I64, _P, _I64, _I, _I64, _P]),
+    "moe_route": (_I, [_P, _I64, _I, _P, _I64, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P]),
+    "moe_route_backward": (_I, [_P, _I64, _I, _P, _P, _P, _P, _I64, _I64, _I, _I, _I, _I, _F, _P]),
+    "moe_experts": (_I, [_P, _P, _P, _P, _I64, _I, _P, _P, _P, _P, _P, _I64, _I64, _I, _P]),
 }
 
 
@@ -265,6 +275,198 @@ def blr_sign_grads(bits_u, h, l, g, x, dy, a_save, gu, gv, gscale=1.0, stream=No
     _check(load().blr_sign_grads(_ptr(bits_u), _ptr(h), _ptr(l), _ptr(g), _ptr(x), _ptr(dy), _ptr(a_save), _ptr(gu),
                                  _ptr(gv), T, d_in, d_out, r, float(gscale), _stream(stream)), "blr_sign_grads")
     return gu, gv
+
+
+class Q4Weight:
+    """E 4-bit matrices [N, K] with group scales resident on the GPU (owns a C handle)."""
+
+    def __init__(self, handle, E, N, K, group):
+        self._h, self.E, self.N, self.K, self.group = handle, E, N, K, group
+
+    @property
+    def handle(self):
+        return self._h
+
+    def free(self):
+        if self._h:
+            _check(load().q4_free(self._h), "q4_free")
+            self._h = None
+
+    def __del__(self):
+        try:
+            if self._h and _lib is not None:
+                _lib.q4_free(self._h)
+        except Exception:
+            pass
+
+
+_dtypes = {}
+
+
+def _dtype(t, where):
+    """tq2_dtype of a tensor."""
+    if not _dtypes:
+        import torch
+        _dtypes.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    try:
+        return _dtypes[t.dtype]
+    except KeyError:
+        raise TypeError(f"{where}: dtype {t.dtype} is not float32, float16 or bfloat16") from None
+
+
+def _rows(t, rows, cols, where, name):
+    """Row stride of a [rows, cols] tensor whose rows are contiguous."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{where}: {name} must be [{rows}, {cols}], got {list(t.shape)}")
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{where}: the rows of {name} must be contiguous")
+    return ld if rows > 1 and cols > 1 else max(ld, cols)
+
+
+def _plane(t, shape, dtype, where, name):
+    """A dense tensor of a given shape and dtype (a torch dtype's name)."""
+    if tuple(t.shape) != shape or not t.is_contiguous() or str(t.dtype) != dtype:
+        raise ValueError(f"{where}: {name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
+_raw_stream = None
+
+
+def _on(t, stream):
+    """The stream of a call on tensor ``t``: the given one or torch's current one of its device."""
+    if stream is not None:
+        return int(stream)
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = torch._C._cuda_getCurrentRawStream
+    return _raw_stream(t.get_device())
+
+
+def q4_upload(codes, scales, zeros=None, group=128, stream=None):
+    """4-bit weights -> :class:`Q4Weight`.  ``codes`` uint8 [E, N, K/2] or [N, K/2] (even k in the low
+    half byte), ``scales`` float16 and ``zeros`` uint8 (or None: 8) [.., N, K/group]; CPU or CUDA tensors."""
+    shape = tuple(codes.shape) if codes.dim() == 3 else (1,) + tuple(codes.shape)
+    if len(shape) != 3:
+        raise ValueError(f"q4_upload: codes must be [E, N, K/2] or [N, K/2], got {list(codes.shape)}")
+    E, N, K = shape[0], shape[1], 2 * shape[2]
+    lead = tuple(codes.shape)[:-1]
+    _plane(codes, lead + (K // 2,), "torch.uint8", "q4_upload", "codes")
+    _plane(scales, lead + (K // group,), "torch.float16", "q4_upload", "scales")
+    if zeros is not None:
+        _plane(zeros, lead + (K // group,), "torch.uint8", "q4_upload", "zeros")
+    h = ctypes.c_void_p()
+    _check(load().q4_upload(_ptr(codes), _ptr(scales), _ptr(zeros), E, N, K, group, ctypes.byref(h),
+                            _stream(stream)), "q4_upload")
+    return Q4Weight(h.value, E, N, K, group)
+
+
+def q4_dequant(w, out, stream=None):
+    """W as float32 [E, N, K] (exact)."""
+    if out.numel() != w.E * w.N * w.K or not out.is_contiguous() or str(out.dtype) != "torch.float32":
+        raise ValueError(f"q4_dequant: out must be contiguous float32 of {w.E}*{w.N}*{w.K} elements")
+    _check(load().q4_dequant(w.handle, _ptr(out), _stream(stream)), "q4_dequant")
+    return out
+
+
+def q4_quantize(w, codes, scales, zeros=None, group=128, stream=None):
+    """Plain weights [.., N, K] to the planes :func:`q4_upload` takes (see include/tq2.h)."""
+    K = w.shape[-1]
+    lead = tuple(w.shape)[:-1]
+    if not w.is_contiguous():
+        raise ValueError("q4_quantize: w must be contiguous")
+    _plane(codes, lead + (K // 2,), "torch.uint8", "q4_quantize", "codes")
+    _plane(scales, lead + (K // group,), "torch.float16", "q4_quantize", "scales")
+    if zeros is not None:
+        _plane(zeros, lead + (K // group,), "torch.uint8", "q4_quantize", "zeros")
+    _check(load().q4_quantize(_ptr(w), _dtype(w, "q4_quantize"), w.numel() // max(K, 1), K, group, _ptr(codes),
+                              _ptr(scales), _ptr(zeros), _stream(stream)), "q4_quantize")
+    return codes, scales, zeros
+
+
+def q4_gemm(w, x, out, stream=None):
+    """out [M, N] = x [M, K] @ W^T for a weight with one matrix; rows may be strided."""
+    M = x.shape[0]
+    ldx = _rows(x, M, w.K, "q4_gemm", "x")
+    ldo = _rows(out, M, w.N, "q4_gemm", "out")
+    if out.dtype != x.dtype:
+        raise TypeError("q4_gemm: x and out must have the same dtype")
+    _check(load().q4_gemm(w.handle, x.data_ptr(), ldx, out.data_ptr(), ldo, _dtype(x, "q4_gemm"), M,
+                          _on(x, stream)), "q4_gemm")
+    return out
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _score(score, where):
+    try:
+        return _SCORES[score]
+    except KeyError:
+        raise ValueError(f"{where}: score must be one of {sorted(_SCORES)}, got {score!r}") from None
+
+
+def moe_route(logits, ids, weights, offsets=None, slots=None, bias=None, score="softmax", groups=1, top_groups=1,
+              renorm=True, scale=1.0, stream=None):
+    """Selection, weights and plan of a router (see include/tq2.h): ``logits`` [T, E] -> ``ids`` int32 and
+    ``weights`` float32 [T, k], and unless None ``offsets`` int32 [E+1], ``slots`` int32 [T*k]."""
+    T, E = logits.shape
+    k = ids.shape[1]
+    ld = _rows(logits, T, E, "moe_route", "logits")
+    _plane(ids, (T, k), "torch.int32", "moe_route", "ids")
+    _plane(weights, (T, k), "torch.float32", "moe_route", "weights")
+    if offsets is not None:
+        _plane(offsets, (E + 1,), "torch.int32", "moe_route", "offsets")
+    if slots is not None:
+        _plane(slots, (T * k,), "torch.int32", "moe_route", "slots")
+    if bias is not None:
+        _plane(bias, (E,), "torch.float32", "moe_route", "bias")
+    _check(load().moe_route(logits.data_ptr(), ld, _dtype(logits, "moe_route"),
+                            None if bias is None else bias.data_ptr(), T, E, k, _score(score, "moe_route"), groups,
+                            top_groups, 1 if renorm else 0, scale, ids.data_ptr(), weights.data_ptr(),
+                            None if offsets is None else offsets.data_ptr(),
+                            None if slots is None else slots.data_ptr(), _on(logits, stream)), "moe_route")
+    return ids, weights, offsets, slots
+
+
+def moe_route_backward(logits, ids, dweights, dlogits, bias=None, score="softmax", renorm=True, scale=1.0,
+                       stream=None):
+    """Gradient of :func:`moe_route`'s weights to its logits, ``dlogits`` [T, E] in the logits' dtype."""
+    T, E = logits.shape
+    k = ids.shape[1]
+    ld = _rows(logits, T, E, "moe_route_backward", "logits")
+    ldd = _rows(dlogits, T, E, "moe_route_backward", "dlogits")
+    if dlogits.dtype != logits.dtype:
+        raise TypeError("moe_route_backward: logits and dlogits must have the same dtype")
+    _plane(ids, (T, k), "torch.int32", "moe_route_backward", "ids")
+    _plane(dweights, (T, k), "torch.float32", "moe_route_backward", "dweights")
+    if bias is not None:
+        _plane(bias, (E,), "torch.float32", "moe_route_backward", "bias")
+    _check(load().moe_route_backward(logits.data_ptr(), ld, _dtype(logits, "moe_route_backward"),
+                                     None if bias is None else bias.data_ptr(), ids.data_ptr(), dweights.data_ptr(),
+                                     dlogits.data_ptr(), ldd, T, E, k, _score(score, "moe_route_backward"),
+                                     1 if renorm else 0, scale, _on(logits, stream)), "moe_route_backward")
+    return dlogits
+
+
+def moe_experts(gate, up, down, x, ids, weights, offsets, slots, out, stream=None):
+    """out [T, D] = the routed experts' gated products of x [T, D] (see include/tq2.h); ids, weights, offsets and
+    slots as :func:`moe_route` wrote them."""
+    T, D = x.shape
+    k = ids.shape[1]
+    ldx = _rows(x, T, gate.K, "moe_experts", "x")
+    ldo = _rows(out, T, D, "moe_experts", "out")
+    if out.dtype != x.dtype:
+        raise TypeError("moe_experts: x and out must have the same dtype")
+    _plane(ids, (T, k), "torch.int32", "moe_experts", "ids")
+    _plane(weights, (T, k), "torch.float32", "moe_experts", "weights")
+    _plane(offsets, (gate.E + 1,), "torch.int32", "moe_experts", "offsets")
+    _plane(slots, (T * k,), "torch.int32", "moe_experts", "slots")
+    _check(load().moe_experts(gate.handle, up.handle, down.handle, x.data_ptr(), ldx, _dtype(x, "moe_experts"),
+                              ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), slots.data_ptr(),
+                              out.data_ptr(), ldo, T, k, _on(x, stream)), "moe_experts")
+    return out
 
 
 def debug_wait_timeout(limit_ns, stream=None):

@@ -7,6 +7,7 @@
 #include <string>
 
 #include "../../include/tq2.h"
+#include "q4.cuh"
 #include "tq2_internal.h"
 #include "tq2_quant.h"
 
@@ -110,7 +111,10 @@ tq2_status tq2_device_status(void* stream) {
     cudaError_t e = cudaStreamSynchronize(S(stream));
     if (e != cudaSuccess) return cuda_fail(e, "tq2_device_status: stream");
     const unsigned int err = tq2::read_clear_dev_error_skinny(S(stream)) | tq2::read_clear_dev_error_umma(S(stream)) |
-                             tq2::read_clear_dev_error_blr(S(stream)) | tq2::read_clear_dev_error_gemv(S(stream));
+                             tq2::read_clear_dev_error_blr(S(stream)) | tq2::read_clear_dev_error_gemv(S(stream)) |
+                             tq2::read_clear_dev_error_q4_g32(S(stream)) |
+                             tq2::read_clear_dev_error_q4_g64(S(stream)) |
+                             tq2::read_clear_dev_error_q4_g128(S(stream));
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "tq2_device_status");
     if (err) return fail(TQ2_ETIMEOUT, "a bounded device-side wait ran out (record 0x%x)", err);

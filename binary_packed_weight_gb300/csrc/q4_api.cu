@@ -1,0 +1,347 @@
+// q4_api.cu -- the C ABI of the 4-bit weights and of the routed experts:
+// argument checks, device memory of the handles, scratch, launches.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+#include <mutex>
+#include <new>
+
+#include "../../include/tq2.h"
+#include "q4.cuh"
+#include "tq2_internal.h"
+
+namespace tq2 {
+
+// The library's stream-ordered pool of a device: like the device's default
+// pool, except that freed scratch stays reserved over synchronizations (the
+// default pool gives it back to the driver at each one, and the next call
+// pays for mapping it again).
+cudaError_t scratch_pool(cudaMemPool_t* pool) {
+    constexpr int MAX_DEVICES = 64;
+    static std::atomic<cudaMemPool_t> pools[MAX_DEVICES];
+    static std::mutex lock;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= MAX_DEVICES) return cudaDeviceGetDefaultMemPool(pool, dev);
+    *pool = pools[dev].load(std::memory_order_acquire);
+    if (*pool) return cudaSuccess;
+    std::lock_guard<std::mutex> hold(lock);
+    *pool = pools[dev].load(std::memory_order_relaxed);
+    if (*pool) return cudaSuccess;
+    cudaMemPoolProps props = {};
+    props.allocType = cudaMemAllocationTypePinned;
+    props.location.type = cudaMemLocationTypeDevice;
+    props.location.id = dev;
+    e = cudaMemPoolCreate(pool, &props);
+    if (e != cudaSuccess) return e;
+    uint64_t keep = ~uint64_t(0);
+    e = cudaMemPoolSetAttribute(*pool, cudaMemPoolAttrReleaseThreshold, &keep);
+    if (e != cudaSuccess) return e;
+    pools[dev].store(*pool, std::memory_order_release);
+    return cudaSuccess;
+}
+
+cudaError_t scratch_alloc(void** p, size_t bytes, cudaStream_t st) {
+    cudaMemPool_t pool = nullptr;
+    cudaError_t e = scratch_pool(&pool);
+    if (e != cudaSuccess) return e;
+    return cudaMallocFromPoolAsync(p, bytes, pool, st);
+}
+
+cudaError_t launch_q4_stream(const Q4Stream& a, cudaStream_t st) {
+    if (a.group == 32) return launch_q4_stream_g32(a, st);
+    if (a.group == 64) return launch_q4_stream_g64(a, st);
+    return launch_q4_stream_g128(a, st);
+}
+
+namespace {
+
+tq2_status cuda_status(cudaError_t e, const char* what) {
+    if (e == cudaSuccess) return TQ2_OK;
+    return (tq2_status)set_error(e == cudaErrorMemoryAllocation ? TQ2_ENOMEM : TQ2_ECUDA, "%s: %s", what,
+                                 cudaGetErrorString(e));
+}
+
+bool dtype_ok(int dtype) { return dtype == TQ2_F32 || dtype == TQ2_F16 || dtype == TQ2_BF16; }
+
+bool format_ok(int64_t K, int group) {
+    return (group == 32 || group == 64 || group == 128) && K >= group && K % group == 0 && K <= 32768;
+}
+
+// A plane as a device pointer: copied to *tmp if it is in host memory.
+cudaError_t to_device(const void* p, size_t bytes, void** tmp, const void** dev, cudaStream_t st) {
+    *tmp = nullptr;
+    cudaPointerAttributes at = {};
+    cudaError_t e = cudaPointerGetAttributes(&at, p);
+    if (e != cudaSuccess) return e;
+    if (at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged) {
+        *dev = p;
+        return cudaSuccess;
+    }
+    e = cudaMallocAsync(tmp, bytes, st);
+    if (e != cudaSuccess) {
+        *tmp = nullptr;
+        return e;
+    }
+    *dev = *tmp;
+    return cudaMemcpyAsync(*tmp, p, bytes, cudaMemcpyHostToDevice, st);
+}
+
+// out[t] = sum_j weights[t,j] y[t*k+j] over the routed j, in order.  One CTA
+// row per token, four columns a thread; y was written by the launch before
+// and is mostly still in L2.
+template <class T>
+__device__ __forceinline__ T round_to(float v);
+template <>
+__device__ __forceinline__ float round_to<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half round_to<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+template <class T>
+__global__ void __launch_bounds__(256)
+moe_combine_kernel(const float* __restrict__ y, const int32_t* __restrict__ ids, const float* __restrict__ weights,
+                   T* __restrict__ out, int64_t ldo, int64_t T_, int D, int k, int vec) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 4;
+    if (c >= D) return;
+    for (int64_t t = blockIdx.x; t < T_; t += gridDim.x) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < k; ++j) {
+            if (ids[t * k + j] < 0) continue;
+            const float w = weights[t * k + j];
+            const float* p = y + (t * k + j) * D + c;
+            if (vec) {
+                const float4 v = *reinterpret_cast<const float4*>(p);
+                s[0] = fmaf(w, v.x, s[0]);
+                s[1] = fmaf(w, v.y, s[1]);
+                s[2] = fmaf(w, v.z, s[2]);
+                s[3] = fmaf(w, v.w, s[3]);
+            } else {
+                for (int i = 0; i < 4 && c + i < D; ++i) s[i] = fmaf(w, p[i], s[i]);
+            }
+        }
+        for (int i = 0; i < 4 && c + i < D; ++i) out[t * ldo + c + i] = round_to<T>(s[i]);
+    }
+}
+
+template <class T>
+cudaError_t launch_combine(const float* y, const int32_t* ids, const float* w, void* out, int64_t ldo, int64_t T_,
+                           int D, int k, cudaStream_t st) {
+    const unsigned gy = (unsigned)((D + 1023) / 1024);
+    const unsigned gx = (unsigned)(T_ < 16384 ? T_ : 16384);
+    return launch_pdl(moe_combine_kernel<T>, dim3(gx, gy), dim3(256), 0, st, y, ids, w, reinterpret_cast<T*>(out),
+                      ldo, T_, D, k, D % 4 == 0 ? 1 : 0);
+}
+
+// Scratch of one call, given back on the same stream whatever happens.
+struct Scratch {
+    void* p = nullptr;
+    cudaStream_t st;
+    explicit Scratch(cudaStream_t s) : st(s) {}
+    ~Scratch() {
+        if (p) cudaFreeAsync(p, st);
+    }
+};
+
+Q4Stream stream_of(const q4_weight* w) {
+    Q4Stream a{};
+    a.w0 = w->blocks;
+    a.mstride = w->mstride;
+    a.N = w->N;
+    a.K = w->K;
+    a.nkc = (int)w->nkc;
+    a.zeros = w->zeros ? 1 : 0;
+    a.group = w->group;
+    a.E = (int)w->E;
+    return a;
+}
+
+}  // namespace
+}  // namespace tq2
+
+using namespace tq2;
+
+extern "C" {
+
+tq2_status q4_upload(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, int64_t E, int64_t N,
+                     int64_t K, int group, q4_handle* out, void* stream) {
+    if (out) *out = nullptr;
+    if (!codes || !scales || !out) return (tq2_status)set_error(TQ2_EINVAL, "q4_upload: null pointer");
+    if (E < 1 || E > 1024 || N < 1 || N > (1 << 24) || !format_ok(K, group))
+        return (tq2_status)set_error(TQ2_ESHAPE,
+                                     "q4_upload: need 1 <= E <= 1024, 1 <= N <= 2^24, group 32, 64 or 128, K a "
+                                     "multiple of it up to 32768 (E=%lld N=%lld K=%lld group=%d)",
+                                     (long long)E, (long long)N, (long long)K, group);
+    if ((reinterpret_cast<uintptr_t>(codes) & 1) != 0 || (reinterpret_cast<uintptr_t>(scales) & 1) != 0)
+        return (tq2_status)set_error(TQ2_EINVAL, "q4_upload: codes and scales must be 2-byte aligned");
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    q4_weight* w = new (std::nothrow) q4_weight();
+    if (!w) return (tq2_status)set_error(TQ2_ENOMEM, "q4_upload: host allocation");
+    w->E = E;
+    w->N = N;
+    w->K = K;
+    w->group = group;
+    w->zeros = zeros != nullptr;
+    w->nkc = (K + Q4_K - 1) / Q4_K;
+    w->mstride = (N + 127) / 128 * 8 * w->nkc * q4_block_bytes(group, w->zeros);
+    cudaGetDevice(&w->device);
+    const size_t ngroups = (size_t)E * N * (K / group);
+    void* tmp[3] = {nullptr, nullptr, nullptr};
+    const void* dev[3] = {nullptr, nullptr, nullptr};
+    cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&w->blocks), (size_t)E * w->mstride);
+    if (e == cudaSuccess) e = to_device(codes, (size_t)E * N * (K / 2), &tmp[0], &dev[0], st);
+    if (e == cudaSuccess) e = to_device(scales, ngroups * 2, &tmp[1], &dev[1], st);
+    if (e == cudaSuccess && zeros) e = to_device(zeros, ngroups, &tmp[2], &dev[2], st);
+    if (e == cudaSuccess)
+        e = launch_q4_pack(static_cast<const uint8_t*>(dev[0]), static_cast<const uint16_t*>(dev[1]),
+                           static_cast<const uint8_t*>(dev[2]), w, st);
+    for (void* p : tmp)
+        if (p) cudaFreeAsync(p, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e != cudaSuccess) {
+        cudaFree(w->blocks);
+        delete w;
+        return cuda_status(e, "q4_upload");
+    }
+    *out = w;
+    return TQ2_OK;
+}
+
+tq2_status q4_free(q4_handle h) {
+    if (!h) return TQ2_OK;
+    cudaError_t e = cudaFree(h->blocks);
+    delete h;
+    return cuda_status(e, "q4_free");
+}
+
+tq2_status q4_shape(q4_handle h, int64_t* E, int64_t* N, int64_t* K, int* group) {
+    if (!h) return (tq2_status)set_error(TQ2_EINVAL, "q4_shape: null handle");
+    if (E) *E = h->E;
+    if (N) *N = h->N;
+    if (K) *K = h->K;
+    if (group) *group = h->group;
+    return TQ2_OK;
+}
+
+tq2_status q4_dequant(q4_handle h, float* w, void* stream) {
+    if (!h || !w) return (tq2_status)set_error(TQ2_EINVAL, "q4_dequant: null pointer");
+    return cuda_status(launch_q4_dequant(h, w, reinterpret_cast<cudaStream_t>(stream)), "q4_dequant");
+}
+
+tq2_status q4_quantize(const void* w, int dtype, int64_t rows, int64_t K, int group, uint8_t* codes,
+                       uint16_t* scales, uint8_t* zeros, void* stream) {
+    if (!w || !codes || !scales) return (tq2_status)set_error(TQ2_EINVAL, "q4_quantize: null pointer");
+    if (!dtype_ok(dtype)) return (tq2_status)set_error(TQ2_EINVAL, "q4_quantize: unknown dtype %d", dtype);
+    if (rows < 1 || rows > ((int64_t)1 << 34) || !format_ok(K, group))
+        return (tq2_status)set_error(TQ2_ESHAPE, "q4_quantize: bad shape (rows=%lld K=%lld group=%d)",
+                                     (long long)rows, (long long)K, group);
+    if ((reinterpret_cast<uintptr_t>(codes) & 3) != 0)
+        return (tq2_status)set_error(TQ2_EINVAL, "q4_quantize: codes must be 4-byte aligned");
+    return cuda_status(launch_q4_quantize(w, dtype, rows, K, group, codes, scales, zeros,
+                                          reinterpret_cast<cudaStream_t>(stream)),
+                       "q4_quantize");
+}
+
+tq2_status q4_gemm(q4_handle h, const void* x, int64_t ldx, void* out, int64_t ldo, int dtype, int64_t M,
+                   void* stream) {
+    if (!h) return (tq2_status)set_error(TQ2_EINVAL, "q4_gemm: null handle");
+    if (!dtype_ok(dtype)) return (tq2_status)set_error(TQ2_EINVAL, "q4_gemm: unknown dtype %d", dtype);
+    if (M < 0 || M > (1 << 20)) return (tq2_status)set_error(TQ2_ESHAPE, "q4_gemm: bad M=%lld", (long long)M);
+    if (M == 0) return TQ2_OK;
+    if (!x || !out) return (tq2_status)set_error(TQ2_EINVAL, "q4_gemm: null pointer");
+    if (h->E != 1)
+        return (tq2_status)set_error(TQ2_ESHAPE, "q4_gemm: the handle holds %lld matrices, not one", (long long)h->E);
+    if (ldx < h->K || ldo < h->N)
+        return (tq2_status)set_error(TQ2_ESHAPE, "q4_gemm: row strides %lld, %lld are shorter than K=%lld, N=%lld",
+                                     (long long)ldx, (long long)ldo, (long long)h->K, (long long)h->N);
+    Q4Stream a = stream_of(h);
+    a.x = x;
+    a.ldx = ldx;
+    a.xmode = dtype == TQ2_F32 ? Q4_X_SPLIT : Q4_X_RAW16;
+    a.bf16 = dtype == TQ2_BF16;
+    a.out = out;
+    a.ldo = ldo;
+    a.otype = dtype;
+    a.M = (int)M;
+    a.tokens = (int)(M < 32 ? M : 32);
+    return cuda_status(launch_q4_stream(a, reinterpret_cast<cudaStream_t>(stream)), "q4_gemm");
+}
+
+tq2_status moe_experts(q4_handle gate, q4_handle up, q4_handle down, const void* x, int64_t ldx, int dtype,
+                       const int32_t* ids, const float* weights, const int32_t* offsets, const int32_t* slots,
+                       void* out, int64_t ldo, int64_t T, int k, void* stream) {
+    if (!gate || !up || !down) return (tq2_status)set_error(TQ2_EINVAL, "moe_experts: null handle");
+    if (!dtype_ok(dtype)) return (tq2_status)set_error(TQ2_EINVAL, "moe_experts: unknown dtype %d", dtype);
+    if (T < 0 || k < 1 || k > 32 || T * k > (1 << 24))
+        return (tq2_status)set_error(TQ2_ESHAPE, "moe_experts: bad T=%lld, k=%d", (long long)T, k);
+    const int64_t D = gate->K, F = gate->N, E = gate->E;
+    if (up->K != D || up->N != F || up->E != E || down->K != F || down->N != D || down->E != E ||
+        up->group != gate->group || up->zeros != gate->zeros)
+        return (tq2_status)set_error(TQ2_ESHAPE,
+                                     "moe_experts: gate, up and down do not fit (%lldx%lldx%lld, %lldx%lldx%lld, "
+                                     "%lldx%lldx%lld, or gate's and up's groups)",
+                                     (long long)E, (long long)F, (long long)D, (long long)up->E, (long long)up->N,
+                                     (long long)up->K, (long long)down->E, (long long)down->N, (long long)down->K);
+    if (ldx < D || ldo < D)
+        return (tq2_status)set_error(TQ2_ESHAPE, "moe_experts: row strides %lld, %lld are shorter than D=%lld",
+                                     (long long)ldx, (long long)ldo, (long long)D);
+    if (T == 0) return TQ2_OK;
+    if (!x || !ids || !weights || !offsets || !slots || !out)
+        return (tq2_status)set_error(TQ2_EINVAL, "moe_experts: null pointer");
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t S = T * k;
+    const size_t hbytes = ((size_t)S * F * 4 + 255) / 256 * 256;
+    Scratch mem(st);
+    cudaError_t e = scratch_alloc(&mem.p, hbytes + (size_t)S * D * 4, st);
+    if (e != cudaSuccess) {
+        mem.p = nullptr;
+        return cuda_status(e, "moe_experts: scratch");
+    }
+    float* hid = static_cast<float*>(mem.p);
+    float* y = reinterpret_cast<float*>(static_cast<char*>(mem.p) + hbytes);
+    // rows of one expert: the average, and room for the spread around it
+    const int64_t mean = (S + E - 1) / E;
+    const int64_t most = mean + 2 * mean < T ? mean + 2 * mean : T;
+    Q4Stream a = stream_of(gate);
+    a.w1 = up->blocks;
+    a.pair = 1;
+    a.x = x;
+    a.ldx = ldx;
+    a.xmode = dtype == TQ2_F32 ? Q4_X_SPLIT : Q4_X_RAW16;
+    a.bf16 = dtype == TQ2_BF16;
+    a.out = hid;                                              // by position of the plan
+    a.ldo = F;
+    a.otype = TQ2_F32;
+    a.offsets = offsets;
+    a.slots = slots;
+    a.nslots = (int)S;
+    a.xdiv = k;
+    a.tokens = (int)(most < 32 ? most : 32);
+    e = launch_q4_stream(a, st);
+    if (e != cudaSuccess) return cuda_status(e, "moe_experts: gate and up");
+    Q4Stream b = stream_of(down);
+    b.x = hid;
+    b.ldx = F;
+    b.xmode = dtype == TQ2_F32 ? Q4_X_SPLIT : Q4_X_SCALED;
+    b.out = y;                                                // by slot
+    b.ldo = D;
+    b.otype = TQ2_F32;
+    b.oslot = 1;
+    b.offsets = offsets;
+    b.slots = slots;
+    b.nslots = (int)S;
+    b.tokens = a.tokens;
+    e = launch_q4_stream(b, st);
+    if (e != cudaSuccess) return cuda_status(e, "moe_experts: down");
+    if (dtype == TQ2_F32) e = launch_combine<float>(y, ids, weights, out, ldo, T, (int)D, k, st);
+    else if (dtype == TQ2_F16) e = launch_combine<__half>(y, ids, weights, out, ldo, T, (int)D, k, st);
+    else e = launch_combine<__nv_bfloat16>(y, ids, weights, out, ldo, T, (int)D, k, st);
+    return cuda_status(e, "moe_experts: combine");
+}
+
+}  // extern "C"

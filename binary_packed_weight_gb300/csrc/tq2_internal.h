@@ -101,6 +101,9 @@ cudaError_t launch_expand_bits(const uint32_t* bits, int64_t rows, int64_t r, ui
                                cudaStream_t st);
 unsigned int read_clear_dev_error_blr(cudaStream_t st);
 
+// q4_api.cu: scratch from the library's stream-ordered pool (freed with cudaFreeAsync).
+cudaError_t scratch_alloc(void** p, size_t bytes, cudaStream_t st);
+
 // api.cu: record the calling thread's last error message; returns `st`.
 int set_error(int st, const char* fmt, ...);
 

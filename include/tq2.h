@@ -421,6 +421,171 @@ TQ2_API tq2_status blr_sign_grads(const uint32_t* bits_u, const float* h, const 
                           const float* x, const float* dy, const float* a_save, float* gu, float* gv,
                           int64_t T, int64_t d_in, int64_t d_out, int64_t r, float gscale, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* 4-bit weights with group scales                                           */
+/* ------------------------------------------------------------------------ */
+
+/* Element types of activations, logits and outputs. */
+typedef enum { TQ2_F32 = 0, TQ2_F16 = 1, TQ2_BF16 = 2 } tq2_dtype;
+
+/* Opaque handle of E 4-bit matrices of the same shape (E = 1: one weight). */
+typedef struct q4_weight* q4_handle;
+
+/*
+ * q4_upload -- lay out 4-bit weights for the products below:
+ *     W[e,n,k] = (c - z) * d,   c = codes[e,n,k],  z, d of the group k/group.
+ *
+ *   codes   uint8[E][N][K/2], the code of an even k in the low half of its
+ *           byte, of the odd k after it in the high half.
+ *   scales  f16 bits [E][N][K/group]; any sign.
+ *   zeros   uint8[E][N][K/group], 0..15 (the upper four bits are ignored), or
+ *           NULL: every zero point is 8.
+ *           All three in HOST or in DEVICE memory (each by itself); codes
+ *           2-byte aligned.  Copied: the caller keeps ownership.
+ *   E, N, K, group   E, N >= 1, E <= 1024, group 32, 64 or 128, K >= group a
+ *           multiple of it, K <= 32768, N <= 2^24.  Else TQ2_ESHAPE.
+ *   out     receives the handle (NULL on failure).
+ *   stream  used for the copies and the layout kernel, after work queued on
+ *           it; the call synchronizes it before returning.
+ *
+ * The handle holds one copy in 16-row x 256-k blocks (codes, then the block's
+ * scales and zero points), N padded to 128 rows and K to 256.
+ */
+TQ2_API tq2_status q4_upload(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, int64_t E,
+                             int64_t N, int64_t K, int group, q4_handle* out, void* stream);
+
+/* Release the handle and its device memory (NULL is accepted).  The caller
+ * must make sure no work that reads it is still pending. */
+TQ2_API tq2_status q4_free(q4_handle h);
+
+/* Shape of a handle (each pointer may be NULL). */
+TQ2_API tq2_status q4_shape(q4_handle h, int64_t* E, int64_t* N, int64_t* K, int* group);
+
+/*
+ * q4_dequant -- W as the products see it: DEVICE float[E][N][K], overwritten;
+ * exact ((c - z) * d has at most 16 significant bits).  Asynchronous.
+ */
+TQ2_API tq2_status q4_dequant(q4_handle h, float* w, void* stream);
+
+/*
+ * q4_quantize -- plain weights to codes, scales and zero points, all in the
+ * layout q4_upload takes.  Per group of a row, in f32:
+ *   zeros given:  lo = min(w, 0), hi = max(w, 0), d = f16((hi - lo) / 15),
+ *                 z = clamp(rint(-lo / d), 0, 15), c = clamp(rint(w / d) + z, 0, 15)
+ *   zeros NULL:   d = f16(max|w| / 7), c = clamp(rint(w / d) + 8, 0, 15)
+ * with the rounded d (at most 65504) and halves to even; where d = 0, c = z
+ * (z = 0, or 8 without zero points).
+ *
+ *   w       DEVICE, dtype (tq2_dtype), [rows][K] dense, finite (NaN or Inf
+ *           give unspecified codes).  rows >= 1, K and group as q4_upload.
+ *   codes, scales, zeros   DEVICE, overwritten; codes 4-byte aligned.
+ * Asynchronous.
+ */
+TQ2_API tq2_status q4_quantize(const void* w, int dtype, int64_t rows, int64_t K, int group, uint8_t* codes,
+                               uint16_t* scales, uint8_t* zeros, void* stream);
+
+/*
+ * q4_gemm -- out[m,n] = sum_k x[m,k] W[n,k], for a handle with E = 1.
+ *
+ *   x       DEVICE, dtype, M rows of K, ldx >= K elements apart.
+ *   out     DEVICE, dtype (that of x), M rows of N, ldo >= N elements apart,
+ *           overwritten; must not overlap x.
+ *   M       0 <= M <= 2^20 (0: nothing is done).
+ *   x and out need only their element's alignment (rows that are 16-byte
+ *   aligned are fetched faster).
+ * Weights and f16 / bf16 activations enter the products exactly; f32
+ * activations as two f16 parts of a row scaled by a power of two, whose sum
+ * is within 2^-22 |x[m,k]| + 2^-38 max_k |x[m,k]| of x.  Accumulation is in
+ * f32 and the result is rounded once to dtype.  The order of the additions depends on the shape
+ * alone, so results are the same from run to run.
+ * Meant for decode batches (M <= 16, where the weights are read once); larger
+ * M runs in passes that read the weights again.  Asynchronous, no scratch.
+ */
+TQ2_API tq2_status q4_gemm(q4_handle h, const void* x, int64_t ldx, void* out, int64_t ldo, int dtype, int64_t M,
+                           void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Mixture of experts                                                        */
+/* ------------------------------------------------------------------------ */
+
+/* Scores of a router. */
+typedef enum { MOE_SOFTMAX = 0, MOE_SIGMOID = 1 } moe_score;
+
+/*
+ * moe_route -- a router's selection, its weights and the order of its slots.
+ *
+ * Per token (row of logits), in f32: expert e is available where its logit
+ * and its bias are neither -inf nor NaN; +inf counts as the largest f32.
+ *   p     softmax of the available logits, or their sigmoid 1/(1+exp(-l)),
+ *         each operation rounded to f32 (so saturated scores tie); 0 for the others.  The softmax sum adds neighbouring experts first
+ *         (a binary tree over the row, padded with zeros to a power of two).
+ *   s     p + bias: what the selection goes by.
+ *   groups > 1 and top_groups < groups: E/groups neighbouring experts form a
+ *         group; its value is the sum of its two largest s (of one, where only
+ *         one is available).  Only the top_groups groups of largest value take part.
+ *   ids   the k experts of largest s, in that order.  Ties, among groups too,
+ *         go to the lower index.  -1 where fewer are available.
+ *   w     p of the selected (0 beside -1), divided by max(their sum,
+ *         2^-126) if renorm, times scale.
+ * The slots t*k+j with an expert, ordered by expert and then by slot, are the
+ * plan that moe_experts takes: those of expert e are
+ * slots[offsets[e]] .. slots[offsets[e+1]-1]; slots past offsets[E] are -1.
+ *
+ *   logits   DEVICE, dtype, T rows of E, ld >= E elements apart.
+ *   bias     DEVICE float[E] or NULL (zero).
+ *   ids      DEVICE int32[T][k];  weights  DEVICE float[T][k].
+ *   offsets  DEVICE int32[E+1];  slots  DEVICE int32[T*k]; or both NULL: no plan.
+ *   0 <= T, T*k <= 2^24;  1 <= E <= 1024;  1 <= k <= 32, k <= E;  groups
+ *   divides E and is at most 32;  1 <= top_groups <= groups.  Else TQ2_ESHAPE.
+ *   score a moe_score, scale finite.  Else TQ2_EINVAL.
+ * Asynchronous; scratch (for a plan of many tokens) from the library's
+ * stream-ordered pool.
+ */
+TQ2_API tq2_status moe_route(const void* logits, int64_t ld, int dtype, const float* bias, int64_t T, int E, int k,
+                             int score, int groups, int top_groups, int renorm, float scale, int32_t* ids,
+                             float* weights, int32_t* offsets, int32_t* slots, void* stream);
+
+/*
+ * moe_route_backward -- gradient of moe_route's weights to its logits (the
+ * selection is piecewise constant and the bias takes no part in the weights).
+ * With g_j = scale * dweights[j] and p as above, sums over the selected j:
+ *   renorm:   q_j = (g_j - sum_i g_i p_i / S) / S,  S = max(sum_i p_i, 2^-126); else q_j = g_j
+ *   softmax:  dlogits[e] = p_e (q_e - sum_j q_j p_j)      (q_e = 0 unless selected;
+ *             with renorm the sum is 0 and only the selected get a gradient)
+ *   sigmoid:  dlogits[e] = p_e (1 - p_e) q_e
+ * ids as moe_route returned them; a slot of -1 takes no part.  dlogits: DEVICE, dtype,
+ * T rows of E, ldd >= E elements apart, overwritten.  Limits as moe_route.  Asynchronous.
+ */
+TQ2_API tq2_status moe_route_backward(const void* logits, int64_t ld, int dtype, const float* bias,
+                                      const int32_t* ids, const float* dweights, void* dlogits, int64_t ldd,
+                                      int64_t T, int E, int k, int score, int renorm, float scale, void* stream);
+
+/*
+ * moe_experts -- the routed experts' gated products:
+ *   out[t] = sum_j weights[t,j] * Down_e ( silu(Gate_e x[t]) * (Up_e x[t]) ),  e = ids[t,j],
+ * over the j with ids[t,j] >= 0 (a token without any gets 0); silu(v) = v/(1+exp(-v)).
+ *
+ *   gate, up  handles of E matrices F x D, the same group and zero-point form.
+ *   down      handle of E matrices D x F.
+ *   x         DEVICE, dtype, T rows of D, ldx >= D elements apart.
+ *   ids, weights, offsets, slots   DEVICE, a plan of moe_route for these E:
+ *             int32[T][k], float[T][k], int32[E+1], int32[T*k].  Of any other
+ *             contents the result is unspecified (offsets and slots are
+ *             clamped to their ranges: nothing outside the arrays is touched).
+ *   out       DEVICE, dtype, T rows of D, ldo >= D elements apart,
+ *             overwritten; must not overlap x.
+ *   0 <= T, T*k <= 2^24, 1 <= k <= 32.
+ * Shapes that do not fit: TQ2_ESHAPE.  Gate and Up take x as q4_gemm takes it,
+ * the gated product between them is kept in f32 and enters Down as f32
+ * activations do (for f16 and bf16 calls as its first f16 part alone, within
+ * 2^-12 of its magnitude).  A token's sum over j runs in the order of j, in f32.
+ * Scratch (T*k rows of F and of D floats) from the library's stream-ordered
+ * pool.  Asynchronous.
+ */
+TQ2_API tq2_status moe_experts(q4_handle gate, q4_handle up, q4_handle down, const void* x, int64_t ldx, int dtype,
+                               const int32_t* ids, const float* weights, const int32_t* offsets,
+                               const int32_t* slots, void* out, int64_t ldo, int64_t T, int k, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

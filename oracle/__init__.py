@@ -12,6 +12,8 @@ Modules
 ``f16``   IEEE-754 binary16 decode written from the format definition.
 ``tq2``   ``BlockTQ2_0_g128`` parse / dequantize and the GEMM
           ``out[m,n] = sum_k x[m,k] * W[n,k]``.
+``q4``    4-bit weights with group scales.
+``moe``   a router (selection, plan, gradient) and the routed experts.
 ``blr``   the binary low-rank layer ``W = diag(h) S_U diag(l) S_V^T diag(g)``:
           sign-bitmap expansion, forward and backward.
 
@@ -28,4 +30,4 @@ Parity status: every function here is pinned by a ``-m "not gpu"`` test in
 ``tests/test_oracle_*.py`` (closed forms, one-hot blocks, bit positions,
 finite differences, library special cases).  No function is unpinned.
 """
-from . import blr, f16, tq2  # noqa: F401
+from . import blr, f16, moe, q4, tq2  # noqa: F401
