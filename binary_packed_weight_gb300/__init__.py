@@ -301,22 +301,30 @@ class Q4Weight:
 
 
 _dtypes = {}
+_names = {}
+_raw_stream = None
+
+
+def _torch_names():
+    """torch objects the argument checks compare with (torch is imported on first use)."""
+    import torch
+    _dtypes.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    _names.update({"int32": torch.int32, "uint8": torch.uint8, "float32": torch.float32, "float16": torch.float16})
 
 
 def _dtype(t, where):
     """tq2_dtype of a tensor."""
     if not _dtypes:
-        import torch
-        _dtypes.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
-    try:
-        return _dtypes[t.dtype]
-    except KeyError:
-        raise TypeError(f"{where}: dtype {t.dtype} is not float32, float16 or bfloat16") from None
+        _torch_names()
+    d = _dtypes.get(t.dtype)
+    if d is None:
+        raise TypeError(f"{where}: dtype {t.dtype} is not float32, float16 or bfloat16")
+    return d
 
 
 def _rows(t, rows, cols, where, name):
     """Row stride of a [rows, cols] tensor whose rows are contiguous."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{where}: {name} must be [{rows}, {cols}], got {list(t.shape)}")
     ld, inner = t.stride()
     if inner != 1 and cols > 1:
@@ -325,12 +333,12 @@ def _rows(t, rows, cols, where, name):
 
 
 def _plane(t, shape, dtype, where, name):
-    """A dense tensor of a given shape and dtype (a torch dtype's name)."""
-    if tuple(t.shape) != shape or not t.is_contiguous() or str(t.dtype) != dtype:
+    """The address of a dense tensor of a given shape and dtype (a torch dtype's name)."""
+    if not _names:
+        _torch_names()
+    if t.dtype is not _names[dtype] or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{where}: {name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-
-
-_raw_stream = None
+    return t.data_ptr()
 
 
 def _on(t, stream):
@@ -352,10 +360,10 @@ def q4_upload(codes, scales, zeros=None, group=128, stream=None):
         raise ValueError(f"q4_upload: codes must be [E, N, K/2] or [N, K/2], got {list(codes.shape)}")
     E, N, K = shape[0], shape[1], 2 * shape[2]
     lead = tuple(codes.shape)[:-1]
-    _plane(codes, lead + (K // 2,), "torch.uint8", "q4_upload", "codes")
-    _plane(scales, lead + (K // group,), "torch.float16", "q4_upload", "scales")
+    _plane(codes, lead + (K // 2,), "uint8", "q4_upload", "codes")
+    _plane(scales, lead + (K // group,), "float16", "q4_upload", "scales")
     if zeros is not None:
-        _plane(zeros, lead + (K // group,), "torch.uint8", "q4_upload", "zeros")
+        _plane(zeros, lead + (K // group,), "uint8", "q4_upload", "zeros")
     h = ctypes.c_void_p()
     _check(load().q4_upload(_ptr(codes), _ptr(scales), _ptr(zeros), E, N, K, group, ctypes.byref(h),
                             _stream(stream)), "q4_upload")
@@ -376,10 +384,10 @@ def q4_quantize(w, codes, scales, zeros=None, group=128, stream=None):
     lead = tuple(w.shape)[:-1]
     if not w.is_contiguous():
         raise ValueError("q4_quantize: w must be contiguous")
-    _plane(codes, lead + (K // 2,), "torch.uint8", "q4_quantize", "codes")
-    _plane(scales, lead + (K // group,), "torch.float16", "q4_quantize", "scales")
+    _plane(codes, lead + (K // 2,), "uint8", "q4_quantize", "codes")
+    _plane(scales, lead + (K // group,), "float16", "q4_quantize", "scales")
     if zeros is not None:
-        _plane(zeros, lead + (K // group,), "torch.uint8", "q4_quantize", "zeros")
+        _plane(zeros, lead + (K // group,), "uint8", "q4_quantize", "zeros")
     _check(load().q4_quantize(_ptr(w), _dtype(w, "q4_quantize"), w.numel() // max(K, 1), K, group, _ptr(codes),
                               _ptr(scales), _ptr(zeros), _stream(stream)), "q4_quantize")
     return codes, scales, zeros
@@ -388,12 +396,11 @@ def q4_quantize(w, codes, scales, zeros=None, group=128, stream=None):
 def q4_gemm(w, x, out, stream=None):
     """out [M, N] = x [M, K] @ W^T for a weight with one matrix; rows may be strided."""
     M = x.shape[0]
-    ldx = _rows(x, M, w.K, "q4_gemm", "x")
-    ldo = _rows(out, M, w.N, "q4_gemm", "out")
-    if out.dtype != x.dtype:
+    if out.dtype is not x.dtype:
         raise TypeError("q4_gemm: x and out must have the same dtype")
-    _check(load().q4_gemm(w.handle, x.data_ptr(), ldx, out.data_ptr(), ldo, _dtype(x, "q4_gemm"), M,
-                          _on(x, stream)), "q4_gemm")
+    _check((_lib or load()).q4_gemm(w._h, x.data_ptr(), _rows(x, M, w.K, "q4_gemm", "x"), out.data_ptr(),
+                                    _rows(out, M, w.N, "q4_gemm", "out"), _dtype(x, "q4_gemm"), M, _on(x, stream)),
+           "q4_gemm")
     return out
 
 
@@ -413,20 +420,14 @@ def moe_route(logits, ids, weights, offsets=None, slots=None, bias=None, score="
     ``weights`` float32 [T, k], and unless None ``offsets`` int32 [E+1], ``slots`` int32 [T*k]."""
     T, E = logits.shape
     k = ids.shape[1]
-    ld = _rows(logits, T, E, "moe_route", "logits")
-    _plane(ids, (T, k), "torch.int32", "moe_route", "ids")
-    _plane(weights, (T, k), "torch.float32", "moe_route", "weights")
-    if offsets is not None:
-        _plane(offsets, (E + 1,), "torch.int32", "moe_route", "offsets")
-    if slots is not None:
-        _plane(slots, (T * k,), "torch.int32", "moe_route", "slots")
-    if bias is not None:
-        _plane(bias, (E,), "torch.float32", "moe_route", "bias")
-    _check(load().moe_route(logits.data_ptr(), ld, _dtype(logits, "moe_route"),
-                            None if bias is None else bias.data_ptr(), T, E, k, _score(score, "moe_route"), groups,
-                            top_groups, 1 if renorm else 0, scale, ids.data_ptr(), weights.data_ptr(),
-                            None if offsets is None else offsets.data_ptr(),
-                            None if slots is None else slots.data_ptr(), _on(logits, stream)), "moe_route")
+    at = "moe_route"
+    _check((_lib or load()).moe_route(
+        logits.data_ptr(), _rows(logits, T, E, at, "logits"), _dtype(logits, at),
+        None if bias is None else _plane(bias, (E,), "float32", at, "bias"), T, E, k, _score(score, at), groups,
+        top_groups, 1 if renorm else 0, scale, _plane(ids, (T, k), "int32", at, "ids"),
+        _plane(weights, (T, k), "float32", at, "weights"),
+        None if offsets is None else _plane(offsets, (E + 1,), "int32", at, "offsets"),
+        None if slots is None else _plane(slots, (T * k,), "int32", at, "slots"), _on(logits, stream)), at)
     return ids, weights, offsets, slots
 
 
@@ -435,18 +436,15 @@ def moe_route_backward(logits, ids, dweights, dlogits, bias=None, score="softmax
     """Gradient of :func:`moe_route`'s weights to its logits, ``dlogits`` [T, E] in the logits' dtype."""
     T, E = logits.shape
     k = ids.shape[1]
-    ld = _rows(logits, T, E, "moe_route_backward", "logits")
-    ldd = _rows(dlogits, T, E, "moe_route_backward", "dlogits")
-    if dlogits.dtype != logits.dtype:
+    at = "moe_route_backward"
+    if dlogits.dtype is not logits.dtype:
         raise TypeError("moe_route_backward: logits and dlogits must have the same dtype")
-    _plane(ids, (T, k), "torch.int32", "moe_route_backward", "ids")
-    _plane(dweights, (T, k), "torch.float32", "moe_route_backward", "dweights")
-    if bias is not None:
-        _plane(bias, (E,), "torch.float32", "moe_route_backward", "bias")
-    _check(load().moe_route_backward(logits.data_ptr(), ld, _dtype(logits, "moe_route_backward"),
-                                     None if bias is None else bias.data_ptr(), ids.data_ptr(), dweights.data_ptr(),
-                                     dlogits.data_ptr(), ldd, T, E, k, _score(score, "moe_route_backward"),
-                                     1 if renorm else 0, scale, _on(logits, stream)), "moe_route_backward")
+    _check((_lib or load()).moe_route_backward(
+        logits.data_ptr(), _rows(logits, T, E, at, "logits"), _dtype(logits, at),
+        None if bias is None else _plane(bias, (E,), "float32", at, "bias"), _plane(ids, (T, k), "int32", at, "ids"),
+        _plane(dweights, (T, k), "float32", at, "dweights"), dlogits.data_ptr(),
+        _rows(dlogits, T, E, at, "dlogits"), T, E, k, _score(score, at), 1 if renorm else 0, scale,
+        _on(logits, stream)), at)
     return dlogits
 
 
@@ -455,17 +453,14 @@ def moe_experts(gate, up, down, x, ids, weights, offsets, slots, out, stream=Non
     slots as :func:`moe_route` wrote them."""
     T, D = x.shape
     k = ids.shape[1]
-    ldx = _rows(x, T, gate.K, "moe_experts", "x")
-    ldo = _rows(out, T, D, "moe_experts", "out")
-    if out.dtype != x.dtype:
+    at = "moe_experts"
+    if out.dtype is not x.dtype:
         raise TypeError("moe_experts: x and out must have the same dtype")
-    _plane(ids, (T, k), "torch.int32", "moe_experts", "ids")
-    _plane(weights, (T, k), "torch.float32", "moe_experts", "weights")
-    _plane(offsets, (gate.E + 1,), "torch.int32", "moe_experts", "offsets")
-    _plane(slots, (T * k,), "torch.int32", "moe_experts", "slots")
-    _check(load().moe_experts(gate.handle, up.handle, down.handle, x.data_ptr(), ldx, _dtype(x, "moe_experts"),
-                              ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), slots.data_ptr(),
-                              out.data_ptr(), ldo, T, k, _on(x, stream)), "moe_experts")
+    _check((_lib or load()).moe_experts(
+        gate.handle, up.handle, down.handle, x.data_ptr(), _rows(x, T, gate.K, at, "x"), _dtype(x, at),
+        _plane(ids, (T, k), "int32", at, "ids"), _plane(weights, (T, k), "float32", at, "weights"),
+        _plane(offsets, (gate.E + 1,), "int32", at, "offsets"), _plane(slots, (T * k,), "int32", at, "slots"),
+        out.data_ptr(), _rows(out, T, D, at, "out"), T, k, _on(x, stream)), at)
     return out
 
 

@@ -9,8 +9,9 @@
 // a multiple of 128 and k to a multiple of 256 with codes equal to their zero
 // point and scale 0, so padding contributes exactly nothing.  A block holds
 //   codes   [4 chunks of 64 k][32 lanes][16 bytes]       2048 bytes
-//   scales  f16 [256/G groups][16 rows]
-//   zeros   u8  [256/G groups][16 rows]                  (if there are any)
+//   scales  f16 [8 rows g][256/G groups][row g, row g+8]
+//   zeros   u8  the same                                  (if there are any)
+// so all of a block that a lane of the products needs is a few wide loads.
 // The 16 bytes of lane (g = lane/4, t = lane%4) are four words j; word j holds
 // k = 32*(j/2) + 8t + 4*(j%2) + {0,1,2,3} of rows g and g+8, one nibble each:
 //   bits  0.. 3 row g   k+0     16..19 row g   k+1
@@ -39,6 +40,8 @@ __host__ __device__ constexpr int q4_groups(int G) { return Q4_K / G; }
 __host__ __device__ constexpr int q4_block_bytes(int G, bool zeros) {
     return Q4_CODES + Q4_ROWS * q4_groups(G) * (zeros ? 3 : 2);
 }
+// Place of row r (0..15) and group gi of a block among its scales (zeros).
+__host__ __device__ constexpr int q4_scale_index(int r, int gi, int ng) { return ((r & 7) * ng + gi) * 2 + (r >> 3); }
 // Block index of 16-row tile rt and 256-k chunk kc (nkc chunks a row).
 __host__ __device__ inline int64_t q4_block_index(int64_t rt, int64_t kc, int64_t nkc) {
     return ((rt >> 3) * nkc + kc) * 8 + (rt & 7);

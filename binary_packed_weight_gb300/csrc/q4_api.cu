@@ -4,6 +4,7 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <cmath>
 #include <mutex>
 #include <new>
 
@@ -306,7 +307,8 @@ tq2_status moe_experts(q4_handle gate, q4_handle up, q4_handle down, const void*
     float* y = reinterpret_cast<float*>(static_cast<char*>(mem.p) + hbytes);
     // rows of one expert: the average, and room for the spread around it
     const int64_t mean = (S + E - 1) / E;
-    const int64_t most = mean + 2 * mean < T ? mean + 2 * mean : T;
+    const int64_t spread = mean + 2 * (int64_t)ceil(sqrt((double)mean));
+    const int64_t most = spread < T ? spread : T;
     Q4Stream a = stream_of(gate);
     a.w1 = up->blocks;
     a.pair = 1;

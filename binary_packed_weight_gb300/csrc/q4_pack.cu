@@ -49,8 +49,9 @@ q4_pack_kernel(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ s
         for (int i = threadIdx.x; i < 16 * ng; i += 128) {
             const int64_t r = rt * 16 + (i & 15), gi = kc * ng + (i >> 4);
             const bool in = r < N && gi < kg;
-            reinterpret_cast<uint16_t*>(out + Q4_CODES)[i] = in ? scales[r * kg + gi] : (uint16_t)0;
-            if (zeros) out[Q4_CODES + 32 * ng + i] = in ? (zeros[r * kg + gi] & 15) : 0;
+            const int at = q4_scale_index(i & 15, i >> 4, ng);
+            reinterpret_cast<uint16_t*>(out + Q4_CODES)[at] = in ? scales[r * kg + gi] : (uint16_t)0;
+            if (zeros) out[Q4_CODES + 32 * ng + at] = in ? (zeros[r * kg + gi] & 15) : 0;
         }
     }
 }
@@ -72,9 +73,9 @@ q4_dequant_kernel(const uint8_t* __restrict__ blocks, float* __restrict__ out, i
         const int t = (kk & 31) >> 3;
         const uint32_t* words =
             reinterpret_cast<const uint32_t*>(b + (kk >> 6) * 512 + ((r & 7) * 4 + t) * 16) + ((kk >> 5) & 1) * 2;
-        const int gi = kk / G;
-        const float d = __half2float(reinterpret_cast<const __half*>(b + Q4_CODES)[gi * 16 + r]);
-        const int z = zeros ? b[Q4_CODES + 32 * ng + gi * 16 + r] : 8;
+        const int at = q4_scale_index(r, kk / G, ng);
+        const float d = __half2float(reinterpret_cast<const __half*>(b + Q4_CODES)[at]);
+        const int z = zeros ? b[Q4_CODES + 32 * ng + at] : 8;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const uint32_t w = words[j] >> (r >= 8 ? 4 : 0);

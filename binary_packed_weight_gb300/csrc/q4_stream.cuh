@@ -9,22 +9,30 @@
 // f16 range nor its subnormals cut it); a group's sum is scaled by its d in
 // f32.  So the only roundings are those of f32 accumulation.
 //
-// The weights are read once and bound the time.  The matrix is cut into units
-// of 16-row tiles over the whole of k; a CTA walks a contiguous range of
-// units, its eight warps splitting k (KS) and tiles (RT).  Each warp streams
-// its own blocks into a private shared-memory ring by bulk copies issued a
-// ring ahead (one contiguous block of q4.cuh each), so warps wait for each
-// other only at the end of a unit, where the k parts are added in a fixed
-// order.  The activations sit in shared memory for the CTA's whole life (one
-// matrix) or per matrix of the plan.
+// The weights are read once and bound the time.  A CTA takes a contiguous range
+// of 16-row tiles; their blocks (tiles x 256-k chunks) are one sequence that is
+// cut evenly among its sixteen warps, so a warp's part may begin and end inside
+// a tile.  A warp reads its blocks straight into registers, one block ahead of
+// the one it multiplies (34 KB in flight on an SM), and leaves its sum of each
+// tile it touches in shared memory; after the last block the parts of every
+// tile are added in a fixed order.  Only there do warps wait for each other.
+// The activations sit in shared memory for the CTA's whole life (one matrix) or
+// per matrix of the plan.
 //
-// With a plan (offsets, slots) matrix e multiplies the rows of positions
-// offsets[e]..offsets[e+1]; `pair` runs two matrices over the same rows and
-// stores silu(first) * second.
+// A decode call lasts a few microseconds, so what a warp does once counts as
+// much as the blocks (two to six a warp): there is one copy of the block's code,
+// the work is cut with shifts and host-side reciprocals, and more rows than
+// fit are further launches.
+//
+// With a plan (offsets, slots; PLAN) matrix e multiplies the rows of positions
+// offsets[e]..offsets[e+1]; `pair` takes tiles of two matrices in turn over the
+// same rows and stores silu(first) * second.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <atomic>
 
 #include "../../include/tq2.h"
 #include "q4.cuh"
@@ -32,19 +40,20 @@
 
 namespace tq2 {
 
-constexpr int Q4_WARPS = 8;
-constexpr int Q4_MAX_DEPTH = 12;
+constexpr int Q4_WARPS = 16;
 constexpr int Q4_RED_PITCH = 20;       // floats of a 16-row column in the reduction buffer (conflict-free)
 
 struct Q4Kernel {
     Q4Stream a;
     int tok;                           // rows of x a pass takes
     int parts;                         // f16 columns of a row
-    int KS, RT, RU;                    // k splits x row tiles of the warps; units of a pass
-    int depth;
+    int tiles;                         // 16-row tiles of a pass (both matrices' of a pair)
+    int each, more;                    // no plan: tiles of a CTA, and CTAs that take one more
+    int batch;                         // tiles summed together
+    uint32_t rcp;                      // ceil(2^20 / nkc): i / nkc for i * nkc < 2^20
     int pitch;                         // bytes of an activation column in shared memory
     int xvec;                          // rows of x are 16-byte aligned
-    int off_prefix, off_scale, off_red, off_x, off_ring;   // shared-memory layout
+    int off_prefix, off_scale, off_red, off_x;   // shared-memory layout
 };
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -62,6 +71,21 @@ __device__ __forceinline__ void q4_mma(float (&d)[4], const uint32_t (&a)[4], ui
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
         mma_16816_pure(d, a, b0, b1);
+}
+
+// The same with a zero accumulator.
+template <bool BF>
+__device__ __forceinline__ void q4_mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (BF)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+            "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+            "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // The integer weights of a word as an A fragment.  f16: a nibble under the
@@ -98,23 +122,17 @@ __device__ __forceinline__ void q4_decode(uint32_t w, uint32_t z0, uint32_t z1, 
 __device__ __forceinline__ int q4_offset(const Q4Stream& a, int e) { return min(max(a.offsets[e], 0), a.nslots); }
 __device__ __forceinline__ int q4_slot(const Q4Stream& a, int p) { return min(max(a.slots[p], 0), a.nslots - 1); }
 
-// The plan's work: pass j (rows p0 .. p0+cnt of matrix e).
+// Pass j of the plan: rows p0 .. p0+cnt of matrix e.
 struct Q4Pass {
     int e, p0, cnt;
 };
 __device__ __forceinline__ Q4Pass q4_pass(const Q4Kernel& k, const int* prefix, int j) {
-    Q4Pass p;
-    if (!k.a.offsets) {
-        p.e = 0;
-        p.p0 = j * k.tok;
-        p.cnt = min(k.tok, k.a.M - p.p0);
-        return p;
-    }
     int lo = 0, hi = k.a.E;                               // prefix[lo] <= j < prefix[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (prefix[mid] <= j) lo = mid; else hi = mid;
     }
+    Q4Pass p;
     p.e = lo;
     p.p0 = q4_offset(k.a, lo) + (j - prefix[lo]) * k.tok;
     p.cnt = min(k.tok, q4_offset(k.a, lo + 1) - p.p0);
@@ -136,67 +154,71 @@ __device__ __forceinline__ bool q4_stage_x(const Q4Kernel& k, uint8_t* smem, con
     float* inv = reinterpret_cast<float*>(smem + k.off_scale);
     int* top = reinterpret_cast<int*>(inv + 32);
     const int K = (int)k.a.K;
-    bool ok = true;
-    fence_proxy_async_shared();
-    __syncthreads();                                       // the previous rows and their scales are done with
     if (k.a.xmode == Q4_X_RAW16) {
-        if (k.xvec) {
-            if (warp == 0) {
-                if (lane == 0) mbar_arrive_expect_tx(xbar, (uint32_t)(p.cnt * K * 2));
-                __syncwarp();
-                if (lane < p.cnt)
-                    bulk_load(xs + lane * k.pitch,
-                              reinterpret_cast<const uint16_t*>(k.a.x) + q4_xrow(k, p.p0 + lane) * k.a.ldx,
-                              (uint32_t)K * 2, xbar);
-            }
-            ok = mbar_wait(xbar, xphase);
-            xphase ^= 1u;
-        } else {
+        if (!k.xvec) {
+            __syncthreads();                               // the previous rows are done with
             for (int i = warp; i < p.cnt; i += Q4_WARPS) {
                 const uint16_t* src = reinterpret_cast<const uint16_t*>(k.a.x) + q4_xrow(k, p.p0 + i) * k.a.ldx;
                 for (int c = lane; c < K; c += 32) reinterpret_cast<uint16_t*>(xs + i * k.pitch)[c] = src[c];
             }
             __syncthreads();
+            return true;
         }
+        fence_proxy_async_shared();
+        __syncthreads();
+        if (warp == 0) {
+            if (lane == 0) mbar_arrive_expect_tx(xbar, (uint32_t)(p.cnt * K * 2));
+            __syncwarp();
+            if (lane < p.cnt)
+                bulk_load(xs + lane * k.pitch,
+                          reinterpret_cast<const uint16_t*>(k.a.x) + q4_xrow(k, p.p0 + lane) * k.a.ldx,
+                          (uint32_t)K * 2, xbar);
+        }
+        const bool ok = mbar_wait(xbar, xphase);
+        xphase ^= 1u;
         return ok;
     }
+    __syncthreads();                                       // the previous rows and their scales are done with
     if (tid < 32) top[tid] = 0;
     __syncthreads();
-    // nw warps a row
-    const int nw = p.cnt > 4 ? 1 : p.cnt > 2 ? 2 : p.cnt > 1 ? 4 : 8;
-    const int step = nw * 32 * 4, first = ((warp & (nw - 1)) * 32 + lane) * 4;
-    for (int i = warp / nw; i < p.cnt; i += Q4_WARPS / nw) {
-        const float* src = reinterpret_cast<const float*>(k.a.x) + q4_xrow(k, p.p0 + i) * k.a.ldx;
-        float m = 0.f;
-        for (int c = first; c < K; c += step) {
-            float4 v;
-            if (k.xvec) v = *reinterpret_cast<const float4*>(src + c);
-            else v = make_float4(src[c], src[c + 1], src[c + 2], src[c + 3]);
-            m = fmaxf(fmaxf(fmaxf(m, fabsf(v.x)), fmaxf(fabsf(v.y), fabsf(v.z))), fabsf(v.w));
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane == 0) atomicMax(top + i, __float_as_int(m));  // m >= 0: the order of its bits; a maximum has no order
-    }
-    __syncthreads();
+    // nw warps a row, which read it twice (the second time from L1)
+    const int nw = p.cnt > 8 ? 1 : p.cnt > 4 ? 2 : p.cnt > 2 ? 4 : p.cnt > 1 ? 8 : 16;
+    const int step = nw * 128, first = ((warp & (nw - 1)) * 32 + lane) * 4;
     const bool split = k.a.xmode == Q4_X_SPLIT;
-    for (int i = warp / nw; i < p.cnt; i += Q4_WARPS / nw) {
-        const float* src = reinterpret_cast<const float*>(k.a.x) + q4_xrow(k, p.p0 + i) * k.a.ldx;
+    auto load = [&](const float* src, int c) {
+        return k.xvec ? *reinterpret_cast<const float4*>(src + c)
+                      : make_float4(src[c], src[c + 1], src[c + 2], src[c + 3]);
+    };
+    for (int i0 = 0; i0 < p.cnt; i0 += Q4_WARPS / nw) {
+        const int i = i0 + warp / nw;
+        const bool on = i < p.cnt;
+        const float* src = reinterpret_cast<const float*>(k.a.x) + (on ? q4_xrow(k, p.p0 + i) * k.a.ldx : 0);
+        float m = 0.f;
+        if (on) {
+#pragma unroll 2
+            for (int c = first; c < K; c += step) {
+                const float4 f = load(src, c);
+                m = fmaxf(fmaxf(fmaxf(m, fabsf(f.x)), fmaxf(fabsf(f.y), fabsf(f.z))), fabsf(f.w));
+            }
+        }
+        // m >= 0: as integers its bits have its order; a maximum does not depend on the order it is taken in
+        const int wm = __reduce_max_sync(0xffffffffu, __float_as_int(m));
+        if (on && lane == 0) atomicMax(top + i, wm);
+        __syncthreads();
+        if (!on) continue;
         // 2^(14 - exponent of the maximum), kept a normal number; 1 for a row of zeros or one with infinities
         const int be = (top[i] >> 23) & 255;
-        int se = 127 + 14 - (be - 127);
-        if (be == 0) se = 253;
+        int se = be == 0 ? 253 : 127 + 14 - (be - 127);
         if (top[i] == 0 || be == 255) se = 127;
         se = se > 253 ? 253 : se;
         const float s = __int_as_float(se << 23);
         if (lane == 0 && (warp & (nw - 1)) == 0) inv[i] = __int_as_float((254 - se) << 23);
         uint8_t* hi = xs + i * k.parts * k.pitch;
         uint8_t* lo = hi + k.pitch;
+#pragma unroll 2
         for (int c = first; c < K; c += step) {
-            float4 v;
-            if (k.xvec) v = *reinterpret_cast<const float4*>(src + c);
-            else v = make_float4(src[c], src[c + 1], src[c + 2], src[c + 3]);
-            const float f[4] = {v.x * s, v.y * s, v.z * s, v.w * s};
+            const float4 u = load(src, c);
+            const float f[4] = {u.x * s, u.y * s, u.z * s, u.w * s};
             __half h[4], l[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -211,43 +233,78 @@ __device__ __forceinline__ bool q4_stage_x(const Q4Kernel& k, uint8_t* smem, con
     return true;
 }
 
-template <int G, int NT, int RP, bool BF>
-__global__ void __launch_bounds__(Q4_WARPS * 32, NT * RP <= 2 ? 2 : 1)
-q4_stream_kernel(const __grid_constant__ Q4Kernel k) {
+__device__ __forceinline__ uint4 ldg_stream128(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// What a lane holds of a block: codes, scales and zero points.
+template <int G>
+struct Q4Block {
+    static constexpr int NG = Q4_K / G;
+    uint4 w[4];
+    uint32_t s[NG];                    // group: scales of rows g (low) and g+8
+    uint32_t z[NG / 2];                // two groups: zero points of rows g, g+8 each
+    __device__ __forceinline__ void load(const uint8_t* b, int lane, int zeros) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) w[c] = ldg_stream128(b + c * 512 + lane * 16);
+        const uint8_t* p = b + Q4_CODES + (lane >> 2) * (4 * NG);
+        if (NG == 2) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+            s[0] = v.x;
+            s[NG - 1] = v.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NG / 4; ++i) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+                s[(4 * i) % NG] = v.x;
+                s[(4 * i + 1) % NG] = v.y;
+                s[(4 * i + 2) % NG] = v.z;
+                s[(4 * i + 3) % NG] = v.w;
+            }
+        }
+        if (zeros) {
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(b + Q4_CODES + 32 * NG + (lane >> 2) * (2 * NG));
+#pragma unroll
+            for (int i = 0; i < NG / 2; ++i) z[i] = __ldg(q + i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NG / 2; ++i) z[i] = 0x08080808u;
+        }
+    }
+};
+
+template <int G, int NT, bool BF, bool PLAN>
+__global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __grid_constant__ Q4Kernel k) {
     extern __shared__ __align__(128) uint8_t smem[];
-    constexpr int NG = Q4_K / G;
-    constexpr int NB = NT * RP <= 2 ? 2 : 1;               // reduction buffers
-    constexpr int RED = Q4_WARPS * RP * NT * 8 * Q4_RED_PITCH;
+    constexpr int SEG = NT * 8 * Q4_RED_PITCH;             // floats of a part of a tile
     const Q4Stream& a = k.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int ks = warp & (k.KS - 1), rtw = warp / k.KS;
-    const int blk = q4_block_bytes(G, a.zeros != 0);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem) + warp * Q4_MAX_DEPTH;
-    uint64_t* xbar = reinterpret_cast<uint64_t*>(smem) + Q4_WARPS * Q4_MAX_DEPTH;
+    const uint32_t blk = (uint32_t)q4_block_bytes(G, a.zeros != 0);
+    uint64_t* xbar = reinterpret_cast<uint64_t*>(smem);
+    int2* ends = reinterpret_cast<int2*>(smem + 128);      // first and last warp of each tile of a batch
     int* prefix = reinterpret_cast<int*>(smem + k.off_prefix);
     const float* inv = reinterpret_cast<const float*>(smem + k.off_scale);
     float* red = reinterpret_cast<float*>(smem + k.off_red);
-    uint8_t* ring = smem + k.off_ring + (size_t)warp * k.depth * RP * blk;
-    const int nrt = (int)((a.N + 15) / 16);
-    const int tpw = a.pair ? 1 : RP;                       // row tiles of a warp
     const int nkc = a.nkc;
 
-    if (lane == 0)
-        for (int d = 0; d < k.depth; ++d) mbar_init(&bars[d], 1);
     if (tid == 0) {
         mbar_init(xbar, 1);
         fence_mbar_init();
     }
-    // k past the row's end is zero for the kernel's whole life
-    for (int c = 0; c < k.tok * k.parts; ++c)
-        for (int i = (int)a.K + 2 * tid; i < nkc * Q4_K; i += 2 * Q4_WARPS * 32)
-            *reinterpret_cast<uint32_t*>(smem + k.off_x + c * k.pitch + i * 2) = 0u;
-    if (lane == 0) fence_mbar_init();
+    if (a.K != nkc * Q4_K)                                 // k past the row's end is zero for the kernel's whole life
+        for (int c = 0; c < k.tok * k.parts; ++c)
+            for (int i = (int)a.K + 2 * tid; i < nkc * Q4_K; i += 2 * Q4_WARPS * 32)
+                *reinterpret_cast<uint32_t*>(smem + k.off_x + c * k.pitch + i * 2) = 0u;
     __syncthreads();
     pdl_launch_dependents();
 
-    int passes;
-    if (a.offsets) {
+    // the CTA's tiles (whole pairs)
+    const int two = PLAN && a.pair ? 2 : 1;
+    int u0, u1;
+    if (PLAN) {
         pdl_wait();                                        // the plan is an earlier kernel's
         if (warp == 0) {
             int run = 0;
@@ -266,261 +323,272 @@ q4_stream_kernel(const __grid_constant__ Q4Kernel k) {
             if (lane == 0) prefix[a.E] = run;
         }
         __syncthreads();
-        passes = prefix[a.E];
+        const unsigned all = (unsigned)prefix[a.E] * (unsigned)(k.tiles / two);
+        const unsigned each = all / gridDim.x, more = all - each * gridDim.x, b = blockIdx.x;
+        u0 = (int)(b * each + min(b, more)) * two;
+        u1 = u0 + (int)(each + (b < more ? 1u : 0u)) * two;
     } else {
-        passes = (a.M + k.tok - 1) / k.tok;
+        const int b = blockIdx.x;
+        u0 = b * k.each + min(b, k.more);
+        u1 = u0 + k.each + (b < k.more ? 1 : 0);
     }
-    const int64_t units = (int64_t)passes * k.RU;
-    const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
+    if (u0 >= u1) return;                                  // uniform; the plan's wait is done
 
-    // the unit's blocks of this warp: chunk 0 of its row tiles, NULL past the last tile
-    auto tiles = [&](int u, const uint8_t* (&b)[RP]) {
-        const int j = u / k.RU, ru = u - j * k.RU;
-        const int64_t e = a.offsets ? q4_pass(k, prefix, j).e : 0;
-#pragma unroll
-        for (int r = 0; r < RP; ++r) {
-            const int rt = (ru * k.RT + rtw) * tpw + (a.pair ? 0 : r);
-            const uint8_t* w = a.pair && r ? a.w1 : a.w0;
-            b[r] = rt < nrt ? w + e * a.mstride + (q4_block_index(rt, 0, nkc)) * blk : nullptr;
-        }
+    // A batch: tiles of one pass; warp w takes its blocks L*w/16 .. L*(w+1)/16.
+    struct Batch {
+        int j, first, n;                                   // pass, first tile of the pass, tiles
+        int i0, i1;                                        // blocks of this warp
+        const uint8_t* w;                                  // the pass's matrix
     };
-    // the part of k a warp takes turns with the row unit, so that no warp always has the longer one
-    auto first_chunk = [&](int u) { return (ks + u % k.RU) & (k.KS - 1); };
-    // producer side: the next block to fetch
-    int pu = u0, pkc = u0 < u1 ? first_chunk(u0) : 0, pit = 0, pslot = 0;
-    const uint8_t* pb[RP];
-    auto seek = [&]() {                                    // to the next unit with a tile of this warp
-        while (pu < u1) {
-            tiles(pu, pb);
-            pkc = first_chunk(pu);
-            if (pb[0]) return;
-            ++pu;
-        }
+    auto batch_at = [&](int u) {
+        Batch b;
+        b.j = PLAN ? u / k.tiles : 0;
+        b.first = u - b.j * k.tiles;
+        b.n = min(min(u1 - u, k.tiles - b.first), k.batch);
+        const int L = b.n * nkc;
+        b.i0 = L * warp / Q4_WARPS;
+        b.i1 = L * (warp + 1) / Q4_WARPS;
+        b.w = a.w0;
+        if (PLAN) b.w += (int64_t)q4_pass(k, prefix, b.j).e * a.mstride;
+        return b;
     };
-    auto fetch = [&]() {
-        if (pu >= u1) return;
-        if (lane == 0) {
-            const bool two = RP == 2 && pb[RP - 1] != nullptr;
-            mbar_arrive_expect_tx(&bars[pslot], (uint32_t)(two ? 2 * blk : blk));
-            uint8_t* dst = ring + (size_t)pslot * RP * blk;
-            bulk_load(dst, pb[0] + (int64_t)pkc * 8 * blk, (uint32_t)blk, &bars[pslot]);
-            if (two) bulk_load(dst + blk, pb[RP - 1] + (int64_t)pkc * 8 * blk, (uint32_t)blk, &bars[pslot]);
-        }
-        ++pit;
-        if (++pslot == k.depth) pslot = 0;
-        pkc += k.KS;
-        if (pkc >= nkc) {
-            ++pu;
-            seek();
-        }
+    const int64_t second = PLAN && a.pair ? a.w1 - a.w0 : 0;
+    auto block_ptr = [&](const Batch& b, int i) {
+        const int tl = (int)((uint32_t)i * k.rcp >> 20), tile = b.first + tl, kc = i - tl * nkc;
+        const int rt = two == 2 ? tile >> 1 : tile;
+        const uint32_t index = (uint32_t)(((rt >> 3) * nkc + kc) * 8 + (rt & 7));
+        const uint8_t* p = b.w + (int64_t)index * blk;
+        return two == 2 && (tile & 1) ? p + second : p;
     };
-    seek();
-    for (int d = 0; d < k.depth; ++d) fetch();
-    if (!a.offsets) pdl_wait();                            // x is an earlier kernel's; the weights are not
+    Batch b = batch_at(u0);
+    Q4Block<G> cur;
+    if (b.i0 < b.i1) cur.load(block_ptr(b, b.i0), lane, a.zeros);
+    if (!PLAN) pdl_wait();                                 // x is an earlier kernel's; the weights are not
 
-    uint32_t xphase = 0, ph = 0;
-    int slot = 0, it = 0;
-    bool ok = true;
-    int cur = -1;
-    Q4Pass pass{0, 0, 0};
-    const uint32_t xaddr = smem_u32(smem + k.off_x) + t * 16 + g * k.pitch;
-    const uint32_t raddr = smem_u32(ring);
-    int buf = 0;
+    uint32_t xphase = 0;
+    int staged = -1;
+    Q4Pass pass{0, 0, a.M};
+    uint32_t xa[NT];
+    int cols = 0;
 
-    for (int u = u0; u < u1; ++u) {
-        const int j = u / k.RU, ru = u - j * k.RU;
-        if (j != cur) {
-            cur = j;
-            pass = q4_pass(k, prefix, j);
-            if (!q4_stage_x(k, smem, pass, xbar, xphase)) ok = false;
-        }
-        const int cols = pass.cnt * k.parts;
-        const int rt0 = (ru * k.RT + rtw) * tpw;
-        float tot[RP][NT][4];
-#pragma unroll
-        for (int r = 0; r < RP; ++r)
+    for (int u = u0;;) {
+        if (b.j != staged) {
+            staged = b.j;
+            if (PLAN) pass = q4_pass(k, prefix, b.j);
+            q4_stage_x(k, smem, pass, xbar, xphase);       // a wait that ran out is on record; the rest is harmless
+            cols = pass.cnt * k.parts;
+            // columns past the last one repeat it and are not stored
 #pragma unroll
             for (int n = 0; n < NT; ++n)
+                xa[n] = smem_u32(smem + k.off_x) + t * 16 + min(n * 8 + g, cols - 1) * k.pitch;
+        }
+        const int un = u + b.n;
+        const bool again = un < u1;
+        Batch next{};
+        if (again) next = batch_at(un);
+        float tot[NT][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) tot[r][n][i] = 0.f;
-        if (rt0 < nrt) {
-            for (int kc = first_chunk(u); kc < nkc; kc += k.KS) {
-                if (ok && !mbar_wait(&bars[slot], ph)) ok = false;
-                const uint32_t base = raddr + (uint32_t)(slot * RP * blk);
-                const uint8_t* sc = ring + (size_t)slot * RP * blk + Q4_CODES;
-                float acc[RP][NT][4];
-                float d0[RP], d1[RP];
-                uint32_t z0[RP], z1[RP];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint4 wv[RP];
+            for (int i = 0; i < 4; ++i) tot[n][i] = 0.f;
+        int tile = (int)((uint32_t)b.i0 * k.rcp >> 20), kc = b.i0 - tile * nkc;
+        if (b.i0 == b.i1 && again && next.i0 < next.i1) cur.load(block_ptr(next, next.i0), lane, a.zeros);
+
+#pragma unroll 1
+        for (int i = b.i0; i < b.i1; ++i) {
+            Q4Block<G> ahead;
+            if (i + 1 < b.i1) ahead.load(block_ptr(b, i + 1), lane, a.zeros);
+            else if (again && next.i0 < next.i1) ahead.load(block_ptr(next, next.i0), lane, a.zeros);
+            const uint32_t xo = (uint32_t)kc * 512u;
+            float acc[NT][4];
+            float d0, d1;
+            uint32_t z0, z1;
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) wv[r] = lds128(base + (uint32_t)(r * blk + c * 512 + lane * 16));
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        constexpr int HG = G / 32;             // halves of a group
-                        const int half = c * 2 + h, gi = half / HG;
-                        if (half % HG == 0) {
-#pragma unroll
-                            for (int r = 0; r < RP; ++r) {
-                                const uint8_t* s = sc + r * blk;
-                                d0[r] = __half2float(reinterpret_cast<const __half*>(s)[gi * 16 + g]);
-                                d1[r] = __half2float(reinterpret_cast<const __half*>(s)[gi * 16 + g + 8]);
-                                uint32_t za = 8, zb = 8;
-                                if (a.zeros) {
-                                    za = s[NG * 32 + gi * 16 + g];
-                                    zb = s[NG * 32 + gi * 16 + g + 8];
-                                }
-                                if (BF) {
-                                    z0[r] = 0x43004300u + za * 0x00010001u;
-                                    z1[r] = 0x43004300u + zb * 0x00010001u;
-                                } else {
-                                    z0[r] = 0x64006400u + za * 0x00010001u;
-                                    z1[r] = 0x64006400u + zb * 0x00100010u;
-                                    d1[r] *= 0.0625f;
-                                }
-#pragma unroll
-                                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) acc[r][n][i] = 0.f;
-                            }
-                        }
-                        uint4 b[NT];
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            b[n] = make_uint4(0, 0, 0, 0);
-                            if (n * 8 + g < cols)
-                                b[n] = lds128(xaddr + (uint32_t)(n * 8 * k.pitch + kc * 512 + c * 128 + h * 64));
-                        }
-#pragma unroll
-                        for (int jj = 0; jj < 2; ++jj)
-#pragma unroll
-                            for (int r = 0; r < RP; ++r) {
-                                uint32_t f[4];
-                                q4_decode<BF>(h ? (jj ? wv[r].w : wv[r].z) : (jj ? wv[r].y : wv[r].x), z0[r], z1[r],
-                                              f);
-#pragma unroll
-                                for (int n = 0; n < NT; ++n)
-                                    if (n == 0 || n * 8 < cols)
-                                        q4_mma<BF>(acc[r][n], f, jj ? b[n].z : b[n].x, jj ? b[n].w : b[n].y);
-                            }
-                        if (half % HG == HG - 1) {
-#pragma unroll
-                            for (int r = 0; r < RP; ++r)
-#pragma unroll
-                                for (int n = 0; n < NT; ++n) {
-                                    tot[r][n][0] = fmaf(acc[r][n][0], d0[r], tot[r][n][0]);
-                                    tot[r][n][1] = fmaf(acc[r][n][1], d0[r], tot[r][n][1]);
-                                    tot[r][n][2] = fmaf(acc[r][n][2], d1[r], tot[r][n][2]);
-                                    tot[r][n][3] = fmaf(acc[r][n][3], d1[r], tot[r][n][3]);
-                                }
-                        }
-                    }
+            for (int h = 0; h < 8; ++h) {                  // 32 k
+                constexpr int HG = G / 32;
+                const int gi = h / HG;
+                if (h % HG == 0) {
+                    const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&cur.s[gi]));
+                    d0 = d.x;
+                    d1 = BF ? d.y : d.y * 0.0625f;
+                    const uint32_t zz = cur.z[gi / 2] >> (gi % 2 * 16);
+                    z0 = (zz & 255u) * 0x00010001u + (BF ? 0x43004300u : 0x64006400u);
+                    z1 = ((zz >> 8) & 255u) * (BF ? 0x00010001u : 0x00100010u) + (BF ? 0x43004300u : 0x64006400u);
                 }
-                // the values are used: the slot is refilled through the async proxy
-                fence_proxy_async_shared();
-                __syncwarp();
-                ++it;
-                if (++slot == k.depth) { slot = 0; ph ^= 1u; }
-                if (ok) fetch();
+                uint4 x[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    if (n == 0 || n * 8 < cols) x[n] = lds128(xa[n] + xo + h * 64);
+                const uint4& w = cur.w[h >> 1];
+#pragma unroll
+                for (int jj = 0; jj < 2; ++jj) {
+                    uint32_t f[4];
+                    q4_decode<BF>((h & 1) ? (jj ? w.w : w.z) : (jj ? w.y : w.x), z0, z1, f);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        if (n == 0 || n * 8 < cols) {
+                            if (h % HG == 0 && jj == 0) q4_mma0<BF>(acc[n], f, x[n].x, x[n].y);
+                            else q4_mma<BF>(acc[n], f, jj ? x[n].z : x[n].x, jj ? x[n].w : x[n].y);
+                        }
+                }
+                if (h % HG == HG - 1) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        if (n == 0 || n * 8 < cols) {
+                            tot[n][0] = fmaf(acc[n][0], d0, tot[n][0]);
+                            tot[n][1] = fmaf(acc[n][1], d0, tot[n][1]);
+                            tot[n][2] = fmaf(acc[n][2], d1, tot[n][2]);
+                            tot[n][3] = fmaf(acc[n][3], d1, tot[n][3]);
+                        }
+                }
+            }
+            cur = ahead;
+            if (++kc == nkc || i + 1 == b.i1) {            // this warp's part of a tile: [column][16 rows]
+                float* q = red + (warp + tile) * SEG + 2 * t * Q4_RED_PITCH + g;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    q[n * 8 * Q4_RED_PITCH] = tot[n][0];
+                    q[n * 8 * Q4_RED_PITCH + Q4_RED_PITCH] = tot[n][1];
+                    q[n * 8 * Q4_RED_PITCH + 8] = tot[n][2];
+                    q[n * 8 * Q4_RED_PITCH + Q4_RED_PITCH + 8] = tot[n][3];
+                    tot[n][0] = tot[n][1] = tot[n][2] = tot[n][3] = 0.f;
+                }
+                ++tile;
+                kc = 0;
             }
         }
-        // k parts and row tiles meet: [warp][r][column][16 rows]
-        float* rb = red + buf * RED + warp * (RED / Q4_WARPS);
-#pragma unroll
-        for (int r = 0; r < RP; ++r)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (n > 0 && n * 8 >= cols) continue;
-                float* q = rb + ((r * NT + n) * 8 + 2 * t) * Q4_RED_PITCH + g;
-                q[0] = tot[r][n][0];
-                q[Q4_RED_PITCH] = tot[r][n][1];
-                q[8] = tot[r][n][2];
-                q[Q4_RED_PITCH + 8] = tot[r][n][3];
-            }
+        const int L = b.n * nkc;
+        if (tid < b.n)                                     // warps of the tile's first and last block
+            ends[tid] = make_int2(((tid * nkc + 1) * Q4_WARPS - 1) / L, ((tid + 1) * nkc * Q4_WARPS - 1) / L);
         __syncthreads();
-        const int rows = k.RT * tpw * 16;
-        for (int i = tid; i < rows * pass.cnt; i += Q4_WARPS * 32) {
-            const int m = i / rows, row = i - m * rows;
-            const int64_t n = (int64_t)ru * rows + row;
-            if (n >= a.N) continue;
-            const int tile = row >> 4, w0 = (a.pair ? tile : tile / RP) * k.KS, r0 = a.pair ? 0 : tile % RP;
-            auto sum = [&](int r) {                        // k parts in order, then the parts of x
+        // sixteen lanes a tile and row of x: parts in the order of the warps, then of x
+        const int nt = b.n / two;
+        const float rnt = 1.0f / (float)nt;
+        for (int q = tid >> 4; q < nt * pass.cnt; q += Q4_WARPS * 2) {
+            const int m = (int)(((float)q + 0.5f) * rnt), tl = (q - m * nt) * two;
+            const int row = ((b.first + tl) / two) * 16 + (tid & 15);
+            auto sum = [&](int tile_) {
+                const int2 w = ends[tile_];
+                const float* s = red + (w.x + tile_) * SEG + m * k.parts * Q4_RED_PITCH + (tid & 15);
                 float v = 0.f;
-                for (int q = 0; q < k.parts; ++q) {
-                    const float* s = red + buf * RED + w0 * (RED / Q4_WARPS) +
-                                     (r * NT * 8 + m * k.parts + q) * Q4_RED_PITCH + (row & 15);
-                    for (int w = 0; w < k.KS; ++w) v += s[w * (RED / Q4_WARPS)];
+#pragma unroll 1
+                for (int i = w.x; i <= w.y; ++i, s += SEG) {
+                    if (L * i / Q4_WARPS == L * (i + 1) / Q4_WARPS) continue;   // fewer blocks than warps
+                    v += s[0];
+                    if (k.parts == 2) v += s[Q4_RED_PITCH];
                 }
                 return a.xmode == Q4_X_RAW16 ? v : v * inv[m];
             };
-            float v = sum(r0);
-            if (a.pair) {
-                const float up = sum(RP - 1);
+            float v = sum(tl);
+            if (PLAN && a.pair) {
+                const float up = sum(tl + 1);
                 v = v / (1.0f + expf(-v)) * up;
             }
+            if (row >= a.N) continue;
             const int p = pass.p0 + m;
-            const int64_t o = (a.oslot ? (int64_t)q4_slot(a, p) : (int64_t)p) * a.ldo + n;
+            const int64_t o = (PLAN && a.oslot ? (int64_t)q4_slot(a, p) : (int64_t)p) * a.ldo + row;
             if (a.otype == TQ2_F32) reinterpret_cast<float*>(a.out)[o] = v;
             else if (a.otype == TQ2_F16) reinterpret_cast<__half*>(a.out)[o] = __float2half_rn(v);
             else reinterpret_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
         }
-        if (NB == 1) __syncthreads();
-        else buf ^= 1;
+        if (!again) break;
+        u = un;
+        b = next;
+        __syncthreads();                                   // the parts are read before the next batch's are left
     }
-    // every copy issued has landed before the CTA can exit (all were waited for unless a wait ran out)
-    if (!ok)
-        for (; it < pit; ++it) {
-            mbar_wait(&bars[slot], ph);
-            if (++slot == k.depth) { slot = 0; ph ^= 1u; }
-        }
 }
 
-template <int G, int NT, int RP, bool BF>
-cudaError_t q4_stream_launch(Q4Kernel& k, int tok, cudaStream_t st) {
-    const Q4Stream& a = k.a;
-    int dev = 0, sms = 152, optin = 0;
+struct Q4Device {
+    int sms, smem;
+};
+inline Q4Device q4_device() {
+    // attributes of a device never change: asked once
+    static Q4Device known[64];
+    int dev = 0;
     cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-    const int blk = q4_block_bytes(G, a.zeros != 0);
-    const int nrt = (int)((a.N + 15) / 16), tpw = a.pair ? 1 : RP;
-    k.tok = tok;
-    // warps: split k while each warp keeps two chunks a unit, or while units would not fill the GPU
-    int ks = 1;
-    while (ks < Q4_WARPS && a.nkc >= 4 * ks) ks *= 2;
-    while (ks < Q4_WARPS && a.nkc >= 2 * ks && (nrt + tpw * (Q4_WARPS / ks) - 1) / (tpw * (Q4_WARPS / ks)) * (a.offsets ? a.E : 1) < sms)
-        ks *= 2;
-    k.KS = ks;
-    k.RT = Q4_WARPS / ks;
-    k.RU = (nrt + tpw * k.RT - 1) / (tpw * k.RT);
-    auto up = [](int v) { return (v + 127) / 128 * 128; };
-    constexpr int NB = NT * RP <= 2 ? 2 : 1;
-    k.off_prefix = up((Q4_WARPS * Q4_MAX_DEPTH + 1) * 8);
-    k.off_scale = up(k.off_prefix + (a.offsets ? (a.E + 1) * 4 : 0));
-    k.off_red = up(k.off_scale + 64 * 4);
-    k.off_x = up(k.off_red + NB * Q4_WARPS * RP * NT * 8 * Q4_RED_PITCH * 4);
-    k.off_ring = up(k.off_x + tok * k.parts * k.pitch);
-    const int slot = Q4_WARPS * RP * blk;
-    // two CTAs an SM when three ring slots a warp fit beside the rows (the
-    // next launch on the stream then starts its weights early), else one
-    const int half = (optin + 1024) / 2 - 1024;
-    const int occ = NT * RP <= 2 && k.off_ring + 3 * slot <= half ? 2 : 1;
-    k.depth = ((occ == 2 ? half : optin) - k.off_ring) / slot;
-    if (k.depth > (occ == 2 ? 6 : Q4_MAX_DEPTH)) k.depth = occ == 2 ? 6 : Q4_MAX_DEPTH;
-    if (k.depth < 1) return cudaErrorInvalidValue;
-    const size_t smem = (size_t)k.off_ring + (size_t)k.depth * slot;
-    cudaError_t e = cudaFuncSetAttribute(q4_stream_kernel<G, NT, RP, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
-    if (e != cudaSuccess) return e;
-    int64_t units = a.offsets ? (int64_t)sms * occ : (int64_t)((a.M + tok - 1) / tok) * k.RU;
-    const int grid = (int)(units < (int64_t)sms * occ ? units : (int64_t)sms * occ);
-    return launch_pdl(q4_stream_kernel<G, NT, RP, BF>, dim3((unsigned)grid), dim3(Q4_WARPS * 32), smem, st, k);
+    Q4Device d = dev < 64 ? known[dev] : Q4Device{0, 0};
+    if (d.sms == 0) {
+        cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+        cudaDeviceGetAttribute(&d.smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+        if (dev < 64) known[dev] = d;
+    }
+    return d;
 }
 
-// The variant by sizes: column tiles (NT) for the rows a pass takes, limited
-// by what shared memory holds beside two ring slots a warp; two row tiles a
-// warp (RP) share the activations' shared-memory reads.
+// Shared memory beside the activation columns, for batches of `batch` tiles.
+template <int NT>
+int q4_fixed(const Q4Stream& a, int batch, Q4Kernel* k) {
+    auto up = [](int v) { return (v + 127) / 128 * 128; };
+    const int prefix = 256;
+    const int scale = up(prefix + (a.offsets ? (a.E + 1) * 4 : 0));
+    const int red = scale + 256;
+    const int x = up(red + (Q4_WARPS + batch - 1) * NT * 8 * Q4_RED_PITCH * 4);
+    if (k) {
+        k->off_prefix = prefix;
+        k->off_scale = scale;
+        k->off_red = red;
+        k->off_x = x;
+    }
+    return x;
+}
+
+constexpr int Q4_MAX_BATCH = 16;
+
+template <int G, int NT, bool BF, bool PLAN>
+cudaError_t q4_stream_launch(Q4Kernel& k, int tok, const Q4Device& dev, cudaStream_t st) {
+    const Q4Stream& a = k.a;
+    k.tok = tok;
+    k.tiles = (int)((a.N + 15) / 16) * (a.pair ? 2 : 1);
+    k.rcp = ((1u << 20) + a.nkc - 1) / a.nkc;
+    const int grid = PLAN || k.tiles > dev.sms ? dev.sms : k.tiles;
+    k.each = k.tiles / grid;
+    k.more = k.tiles - k.each * grid;
+    // no longer batches than a CTA has tiles, nor than shared memory holds
+    int batch = PLAN || k.each >= Q4_MAX_BATCH ? Q4_MAX_BATCH : k.each + 1;
+    const int xbytes = tok * k.parts * k.pitch;
+    if (a.pair) batch = (batch + 1) / 2 * 2;
+    while (batch > 2 && q4_fixed<NT>(a, batch, nullptr) + xbytes > dev.smem) batch -= 2;
+    k.batch = batch;
+    const int smem = q4_fixed<NT>(a, k.batch, &k) + xbytes;
+    if (smem > dev.smem) return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> raised{0};                // devices whose limit of this kernel is raised
+    int d = 0;
+    cudaGetDevice(&d);
+    if (smem > 48 * 1024 && (d >= 64 || !((raised.load(std::memory_order_relaxed) >> d) & 1))) {
+        cudaError_t e = cudaFuncSetAttribute(q4_stream_kernel<G, NT, BF, PLAN>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, dev.smem);
+        if (e != cudaSuccess) return e;
+        if (d < 64) raised.fetch_or(uint64_t(1) << d, std::memory_order_relaxed);
+    }
+    if (PLAN)
+        return launch_pdl(q4_stream_kernel<G, NT, BF, PLAN>, dim3((unsigned)grid), dim3(Q4_WARPS * 32), (size_t)smem,
+                          st, k);
+    // rows beyond a pass: further launches
+    const int M = a.M;
+    const size_t xs = (a.xmode == Q4_X_RAW16 ? 2 : 4) * (size_t)a.ldx, os = (a.otype == TQ2_F32 ? 4 : 2) * (size_t)a.ldo;
+    cudaError_t e = cudaSuccess;
+    for (int m = 0; m < M && e == cudaSuccess; m += tok) {
+        Q4Kernel p = k;
+        p.a.M = M - m < tok ? M - m : tok;
+        p.a.x = static_cast<const char*>(a.x) + m * xs;
+        p.a.out = static_cast<char*>(a.out) + m * os;
+        e = launch_pdl(q4_stream_kernel<G, NT, BF, PLAN>, dim3((unsigned)grid), dim3(Q4_WARPS * 32), (size_t)smem, st,
+                       p);
+    }
+    return e;
+}
+
+template <int G, int NT>
+cudaError_t q4_stream_pick(Q4Kernel& k, int tok, const Q4Device& dev, cudaStream_t st) {
+    if (k.a.offsets)
+        return k.a.bf16 ? q4_stream_launch<G, NT, true, true>(k, tok, dev, st)
+                        : q4_stream_launch<G, NT, false, true>(k, tok, dev, st);
+    return k.a.bf16 ? q4_stream_launch<G, NT, true, false>(k, tok, dev, st)
+                    : q4_stream_launch<G, NT, false, false>(k, tok, dev, st);
+}
+
+// The variant by sizes: column tiles (NT) for the rows a pass takes, as far as
+// shared memory holds their columns; f32 rows take two columns each.
 template <int G>
 cudaError_t q4_stream_run(const Q4Stream& a, cudaStream_t st) {
     Q4Kernel k{};
@@ -529,37 +597,18 @@ cudaError_t q4_stream_run(const Q4Stream& a, cudaStream_t st) {
     k.pitch = a.nkc * Q4_K * 2 + 64;
     const int el = a.xmode == Q4_X_RAW16 ? 2 : 4;
     k.xvec = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && (a.ldx * el) % 16 == 0;
-    int dev = 0, optin = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-    const int blk = q4_block_bytes(G, a.zeros != 0);
-    const int nrt = (int)((a.N + 15) / 16);
-    auto room = [&](int nt, int rp) {                      // columns that fit
-        const int nb = nt * rp <= 2 ? 2 : 1;
-        const int fixed = 2048 + (a.offsets ? (a.E + 1) * 4 : 0) + nb * Q4_WARPS * rp * nt * 8 * Q4_RED_PITCH * 4 +
-                          2 * Q4_WARPS * rp * blk;
-        const int c = (optin - fixed) / k.pitch;
-        return c < 8 * nt ? (c < 0 ? 0 : c) : 8 * nt;
-    };
-    const int want = a.tokens * k.parts;
-    auto tokens = [&](int nt, int rp) {
-        const int c = room(nt, rp) / k.parts;
+    const Q4Device dev = q4_device();
+    auto tokens = [&](int nt, int fixed) {                 // rows a pass of nt column tiles can take
+        int c = (dev.smem - fixed) / k.pitch;
+        c = (c < 8 * nt ? c : 8 * nt) / k.parts;
         return c < a.tokens ? c : a.tokens;
     };
-    if (want > 16 && tokens(4, 2) > tokens(2, 2) && tokens(2, 2) > 0)
-        return a.bf16 ? q4_stream_launch<G, 4, 2, true>(k, tokens(4, 2), st)
-                      : q4_stream_launch<G, 4, 2, false>(k, tokens(4, 2), st);
-    if (want > 8 && tokens(2, 2) > tokens(1, 2) && tokens(1, 2) > 0)
-        return a.bf16 ? q4_stream_launch<G, 2, 2, true>(k, tokens(2, 2), st)
-                      : q4_stream_launch<G, 2, 2, false>(k, tokens(2, 2), st);
-    int sms = 152;
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const bool wide = tokens(1, 2) > 0 && (a.pair || nrt >= 8 * sms);
-    const int tok = wide ? tokens(1, 2) : tokens(1, 1);
-    if (tok < 1 || (a.pair && !wide)) return cudaErrorInvalidValue;
-    if (wide)
-        return a.bf16 ? q4_stream_launch<G, 1, 2, true>(k, tok, st) : q4_stream_launch<G, 1, 2, false>(k, tok, st);
-    return a.bf16 ? q4_stream_launch<G, 1, 1, true>(k, tok, st) : q4_stream_launch<G, 1, 1, false>(k, tok, st);
+    const int t4 = tokens(4, q4_fixed<4>(a, 2, nullptr)), t2 = tokens(2, q4_fixed<2>(a, 2, nullptr)),
+              t1 = tokens(1, q4_fixed<1>(a, 2, nullptr));
+    if (t4 > t2 && t4 * k.parts > 16) return q4_stream_pick<G, 4>(k, t4, dev, st);
+    if (t2 > t1 && t2 * k.parts > 8) return q4_stream_pick<G, 2>(k, t2, dev, st);
+    if (t1 < 1) return cudaErrorInvalidValue;
+    return q4_stream_pick<G, 1>(k, t1, dev, st);
 }
 
 }  // namespace tq2
