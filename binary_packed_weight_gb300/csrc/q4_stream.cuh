@@ -93,27 +93,37 @@ __device__ __forceinline__ void q4_mma0(float (&d)[4], const uint32_t (&a)[4], u
 // 1024 + z (1024 + 16 z) is exact, and rows g+8 come out times 16, which their
 // scale takes back.  bf16 has 7 mantissa bits: every nibble is shifted low
 // and read as 128 + c.
+// (M is a value of the register file that the compiler cannot see through: as a
+// literal it is loaded anew for every word.)
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t m) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(m));
+    return r;
+}
 template <bool BF>
-__device__ __forceinline__ void q4_decode(uint32_t w, uint32_t z0, uint32_t z1, uint32_t (&a)[4]) {
+__device__ __forceinline__ uint32_t q4_exponent() {
+    uint32_t m;
+    if (BF) asm volatile("mov.b32 %0, 0x43004300;" : "=r"(m));
+    else asm volatile("mov.b32 %0, 0x64006400;" : "=r"(m));
+    return m;
+}
+template <bool BF>
+__device__ __forceinline__ void q4_decode(uint32_t w, uint32_t m, uint32_t z0, uint32_t z1, uint32_t (&a)[4]) {
     constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;
-    if (BF) {
-        constexpr uint32_t M = 0x43004300u;
-        const uint32_t v[4] = {(w & LO) | M, ((w >> 4) & LO) | M, ((w >> 8) & LO) | M, ((w >> 12) & LO) | M};
+    const uint32_t w8 = w >> 8;
+    const uint32_t v[4] = {and_or<LO>(w, m), BF ? and_or<LO>(w >> 4, m) : and_or<HI>(w, m), and_or<LO>(w8, m),
+                           BF ? and_or<LO>(w >> 12, m) : and_or<HI>(w8, m)};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v[i]),
-                                       *reinterpret_cast<const __nv_bfloat162*>((i & 1) ? &z1 : &z0));
-            a[i] = *reinterpret_cast<uint32_t*>(&r);
-        }
-    } else {
-        constexpr uint32_t M = 0x64006400u;
-        const uint32_t w8 = w >> 8;
-        const uint32_t v[4] = {(w & LO) | M, (w & HI) | M, (w8 & LO) | M, (w8 & HI) | M};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&v[i]),
-                                *reinterpret_cast<const __half2*>((i & 1) ? &z1 : &z0));
-            a[i] = *reinterpret_cast<uint32_t*>(&r);
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t z = (i & 1) ? z1 : z0;
+        if (BF) {
+            const __nv_bfloat162 r =
+                __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v[i]), *reinterpret_cast<const __nv_bfloat162*>(&z));
+            a[i] = *reinterpret_cast<const uint32_t*>(&r);
+        } else {
+            const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&v[i]), *reinterpret_cast<const __half2*>(&z));
+            a[i] = *reinterpret_cast<const uint32_t*>(&r);
         }
     }
 }
@@ -365,6 +375,7 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
     if (b.i0 < b.i1) cur.load(block_ptr(b, b.i0), lane, a.zeros);
     if (!PLAN) pdl_wait();                                 // x is an earlier kernel's; the weights are not
 
+    const uint32_t expo = q4_exponent<BF>();
     uint32_t xphase = 0;
     int staged = -1;
     Q4Pass pass{0, 0, a.M};
@@ -423,7 +434,7 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
 #pragma unroll
                 for (int jj = 0; jj < 2; ++jj) {
                     uint32_t f[4];
-                    q4_decode<BF>((h & 1) ? (jj ? w.w : w.z) : (jj ? w.y : w.x), z0, z1, f);
+                    q4_decode<BF>((h & 1) ? (jj ? w.w : w.z) : (jj ? w.y : w.x), expo, z0, z1, f);
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
                         if (n == 0 || n * 8 < cols) {
