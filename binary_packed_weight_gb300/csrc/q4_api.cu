@@ -139,6 +139,9 @@ cudaError_t launch_combine(const float* y, const int32_t* ids, const float* w, v
                       ldo, T_, D, k, D % 4 == 0 ? 1 : 0);
 }
 
+// Average rows of a matrix from which f16 and bf16 calls take the tensor-core path.
+constexpr int64_t MOE_TENSOR_ROWS = 32;
+
 // Scratch of one call, given back on the same stream whatever happens.
 struct Scratch {
     void* p = nullptr;
@@ -194,13 +197,18 @@ tq2_status q4_upload(const uint8_t* codes, const uint16_t* scales, const uint8_t
     const size_t ngroups = (size_t)E * N * (K / group);
     void* tmp[3] = {nullptr, nullptr, nullptr};
     const void* dev[3] = {nullptr, nullptr, nullptr};
-    cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&w->blocks), (size_t)E * w->mstride);
+    // the bounds sit behind the blocks
+    const size_t blocks_bytes = ((size_t)E * w->mstride + 255) / 256 * 256;
+    cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&w->blocks), blocks_bytes + (size_t)E * 4);
+    if (e == cudaSuccess) w->bound = reinterpret_cast<float*>(w->blocks + blocks_bytes);
     if (e == cudaSuccess) e = to_device(codes, (size_t)E * N * (K / 2), &tmp[0], &dev[0], st);
     if (e == cudaSuccess) e = to_device(scales, ngroups * 2, &tmp[1], &dev[1], st);
     if (e == cudaSuccess && zeros) e = to_device(zeros, ngroups, &tmp[2], &dev[2], st);
     if (e == cudaSuccess)
         e = launch_q4_pack(static_cast<const uint8_t*>(dev[0]), static_cast<const uint16_t*>(dev[1]),
                            static_cast<const uint8_t*>(dev[2]), w, st);
+    if (e == cudaSuccess)
+        e = launch_q4_bound(static_cast<const uint16_t*>(dev[1]), static_cast<const uint8_t*>(dev[2]), w, st);
     for (void* p : tmp)
         if (p) cudaFreeAsync(p, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
@@ -296,15 +304,31 @@ tq2_status moe_experts(q4_handle gate, q4_handle up, q4_handle down, const void*
         return (tq2_status)set_error(TQ2_EINVAL, "moe_experts: null pointer");
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int64_t S = T * k;
-    const size_t hbytes = ((size_t)S * F * 4 + 255) / 256 * 256;
+    auto combine = [&](const float* y) {
+        if (dtype == TQ2_F32) return launch_combine<float>(y, ids, weights, out, ldo, T, (int)D, k, st);
+        if (dtype == TQ2_F16) return launch_combine<__half>(y, ids, weights, out, ldo, T, (int)D, k, st);
+        return launch_combine<__nv_bfloat16>(y, ids, weights, out, ldo, T, (int)D, k, st);
+    };
     Scratch mem(st);
-    cudaError_t e = scratch_alloc(&mem.p, hbytes + (size_t)S * D * 4, st);
+    const size_t ybytes = ((size_t)S * D * 4 + 255) / 256 * 256;
+    if (dtype != TQ2_F32 && S >= MOE_TENSOR_ROWS * E) {
+        cudaError_t e = scratch_alloc(&mem.p, ybytes + moe_tensor_scratch(S, D, F), st);
+        if (e != cudaSuccess) {
+            mem.p = nullptr;
+            return cuda_status(e, "moe_experts: scratch");
+        }
+        const MoeTensor m{gate, up, down, x, ldx, dtype, offsets, slots, (int)S, k, static_cast<float*>(mem.p)};
+        e = launch_moe_tensor(m, static_cast<char*>(mem.p) + ybytes, st);
+        if (e == cudaSuccess) e = combine(m.y);
+        return cuda_status(e, "moe_experts: tensor path");
+    }
+    cudaError_t e = scratch_alloc(&mem.p, ybytes + (size_t)S * F * 4, st);
     if (e != cudaSuccess) {
         mem.p = nullptr;
         return cuda_status(e, "moe_experts: scratch");
     }
-    float* hid = static_cast<float*>(mem.p);
-    float* y = reinterpret_cast<float*>(static_cast<char*>(mem.p) + hbytes);
+    float* y = static_cast<float*>(mem.p);
+    float* hid = reinterpret_cast<float*>(static_cast<char*>(mem.p) + ybytes);
     // rows of one expert: the average, and room for the spread around it
     const int64_t mean = (S + E - 1) / E;
     const int64_t spread = mean + 2 * (int64_t)ceil(sqrt((double)mean));
@@ -340,9 +364,7 @@ tq2_status moe_experts(q4_handle gate, q4_handle up, q4_handle down, const void*
     b.tokens = a.tokens;
     e = launch_q4_stream(b, st);
     if (e != cudaSuccess) return cuda_status(e, "moe_experts: down");
-    if (dtype == TQ2_F32) e = launch_combine<float>(y, ids, weights, out, ldo, T, (int)D, k, st);
-    else if (dtype == TQ2_F16) e = launch_combine<__half>(y, ids, weights, out, ldo, T, (int)D, k, st);
-    else e = launch_combine<__nv_bfloat16>(y, ids, weights, out, ldo, T, (int)D, k, st);
+    e = combine(y);
     return cuda_status(e, "moe_experts: combine");
 }
 

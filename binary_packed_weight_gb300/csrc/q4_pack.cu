@@ -31,19 +31,19 @@ q4_pack_kernel(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ s
     for (int64_t b = blockIdx.x; b < nblocks; b += gridDim.x) {
         const int64_t sub = b & 7, kc = (b >> 3) % nkc, rt = ((b >> 3) / nkc) * 8 + sub;
         uint8_t* out = blocks + b * blk;
-        const int64_t r0 = rt * 16 + (lane >> 2), r1 = r0 + 8;
+        const int g = lane & 7, t = lane >> 3;
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int64_t k = kc * 256 + c * 64 + 32 * (j >> 1) + 8 * (lane & 3) + 4 * (j & 1);
-            auto four = [&](int64_t r) -> uint32_t {          // codes k..k+3 of row r
-                if (r < N && k < K) return *reinterpret_cast<const uint16_t*>(codes + r * (K / 2) + k / 2);
-                return zeros ? 0u : 0x8888u;                   // padding: the code of its zero point
-            };
-            const uint32_t p = four(r0), q = four(r1);
-            w[j] = (p & 15u) | ((q & 15u) << 4) | (((p >> 8) & 15u) << 8) | (((q >> 8) & 15u) << 12) |
-                   (((p >> 4) & 15u) << 16) | (((q >> 4) & 15u) << 20) | (((p >> 12) & 15u) << 24) |
-                   (((q >> 12) & 15u) << 28);
+            const int64_t k = kc * 256 + c * 64 + 32 * (j & 1) + 8 * t, r = rt * 16 + g + 8 * (j >> 1);
+            uint32_t p = zeros ? 0u : 0x88888888u;             // padding: the code of its zero point
+            if (r < N && k < K) {
+                const uint16_t* src = reinterpret_cast<const uint16_t*>(codes + r * (K / 2) + k / 2);
+                p = src[0] | ((uint32_t)src[1] << 16);         // code i of k+i in bits 4i
+            }
+            w[j] = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[j] |= ((p >> (4 * i)) & 15u) << (4 * (i >> 1) + 16 * (i & 1));
         }
         *reinterpret_cast<uint4*>(out + c * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
         for (int i = threadIdx.x; i < 16 * ng; i += 128) {
@@ -54,6 +54,29 @@ q4_pack_kernel(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ s
             if (zeros) out[Q4_CODES + 32 * ng + at] = in ? (zeros[r * kg + gi] & 15) : 0;
         }
     }
+}
+
+// A warp a row: its 2-norm is at most sqrt(G sum_g (d_g max|c - z_g|)^2); the
+// largest of a matrix, as the bits of a non-negative float (a maximum has no order).
+__global__ void __launch_bounds__(256)
+q4_bound_kernel(const uint16_t* __restrict__ scales, const uint8_t* __restrict__ zeros, float* __restrict__ bound,
+                int64_t N, int64_t kg, int G) {
+    const int lane = threadIdx.x & 31;
+    scales += (int64_t)blockIdx.y * N * kg;
+    if (zeros) zeros += (int64_t)blockIdx.y * N * kg;
+    float most = 0.f;
+    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < N; r += (int64_t)gridDim.x * 8) {
+        float s = 0.f;
+        for (int64_t i = lane; i < kg; i += 32) {
+            const int z = zeros ? zeros[r * kg + i] & 15 : 8;
+            const float v = __half2float(__ushort_as_half(scales[r * kg + i])) * (float)(z > 15 - z ? z : 15 - z);
+            s = fmaf(v, v, s);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        most = fmaxf(most, sqrtf(s * (float)G));
+    }
+    if (lane == 0) atomicMax(reinterpret_cast<int*>(bound) + blockIdx.y, __float_as_int(most));
 }
 
 // One thread per (row, 8 k): out[e][row][k..k+7], exact in f32 (5 + 11 bits).
@@ -71,20 +94,14 @@ q4_dequant_kernel(const uint8_t* __restrict__ blocks, float* __restrict__ out, i
         const int kk = (int)(k & 255);
         const uint8_t* b = blocks + q4_block_index(row >> 4, k >> 8, nkc) * blk;
         const int t = (kk & 31) >> 3;
-        const uint32_t* words =
-            reinterpret_cast<const uint32_t*>(b + (kk >> 6) * 512 + ((r & 7) * 4 + t) * 16) + ((kk >> 5) & 1) * 2;
+        const uint32_t w = reinterpret_cast<const uint32_t*>(b + (kk >> 6) * 512 + (t * 8 + (r & 7)) * 16)
+            [2 * (r >> 3) + ((kk >> 5) & 1)];
         const int at = q4_scale_index(r, kk / G, ng);
         const float d = __half2float(reinterpret_cast<const __half*>(b + Q4_CODES)[at]);
         const int z = zeros ? b[Q4_CODES + 32 * ng + at] : 8;
+        float* o = out + row * K + k;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t w = words[j] >> (r >= 8 ? 4 : 0);
-            float* o = out + row * K + k + 4 * j;
-            o[0] = (float)((int)(w & 15u) - z) * d;
-            o[1] = (float)((int)((w >> 16) & 15u) - z) * d;
-            o[2] = (float)((int)((w >> 8) & 15u) - z) * d;
-            o[3] = (float)((int)((w >> 24) & 15u) - z) * d;
-        }
+        for (int i = 0; i < 8; ++i) o[i] = (float)((int)((w >> (4 * (i >> 1) + 16 * (i & 1))) & 15u) - z) * d;
     }
 }
 
@@ -148,6 +165,15 @@ cudaError_t launch_q4_pack(const uint8_t* codes, const uint16_t* scales, const u
     const int64_t nblocks = (w->N + 127) / 128 * 8 * w->nkc;
     q4_pack_kernel<<<dim3(grid_of(nblocks), (unsigned)w->E), 128, 0, st>>>(codes, scales, zeros, w->blocks, w->N,
                                                                          w->K, w->nkc, w->group, w->mstride, nblocks);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_q4_bound(const uint16_t* scales, const uint8_t* zeros, const q4_weight* w, cudaStream_t st) {
+    cudaError_t e = cudaMemsetAsync(w->bound, 0, (size_t)w->E * 4, st);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)((w->N + 7) / 8 < 256 ? (w->N + 7) / 8 : 256);
+    q4_bound_kernel<<<dim3(grid, (unsigned)w->E), 256, 0, st>>>(scales, zeros, w->bound, w->N, w->K / w->group,
+                                                               w->group);
     return cudaGetLastError();
 }
 

@@ -88,49 +88,8 @@ __device__ __forceinline__ void q4_mma0(float (&d)[4], const uint32_t (&a)[4], u
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// The integer weights of a word as an A fragment.  f16: a nibble under the
-// exponent of 1024 is 1024 + c (low) or 1024 + 16 c (bits 4..7); subtracting
-// 1024 + z (1024 + 16 z) is exact, and rows g+8 come out times 16, which their
-// scale takes back.  bf16 has 7 mantissa bits: every nibble is shifted low
-// and read as 128 + c.
-// (M is a value of the register file that the compiler cannot see through: as a
-// literal it is loaded anew for every word.)
-template <uint32_t MASK>
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t m) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(m));
-    return r;
-}
-template <bool BF>
-__device__ __forceinline__ uint32_t q4_exponent() {
-    uint32_t m;
-    if (BF) asm volatile("mov.b32 %0, 0x43004300;" : "=r"(m));
-    else asm volatile("mov.b32 %0, 0x64006400;" : "=r"(m));
-    return m;
-}
-template <bool BF>
-__device__ __forceinline__ void q4_decode(uint32_t w, uint32_t m, uint32_t z0, uint32_t z1, uint32_t (&a)[4]) {
-    constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;
-    const uint32_t w8 = w >> 8;
-    const uint32_t v[4] = {and_or<LO>(w, m), BF ? and_or<LO>(w >> 4, m) : and_or<HI>(w, m), and_or<LO>(w8, m),
-                           BF ? and_or<LO>(w >> 12, m) : and_or<HI>(w8, m)};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t z = (i & 1) ? z1 : z0;
-        if (BF) {
-            const __nv_bfloat162 r =
-                __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v[i]), *reinterpret_cast<const __nv_bfloat162*>(&z));
-            a[i] = *reinterpret_cast<const uint32_t*>(&r);
-        } else {
-            const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&v[i]), *reinterpret_cast<const __half2*>(&z));
-            a[i] = *reinterpret_cast<const uint32_t*>(&r);
-        }
-    }
-}
-
-// A plan's values, kept inside their ranges whatever it holds.
-__device__ __forceinline__ int q4_offset(const Q4Stream& a, int e) { return min(max(a.offsets[e], 0), a.nslots); }
-__device__ __forceinline__ int q4_slot(const Q4Stream& a, int p) { return min(max(a.slots[p], 0), a.nslots - 1); }
+__device__ __forceinline__ int q4_offset(const Q4Stream& a, int e) { return plan_offset(a.offsets, a.nslots, e); }
+__device__ __forceinline__ int q4_slot(const Q4Stream& a, int p) { return plan_slot(a.slots, a.nslots, p); }
 
 // Pass j of the plan: rows p0 .. p0+cnt of matrix e.
 struct Q4Pass {
@@ -259,7 +218,7 @@ struct Q4Block {
     uint32_t z[NG / 2];                // two groups: zero points of rows g, g+8 each
     __device__ __forceinline__ void load(const uint8_t* b, int lane, int zeros) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) w[c] = ldg_stream128(b + c * 512 + lane * 16);
+        for (int c = 0; c < 4; ++c) w[c] = ldg_stream128(b + c * 512 + ((lane & 3) * 8 + (lane >> 2)) * 16);
         const uint8_t* p = b + Q4_CODES + (lane >> 2) * (4 * NG);
         if (NG == 2) {
             const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
@@ -413,7 +372,7 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
             const uint32_t xo = (uint32_t)kc * 512u;
             float acc[NT][4];
             float d0, d1;
-            uint32_t z0, z1;
+            Q4Zero z0, z1;
 #pragma unroll
             for (int h = 0; h < 8; ++h) {                  // 32 k
                 constexpr int HG = G / 32;
@@ -421,20 +380,22 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
                 if (h % HG == 0) {
                     const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&cur.s[gi]));
                     d0 = d.x;
-                    d1 = BF ? d.y : d.y * 0.0625f;
+                    d1 = d.y;
                     const uint32_t zz = cur.z[gi / 2] >> (gi % 2 * 16);
-                    z0 = (zz & 255u) * 0x00010001u + (BF ? 0x43004300u : 0x64006400u);
-                    z1 = ((zz >> 8) & 255u) * (BF ? 0x00010001u : 0x00100010u) + (BF ? 0x43004300u : 0x64006400u);
+                    z0 = q4_zero<BF>(zz & 255u);
+                    z1 = q4_zero<BF>((zz >> 8) & 255u);
                 }
                 uint4 x[NT];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     if (n == 0 || n * 8 < cols) x[n] = lds128(xa[n] + xo + h * 64);
                 const uint4& w = cur.w[h >> 1];
+                uint32_t p[4], q[4];                       // pairs of rows g and g+8
+                q4_decode<BF>((h & 1) ? w.y : w.x, expo, z0, p);
+                q4_decode<BF>((h & 1) ? w.w : w.z, expo, z1, q);
 #pragma unroll
                 for (int jj = 0; jj < 2; ++jj) {
-                    uint32_t f[4];
-                    q4_decode<BF>((h & 1) ? (jj ? w.w : w.z) : (jj ? w.y : w.x), expo, z0, z1, f);
+                    const uint32_t f[4] = {p[2 * jj], q[2 * jj], p[2 * jj + 1], q[2 * jj + 1]};
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
                         if (n == 0 || n * 8 < cols) {

@@ -4,7 +4,9 @@ Ids and the plan are equal, whatever is masked.  Bounds (derived before the
 first run): a score is a handful of f32 operations (exp within 2 ulp, a sum of
 at most 1024 positives as a tree of depth 10, a division), so weights are
 within 2^-19 of their size; their gradient adds sums over at most 32 terms
-whose absolute sum scales it.  Products are bounded as in test_gpu_q4.py.
+whose absolute sum scales it.  Products are bounded as in test_gpu_q4.py; with
+many tokens an expert (f16, bf16) the weights are rounded to f16 as well, up to
+2^-11 of each, and one accumulator runs over all of k, K/16 steps of 2^-22.
 """
 import numpy as np
 import pytest
@@ -196,7 +198,9 @@ def run_experts(lib, x, ids, weights, w3, dtype, E, pad=0):
 @pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
 @pytest.mark.parametrize("T,E,k,D,F,group,zeros", [(1, 4, 2, 256, 128, 128, False), (1, 1, 1, 128, 32, 32, True),
                                                    (6, 8, 3, 384, 96, 32, True), (40, 5, 2, 256, 320, 64, False),
-                                                   (90, 3, 3, 128, 64, 32, False), (17, 16, 4, 288, 1056, 32, True)])
+                                                   (90, 3, 3, 128, 64, 32, False), (17, 16, 4, 288, 1056, 32, True),
+                                                   (600, 2, 1, 384, 96, 32, True), (300, 4, 2, 544, 352, 32, False),
+                                                   (130, 1, 1, 256, 1024, 128, True), (700, 3, 2, 64, 192, 64, True)])
 def test_experts(lib, dtype, T, E, k, D, F, group, zeros):
     rng = np.random.default_rng(T + E)
     mats, handles = [], []
@@ -215,10 +219,33 @@ def test_experts(lib, dtype, T, E, k, D, F, group, zeros):
     x, got = run_experts(lib, rng.normal(size=(T, D)) * 0.2, ids, weights, handles, dtype, E, pad=5 if T == 6 else 0)
     want = omoe.experts(x, ids, weights, *mats)
     eps = (8 + max(D, F) / group + 16) * 2.0 ** -22 + 2.0 ** -22
+    if dtype != "float32" and T * k >= 32 * E:                        # the path of many tokens an expert
+        eps = 2.0 ** -11 + (max(D, F) / 16 + 16) * 2.0 ** -22
     bound = omoe.experts_bound(x, ids, weights, *mats, eps, eps, 2.0 ** -20 if dtype == "float32" else 2.0 ** -11)
     bound = 1.01 * bound + (k * 2.0 ** -23) * np.abs(bound) + (HALF_ULP[dtype] + k * 2.0 ** -22) * np.abs(want) + 1e-7
     bad = ~(np.abs(got - want) <= bound)
     assert not bad.any(), f"{bad.sum()} off, worst {np.max(np.abs(got - want) / bound):.3g} of the bound"
+
+
+@pytest.mark.parametrize("magnitude", [1e-12, 1e-4, 1e4])
+def test_experts_many_tokens_of_any_magnitude(lib, magnitude):
+    """The f16 operands of the path of many tokens are scaled by row: rows of any size come out alike."""
+    rng = np.random.default_rng(21)
+    E, T, D, F = 2, 100, 256, 128
+    mats, handles = [], []
+    for N, K in ((F, D), (F, D), (D, F)):
+        c, d, z = planes(rng, E, N, K, 128, True)
+        mats.append(oq4.dequant(c, d.view(np.uint16), z, 128))
+        handles.append(upload(lib, c, d, z, 128))
+    ids = np.arange(T)[:, None] % E
+    x0 = rng.normal(size=(T, D))
+    x0[: T // 2] *= magnitude                                         # beside rows of ordinary size
+    x, got = run_experts(lib, x0, ids, np.ones((T, 1)), handles, "bfloat16", E)
+    want = omoe.experts(x, ids, np.ones((T, 1)), *mats)
+    eps = 2.0 ** -11 + (D / 16 + 16) * 2.0 ** -22
+    bound = omoe.experts_bound(x, ids, np.ones((T, 1)), *mats, eps, eps, 2.0 ** -11)
+    bound = 1.02 * bound + 2.0 ** -8 * np.abs(want) + 1e-36
+    assert np.all(np.abs(got - want) <= bound)
 
 
 def test_experts_no_tokens_and_no_slots(lib):
