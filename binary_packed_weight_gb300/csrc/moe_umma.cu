@@ -41,6 +41,8 @@ struct MuBars {
     uint64_t full[MU_STAGES], empty[MU_STAGES], raw_full[MU_RAW], raw_empty[MU_RAW], acc_full, acc_empty;
     uint32_t tmem_base;
     int abort;
+    float2 scale[MU_BN];                   // epilogue: the tile's scales and output rows
+    int row[MU_BN];
 };
 
 struct MuArgs {
@@ -61,6 +63,9 @@ struct MuArgs {
 struct MuTile {
     int e, p0, cnt, r;
 };
+
+// Barrier of the four epilogue warps.
+__device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 template <int G, bool PAIR>
 __global__ void __launch_bounds__(MU_THREADS, 1)
@@ -312,6 +317,13 @@ moe_umma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
         int lt = 0;
         for (int t = blockIdx.x; t < total; t += gridDim.x, ++lt) {
             const MuTile m = tile_at(t);
+            const int et = tid - 12 * 32;                  // the tile's scales and rows, while the MMAs run
+            epi_bar();                                     // the last tile's are done with
+            for (int i = et; i < m.cnt; i += 128) {
+                bars->scale[i] = a.scales[m.p0 + i];
+                bars->row[i] = PAIR ? m.p0 + i : plan_slot(a.slots, a.nslots, m.p0 + i);
+            }
+            epi_bar();
             if (!mbar_wait_or_abort(&bars->acc_full, (uint32_t)lt & 1u, abort_flag)) {
                 *abort_flag = 1;
                 break;
@@ -326,32 +338,38 @@ moe_umma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars->acc_empty);
                 }
+                const int left = m.cnt - cc;
                 if (PAIR) {
                     // this lane finishes 16 of the 32 positions of its row
                     const bool upper = lane >= 16;
                     const int n = m.r * 64 + q * 16 + (lane & 15);
-                    const int c0 = cc + (upper ? 16 : 0);
+                    const int o = upper ? 16 : 0;
+                    const bool mine = n < a.N;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[16 + i], 16);
-                        if (c0 + i < m.cnt && n < a.N) {
-                            const float2 sc = a.scales[m.p0 + c0 + i];
-                            const float gt = __uint_as_float(upper ? other : v[i]) * sc.x;
-                            const float up = __uint_as_float(upper ? v[16 + i] : other) * sc.x;
-                            const float hv = __fdividef(gt, 1.0f + __expf(-gt)) * up;
-                            a.hidden[(int64_t)(m.p0 + c0 + i) * a.N + n] = __float2half_rn(hv * sc.y);
-                        }
+                        const float2 sc = bars->scale[cc + o + i];
+                        const float gt = __uint_as_float(upper ? other : v[i]) * sc.x;
+                        const float up = __uint_as_float(upper ? v[16 + i] : other) * sc.x;
+                        const float hv = __fdividef(gt, 1.0f + __expf(-gt)) * up;
+                        if (mine && o + i < left)
+                            a.hidden[(int64_t)(m.p0 + cc + o + i) * a.N + n] = __float2half_rn(hv * sc.y);
                     }
                 } else {
                     const int n = m.r * 128 + q * 32 + lane;
                     if (n < a.N) {
+                        if (left >= 32) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (cc + i < m.cnt) {
-                                const int p = m.p0 + cc + i;
-                                a.y[(int64_t)plan_slot(a.slots, a.nslots, p) * a.N + n] =
-                                    __uint_as_float(v[i]) * a.scales[p].y;
-                            }
+                            for (int i = 0; i < 32; ++i)
+                                a.y[(int64_t)bars->row[cc + i] * a.N + n] =
+                                    __uint_as_float(v[i]) * bars->scale[cc + i].y;
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i < left)
+                                    a.y[(int64_t)bars->row[cc + i] * a.N + n] =
+                                        __uint_as_float(v[i]) * bars->scale[cc + i].y;
+                        }
                     }
                 }
             }
@@ -365,10 +383,25 @@ moe_umma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
     }
 }
 
-// A warp a position: its row of x as f16, scaled, and the scales.
+// Eight elements of a row.
+template <class T>
+__device__ __forceinline__ void load8(const T* p, bool vec, float (&f)[8]) {
+    T raw[8];
+    if (vec) {
+        *reinterpret_cast<uint4*>(raw) = *reinterpret_cast<const uint4*>(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) raw[i] = p[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = (float)raw[i];
+}
+
+// A warp a position: its row of x as f16, scaled, and the scales.  Two passes
+// over the row, the second from L1; a token's rows share its lines in L2.
 template <class T>
 __global__ void __launch_bounds__(256)
-moe_stage_kernel(const T* __restrict__ x, int64_t ldx, int D, const int* __restrict__ offsets,
+moe_stage_kernel(const T* __restrict__ x, int64_t ldx, int vec, int D, const int* __restrict__ offsets,
                  const int* __restrict__ slots, int nslots, int k, int E, const float* __restrict__ bound0,
                  const float* __restrict__ bound1, __half* __restrict__ xs, float2* __restrict__ first,
                  float2* __restrict__ second) {
@@ -378,19 +411,31 @@ moe_stage_kernel(const T* __restrict__ x, int64_t ldx, int D, const int* __restr
     const int end = plan_offset(offsets, nslots, E);
     for (int p = blockIdx.x * 8 + (threadIdx.x >> 5); p < end; p += gridDim.x * 8) {
         const T* row = x + (int64_t)(plan_slot(slots, nslots, p) / k) * ldx;
-        float m = 0.f, ss = 0.f;
-        for (int c = lane; c < D; c += 32) m = fmaxf(m, fabsf((float)row[c]));
+        float m = 0.f, ss = 0.f, f[8];
+#pragma unroll 4
+        for (int c = lane * 8; c < D; c += 256) {
+            load8(row + c, vec != 0, f);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
+        }
+        m = __int_as_float(__reduce_max_sync(0xffffffffu, __float_as_int(m)));   // m >= 0: its bits have its order
         const int be = (__float_as_int(m) >> 23) & 255;
         int se = be == 0 ? 253 : 127 + 14 - (be - 127);
         if (m == 0.f || be == 255) se = 127;
         se = se > 253 ? 253 : se;
         const float s = __int_as_float(se << 23);
-        for (int c = lane; c < D; c += 32) {
-            const float v = (float)row[c] * s;
-            ss = fmaf(v, v, ss);
-            xs[(int64_t)p * D + c] = __float2half_rn(v);
+#pragma unroll 4
+        for (int c = lane * 8; c < D; c += 256) {
+            load8(row + c, vec != 0, f);
+            __half2 h[4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                f[i] *= s;
+                ss = fmaf(f[i], f[i], ss);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+            *reinterpret_cast<uint4*>(xs + (int64_t)p * D + c) = *reinterpret_cast<uint4*>(h);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -454,16 +499,17 @@ cudaError_t launch_moe_tensor(const MoeTensor& m, void* scratch, cudaStream_t st
     float2* second = reinterpret_cast<float2*>(at);
     int64_t grid = (S + 7) / 8;
     if (grid > 152 * 16) grid = 152 * 16;
+    const int vec = (reinterpret_cast<uintptr_t>(m.x) & 15) == 0 && m.ldx % 8 == 0;
     cudaError_t e;
     const int E = (int)m.gate->E;
     if (m.dtype == TQ2_F16)
         e = launch_pdl(moe_stage_kernel<__half>, dim3((unsigned)grid), dim3(256), 0, st,
-                       static_cast<const __half*>(m.x), m.ldx, (int)D, m.offsets, m.slots, (int)S, m.k, E,
+                       static_cast<const __half*>(m.x), m.ldx, vec, (int)D, m.offsets, m.slots, (int)S, m.k, E,
                        static_cast<const float*>(m.gate->bound), static_cast<const float*>(m.up->bound), xs, first,
                        second);
     else
         e = launch_pdl(moe_stage_kernel<__nv_bfloat16>, dim3((unsigned)grid), dim3(256), 0, st,
-                       static_cast<const __nv_bfloat16*>(m.x), m.ldx, (int)D, m.offsets, m.slots, (int)S, m.k, E,
+                       static_cast<const __nv_bfloat16*>(m.x), m.ldx, vec, (int)D, m.offsets, m.slots, (int)S, m.k, E,
                        static_cast<const float*>(m.gate->bound), static_cast<const float*>(m.up->bound), xs, first,
                        second);
     if (e != cudaSuccess) return e;
