@@ -4,13 +4,14 @@
 //   hidden[p] = silu(Gate x[p]) * (Up x[p]),   y[slot(p)] = Down hidden[p]
 //
 // Both products are D[n, p] = sum_k W[n,k] act[p,k] with 128 weight rows and up
-// to 256 positions a tile, f16 operands and f32 accumulators in tensor memory:
+// to 192 positions a tile, f16 operands and f32 accumulators in tensor memory:
 //   * warp 0 streams the activations (B, 64 k a stage, 128-byte swizzle) by TMA;
 //   * warp 3 streams the packed blocks of 256 k by bulk copies;
 //   * warps 4..11 decode a block's rows, one weight row a thread, and store
 //     them as the A operand in tensor memory (rounding (c - z) d to f16 is
 //     the only rounding of the weights);
-//   * warp 1 issues the MMAs; warps 12..15 drain the finished tile.
+//   * warp 1 issues the MMAs into one of two accumulators; warps 12..15 and
+//     16..19 drain one each while the other fills.
 // A tile of the first product holds 64 rows of Gate and the same 64 of Up: lanes
 // 0..15 of each quarter are Gate's, 16..31 Up's, so one shuffle meets the two.
 //
@@ -30,19 +31,36 @@ namespace tq2 {
 
 namespace {
 
-constexpr int MU_THREADS = 512;
-constexpr int MU_BN = 256;                 // positions of a tile
-constexpr int MU_STAGES = 4;               // 64-k stages of B and A
-constexpr int MU_RAW = 4;                  // 256-k stages of packed blocks
-constexpr int MU_B_STAGE = MU_BN * 128;    // 32 KB
-constexpr int MU_ACOL = MU_BN;             // first tensor-memory column of the A stages
+constexpr int MU_THREADS = 640;
+constexpr int MU_BN = 192;                 // positions of a tile: two accumulators and four A stages fill 512 columns
+constexpr int MU_B = 6;                    // 64-k stages of activations
+constexpr int MU_A = 4;                    // 64-k stages of decoded weights (32 columns each)
+constexpr int MU_RAW = 3;                  // 256-k stages of packed blocks
+constexpr int MU_B_STAGE = MU_BN * 128;    // 24 KB
+constexpr int MU_ACOL = 2 * MU_BN;         // first tensor-memory column of the A stages
 
 struct MuBars {
-    uint64_t full[MU_STAGES], empty[MU_STAGES], raw_full[MU_RAW], raw_empty[MU_RAW], acc_full, acc_empty;
+    uint64_t b_full[MU_B], b_empty[MU_B], a_full[MU_A], a_empty[MU_A], raw_full[MU_RAW], raw_empty[MU_RAW];
+    uint64_t acc_full[2], acc_empty[2];
     uint32_t tmem_base;
     int abort;
-    float2 scale[MU_BN];                   // epilogue: the tile's scales and output rows
-    int row[MU_BN];
+    float2 scale[2][MU_BN];                // epilogue: a tile's scales and output rows
+    int row[2][MU_BN];
+};
+
+// Slot and phase parity of a ring's next item.
+template <int S>
+struct Ring {
+    int s = 0;
+    uint32_t ph = 0;
+    bool first = true;                     // no slot has been used twice yet
+    __device__ __forceinline__ void next() {
+        if (++s == S) {
+            s = 0;
+            ph ^= 1u;
+            first = false;
+        }
+    }
 };
 
 struct MuArgs {
@@ -64,8 +82,8 @@ struct MuTile {
     int e, p0, cnt, r;
 };
 
-// Barrier of the four epilogue warps.
-__device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Barrier of the four warps of epilogue group b.
+__device__ __forceinline__ void epi_bar(int b) { asm volatile("bar.sync %0, 128;" ::"r"(1 + b) : "memory"); }
 
 template <int G, bool PAIR>
 __global__ void __launch_bounds__(MU_THREADS, 1)
@@ -74,23 +92,29 @@ moe_umma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
     constexpr int NG = Q4_K / G;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int blk = q4_block_bytes(G, a.zeros != 0);
-    uint8_t* raw_ring = smem + MU_STAGES * MU_B_STAGE;
+    uint8_t* raw_ring = smem + MU_B * MU_B_STAGE;
     MuBars* bars = reinterpret_cast<MuBars*>(raw_ring + MU_RAW * 8 * blk);
     int* prefix = reinterpret_cast<int*>(bars + 1);        // token tiles before each matrix
     int* offs = prefix + a.E + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
-        for (int s = 0; s < MU_STAGES; ++s) {
-            mbar_init(&bars->full[s], 5);                  // the TMA producer and the stage's 4 decoder warps
-            mbar_init(&bars->empty[s], 1);                 // the MMA warp's commit
+        for (int s = 0; s < MU_B; ++s) {
+            mbar_init(&bars->b_full[s], 1);
+            mbar_init(&bars->b_empty[s], 1);               // the MMA warp's commit
+        }
+        for (int s = 0; s < MU_A; ++s) {
+            mbar_init(&bars->a_full[s], 4);                // the stage's decoder warps
+            mbar_init(&bars->a_empty[s], 1);
         }
         for (int r = 0; r < MU_RAW; ++r) {
             mbar_init(&bars->raw_full[r], 1);
             mbar_init(&bars->raw_empty[r], 8);             // every decoder warp
         }
-        mbar_init(&bars->acc_full, 1);
-        mbar_init(&bars->acc_empty, 4);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&bars->acc_full[b], 1);
+            mbar_init(&bars->acc_empty[b], 4);
+        }
         bars->abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&xmap);
@@ -148,32 +172,31 @@ moe_umma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
     if (warp == 0) {
         if (lane == 0) {                                   // ---- activations
             pdl_wait();
-            int it = 0;
+            Ring<MU_B> b;
             bool ok = true;
             for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
                 const MuTile m = tile_at(t);
                 const int boxes = (m.cnt + 31) / 32;
-                for (int ks = 0; ks < a.nk; ++ks, ++it) {
-                    const int s = it % MU_STAGES;
-                    if (it >= MU_STAGES &&
-                        !mbar_wait_or_abort(&bars->empty[s], (uint32_t)(it / MU_STAGES - 1) & 1u, abort_flag)) {
+                for (int ks = 0; ks < a.nk; ++ks, b.next()) {
+                    if (!b.first && !mbar_wait_or_abort(&bars->b_empty[b.s], b.ph ^ 1u, abort_flag)) {
                         *abort_flag = 1;
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&bars->full[s], (uint32_t)boxes * 4096u);
-                    for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(smem + s * MU_B_STAGE + b * 4096, &xmap, &bars->full[s], ks * 64, m.p0 + 32 * b);
+                    mbar_arrive_expect_tx(&bars->b_full[b.s], (uint32_t)boxes * 4096u);
+                    for (int i = 0; i < boxes; ++i)
+                        tma_load_2d(smem + b.s * MU_B_STAGE + i * 4096, &xmap, &bars->b_full[b.s], ks * 64,
+                                    m.p0 + 32 * i);
                 }
             }
-            // the copies already issued land before the CTA can exit
+            // after a wait that ran out: the copies already issued land before the CTA can exit
             if (!ok)
-                for (int i = (it > MU_STAGES ? it - MU_STAGES : 0); i < it; ++i)
-                    mbar_wait(&bars->full[i % MU_STAGES], (uint32_t)(i / MU_STAGES) & 1u);
+                for (int i = 0; i < MU_B; ++i)
+                    mbar_wait(&bars->b_full[i], i < b.s ? b.ph : b.ph ^ 1u);
         }
     } else if (warp == 3) {
         if (lane == 0) {                                   // ---- packed blocks
-            int it = 0;
+            Ring<MU_RAW> r;
             bool ok = true;
             const uint32_t bytes = 8u * (uint32_t)blk;
             for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
@@ -181,61 +204,62 @@ moe_umma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
                 // first of the tile's blocks of a chunk: 8 row tiles of one matrix, or 4 of each of two
                 const int rt = PAIR ? m.r * 4 : m.r * 8;
                 const int64_t first = (int64_t)m.e * a.mstride + q4_block_index(rt, 0, a.nkc) * blk;
-                for (int kc = 0; kc * 4 < a.nk; ++kc, ++it) {
-                    const int r = it % MU_RAW;
-                    if (it >= MU_RAW &&
-                        !mbar_wait_or_abort(&bars->raw_empty[r], (uint32_t)(it / MU_RAW - 1) & 1u, abort_flag)) {
+                for (int kc = 0; kc * 4 < a.nk; ++kc, r.next()) {
+                    if (!r.first && !mbar_wait_or_abort(&bars->raw_empty[r.s], r.ph ^ 1u, abort_flag)) {
                         *abort_flag = 1;
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&bars->raw_full[r], bytes);
-                    uint8_t* dst = raw_ring + (size_t)r * bytes;
+                    mbar_arrive_expect_tx(&bars->raw_full[r.s], bytes);
+                    uint8_t* dst = raw_ring + (size_t)r.s * bytes;
                     const int64_t at = first + (int64_t)kc * 8 * blk;
                     if (PAIR) {
-                        bulk_load(dst, a.w0 + at, bytes / 2, &bars->raw_full[r]);
-                        bulk_load(dst + bytes / 2, a.w1 + at, bytes / 2, &bars->raw_full[r]);
+                        bulk_load(dst, a.w0 + at, bytes / 2, &bars->raw_full[r.s]);
+                        bulk_load(dst + bytes / 2, a.w1 + at, bytes / 2, &bars->raw_full[r.s]);
                     } else {
-                        bulk_load(dst, a.w0 + at, bytes, &bars->raw_full[r]);
+                        bulk_load(dst, a.w0 + at, bytes, &bars->raw_full[r.s]);
                     }
                 }
             }
             if (!ok)
-                for (int i = (it > MU_RAW ? it - MU_RAW : 0); i < it; ++i)
-                    mbar_wait(&bars->raw_full[i % MU_RAW], (uint32_t)(i / MU_RAW) & 1u);
+                for (int i = 0; i < MU_RAW; ++i)
+                    mbar_wait(&bars->raw_full[i], i < r.s ? r.ph : r.ph ^ 1u);
         }
     } else if (warp == 1) {                                // ---- MMA issuer (the whole warp, elect.sync)
         auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, abort_flag, true)) != 0;
         };
-        int it = 0, lt = 0;
+        Ring<MU_B> b;
+        Ring<MU_A> w;
+        Ring<2> acc;
         bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++lt) {
+        for (int t = blockIdx.x; t < total && ok; t += gridDim.x, acc.next()) {
             const MuTile m = tile_at(t);
             const uint32_t idesc = idesc_f16_f32(128, (uint32_t)((m.cnt + 15) / 16 * 16));
-            if (lt > 0 && !wait_all(&bars->acc_empty, (uint32_t)(lt - 1) & 1u)) {
+            const uint32_t dcol = tmem + (uint32_t)(acc.s * MU_BN);
+            if (!acc.first && !wait_all(&bars->acc_empty[acc.s], acc.ph ^ 1u)) {
                 *abort_flag = 1;
                 break;
             }
             tc_fence_after();
-            for (int ks = 0; ks < a.nk; ++ks, ++it) {
-                const int s = it % MU_STAGES;
-                if (!wait_all(&bars->full[s], (uint32_t)(it / MU_STAGES) & 1u)) {
+            for (int ks = 0; ks < a.nk; ++ks, b.next(), w.next()) {
+                if (!wait_all(&bars->b_full[b.s], b.ph) || !wait_all(&bars->a_full[w.s], w.ph)) {
                     *abort_flag = 1;
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint64_t bdesc = sdesc_kmajor_sw128(smem_u32(smem + s * MU_B_STAGE));
-                const uint32_t acol = tmem + MU_ACOL + (uint32_t)(s * 32);
+                const uint64_t bdesc = sdesc_kmajor_sw128(smem_u32(smem + b.s * MU_B_STAGE));
+                const uint32_t acol = tmem + MU_ACOL + (uint32_t)(w.s * 32);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    umma_f16_ts_elect(tmem, acol + (uint32_t)(j * 8), bdesc + (uint64_t)(2 * j), idesc,
+                    umma_f16_ts_elect(dcol, acol + (uint32_t)(j * 8), bdesc + (uint64_t)(2 * j), idesc,
                                       (ks > 0 || j > 0) ? 1u : 0u);
-                umma_commit_elect(&bars->empty[s]);
+                umma_commit_elect(&bars->b_empty[b.s]);
+                umma_commit_elect(&bars->a_empty[w.s]);
             }
             if (!ok) break;
-            umma_commit_elect(&bars->acc_full);
+            umma_commit_elect(&bars->acc_full[acc.s]);
         }
     } else if (warp >= 4 && warp < 12) {                   // ---- decoders
         // quarter q of the rows, stages of parity h; rows 0..15 of a quarter are one
@@ -245,17 +269,17 @@ moe_umma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
         const int b = PAIR ? (lane >> 4) * 4 + q : q * 2 + (lane >> 4);
         const uint32_t expo = q4_exponent<false>();
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16) + MU_ACOL;
-        int it0 = 0, rit = 0;
+        Ring<MU_RAW> r;
+        int it0 = 0;                                       // stages of the tiles before
         bool ok = true;
         for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-            for (int kc = 0; kc * 4 < a.nk && ok; ++kc, ++rit) {
-                const int r = rit % MU_RAW;
-                if (!mbar_wait_or_abort(&bars->raw_full[r], (uint32_t)(rit / MU_RAW) & 1u, abort_flag)) {
+            for (int kc = 0; kc * 4 < a.nk && ok; ++kc, r.next()) {
+                if (!mbar_wait_or_abort(&bars->raw_full[r.s], r.ph, abort_flag)) {
                     *abort_flag = 1;
                     ok = false;
                     break;
                 }
-                const uint8_t* src = raw_ring + (size_t)r * 8 * blk + b * blk;
+                const uint8_t* src = raw_ring + (size_t)r.s * 8 * blk + b * blk;
                 const uint8_t* sc = src + Q4_CODES + q4_scale_index(row, 0, NG) * 2;
                 const uint8_t* zp = src + Q4_CODES + 32 * NG + q4_scale_index(row, 0, NG);
                 for (int c = h; c < 4; c += 2) {
@@ -289,9 +313,9 @@ moe_umma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
                             }
                         }
                     }
-                    const int it = it0 + ks, s = it % MU_STAGES;
-                    if (it >= MU_STAGES &&
-                        !mbar_wait_or_abort(&bars->empty[s], (uint32_t)(it / MU_STAGES - 1) & 1u, abort_flag)) {
+                    const int it = it0 + ks, s = it % MU_A;
+                    if (it >= MU_A &&
+                        !mbar_wait_or_abort(&bars->a_empty[s], (uint32_t)(it / MU_A - 1) & 1u, abort_flag)) {
                         *abort_flag = 1;
                         ok = false;
                         break;
@@ -301,34 +325,39 @@ moe_umma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->full[s]);
+                    if (lane == 0) mbar_arrive(&bars->a_full[s]);
                 }
                 // the values are used: the slot is refilled through the async proxy
                 fence_proxy_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->raw_empty[r]);
+                if (lane == 0) mbar_arrive(&bars->raw_empty[r.s]);
             }
             it0 += a.nk;
         }
-    } else if (warp >= 12) {                               // ---- epilogue
-        const int q = warp & 3;
-        const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
+    } else if (warp >= 12) {                               // ---- epilogue: group b drains accumulator b
+        const int q = warp & 3, b = (warp - 12) >> 2;
+        const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * MU_BN);
+        const float2* scale = bars->scale[b];
+        const int* orow = bars->row[b];
         pdl_wait();
-        int lt = 0;
-        for (int t = blockIdx.x; t < total; t += gridDim.x, ++lt) {
+        uint32_t ph = 0;
+        for (int t = blockIdx.x + b * gridDim.x; t < total; t += 2 * gridDim.x, ph ^= 1u) {
             const MuTile m = tile_at(t);
-            const int et = tid - 12 * 32;                  // the tile's scales and rows, while the MMAs run
-            epi_bar();                                     // the last tile's are done with
-            for (int i = et; i < m.cnt; i += 128) {
-                bars->scale[i] = a.scales[m.p0 + i];
-                bars->row[i] = PAIR ? m.p0 + i : plan_slot(a.slots, a.nslots, m.p0 + i);
+            epi_bar(b);                                    // the last tile's scales and rows are done with
+            for (int i = tid - (12 + 4 * b) * 32; i < m.cnt; i += 128) {
+                bars->scale[b][i] = a.scales[m.p0 + i];
+                if (!PAIR) bars->row[b][i] = plan_slot(a.slots, a.nslots, m.p0 + i);
             }
-            epi_bar();
-            if (!mbar_wait_or_abort(&bars->acc_full, (uint32_t)lt & 1u, abort_flag)) {
+            epi_bar(b);
+            if (!mbar_wait_or_abort(&bars->acc_full[b], ph, abort_flag)) {
                 *abort_flag = 1;
                 break;
             }
             tc_fence_after();
+            // pair: this lane finishes 16 of 32 positions of its row, else all of them
+            const bool upper = PAIR && lane >= 16;
+            const int n = PAIR ? m.r * 64 + q * 16 + (lane & 15) : m.r * 128 + q * 32 + lane;
+            const bool mine = n < a.N;
             for (int cc = 0; cc < m.cnt; cc += 32) {
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(lane_addr + (uint32_t)cc, v);
@@ -336,40 +365,31 @@ moe_umma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
                 if (cc + 32 >= m.cnt) {                    // accumulator read: hand it back
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->acc_empty);
+                    if (lane == 0) mbar_arrive(&bars->acc_empty[b]);
                 }
-                const int left = m.cnt - cc;
                 if (PAIR) {
-                    // this lane finishes 16 of the 32 positions of its row
-                    const bool upper = lane >= 16;
-                    const int n = m.r * 64 + q * 16 + (lane & 15);
-                    const int o = upper ? 16 : 0;
-                    const bool mine = n < a.N;
+                    const int c0 = cc + (upper ? 16 : 0), left = mine ? m.cnt - c0 : 0;
+                    __half* out = a.hidden + (int64_t)(m.p0 + c0) * a.N + n;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < 16; ++i, out += a.N) {
                         const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[16 + i], 16);
-                        const float2 sc = bars->scale[cc + o + i];
+                        const float2 sc = scale[c0 + i];
                         const float gt = __uint_as_float(upper ? other : v[i]) * sc.x;
                         const float up = __uint_as_float(upper ? v[16 + i] : other) * sc.x;
                         const float hv = __fdividef(gt, 1.0f + __expf(-gt)) * up;
-                        if (mine && o + i < left)
-                            a.hidden[(int64_t)(m.p0 + cc + o + i) * a.N + n] = __float2half_rn(hv * sc.y);
+                        if (i < left) *out = __float2half_rn(hv * sc.y);
                     }
-                } else {
-                    const int n = m.r * 128 + q * 32 + lane;
-                    if (n < a.N) {
-                        if (left >= 32) {
+                } else if (mine) {
+                    float* out = a.y + n;
+                    const int left = m.cnt - cc;
+                    if (left >= 32) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                a.y[(int64_t)bars->row[cc + i] * a.N + n] =
-                                    __uint_as_float(v[i]) * bars->scale[cc + i].y;
-                        } else {
+                        for (int i = 0; i < 32; ++i)
+                            out[(int64_t)orow[cc + i] * a.N] = __uint_as_float(v[i]) * scale[cc + i].y;
+                    } else {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (i < left)
-                                    a.y[(int64_t)bars->row[cc + i] * a.N + n] =
-                                        __uint_as_float(v[i]) * bars->scale[cc + i].y;
-                        }
+                        for (int i = 0; i < 32; ++i)
+                            if (i < left) out[(int64_t)orow[cc + i] * a.N] = __uint_as_float(v[i]) * scale[cc + i].y;
                     }
                 }
             }
@@ -463,7 +483,7 @@ cudaError_t launch_umma_moe(const CUtensorMap& xmap, const MuArgs& a, cudaStream
     int dev = 0, sms = 152;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const size_t smem = 1024 + (size_t)MU_STAGES * MU_B_STAGE + (size_t)MU_RAW * 8 * q4_block_bytes(G, a.zeros != 0) +
+    const size_t smem = 1024 + (size_t)MU_B * MU_B_STAGE + (size_t)MU_RAW * 8 * q4_block_bytes(G, a.zeros != 0) +
                         sizeof(MuBars) + (size_t)(2 * (a.E + 1)) * 4;
     cudaError_t e = cudaFuncSetAttribute(moe_umma_kernel<G, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
