@@ -4,14 +4,18 @@
 //   hidden[p] = silu(Gate x[p]) * (Up x[p]),   y[slot(p)] = Down hidden[p]
 //
 // Both products are D[n, p] = sum_k W[n,k] act[p,k] with 128 weight rows and up
-// to 192 positions a tile, f16 operands and f32 accumulators in tensor memory:
-//   * warp 0 streams the activations (B, 64 k a stage, 128-byte swizzle) by TMA;
+// to 256 positions a tile, f16 operands and one f32 accumulator in tensor memory,
+// in stages of 128 k (what a stage costs besides its MMAs -- waits, commits, the
+// decoders' hand-offs, several hundred cycles -- does not grow with its k):
+//   * warp 0 streams the activations (B, 128-byte swizzle, 64 k a slot) by TMA;
 //   * warp 3 streams the packed blocks of 256 k by bulk copies;
 //   * warps 4..11 decode a block's rows, one weight row a thread, and store
 //     them as the A operand in tensor memory (rounding (c - z) d to f16 is
 //     the only rounding of the weights);
-//   * warp 1 issues the MMAs into one of two accumulators; warps 12..15 and
-//     16..19 drain one each while the other fills.
+//   * warp 1 issues the MMAs; one barrier a stage covers both operands, and the
+//     next stage's is tested while this stage's MMAs run;
+//   * warps 12..19 drain the finished tile, 32 columns each in turn, while the
+//     next tile's operands fill their rings.
 // A tile of the first product holds 64 rows of Gate and the same 64 of Up: lanes
 // 0..15 of each quarter are Gate's, 16..31 Up's, so one shuffle meets the two.
 //
@@ -32,20 +36,26 @@ namespace tq2 {
 namespace {
 
 constexpr int MU_THREADS = 640;
-constexpr int MU_BN = 192;                 // positions of a tile: two accumulators and four A stages fill 512 columns
-constexpr int MU_B = 6;                    // 64-k stages of activations
-constexpr int MU_A = 4;                    // 64-k stages of decoded weights (32 columns each)
-constexpr int MU_RAW = 3;                  // 256-k stages of packed blocks
-constexpr int MU_B_STAGE = MU_BN * 128;    // 24 KB
-constexpr int MU_ACOL = 2 * MU_BN;         // first tensor-memory column of the A stages
+constexpr int MU_BN = 256;                 // positions of a tile
+constexpr int MU_B = 5;                    // activation slots of 64 k (32 KB)
+constexpr int MU_A = 4;                    // stages of 128 k: decoded weights (64 tensor-memory columns each)
+constexpr int MU_RAW = 3;                  // packed blocks of 256 k
+constexpr int MU_B_SLOT = MU_BN * 128;
+constexpr int MU_ACOL = MU_BN;             // first tensor-memory column of the A stages
+constexpr int MU_LIST = 64;                // tiles of a CTA that are looked up ahead
+
+struct MuTile {
+    int e, p0, cnt, r;
+};
 
 struct MuBars {
-    uint64_t b_full[MU_B], b_empty[MU_B], a_full[MU_A], a_empty[MU_A], raw_full[MU_RAW], raw_empty[MU_RAW];
-    uint64_t acc_full[2], acc_empty[2];
+    uint64_t full[MU_A], a_empty[MU_A], b_empty[MU_B], raw_full[MU_RAW], raw_empty[MU_RAW];
+    uint64_t acc_full, acc_empty;
     uint32_t tmem_base;
     int abort;
-    float2 scale[2][MU_BN];                // epilogue: a tile's scales and output rows
-    int row[2][MU_BN];
+    MuTile list[MU_LIST];
+    float2 scale[MU_BN];                   // epilogue: a tile's scales and output rows
+    int row[MU_BN];
 };
 
 // Slot and phase parity of a ring's next item.
@@ -78,12 +88,8 @@ struct MuArgs {
     float* y;                              // else: [slot][N]
 };
 
-struct MuTile {
-    int e, p0, cnt, r;
-};
-
-// Barrier of the four warps of epilogue group b.
-__device__ __forceinline__ void epi_bar(int b) { asm volatile("bar.sync %0, 128;" ::"r"(1 + b) : "memory"); }
+// Barrier of the eight epilogue warps.
+__device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 template <int G, bool PAIR>
 __global__ void __launch_bounds__(MU_THREADS, 1)
@@ -92,29 +98,23 @@ moe_umma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
     constexpr int NG = Q4_K / G;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int blk = q4_block_bytes(G, a.zeros != 0);
-    uint8_t* raw_ring = smem + MU_B * MU_B_STAGE;
+    uint8_t* raw_ring = smem + MU_B * MU_B_SLOT;
     MuBars* bars = reinterpret_cast<MuBars*>(raw_ring + MU_RAW * 8 * blk);
     int* prefix = reinterpret_cast<int*>(bars + 1);        // token tiles before each matrix
-    int* offs = prefix + a.E + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
-        for (int s = 0; s < MU_B; ++s) {
-            mbar_init(&bars->b_full[s], 1);
-            mbar_init(&bars->b_empty[s], 1);               // the MMA warp's commit
-        }
         for (int s = 0; s < MU_A; ++s) {
-            mbar_init(&bars->a_full[s], 4);                // the stage's decoder warps
-            mbar_init(&bars->a_empty[s], 1);
+            mbar_init(&bars->full[s], 5);                  // the TMA producer and the stage's 4 decoder warps
+            mbar_init(&bars->a_empty[s], 1);               // the MMA warp's commits
         }
+        for (int s = 0; s < MU_B; ++s) mbar_init(&bars->b_empty[s], 1);
         for (int r = 0; r < MU_RAW; ++r) {
             mbar_init(&bars->raw_full[r], 1);
             mbar_init(&bars->raw_empty[r], 8);             // every decoder warp
         }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&bars->acc_full[b], 1);
-            mbar_init(&bars->acc_empty[b], 4);
-        }
+        mbar_init(&bars->acc_full, 1);
+        mbar_init(&bars->acc_empty, 8);                    // every epilogue warp
         bars->abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&xmap);
@@ -137,10 +137,7 @@ moe_umma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
                 const int up = __shfl_up_sync(0xffffffffu, s, d);
                 if (lane >= d) s += up;
             }
-            if (e <= a.E) {
-                prefix[e] = run + s - n;
-                offs[e] = o;
-            }
+            if (e <= a.E) prefix[e] = run + s - n;
             run += __shfl_sync(0xffffffffu, s, 31);
         }
     }
@@ -152,7 +149,7 @@ moe_umma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
     const int total = prefix[a.E] * a.row_tiles;
 
     // tile t: row tiles fastest; a matrix's positions are cut evenly
-    auto tile_at = [&](int t) {
+    auto find_tile = [&](int t) {
         MuTile m;
         const int tt = t / a.row_tiles;
         m.r = t - tt * a.row_tiles;
@@ -162,45 +159,58 @@ moe_umma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
             if (prefix[mid] <= tt) lo = mid; else hi = mid;
         }
         m.e = lo;
-        const int i = tt - prefix[lo], n = prefix[lo + 1] - prefix[lo], c = offs[lo + 1] - offs[lo];
+        const int i = tt - prefix[lo], n = prefix[lo + 1] - prefix[lo], o = plan_offset(a.offsets, a.nslots, lo),
+                  c = plan_offset(a.offsets, a.nslots, lo + 1) - o;
         const int each = c / n, more = c - each * n;
-        m.p0 = offs[lo] + i * each + min(i, more);
+        m.p0 = o + i * each + min(i, more);
         m.cnt = each + (i < more ? 1 : 0);
         return m;
     };
+    // this CTA's i-th tile
+    const int mine = total > (int)blockIdx.x ? (total - blockIdx.x - 1) / gridDim.x + 1 : 0;
+    for (int i = tid; i < min(mine, MU_LIST); i += MU_THREADS) bars->list[i] = find_tile(blockIdx.x + i * gridDim.x);
+    __syncthreads();
+    auto tile_at = [&](int i) { return i < MU_LIST ? bars->list[i] : find_tile(blockIdx.x + i * gridDim.x); };
+    const int stages = (a.nk + 1) / 2;                     // of 128 k, the last one maybe of 64
 
     if (warp == 0) {
         if (lane == 0) {                                   // ---- activations
             pdl_wait();
             Ring<MU_B> b;
+            Ring<MU_A> f;
             bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-                const MuTile m = tile_at(t);
+            for (int i = 0; i < mine && ok; ++i) {
+                const MuTile m = tile_at(i);
                 const int boxes = (m.cnt + 31) / 32;
                 for (int ks = 0; ks < a.nk; ++ks, b.next()) {
-                    if (!b.first && !mbar_wait_or_abort(&bars->b_empty[b.s], b.ph ^ 1u, abort_flag)) {
+                    // the slot's last MMAs are done, and those of the stage that last used the barrier
+                    if ((!b.first && !mbar_wait_or_abort(&bars->b_empty[b.s], b.ph ^ 1u, abort_flag)) ||
+                        ((ks & 1) == 0 && !f.first &&
+                         !mbar_wait_or_abort(&bars->a_empty[f.s], f.ph ^ 1u, abort_flag))) {
                         *abort_flag = 1;
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&bars->b_full[b.s], (uint32_t)boxes * 4096u);
-                    for (int i = 0; i < boxes; ++i)
-                        tma_load_2d(smem + b.s * MU_B_STAGE + i * 4096, &xmap, &bars->b_full[b.s], ks * 64,
-                                    m.p0 + 32 * i);
+                    if ((ks & 1) == 0)
+                        mbar_arrive_expect_tx(&bars->full[f.s], (uint32_t)boxes * (ks + 1 < a.nk ? 8192u : 4096u));
+                    for (int x = 0; x < boxes; ++x)
+                        tma_load_2d(smem + b.s * MU_B_SLOT + x * 4096, &xmap, &bars->full[f.s], ks * 64,
+                                    m.p0 + 32 * x);
+                    if ((ks & 1) == 1 || ks + 1 == a.nk) f.next();
                 }
             }
-            // after a wait that ran out: the copies already issued land before the CTA can exit
+            // After a wait that ran out the copies already issued must land before the CTA exits.  Each is
+            // short of its barrier's phase, which may never complete: give them their (bounded) time.
             if (!ok)
-                for (int i = 0; i < MU_B; ++i)
-                    mbar_wait(&bars->b_full[i], i < b.s ? b.ph : b.ph ^ 1u);
+                for (int x = 0; x < MU_A; ++x) mbar_wait(&bars->full[x], x < f.s ? f.ph : f.ph ^ 1u);
         }
     } else if (warp == 3) {
         if (lane == 0) {                                   // ---- packed blocks
             Ring<MU_RAW> r;
             bool ok = true;
             const uint32_t bytes = 8u * (uint32_t)blk;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-                const MuTile m = tile_at(t);
+            for (int i = 0; i < mine && ok; ++i) {
+                const MuTile m = tile_at(i);
                 // first of the tile's blocks of a chunk: 8 row tiles of one matrix, or 4 of each of two
                 const int rt = PAIR ? m.r * 4 : m.r * 8;
                 const int64_t first = (int64_t)m.e * a.mstride + q4_block_index(rt, 0, a.nkc) * blk;
@@ -230,49 +240,59 @@ moe_umma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
             return __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, abort_flag, true)) != 0;
         };
         Ring<MU_B> b;
-        Ring<MU_A> w;
-        Ring<2> acc;
-        bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x, acc.next()) {
-            const MuTile m = tile_at(t);
-            const uint32_t idesc = idesc_f16_f32(128, (uint32_t)((m.cnt + 15) / 16 * 16));
-            const uint32_t dcol = tmem + (uint32_t)(acc.s * MU_BN);
-            if (!acc.first && !wait_all(&bars->acc_empty[acc.s], acc.ph ^ 1u)) {
+        Ring<MU_A> f;
+        bool ok = true, ready = false;
+        int cnt = mine > 0 ? tile_at(0).cnt : 0;
+        for (int i = 0; i < mine && ok; ++i) {
+            const uint32_t idesc = idesc_f16_f32(128, (uint32_t)((cnt + 15) / 16 * 16));
+            if (i > 0 && !wait_all(&bars->acc_empty, (uint32_t)(i - 1) & 1u)) {
                 *abort_flag = 1;
                 break;
             }
             tc_fence_after();
-            for (int ks = 0; ks < a.nk; ++ks, b.next(), w.next()) {
-                if (!wait_all(&bars->b_full[b.s], b.ph) || !wait_all(&bars->a_full[w.s], w.ph)) {
+            for (int st = 0; st < stages; ++st) {
+                if (!ready && !wait_all(&bars->full[f.s], f.ph)) {
                     *abort_flag = 1;
                     ok = false;
                     break;
                 }
+                Ring<MU_A> g = f;
+                g.next();
+                ready = mbar_test_wait(&bars->full[g.s], g.ph);   // its latency hides under the MMAs below
                 tc_fence_after();
-                const uint64_t bdesc = sdesc_kmajor_sw128(smem_u32(smem + b.s * MU_B_STAGE));
-                const uint32_t acol = tmem + MU_ACOL + (uint32_t)(w.s * 32);
+                const uint32_t acol = tmem + MU_ACOL + (uint32_t)(f.s * 64);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    umma_f16_ts_elect(dcol, acol + (uint32_t)(j * 8), bdesc + (uint64_t)(2 * j), idesc,
-                                      (ks > 0 || j > 0) ? 1u : 0u);
-                umma_commit_elect(&bars->b_empty[b.s]);
-                umma_commit_elect(&bars->a_empty[w.s]);
+                for (int at = 0; at < 2; ++at) {
+                    if (at == 1 && 2 * st + 1 >= a.nk) break;
+                    const uint64_t bdesc = sdesc_kmajor_sw128(smem_u32(smem + b.s * MU_B_SLOT));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        umma_f16_ts_elect(tmem, acol + (uint32_t)(at * 32 + j * 8), bdesc + (uint64_t)(2 * j), idesc,
+                                          (st > 0 || at > 0 || j > 0) ? 1u : 0u);
+                    umma_commit_elect(&bars->b_empty[b.s]);
+                    b.next();
+                }
+                umma_commit_elect(&bars->a_empty[f.s]);
+                f = g;
+                ready = __all_sync(0xffffffffu, ready);
             }
             if (!ok) break;
-            umma_commit_elect(&bars->acc_full[acc.s]);
+            umma_commit_elect(&bars->acc_full);
+            if (i + 1 < mine) cnt = tile_at(i + 1).cnt;
         }
     } else if (warp >= 4 && warp < 12) {                   // ---- decoders
-        // quarter q of the rows, stages of parity h; rows 0..15 of a quarter are one
-        // 16-row tile's, 16..31 the next one's (pair: Gate's and Up's)
+        // quarter q of the rows, stages of parity h of the CTA's sequence; rows 0..15 of a
+        // quarter are one 16-row tile's, 16..31 the next one's (pair: Gate's and Up's)
         const int q = warp & 3, h = (warp - 4) >> 2;
         const int row = lane & 15, g = row & 7, hi = row >> 3;
         const int b = PAIR ? (lane >> 4) * 4 + q : q * 2 + (lane >> 4);
         const uint32_t expo = q4_exponent<false>();
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16) + MU_ACOL;
         Ring<MU_RAW> r;
-        int it0 = 0;                                       // stages of the tiles before
+        Ring<MU_A> f;
+        int turn = 0;                                      // parity of the next stage
         bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        for (int i = 0; i < mine && ok; ++i) {
             for (int kc = 0; kc * 4 < a.nk && ok; ++kc, r.next()) {
                 if (!mbar_wait_or_abort(&bars->raw_full[r.s], r.ph, abort_flag)) {
                     *abort_flag = 1;
@@ -282,74 +302,73 @@ moe_umma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
                 const uint8_t* src = raw_ring + (size_t)r.s * 8 * blk + b * blk;
                 const uint8_t* sc = src + Q4_CODES + q4_scale_index(row, 0, NG) * 2;
                 const uint8_t* zp = src + Q4_CODES + 32 * NG + q4_scale_index(row, 0, NG);
-                for (int c = h; c < 4; c += 2) {
-                    const int ks = kc * 4 + c;
-                    if (ks >= a.nk) break;
-                    uint32_t v[32];
-                    __half2 d[2];
-                    Q4Zero z[2];
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (half == 1 && G > 32) {
-                            d[1] = d[0];
-                            z[1] = z[0];
-                            break;
-                        }
-                        const int gi = (c * 2 + half) / (G / 32);
-                        d[half] = __half2half2(*reinterpret_cast<const __half*>(sc + gi * 4));
-                        z[half] = q4_zero<false>(a.zeros ? zp[gi * 2] : 8u);
-                    }
-#pragma unroll
-                    for (int tt = 0; tt < 4; ++tt) {
-                        const uint2 w = *reinterpret_cast<const uint2*>(src + c * 512 + (tt * 8 + g) * 16 + hi * 8);
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            uint32_t p[4];
-                            q4_decode<false>(half ? w.y : w.x, expo, z[half], p);
-#pragma unroll
-                            for (int f = 0; f < 4; ++f) {
-                                const __half2 m = __hmul2(*reinterpret_cast<const __half2*>(&p[f]), d[half]);
-                                v[16 * half + 4 * tt + f] = *reinterpret_cast<const uint32_t*>(&m);
-                            }
-                        }
-                    }
-                    const int it = it0 + ks, s = it % MU_A;
-                    if (it >= MU_A &&
-                        !mbar_wait_or_abort(&bars->a_empty[s], (uint32_t)(it / MU_A - 1) & 1u, abort_flag)) {
+                for (int c2 = 0; c2 < 2 && kc * 4 + c2 * 2 < a.nk; ++c2, f.next(), turn ^= 1) {
+                    if (turn != h) continue;
+                    if (!f.first && !mbar_wait_or_abort(&bars->a_empty[f.s], f.ph ^ 1u, abort_flag)) {
                         *abort_flag = 1;
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    tmem_st_32x32b_x32(lane_addr + (uint32_t)(s * 32), v);
+#pragma unroll
+                    for (int at = 0; at < 2; ++at) {       // two chunks of 64 k
+                        const int c = c2 * 2 + at;
+                        uint32_t v[32];
+                        __half2 d[2];
+                        Q4Zero z[2];
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            if (half == 1 && G > 32) {
+                                d[1] = d[0];
+                                z[1] = z[0];
+                                break;
+                            }
+                            const int gi = (c * 2 + half) / (G / 32);
+                            d[half] = __half2half2(*reinterpret_cast<const __half*>(sc + gi * 4));
+                            z[half] = q4_zero<false>(a.zeros ? zp[gi * 2] : 8u);
+                        }
+#pragma unroll
+                        for (int tt = 0; tt < 4; ++tt) {
+                            const uint2 w =
+                                *reinterpret_cast<const uint2*>(src + c * 512 + (tt * 8 + g) * 16 + hi * 8);
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                uint32_t p[4];
+                                q4_decode<false>(half ? w.y : w.x, expo, z[half], p);
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) {
+                                    const __half2 m = __hmul2(*reinterpret_cast<const __half2*>(&p[x]), d[half]);
+                                    v[16 * half + 4 * tt + x] = *reinterpret_cast<const uint32_t*>(&m);
+                                }
+                            }
+                        }
+                        // (an odd last stage's second half is decoded from the block's padding and not used)
+                        tmem_st_32x32b_x32(lane_addr + (uint32_t)(f.s * 64 + at * 32), v);
+                    }
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->a_full[s]);
+                    if (lane == 0) mbar_arrive(&bars->full[f.s]);
                 }
                 // the values are used: the slot is refilled through the async proxy
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->raw_empty[r.s]);
             }
-            it0 += a.nk;
         }
-    } else if (warp >= 12) {                               // ---- epilogue: group b drains accumulator b
+    } else if (warp >= 12) {                               // ---- epilogue: 32 columns in turn
         const int q = warp & 3, b = (warp - 12) >> 2;
-        const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * MU_BN);
-        const float2* scale = bars->scale[b];
-        const int* orow = bars->row[b];
+        const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
         pdl_wait();
-        uint32_t ph = 0;
-        for (int t = blockIdx.x + b * gridDim.x; t < total; t += 2 * gridDim.x, ph ^= 1u) {
-            const MuTile m = tile_at(t);
-            epi_bar(b);                                    // the last tile's scales and rows are done with
-            for (int i = tid - (12 + 4 * b) * 32; i < m.cnt; i += 128) {
-                bars->scale[b][i] = a.scales[m.p0 + i];
-                if (!PAIR) bars->row[b][i] = plan_slot(a.slots, a.nslots, m.p0 + i);
+        for (int ti = 0; ti < mine; ++ti) {
+            const MuTile m = tile_at(ti);
+            epi_bar();                                     // the last tile's scales and rows are done with
+            for (int i = tid - 12 * 32; i < m.cnt; i += 256) {
+                bars->scale[i] = a.scales[m.p0 + i];
+                if (!PAIR) bars->row[i] = plan_slot(a.slots, a.nslots, m.p0 + i);
             }
-            epi_bar(b);
-            if (!mbar_wait_or_abort(&bars->acc_full[b], ph, abort_flag)) {
+            epi_bar();
+            if (!mbar_wait_or_abort(&bars->acc_full, (uint32_t)ti & 1u, abort_flag)) {
                 *abort_flag = 1;
                 break;
             }
@@ -357,41 +376,49 @@ moe_umma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
             // pair: this lane finishes 16 of 32 positions of its row, else all of them
             const bool upper = PAIR && lane >= 16;
             const int n = PAIR ? m.r * 64 + q * 16 + (lane & 15) : m.r * 128 + q * 32 + lane;
-            const bool mine = n < a.N;
-            for (int cc = 0; cc < m.cnt; cc += 32) {
+            const bool in = n < a.N;
+            bool held = true;
+            for (int cc = 32 * b; cc < m.cnt; cc += 64) {
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(lane_addr + (uint32_t)cc, v);
                 tmem_wait_ld();
-                if (cc + 32 >= m.cnt) {                    // accumulator read: hand it back
+                if (cc + 64 >= m.cnt) {                    // this warp's last columns: hand the accumulator back
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->acc_empty[b]);
+                    if (lane == 0) mbar_arrive(&bars->acc_empty);
+                    held = false;
                 }
                 if (PAIR) {
-                    const int c0 = cc + (upper ? 16 : 0), left = mine ? m.cnt - c0 : 0;
+                    const int c0 = cc + (upper ? 16 : 0), left = in ? m.cnt - c0 : 0;
                     __half* out = a.hidden + (int64_t)(m.p0 + c0) * a.N + n;
 #pragma unroll
                     for (int i = 0; i < 16; ++i, out += a.N) {
                         const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[16 + i], 16);
-                        const float2 sc = scale[c0 + i];
+                        const float2 sc = bars->scale[c0 + i];
                         const float gt = __uint_as_float(upper ? other : v[i]) * sc.x;
                         const float up = __uint_as_float(upper ? v[16 + i] : other) * sc.x;
                         const float hv = __fdividef(gt, 1.0f + __expf(-gt)) * up;
                         if (i < left) *out = __float2half_rn(hv * sc.y);
                     }
-                } else if (mine) {
+                } else if (in) {
                     float* out = a.y + n;
                     const int left = m.cnt - cc;
                     if (left >= 32) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            out[(int64_t)orow[cc + i] * a.N] = __uint_as_float(v[i]) * scale[cc + i].y;
+                            out[(int64_t)bars->row[cc + i] * a.N] = __uint_as_float(v[i]) * bars->scale[cc + i].y;
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (i < left) out[(int64_t)orow[cc + i] * a.N] = __uint_as_float(v[i]) * scale[cc + i].y;
+                            if (i < left)
+                                out[(int64_t)bars->row[cc + i] * a.N] =
+                                    __uint_as_float(v[i]) * bars->scale[cc + i].y;
                     }
                 }
+            }
+            if (held) {                                    // a narrow tile: no columns for this warp
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->acc_empty);
             }
         }
     }
@@ -483,8 +510,8 @@ cudaError_t launch_umma_moe(const CUtensorMap& xmap, const MuArgs& a, cudaStream
     int dev = 0, sms = 152;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const size_t smem = 1024 + (size_t)MU_B * MU_B_STAGE + (size_t)MU_RAW * 8 * q4_block_bytes(G, a.zeros != 0) +
-                        sizeof(MuBars) + (size_t)(2 * (a.E + 1)) * 4;
+    const size_t smem = 1024 + (size_t)MU_B * MU_B_SLOT + (size_t)MU_RAW * 8 * q4_block_bytes(G, a.zeros != 0) +
+                        sizeof(MuBars) + (size_t)(a.E + 1) * 4;
     cudaError_t e = cudaFuncSetAttribute(moe_umma_kernel<G, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
     if (e != cudaSuccess) return e;
