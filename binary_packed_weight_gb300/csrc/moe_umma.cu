@@ -44,6 +44,12 @@ constexpr int MU_B_SLOT = MU_BN * 128;
 constexpr int MU_ACOL = MU_BN;             // first tensor-memory column of the A stages
 constexpr int MU_LIST = 64;                // tiles of a CTA that are looked up ahead
 
+// Activation rows in boxes of 32, 64, 128 and 256: a tile is loaded in at most
+// three copies a slot (one thread issues them, at about 170 cycles each).
+struct MuMaps {
+    CUtensorMap box[4];
+};
+
 struct MuTile {
     int e, p0, cnt, r;
 };
@@ -93,7 +99,7 @@ __device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, 256;" ::: 
 
 template <int G, bool PAIR>
 __global__ void __launch_bounds__(MU_THREADS, 1)
-moe_umma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ MuArgs a) {
+moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     constexpr int NG = Q4_K / G;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -117,7 +123,7 @@ moe_umma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
         mbar_init(&bars->acc_empty, 8);                    // every epilogue warp
         bars->abort = 0;
         fence_mbar_init();
-        tma_prefetch_desc(&xmap);
+        for (int i = 0; i < 4; ++i) tma_prefetch_desc(&maps.box[i]);
     }
     if (warp == 2) {
         tmem_alloc(&bars->tmem_base, 512);
@@ -193,9 +199,14 @@ moe_umma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
                     }
                     if ((ks & 1) == 0)
                         mbar_arrive_expect_tx(&bars->full[f.s], (uint32_t)boxes * (ks + 1 < a.nk ? 8192u : 4096u));
-                    for (int x = 0; x < boxes; ++x)
-                        tma_load_2d(smem + b.s * MU_B_SLOT + x * 4096, &xmap, &bars->full[f.s], ks * 64,
-                                    m.p0 + 32 * x);
+                    int at = 0;
+#pragma unroll
+                    for (int x = 3; x >= 0; --x)
+                        if (boxes & (1 << x)) {
+                            tma_load_2d(smem + b.s * MU_B_SLOT + at * 4096, &maps.box[x], &bars->full[f.s], ks * 64,
+                                        m.p0 + 32 * at);
+                            at += 1 << x;
+                        }
                     if ((ks & 1) == 1 || ks + 1 == a.nk) f.next();
                 }
             }
@@ -506,7 +517,7 @@ moe_stage_kernel(const T* __restrict__ x, int64_t ldx, int vec, int D, const int
 }
 
 template <int G, bool PAIR>
-cudaError_t launch_umma_moe(const CUtensorMap& xmap, const MuArgs& a, cudaStream_t st) {
+cudaError_t launch_umma_moe(const MuMaps& maps, const MuArgs& a, cudaStream_t st) {
     int dev = 0, sms = 152;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -515,14 +526,23 @@ cudaError_t launch_umma_moe(const CUtensorMap& xmap, const MuArgs& a, cudaStream
     cudaError_t e = cudaFuncSetAttribute(moe_umma_kernel<G, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(moe_umma_kernel<G, PAIR>, dim3((unsigned)sms), dim3(MU_THREADS), smem, st, xmap, a);
+    return launch_pdl(moe_umma_kernel<G, PAIR>, dim3((unsigned)sms), dim3(MU_THREADS), smem, st, maps, a);
+}
+
+// f16 rows of length `inner`.
+bool row_maps(MuMaps& m, __half* rows, int64_t inner, int64_t n) {
+    for (int i = 0; i < 4; ++i)
+        if (!make_tensor_map_2d(&m.box[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rows, (uint64_t)inner, (uint64_t)n,
+                                (uint64_t)inner * 2, 64u, 32u << i, CU_TENSOR_MAP_SWIZZLE_128B))
+            return false;
+    return true;
 }
 
 template <bool PAIR>
-cudaError_t launch_by_group(int group, const CUtensorMap& xmap, const MuArgs& a, cudaStream_t st) {
-    if (group == 32) return launch_umma_moe<32, PAIR>(xmap, a, st);
-    if (group == 64) return launch_umma_moe<64, PAIR>(xmap, a, st);
-    return launch_umma_moe<128, PAIR>(xmap, a, st);
+cudaError_t launch_by_group(int group, const MuMaps& maps, const MuArgs& a, cudaStream_t st) {
+    if (group == 32) return launch_umma_moe<32, PAIR>(maps, a, st);
+    if (group == 64) return launch_umma_moe<64, PAIR>(maps, a, st);
+    return launch_umma_moe<128, PAIR>(maps, a, st);
 }
 
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
@@ -560,12 +580,8 @@ cudaError_t launch_moe_tensor(const MoeTensor& m, void* scratch, cudaStream_t st
                        static_cast<const float*>(m.gate->bound), static_cast<const float*>(m.up->bound), xs, first,
                        second);
     if (e != cudaSuccess) return e;
-    CUtensorMap xmap, hmap;
-    if (!make_tensor_map_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xs, (uint64_t)D, (uint64_t)S, (uint64_t)D * 2, 64u,
-                            32u, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_tensor_map_2d(&hmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, hid, (uint64_t)F, (uint64_t)S, (uint64_t)F * 2,
-                            64u, 32u, CU_TENSOR_MAP_SWIZZLE_128B))
-        return cudaErrorInvalidValue;
+    MuMaps xmaps, hmaps;
+    if (!row_maps(xmaps, xs, D, S) || !row_maps(hmaps, hid, F, S)) return cudaErrorInvalidValue;
     MuArgs a{};
     a.w0 = m.gate->blocks;
     a.w1 = m.up->blocks;
@@ -581,7 +597,7 @@ cudaError_t launch_moe_tensor(const MoeTensor& m, void* scratch, cudaStream_t st
     a.slots = m.slots;
     a.scales = first;
     a.hidden = hid;
-    e = launch_by_group<true>(m.gate->group, xmap, a, st);
+    e = launch_by_group<true>(m.gate->group, xmaps, a, st);
     if (e != cudaSuccess) return e;
     MuArgs b = a;
     b.w0 = m.down->blocks;
@@ -595,7 +611,7 @@ cudaError_t launch_moe_tensor(const MoeTensor& m, void* scratch, cudaStream_t st
     b.scales = second;
     b.hidden = nullptr;
     b.y = m.y;
-    return launch_by_group<false>(m.down->group, hmap, b, st);
+    return launch_by_group<false>(m.down->group, hmaps, b, st);
 }
 
 unsigned int read_clear_dev_error_moe_umma(cudaStream_t st) {
