@@ -45,7 +45,7 @@ constexpr int MU_ACOL = MU_BN;             // first tensor-memory column of the 
 constexpr int MU_LIST = 64;                // tiles of a CTA that are looked up ahead
 
 // Activation rows in boxes of 32, 64, 128 and 256: a tile is loaded in at most
-// three copies a slot (one thread issues them, at about 170 cycles each).
+// three copies a slot.
 struct MuMaps {
     CUtensorMap box[4];
 };
@@ -179,42 +179,42 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
     auto tile_at = [&](int i) { return i < MU_LIST ? bars->list[i] : find_tile(blockIdx.x + i * gridDim.x); };
     const int stages = (a.nk + 1) / 2;                     // of 128 k, the last one maybe of 64
 
-    if (warp == 0) {
-        if (lane == 0) {                                   // ---- activations
-            pdl_wait();
-            Ring<MU_B> b;
-            Ring<MU_A> f;
-            bool ok = true;
-            for (int i = 0; i < mine && ok; ++i) {
-                const MuTile m = tile_at(i);
-                const int boxes = (m.cnt + 31) / 32;
-                for (int ks = 0; ks < a.nk; ++ks, b.next()) {
-                    // the slot's last MMAs are done, and those of the stage that last used the barrier
-                    if ((!b.first && !mbar_wait_or_abort(&bars->b_empty[b.s], b.ph ^ 1u, abort_flag)) ||
-                        ((ks & 1) == 0 && !f.first &&
-                         !mbar_wait_or_abort(&bars->a_empty[f.s], f.ph ^ 1u, abort_flag))) {
-                        *abort_flag = 1;
-                        ok = false;
-                        break;
-                    }
-                    if ((ks & 1) == 0)
-                        mbar_arrive_expect_tx(&bars->full[f.s], (uint32_t)boxes * (ks + 1 < a.nk ? 8192u : 4096u));
-                    int at = 0;
-#pragma unroll
-                    for (int x = 3; x >= 0; --x)
-                        if (boxes & (1 << x)) {
-                            tma_load_2d(smem + b.s * MU_B_SLOT + at * 4096, &maps.box[x], &bars->full[f.s], ks * 64,
-                                        m.p0 + 32 * at);
-                            at += 1 << x;
-                        }
-                    if ((ks & 1) == 1 || ks + 1 == a.nk) f.next();
+    if (warp == 0) {                                       // ---- activations (the whole warp, elect.sync)
+        pdl_wait();
+        Ring<MU_B> b;
+        Ring<MU_A> f;
+        bool ok = true;
+        auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, abort_flag)) != 0;
+        };
+        for (int i = 0; i < mine && ok; ++i) {
+            const MuTile m = tile_at(i);
+            const int boxes = (m.cnt + 31) / 32;
+            for (int ks = 0; ks < a.nk; ++ks, b.next()) {
+                // the slot's last MMAs are done, and those of the stage that last used the barrier
+                if ((!b.first && !wait_all(&bars->b_empty[b.s], b.ph ^ 1u)) ||
+                    ((ks & 1) == 0 && !f.first && !wait_all(&bars->a_empty[f.s], f.ph ^ 1u))) {
+                    *abort_flag = 1;
+                    ok = false;
+                    break;
                 }
+                if ((ks & 1) == 0)
+                    mbar_arrive_expect_tx_elect(&bars->full[f.s], (uint32_t)boxes * (ks + 1 < a.nk ? 8192u : 4096u));
+                int at = 0;
+#pragma unroll
+                for (int x = 3; x >= 0; --x)
+                    if (boxes & (1 << x)) {
+                        tma_load_2d_elect(smem + b.s * MU_B_SLOT + at * 4096, &maps.box[x], &bars->full[f.s], ks * 64,
+                                          m.p0 + 32 * at);
+                        at += 1 << x;
+                    }
+                if ((ks & 1) == 1 || ks + 1 == a.nk) f.next();
             }
-            // After a wait that ran out the copies already issued must land before the CTA exits.  Each is
-            // short of its barrier's phase, which may never complete: give them their (bounded) time.
-            if (!ok)
-                for (int x = 0; x < MU_A; ++x) mbar_wait(&bars->full[x], x < f.s ? f.ph : f.ph ^ 1u);
         }
+        // After a wait that ran out the copies already issued must land before the CTA exits.  Each is
+        // short of its barrier's phase, which may never complete: give them their (bounded) time.
+        if (!ok)
+            for (int x = 0; x < MU_A; ++x) mbar_wait(&bars->full[x], x < f.s ? f.ph : f.ph ^ 1u);
     } else if (warp == 3) {
         if (lane == 0) {                                   // ---- packed blocks
             Ring<MU_RAW> r;
