@@ -7,7 +7,8 @@
 // to 256 positions a tile, f16 operands and one f32 accumulator in tensor memory,
 // in stages of 128 k (what a stage costs besides its MMAs -- waits, commits, the
 // decoders' hand-offs, several hundred cycles -- does not grow with its k):
-//   * warp 0 streams the activations (B, 128-byte swizzle, 64 k a slot) by TMA;
+//   * warps 0 and 2 stream the activations (B, 128-byte swizzle) by TMA, the first
+//     and the second 64 k of a stage (one warp takes ~650 cycles a slot);
 //   * warp 3 streams the packed blocks of 256 k by bulk copies;
 //   * warps 4..11 decode a block's rows, one weight row a thread, and store
 //     them as the A operand in tensor memory (rounding (c - z) d to f16 is
@@ -111,7 +112,7 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
 
     if (tid == 0) {
         for (int s = 0; s < MU_A; ++s) {
-            mbar_init(&bars->full[s], 5);                  // the TMA producer and the stage's 4 decoder warps
+            mbar_init(&bars->full[s], 6);                  // two TMA producers and the stage's 4 decoder warps
             mbar_init(&bars->a_empty[s], 1);               // the MMA warp's commits
         }
         for (int s = 0; s < MU_B; ++s) mbar_init(&bars->b_empty[s], 1);
@@ -179,36 +180,39 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
     auto tile_at = [&](int i) { return i < MU_LIST ? bars->list[i] : find_tile(blockIdx.x + i * gridDim.x); };
     const int stages = (a.nk + 1) / 2;                     // of 128 k, the last one maybe of 64
 
-    if (warp == 0) {                                       // ---- activations (the whole warp, elect.sync)
+    if (warp == 0 || warp == 2) {                          // ---- activations (the whole warp, elect.sync)
         pdl_wait();
-        Ring<MU_B> b;
+        const int half = warp >> 1;                        // first or second 64 k of the stages
         Ring<MU_A> f;
         bool ok = true;
         auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, abort_flag)) != 0;
         };
-        for (int i = 0; i < mine && ok; ++i) {
+        uint32_t before = 0;                               // slots of the tiles before
+        for (int i = 0; i < mine && ok; ++i, before += a.nk) {
             const MuTile m = tile_at(i);
             const int boxes = (m.cnt + 31) / 32;
-            for (int ks = 0; ks < a.nk; ++ks, b.next()) {
-                // the slot's last MMAs are done, and those of the stage that last used the barrier
-                if ((!b.first && !wait_all(&bars->b_empty[b.s], b.ph ^ 1u)) ||
-                    ((ks & 1) == 0 && !f.first && !wait_all(&bars->a_empty[f.s], f.ph ^ 1u))) {
+            for (int ks = half; ks < 2 * stages; ks += 2, f.next()) {
+                const uint32_t n = before + ks, slot = n % MU_B;
+                const bool there = ks < a.nk;              // the last stage may be one slot
+                // The slot's last MMAs are done.  Where a stage is two slots that says the same of the stage
+                // that used the barrier last (four stages are at least six slots, the ring has five); else ask.
+                if ((there && n >= MU_B && !wait_all(&bars->b_empty[slot], (n / MU_B - 1) & 1u)) ||
+                    ((a.nk == 1 || !there) && !f.first && !wait_all(&bars->a_empty[f.s], f.ph ^ 1u))) {
                     *abort_flag = 1;
                     ok = false;
                     break;
                 }
-                if ((ks & 1) == 0)
-                    mbar_arrive_expect_tx_elect(&bars->full[f.s], (uint32_t)boxes * (ks + 1 < a.nk ? 8192u : 4096u));
+                mbar_arrive_expect_tx_elect(&bars->full[f.s], there ? (uint32_t)boxes * 4096u : 0u);
+                if (!there) continue;
                 int at = 0;
 #pragma unroll
                 for (int x = 3; x >= 0; --x)
                     if (boxes & (1 << x)) {
-                        tma_load_2d_elect(smem + b.s * MU_B_SLOT + at * 4096, &maps.box[x], &bars->full[f.s], ks * 64,
+                        tma_load_2d_elect(smem + slot * MU_B_SLOT + at * 4096, &maps.box[x], &bars->full[f.s], ks * 64,
                                           m.p0 + 32 * at);
                         at += 1 << x;
                     }
-                if ((ks & 1) == 1 || ks + 1 == a.nk) f.next();
             }
         }
         // After a wait that ran out the copies already issued must land before the CTA exits.  Each is
@@ -389,25 +393,28 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
             const int n = PAIR ? m.r * 64 + q * 16 + (lane & 15) : m.r * 128 + q * 32 + lane;
             const bool in = n < a.N;
             bool held = true;
-            for (int cc = 32 * b; cc < m.cnt; cc += 64) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(lane_addr + (uint32_t)cc, v);
+            uint32_t v[32], w[32];
+            // the columns after the ones at hand are read ahead; with the last ones the accumulator is handed back
+            auto read = [&](uint32_t (&x)[32], int cc) {
+                tmem_ld_32x32b_x32(lane_addr + (uint32_t)cc, x);
                 tmem_wait_ld();
-                if (cc + 64 >= m.cnt) {                    // this warp's last columns: hand the accumulator back
+                if (cc + 64 >= m.cnt) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars->acc_empty);
                     held = false;
                 }
+            };
+            auto finish = [&](const uint32_t (&x)[32], int cc) {
                 if (PAIR) {
                     const int c0 = cc + (upper ? 16 : 0), left = in ? m.cnt - c0 : 0;
                     __half* out = a.hidden + (int64_t)(m.p0 + c0) * a.N + n;
 #pragma unroll
                     for (int i = 0; i < 16; ++i, out += a.N) {
-                        const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[16 + i], 16);
+                        const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? x[i] : x[16 + i], 16);
                         const float2 sc = bars->scale[c0 + i];
-                        const float gt = __uint_as_float(upper ? other : v[i]) * sc.x;
-                        const float up = __uint_as_float(upper ? v[16 + i] : other) * sc.x;
+                        const float gt = __uint_as_float(upper ? other : x[i]) * sc.x;
+                        const float up = __uint_as_float(upper ? x[16 + i] : other) * sc.x;
                         const float hv = __fdividef(gt, 1.0f + __expf(-gt)) * up;
                         if (i < left) *out = __float2half_rn(hv * sc.y);
                     }
@@ -417,14 +424,23 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
                     if (left >= 32) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            out[(int64_t)bars->row[cc + i] * a.N] = __uint_as_float(v[i]) * bars->scale[cc + i].y;
+                            out[(int64_t)bars->row[cc + i] * a.N] = __uint_as_float(x[i]) * bars->scale[cc + i].y;
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (i < left)
                                 out[(int64_t)bars->row[cc + i] * a.N] =
-                                    __uint_as_float(v[i]) * bars->scale[cc + i].y;
+                                    __uint_as_float(x[i]) * bars->scale[cc + i].y;
                     }
+                }
+            };
+            if (32 * b < m.cnt) read(v, 32 * b);
+            for (int cc = 32 * b; cc < m.cnt; cc += 128) {
+                if (cc + 64 < m.cnt) read(w, cc + 64);
+                finish(v, cc);
+                if (cc + 64 < m.cnt) {
+                    if (cc + 128 < m.cnt) read(v, cc + 128);
+                    finish(w, cc + 64);
                 }
             }
             if (held) {                                    // a narrow tile: no columns for this warp
