@@ -457,18 +457,34 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
     }
 }
 
+// Pairs of f16 or bf16.
+template <class T>
+struct Pair;
+template <>
+struct Pair<__half> {
+    using type = __half2;
+    static __device__ __forceinline__ float2 f32(__half2 v) { return __half22float2(v); }
+};
+template <>
+struct Pair<__nv_bfloat16> {
+    using type = __nv_bfloat162;
+    static __device__ __forceinline__ float2 f32(__nv_bfloat162 v) { return __bfloat1622float2(v); }
+};
 // Eight elements of a row.
 template <class T>
-__device__ __forceinline__ void load8(const T* p, bool vec, float (&f)[8]) {
-    T raw[8];
+__device__ __forceinline__ void load8(const T* p, bool vec, typename Pair<T>::type (&v)[4]) {
     if (vec) {
-        *reinterpret_cast<uint4*>(raw) = *reinterpret_cast<const uint4*>(p);
+        *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
     } else {
+        T raw[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) raw[i] = p[i];
-    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = (float)raw[i];
+        for (int i = 0; i < 4; ++i) {
+            v[i].x = raw[2 * i];
+            v[i].y = raw[2 * i + 1];
+        }
+    }
 }
 
 // A warp a position: its row of x as f16, scaled, and the scales.  Two passes
@@ -485,13 +501,19 @@ moe_stage_kernel(const T* __restrict__ x, int64_t ldx, int vec, int D, const int
     const int end = plan_offset(offsets, nslots, E);
     for (int p = blockIdx.x * 8 + (threadIdx.x >> 5); p < end; p += gridDim.x * 8) {
         const T* row = x + (int64_t)(plan_slot(slots, nslots, p) / k) * ldx;
-        float m = 0.f, ss = 0.f, f[8];
-#pragma unroll 4
-        for (int c = lane * 8; c < D; c += 256) {
-            load8(row + c, vec != 0, f);
+        typename Pair<T>::type v[4], top[4];
+        float ss = 0.f;
+        load8(row + (lane * 8 < D ? lane * 8 : 0), vec != 0, v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
+        for (int i = 0; i < 4; ++i) top[i] = __habs2(v[i]);
+#pragma unroll 4
+        for (int c = lane * 8 + 256; c < D; c += 256) {
+            load8(row + c, vec != 0, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top[i] = __hmax2(top[i], __habs2(v[i]));
         }
+        top[0] = __hmax2(__hmax2(top[0], top[1]), __hmax2(top[2], top[3]));
+        float m = fmaxf(Pair<T>::f32(top[0]).x, Pair<T>::f32(top[0]).y);
         m = __int_as_float(__reduce_max_sync(0xffffffffu, __float_as_int(m)));   // m >= 0: its bits have its order
         const int be = (__float_as_int(m) >> 23) & 255;
         int se = be == 0 ? 253 : 127 + 14 - (be - 127);
@@ -500,15 +522,17 @@ moe_stage_kernel(const T* __restrict__ x, int64_t ldx, int vec, int D, const int
         const float s = __int_as_float(se << 23);
 #pragma unroll 4
         for (int c = lane * 8; c < D; c += 256) {
-            load8(row + c, vec != 0, f);
+            load8(row + c, vec != 0, v);
             __half2 h[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                f[i] *= s;
-                ss = fmaf(f[i], f[i], ss);
+            for (int i = 0; i < 4; ++i) {
+                float2 f = Pair<T>::f32(v[i]);
+                f.x *= s;
+                f.y *= s;
+                ss = fmaf(f.x, f.x, ss);
+                ss = fmaf(f.y, f.y, ss);
+                h[i] = __float22half2_rn(f);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
             *reinterpret_cast<uint4*>(xs + (int64_t)p * D + c) = *reinterpret_cast<uint4*>(h);
         }
 #pragma unroll

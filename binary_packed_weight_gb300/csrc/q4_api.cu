@@ -90,9 +90,9 @@ cudaError_t to_device(const void* p, size_t bytes, void** tmp, const void** dev,
     return cudaMemcpyAsync(*tmp, p, bytes, cudaMemcpyHostToDevice, st);
 }
 
-// out[t] = sum_j weights[t,j] y[t*k+j] over the routed j, in order.  One CTA
-// row per token, four columns a thread; y was written by the launch before
-// and is mostly still in L2.
+// out[t] = sum_j weights[t,j] y[t*k+j] over the routed j, in order.  A thread
+// takes four columns of a token and reads its k rows four at a time, so that
+// enough of the k*D*4 bytes a token are in flight to stream them.
 template <class T>
 __device__ __forceinline__ T round_to(float v);
 template <>
@@ -112,18 +112,33 @@ moe_combine_kernel(const float* __restrict__ y, const int32_t* __restrict__ ids,
     if (c >= D) return;
     for (int64_t t = blockIdx.x; t < T_; t += gridDim.x) {
         float s[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int j = 0; j < k; ++j) {
-            if (ids[t * k + j] < 0) continue;
-            const float w = weights[t * k + j];
-            const float* p = y + (t * k + j) * D + c;
-            if (vec) {
-                const float4 v = *reinterpret_cast<const float4*>(p);
-                s[0] = fmaf(w, v.x, s[0]);
-                s[1] = fmaf(w, v.y, s[1]);
-                s[2] = fmaf(w, v.z, s[2]);
-                s[3] = fmaf(w, v.w, s[3]);
-            } else {
-                for (int i = 0; i < 4 && c + i < D; ++i) s[i] = fmaf(w, p[i], s[i]);
+        const float* p = y + t * k * D + c;
+        if (vec) {
+            for (int j0 = 0; j0 < k; j0 += 4) {
+                float4 v[4];
+                float w[4];
+                bool on[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = j0 + i;
+                    on[i] = j < k && ids[t * k + j] >= 0;
+                    w[i] = on[i] ? weights[t * k + j] : 0.f;
+                    if (on[i]) v[i] = __ldcs(reinterpret_cast<const float4*>(p + (int64_t)j * D));
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (on[i]) {
+                        s[0] = fmaf(w[i], v[i].x, s[0]);
+                        s[1] = fmaf(w[i], v[i].y, s[1]);
+                        s[2] = fmaf(w[i], v[i].z, s[2]);
+                        s[3] = fmaf(w[i], v[i].w, s[3]);
+                    }
+            }
+        } else {
+            for (int j = 0; j < k; ++j) {
+                if (ids[t * k + j] < 0) continue;
+                const float w = weights[t * k + j];
+                for (int i = 0; i < 4 && c + i < D; ++i) s[i] = fmaf(w, p[(int64_t)j * D + i], s[i]);
             }
         }
         for (int i = 0; i < 4 && c + i < D; ++i) out[t * ldo + c + i] = round_to<T>(s[i]);
