@@ -7,14 +7,15 @@
 // holds the lowest expert, and the softmax sum's tree over neighbouring
 // experts is V-1 additions in the lane and five shuffles.  Selection values
 // are compared as order-preserving 32-bit keys: one redux.max and one ballot
-// for each of the k experts, and only the winner's lane looks for its next
-// best.
+// for each of the k experts.  A lane keeps its two best at hand and looks
+// through its keys again only if it wins a third time.
 //
-// The plan is a stable counting sort of the T*k slots.  Up to 32 tokens one
-// CTA does all of it.  Beyond, each CTA of the routing kernel leaves its
-// chunk's counts, and a second kernel (its launch overlaps the first)
-// turns them into each chunk's first positions and writes the slots: within
-// a chunk, warps count their 32 slots by match.any and a prefix over the
+// The plan is a stable counting sort of the T*k slots.  Up to a few hundred
+// tokens one cluster of CTAs does all of it, each CTA reading the others'
+// counts through distributed shared memory.  Beyond, each CTA of the routing
+// kernel leaves its chunk's counts, and a second kernel (its launch overlaps
+// the first) turns them into each chunk's first positions and writes the slots.
+// Within a chunk, warps count their 32 slots by match.any and a prefix over the
 // warps orders them, so there is no atomic whose order could matter.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -29,7 +30,7 @@ namespace {
 
 constexpr float ROUTE_TINY = 1.17549435e-38f;      // 2^-126
 constexpr float ROUTE_MOST = 3.402823466e+38f;     // largest f32
-constexpr int ROUTE_FUSED = 32;                    // tokens that one CTA plans in the routing kernel
+constexpr int ROUTE_CLUSTER = 16;                  // CTAs of a cluster at most
 
 struct RouteArgs {
     const void* logits;
@@ -45,6 +46,7 @@ struct RouteArgs {
     int32_t* counts;                               // [chunks][E], two-kernel plan
     int64_t chunk;                                 // tokens of a CTA
     int vec;                                       // rows can be read in wide loads
+    int off_rows;                                  // groups: the warps' rows in shared memory (int index)
 };
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
@@ -143,7 +145,7 @@ __device__ __forceinline__ float warp_sum(float s) {
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s;
 }
-__device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
+__device__ __forceinline__ float sigmoid(float l) { return __frcp_rn(1.0f + expf(-l)); }   // = 1 / (..), rounded
 
 // Larger value, larger key; 0 is below every number's key.
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -165,7 +167,7 @@ __device__ __forceinline__ void place_slots(const int32_t* ids, int64_t s0, int 
                                             int32_t* slots) {
     const int tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31, nw = nt >> 5;
     for (int i0 = 0; i0 < n; i0 += nt) {
-        for (int i = tid; i < nw * E; i += nt) cnt[i] = 0;
+        for (int i = tid; i < (nw * E + 1) / 2; i += nt) reinterpret_cast<uint32_t*>(cnt)[i] = 0;
         __syncthreads();
         const int i = i0 + tid;
         const int e = i < n ? ids[i] : -1;
@@ -175,6 +177,7 @@ __device__ __forceinline__ void place_slots(const int32_t* ids, int64_t s0, int 
         __syncthreads();
         for (int x = tid; x < E; x += nt) {                // exclusive prefix over the warps
             int run = 0;
+#pragma unroll 8
             for (int w = 0; w < nw; ++w) {
                 const int c = cnt[w * E + x];
                 cnt[w * E + x] = (uint16_t)run;
@@ -192,53 +195,92 @@ __device__ __forceinline__ void place_slots(const int32_t* ids, int64_t s0, int 
     }
 }
 
-// Exclusive prefix of v[0..E) in place by the first warp; returns nothing, v[E] the total.
-__device__ __forceinline__ void exclusive_prefix(int* v, int E, int lane) {
+// Exclusive prefix of v[0..E) in place, v[E] the total, by the whole CTA (in
+// rounds of its size); warps: one int a warp, plus one.
+__device__ __forceinline__ void exclusive_prefix(int* v, int E, int* warps) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
     int run = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-        const int e = e0 + lane, n = e < E ? v[e] : 0;
+    for (int e0 = 0; e0 < E; e0 += blockDim.x) {
+        const int e = e0 + tid, n = e < E ? v[e] : 0;
         int s = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int up = __shfl_up_sync(0xffffffffu, s, o);
             if (lane >= o) s += up;
         }
-        if (e < E) v[e] = run + s - n;
-        run += __shfl_sync(0xffffffffu, s, 31);
+        if (lane == 31) warps[warp] = s;
+        __syncthreads();
+        if (warp == 0) {
+            const int w = lane < nw ? warps[lane] : 0;
+            int t = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, t, o);
+                if (lane >= o) t += up;
+            }
+            if (lane < nw) warps[lane] = t - w;
+            if (lane == 31) warps[nw] = t;
+        }
+        __syncthreads();
+        if (e < E) v[e] = run + warps[warp] + s - n;
+        run += warps[nw];
+        __syncthreads();
     }
-    if (lane == 0) v[E] = run;
+    if (tid == 0) v[E] = run;
+    __syncthreads();
 }
 
+// The two best keys of a lane that come after (last, at) in the order of the
+// selection (larger key, then lower index).
+template <int V>
+__device__ __forceinline__ void two_best(const uint32_t (&key)[V], uint32_t last, int at, uint32_t& k1, int& i1,
+                                         uint32_t& k2, int& i2) {
+    k1 = k2 = 0u;
+    i1 = i2 = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const uint32_t k = key[i] < last || (key[i] == last && i > at) ? key[i] : 0u;
+        const bool first = k > k1, second = k > k2;
+        k2 = first ? k1 : second ? k : k2;
+        i2 = first ? i1 : second ? i : i2;
+        k1 = first ? k : k1;
+        i1 = first ? i : i1;
+    }
+}
+
+// One token: ids and weights, and its experts counted in hist (if any).
+// b: the bias of this lane's experts; row_s: E floats of this warp (groups).
 template <class T, int V>
-__device__ __forceinline__ void route_token(const RouteArgs& a, int64_t tok, int lane, int* hist) {
+__device__ __forceinline__ void route_token(const RouteArgs& a, int64_t tok, int lane, const float (&b)[V], int* hist,
+                                            float* row_s) {
     const unsigned FULL = 0xffffffffu;
     const int e0 = lane * V;
-    float l[V], p[V];
-    load_row<T, V>(reinterpret_cast<const T*>(a.logits) + tok * a.ld, a.E, lane, a.vec != 0, l);
-    float b[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) b[i] = a.bias && e0 + i < a.E ? a.bias[e0 + i] : 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) l[i] = available(l[i], b[i]);
-    if (a.score == MOE_SOFTMAX) {
-        float m = l[0];
-#pragma unroll
-        for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
-        m = warp_max(m);
-#pragma unroll
-        for (int i = 0; i < V; ++i) p[i] = l[i] > -INFINITY ? expf(l[i] - m) : 0.f;
-        const float s = tree_sum<V>(p);
-#pragma unroll
-        for (int i = 0; i < V; ++i) p[i] = l[i] > -INFINITY ? p[i] / s : 0.f;
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) p[i] = l[i] > -INFINITY ? sigmoid(l[i]) : 0.f;
-    }
+    const T* row = reinterpret_cast<const T*>(a.logits) + tok * a.ld;
     uint32_t key[V];
+    float most = 0.f, sum = 1.f;                           // of the softmax
     {
-        float s[V];
+        float l[V], s[V];
+        load_row<T, V>(row, a.E, lane, a.vec != 0, l);
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[i] = l[i] > -INFINITY ? (a.bias ? p[i] + b[i] : p[i]) : -INFINITY;
+        for (int i = 0; i < V; ++i) l[i] = l[i] > -INFINITY ? fminf(l[i], ROUTE_MOST) : -INFINITY;
+        if (a.bias) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) l[i] = b[i] > -INFINITY ? l[i] : -INFINITY;
+        }
+        if (a.score == MOE_SOFTMAX) {
+            most = l[0];
+#pragma unroll
+            for (int i = 1; i < V; ++i) most = fmaxf(most, l[i]);
+            most = warp_max(most);
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[i] = l[i] > -INFINITY ? expf(l[i] - most) : 0.f;
+            sum = tree_sum<V>(s);
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[i] = l[i] > -INFINITY ? s[i] / sum + b[i] : -INFINITY;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[i] = l[i] > -INFINITY ? sigmoid(l[i]) + b[i] : -INFINITY;
+        }
         uint32_t in = FULL;                                // groups that take part
         const int gs = a.E / a.groups;
         const bool grouped = a.top_groups < a.groups;
@@ -257,18 +299,25 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t tok, int
                 value = __shfl_sync(FULL, two, (lane * per) & 31);
                 if (lane >= a.groups) value = -INFINITY;
             } else {
-                for (int q = 0; q < a.groups; ++q) {
-                    float m1 = -INFINITY, m2 = -INFINITY;
+                // 32 / G lanes a group (G: a power of two) go through its values in shared memory
+                int lanes = 32;
+                while (lanes * a.groups > 32) lanes >>= 1;
 #pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        if (e0 + i >= q * gs && e0 + i < (q + 1) * gs) merge_two(m1, m2, s[i], -INFINITY);
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const float q1 = __shfl_xor_sync(FULL, m1, o), q2 = __shfl_xor_sync(FULL, m2, o);
-                        merge_two(m1, m2, q1, q2);
-                    }
-                    if (lane == q) value = m1 + (m2 > -INFINITY ? m2 : 0.f);
+                for (int i = 0; i < V; ++i)
+                    if (e0 + i < a.E) row_s[e0 + i] = s[i];
+                __syncwarp();
+                const int q = lane / lanes;
+                float m1 = -INFINITY, m2 = -INFINITY;
+                if (q < a.groups)
+                    for (int i = lane & (lanes - 1); i < gs; i += lanes) merge_two(m1, m2, row_s[q * gs + i], -INFINITY);
+                __syncwarp();
+                for (int o = 1; o < lanes; o <<= 1) {
+                    const float q1 = __shfl_xor_sync(FULL, m1, o), q2 = __shfl_xor_sync(FULL, m2, o);
+                    merge_two(m1, m2, q1, q2);
                 }
+                const float two = m1 + (m2 > -INFINITY ? m2 : 0.f);
+                value = __shfl_sync(FULL, two, (lane * lanes) & 31);
+                if (lane >= a.groups) value = -INFINITY;
             }
             int before = 0;                                // groups ahead of this one
             for (int q = 0; q < a.groups; ++q) {
@@ -276,52 +325,48 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t tok, int
                 before += (o > value || (o == value && q < lane)) ? 1 : 0;
             }
             in = __ballot_sync(FULL, lane < a.groups && before < a.top_groups);
-        }
-        int grp = grouped ? e0 / gs : 0, left = grouped ? (grp + 1) * gs - e0 : V;
+            int grp = e0 / gs, left = (grp + 1) * gs - e0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if (left == 0) {
-                ++grp;
-                left = gs;
+            for (int i = 0; i < V; ++i) {
+                if (left == 0) {
+                    ++grp;
+                    left = gs;
+                }
+                --left;
+                if (!((in >> (grp & 31)) & 1u)) s[i] = -INFINITY;
             }
-            --left;
-            key[i] = s[i] > -INFINITY && ((in >> (grp & 31)) & 1u) ? order_key(s[i]) : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = s[i] > -INFINITY ? order_key(s[i]) : 0u;
+    }
+    uint32_t k1, k2;
+    int i1, i2;
+    two_best<V>(key, FULL, V, k1, i1, k2, i2);             // (no key is all ones)
+    int id = -1;
+    bool spent = false;                                    // the second best moved up: k2 is not the next one
+    for (int j = 0; j < a.k; ++j) {
+        const uint32_t m = __reduce_max_sync(FULL, k1);
+        if (m == 0u) break;                                // none left
+        const int win = __ffs(__ballot_sync(FULL, k1 == m)) - 1;
+        const int e = __shfl_sync(FULL, e0 + i1, win);
+        if (lane == j) id = e;
+        const bool won = lane == win;
+        if (__any_sync(FULL, won && spent)) {
+            if (won) {
+                two_best<V>(key, k1, i1, k1, i1, k2, i2);
+                spent = false;
+            }
+        } else if (won) {
+            k1 = k2;
+            i1 = i2;
+            spent = true;
         }
     }
-    uint32_t best = 0;
-    int bi = 0;
-    float bp = 0.f;
-    auto look = [&]() {
-        best = 0;
-        bi = 0;
-        bp = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                bi = i;
-                bp = p[i];
-            }
-    };
-    look();
-    int id = -1;
+    // the weights: lane j scores its expert again
     float w = 0.f;
-    for (int j = 0; j < a.k; ++j) {
-        const uint32_t m = __reduce_max_sync(FULL, best);
-        if (m == 0u) break;                                // none left
-        const int win = __ffs(__ballot_sync(FULL, best == m)) - 1;
-        const int e = __shfl_sync(FULL, e0 + bi, win);
-        const float q = __shfl_sync(FULL, bp, win);
-        if (lane == j) {
-            id = e;
-            w = q;
-        }
-        if (lane == win) {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (i == bi) key[i] = 0u;
-            look();
-        }
+    if (id >= 0) {
+        const float l = available(to_f32(row[id]), 0.f);
+        w = a.score == MOE_SOFTMAX ? expf(l - most) / sum : sigmoid(l);
     }
     if (a.renorm) w = w / fmaxf(warp_sum(w), ROUTE_TINY);
     if (lane < a.k) {
@@ -331,40 +376,69 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t tok, int
     }
 }
 
-// One CTA a chunk of tokens.  FUSED: one CTA for all of them, which also
-// writes the plan.  Shared memory: counts int[E+1]; FUSED: the ids of the
-// chunk and the warps' counts too.
+// One CTA a chunk of tokens.  FUSED: the grid is one cluster, which also writes
+// the plan.  Shared memory: counts int[E+1]; FUSED: base int[E+1], before
+// int[E+1], 33 ints and the warps' counts too.
 template <class T, int V, bool FUSED>
 __global__ void __launch_bounds__(V <= 8 ? 1024 : 256) moe_route_kernel(const __grid_constant__ RouteArgs a) {
     extern __shared__ int route_smem[];
     int* hist = route_smem;
-    const int tid = threadIdx.x, nw = blockDim.x >> 5, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, nt = blockDim.x, nw = nt >> 5, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
     if (a.offsets) {
-        for (int e = tid; e <= a.E; e += blockDim.x) hist[e] = 0;
+        for (int e = tid; e <= a.E; e += nt) hist[e] = 0;
         __syncthreads();
     }
     pdl_wait();
+    float b[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        b[i] = a.bias && lane * V + i < a.E ? a.bias[lane * V + i] : 0.f;
+        if (!(b[i] > -INFINITY)) b[i] = -INFINITY;         // (a NaN too)
+    }
     const int64_t t0 = (int64_t)blockIdx.x * a.chunk;
     const int64_t t1 = t0 + a.chunk < a.T ? t0 + a.chunk : a.T;
-    for (int64_t t = t0 + warp; t < t1; t += nw) route_token<T, V>(a, t, lane, a.offsets ? hist : nullptr);
+    float* row_s = reinterpret_cast<float*>(route_smem + a.off_rows) + warp * a.E;
+    for (int64_t t = t0 + warp; t < t1; t += nw) route_token<T, V>(a, t, lane, b, a.offsets ? hist : nullptr, row_s);
     if (!a.offsets) return;
     __syncthreads();
     if (!FUSED) {
-        for (int e = tid; e < a.E; e += blockDim.x) a.counts[(int64_t)blockIdx.x * a.E + e] = hist[e];
+        for (int e = tid; e < a.E; e += nt) a.counts[(int64_t)blockIdx.x * a.E + e] = hist[e];
         return;
     }
-    if (warp == 0) exclusive_prefix(hist, a.E, lane);
+    int* base = hist + a.E + 1;
+    int* before = base + a.E + 1;                          // slots of the CTAs before
+    int* warps = before + a.E + 1;
+    uint16_t* cnt = reinterpret_cast<uint16_t*>(warps + 34);
+    const int rank = (int)blockIdx.x, C = (int)gridDim.x;
+    if (C > 1) cluster_sync();                             // every CTA's counts are there
+    for (int e = tid; e < a.E; e += nt) {
+        int all = 0, ahead = 0;
+        for (int c = 0; c < C; ++c) {
+            const int v = c == rank ? hist[e] : (int)ld_dsmem_u32(mapa_shared(smem_u32(hist + e), c));
+            all += v;
+            ahead += c < rank ? v : 0;
+        }
+        base[e] = all;
+        before[e] = ahead;
+    }
+    if (C > 1) cluster_sync();                             // the counts are read: a CTA may go
     __syncthreads();
-    const int S = (int)(a.T * a.k), total = hist[a.E];
-    for (int e = tid; e <= a.E; e += blockDim.x) a.offsets[e] = hist[e];
-    for (int s = total + tid; s < S; s += blockDim.x) a.slots[s] = -1;
-    // the ids were written by this CTA's own warps (ordered by the barrier above)
-    place_slots(a.ids, 0, S, a.E, hist, reinterpret_cast<uint16_t*>(hist + a.E + 1 + (a.E + 1) % 2), a.slots);
+    exclusive_prefix(base, a.E, warps);
+    const int64_t S = a.T * a.k;
+    const int total = base[a.E];
+    if (rank == 0)
+        for (int e = tid; e <= a.E; e += nt) a.offsets[e] = base[e];
+    for (int64_t s = total + rank * nt + tid; s < S; s += C * nt) a.slots[s] = -1;
+    __syncthreads();
+    for (int e = tid; e < a.E; e += nt) base[e] += before[e];
+    __syncthreads();
+    // the ids were written by this CTA's own warps (ordered by the barriers above)
+    if (t1 > t0) place_slots(a.ids + t0 * a.k, t0 * a.k, (int)((t1 - t0) * a.k), a.E, base, cnt, a.slots);
 }
 
 // Second kernel of the plan: CTA b places the slots of chunk b.  Shared
-// memory: base int[E+1], part int[2*E], the warps' counts.
+// memory: base int[E+1], before int[E], 33 ints, the warps' counts.
 __global__ void __launch_bounds__(1024) moe_plan_kernel(const int32_t* __restrict__ ids,
                                                         const int32_t* __restrict__ counts, int chunks, int64_t chunk,
                                                         int64_t T, int E, int k, int32_t* __restrict__ offsets,
@@ -372,32 +446,45 @@ __global__ void __launch_bounds__(1024) moe_plan_kernel(const int32_t* __restric
     extern __shared__ int plan_smem[];
     int* base = plan_smem;                                 // first the totals, then each expert's first position
     int* before = base + E + 1;                            // slots of earlier chunks
-    uint16_t* cnt = reinterpret_cast<uint16_t*>(before + E + (E + 1 + E) % 2);
+    int* warps = before + E;
+    uint16_t* cnt = reinterpret_cast<uint16_t*>(warps + 34 + (E + 1 + E) % 2);
     const int tid = threadIdx.x, nt = blockDim.x, b = blockIdx.x;
     pdl_launch_dependents();
+    pdl_wait();
+    // column sums of the counts, many loads in flight: as many threads to a column as fit
     for (int i = tid; i < E; i += nt) {
         base[i] = 0;
         before[i] = 0;
     }
     __syncthreads();
-    pdl_wait();
-    // column sums of the counts: as many threads to a column as fit
     const int cols = E < nt ? E : nt, rows = nt / cols;
-    if (tid < cols * rows)
-        for (int e = tid % cols; e < E; e += cols) {
-            int all = 0, mine = 0;
+    if (tid < cols * rows) {
+        const int c0 = tid / cols;
+        for (int e = tid - c0 * cols; e < E; e += cols) {
+            const int32_t* p = counts + e;
+            int all = 0, mine = 0, c = c0;
+            for (; c + 15 * rows < chunks; c += 16 * rows) {
+                int v[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = p[(int64_t)(c + i * rows) * E];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    all += v[i];
+                    mine += c + i * rows < b ? v[i] : 0;
+                }
+            }
 #pragma unroll 8
-            for (int c = tid / cols; c < chunks; c += rows) {
-                const int v = counts[(int64_t)c * E + e];
+            for (; c < chunks; c += rows) {
+                const int v = p[(int64_t)c * E];
                 all += v;
                 mine += c < b ? v : 0;
             }
             atomicAdd(base + e, all);                      // counts: the order does not matter
             atomicAdd(before + e, mine);
         }
+    }
     __syncthreads();
-    if (tid < 32) exclusive_prefix(base, E, tid);
-    __syncthreads();
+    exclusive_prefix(base, E, warps);
     const int64_t S = T * k;
     if (b == 0)
         for (int e = tid; e <= E; e += nt) offsets[e] = base[e];
@@ -501,28 +588,60 @@ int experts_a_lane(int E) {
     return V;
 }
 
+template <class F>
+cudaError_t raise_smem(F* kernel, size_t smem) {
+    if (smem <= 48 * 1024) return cudaSuccess;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+}
+
+int sm_count() {
+    static int known[64];                                  // never changes: asked once
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 64 && known[dev]) return known[dev];
+    int sms = 152;
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (dev < 64) known[dev] = sms;
+    return sms;
+}
+
 template <class T, int V>
 cudaError_t launch_route(RouteArgs a, cudaStream_t st) {
     a.vec = wide_ok(a.logits, a.ld, a.E, V, (int)sizeof(T)) ? 1 : 0;
     constexpr int MOST = V <= 8 ? 32 : 8;                  // warps of a CTA
-    const size_t head = (size_t)(a.E + 1 + (a.E + 1) % 2) * 4;
-    if (a.T <= ROUTE_FUSED) {
-        const int nw = a.T < MOST ? (int)a.T : MOST;
-        a.chunk = a.T;
-        const size_t smem = head + (size_t)nw * a.E * 2;
-        if (smem > 48 * 1024) {
-            cudaError_t e = cudaFuncSetAttribute(moe_route_kernel<T, V, true>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e != cudaSuccess) return e;
-        }
-        return launch_pdl(moe_route_kernel<T, V, true>, dim3(1), dim3(nw * 32), smem, st, a);
+    const size_t head = (size_t)(3 * (a.E + 1) + 34) * 4;
+    const bool grouped = a.top_groups < a.groups;
+    // one cluster, a token a warp
+    if (a.T <= ROUTE_CLUSTER * MOST) {
+        int C = 1;
+        while (C < ROUTE_CLUSTER && C * 4 < a.T) C *= 2;   // few tokens a CTA: their instructions bound it
+        a.chunk = (a.T + C - 1) / C;
+        const int nw = a.chunk < MOST ? (int)a.chunk : MOST;
+        a.off_rows = (int)((head + ((size_t)nw * a.E * 2 + 3) / 4 * 4) / 4);
+        const size_t smem = (size_t)a.off_rows * 4 + (grouped ? (size_t)nw * a.E * 4 : 0);
+        cudaError_t e = raise_smem(moe_route_kernel<T, V, true>, smem);
+        if (e == cudaSuccess && C > 8)
+            e = cudaFuncSetAttribute(moe_route_kernel<T, V, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)C);
+        cfg.blockDim = dim3((unsigned)nw * 32);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)C;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = C > 1 ? 2 : 1;
+        return cudaLaunchKernelEx(&cfg, moe_route_kernel<T, V, true>, a);
     }
-    int dev = 0, sms = 152;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     // a chunk a CTA, at most one CTA of 32 warps (four of 8) on each SM
     int64_t chunks = (a.T + MOST - 1) / MOST;
-    const int64_t limit = (int64_t)sms * (MOST == 32 ? 1 : 4);
+    const int64_t limit = (int64_t)sm_count() * (MOST == 32 ? 1 : 4);
     if (chunks > limit) chunks = limit;
     a.chunk = (a.T + chunks - 1) / chunks;
     chunks = (a.T + a.chunk - 1) / a.chunk;
@@ -533,13 +652,16 @@ cudaError_t launch_route(RouteArgs a, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         a.counts = static_cast<int32_t*>(mem);
     }
-    e = launch_pdl(moe_route_kernel<T, V, false>, dim3((unsigned)chunks), dim3(MOST * 32), head, st, a);
+    a.off_rows = (int)(head / 4);
+    const size_t smem = head + (grouped ? (size_t)MOST * a.E * 4 : 0);
+    e = raise_smem(moe_route_kernel<T, V, false>, smem);
+    if (e == cudaSuccess)
+        e = launch_pdl(moe_route_kernel<T, V, false>, dim3((unsigned)chunks), dim3(MOST * 32), smem, st, a);
     if (e == cudaSuccess && a.offsets) {
-        const size_t smem = (size_t)(2 * a.E + 2) * 4 + (size_t)32 * a.E * 2;
-        if (smem > 48 * 1024)
-            e = cudaFuncSetAttribute(moe_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const size_t plan = (size_t)(2 * a.E + 36) * 4 + (size_t)32 * a.E * 2;
+        e = raise_smem(moe_plan_kernel, plan);
         if (e == cudaSuccess)
-            e = launch_pdl(moe_plan_kernel, dim3((unsigned)chunks), dim3(1024), smem, st,
+            e = launch_pdl(moe_plan_kernel, dim3((unsigned)chunks), dim3(1024), plan, st,
                            static_cast<const int32_t*>(a.ids), static_cast<const int32_t*>(a.counts), (int)chunks,
                            a.chunk, a.T, a.E, a.k, a.offsets, a.slots);
     }
@@ -554,11 +676,8 @@ template <class T, int V>
 cudaError_t launch_route_backward(RouteBackArgs a, cudaStream_t st) {
     a.vec = wide_ok(a.logits, a.ld, a.E, V, (int)sizeof(T)) ? 1 : 0;
     a.vecd = wide_ok(a.dl, a.ldd, a.E, V, (int)sizeof(T)) ? 1 : 0;
-    int dev = 0, sms = 152;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     int64_t grid = (a.T + 7) / 8;
-    if (grid > (int64_t)sms * 8) grid = (int64_t)sms * 8;
+    if (grid > (int64_t)sm_count() * 8) grid = (int64_t)sm_count() * 8;
     return launch_pdl(moe_route_backward_kernel<T, V>, dim3((unsigned)grid), dim3(256), 0, st, a);
 }
 
