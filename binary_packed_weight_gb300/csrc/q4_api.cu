@@ -191,10 +191,10 @@ tq2_status q4_upload(const uint8_t* codes, const uint16_t* scales, const uint8_t
                      int64_t K, int group, q4_handle* out, void* stream) {
     if (out) *out = nullptr;
     if (!codes || !scales || !out) return (tq2_status)set_error(TQ2_EINVAL, "q4_upload: null pointer");
-    if (E < 1 || E > 1024 || N < 1 || N > (1 << 24) || !format_ok(K, group))
+    if (E < 1 || E > 1024 || N < 1 || N > (1 << 24) || !format_ok(K, group) || N * K > ((int64_t)1 << 36))
         return (tq2_status)set_error(TQ2_ESHAPE,
                                      "q4_upload: need 1 <= E <= 1024, 1 <= N <= 2^24, group 32, 64 or 128, K a "
-                                     "multiple of it up to 32768 (E=%lld N=%lld K=%lld group=%d)",
+                                     "multiple of it up to 32768, N*K <= 2^36 (E=%lld N=%lld K=%lld group=%d)",
                                      (long long)E, (long long)N, (long long)K, group);
     if ((reinterpret_cast<uintptr_t>(codes) & 1) != 0 || (reinterpret_cast<uintptr_t>(scales) & 1) != 0)
         return (tq2_status)set_error(TQ2_EINVAL, "q4_upload: codes and scales must be 2-byte aligned");
@@ -346,7 +346,7 @@ tq2_status moe_experts(q4_handle gate, q4_handle up, q4_handle down, const void*
     float* hid = reinterpret_cast<float*>(static_cast<char*>(mem.p) + ybytes);
     // rows of one expert: the average, and room for the spread around it
     const int64_t mean = (S + E - 1) / E;
-    const int64_t spread = mean + 2 * (int64_t)ceil(sqrt((double)mean));
+    const int64_t spread = (mean + 2 * (int64_t)ceil(sqrt((double)mean)) + 7) / 8 * 8;
     const int64_t most = spread < T ? spread : T;
     Q4Stream a = stream_of(gate);
     a.w1 = up->blocks;

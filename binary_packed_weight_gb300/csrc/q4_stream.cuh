@@ -10,14 +10,15 @@
 // f32.  So the only roundings are those of f32 accumulation.
 //
 // The weights are read once and bound the time.  A CTA takes a contiguous range
-// of 16-row tiles; their blocks (tiles x 256-k chunks) are one sequence that is
-// cut evenly among its sixteen warps, so a warp's part may begin and end inside
-// a tile.  A warp reads its blocks straight into registers, one block ahead of
-// the one it multiplies (34 KB in flight on an SM), and leaves its sum of each
-// tile it touches in shared memory; after the last block the parts of every
-// tile are added in a fixed order.  Only there do warps wait for each other.
-// The activations sit in shared memory for the CTA's whole life (one matrix) or
-// per matrix of the plan.
+// of 16-row tiles; the blocks (tiles x 256-k chunks) of one pass over its rows
+// of x are one sequence that is cut evenly among its sixteen warps, so a warp's
+// part may begin and end inside a tile.  A warp reads its blocks straight into
+// registers, one block ahead of the one it multiplies (34 KB in flight on an
+// SM).  Tiles that it has to itself it stores from registers; of the at most
+// two that it shares it leaves its part in shared memory, and after the last
+// block those parts are added in a fixed order.  Only there do warps wait for
+// each other.  The activations sit in shared memory for the CTA's whole life
+// (one matrix) or per pass of the plan.
 //
 // A decode call lasts a few microseconds, so what a warp does once counts as
 // much as the blocks (two to six a warp): there is one copy of the block's code,
@@ -49,8 +50,7 @@ struct Q4Kernel {
     int parts;                         // f16 columns of a row
     int tiles;                         // 16-row tiles of a pass (both matrices' of a pair)
     int each, more;                    // no plan: tiles of a CTA, and CTAs that take one more
-    int batch;                         // tiles summed together
-    uint32_t rcp;                      // ceil(2^20 / nkc): i / nkc for i * nkc < 2^20
+    uint32_t rcp;                      // ceil(2^32 / nkc) (nkc > 1): i / nkc for i * nkc < 2^32
     int pitch;                         // bytes of an activation column in shared memory
     int xvec;                          // rows of x are 16-byte aligned
     int off_prefix, off_scale, off_red, off_x;   // shared-memory layout
@@ -96,6 +96,7 @@ struct Q4Pass {
     int e, p0, cnt;
 };
 __device__ __forceinline__ Q4Pass q4_pass(const Q4Kernel& k, const int* prefix, int j) {
+    const int* offs = prefix + k.a.E + 1;
     int lo = 0, hi = k.a.E;                               // prefix[lo] <= j < prefix[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -103,8 +104,8 @@ __device__ __forceinline__ Q4Pass q4_pass(const Q4Kernel& k, const int* prefix, 
     }
     Q4Pass p;
     p.e = lo;
-    p.p0 = q4_offset(k.a, lo) + (j - prefix[lo]) * k.tok;
-    p.cnt = min(k.tok, q4_offset(k.a, lo + 1) - p.p0);
+    p.p0 = offs[lo] + (j - prefix[lo]) * k.tok;
+    p.cnt = min(k.tok, offs[lo + 1] - p.p0);
     return p;
 }
 
@@ -122,10 +123,12 @@ __device__ __forceinline__ bool q4_stage_x(const Q4Kernel& k, uint8_t* smem, con
     uint8_t* xs = smem + k.off_x;
     float* inv = reinterpret_cast<float*>(smem + k.off_scale);
     int* top = reinterpret_cast<int*>(inv + 32);
+    int* orow = top + 32;
     const int K = (int)k.a.K;
+    __syncthreads();                                       // the previous rows and their scales are done with
+    if (warp == Q4_WARPS - 1 && lane < p.cnt) orow[lane] = k.a.oslot ? q4_slot(k.a, p.p0 + lane) : p.p0 + lane;
     if (k.a.xmode == Q4_X_RAW16) {
         if (!k.xvec) {
-            __syncthreads();                               // the previous rows are done with
             for (int i = warp; i < p.cnt; i += Q4_WARPS) {
                 const uint16_t* src = reinterpret_cast<const uint16_t*>(k.a.x) + q4_xrow(k, p.p0 + i) * k.a.ldx;
                 for (int c = lane; c < K; c += 32) reinterpret_cast<uint16_t*>(xs + i * k.pitch)[c] = src[c];
@@ -133,8 +136,6 @@ __device__ __forceinline__ bool q4_stage_x(const Q4Kernel& k, uint8_t* smem, con
             __syncthreads();
             return true;
         }
-        fence_proxy_async_shared();
-        __syncthreads();
         if (warp == 0) {
             if (lane == 0) mbar_arrive_expect_tx(xbar, (uint32_t)(p.cnt * K * 2));
             __syncwarp();
@@ -145,9 +146,9 @@ __device__ __forceinline__ bool q4_stage_x(const Q4Kernel& k, uint8_t* smem, con
         }
         const bool ok = mbar_wait(xbar, xphase);
         xphase ^= 1u;
+        __syncthreads();                                   // (the output rows)
         return ok;
     }
-    __syncthreads();                                       // the previous rows and their scales are done with
     if (tid < 32) top[tid] = 0;
     __syncthreads();
     // nw warps a row, which read it twice (the second time from L1)
@@ -248,14 +249,15 @@ struct Q4Block {
 template <int G, int NT, bool BF, bool PLAN>
 __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __grid_constant__ Q4Kernel k) {
     extern __shared__ __align__(128) uint8_t smem[];
-    constexpr int SEG = NT * 8 * Q4_RED_PITCH;             // floats of a part of a tile
     const Q4Stream& a = k.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const uint32_t blk = (uint32_t)q4_block_bytes(G, a.zeros != 0);
     uint64_t* xbar = reinterpret_cast<uint64_t*>(smem);
-    int2* ends = reinterpret_cast<int2*>(smem + 128);      // first and last warp of each tile of a batch
+    int* nshared = reinterpret_cast<int*>(smem + 8);
+    int4* shared_units = reinterpret_cast<int4*>(smem + 16);   // unit, first and last warp
     int* prefix = reinterpret_cast<int*>(smem + k.off_prefix);
     const float* inv = reinterpret_cast<const float*>(smem + k.off_scale);
+    const int* orow = reinterpret_cast<const int*>(inv + 64);
     float* red = reinterpret_cast<float*>(smem + k.off_red);
     const int nkc = a.nkc;
 
@@ -263,33 +265,39 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
         mbar_init(xbar, 1);
         fence_mbar_init();
     }
-    if (a.K != nkc * Q4_K)                                 // k past the row's end is zero for the kernel's whole life
+    if (a.K != nkc * Q4_K) {                               // k past the row's end is zero for the kernel's whole life
         for (int c = 0; c < k.tok * k.parts; ++c)
             for (int i = (int)a.K + 2 * tid; i < nkc * Q4_K; i += 2 * Q4_WARPS * 32)
                 *reinterpret_cast<uint32_t*>(smem + k.off_x + c * k.pitch + i * 2) = 0u;
+        fence_proxy_async_shared();
+    }
     __syncthreads();
     pdl_launch_dependents();
 
-    // the CTA's tiles (whole pairs)
+    // the CTA's tiles (whole units: a tile, or a pair of them)
     const int two = PLAN && a.pair ? 2 : 1;
     int u0, u1;
     if (PLAN) {
         pdl_wait();                                        // the plan is an earlier kernel's
         if (warp == 0) {
+            int* offs = prefix + a.E + 1;
             int run = 0;
-            for (int e0 = 0; e0 < a.E; e0 += 32) {
+            for (int e0 = 0; e0 <= a.E; e0 += 32) {
                 const int e = e0 + lane;
-                const int n = e < a.E ? max(q4_offset(a, e + 1) - q4_offset(a, e) + k.tok - 1, 0) / k.tok : 0;
+                const int o = e <= a.E ? q4_offset(a, e) : 0;
+                const int n = e < a.E ? max(q4_offset(a, e + 1) - o + k.tok - 1, 0) / k.tok : 0;
                 int s = n;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int up = __shfl_up_sync(0xffffffffu, s, o);
-                    if (lane >= o) s += up;
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int up = __shfl_up_sync(0xffffffffu, s, d);
+                    if (lane >= d) s += up;
                 }
-                if (e < a.E) prefix[e] = run + s - n;
+                if (e <= a.E) {
+                    prefix[e] = run + s - n;
+                    offs[e] = o;
+                }
                 run += __shfl_sync(0xffffffffu, s, 31);
             }
-            if (lane == 0) prefix[a.E] = run;
         }
         __syncthreads();
         const unsigned all = (unsigned)prefix[a.E] * (unsigned)(k.tiles / two);
@@ -303,7 +311,7 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
     }
     if (u0 >= u1) return;                                  // uniform; the plan's wait is done
 
-    // A batch: tiles of one pass; warp w takes its blocks L*w/16 .. L*(w+1)/16.
+    // The tiles of one pass; warp w takes their blocks L*w/16 .. L*(w+1)/16.
     struct Batch {
         int j, first, n;                                   // pass, first tile of the pass, tiles
         int i0, i1;                                        // blocks of this warp
@@ -313,7 +321,7 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
         Batch b;
         b.j = PLAN ? u / k.tiles : 0;
         b.first = u - b.j * k.tiles;
-        b.n = min(min(u1 - u, k.tiles - b.first), k.batch);
+        b.n = min(u1 - u, k.tiles - b.first);
         const int L = b.n * nkc;
         b.i0 = L * warp / Q4_WARPS;
         b.i1 = L * (warp + 1) / Q4_WARPS;
@@ -322,16 +330,20 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
         return b;
     };
     const int64_t second = PLAN && a.pair ? a.w1 - a.w0 : 0;
-    auto block_ptr = [&](const Batch& b, int i) {
-        const int tl = (int)((uint32_t)i * k.rcp >> 20), tile = b.first + tl, kc = i - tl * nkc;
-        const int rt = two == 2 ? tile >> 1 : tile;
+    auto tile_of = [&](int i) { return nkc > 1 ? (int)__umulhi((uint32_t)i, k.rcp) : i; };
+    auto block_ptr = [&](const Batch& b, int tl, int kc) {
+        const int tile = b.first + tl, rt = two == 2 ? tile >> 1 : tile;
         const uint32_t index = (uint32_t)(((rt >> 3) * nkc + kc) * 8 + (rt & 7));
         const uint8_t* p = b.w + (int64_t)index * blk;
         return two == 2 && (tile & 1) ? p + second : p;
     };
+    auto first_ptr = [&](const Batch& b) {
+        const int tl = tile_of(b.i0);
+        return block_ptr(b, tl, b.i0 - tl * nkc);
+    };
     Batch b = batch_at(u0);
     Q4Block<G> cur;
-    if (b.i0 < b.i1) cur.load(block_ptr(b, b.i0), lane, a.zeros);
+    if (b.i0 < b.i1) cur.load(first_ptr(b), lane, a.zeros);
     if (!PLAN) pdl_wait();                                 // x is an earlier kernel's; the weights are not
 
     const uint32_t expo = q4_exponent<BF>();
@@ -340,6 +352,13 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
     Q4Pass pass{0, 0, a.M};
     uint32_t xa[NT];
     int cols = 0;
+
+    auto store = [&](float v, int m, int row) {
+        const int64_t o = (int64_t)orow[m] * a.ldo + row;
+        if (PLAN || a.otype == TQ2_F32) reinterpret_cast<float*>(a.out)[o] = v;
+        else if (a.otype == TQ2_F16) reinterpret_cast<__half*>(a.out)[o] = __float2half_rn(v);
+        else reinterpret_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
+    };
 
     for (int u = u0;;) {
         if (b.j != staged) {
@@ -353,22 +372,25 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
                 xa[n] = smem_u32(smem + k.off_x) + t * 16 + min(n * 8 + g, cols - 1) * k.pitch;
         }
         const int un = u + b.n;
-        const bool again = un < u1;
+        const bool again = PLAN && un < u1;
         Batch next{};
         if (again) next = batch_at(un);
-        float tot[NT][4];
+        const int L = b.n * nkc, U = two * nkc;
+        const int seg = cols * Q4_RED_PITCH;               // floats of a part of a tile
+        float tot[NT][4], hold[PLAN ? NT : 1][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) tot[n][i] = 0.f;
-        int tile = (int)((uint32_t)b.i0 * k.rcp >> 20), kc = b.i0 - tile * nkc;
-        if (b.i0 == b.i1 && again && next.i0 < next.i1) cur.load(block_ptr(next, next.i0), lane, a.zeros);
+        int tl = tile_of(b.i0), kc = b.i0 - tl * nkc;
+        if (PLAN && b.i0 == b.i1 && again && next.i0 < next.i1) cur.load(first_ptr(next), lane, a.zeros);
 
 #pragma unroll 1
         for (int i = b.i0; i < b.i1; ++i) {
             Q4Block<G> ahead;
-            if (i + 1 < b.i1) ahead.load(block_ptr(b, i + 1), lane, a.zeros);
-            else if (again && next.i0 < next.i1) ahead.load(block_ptr(next, next.i0), lane, a.zeros);
+            const bool last = kc + 1 == nkc;
+            if (i + 1 < b.i1) ahead.load(block_ptr(b, last ? tl + 1 : tl, last ? 0 : kc + 1), lane, a.zeros);
+            else if (again && next.i0 < next.i1) ahead.load(first_ptr(next), lane, a.zeros);
             const uint32_t xo = (uint32_t)kc * 512u;
             float acc[NT][4];
             float d0, d1;
@@ -415,58 +437,104 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
                 }
             }
             cur = ahead;
-            if (++kc == nkc || i + 1 == b.i1) {            // this warp's part of a tile: [column][16 rows]
-                float* q = red + (warp + tile) * SEG + 2 * t * Q4_RED_PITCH + g;
+            if (last || i + 1 == b.i1) {
+                const int unit = two == 2 ? tl >> 1 : tl, half = tl & (two - 1);
+                if (unit * U >= b.i0 && (unit + 1) * U <= b.i1) {   // this warp has the unit to itself
+                    if (PLAN && half + 1 < two) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    q[n * 8 * Q4_RED_PITCH] = tot[n][0];
-                    q[n * 8 * Q4_RED_PITCH + Q4_RED_PITCH] = tot[n][1];
-                    q[n * 8 * Q4_RED_PITCH + 8] = tot[n][2];
-                    q[n * 8 * Q4_RED_PITCH + Q4_RED_PITCH + 8] = tot[n][3];
-                    tot[n][0] = tot[n][1] = tot[n][2] = tot[n][3] = 0.f;
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) hold[PLAN ? n : 0][c] = tot[n][c];
+                    } else {
+                        const int row = ((b.first + tl) / two) * 16 + g;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                // split rows: columns 2t, 2t+1 are the two parts of row n*4 + t
+                                const int m = k.parts == 2 ? n * 4 + t : n * 8 + 2 * t + c;
+                                if (m >= pass.cnt || (k.parts == 2 && c == 1)) continue;
+                                const float s = a.xmode == Q4_X_RAW16 ? 1.f : inv[m];
+#pragma unroll
+                                for (int r = 0; r < 2; ++r) {
+                                    float v = tot[n][2 * r + c];
+                                    if (k.parts == 2) v += tot[n][2 * r + 1];
+                                    v *= s;
+                                    if (PLAN && a.pair) {
+                                        float f = hold[PLAN ? n : 0][2 * r + c];
+                                        if (k.parts == 2) f += hold[PLAN ? n : 0][2 * r + 1];
+                                        f *= s;
+                                        v = f / (1.0f + expf(-f)) * v;
+                                    }
+                                    if (row + 8 * r < a.N) store(v, m, row + 8 * r);
+                                }
+                            }
+                    }
+                } else {                                   // its part of the tile: [column][16 rows]
+                    const int slot = 2 * warp + (b.i0 >= unit * U ? 0 : 1);
+                    float* q = red + (slot * two + half) * seg + 2 * t * Q4_RED_PITCH + g;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            if (n * 8 + 2 * t + c < cols) {
+                                q[(n * 8 + c) * Q4_RED_PITCH] = tot[n][c];
+                                q[(n * 8 + c) * Q4_RED_PITCH + 8] = tot[n][2 + c];
+                            }
                 }
-                ++tile;
-                kc = 0;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) tot[n][0] = tot[n][1] = tot[n][2] = tot[n][3] = 0.f;
             }
+            kc = last ? 0 : kc + 1;
+            tl = last ? tl + 1 : tl;
         }
-        const int L = b.n * nkc;
-        if (tid < b.n)                                     // warps of the tile's first and last block
-            ends[tid] = make_int2(((tid * nkc + 1) * Q4_WARPS - 1) / L, ((tid + 1) * nkc * Q4_WARPS - 1) / L);
+        // the units that warps share: warp w's part begins inside one
+        if (warp == 0) {
+            const int at = L * lane / Q4_WARPS, before = L * (lane - 1) / Q4_WARPS;
+            const int unit = (two == 2 ? tile_of(at) >> 1 : tile_of(at)), start = unit * U;
+            // the first boundary strictly inside the unit lists it
+            const bool mine = lane > 0 && lane < Q4_WARPS && at > start && (lane == 1 || before <= start);
+            const uint32_t who = __ballot_sync(0xffffffffu, mine);
+            if (mine) {
+                int lastw = lane;
+                while (lastw + 1 < Q4_WARPS && L * (lastw + 1) / Q4_WARPS < start + U) ++lastw;
+                shared_units[__popc(who & ((1u << lane) - 1u))] = make_int4(unit, lane - 1, lastw, 0);
+            }
+            if (lane == 0) *nshared = __popc(who);
+        }
         __syncthreads();
-        // sixteen lanes a tile and row of x: parts in the order of the warps, then of x
-        const int nt = b.n / two;
-        const float rnt = 1.0f / (float)nt;
-        for (int q = tid >> 4; q < nt * pass.cnt; q += Q4_WARPS * 2) {
-            const int m = (int)(((float)q + 0.5f) * rnt), tl = (q - m * nt) * two;
-            const int row = ((b.first + tl) / two) * 16 + (tid & 15);
-            auto sum = [&](int tile_) {
-                const int2 w = ends[tile_];
-                const float* s = red + (w.x + tile_) * SEG + m * k.parts * Q4_RED_PITCH + (tid & 15);
+        // sixteen lanes a unit and row of x: parts in the order of the warps, then of x
+        const int nu = *nshared;
+        const float rnu = 1.0f / (float)nu;
+        for (int q = tid >> 4; q < nu * pass.cnt; q += Q4_WARPS * 2) {
+            const int m = (int)(((float)q + 0.5f) * rnu);
+            const int4 su = shared_units[q - m * nu];
+            const int row = (b.first / two + su.x) * 16 + (tid & 15);
+            auto sum = [&](int half) {
+                const int ts = su.x * U + half * nkc, te = ts + nkc;
                 float v = 0.f;
 #pragma unroll 1
-                for (int i = w.x; i <= w.y; ++i, s += SEG) {
-                    if (L * i / Q4_WARPS == L * (i + 1) / Q4_WARPS) continue;   // fewer blocks than warps
+                for (int w = su.y; w <= su.z; ++w) {
+                    const int w0 = L * w / Q4_WARPS, w1 = L * (w + 1) / Q4_WARPS;
+                    if (max(w0, ts) >= min(w1, te)) continue;   // no block of this tile
+                    const float* s = red + ((2 * w + (w0 >= su.x * U ? 0 : 1)) * two + half) * seg +
+                                     m * k.parts * Q4_RED_PITCH + (tid & 15);
                     v += s[0];
                     if (k.parts == 2) v += s[Q4_RED_PITCH];
                 }
                 return a.xmode == Q4_X_RAW16 ? v : v * inv[m];
             };
-            float v = sum(tl);
+            float v = sum(0);
             if (PLAN && a.pair) {
-                const float up = sum(tl + 1);
+                const float up = sum(1);
                 v = v / (1.0f + expf(-v)) * up;
             }
-            if (row >= a.N) continue;
-            const int p = pass.p0 + m;
-            const int64_t o = (PLAN && a.oslot ? (int64_t)q4_slot(a, p) : (int64_t)p) * a.ldo + row;
-            if (a.otype == TQ2_F32) reinterpret_cast<float*>(a.out)[o] = v;
-            else if (a.otype == TQ2_F16) reinterpret_cast<__half*>(a.out)[o] = __float2half_rn(v);
-            else reinterpret_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
+            if (row < a.N) store(v, m, row);
         }
         if (!again) break;
         u = un;
         b = next;
-        __syncthreads();                                   // the parts are read before the next batch's are left
+        fence_proxy_async_shared();                        // the next pass's rows come through the async proxy
     }
 }
 
@@ -487,41 +555,32 @@ inline Q4Device q4_device() {
     return d;
 }
 
-// Shared memory beside the activation columns, for batches of `batch` tiles.
-template <int NT>
-int q4_fixed(const Q4Stream& a, int batch, Q4Kernel* k) {
+// Shared memory of a launch that takes `tok` rows a pass.
+inline int q4_smem(const Q4Stream& a, int parts, int pitch, int tok, Q4Kernel* k) {
     auto up = [](int v) { return (v + 127) / 128 * 128; };
-    const int prefix = 256;
-    const int scale = up(prefix + (a.offsets ? (a.E + 1) * 4 : 0));
-    const int red = scale + 256;
-    const int x = up(red + (Q4_WARPS + batch - 1) * NT * 8 * Q4_RED_PITCH * 4);
+    const int prefix = up(16 + 16 * Q4_WARPS);
+    const int scale = up(prefix + (a.offsets ? 2 * (a.E + 1) * 4 : 0));
+    const int red = scale + 3 * 32 * 4;
+    const int x = up(red + 2 * Q4_WARPS * (a.pair ? 2 : 1) * tok * parts * Q4_RED_PITCH * 4);
     if (k) {
         k->off_prefix = prefix;
         k->off_scale = scale;
         k->off_red = red;
         k->off_x = x;
     }
-    return x;
+    return x + tok * parts * pitch;
 }
-
-constexpr int Q4_MAX_BATCH = 16;
 
 template <int G, int NT, bool BF, bool PLAN>
 cudaError_t q4_stream_launch(Q4Kernel& k, int tok, const Q4Device& dev, cudaStream_t st) {
     const Q4Stream& a = k.a;
     k.tok = tok;
     k.tiles = (int)((a.N + 15) / 16) * (a.pair ? 2 : 1);
-    k.rcp = ((1u << 20) + a.nkc - 1) / a.nkc;
+    k.rcp = a.nkc > 1 ? (uint32_t)((((uint64_t)1 << 32) + a.nkc - 1) / a.nkc) : 0;
     const int grid = PLAN || k.tiles > dev.sms ? dev.sms : k.tiles;
     k.each = k.tiles / grid;
     k.more = k.tiles - k.each * grid;
-    // no longer batches than a CTA has tiles, nor than shared memory holds
-    int batch = PLAN || k.each >= Q4_MAX_BATCH ? Q4_MAX_BATCH : k.each + 1;
-    const int xbytes = tok * k.parts * k.pitch;
-    if (a.pair) batch = (batch + 1) / 2 * 2;
-    while (batch > 2 && q4_fixed<NT>(a, batch, nullptr) + xbytes > dev.smem) batch -= 2;
-    k.batch = batch;
-    const int smem = q4_fixed<NT>(a, k.batch, &k) + xbytes;
+    const int smem = q4_smem(a, k.parts, k.pitch, tok, &k);
     if (smem > dev.smem) return cudaErrorInvalidValue;
     static std::atomic<uint64_t> raised{0};                // devices whose limit of this kernel is raised
     int d = 0;
@@ -570,13 +629,12 @@ cudaError_t q4_stream_run(const Q4Stream& a, cudaStream_t st) {
     const int el = a.xmode == Q4_X_RAW16 ? 2 : 4;
     k.xvec = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && (a.ldx * el) % 16 == 0;
     const Q4Device dev = q4_device();
-    auto tokens = [&](int nt, int fixed) {                 // rows a pass of nt column tiles can take
-        int c = (dev.smem - fixed) / k.pitch;
-        c = (c < 8 * nt ? c : 8 * nt) / k.parts;
-        return c < a.tokens ? c : a.tokens;
+    auto tokens = [&](int nt) {                            // rows a pass of nt column tiles can take
+        int tok = a.tokens * k.parts < 8 * nt ? a.tokens : 8 * nt / k.parts;
+        while (tok > 0 && q4_smem(a, k.parts, k.pitch, tok, nullptr) > dev.smem) --tok;
+        return tok;
     };
-    const int t4 = tokens(4, q4_fixed<4>(a, 2, nullptr)), t2 = tokens(2, q4_fixed<2>(a, 2, nullptr)),
-              t1 = tokens(1, q4_fixed<1>(a, 2, nullptr));
+    const int t4 = tokens(4), t2 = tokens(2), t1 = tokens(1);
     if (t4 > t2 && t4 * k.parts > 16) return q4_stream_pick<G, 4>(k, t4, dev, st);
     if (t2 > t1 && t2 * k.parts > 8) return q4_stream_pick<G, 2>(k, t2, dev, st);
     if (t1 < 1) return cudaErrorInvalidValue;

@@ -443,7 +443,8 @@ typedef struct q4_weight* q4_handle;
  *           All three in HOST or in DEVICE memory (each by itself); codes
  *           2-byte aligned.  Copied: the caller keeps ownership.
  *   E, N, K, group   E, N >= 1, E <= 1024, group 32, 64 or 128, K >= group a
- *           multiple of it, K <= 32768, N <= 2^24.  Else TQ2_ESHAPE.
+ *           multiple of it, K <= 32768, N <= 2^24, N*K <= 2^36.  Else
+ *           TQ2_ESHAPE.
  *   out     receives the handle (NULL on failure).
  *   stream  used for the copies and the layout kernel, after work queued on
  *           it; the call synchronizes it before returning.
