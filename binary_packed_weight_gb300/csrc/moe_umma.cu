@@ -10,13 +10,13 @@
 //   * warps 0 and 2 stream the activations (B, 128-byte swizzle) by TMA, the first
 //     and the second 64 k of a stage (one warp takes ~650 cycles a slot);
 //   * warp 3 streams the packed blocks of 256 k by bulk copies;
-//   * warps 4..11 decode a block's rows, one weight row a thread, and store
-//     them as the A operand in tensor memory (rounding (c - z) d to f16 is
-//     the only rounding of the weights);
+//   * two or three groups of four decoder warps, which take turns, decode a
+//     block's rows, one weight row a thread, and store them as the A operand in
+//     tensor memory (rounding (c - z) d to f16 is the only rounding of the weights);
 //   * warp 1 issues the MMAs; one barrier a stage covers both operands, and the
 //     next stage's is tested while this stage's MMAs run;
-//   * warps 12..19 drain the finished tile, 32 columns each in turn, while the
-//     next tile's operands fill their rings.
+//   * eight epilogue warps drain the finished tile, some columns each in turn,
+//     while the next tile's operands fill their rings.
 // A tile of the first product holds 64 rows of Gate and the same 64 of Up: lanes
 // 0..15 of each quarter are Gate's, 16..31 Up's, so one shuffle meets the two.
 //
@@ -36,7 +36,17 @@ namespace tq2 {
 
 namespace {
 
-constexpr int MU_THREADS = 640;
+// Decoder groups (of four warps) and columns an epilogue warp takes at a time:
+// three groups feed narrow tiles, whose MMAs are short; with two, an epilogue
+// warp has the registers for 32 columns and the next 32 (64 experts of
+// 2048x1024, 64 / 512 / 2048 tokens of top 8: 96 / 115 / 277 us against 107 / 117 / 259 us).
+template <bool WIDE>
+struct MuShape {
+    static constexpr int GROUPS = WIDE ? 2 : 3;
+    static constexpr int EPI = 4 + 4 * GROUPS;             // first epilogue warp
+    static constexpr int THREADS = 32 * (EPI + 8);
+    static constexpr int CW = WIDE ? 32 : 16;
+};
 constexpr int MU_BN = 256;                 // positions of a tile
 constexpr int MU_B = 5;                    // activation slots of 64 k (32 KB)
 constexpr int MU_A = 4;                    // stages of 128 k: decoded weights (64 tensor-memory columns each)
@@ -56,7 +66,7 @@ struct MuTile {
 };
 
 struct MuBars {
-    uint64_t full[MU_A], a_empty[MU_A], b_empty[MU_B], raw_full[MU_RAW], raw_empty[MU_RAW];
+    uint64_t full[MU_A], empty[MU_A], half_empty[MU_A], raw_full[MU_RAW], raw_empty[MU_RAW];
     uint64_t acc_full, acc_empty;
     uint32_t tmem_base;
     int abort;
@@ -98,11 +108,13 @@ struct MuArgs {
 // Barrier of the eight epilogue warps.
 __device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-template <int G, bool PAIR>
-__global__ void __launch_bounds__(MU_THREADS, 1)
+template <int G, bool PAIR, bool WIDE>
+__global__ void __launch_bounds__(MuShape<WIDE>::THREADS, 1)
 moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     constexpr int NG = Q4_K / G;
+    constexpr int MU_GROUPS = MuShape<WIDE>::GROUPS, MU_EPI = MuShape<WIDE>::EPI, MU_THREADS = MuShape<WIDE>::THREADS;
+    constexpr int CW = MuShape<WIDE>::CW;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int blk = q4_block_bytes(G, a.zeros != 0);
     uint8_t* raw_ring = smem + MU_B * MU_B_SLOT;
@@ -113,12 +125,12 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
     if (tid == 0) {
         for (int s = 0; s < MU_A; ++s) {
             mbar_init(&bars->full[s], 6);                  // two TMA producers and the stage's 4 decoder warps
-            mbar_init(&bars->a_empty[s], 1);               // the MMA warp's commits
+            mbar_init(&bars->empty[s], 1);                 // the MMA warp's commits: a stage, its first 64 k
+            mbar_init(&bars->half_empty[s], 1);
         }
-        for (int s = 0; s < MU_B; ++s) mbar_init(&bars->b_empty[s], 1);
         for (int r = 0; r < MU_RAW; ++r) {
             mbar_init(&bars->raw_full[r], 1);
-            mbar_init(&bars->raw_empty[r], 8);             // every decoder warp
+            mbar_init(&bars->raw_empty[r], 4 * MU_GROUPS); // every decoder warp
         }
         mbar_init(&bars->acc_full, 1);
         mbar_init(&bars->acc_empty, 8);                    // every epilogue warp
@@ -180,47 +192,47 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
     auto tile_at = [&](int i) { return i < MU_LIST ? bars->list[i] : find_tile(blockIdx.x + i * gridDim.x); };
     const int stages = (a.nk + 1) / 2;                     // of 128 k, the last one maybe of 64
 
-    if (warp == 0 || warp == 2) {                          // ---- activations (the whole warp, elect.sync)
+    if (warp == 0 || warp == 2) {                          // ---- activations
         pdl_wait();
-        const int half = warp >> 1;                        // first or second 64 k of the stages
-        Ring<MU_A> f;
-        bool ok = true;
-        auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
-            return __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, abort_flag)) != 0;
-        };
-        uint32_t before = 0;                               // slots of the tiles before
-        for (int i = 0; i < mine && ok; ++i, before += a.nk) {
-            const MuTile m = tile_at(i);
-            const int boxes = (m.cnt + 31) / 32;
-            for (int ks = half; ks < 2 * stages; ks += 2, f.next()) {
-                const uint32_t n = before + ks, slot = n % MU_B;
-                const bool there = ks < a.nk;              // the last stage may be one slot
-                // The slot's last MMAs are done.  Where a stage is two slots that says the same of the stage
-                // that used the barrier last (four stages are at least six slots, the ring has five); else ask.
-                if ((there && n >= MU_B && !wait_all(&bars->b_empty[slot], (n / MU_B - 1) & 1u)) ||
-                    ((a.nk == 1 || !there) && !f.first && !wait_all(&bars->a_empty[f.s], f.ph ^ 1u))) {
-                    *abort_flag = 1;
-                    ok = false;
-                    break;
-                }
-                mbar_arrive_expect_tx_elect(&bars->full[f.s], there ? (uint32_t)boxes * 4096u : 0u);
-                if (!there) continue;
-                int at = 0;
-#pragma unroll
-                for (int x = 3; x >= 0; --x)
-                    if (boxes & (1 << x)) {
-                        tma_load_2d_elect(smem + slot * MU_B_SLOT + at * 4096, &maps.box[x], &bars->full[f.s], ks * 64,
-                                          m.p0 + 32 * at);
-                        at += 1 << x;
+        if (elect_one()) {
+            const int half = warp >> 1;                    // first or second 64 k of the stages
+            Ring<MU_A> f;
+            bool ok = true;
+            uint32_t stage = 0;                            // of the CTA's sequence; its slots are 2*stage, 2*stage + 1
+            for (int i = 0; i < mine && ok; ++i) {
+                const MuTile m = tile_at(i);
+                const int boxes = (m.cnt + 31) / 32;
+                for (int ks = half; ks < 2 * stages; ks += 2, ++stage, f.next()) {
+                    // the slot's last use, five slots ago, was in the other half of stage (2*stage + half - 5) / 2:
+                    // its MMAs are done
+                    const uint32_t n = 2 * stage + half, slot = n % MU_B, old = (n - MU_B) / 2;
+                    uint64_t* freed = half ? &bars->half_empty[old % MU_A] : &bars->empty[old % MU_A];
+                    if (n >= MU_B && !mbar_wait_or_abort(freed, (old / MU_A) & 1u, abort_flag)) {
+                        *abort_flag = 1;
+                        ok = false;
+                        break;
                     }
+                    const bool there = ks < a.nk;          // the last stage may be one slot
+                    mbar_arrive_expect_tx(&bars->full[f.s], there ? (uint32_t)boxes * 4096u : 0u);
+                    if (!there) continue;
+                    int at = 0;
+#pragma unroll
+                    for (int x = 3; x >= 0; --x)
+                        if (boxes & (1 << x)) {
+                            tma_load_2d(smem + slot * MU_B_SLOT + at * 4096, &maps.box[x], &bars->full[f.s], ks * 64,
+                                        m.p0 + 32 * at);
+                            at += 1 << x;
+                        }
+                }
             }
+            // After a wait that ran out the copies already issued must land before the CTA exits.  Each is
+            // short of its barrier's phase, which may never complete: give them their (bounded) time.
+            if (!ok)
+                for (int x = 0; x < MU_A; ++x) mbar_wait(&bars->full[x], x < f.s ? f.ph : f.ph ^ 1u);
         }
-        // After a wait that ran out the copies already issued must land before the CTA exits.  Each is
-        // short of its barrier's phase, which may never complete: give them their (bounded) time.
-        if (!ok)
-            for (int x = 0; x < MU_A; ++x) mbar_wait(&bars->full[x], x < f.s ? f.ph : f.ph ^ 1u);
+        __syncwarp();
     } else if (warp == 3) {
-        if (lane == 0) {                                   // ---- packed blocks
+        if (elect_one()) {                                 // ---- packed blocks
             Ring<MU_RAW> r;
             bool ok = true;
             const uint32_t bytes = 8u * (uint32_t)blk;
@@ -250,62 +262,61 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
                 for (int i = 0; i < MU_RAW; ++i)
                     mbar_wait(&bars->raw_full[i], i < r.s ? r.ph : r.ph ^ 1u);
         }
-    } else if (warp == 1) {                                // ---- MMA issuer (the whole warp, elect.sync)
-        auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
-            return __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, abort_flag, true)) != 0;
-        };
-        Ring<MU_B> b;
-        Ring<MU_A> f;
-        bool ok = true, ready = false;
-        int cnt = mine > 0 ? tile_at(0).cnt : 0;
-        for (int i = 0; i < mine && ok; ++i) {
-            const uint32_t idesc = idesc_f16_f32(128, (uint32_t)((cnt + 15) / 16 * 16));
-            if (i > 0 && !wait_all(&bars->acc_empty, (uint32_t)(i - 1) & 1u)) {
-                *abort_flag = 1;
-                break;
-            }
-            tc_fence_after();
-            for (int st = 0; st < stages; ++st) {
-                if (!ready && !wait_all(&bars->full[f.s], f.ph)) {
+    } else if (warp == 1) {                                // ---- MMA issuer
+        if (elect_one()) {
+            uint32_t slot = 0;                             // of the stage's first 64 k
+            Ring<MU_A> f;
+            bool ok = true, ready = false;
+            int cnt = mine > 0 ? tile_at(0).cnt : 0;
+            for (int i = 0; i < mine && ok; ++i) {
+                const uint32_t idesc = idesc_f16_f32(128, (uint32_t)((cnt + 15) / 16 * 16));
+                if (i > 0 && !mbar_wait_or_abort(&bars->acc_empty, (uint32_t)(i - 1) & 1u, abort_flag, true)) {
                     *abort_flag = 1;
-                    ok = false;
                     break;
                 }
-                Ring<MU_A> g = f;
-                g.next();
-                ready = mbar_test_wait(&bars->full[g.s], g.ph);   // its latency hides under the MMAs below
                 tc_fence_after();
-                const uint32_t acol = tmem + MU_ACOL + (uint32_t)(f.s * 64);
+                for (int st = 0; st < stages; ++st) {
+                    if (!ready && !mbar_wait_or_abort(&bars->full[f.s], f.ph, abort_flag, true)) {
+                        *abort_flag = 1;
+                        ok = false;
+                        break;
+                    }
+                    Ring<MU_A> g = f;
+                    g.next();
+                    ready = mbar_test_wait(&bars->full[g.s], g.ph);   // its latency hides under the MMAs below
+                    tc_fence_after();
+                    const uint32_t acol = tmem + MU_ACOL + (uint32_t)(f.s * 64);
 #pragma unroll
-                for (int at = 0; at < 2; ++at) {
-                    if (at == 1 && 2 * st + 1 >= a.nk) break;
-                    const uint64_t bdesc = sdesc_kmajor_sw128(smem_u32(smem + b.s * MU_B_SLOT));
+                    for (int at = 0; at < 2; ++at) {
+                        if (at == 0 || 2 * st + 1 < a.nk) {
+                            const uint64_t bdesc = sdesc_kmajor_sw128(smem_u32(smem + slot * MU_B_SLOT));
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        umma_f16_ts_elect(tmem, acol + (uint32_t)(at * 32 + j * 8), bdesc + (uint64_t)(2 * j), idesc,
-                                          (st > 0 || at > 0 || j > 0) ? 1u : 0u);
-                    umma_commit_elect(&bars->b_empty[b.s]);
-                    b.next();
+                            for (int j = 0; j < 4; ++j)
+                                umma_f16_ts(tmem, acol + (uint32_t)(at * 32 + j * 8), bdesc + (uint64_t)(2 * j), idesc,
+                                            (st > 0 || at > 0 || j > 0) ? 1u : 0u);
+                        }
+                        if (++slot == MU_B) slot = 0;
+                        umma_commit(at == 0 ? &bars->half_empty[f.s] : &bars->empty[f.s]);
+                    }
+                    f = g;
                 }
-                umma_commit_elect(&bars->a_empty[f.s]);
-                f = g;
-                ready = __all_sync(0xffffffffu, ready);
+                if (!ok) break;
+                umma_commit(&bars->acc_full);
+                if (i + 1 < mine) cnt = tile_at(i + 1).cnt;
             }
-            if (!ok) break;
-            umma_commit_elect(&bars->acc_full);
-            if (i + 1 < mine) cnt = tile_at(i + 1).cnt;
         }
-    } else if (warp >= 4 && warp < 12) {                   // ---- decoders
-        // quarter q of the rows, stages of parity h of the CTA's sequence; rows 0..15 of a
+        __syncwarp();
+    } else if (warp >= 4 && warp < MU_EPI) {               // ---- decoders
+        // quarter q of the rows, every third stage of the CTA's sequence; rows 0..15 of a
         // quarter are one 16-row tile's, 16..31 the next one's (pair: Gate's and Up's)
-        const int q = warp & 3, h = (warp - 4) >> 2;
+        const int q = warp & 3;
         const int row = lane & 15, g = row & 7, hi = row >> 3;
         const int b = PAIR ? (lane >> 4) * 4 + q : q * 2 + (lane >> 4);
         const uint32_t expo = q4_exponent<false>();
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16) + MU_ACOL;
         Ring<MU_RAW> r;
         Ring<MU_A> f;
-        int turn = 0;                                      // parity of the next stage
+        int turn = (warp - 4) >> 2;                        // stages until this group's next one
         bool ok = true;
         for (int i = 0; i < mine && ok; ++i) {
             for (int kc = 0; kc * 4 < a.nk && ok; ++kc, r.next()) {
@@ -317,49 +328,48 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
                 const uint8_t* src = raw_ring + (size_t)r.s * 8 * blk + b * blk;
                 const uint8_t* sc = src + Q4_CODES + q4_scale_index(row, 0, NG) * 2;
                 const uint8_t* zp = src + Q4_CODES + 32 * NG + q4_scale_index(row, 0, NG);
-                for (int c2 = 0; c2 < 2 && kc * 4 + c2 * 2 < a.nk; ++c2, f.next(), turn ^= 1) {
-                    if (turn != h) continue;
-                    if (!f.first && !mbar_wait_or_abort(&bars->a_empty[f.s], f.ph ^ 1u, abort_flag)) {
-                        *abort_flag = 1;
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                for (int c2 = 0; c2 < 2 && kc * 4 + c2 * 2 < a.nk; ++c2, f.next()) {
+                    if (turn-- > 0) continue;
+                    turn = MU_GROUPS - 1;
+                    // (an odd last stage's second half is decoded from the block's padding and not used)
+                    uint2 w[2][4];
+#pragma unroll
+                    for (int at = 0; at < 2; ++at)
+#pragma unroll
+                        for (int tt = 0; tt < 4; ++tt)
+                            w[at][tt] = *reinterpret_cast<const uint2*>(src + (c2 * 2 + at) * 512 + (tt * 8 + g) * 16 +
+                                                                        hi * 8);
 #pragma unroll
                     for (int at = 0; at < 2; ++at) {       // two chunks of 64 k
                         const int c = c2 * 2 + at;
                         uint32_t v[32];
-                        __half2 d[2];
-                        Q4Zero z[2];
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
-                            if (half == 1 && G > 32) {
-                                d[1] = d[0];
-                                z[1] = z[0];
-                                break;
-                            }
                             const int gi = (c * 2 + half) / (G / 32);
-                            d[half] = __half2half2(*reinterpret_cast<const __half*>(sc + gi * 4));
-                            z[half] = q4_zero<false>(a.zeros ? zp[gi * 2] : 8u);
-                        }
+                            const __half2 d = __half2half2(*reinterpret_cast<const __half*>(sc + gi * 4));
+                            const Q4Zero z = q4_zero<false>(a.zeros ? zp[gi * 2] : 8u);
 #pragma unroll
-                        for (int tt = 0; tt < 4; ++tt) {
-                            const uint2 w =
-                                *reinterpret_cast<const uint2*>(src + c * 512 + (tt * 8 + g) * 16 + hi * 8);
-#pragma unroll
-                            for (int half = 0; half < 2; ++half) {
+                            for (int tt = 0; tt < 4; ++tt) {
                                 uint32_t p[4];
-                                q4_decode<false>(half ? w.y : w.x, expo, z[half], p);
+                                q4_decode<false>(half ? w[at][tt].y : w[at][tt].x, expo, z, p);
 #pragma unroll
                                 for (int x = 0; x < 4; ++x) {
-                                    const __half2 m = __hmul2(*reinterpret_cast<const __half2*>(&p[x]), d[half]);
+                                    const __half2 m = __hmul2(*reinterpret_cast<const __half2*>(&p[x]), d);
                                     v[16 * half + 4 * tt + x] = *reinterpret_cast<const uint32_t*>(&m);
                                 }
                             }
                         }
-                        // (an odd last stage's second half is decoded from the block's padding and not used)
+                        if (at == 0) {
+                            if (!f.first && !mbar_wait_or_abort(&bars->empty[f.s], f.ph ^ 1u, abort_flag)) {
+                                *abort_flag = 1;
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                        }
                         tmem_st_32x32b_x32(lane_addr + (uint32_t)(f.s * 64 + at * 32), v);
                     }
+                    if (!ok) break;
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -371,14 +381,14 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
                 if (lane == 0) mbar_arrive(&bars->raw_empty[r.s]);
             }
         }
-    } else if (warp >= 12) {                               // ---- epilogue: 32 columns in turn
-        const int q = warp & 3, b = (warp - 12) >> 2;
+    } else if (warp >= MU_EPI) {                           // ---- epilogue: 32 columns in turn
+        const int q = warp & 3, b = (warp - MU_EPI) >> 2;
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
         pdl_wait();
         for (int ti = 0; ti < mine; ++ti) {
             const MuTile m = tile_at(ti);
             epi_bar();                                     // the last tile's scales and rows are done with
-            for (int i = tid - 12 * 32; i < m.cnt; i += 256) {
+            for (int i = tid - MU_EPI * 32; i < m.cnt; i += 256) {
                 bars->scale[i] = a.scales[m.p0 + i];
                 if (!PAIR) bars->row[i] = plan_slot(a.slots, a.nslots, m.p0 + i);
             }
@@ -388,59 +398,61 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
                 break;
             }
             tc_fence_after();
-            // pair: this lane finishes 16 of 32 positions of its row, else all of them
+            // pair: this lane finishes half of CW positions of its row, else all of them
             const bool upper = PAIR && lane >= 16;
             const int n = PAIR ? m.r * 64 + q * 16 + (lane & 15) : m.r * 128 + q * 32 + lane;
             const bool in = n < a.N;
             bool held = true;
-            uint32_t v[32], w[32];
+            uint32_t v[CW], w[CW];
             // the columns after the ones at hand are read ahead; with the last ones the accumulator is handed back
-            auto read = [&](uint32_t (&x)[32], int cc) {
-                tmem_ld_32x32b_x32(lane_addr + (uint32_t)cc, x);
+            auto read = [&](uint32_t (&x)[CW], int cc) {
+                if constexpr (CW == 32) tmem_ld_32x32b_x32(lane_addr + (uint32_t)cc, x);
+                else tmem_ld_32x32b_x16(lane_addr + (uint32_t)cc, x);
                 tmem_wait_ld();
-                if (cc + 64 >= m.cnt) {
+                if (cc + 2 * CW >= m.cnt) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars->acc_empty);
                     held = false;
                 }
             };
-            auto finish = [&](const uint32_t (&x)[32], int cc) {
+            auto finish = [&](const uint32_t (&x)[CW], int cc) {
                 if (PAIR) {
-                    const int c0 = cc + (upper ? 16 : 0), left = in ? m.cnt - c0 : 0;
+                    constexpr int H = CW / 2;
+                    const int c0 = cc + (upper ? H : 0), left = in ? m.cnt - c0 : 0;
                     __half* out = a.hidden + (int64_t)(m.p0 + c0) * a.N + n;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i, out += a.N) {
-                        const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? x[i] : x[16 + i], 16);
+                    for (int i = 0; i < H; ++i, out += a.N) {
+                        const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? x[i] : x[H + i], 16);
                         const float2 sc = bars->scale[c0 + i];
                         const float gt = __uint_as_float(upper ? other : x[i]) * sc.x;
-                        const float up = __uint_as_float(upper ? x[16 + i] : other) * sc.x;
+                        const float up = __uint_as_float(upper ? x[H + i] : other) * sc.x;
                         const float hv = __fdividef(gt, 1.0f + __expf(-gt)) * up;
                         if (i < left) *out = __float2half_rn(hv * sc.y);
                     }
                 } else if (in) {
                     float* out = a.y + n;
                     const int left = m.cnt - cc;
-                    if (left >= 32) {
+                    if (left >= CW) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
+                        for (int i = 0; i < CW; ++i)
                             out[(int64_t)bars->row[cc + i] * a.N] = __uint_as_float(x[i]) * bars->scale[cc + i].y;
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
+                        for (int i = 0; i < CW; ++i)
                             if (i < left)
                                 out[(int64_t)bars->row[cc + i] * a.N] =
                                     __uint_as_float(x[i]) * bars->scale[cc + i].y;
                     }
                 }
             };
-            if (32 * b < m.cnt) read(v, 32 * b);
-            for (int cc = 32 * b; cc < m.cnt; cc += 128) {
-                if (cc + 64 < m.cnt) read(w, cc + 64);
+            if (CW * b < m.cnt) read(v, CW * b);
+            for (int cc = CW * b; cc < m.cnt; cc += 4 * CW) {
+                if (cc + 2 * CW < m.cnt) read(w, cc + 2 * CW);
                 finish(v, cc);
-                if (cc + 64 < m.cnt) {
-                    if (cc + 128 < m.cnt) read(v, cc + 128);
-                    finish(w, cc + 64);
+                if (cc + 2 * CW < m.cnt) {
+                    if (cc + 4 * CW < m.cnt) read(v, cc + 4 * CW);
+                    finish(w, cc + 2 * CW);
                 }
             }
             if (held) {                                    // a narrow tile: no columns for this warp
@@ -556,17 +568,18 @@ moe_stage_kernel(const T* __restrict__ x, int64_t ldx, int vec, int D, const int
     }
 }
 
-template <int G, bool PAIR>
+template <int G, bool PAIR, bool WIDE>
 cudaError_t launch_umma_moe(const MuMaps& maps, const MuArgs& a, cudaStream_t st) {
     int dev = 0, sms = 152;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const size_t smem = 1024 + (size_t)MU_B * MU_B_SLOT + (size_t)MU_RAW * 8 * q4_block_bytes(G, a.zeros != 0) +
                         sizeof(MuBars) + (size_t)(a.E + 1) * 4;
-    cudaError_t e = cudaFuncSetAttribute(moe_umma_kernel<G, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(moe_umma_kernel<G, PAIR, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(moe_umma_kernel<G, PAIR>, dim3((unsigned)sms), dim3(MU_THREADS), smem, st, maps, a);
+    return launch_pdl(moe_umma_kernel<G, PAIR, WIDE>, dim3((unsigned)sms), dim3(MuShape<WIDE>::THREADS), smem, st,
+                      maps, a);
 }
 
 // f16 rows of length `inner`.
@@ -580,9 +593,13 @@ bool row_maps(MuMaps& m, __half* rows, int64_t inner, int64_t n) {
 
 template <bool PAIR>
 cudaError_t launch_by_group(int group, const MuMaps& maps, const MuArgs& a, cudaStream_t st) {
-    if (group == 32) return launch_umma_moe<32, PAIR>(maps, a, st);
-    if (group == 64) return launch_umma_moe<64, PAIR>(maps, a, st);
-    return launch_umma_moe<128, PAIR>(maps, a, st);
+    // wide tiles from 96 rows a matrix on average
+    const bool wide = a.nslots >= 96 * (int64_t)a.E;
+    if (group == 32)
+        return wide ? launch_umma_moe<32, PAIR, true>(maps, a, st) : launch_umma_moe<32, PAIR, false>(maps, a, st);
+    if (group == 64)
+        return wide ? launch_umma_moe<64, PAIR, true>(maps, a, st) : launch_umma_moe<64, PAIR, false>(maps, a, st);
+    return wide ? launch_umma_moe<128, PAIR, true>(maps, a, st) : launch_umma_moe<128, PAIR, false>(maps, a, st);
 }
 
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }

@@ -155,7 +155,7 @@ cudaError_t launch_combine(const float* y, const int32_t* ids, const float* w, v
 }
 
 // Average rows of a matrix from which f16 and bf16 calls take the tensor-core path.
-constexpr int64_t MOE_TENSOR_ROWS = 32;
+constexpr int64_t MOE_TENSOR_ROWS = 10;
 
 // Scratch of one call, given back on the same stream whatever happens.
 struct Scratch {
