@@ -53,7 +53,7 @@ struct Q4Kernel {
     uint32_t rcp;                      // ceil(2^32 / nkc) (nkc > 1): i / nkc for i * nkc < 2^32
     int pitch;                         // bytes of an activation column in shared memory
     int xvec;                          // rows of x are 16-byte aligned
-    int off_prefix, off_scale, off_red, off_x;   // shared-memory layout
+    int off_prefix, off_slots, off_scale, off_red, off_x;   // shared-memory layout (off_slots 0: none)
 };
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -90,6 +90,7 @@ __device__ __forceinline__ void q4_mma0(float (&d)[4], const uint32_t (&a)[4], u
 
 __device__ __forceinline__ int q4_offset(const Q4Stream& a, int e) { return plan_offset(a.offsets, a.nslots, e); }
 __device__ __forceinline__ int q4_slot(const Q4Stream& a, int p) { return plan_slot(a.slots, a.nslots, p); }
+constexpr int Q4_PLAN_SLOTS = 512;     // plans of at most this many slots are kept in shared memory whole
 
 // Pass j of the plan: rows p0 .. p0+cnt of matrix e.
 struct Q4Pass {
@@ -109,8 +110,12 @@ __device__ __forceinline__ Q4Pass q4_pass(const Q4Kernel& k, const int* prefix, 
     return p;
 }
 
-__device__ __forceinline__ int64_t q4_xrow(const Q4Kernel& k, int p) {
-    return k.a.xdiv ? q4_slot(k.a, p) / k.a.xdiv : p;
+// Slot and x row of position p.
+__device__ __forceinline__ int q4_slot_of(const Q4Kernel& k, const uint8_t* smem, int p) {
+    return k.off_slots ? reinterpret_cast<const int*>(smem + k.off_slots)[p] : q4_slot(k.a, p);
+}
+__device__ __forceinline__ int64_t q4_xrow(const Q4Kernel& k, const uint8_t* smem, int p) {
+    return k.a.xdiv ? q4_slot_of(k, smem, p) / k.a.xdiv : p;
 }
 
 // Activation rows of a pass into shared memory: column (row i, part q) at
@@ -126,11 +131,11 @@ __device__ __forceinline__ bool q4_stage_x(const Q4Kernel& k, uint8_t* smem, con
     int* orow = top + 32;
     const int K = (int)k.a.K;
     __syncthreads();                                       // the previous rows and their scales are done with
-    if (warp == Q4_WARPS - 1 && lane < p.cnt) orow[lane] = k.a.oslot ? q4_slot(k.a, p.p0 + lane) : p.p0 + lane;
+    if (warp == Q4_WARPS - 1 && lane < p.cnt) orow[lane] = k.a.oslot ? q4_slot_of(k, smem, p.p0 + lane) : p.p0 + lane;
     if (k.a.xmode == Q4_X_RAW16) {
         if (!k.xvec) {
             for (int i = warp; i < p.cnt; i += Q4_WARPS) {
-                const uint16_t* src = reinterpret_cast<const uint16_t*>(k.a.x) + q4_xrow(k, p.p0 + i) * k.a.ldx;
+                const uint16_t* src = reinterpret_cast<const uint16_t*>(k.a.x) + q4_xrow(k, smem, p.p0 + i) * k.a.ldx;
                 for (int c = lane; c < K; c += 32) reinterpret_cast<uint16_t*>(xs + i * k.pitch)[c] = src[c];
             }
             __syncthreads();
@@ -141,7 +146,7 @@ __device__ __forceinline__ bool q4_stage_x(const Q4Kernel& k, uint8_t* smem, con
             __syncwarp();
             if (lane < p.cnt)
                 bulk_load(xs + lane * k.pitch,
-                          reinterpret_cast<const uint16_t*>(k.a.x) + q4_xrow(k, p.p0 + lane) * k.a.ldx,
+                          reinterpret_cast<const uint16_t*>(k.a.x) + q4_xrow(k, smem, p.p0 + lane) * k.a.ldx,
                           (uint32_t)K * 2, xbar);
         }
         const bool ok = mbar_wait(xbar, xphase);
@@ -162,7 +167,7 @@ __device__ __forceinline__ bool q4_stage_x(const Q4Kernel& k, uint8_t* smem, con
     for (int i0 = 0; i0 < p.cnt; i0 += Q4_WARPS / nw) {
         const int i = i0 + warp / nw;
         const bool on = i < p.cnt;
-        const float* src = reinterpret_cast<const float*>(k.a.x) + (on ? q4_xrow(k, p.p0 + i) * k.a.ldx : 0);
+        const float* src = reinterpret_cast<const float*>(k.a.x) + (on ? q4_xrow(k, smem, p.p0 + i) * k.a.ldx : 0);
         float m = 0.f;
         if (on) {
 #pragma unroll 2
@@ -279,31 +284,41 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
     int u0, u1;
     if (PLAN) {
         pdl_wait();                                        // the plan is an earlier kernel's
+        int* offs = prefix + a.E + 1;
+        for (int e = tid; e <= a.E; e += Q4_WARPS * 32) offs[e] = q4_offset(a, e);
+        if (k.off_slots && tid < a.nslots) reinterpret_cast<int*>(smem + k.off_slots)[tid] = q4_slot(a, tid);
+        __syncthreads();
         if (warp == 0) {
-            int* offs = prefix + a.E + 1;
             int run = 0;
             for (int e0 = 0; e0 <= a.E; e0 += 32) {
                 const int e = e0 + lane;
-                const int o = e <= a.E ? q4_offset(a, e) : 0;
-                const int n = e < a.E ? max(q4_offset(a, e + 1) - o + k.tok - 1, 0) / k.tok : 0;
+                const int n = e < a.E ? max(offs[e + 1] - offs[e] + k.tok - 1, 0) / k.tok : 0;
                 int s = n;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
                     const int up = __shfl_up_sync(0xffffffffu, s, d);
                     if (lane >= d) s += up;
                 }
-                if (e <= a.E) {
-                    prefix[e] = run + s - n;
-                    offs[e] = o;
-                }
+                if (e <= a.E) prefix[e] = run + s - n;
                 run += __shfl_sync(0xffffffffu, s, 31);
             }
         }
         __syncthreads();
-        const unsigned all = (unsigned)prefix[a.E] * (unsigned)(k.tiles / two);
-        const unsigned each = all / gridDim.x, more = all - each * gridDim.x, b = blockIdx.x;
-        u0 = (int)(b * each + min(b, more)) * two;
-        u1 = u0 + (int)(each + (b < more ? 1u : 0u)) * two;
+        const unsigned jobs = (unsigned)prefix[a.E], units = (unsigned)(k.tiles / two), grid = gridDim.x;
+        const unsigned b = blockIdx.x;
+        if (jobs > 0 && 4 * jobs <= grid) {
+            // few passes: each has CTAs to itself (one that spans two passes stages x twice, 5 us on the path)
+            const unsigned per = grid / jobs, wide = grid - per * jobs;   // `wide` passes get one more
+            const unsigned cut = wide * (per + 1);
+            const unsigned n = b < cut ? per + 1 : per, c = b < cut ? b : b - cut;
+            const unsigned j = (b < cut ? 0 : wide) + c / n, i = c - c / n * n;
+            u0 = (int)(j * units + units * i / n) * two;
+            u1 = (int)(j * units + units * (i + 1) / n) * two;
+        } else {
+            const unsigned all = jobs * units, each = all / grid, more = all - each * grid;
+            u0 = (int)(b * each + min(b, more)) * two;
+            u1 = u0 + (int)(each + (b < more ? 1u : 0u)) * two;
+        }
     } else {
         const int b = blockIdx.x;
         u0 = b * k.each + min(b, k.more);
@@ -559,11 +574,14 @@ inline Q4Device q4_device() {
 inline int q4_smem(const Q4Stream& a, int parts, int pitch, int tok, Q4Kernel* k) {
     auto up = [](int v) { return (v + 127) / 128 * 128; };
     const int prefix = up(16 + 16 * Q4_WARPS);
-    const int scale = up(prefix + (a.offsets ? 2 * (a.E + 1) * 4 : 0));
+    const int slots = up(prefix + (a.offsets ? 2 * (a.E + 1) * 4 : 0));
+    const bool held = a.offsets && a.nslots <= Q4_PLAN_SLOTS;
+    const int scale = up(slots + (held ? a.nslots * 4 : 0));
     const int red = scale + 3 * 32 * 4;
     const int x = up(red + 2 * Q4_WARPS * (a.pair ? 2 : 1) * tok * parts * Q4_RED_PITCH * 4);
     if (k) {
         k->off_prefix = prefix;
+        k->off_slots = held ? slots : 0;
         k->off_scale = scale;
         k->off_red = red;
         k->off_x = x;
