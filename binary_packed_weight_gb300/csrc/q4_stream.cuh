@@ -20,6 +20,10 @@
 // each other.  The activations sit in shared memory for the CTA's whole life
 // (one matrix) or per pass of the plan.
 //
+// Long rows of x do not fit shared memory whole: a cluster of CTAs then takes
+// the tiles together, each CTA a range of k, and the CTAs' sums of a tile meet
+// through distributed shared memory, in the order of their ranks.
+//
 // A decode call lasts a few microseconds, so what a warp does once counts as
 // much as the blocks (two to six a warp): there is one copy of the block's code,
 // the work is cut with shifts and host-side reciprocals, and more rows than
@@ -50,10 +54,10 @@ struct Q4Kernel {
     int parts;                         // f16 columns of a row
     int tiles;                         // 16-row tiles of a pass (both matrices' of a pair)
     int each, more;                    // no plan: tiles of a CTA, and CTAs that take one more
-    uint32_t rcp;                      // ceil(2^32 / nkc) (nkc > 1): i / nkc for i * nkc < 2^32
+    int split, teams;                  // no plan: CTAs of a cluster, each with a range of k; clusters
     int pitch;                         // bytes of an activation column in shared memory
     int xvec;                          // rows of x are 16-byte aligned
-    int off_prefix, off_slots, off_scale, off_red, off_x;   // shared-memory layout (off_slots 0: none)
+    int off_prefix, off_slots, off_scale, off_red, off_sum, off_x;   // shared-memory layout (off_slots 0: none)
 };
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -121,21 +125,21 @@ __device__ __forceinline__ int64_t q4_xrow(const Q4Kernel& k, const uint8_t* sme
 // Activation rows of a pass into shared memory: column (row i, part q) at
 // (i*parts + q)*pitch, f16 or bf16 in k order.  Rows are copied by the copy
 // engine where they are 16-byte aligned; f32 rows are scaled to a largest
-// magnitude of 2^14..2^15 and split.  Every thread of the CTA calls it.
-__device__ __forceinline__ bool q4_stage_x(const Q4Kernel& k, uint8_t* smem, const Q4Pass& p, uint64_t* xbar,
-                                           uint32_t& xphase) {
+// magnitude of 2^14..2^15 and split.  Only k = k0 .. k0 + K of the rows is taken.
+// Every thread of the CTA calls it.
+__device__ __forceinline__ bool q4_stage_x(const Q4Kernel& k, uint8_t* smem, const Q4Pass& p, int k0, int K,
+                                           uint64_t* xbar, uint32_t& xphase) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint8_t* xs = smem + k.off_x;
     float* inv = reinterpret_cast<float*>(smem + k.off_scale);
     int* top = reinterpret_cast<int*>(inv + 32);
     int* orow = top + 32;
-    const int K = (int)k.a.K;
     __syncthreads();                                       // the previous rows and their scales are done with
     if (warp == Q4_WARPS - 1 && lane < p.cnt) orow[lane] = k.a.oslot ? q4_slot_of(k, smem, p.p0 + lane) : p.p0 + lane;
     if (k.a.xmode == Q4_X_RAW16) {
         if (!k.xvec) {
             for (int i = warp; i < p.cnt; i += Q4_WARPS) {
-                const uint16_t* src = reinterpret_cast<const uint16_t*>(k.a.x) + q4_xrow(k, smem, p.p0 + i) * k.a.ldx;
+                const uint16_t* src = reinterpret_cast<const uint16_t*>(k.a.x) + q4_xrow(k, smem, p.p0 + i) * k.a.ldx + k0;
                 for (int c = lane; c < K; c += 32) reinterpret_cast<uint16_t*>(xs + i * k.pitch)[c] = src[c];
             }
             __syncthreads();
@@ -146,7 +150,7 @@ __device__ __forceinline__ bool q4_stage_x(const Q4Kernel& k, uint8_t* smem, con
             __syncwarp();
             if (lane < p.cnt)
                 bulk_load(xs + lane * k.pitch,
-                          reinterpret_cast<const uint16_t*>(k.a.x) + q4_xrow(k, smem, p.p0 + lane) * k.a.ldx,
+                          reinterpret_cast<const uint16_t*>(k.a.x) + q4_xrow(k, smem, p.p0 + lane) * k.a.ldx + k0,
                           (uint32_t)K * 2, xbar);
         }
         const bool ok = mbar_wait(xbar, xphase);
@@ -167,7 +171,7 @@ __device__ __forceinline__ bool q4_stage_x(const Q4Kernel& k, uint8_t* smem, con
     for (int i0 = 0; i0 < p.cnt; i0 += Q4_WARPS / nw) {
         const int i = i0 + warp / nw;
         const bool on = i < p.cnt;
-        const float* src = reinterpret_cast<const float*>(k.a.x) + (on ? q4_xrow(k, smem, p.p0 + i) * k.a.ldx : 0);
+        const float* src = reinterpret_cast<const float*>(k.a.x) + (on ? q4_xrow(k, smem, p.p0 + i) * k.a.ldx + k0 : 0);
         float m = 0.f;
         if (on) {
 #pragma unroll 2
@@ -264,15 +268,20 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
     const float* inv = reinterpret_cast<const float*>(smem + k.off_scale);
     const int* orow = reinterpret_cast<const int*>(inv + 64);
     float* red = reinterpret_cast<float*>(smem + k.off_red);
-    const int nkc = a.nkc;
+    float* csum = reinterpret_cast<float*>(smem + k.off_sum);  // cluster: [tile][row of x][16 rows]
+    // this CTA's range of k, in chunks
+    const int split = PLAN ? 1 : k.split, rank = split > 1 ? (int)(blockIdx.x % split) : 0;
+    const int c0 = split > 1 ? a.nkc * rank / split : 0;
+    const int nkc = split > 1 ? a.nkc * (rank + 1) / split - c0 : a.nkc;
+    const int kl = min((int)a.K - c0 * Q4_K, nkc * Q4_K);
 
     if (tid == 0) {
         mbar_init(xbar, 1);
         fence_mbar_init();
     }
-    if (a.K != nkc * Q4_K) {                               // k past the row's end is zero for the kernel's whole life
+    if (kl != nkc * Q4_K) {                                // k past the row's end is zero for the kernel's whole life
         for (int c = 0; c < k.tok * k.parts; ++c)
-            for (int i = (int)a.K + 2 * tid; i < nkc * Q4_K; i += 2 * Q4_WARPS * 32)
+            for (int i = kl + 2 * tid; i < nkc * Q4_K; i += 2 * Q4_WARPS * 32)
                 *reinterpret_cast<uint32_t*>(smem + k.off_x + c * k.pitch + i * 2) = 0u;
         fence_proxy_async_shared();
     }
@@ -320,7 +329,7 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
             u1 = u0 + (int)(each + (b < more ? 1u : 0u)) * two;
         }
     } else {
-        const int b = blockIdx.x;
+        const int b = split > 1 ? blockIdx.x / split : blockIdx.x;
         u0 = b * k.each + min(b, k.more);
         u1 = u0 + k.each + (b < k.more ? 1 : 0);
     }
@@ -345,10 +354,10 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
         return b;
     };
     const int64_t second = PLAN && a.pair ? a.w1 - a.w0 : 0;
-    auto tile_of = [&](int i) { return nkc > 1 ? (int)__umulhi((uint32_t)i, k.rcp) : i; };
+    auto tile_of = [&](int i) { return i / nkc; };
     auto block_ptr = [&](const Batch& b, int tl, int kc) {
         const int tile = b.first + tl, rt = two == 2 ? tile >> 1 : tile;
-        const uint32_t index = (uint32_t)(((rt >> 3) * nkc + kc) * 8 + (rt & 7));
+        const uint32_t index = (uint32_t)(((rt >> 3) * a.nkc + c0 + kc) * 8 + (rt & 7));
         const uint8_t* p = b.w + (int64_t)index * blk;
         return two == 2 && (tile & 1) ? p + second : p;
     };
@@ -368,7 +377,12 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
     uint32_t xa[NT];
     int cols = 0;
 
-    auto store = [&](float v, int m, int row) {
+    auto store = [&](float v, int m, int row, int tl) {
+        if (split > 1) {
+            csum[(tl * pass.cnt + m) * 16 + (row & 15)] = v;
+            return;
+        }
+        if (row >= a.N) return;
         const int64_t o = (int64_t)orow[m] * a.ldo + row;
         if (PLAN || a.otype == TQ2_F32) reinterpret_cast<float*>(a.out)[o] = v;
         else if (a.otype == TQ2_F16) reinterpret_cast<__half*>(a.out)[o] = __float2half_rn(v);
@@ -379,7 +393,7 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
         if (b.j != staged) {
             staged = b.j;
             if (PLAN) pass = q4_pass(k, prefix, b.j);
-            q4_stage_x(k, smem, pass, xbar, xphase);       // a wait that ran out is on record; the rest is harmless
+            q4_stage_x(k, smem, pass, c0 * Q4_K, kl, xbar, xphase);   // a wait that ran out is on record; the rest is harmless
             cols = pass.cnt * k.parts;
             // columns past the last one repeat it and are not stored
 #pragma unroll
@@ -481,7 +495,7 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
                                         f *= s;
                                         v = f / (1.0f + expf(-f)) * v;
                                     }
-                                    if (row + 8 * r < a.N) store(v, m, row + 8 * r);
+                                    store(v, m, row + 8 * r, tl);
                                 }
                             }
                     }
@@ -544,7 +558,23 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
                 const float up = sum(1);
                 v = v / (1.0f + expf(-v)) * up;
             }
-            if (row < a.N) store(v, m, row);
+            store(v, m, row, su.x);
+        }
+        if (split > 1) {
+            // the CTAs' sums, in the order of their ranks; each CTA finishes its share
+            cluster_sync();
+            for (int i = rank * Q4_WARPS * 32 + tid; i < b.n * pass.cnt * 16; i += split * Q4_WARPS * 32) {
+                float v = 0.f;
+                for (int c = 0; c < split; ++c)
+                    v += __uint_as_float(ld_dsmem_u32(mapa_shared(smem_u32(csum + i), (uint32_t)c)));
+                const int q = i >> 4, tl = q / pass.cnt, m = q - tl * pass.cnt, row = (b.first + tl) * 16 + (i & 15);
+                if (row >= a.N) continue;
+                const int64_t o = (int64_t)m * a.ldo + row;
+                if (a.otype == TQ2_F32) reinterpret_cast<float*>(a.out)[o] = v;
+                else if (a.otype == TQ2_F16) reinterpret_cast<__half*>(a.out)[o] = __float2half_rn(v);
+                else reinterpret_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
+            }
+            cluster_sync();                                // a CTA stays while others read its sums
         }
         if (!again) break;
         u = un;
@@ -570,36 +600,45 @@ inline Q4Device q4_device() {
     return d;
 }
 
-// Shared memory of a launch that takes `tok` rows a pass.
-inline int q4_smem(const Q4Stream& a, int parts, int pitch, int tok, Q4Kernel* k) {
+// Shared memory of a launch that takes `tok` rows a pass over clusters of `split`.
+inline int q4_smem(const Q4Stream& a, int parts, int tok, int split, const Q4Device& dev, Q4Kernel* k) {
     auto up = [](int v) { return (v + 127) / 128 * 128; };
+    const int pitch = (a.nkc + split - 1) / split * Q4_K * 2 + 64;
+    const int tiles = (int)((a.N + 15) / 16) * (a.pair ? 2 : 1);
+    const int teams = a.offsets ? dev.sms : tiles < dev.sms / split ? tiles : dev.sms / split;
     const int prefix = up(16 + 16 * Q4_WARPS);
     const int slots = up(prefix + (a.offsets ? 2 * (a.E + 1) * 4 : 0));
     const bool held = a.offsets && a.nslots <= Q4_PLAN_SLOTS;
     const int scale = up(slots + (held ? a.nslots * 4 : 0));
     const int red = scale + 3 * 32 * 4;
-    const int x = up(red + 2 * Q4_WARPS * (a.pair ? 2 : 1) * tok * parts * Q4_RED_PITCH * 4);
+    const int sum = up(red + 2 * Q4_WARPS * (a.pair ? 2 : 1) * tok * parts * Q4_RED_PITCH * 4);
+    const int64_t x = sum + (split > 1 ? (int64_t)(tiles / teams + 1) * tok * 64 : 0);
+    const int64_t end = (x + 127) / 128 * 128 + (int64_t)tok * parts * pitch;
     if (k) {
+        k->tiles = tiles;
+        k->split = split;
+        k->teams = teams;
+        k->each = tiles / teams;
+        k->more = tiles - k->each * teams;
+        k->pitch = pitch;
         k->off_prefix = prefix;
         k->off_slots = held ? slots : 0;
         k->off_scale = scale;
         k->off_red = red;
-        k->off_x = x;
+        k->off_sum = sum;
+        k->off_x = up((int)x);
+        return (int)end;
     }
-    return x + tok * parts * pitch;
+    return end > dev.smem ? dev.smem + 1 : (int)end;
 }
 
 template <int G, int NT, bool BF, bool PLAN>
-cudaError_t q4_stream_launch(Q4Kernel& k, int tok, const Q4Device& dev, cudaStream_t st) {
+cudaError_t q4_stream_launch(Q4Kernel& k, int tok, int split, const Q4Device& dev, cudaStream_t st) {
     const Q4Stream& a = k.a;
     k.tok = tok;
-    k.tiles = (int)((a.N + 15) / 16) * (a.pair ? 2 : 1);
-    k.rcp = a.nkc > 1 ? (uint32_t)((((uint64_t)1 << 32) + a.nkc - 1) / a.nkc) : 0;
-    const int grid = PLAN || k.tiles > dev.sms ? dev.sms : k.tiles;
-    k.each = k.tiles / grid;
-    k.more = k.tiles - k.each * grid;
-    const int smem = q4_smem(a, k.parts, k.pitch, tok, &k);
+    const int smem = q4_smem(a, k.parts, tok, split, dev, &k);
     if (smem > dev.smem) return cudaErrorInvalidValue;
+    const int grid = PLAN ? dev.sms : k.teams * split;
     static std::atomic<uint64_t> raised{0};                // devices whose limit of this kernel is raised
     int d = 0;
     cudaGetDevice(&d);
@@ -621,42 +660,64 @@ cudaError_t q4_stream_launch(Q4Kernel& k, int tok, const Q4Device& dev, cudaStre
         p.a.M = M - m < tok ? M - m : tok;
         p.a.x = static_cast<const char*>(a.x) + m * xs;
         p.a.out = static_cast<char*>(a.out) + m * os;
-        e = launch_pdl(q4_stream_kernel<G, NT, BF, PLAN>, dim3((unsigned)grid), dim3(Q4_WARPS * 32), (size_t)smem, st,
-                       p);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)grid);
+        cfg.blockDim = dim3(Q4_WARPS * 32);
+        cfg.dynamicSmemBytes = (size_t)smem;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)split;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = split > 1 ? 2 : 1;
+        e = cudaLaunchKernelEx(&cfg, q4_stream_kernel<G, NT, BF, PLAN>, p);
     }
     return e;
 }
 
 template <int G, int NT>
-cudaError_t q4_stream_pick(Q4Kernel& k, int tok, const Q4Device& dev, cudaStream_t st) {
+cudaError_t q4_stream_pick(Q4Kernel& k, int tok, int split, const Q4Device& dev, cudaStream_t st) {
     if (k.a.offsets)
-        return k.a.bf16 ? q4_stream_launch<G, NT, true, true>(k, tok, dev, st)
-                        : q4_stream_launch<G, NT, false, true>(k, tok, dev, st);
-    return k.a.bf16 ? q4_stream_launch<G, NT, true, false>(k, tok, dev, st)
-                    : q4_stream_launch<G, NT, false, false>(k, tok, dev, st);
+        return k.a.bf16 ? q4_stream_launch<G, NT, true, true>(k, tok, 1, dev, st)
+                        : q4_stream_launch<G, NT, false, true>(k, tok, 1, dev, st);
+    return k.a.bf16 ? q4_stream_launch<G, NT, true, false>(k, tok, split, dev, st)
+                    : q4_stream_launch<G, NT, false, false>(k, tok, split, dev, st);
 }
 
-// The variant by sizes: column tiles (NT) for the rows a pass takes, as far as
-// shared memory holds their columns; f32 rows take two columns each.
+// The variant by sizes: the rows a pass takes, as far as shared memory holds
+// their columns (f32 rows take two each), and the column tiles (NT) they need.
+// Without a plan k is split over clusters until they fit whole (13 rows of
+// 10624 f32 and 106 columns: @@A@@ us in passes, @@B@@ in a cluster of 4), and while that gives idle SMs
+// a CTA of at least 32 chunks a tile.
 template <int G>
 cudaError_t q4_stream_run(const Q4Stream& a, cudaStream_t st) {
     Q4Kernel k{};
     k.a = a;
     k.parts = a.xmode == Q4_X_SPLIT ? 2 : 1;
-    k.pitch = a.nkc * Q4_K * 2 + 64;
     const int el = a.xmode == Q4_X_RAW16 ? 2 : 4;
     k.xvec = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && (a.ldx * el) % 16 == 0;
     const Q4Device dev = q4_device();
-    auto tokens = [&](int nt) {                            // rows a pass of nt column tiles can take
-        int tok = a.tokens * k.parts < 8 * nt ? a.tokens : 8 * nt / k.parts;
-        while (tok > 0 && q4_smem(a, k.parts, k.pitch, tok, nullptr) > dev.smem) --tok;
+    const int most = a.tokens * k.parts < 32 ? a.tokens : 32 / k.parts;
+    auto rows = [&](int split) {
+        int tok = most;
+        while (tok > 0 && q4_smem(a, k.parts, tok, split, dev, nullptr) > dev.smem) --tok;
         return tok;
     };
-    const int t4 = tokens(4), t2 = tokens(2), t1 = tokens(1);
-    if (t4 > t2 && t4 * k.parts > 16) return q4_stream_pick<G, 4>(k, t4, dev, st);
-    if (t2 > t1 && t2 * k.parts > 8) return q4_stream_pick<G, 2>(k, t2, dev, st);
-    if (t1 < 1) return cudaErrorInvalidValue;
-    return q4_stream_pick<G, 1>(k, t1, dev, st);
+    int split = 1, tok = rows(1);
+    if (!a.offsets) {
+        const int tiles = (int)((a.N + 15) / 16);
+        while (split < 8 && tok < most && a.nkc >= 2 * split) tok = rows(split *= 2);
+        while (split < 8 && tiles * 2 * split <= dev.sms && a.nkc >= 64 * split && rows(2 * split) >= tok)
+            tok = rows(split *= 2);
+    }
+    if (tok < 1) return cudaErrorInvalidValue;
+    if (tok * k.parts > 16) return q4_stream_pick<G, 4>(k, tok, split, dev, st);
+    if (tok * k.parts > 8) return q4_stream_pick<G, 2>(k, tok, split, dev, st);
+    return q4_stream_pick<G, 1>(k, tok, split, dev, st);
 }
 
 }  // namespace tq2

@@ -131,6 +131,21 @@ def test_gemm_wide(lib, dtype, M, N, K):
     check(got, x, W, K, 128, dtype, f"{M}x{N}x{K}")
 
 
+@pytest.mark.parametrize("dtype,M,N,K,group", [("float32", 13, 106, 10624, 128), ("bfloat16", 13, 82, 11136, 64),
+                                               ("float32", 16, 33, 4096, 32), ("float16", 16, 300, 32768, 128),
+                                               ("float32", 16, 3000, 6176, 32), ("bfloat16", 40, 40, 9600, 128),
+                                               ("float32", 9, 16, 32768, 64)])
+def test_gemm_rows_longer_than_shared_memory(lib, dtype, M, N, K, group):
+    """Several CTAs share a tile's k; their ranges and the last chunk are uneven."""
+    rng = np.random.default_rng(13)
+    c, d, z = planes(rng, 1, N, K, group, True)
+    W = oq4.dequant(c, d.view(np.uint16), z, group)[0]
+    w = upload(lib, c, d, z, group)
+    for ldx in (0, 3):
+        x, got = run(lib, w, rng.normal(size=(M, K)), dtype, ldx)
+        check(got, x, W, K, group, dtype, f"{M}x{N}x{K}")
+
+
 @pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
 def test_gemm_strided_and_unaligned_rows(lib, dtype):
     rng = np.random.default_rng(6)
