@@ -38,6 +38,7 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "../../include/tq2.h"
 #include "q4.cuh"
@@ -585,18 +586,45 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
 
 struct Q4Device {
     int sms, smem;
+    int clusters[4];                   // of 1, 2, 4, 8 CTAs that fit the GPU at once, one CTA an SM
 };
-inline Q4Device q4_device() {
-    // attributes of a device never change: asked once
+// Attributes of a device never change: asked once.  (Clusters do not cross the
+// hardware's groups of SMs, so fewer fit than the SMs would say.)
+template <int G>
+const Q4Device& q4_device() {
     static Q4Device known[64];
+    static std::mutex lock;
+    static std::atomic<uint64_t> ready{0};
     int dev = 0;
     cudaGetDevice(&dev);
-    Q4Device d = dev < 64 ? known[dev] : Q4Device{0, 0};
-    if (d.sms == 0) {
-        cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-        cudaDeviceGetAttribute(&d.smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-        if (dev < 64) known[dev] = d;
+    if (dev > 63) dev = 63;
+    Q4Device& d = known[dev];
+    if ((ready.load(std::memory_order_acquire) >> dev) & 1) return d;
+    std::lock_guard<std::mutex> hold(lock);
+    cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+    cudaDeviceGetAttribute(&d.smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    cudaFuncSetAttribute(q4_stream_kernel<G, 1, false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem);
+    d.clusters[0] = d.sms;
+    for (int i = 1; i < 4; ++i) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)d.sms / 8 * 8);
+        cfg.blockDim = dim3(Q4_WARPS * 32);
+        cfg.dynamicSmemBytes = (size_t)d.smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 1u << i;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, q4_stream_kernel<G, 1, false, false>, &cfg) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            n = 1;
+        }
+        d.clusters[i] = n;
     }
+    ready.fetch_or(uint64_t(1) << dev, std::memory_order_release);
     return d;
 }
 
@@ -605,7 +633,8 @@ inline int q4_smem(const Q4Stream& a, int parts, int tok, int split, const Q4Dev
     auto up = [](int v) { return (v + 127) / 128 * 128; };
     const int pitch = (a.nkc + split - 1) / split * Q4_K * 2 + 64;
     const int tiles = (int)((a.N + 15) / 16) * (a.pair ? 2 : 1);
-    const int teams = a.offsets ? dev.sms : tiles < dev.sms / split ? tiles : dev.sms / split;
+    const int fit = dev.clusters[split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3];
+    const int teams = tiles < fit ? tiles : fit;
     const int prefix = up(16 + 16 * Q4_WARPS);
     const int slots = up(prefix + (a.offsets ? 2 * (a.E + 1) * 4 : 0));
     const bool held = a.offsets && a.nslots <= Q4_PLAN_SLOTS;
@@ -700,7 +729,7 @@ cudaError_t q4_stream_run(const Q4Stream& a, cudaStream_t st) {
     k.parts = a.xmode == Q4_X_SPLIT ? 2 : 1;
     const int el = a.xmode == Q4_X_RAW16 ? 2 : 4;
     k.xvec = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && (a.ldx * el) % 16 == 0;
-    const Q4Device dev = q4_device();
+    const Q4Device& dev = q4_device<G>();
     const int most = a.tokens * k.parts < 32 ? a.tokens : 32 / k.parts;
     auto rows = [&](int split) {
         int tok = most;
@@ -711,7 +740,8 @@ cudaError_t q4_stream_run(const Q4Stream& a, cudaStream_t st) {
     if (!a.offsets) {
         const int tiles = (int)((a.N + 15) / 16);
         while (split < 8 && tok < most && a.nkc >= 2 * split) tok = rows(split *= 2);
-        while (split < 8 && tiles * 2 * split <= dev.sms && a.nkc >= 64 * split && rows(2 * split) >= tok)
+        for (int i = split == 1 ? 1 : split == 2 ? 2 : 3; i < 4 && split < 8 && tiles <= dev.clusters[i] &&
+                                                       a.nkc >= 64 * split && rows(2 * split) >= tok; ++i)
             tok = rows(split *= 2);
     }
     if (tok < 1) return cudaErrorInvalidValue;
