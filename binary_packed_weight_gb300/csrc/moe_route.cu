@@ -20,6 +20,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "../../include/tq2.h"
 #include "ptx.cuh"
 #include "tq2_internal.h"
@@ -595,7 +597,7 @@ cudaError_t raise_smem(F* kernel, size_t smem) {
 }
 
 int sm_count() {
-    static int known[64];                                  // never changes: asked once
+    static std::atomic<int> known[64];                     // never changes: asked once
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 64 && known[dev]) return known[dev];
@@ -719,7 +721,7 @@ tq2_status check(const char* fn, int64_t ld, int dtype, int64_t T, int E, int k,
     if (score != MOE_SOFTMAX && score != MOE_SIGMOID)
         return (tq2_status)set_error(TQ2_EINVAL, "%s: unknown score %d", fn, score);
     if (!(scale - scale == 0.f)) return (tq2_status)set_error(TQ2_EINVAL, "%s: scale must be finite", fn);
-    if (E < 1 || E > 1024 || k < 1 || k > 32 || k > E || T < 0 || T * k > (1 << 24) || T > (1 << 24))
+    if (E < 1 || E > 1024 || k < 1 || k > 32 || k > E || T < 0 || T > (1 << 24) || T * k > (1 << 24))
         return (tq2_status)set_error(TQ2_ESHAPE,
                                      "%s: need 1 <= E <= 1024, 1 <= k <= min(E, 32), T*k <= 2^24 (T=%lld E=%d k=%d)",
                                      fn, (long long)T, E, k);
@@ -750,6 +752,9 @@ tq2_status moe_route(const void* logits, int64_t ld, int dtype, const float* bia
         return TQ2_OK;
     }
     if (!logits || !ids || !weights) return (tq2_status)set_error(TQ2_EINVAL, "moe_route: null pointer");
+    if (off_element(logits, element_size(dtype)) || off_element(bias, 4) || off_element(ids, 4) ||
+        off_element(weights, 4) || off_element(offsets, 4) || off_element(slots, 4))
+        return (tq2_status)set_error(TQ2_EINVAL, "moe_route: pointers must be element-aligned");
     RouteArgs a{};
     a.logits = logits;
     a.ld = ld;
@@ -777,6 +782,9 @@ tq2_status moe_route_backward(const void* logits, int64_t ld, int dtype, const f
     if (T == 0) return TQ2_OK;
     if (!logits || !ids || !dweights || !dlogits)
         return (tq2_status)set_error(TQ2_EINVAL, "moe_route_backward: null pointer");
+    if (off_element(logits, element_size(dtype)) || off_element(dlogits, element_size(dtype)) || off_element(bias, 4) ||
+        off_element(ids, 4) || off_element(dweights, 4))
+        return (tq2_status)set_error(TQ2_EINVAL, "moe_route_backward: pointers must be element-aligned");
     RouteBackArgs a{};
     a.logits = logits;
     a.ld = ld;

@@ -146,10 +146,13 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
     if (warp == 1) {
         pdl_wait();                                        // the plan is an earlier kernel's
         int run = 0;
+        bool down = false;                                 // ranges that go back are no plan: nothing is done
         for (int e0 = 0; e0 <= a.E; e0 += 32) {
             const int e = e0 + lane;
             const int o = e <= a.E ? plan_offset(a.offsets, a.nslots, e) : 0;
-            const int n = e < a.E ? max(plan_offset(a.offsets, a.nslots, e + 1) - o + MU_BN - 1, 0) / MU_BN : 0;
+            const int rows = e < a.E ? plan_offset(a.offsets, a.nslots, e + 1) - o : 0;
+            const int n = (rows + MU_BN - 1) / MU_BN;
+            down |= rows < 0;
             int s = n;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -159,6 +162,8 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
             if (e <= a.E) prefix[e] = run + s - n;
             run += __shfl_sync(0xffffffffu, s, 31);
         }
+        __syncwarp();
+        if (__any_sync(0xffffffffu, down) && lane == 0) prefix[a.E] = 0;
     }
     tc_fence_before();
     __syncthreads();
@@ -307,7 +312,7 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
         }
         __syncwarp();
     } else if (warp >= 4 && warp < MU_EPI) {               // ---- decoders
-        // quarter q of the rows, every third stage of the CTA's sequence; rows 0..15 of a
+        // quarter q of the rows, the group's stages of the CTA's sequence; rows 0..15 of a
         // quarter are one 16-row tile's, 16..31 the next one's (pair: Gate's and Up's)
         const int q = warp & 3;
         const int row = lane & 15, g = row & 7, hi = row >> 3;
@@ -381,7 +386,7 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
                 if (lane == 0) mbar_arrive(&bars->raw_empty[r.s]);
             }
         }
-    } else if (warp >= MU_EPI) {                           // ---- epilogue: 32 columns in turn
+    } else if (warp >= MU_EPI) {                           // ---- epilogue: CW columns in turn
         const int q = warp & 3, b = (warp - MU_EPI) >> 2;
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
         pdl_wait();

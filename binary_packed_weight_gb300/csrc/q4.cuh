@@ -121,7 +121,6 @@ struct q4_weight {
     int64_t mstride = 0;               // bytes of one matrix
     uint8_t* blocks = nullptr;
     float* bound = nullptr;            // [E] no row of W[e] has a larger 2-norm
-    int device = 0;
 };
 
 namespace tq2 {

@@ -196,7 +196,7 @@ tq2_status q4_upload(const uint8_t* codes, const uint16_t* scales, const uint8_t
                                      "q4_upload: need 1 <= E <= 1024, 1 <= N <= 2^24, group 32, 64 or 128, K a "
                                      "multiple of it up to 32768, N*K <= 2^36 (E=%lld N=%lld K=%lld group=%d)",
                                      (long long)E, (long long)N, (long long)K, group);
-    if ((reinterpret_cast<uintptr_t>(codes) & 1) != 0 || (reinterpret_cast<uintptr_t>(scales) & 1) != 0)
+    if (off_element(codes, 2) || off_element(scales, 2))
         return (tq2_status)set_error(TQ2_EINVAL, "q4_upload: codes and scales must be 2-byte aligned");
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     q4_weight* w = new (std::nothrow) q4_weight();
@@ -208,7 +208,6 @@ tq2_status q4_upload(const uint8_t* codes, const uint16_t* scales, const uint8_t
     w->zeros = zeros != nullptr;
     w->nkc = (K + Q4_K - 1) / Q4_K;
     w->mstride = (N + 127) / 128 * 8 * w->nkc * q4_block_bytes(group, w->zeros);
-    cudaGetDevice(&w->device);
     const size_t ngroups = (size_t)E * N * (K / group);
     void* tmp[3] = {nullptr, nullptr, nullptr};
     const void* dev[3] = {nullptr, nullptr, nullptr};
@@ -226,7 +225,8 @@ tq2_status q4_upload(const uint8_t* codes, const uint16_t* scales, const uint8_t
         e = launch_q4_bound(static_cast<const uint16_t*>(dev[1]), static_cast<const uint8_t*>(dev[2]), w, st);
     for (void* p : tmp)
         if (p) cudaFreeAsync(p, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    const cudaError_t done = cudaStreamSynchronize(st);        // the caller's planes are read, whatever happened
+    if (e == cudaSuccess) e = done;
     if (e != cudaSuccess) {
         cudaFree(w->blocks);
         delete w;
@@ -254,6 +254,7 @@ tq2_status q4_shape(q4_handle h, int64_t* E, int64_t* N, int64_t* K, int* group)
 
 tq2_status q4_dequant(q4_handle h, float* w, void* stream) {
     if (!h || !w) return (tq2_status)set_error(TQ2_EINVAL, "q4_dequant: null pointer");
+    if (off_element(w, 4)) return (tq2_status)set_error(TQ2_EINVAL, "q4_dequant: w must be 4-byte aligned");
     return cuda_status(launch_q4_dequant(h, w, reinterpret_cast<cudaStream_t>(stream)), "q4_dequant");
 }
 
@@ -264,8 +265,8 @@ tq2_status q4_quantize(const void* w, int dtype, int64_t rows, int64_t K, int gr
     if (rows < 1 || rows > ((int64_t)1 << 34) || !format_ok(K, group))
         return (tq2_status)set_error(TQ2_ESHAPE, "q4_quantize: bad shape (rows=%lld K=%lld group=%d)",
                                      (long long)rows, (long long)K, group);
-    if ((reinterpret_cast<uintptr_t>(codes) & 3) != 0)
-        return (tq2_status)set_error(TQ2_EINVAL, "q4_quantize: codes must be 4-byte aligned");
+    if (off_element(codes, 4) || off_element(scales, 2) || off_element(w, element_size(dtype)))
+        return (tq2_status)set_error(TQ2_EINVAL, "q4_quantize: codes must be 4-byte aligned, w and scales element-aligned");
     return cuda_status(launch_q4_quantize(w, dtype, rows, K, group, codes, scales, zeros,
                                           reinterpret_cast<cudaStream_t>(stream)),
                        "q4_quantize");
@@ -278,6 +279,8 @@ tq2_status q4_gemm(q4_handle h, const void* x, int64_t ldx, void* out, int64_t l
     if (M < 0 || M > (1 << 20)) return (tq2_status)set_error(TQ2_ESHAPE, "q4_gemm: bad M=%lld", (long long)M);
     if (M == 0) return TQ2_OK;
     if (!x || !out) return (tq2_status)set_error(TQ2_EINVAL, "q4_gemm: null pointer");
+    if (off_element(x, element_size(dtype)) || off_element(out, element_size(dtype)))
+        return (tq2_status)set_error(TQ2_EINVAL, "q4_gemm: x and out must be element-aligned");
     if (h->E != 1)
         return (tq2_status)set_error(TQ2_ESHAPE, "q4_gemm: the handle holds %lld matrices, not one", (long long)h->E);
     if (ldx < h->K || ldo < h->N)
@@ -301,7 +304,7 @@ tq2_status moe_experts(q4_handle gate, q4_handle up, q4_handle down, const void*
                        void* out, int64_t ldo, int64_t T, int k, void* stream) {
     if (!gate || !up || !down) return (tq2_status)set_error(TQ2_EINVAL, "moe_experts: null handle");
     if (!dtype_ok(dtype)) return (tq2_status)set_error(TQ2_EINVAL, "moe_experts: unknown dtype %d", dtype);
-    if (T < 0 || k < 1 || k > 32 || T * k > (1 << 24))
+    if (T < 0 || T > (1 << 24) || k < 1 || k > 32 || T * k > (1 << 24))
         return (tq2_status)set_error(TQ2_ESHAPE, "moe_experts: bad T=%lld, k=%d", (long long)T, k);
     const int64_t D = gate->K, F = gate->N, E = gate->E;
     if (up->K != D || up->N != F || up->E != E || down->K != F || down->N != D || down->E != E ||
@@ -314,9 +317,16 @@ tq2_status moe_experts(q4_handle gate, q4_handle up, q4_handle down, const void*
     if (ldx < D || ldo < D)
         return (tq2_status)set_error(TQ2_ESHAPE, "moe_experts: row strides %lld, %lld are shorter than D=%lld",
                                      (long long)ldx, (long long)ldo, (long long)D);
+    // a launch's row tiles are counted in 32 bits, of one row of x a pass at worst
+    if ((T * k + E) * (D > 2 * F ? D : 2 * F) >= ((int64_t)1 << 35))
+        return (tq2_status)set_error(TQ2_ESHAPE, "moe_experts: %lld slots of D=%lld, F=%lld are too many for one call",
+                                     (long long)(T * k), (long long)D, (long long)F);
     if (T == 0) return TQ2_OK;
     if (!x || !ids || !weights || !offsets || !slots || !out)
         return (tq2_status)set_error(TQ2_EINVAL, "moe_experts: null pointer");
+    if (off_element(x, element_size(dtype)) || off_element(out, element_size(dtype)) || off_element(ids, 4) ||
+        off_element(weights, 4) || off_element(offsets, 4) || off_element(slots, 4))
+        return (tq2_status)set_error(TQ2_EINVAL, "moe_experts: pointers must be element-aligned");
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int64_t S = T * k;
     auto combine = [&](const float* y) {

@@ -300,9 +300,12 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
         __syncthreads();
         if (warp == 0) {
             int run = 0;
+            bool down = false;                             // ranges that go back are no plan: nothing is done
             for (int e0 = 0; e0 <= a.E; e0 += 32) {
                 const int e = e0 + lane;
-                const int n = e < a.E ? max(offs[e + 1] - offs[e] + k.tok - 1, 0) / k.tok : 0;
+                const int rows = e < a.E ? offs[e + 1] - offs[e] : 0;
+                const int n = (rows + k.tok - 1) / k.tok;
+                down |= rows < 0;
                 int s = n;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
@@ -312,6 +315,8 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
                 if (e <= a.E) prefix[e] = run + s - n;
                 run += __shfl_sync(0xffffffffu, s, 31);
             }
+            __syncwarp();
+            if (__any_sync(0xffffffffu, down) && lane == 0) prefix[a.E] = 0;
         }
         __syncthreads();
         const unsigned jobs = (unsigned)prefix[a.E], units = (unsigned)(k.tiles / two), grid = gridDim.x;
@@ -719,9 +724,9 @@ cudaError_t q4_stream_pick(Q4Kernel& k, int tok, int split, const Q4Device& dev,
 
 // The variant by sizes: the rows a pass takes, as far as shared memory holds
 // their columns (f32 rows take two each), and the column tiles (NT) they need.
-// Without a plan k is split over clusters until they fit whole (13 rows of
-// 10624 f32 and 106 columns: @@A@@ us in passes, @@B@@ in a cluster of 4), and while that gives idle SMs
-// a CTA of at least 32 chunks a tile.
+// Without a plan k is split over the clusters that let a pass take most rows
+// (13 rows of 10624 f32 and 106 columns: 41.8 us in passes, 11.9 in a cluster of
+// 4), and further while that gives idle SMs a CTA of at least 32 chunks a tile.
 template <int G>
 cudaError_t q4_stream_run(const Q4Stream& a, cudaStream_t st) {
     Q4Kernel k{};
@@ -739,7 +744,13 @@ cudaError_t q4_stream_run(const Q4Stream& a, cudaStream_t st) {
     int split = 1, tok = rows(1);
     if (!a.offsets) {
         const int tiles = (int)((a.N + 15) / 16);
-        while (split < 8 && tok < most && a.nkc >= 2 * split) tok = rows(split *= 2);
+        for (int s = 2; s <= 8 && tok < most && a.nkc >= s; s *= 2) {
+            const int n = rows(s);                         // (many columns: a CTA's sums of them take space too)
+            if (n > tok) {
+                tok = n;
+                split = s;
+            }
+        }
         for (int i = split == 1 ? 1 : split == 2 ? 2 : 3; i < 4 && split < 8 && tiles <= dev.clusters[i] &&
                                                        a.nkc >= 64 * split && rows(2 * split) >= tok; ++i)
             tok = rows(split *= 2);

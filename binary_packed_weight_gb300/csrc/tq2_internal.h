@@ -7,6 +7,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "../../include/tq2.h"
+
 namespace tq2 {
 // Tensor maps of a plane for the tcgen05 core (umma_core.cuh).
 struct PlaneMaps {
@@ -103,6 +105,10 @@ unsigned int read_clear_dev_error_blr(cudaStream_t st);
 
 // q4_api.cu: scratch from the library's stream-ordered pool (freed with cudaFreeAsync).
 cudaError_t scratch_alloc(void** p, size_t bytes, cudaStream_t st);
+
+// Whether p is off an element of `size` bytes (a power of two).
+inline bool off_element(const void* p, size_t size) { return (reinterpret_cast<uintptr_t>(p) & (size - 1)) != 0; }
+inline size_t element_size(int dtype) { return dtype == TQ2_F32 ? 4 : 2; }
 
 // api.cu: record the calling thread's last error message; returns `st`.
 int set_error(int st, const char* fmt, ...);

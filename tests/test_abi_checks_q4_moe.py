@@ -50,6 +50,7 @@ def test_q4_quantize(lib):
     assert lib.q4_quantize(A, 0, 1, 128, 128, None, A, None, None) == TQ2_EINVAL
     assert lib.q4_quantize(A, 3, 1, 128, 128, A, A, None, None) == TQ2_EINVAL
     assert lib.q4_quantize(A, 0, 1, 128, 128, A + 2, A, None, None) == TQ2_EINVAL
+    assert lib.q4_quantize(A + 2, 0, 1, 128, 128, A, A, None, None) == TQ2_EINVAL
     for rows, K, g in ((0, 128, 128), (1, 100, 32), (1, 128, 48), (1, 0, 32), (1 << 35, 128, 128)):
         assert lib.q4_quantize(A, 0, rows, K, g, A, A, None, None) == TQ2_ESHAPE, (rows, K, g)
 
@@ -80,6 +81,8 @@ def test_moe_route(lib):
                 dict(groups=3), dict(groups=0), dict(groups=4, top=5), dict(groups=4, top=0),
                 dict(E=64, ld=64, groups=64), dict(T=(1 << 23) + 1), dict(E=64, ld=64, k=33)):
         assert _route(lib, **bad) == TQ2_ESHAPE, bad
+    for bad in (dict(logits=A + 2), dict(logits=A + 1, dtype=2), dict(off=A + 2), dict(slots=A + 1)):
+        assert _route(lib, **bad) == TQ2_EINVAL and "aligned" in _err(lib), bad
     assert _route(lib, T=0, off=None, slots=None) == TQ2_OK
 
 
@@ -92,6 +95,7 @@ def test_moe_route_backward(lib):
     assert back(score=5) == TQ2_EINVAL
     for bad in (dict(ld=7), dict(ldd=7), dict(k=9), dict(T=-1), dict(E=2000, ld=2000, ldd=2000)):
         assert back(**bad) == TQ2_ESHAPE, bad
+    assert back(logits=A + 2) == TQ2_EINVAL and back(dl=A + 1, dtype=1) == TQ2_EINVAL
     assert back(T=0) == TQ2_OK
 
 
@@ -100,5 +104,5 @@ def test_moe_experts(lib):
         return lib.moe_experts(gate, A, A, A, 64, dtype, A, A, A, A, A, 64, T, k, None)
     assert experts(gate=None) == TQ2_EINVAL
     assert experts(dtype=9) == TQ2_EINVAL
-    for bad in (dict(T=-1), dict(k=0), dict(k=33), dict(T=1 << 24)):      # refused before a handle is read
+    for bad in (dict(T=-1), dict(k=0), dict(k=33), dict(T=1 << 24), dict(T=1 << 62, k=4)):      # refused before a handle is read
         assert experts(**bad) == TQ2_ESHAPE, bad

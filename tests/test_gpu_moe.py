@@ -282,6 +282,40 @@ def test_experts_refusals(lib):
         lib.moe_route(torch.zeros((3, 8), device="cuda"), ids, w, groups=3)
 
 
+def test_experts_too_many_for_one_call(lib):
+    """Refused before anything is allocated or read (the tensors are views of one row)."""
+    import torch
+    rng = np.random.default_rng(15)
+    g, u, d = [upload(lib, *planes(rng, 1, N, K, 128, False), 128) for N, K in ((128, 4096), (128, 4096), (4096, 128))]
+    T, k = 1 << 19, 16
+    x = torch.zeros((1, 4096), dtype=torch.bfloat16, device="cuda").expand(T, 4096)
+    ids = torch.zeros((T, k), dtype=torch.int32, device="cuda")
+    off, slots = torch.zeros(2, dtype=torch.int32, device="cuda"), ids.reshape(-1)
+    rc = lib.load().moe_experts(g.handle, u.handle, d.handle, x.data_ptr(), 4096, 2, ids.data_ptr(), ids.data_ptr(),
+                                off.data_ptr(), slots.data_ptr(), x.data_ptr(), 4096, T, k, None)
+    assert rc == 2
+
+
+@pytest.mark.parametrize("T", [6, 120])
+@pytest.mark.parametrize("kind", ["back and forth", "out of range"])
+def test_experts_of_no_plan_stay_inside(lib, T, kind):
+    """offsets and slots that are no plan: the result is unspecified, but nothing beside out is written."""
+    import torch
+    rng = np.random.default_rng(16)
+    E, k, D, F = 8, 2, 128, 64
+    h = [upload(lib, *planes(rng, E, N, K, 32, False), 32) for N, K in ((F, D), (F, D), (D, F))]
+    S = T * k
+    off = [0, S] * 4 + [0] if kind == "back and forth" else [-9] * 4 + [3 * S] * 5
+    slots = rng.integers(0, S, S) if kind == "back and forth" else rng.choice([-5, S, 10 ** 9], S)
+    x = torch.randn((T, D), device="cuda").to(torch.bfloat16)
+    buf = torch.full((T + 2, D + 16), 7.0, dtype=torch.bfloat16, device="cuda")
+    ids = torch.from_numpy(rng.integers(0, E, (T, k)).astype(np.int32)).cuda()
+    lib.moe_experts(*h, x, ids, torch.ones((T, k), device="cuda"), torch.tensor(off, dtype=torch.int32, device="cuda"),
+                    torch.from_numpy(slots.astype(np.int32)).cuda(), buf[1:T + 1, 8:D + 8])
+    lib.device_status()
+    assert bool((buf[0] == 7).all() and (buf[-1] == 7).all() and (buf[:, :8] == 7).all() and (buf[:, -8:] == 7).all())
+
+
 def test_route_feeds_experts(lib):
     """The two together, as a layer: logits -> plan -> experts, twice with the same bits."""
     import torch

@@ -256,3 +256,26 @@ def test_gemm_in_a_graph(lib):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_gemm_beyond_32_bit_offsets(lib):
+    """17 GB of codes in rows too long for shared memory, more columns than a cluster's sums fit in."""
+    import torch
+    N, K, group = (1 << 20) - 5, 32768, 128
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB of free device memory")
+    gen = torch.Generator(device="cuda").manual_seed(13)
+    codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda", generator=gen)
+    d = torch.rand((N, K // group), device="cuda", generator=gen).mul_(0.1).half()
+    w = lib.q4_upload(codes, d, None, group=group)
+    rows = np.unique(np.concatenate([[0, 1, N - 1], np.random.default_rng(14).integers(0, N, 60)]))
+    pick = torch.from_numpy(rows).cuda()
+    W = oq4.dequant(codes[pick].cpu().numpy()[None], d[pick].cpu().numpy().view(np.uint16)[None], None, group)[0]
+    del codes, d
+    for dtype, M in (("float32", 2), ("bfloat16", 3)):
+        x = torch.randn((M, K), device="cuda", generator=gen).to(getattr(torch, dtype))
+        out = lib.q4_gemm(w, x, torch.empty((M, N), dtype=x.dtype, device="cuda"))
+        lib.device_status()
+        check(out[:, pick].cpu().double().numpy(), x.cpu().double().numpy(), W, K, group, dtype, "sampled rows")
+        assert bool(torch.isfinite(out).all())
+    w.free()
