@@ -7,8 +7,8 @@
 // holds the lowest expert, and the softmax sum's tree over neighbouring
 // experts is V-1 additions in the lane and five shuffles.  Selection values
 // are compared as order-preserving 32-bit keys: one redux.max and one ballot
-// for each of the k experts.  A lane keeps its two best at hand and looks
-// through its keys again only if it wins a third time.
+// for each of the k experts.  A lane keeps its three best at hand and looks
+// through its keys again only when it has won three times.
 //
 // The plan is a stable counting sort of the T*k slots.  Up to a few hundred
 // tokens one cluster of CTAs does all of it, each CTA reading the others'
@@ -45,9 +45,10 @@ struct RouteArgs {
     float* weights;
     int32_t* offsets;
     int32_t* slots;
-    int32_t* counts;                               // [chunks][E], two-kernel plan
+    uint16_t* counts;                              // [chunks][E rounded up to even], two-kernel plan
     int64_t chunk;                                 // tokens of a CTA
     int vec;                                       // rows can be read in wide loads
+    int gsize, gshift, gwhole;                     // groups: experts, log2 of the lanes; its lanes hold its experts
     int off_rows;                                  // groups: the warps' rows in shared memory (int index)
 };
 
@@ -90,9 +91,12 @@ __device__ __forceinline__ void load_row(const T* row, int E, int lane, bool vec
             for (int i = 0; i < Wide<T, V>::WORDS; ++i)
                 reinterpret_cast<typename Wide<T, V>::word*>(raw)[i] =
                     reinterpret_cast<const typename Wide<T, V>::word*>(row + e0)[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) raw[i] = from_f32<T>(-INFINITY);
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = e0 < E ? to_f32(raw[i]) : -INFINITY;
+        for (int i = 0; i < V; ++i) v[i] = to_f32(raw[i]);
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = e0 + i < E ? to_f32(row[e0 + i]) : -INFINITY;
@@ -149,11 +153,13 @@ __device__ __forceinline__ float warp_sum(float s) {
 }
 __device__ __forceinline__ float sigmoid(float l) { return __frcp_rn(1.0f + expf(-l)); }   // = 1 / (..), rounded
 
-// Larger value, larger key; 0 is below every number's key.
+// Larger value, larger key (v is not -0: scores are sums of +0 or more and a
+// bias).  ROUTE_NONE is the key of -inf, 0 that of nothing.
 __device__ __forceinline__ uint32_t order_key(float v) {
-    const uint32_t b = __float_as_uint(v + 0.0f);          // -0 and 0 compare equal
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
+    const int32_t b = __float_as_int(v);
+    return (uint32_t)b ^ ((uint32_t)(b >> 31) | 0x80000000u);
 }
+constexpr uint32_t ROUTE_NONE = 0x007FFFFFu;
 
 // Two largest of two sorted pairs (a1 >= a2, b1 >= b2).
 __device__ __forceinline__ void merge_two(float& a1, float& a2, float b1, float b2) {
@@ -179,11 +185,15 @@ __device__ __forceinline__ void place_slots(const int32_t* ids, int64_t s0, int 
         __syncthreads();
         for (int x = tid; x < E; x += nt) {                // exclusive prefix over the warps
             int run = 0;
-#pragma unroll 8
-            for (int w = 0; w < nw; ++w) {
-                const int c = cnt[w * E + x];
-                cnt[w * E + x] = (uint16_t)run;
-                run += c;
+            for (int w0 = 0; w0 < nw; w0 += 8) {           // eight loads in flight
+                int c[8];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) c[w] = w0 + w < nw ? cnt[(w0 + w) * E + x] : 0;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    if (w0 + w < nw) cnt[(w0 + w) * E + x] = (uint16_t)run;
+                    run += c[w];
+                }
             }
         }
         __syncthreads();
@@ -232,22 +242,27 @@ __device__ __forceinline__ void exclusive_prefix(int* v, int E, int* warps) {
     __syncthreads();
 }
 
-// The two best keys of a lane that come after (last, at) in the order of the
-// selection (larger key, then lower index).
-template <int V>
-__device__ __forceinline__ void two_best(const uint32_t (&key)[V], uint32_t last, int at, uint32_t& k1, int& i1,
-                                         uint32_t& k2, int& i2) {
-    k1 = k2 = 0u;
-    i1 = i2 = 0;
+// The three best keys of a lane and their indices, in the order of the
+// selection (larger key, then lower index); REST: of those after (last, at).
+struct Best {
+    uint32_t k1, k2, k3;
+    int i1, i2, i3;
+};
+template <int V, bool REST>
+__device__ __forceinline__ Best three_best(const uint32_t (&key)[V], uint32_t last, int at) {
+    Best b{0u, 0u, 0u, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const uint32_t k = key[i] < last || (key[i] == last && i > at) ? key[i] : 0u;
-        const bool first = k > k1, second = k > k2;
-        k2 = first ? k1 : second ? k : k2;
-        i2 = first ? i1 : second ? i : i2;
-        k1 = first ? k : k1;
-        i1 = first ? i : i1;
+        const uint32_t k = !REST || key[i] < last || (key[i] == last && i > at) ? key[i] : 0u;
+        const bool first = k > b.k1, second = k > b.k2, third = k > b.k3;
+        b.k3 = second ? b.k2 : third ? k : b.k3;
+        b.i3 = second ? b.i2 : third ? i : b.i3;
+        b.k2 = first ? b.k1 : second ? k : b.k2;
+        b.i2 = first ? b.i1 : second ? i : b.i2;
+        b.k1 = first ? k : b.k1;
+        b.i1 = first ? i : b.i1;
     }
+    return b;
 }
 
 // One token: ids and weights, and its experts counted in hist (if any).
@@ -263,13 +278,9 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t tok, int
     {
         float l[V], s[V];
         load_row<T, V>(row, a.E, lane, a.vec != 0, l);
-#pragma unroll
-        for (int i = 0; i < V; ++i) l[i] = l[i] > -INFINITY ? fminf(l[i], ROUTE_MOST) : -INFINITY;
-        if (a.bias) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) l[i] = b[i] > -INFINITY ? l[i] : -INFINITY;
-        }
         if (a.score == MOE_SOFTMAX) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) l[i] = available(l[i], b[i]);
             most = l[0];
 #pragma unroll
             for (int i = 1; i < V; ++i) most = fmaxf(most, l[i]);
@@ -280,88 +291,74 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t tok, int
 #pragma unroll
             for (int i = 0; i < V; ++i) s[i] = l[i] > -INFINITY ? s[i] / sum + b[i] : -INFINITY;
         } else {
+            // (a bias of -inf makes its sum -inf; +inf and the largest f32 have the same sigmoid)
 #pragma unroll
             for (int i = 0; i < V; ++i) s[i] = l[i] > -INFINITY ? sigmoid(l[i]) + b[i] : -INFINITY;
         }
-        uint32_t in = FULL;                                // groups that take part
-        const int gs = a.E / a.groups;
-        const bool grouped = a.top_groups < a.groups;
-        if (grouped) {
-            float value = -INFINITY;                       // of group `lane`
-            const int per = gs / V;                        // lanes of a group, where it is whole lanes
-            if (per * V == gs && (per & (per - 1)) == 0) {
-                float m1 = -INFINITY, m2 = -INFINITY;
+        if (a.top_groups < a.groups) {
+            float m1 = -INFINITY, m2 = -INFINITY;          // of group lane >> gshift
+            const int gs = a.gsize;
+            if (a.gwhole) {                                // whole lanes, a power of two
 #pragma unroll
                 for (int i = 0; i < V; ++i) merge_two(m1, m2, s[i], -INFINITY);
-                for (int o = 1; o < per; o <<= 1) {
-                    const float q1 = __shfl_xor_sync(FULL, m1, o), q2 = __shfl_xor_sync(FULL, m2, o);
-                    merge_two(m1, m2, q1, q2);
-                }
-                const float two = m1 + (m2 > -INFINITY ? m2 : 0.f);
-                value = __shfl_sync(FULL, two, (lane * per) & 31);
-                if (lane >= a.groups) value = -INFINITY;
-            } else {
-                // 32 / G lanes a group (G: a power of two) go through its values in shared memory
-                int lanes = 32;
-                while (lanes * a.groups > 32) lanes >>= 1;
+            } else {                                       // its lanes go through its values in shared memory
 #pragma unroll
                 for (int i = 0; i < V; ++i)
                     if (e0 + i < a.E) row_s[e0 + i] = s[i];
                 __syncwarp();
-                const int q = lane / lanes;
-                float m1 = -INFINITY, m2 = -INFINITY;
+                const int q = lane >> a.gshift, lanes = 1 << a.gshift;
                 if (q < a.groups)
                     for (int i = lane & (lanes - 1); i < gs; i += lanes) merge_two(m1, m2, row_s[q * gs + i], -INFINITY);
                 __syncwarp();
-                for (int o = 1; o < lanes; o <<= 1) {
-                    const float q1 = __shfl_xor_sync(FULL, m1, o), q2 = __shfl_xor_sync(FULL, m2, o);
-                    merge_two(m1, m2, q1, q2);
-                }
-                const float two = m1 + (m2 > -INFINITY ? m2 : 0.f);
-                value = __shfl_sync(FULL, two, (lane * lanes) & 31);
-                if (lane >= a.groups) value = -INFINITY;
             }
-            int before = 0;                                // groups ahead of this one
-            for (int q = 0; q < a.groups; ++q) {
-                const float o = __shfl_sync(FULL, value, q);
-                before += (o > value || (o == value && q < lane)) ? 1 : 0;
+            for (int o = 1; o < 1 << a.gshift; o <<= 1) {
+                const float q1 = __shfl_xor_sync(FULL, m1, o), q2 = __shfl_xor_sync(FULL, m2, o);
+                merge_two(m1, m2, q1, q2);
             }
-            in = __ballot_sync(FULL, lane < a.groups && before < a.top_groups);
-            int grp = e0 / gs, left = (grp + 1) * gs - e0;
+            const int mine = lane >> a.gshift;
+            uint32_t gkey = mine < a.groups ? order_key(m1 + (m2 > -INFINITY ? m2 : 0.f)) : 0u;
+            uint32_t in = 0u;                              // groups that take part
+            for (int j = 0; j < a.top_groups; ++j) {
+                const uint32_t m = __reduce_max_sync(FULL, gkey);
+                const int win = (__ffs(__ballot_sync(FULL, gkey == m)) - 1) >> a.gshift;
+                in |= 1u << win;
+                if (mine == win) gkey = 0u;
+            }
+            if (a.gwhole) {
+                const bool on = (in >> mine) & 1u;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                if (left == 0) {
-                    ++grp;
-                    left = gs;
+                for (int i = 0; i < V; ++i) s[i] = on ? s[i] : -INFINITY;
+            } else {
+                int grp = e0 / gs, left = (grp + 1) * gs - e0;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    if (left == 0) {
+                        ++grp;
+                        left = gs;
+                    }
+                    --left;
+                    if (!((in >> (grp & 31)) & 1u)) s[i] = -INFINITY;
                 }
-                --left;
-                if (!((in >> (grp & 31)) & 1u)) s[i] = -INFINITY;
             }
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = s[i] > -INFINITY ? order_key(s[i]) : 0u;
+        for (int i = 0; i < V; ++i) key[i] = order_key(s[i]);
     }
-    uint32_t k1, k2;
-    int i1, i2;
-    two_best<V>(key, FULL, V, k1, i1, k2, i2);             // (no key is all ones)
-    int id = -1;
-    bool spent = false;                                    // the second best moved up: k2 is not the next one
+    Best top = three_best<V, false>(key, 0u, 0);
+    int id = -1, at_hand = 3;
     for (int j = 0; j < a.k; ++j) {
-        const uint32_t m = __reduce_max_sync(FULL, k1);
-        if (m == 0u) break;                                // none left
-        const int win = __ffs(__ballot_sync(FULL, k1 == m)) - 1;
-        const int e = __shfl_sync(FULL, e0 + i1, win);
+        const uint32_t m = __reduce_max_sync(FULL, top.k1);
+        if (m <= ROUTE_NONE) break;                        // none left
+        const int win = __ffs(__ballot_sync(FULL, top.k1 == m)) - 1;
+        const int e = __shfl_sync(FULL, e0 + top.i1, win);
         if (lane == j) id = e;
-        const bool won = lane == win;
-        if (__any_sync(FULL, won && spent)) {
-            if (won) {
-                two_best<V>(key, k1, i1, k1, i1, k2, i2);
-                spent = false;
+        if (lane == win) {
+            if (V > 3 && --at_hand == 0) {
+                top = three_best<V, true>(key, m, top.i1);
+                at_hand = 3;
+            } else {
+                top = Best{top.k2, top.k3, 0u, top.i2, top.i3, 0};
             }
-        } else if (won) {
-            k1 = k2;
-            i1 = i2;
-            spent = true;
         }
     }
     // the weights: lane j scores its expert again
@@ -405,7 +402,10 @@ __global__ void __launch_bounds__(V <= 8 ? 1024 : 256) moe_route_kernel(const __
     if (!a.offsets) return;
     __syncthreads();
     if (!FUSED) {
-        for (int e = tid; e < a.E; e += nt) a.counts[(int64_t)blockIdx.x * a.E + e] = hist[e];
+        // two experts a word (hist[E] is 0)
+        const int words = (a.E + 1) / 2;
+        uint32_t* to = reinterpret_cast<uint32_t*>(a.counts) + (int64_t)blockIdx.x * words;
+        for (int e = tid; e < words; e += nt) to[e] = (uint32_t)hist[2 * e] | ((uint32_t)hist[2 * e + 1] << 16);
         return;
     }
     int* base = hist + a.E + 1;
@@ -440,50 +440,53 @@ __global__ void __launch_bounds__(V <= 8 ? 1024 : 256) moe_route_kernel(const __
 }
 
 // Second kernel of the plan: CTA b places the slots of chunk b.  Shared
-// memory: base int[E+1], before int[E], 33 ints, the warps' counts.
+// memory: base int[E+2], before int[E+2], 33 ints, the warps' counts.  Every CTA
+// sums all chunks' counts (16 bits each, two to a word: 16384 tokens of 256 experts
+// are 12 MB out of L2 for all CTAs together).
 __global__ void __launch_bounds__(1024) moe_plan_kernel(const int32_t* __restrict__ ids,
-                                                        const int32_t* __restrict__ counts, int chunks, int64_t chunk,
+                                                        const uint32_t* __restrict__ counts, int chunks, int64_t chunk,
                                                         int64_t T, int E, int k, int32_t* __restrict__ offsets,
                                                         int32_t* __restrict__ slots) {
     extern __shared__ int plan_smem[];
+    const int words = (E + 1) / 2;
     int* base = plan_smem;                                 // first the totals, then each expert's first position
-    int* before = base + E + 1;                            // slots of earlier chunks
-    int* warps = before + E;
-    uint16_t* cnt = reinterpret_cast<uint16_t*>(warps + 34 + (E + 1 + E) % 2);
+    int* before = base + 2 * words + 2;                    // slots of earlier chunks
+    int* warps = before + 2 * words + 2;
+    uint16_t* cnt = reinterpret_cast<uint16_t*>(warps + 34);
     const int tid = threadIdx.x, nt = blockDim.x, b = blockIdx.x;
     pdl_launch_dependents();
-    pdl_wait();
-    // column sums of the counts, many loads in flight: as many threads to a column as fit
-    for (int i = tid; i < E; i += nt) {
+    for (int i = tid; i < 2 * words; i += nt) {
         base[i] = 0;
         before[i] = 0;
     }
     __syncthreads();
-    const int cols = E < nt ? E : nt, rows = nt / cols;
-    if (tid < cols * rows) {
-        const int c0 = tid / cols;
-        for (int e = tid - c0 * cols; e < E; e += cols) {
-            const int32_t* p = counts + e;
-            int all = 0, mine = 0, c = c0;
-            for (; c + 15 * rows < chunks; c += 16 * rows) {
-                int v[16];
+    pdl_wait();
+    // column sums of the counts, many loads in flight: as many threads to a column as fit
+    const int rows = nt / words;
+    if (tid < words * rows) {
+        const int c0 = tid / words, e = tid - c0 * words;
+        const uint32_t* p = counts + e;
+        int all0 = 0, all1 = 0, mine0 = 0, mine1 = 0, c = c0;
+        auto add = [&](uint32_t v, int at) {
+            const int v0 = (int)(v & 0xFFFFu), v1 = (int)(v >> 16);
+            all0 += v0;
+            all1 += v1;
+            mine0 += at < b ? v0 : 0;
+            mine1 += at < b ? v1 : 0;
+        };
+        for (; c + 7 * rows < chunks; c += 8 * rows) {
+            uint32_t v[8];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = p[(int64_t)(c + i * rows) * E];
+            for (int i = 0; i < 8; ++i) v[i] = p[(int64_t)(c + i * rows) * words];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    all += v[i];
-                    mine += c + i * rows < b ? v[i] : 0;
-                }
-            }
-#pragma unroll 8
-            for (; c < chunks; c += rows) {
-                const int v = p[(int64_t)c * E];
-                all += v;
-                mine += c < b ? v : 0;
-            }
-            atomicAdd(base + e, all);                      // counts: the order does not matter
-            atomicAdd(before + e, mine);
+            for (int i = 0; i < 8; ++i) add(v[i], c + i * rows);
         }
+#pragma unroll 4
+        for (; c < chunks; c += rows) add(p[(int64_t)c * words], c);
+        atomicAdd(base + 2 * e, all0);                     // counts: the order does not matter
+        atomicAdd(base + 2 * e + 1, all1);
+        atomicAdd(before + 2 * e, mine0);
+        atomicAdd(before + 2 * e + 1, mine1);
     }
     __syncthreads();
     exclusive_prefix(base, E, warps);
@@ -612,7 +615,7 @@ cudaError_t launch_route(RouteArgs a, cudaStream_t st) {
     a.vec = wide_ok(a.logits, a.ld, a.E, V, (int)sizeof(T)) ? 1 : 0;
     constexpr int MOST = V <= 8 ? 32 : 8;                  // warps of a CTA
     const size_t head = (size_t)(3 * (a.E + 1) + 34) * 4;
-    const bool grouped = a.top_groups < a.groups;
+    const bool grouped = a.top_groups < a.groups && !a.gwhole;   // rows pass through shared memory
     // one cluster, a token a warp
     if (a.T <= ROUTE_CLUSTER * MOST) {
         int C = 1;
@@ -643,16 +646,16 @@ cudaError_t launch_route(RouteArgs a, cudaStream_t st) {
     }
     // a chunk a CTA, at most one CTA of 32 warps (four of 8) on each SM
     int64_t chunks = (a.T + MOST - 1) / MOST;
-    const int64_t limit = (int64_t)sm_count() * (MOST == 32 ? 1 : 4);
-    if (chunks > limit) chunks = limit;
+    const int64_t limit = (int64_t)sm_count() * (MOST == 32 ? 1 : 4), least = (a.T + 65534) / 65535;   // counts of 16 bits
+    if (chunks > limit) chunks = limit > least ? limit : least;
     a.chunk = (a.T + chunks - 1) / chunks;
     chunks = (a.T + a.chunk - 1) / a.chunk;
     void* mem = nullptr;
     cudaError_t e = cudaSuccess;
     if (a.offsets) {
-        e = scratch_alloc(&mem, (size_t)chunks * a.E * 4, st);
+        e = scratch_alloc(&mem, (size_t)chunks * ((a.E + 1) / 2) * 4, st);
         if (e != cudaSuccess) return e;
-        a.counts = static_cast<int32_t*>(mem);
+        a.counts = static_cast<uint16_t*>(mem);
     }
     a.off_rows = (int)(head / 4);
     const size_t smem = head + (grouped ? (size_t)MOST * a.E * 4 : 0);
@@ -660,11 +663,11 @@ cudaError_t launch_route(RouteArgs a, cudaStream_t st) {
     if (e == cudaSuccess)
         e = launch_pdl(moe_route_kernel<T, V, false>, dim3((unsigned)chunks), dim3(MOST * 32), smem, st, a);
     if (e == cudaSuccess && a.offsets) {
-        const size_t plan = (size_t)(2 * a.E + 36) * 4 + (size_t)32 * a.E * 2;
+        const size_t plan = (size_t)(2 * (a.E + 3) + 34) * 4 + (size_t)32 * a.E * 2;
         e = raise_smem(moe_plan_kernel, plan);
         if (e == cudaSuccess)
             e = launch_pdl(moe_plan_kernel, dim3((unsigned)chunks), dim3(1024), plan, st,
-                           static_cast<const int32_t*>(a.ids), static_cast<const int32_t*>(a.counts), (int)chunks,
+                           static_cast<const int32_t*>(a.ids), reinterpret_cast<const uint32_t*>(a.counts), (int)chunks,
                            a.chunk, a.T, a.E, a.k, a.offsets, a.slots);
     }
     if (mem) {
@@ -765,6 +768,11 @@ tq2_status moe_route(const void* logits, int64_t ld, int dtype, const float* bia
     a.score = score;
     a.groups = groups;
     a.top_groups = top_groups;
+    a.gsize = E / groups;
+    const int V = experts_a_lane(E), per = a.gsize / V;
+    a.gwhole = per * V == a.gsize && (per & (per - 1)) == 0;
+    // else the lanes of a warp are shared out among the groups
+    while (a.gwhole ? (2 << a.gshift) <= per : (2 << a.gshift) * groups <= 32) ++a.gshift;
     a.renorm = renorm;
     a.scale = scale;
     a.ids = ids;

@@ -129,6 +129,26 @@ def test_route_many_tokens(lib):
         assert torch.equal(ids[rows].long(), i[rows, :k])
 
 
+@pytest.mark.parametrize("E", [1, 3])
+def test_route_most_tokens(lib, E):
+    """2^24 slots; of one expert, every count of a plan's chunk is as large as it gets."""
+    import torch
+    T = 1 << 24
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    logits = torch.randn((T, E), device="cuda", generator=gen).half()
+    logits[T // 4:T // 2, 1:] = -float("inf")
+    ids, w = torch.empty((T, 1), dtype=torch.int32, device="cuda"), torch.empty((T, 1), device="cuda")
+    off, slots = torch.empty(E + 1, dtype=torch.int32, device="cuda"), torch.empty(T, dtype=torch.int32, device="cuda")
+    lib.moe_route(logits, ids, w, off, slots)
+    lib.device_status()
+    top = logits.float().max(1, keepdim=True).values
+    want = (logits.float() == top).to(torch.uint8).argmax(1)              # the first of equals
+    assert torch.equal(ids[:, 0].long(), want)
+    counts = torch.bincount(want, minlength=E)
+    assert off.tolist() == [0] + torch.cumsum(counts, 0).tolist()
+    assert torch.equal(slots.long(), torch.sort(want, stable=True).indices)
+
+
 def test_route_empty_and_without_plan(lib):
     import torch
     off = torch.full((9,), 5, dtype=torch.int32, device="cuda")
