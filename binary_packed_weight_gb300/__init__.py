@@ -326,18 +326,22 @@ def _rows(t, rows, cols, where, name):
     """Row stride of a [rows, cols] tensor whose rows are contiguous."""
     if t.shape != (rows, cols):
         raise ValueError(f"{where}: {name} must be [{rows}, {cols}], got {list(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{where}: {name} must be on the GPU")
     ld, inner = t.stride()
     if inner != 1 and cols > 1:
         raise ValueError(f"{where}: the rows of {name} must be contiguous")
     return ld if rows > 1 and cols > 1 else max(ld, cols)
 
 
-def _plane(t, shape, dtype, where, name):
-    """The address of a dense tensor of a given shape and dtype (a torch dtype's name)."""
+def _plane(t, shape, dtype, where, name, host=False):
+    """The address of a dense tensor of a given shape and dtype (a torch dtype's name); host: a CPU one will do."""
     if not _names:
         _torch_names()
     if t.dtype is not _names[dtype] or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{where}: {name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if not (t.is_cuda or host):
+        raise ValueError(f"{where}: {name} must be on the GPU")
     return t.data_ptr()
 
 
@@ -360,10 +364,10 @@ def q4_upload(codes, scales, zeros=None, group=128, stream=None):
         raise ValueError(f"q4_upload: codes must be [E, N, K/2] or [N, K/2], got {list(codes.shape)}")
     E, N, K = shape[0], shape[1], 2 * shape[2]
     lead = tuple(codes.shape)[:-1]
-    _plane(codes, lead + (K // 2,), "uint8", "q4_upload", "codes")
-    _plane(scales, lead + (K // group,), "float16", "q4_upload", "scales")
+    _plane(codes, lead + (K // 2,), "uint8", "q4_upload", "codes", host=True)
+    _plane(scales, lead + (K // group,), "float16", "q4_upload", "scales", host=True)
     if zeros is not None:
-        _plane(zeros, lead + (K // group,), "uint8", "q4_upload", "zeros")
+        _plane(zeros, lead + (K // group,), "uint8", "q4_upload", "zeros", host=True)
     h = ctypes.c_void_p()
     _check(load().q4_upload(_ptr(codes), _ptr(scales), _ptr(zeros), E, N, K, group, ctypes.byref(h),
                             _stream(stream)), "q4_upload")
@@ -372,8 +376,8 @@ def q4_upload(codes, scales, zeros=None, group=128, stream=None):
 
 def q4_dequant(w, out, stream=None):
     """W as float32 [E, N, K] (exact)."""
-    if out.numel() != w.E * w.N * w.K or not out.is_contiguous() or str(out.dtype) != "torch.float32":
-        raise ValueError(f"q4_dequant: out must be contiguous float32 of {w.E}*{w.N}*{w.K} elements")
+    if out.numel() != w.E * w.N * w.K or not (out.is_contiguous() and out.is_cuda) or str(out.dtype) != "torch.float32":
+        raise ValueError(f"q4_dequant: out must be contiguous float32 on the GPU, of {w.E}*{w.N}*{w.K} elements")
     _check(load().q4_dequant(w.handle, _ptr(out), _stream(stream)), "q4_dequant")
     return out
 
@@ -382,8 +386,8 @@ def q4_quantize(w, codes, scales, zeros=None, group=128, stream=None):
     """Plain weights [.., N, K] to the planes :func:`q4_upload` takes (see include/tq2.h)."""
     K = w.shape[-1]
     lead = tuple(w.shape)[:-1]
-    if not w.is_contiguous():
-        raise ValueError("q4_quantize: w must be contiguous")
+    if not (w.is_contiguous() and w.is_cuda):
+        raise ValueError("q4_quantize: w must be contiguous and on the GPU")
     _plane(codes, lead + (K // 2,), "uint8", "q4_quantize", "codes")
     _plane(scales, lead + (K // group,), "float16", "q4_quantize", "scales")
     if zeros is not None:

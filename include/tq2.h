@@ -450,7 +450,8 @@ typedef struct q4_weight* q4_handle;
  *           it; the call synchronizes it before returning.
  *
  * The handle holds one copy in 16-row x 256-k blocks (codes, then the block's
- * scales and zero points), N padded to 128 rows and K to 256.
+ * scales and zero points), N padded to 128 rows and K to 256, and a bound of
+ * each matrix's row norms (for moe_experts).
  */
 TQ2_API tq2_status q4_upload(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, int64_t E,
                              int64_t N, int64_t K, int group, q4_handle* out, void* stream);
@@ -479,7 +480,8 @@ TQ2_API tq2_status q4_dequant(q4_handle h, float* w, void* stream);
  *
  *   w       DEVICE, dtype (tq2_dtype), [rows][K] dense, finite (NaN or Inf
  *           give unspecified codes).  rows >= 1, K and group as q4_upload.
- *   codes, scales, zeros   DEVICE, overwritten; codes 4-byte aligned.
+ *   codes, scales, zeros   DEVICE, overwritten; codes 4-byte aligned, w and
+ *           scales aligned to their elements (else TQ2_EINVAL).
  * Asynchronous.
  */
 TQ2_API tq2_status q4_quantize(const void* w, int dtype, int64_t rows, int64_t K, int group, uint8_t* codes,
@@ -492,15 +494,17 @@ TQ2_API tq2_status q4_quantize(const void* w, int dtype, int64_t rows, int64_t K
  *   out     DEVICE, dtype (that of x), M rows of N, ldo >= N elements apart,
  *           overwritten; must not overlap x.
  *   M       0 <= M <= 2^20 (0: nothing is done).
- *   x and out need only their element's alignment (rows that are 16-byte
- *   aligned are fetched faster).
+ *   x and out need only their element's alignment (else TQ2_EINVAL); rows that
+ *   are 16-byte aligned are fetched faster.
  * Weights and f16 / bf16 activations enter the products exactly; f32
  * activations as two f16 parts of a row scaled by a power of two, whose sum
  * is within 2^-22 |x[m,k]| + 2^-38 max_k |x[m,k]| of x.  Accumulation is in
- * f32 and the result is rounded once to dtype.  The order of the additions depends on the shape
- * alone, so results are the same from run to run.
- * Meant for decode batches (M <= 16, where the weights are read once); larger
- * M runs in passes that read the weights again.  Asynchronous, no scratch.
+ * f32 and the result is rounded once to dtype.  The order of the additions
+ * depends on the shape and the GPU alone, so results are the same from run to
+ * run.  A row of x with NaN or Inf has NaN or Inf in its own row of out only.
+ * Meant for decode batches: up to 32 rows of f16 or bf16 (16 of f32) read the
+ * weights once, larger M runs as launches of so many rows (of fewer, where they
+ * do not fit the shared memory of eight SMs).  Asynchronous, no scratch.
  */
 TQ2_API tq2_status q4_gemm(q4_handle h, const void* x, int64_t ldx, void* out, int64_t ldo, int dtype, int64_t M,
                            void* stream);
@@ -518,8 +522,9 @@ typedef enum { MOE_SOFTMAX = 0, MOE_SIGMOID = 1 } moe_score;
  * Per token (row of logits), in f32: expert e is available where its logit
  * and its bias are neither -inf nor NaN; +inf counts as the largest f32.
  *   p     softmax of the available logits, or their sigmoid 1/(1+exp(-l)),
- *         each operation rounded to f32 (so saturated scores tie); 0 for the others.  The softmax sum adds neighbouring experts first
- *         (a binary tree over the row, padded with zeros to a power of two).
+ *         each operation rounded to f32 (so saturated scores tie); 0 for the
+ *         others.  The softmax sum adds neighbouring experts first (a binary
+ *         tree over the row, padded with zeros to a power of two).
  *   s     p + bias: what the selection goes by.
  *   groups > 1 and top_groups < groups: E/groups neighbouring experts form a
  *         group; its value is the sum of its two largest s (of one, where only
@@ -538,7 +543,8 @@ typedef enum { MOE_SOFTMAX = 0, MOE_SIGMOID = 1 } moe_score;
  *   offsets  DEVICE int32[E+1];  slots  DEVICE int32[T*k]; or both NULL: no plan.
  *   0 <= T, T*k <= 2^24;  1 <= E <= 1024;  1 <= k <= 32, k <= E;  groups
  *   divides E and is at most 32;  1 <= top_groups <= groups.  Else TQ2_ESHAPE.
- *   score a moe_score, scale finite.  Else TQ2_EINVAL.
+ *   score a moe_score, scale finite, pointers aligned to their elements.  Else
+ *   TQ2_EINVAL.
  * Asynchronous; scratch (for a plan of many tokens) from the library's
  * stream-ordered pool.
  */
@@ -554,8 +560,9 @@ TQ2_API tq2_status moe_route(const void* logits, int64_t ld, int dtype, const fl
  *   softmax:  dlogits[e] = p_e (q_e - sum_j q_j p_j)      (q_e = 0 unless selected;
  *             with renorm the sum is 0 and only the selected get a gradient)
  *   sigmoid:  dlogits[e] = p_e (1 - p_e) q_e
- * ids as moe_route returned them; a slot of -1 takes no part.  dlogits: DEVICE, dtype,
- * T rows of E, ldd >= E elements apart, overwritten.  Limits as moe_route.  Asynchronous.
+ * ids as moe_route returned them; a slot of -1 takes no part.  dlogits: DEVICE,
+ * dtype, T rows of E, ldd >= E elements apart, overwritten.  Limits as
+ * moe_route.  Asynchronous, no scratch.
  */
 TQ2_API tq2_status moe_route_backward(const void* logits, int64_t ld, int dtype, const float* bias,
                                       const int32_t* ids, const float* dweights, void* dlogits, int64_t ldd,
@@ -575,13 +582,23 @@ TQ2_API tq2_status moe_route_backward(const void* logits, int64_t ld, int dtype,
  *             clamped to their ranges: nothing outside the arrays is touched).
  *   out       DEVICE, dtype, T rows of D, ldo >= D elements apart,
  *             overwritten; must not overlap x.
- *   0 <= T, T*k <= 2^24, 1 <= k <= 32.
- * Shapes that do not fit: TQ2_ESHAPE.  Gate and Up take x as q4_gemm takes it,
- * the gated product between them is kept in f32 and enters Down as f32
- * activations do (for f16 and bf16 calls as its first f16 part alone, within
- * 2^-12 of its magnitude).  A token's sum over j runs in the order of j, in f32.
- * Scratch (T*k rows of F and of D floats) from the library's stream-ordered
- * pool.  Asynchronous.
+ *   0 <= T, T*k <= 2^24, 1 <= k <= 32, (T*k + E) * max(D, 2F) < 2^35, shapes
+ *   that fit each other: else TQ2_ESHAPE.  Pointers aligned to their elements:
+ *   else TQ2_EINVAL.
+ *
+ * Calls of f32, and those of f16 and bf16 with fewer than 10 slots a matrix on
+ * average (T*k < 10 E): Gate and Up take x as q4_gemm takes it; the gated product
+ * is kept in f32 and enters Down as f32 activations do (for f16 and bf16 as its
+ * first f16 part alone, within 2^-11 of its magnitude).
+ * f16 and bf16 calls with more: the weights are rounded to f16, rows of x and of
+ * the gated product are f16 scaled by a power of two each (of x so that its
+ * largest element is just below 2^15; of the gated product by a bound of it,
+ * |x|^2 times the bounds of Gate's and Up's row norms, so that elements below
+ * 2^-28 of that bound lose bits), and a product's sum over k runs in f32.
+ * Either way a token's sum over j runs in the order of j, in f32, and is
+ * rounded once to dtype.
+ * Scratch from the library's stream-ordered pool: T*k rows of D floats, and of F
+ * floats (f16 and bf16 calls with many slots: of F and of D halves).  Asynchronous.
  */
 TQ2_API tq2_status moe_experts(q4_handle gate, q4_handle up, q4_handle down, const void* x, int64_t ldx, int dtype,
                                const int32_t* ids, const float* weights, const int32_t* offsets,

@@ -106,3 +106,30 @@ def test_moe_experts(lib):
     assert experts(dtype=9) == TQ2_EINVAL
     for bad in (dict(T=-1), dict(k=0), dict(k=33), dict(T=1 << 24), dict(T=1 << 62, k=4)):      # refused before a handle is read
         assert experts(**bad) == TQ2_ESHAPE, bad
+
+
+def test_binding_refuses_host_tensors_and_wrong_shapes(lib):
+    import torch
+    import binary_packed_weight_gb300 as bpw
+    w = bpw.Q4Weight(None, 1, 16, 128, 128)
+    x, out = torch.zeros((2, 128)), torch.zeros((2, 16))
+    with pytest.raises(ValueError, match="on the GPU"):
+        bpw.q4_gemm(w, x, out)
+    with pytest.raises(ValueError, match=r"x must be \[2, 128\]"):
+        bpw.q4_gemm(w, x[:, :64], out)
+    with pytest.raises(TypeError):
+        bpw.q4_gemm(w, x.half(), out)
+    with pytest.raises(ValueError, match="on the GPU"):
+        bpw.q4_dequant(w, torch.zeros((1, 16, 128)))
+    with pytest.raises(ValueError, match="on the GPU"):
+        bpw.q4_quantize(x, torch.zeros((2, 64), dtype=torch.uint8), torch.zeros((2, 1), dtype=torch.float16))
+    ids, wt = torch.zeros((2, 4), dtype=torch.int32), torch.zeros((2, 4))
+    with pytest.raises(ValueError, match="on the GPU"):
+        bpw.moe_route(out, ids, wt)
+    with pytest.raises(ValueError, match="score"):
+        bpw._score("tanh", "moe_route")
+    with pytest.raises(ValueError, match="on the GPU"):
+        bpw.moe_route_backward(out, ids, wt, torch.zeros_like(out))
+    with pytest.raises(ValueError, match="on the GPU"):
+        bpw.moe_experts(w, w, w, x, ids, wt, torch.zeros(2, dtype=torch.int32), torch.zeros(8, dtype=torch.int32),
+                        torch.zeros_like(x))
