@@ -4,9 +4,9 @@
 //   hidden[p] = silu(Gate x[p]) * (Up x[p]),   y[slot(p)] = Down hidden[p]
 //
 // Both products are D[n, p] = sum_k W[n,k] act[p,k] with 128 weight rows and up
-// to 256 positions a tile, f16 operands and one f32 accumulator in tensor memory,
-// in stages of 128 k (what a stage costs besides its MMAs -- waits, commits, the
-// decoders' hand-offs, several hundred cycles -- does not grow with its k):
+// to 256 (wide tiles: 384) positions a tile, f16 operands and one f32 accumulator in
+// tensor memory, in stages of 128 k (what a stage costs besides its MMAs -- waits,
+// commits, the decoders' hand-offs, several hundred cycles -- does not grow with its k):
 //   * warps 0 and 2 stream the activations (B, 128-byte swizzle) by TMA, the first
 //     and the second 64 k of a stage (one warp takes ~650 cycles a slot);
 //   * warp 3 streams the packed blocks of 256 k by bulk copies;
@@ -15,8 +15,12 @@
 //     tensor memory (rounding (c - z) d to f16 is the only rounding of the weights);
 //   * warp 1 issues the MMAs; one barrier a stage covers both operands, and the
 //     next stage's is tested while this stage's MMAs run;
-//   * eight epilogue warps drain the finished tile, some columns each in turn,
-//     while the next tile's operands fill their rings.
+//   * eight or sixteen epilogue warps drain the finished tile, some columns each in
+//     turn, while the next tile's operands fill their rings.
+// A matrix's weights are decoded once for each of its tiles, so tiles are as wide as
+// tensor memory allows: 256 columns of accumulator leave room for four stages of
+// weights, 320 for three, 384 for two.  (With 256 at most, experts of 257 rows were
+// two tiles, each bound by the decoders: 2048 tokens of 64 experts 243 us, now 219.)
 // A tile of the first product holds 64 rows of Gate and the same 64 of Up: lanes
 // 0..15 of each quarter are Gate's, 16..31 Up's, so one shuffle meets the two.
 //
@@ -36,23 +40,24 @@ namespace tq2 {
 
 namespace {
 
-// Decoder groups (of four warps) and columns an epilogue warp takes at a time:
-// three groups feed narrow tiles, whose MMAs are short; with two, an epilogue
-// warp has the registers for 32 columns and the next 32 (64 experts of
-// 2048x1024, 64 / 512 / 2048 tokens of top 8: 96 / 115 / 277 us against 107 / 117 / 259 us).
+// Decoder groups (of four warps), epilogue warps and the columns one of those takes
+// at a time.  Narrow tiles, whose MMAs are short, need three groups to feed them; the
+// epilogue of wide ones, which the next tile's MMAs wait for, needs sixteen warps
+// (64 experts of 2048x1024 bf16, top 8, 2048 tokens: 219 us with 2 groups and 16
+// warps, 227 with 2 and 12, 230 with 3 and 12, 248 with 3 and 8).
 template <bool WIDE>
 struct MuShape {
     static constexpr int GROUPS = WIDE ? 2 : 3;
     static constexpr int EPI = 4 + 4 * GROUPS;             // first epilogue warp
-    static constexpr int THREADS = 32 * (EPI + 8);
-    static constexpr int CW = WIDE ? 32 : 16;
+    static constexpr int DRAIN = WIDE ? 16 : 8;            // epilogue warps
+    static constexpr int THREADS = 32 * (EPI + DRAIN);
+    static constexpr int CW = 16;
 };
-constexpr int MU_BN = 256;                 // positions of a tile
-constexpr int MU_B = 5;                    // activation slots of 64 k (32 KB)
+constexpr int MU_BN = 384;                 // positions of a tile at most
+constexpr int MU_B = 160 * 1024;           // bytes of the activation ring
 constexpr int MU_A = 4;                    // stages of 128 k: decoded weights (64 tensor-memory columns each)
 constexpr int MU_RAW = 3;                  // packed blocks of 256 k
-constexpr int MU_B_SLOT = MU_BN * 128;
-constexpr int MU_ACOL = MU_BN;             // first tensor-memory column of the A stages
+constexpr int MU_ACOL = 256;               // first tensor-memory column of the A stages
 constexpr int MU_LIST = 64;                // tiles of a CTA that are looked up ahead
 
 // Activation rows in boxes of 32, 64, 128 and 256: a tile is loaded in at most
@@ -67,12 +72,41 @@ struct MuTile {
 
 struct MuBars {
     uint64_t full[MU_A], empty[MU_A], half_empty[MU_A], raw_full[MU_RAW], raw_empty[MU_RAW];
-    uint64_t acc_full, acc_empty;
+    uint64_t acc_full, acc_empty, drained;
     uint32_t tmem_base;
     int abort;
     MuTile list[MU_LIST];
-    float2 scale[MU_BN];                   // epilogue: a tile's scales and output rows
-    int row[MU_BN];
+    float2 scale[MU_BN];                   // epilogue: a tile's scales (or output rows and scales)
+};
+
+// The stage at hand and the parities of its barriers' phases.  A tile of more
+// than 256 (320) positions has its last accumulator columns where stage 0 (and
+// 1) would be, so it goes without; a later tile that takes such a stage up again
+// waits for `drained`, which the MMA warp completes then.  (Two groups of
+// decoders need two stages: a group's last wait must be past every older phase
+// of the stage that it waits for next.)
+template <bool WIDE>
+struct MuStages {
+    int s = 0;
+    int lowest = 0;                        // (stays 0 unless WIDE)
+    uint32_t used = 0;
+    // The next tile; returns the last one's lowest stage.
+    __device__ __forceinline__ int begin(int cnt) {
+        const int was = WIDE ? lowest : 0;
+        if (WIDE) {
+            lowest = cnt > 320 ? 2 : cnt > 256 ? 1 : 0;
+            s = s < lowest ? lowest : s;
+        }
+        return was;
+    }
+    __device__ __forceinline__ void next() {
+        used ^= 1u << s;
+        s = s + 1 == MU_A ? (WIDE ? lowest : 0) : s + 1;
+    }
+    __device__ __forceinline__ uint32_t parity() const { return (used >> s) & 1u; }
+    // Activation slots of 64 k in the ring, and their bytes.
+    __device__ __forceinline__ int slots() const { return WIDE ? 5 - lowest : 5; }
+    __device__ __forceinline__ uint32_t slot_bytes() const { return WIDE ? 32768u + 8192u * (uint32_t)lowest : 32768u; }
 };
 
 // Slot and phase parity of a ring's next item.
@@ -97,7 +131,8 @@ struct MuArgs {
     int nkc, zeros, E, nslots;
     int N;                                 // output columns (F, or D)
     int row_tiles;                         // tiles along them
-    int nk;                                // 64-k stages of a tile
+    int nk;                                // 64-k slots of a tile
+    int bn;                                // positions of a tile at most
     const int* offsets;
     const int* slots;
     const float2* scales;                  // [position] of a row of x: 1/scale; of the hidden row: scale
@@ -106,7 +141,8 @@ struct MuArgs {
 };
 
 // Barrier of the eight epilogue warps.
-__device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+template <int WARPS>
+__device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory"); }
 
 template <int G, bool PAIR, bool WIDE>
 __global__ void __launch_bounds__(MuShape<WIDE>::THREADS, 1)
@@ -114,10 +150,11 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     constexpr int NG = Q4_K / G;
     constexpr int MU_GROUPS = MuShape<WIDE>::GROUPS, MU_EPI = MuShape<WIDE>::EPI, MU_THREADS = MuShape<WIDE>::THREADS;
-    constexpr int CW = MuShape<WIDE>::CW;
+    constexpr int CW = MuShape<WIDE>::CW, DRAIN = MuShape<WIDE>::DRAIN;
+    constexpr int STEP = CW * DRAIN / 4;                   // columns that the epilogue warps of a quarter take in turn
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int blk = q4_block_bytes(G, a.zeros != 0);
-    uint8_t* raw_ring = smem + MU_B * MU_B_SLOT;
+    uint8_t* raw_ring = smem + MU_B;
     MuBars* bars = reinterpret_cast<MuBars*>(raw_ring + MU_RAW * 8 * blk);
     int* prefix = reinterpret_cast<int*>(bars + 1);        // token tiles before each matrix
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -133,7 +170,8 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
             mbar_init(&bars->raw_empty[r], 4 * MU_GROUPS); // every decoder warp
         }
         mbar_init(&bars->acc_full, 1);
-        mbar_init(&bars->acc_empty, 8);                    // every epilogue warp
+        mbar_init(&bars->acc_empty, DRAIN);                    // every epilogue warp
+        mbar_init(&bars->drained, 1);                      // the MMA warp
         bars->abort = 0;
         fence_mbar_init();
         for (int i = 0; i < 4; ++i) tma_prefetch_desc(&maps.box[i]);
@@ -151,7 +189,7 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
             const int e = e0 + lane;
             const int o = e <= a.E ? plan_offset(a.offsets, a.nslots, e) : 0;
             const int rows = e < a.E ? plan_offset(a.offsets, a.nslots, e + 1) - o : 0;
-            const int n = (rows + MU_BN - 1) / MU_BN;
+            const int n = (rows + a.bn - 1) / a.bn;
             down |= rows < 0;
             int s = n;
 #pragma unroll
@@ -200,40 +238,72 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
     if (warp == 0 || warp == 2) {                          // ---- activations
         pdl_wait();
         if (elect_one()) {
+            // The ring's slots are cut anew where a tile has another number of them than the one before: after
+            // that one's last MMA, while its accumulator is drained.  Otherwise slot n is free after the MMAs
+            // of slot n - slots, whose stage `old` follows `late` stages behind.
             const int half = warp >> 1;                    // first or second 64 k of the stages
-            Ring<MU_A> f;
+            MuStages<WIDE> f, old;
             bool ok = true;
-            uint32_t stage = 0;                            // of the CTA's sequence; its slots are 2*stage, 2*stage + 1
+            int slot = half, run = 0;                      // stages since the ring was cut
+            uint32_t armed = 0, parity = 0;                // stages whose full barrier was armed, and for which phase
+            uint64_t* last = nullptr;                      // of the stage before
+            uint32_t last_parity = 0;
             for (int i = 0; i < mine && ok; ++i) {
                 const MuTile m = tile_at(i);
                 const int boxes = (m.cnt + 31) / 32;
-                for (int ks = half; ks < 2 * stages; ks += 2, ++stage, f.next()) {
-                    // the slot's last use, five slots ago, was in the other half of stage (2*stage + half - 5) / 2:
-                    // its MMAs are done
-                    const uint32_t n = 2 * stage + half, slot = n % MU_B, old = (n - MU_B) / 2;
-                    uint64_t* freed = half ? &bars->half_empty[old % MU_A] : &bars->empty[old % MU_A];
-                    if (n >= MU_B && !mbar_wait_or_abort(freed, (old / MU_A) & 1u, abort_flag)) {
-                        *abort_flag = 1;
+                if (f.begin(m.cnt) != f.lowest) {
+                    if (last && !mbar_wait_or_abort(last, last_parity, abort_flag)) {
                         ok = false;
                         break;
                     }
-                    const bool there = ks < a.nk;          // the last stage may be one slot
-                    mbar_arrive_expect_tx(&bars->full[f.s], there ? (uint32_t)boxes * 4096u : 0u);
-                    if (!there) continue;
-                    int at = 0;
-#pragma unroll
-                    for (int x = 3; x >= 0; --x)
-                        if (boxes & (1 << x)) {
-                            tma_load_2d(smem + slot * MU_B_SLOT + at * 4096, &maps.box[x], &bars->full[f.s], ks * 64,
-                                        m.p0 + 32 * at);
-                            at += 1 << x;
+                    slot = half;
+                    run = 0;
+                }
+                if (run == 0) old = f;
+                const int slots = f.slots();
+                const uint32_t bytes = f.slot_bytes();
+                // slot 2 st + half - slots
+                const int late = (slots - half + 1) / 2;
+                uint64_t* freed = (slots - half) & 1 ? bars->empty : bars->half_empty;
+                for (int st = 0; st < stages; ++st) {
+                    if (run >= late) {
+                        if (!mbar_wait_or_abort(&freed[old.s], old.parity(), abort_flag)) {
+                            ok = false;
+                            break;
                         }
+                        old.next();
+                    }
+                    ++run;
+                    const bool there = 2 * st + half < a.nk;   // the last stage may be one slot
+                    uint64_t* bar = &bars->full[f.s];
+                    armed |= 1u << f.s;
+                    parity = (parity & ~(1u << f.s)) | f.parity() << f.s;
+                    mbar_arrive_expect_tx(bar, there ? (uint32_t)boxes * 4096u : 0u);
+                    if (there) {
+                        uint8_t* dst = smem + (uint32_t)slot * bytes;
+                        int row = m.p0;
+#pragma unroll
+                        for (int x = 3; x >= 0; --x)
+                            if (boxes & (1 << x)) {
+                                tma_load_2d(dst, &maps.box[x], bar, (2 * st + half) * 64, row);
+                                dst += 4096 << x;
+                                row += 32 << x;
+                            }
+                    }
+                    slot += 2;
+                    slot -= slot >= slots ? slots : 0;
+                    last = &bars->empty[f.s];
+                    last_parity = f.parity();
+                    f.next();
                 }
             }
             // After a wait that ran out the copies already issued must land before the CTA exits.  Each is
             // short of its barrier's phase, which may never complete: give them their (bounded) time.
-            if (!ok)
-                for (int x = 0; x < MU_A; ++x) mbar_wait(&bars->full[x], x < f.s ? f.ph : f.ph ^ 1u);
+            if (!ok) {
+                *abort_flag = 1;
+                for (int x = 0; x < MU_A; ++x)
+                    if ((armed >> x) & 1u) mbar_wait(&bars->full[x], (parity >> x) & 1u);
+            }
         }
         __syncwarp();
     } else if (warp == 3) {
@@ -269,39 +339,57 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
         }
     } else if (warp == 1) {                                // ---- MMA issuer
         if (elect_one()) {
-            uint32_t slot = 0;                             // of the stage's first 64 k
-            Ring<MU_A> f;
-            bool ok = true, ready = false;
+            int slot = 0;                                  // of the stage's first 64 k
+            MuStages<WIDE> f;
+            bool ok = true;
             int cnt = mine > 0 ? tile_at(0).cnt : 0;
             for (int i = 0; i < mine && ok; ++i) {
-                const uint32_t idesc = idesc_f16_f32(128, (uint32_t)((cnt + 15) / 16 * 16));
-                if (i > 0 && !mbar_wait_or_abort(&bars->acc_empty, (uint32_t)(i - 1) & 1u, abort_flag, true)) {
-                    *abort_flag = 1;
-                    break;
+                // more than 256 positions are two MMAs side by side
+                const int n16 = (cnt + 15) / 16 * 16, n1 = WIDE && cnt > 256 ? (n16 / 16 + 1) / 2 * 16 : n16, n2 = n16 - n1;
+                const uint32_t idesc = idesc_f16_f32(128, (uint32_t)n1), idesc2 = idesc_f16_f32(128, (uint32_t)n2);
+                if (i > 0) {
+                    if (!mbar_wait_or_abort(&bars->acc_empty, (uint32_t)(i - 1) & 1u, abort_flag, true)) {
+                        *abort_flag = 1;
+                        break;
+                    }
                 }
+                const int was = f.begin(cnt);
+                if (f.lowest < was) mbar_arrive(&bars->drained);
+                if (f.lowest != was) slot = 0;
+                const int slots = f.slots();
+                const uint32_t bytes = f.slot_bytes();
+                bool ready = false;
                 tc_fence_after();
                 for (int st = 0; st < stages; ++st) {
-                    if (!ready && !mbar_wait_or_abort(&bars->full[f.s], f.ph, abort_flag, true)) {
+                    if (!ready && !mbar_wait_or_abort(&bars->full[f.s], f.parity(), abort_flag, true)) {
                         *abort_flag = 1;
                         ok = false;
                         break;
                     }
-                    Ring<MU_A> g = f;
+                    MuStages<WIDE> g = f;
                     g.next();
-                    ready = mbar_test_wait(&bars->full[g.s], g.ph);   // its latency hides under the MMAs below
+                    // (its latency hides under the MMAs below)
+                    ready = st + 1 < stages && mbar_test_wait(&bars->full[g.s], g.parity());
                     tc_fence_after();
                     const uint32_t acol = tmem + MU_ACOL + (uint32_t)(f.s * 64);
 #pragma unroll
-                    for (int at = 0; at < 2; ++at) {
-                        if (at == 0 || 2 * st + 1 < a.nk) {
-                            const uint64_t bdesc = sdesc_kmajor_sw128(smem_u32(smem + slot * MU_B_SLOT));
+                    for (int h = 0; h < 2; ++h) {
+                        if (h == 0 || 2 * st + 1 < a.nk) {
+                            const uint64_t bdesc = sdesc_kmajor_sw128(smem_u32(smem + (uint32_t)slot * bytes));
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                umma_f16_ts(tmem, acol + (uint32_t)(at * 32 + j * 8), bdesc + (uint64_t)(2 * j), idesc,
-                                            (st > 0 || at > 0 || j > 0) ? 1u : 0u);
+                                umma_f16_ts(tmem, acol + (uint32_t)(h * 32 + j * 8), bdesc + (uint64_t)(2 * j), idesc,
+                                            (st > 0 || h > 0 || j > 0) ? 1u : 0u);
+                            if (WIDE && n2) {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    umma_f16_ts(tmem + (uint32_t)n1, acol + (uint32_t)(h * 32 + j * 8),
+                                                bdesc + (uint64_t)(2 * j + n1 * 8), idesc2,
+                                                (st > 0 || h > 0 || j > 0) ? 1u : 0u);
+                            }
                         }
-                        if (++slot == MU_B) slot = 0;
-                        umma_commit(at == 0 ? &bars->half_empty[f.s] : &bars->empty[f.s]);
+                        if (++slot == slots) slot = 0;
+                        umma_commit(h == 0 ? &bars->half_empty[f.s] : &bars->empty[f.s]);
                     }
                     f = g;
                 }
@@ -320,10 +408,12 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
         const uint32_t expo = q4_exponent<false>();
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16) + MU_ACOL;
         Ring<MU_RAW> r;
-        Ring<MU_A> f;
+        MuStages<WIDE> f;
         int turn = (warp - 4) >> 2;                        // stages until this group's next one
+        uint32_t drains = 0;
         bool ok = true;
         for (int i = 0; i < mine && ok; ++i) {
+            bool owed = f.begin(tile_at(i).cnt) > f.lowest;   // a wait before this tile's first store
             for (int kc = 0; kc * 4 < a.nk && ok; ++kc, r.next()) {
                 if (!mbar_wait_or_abort(&bars->raw_full[r.s], r.ph, abort_flag)) {
                     *abort_flag = 1;
@@ -365,7 +455,13 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
                             }
                         }
                         if (at == 0) {
-                            if (!f.first && !mbar_wait_or_abort(&bars->empty[f.s], f.ph ^ 1u, abort_flag)) {
+                            if (owed) {
+                                ok = mbar_wait_or_abort(&bars->drained, drains & 1u, abort_flag);
+                                ++drains;
+                                owed = false;
+                            }
+                            // (passes at a stage's first use)
+                            if (!ok || !mbar_wait_or_abort(&bars->empty[f.s], f.parity() ^ 1u, abort_flag)) {
                                 *abort_flag = 1;
                                 ok = false;
                                 break;
@@ -392,12 +488,13 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
         pdl_wait();
         for (int ti = 0; ti < mine; ++ti) {
             const MuTile m = tile_at(ti);
-            epi_bar();                                     // the last tile's scales and rows are done with
-            for (int i = tid - MU_EPI * 32; i < m.cnt; i += 256) {
-                bars->scale[i] = a.scales[m.p0 + i];
-                if (!PAIR) bars->row[i] = plan_slot(a.slots, a.nslots, m.p0 + i);
+            epi_bar<DRAIN>();                                     // the last tile's scales and rows are done with
+            for (int i = tid - MU_EPI * 32; i < m.cnt; i += DRAIN * 32) {
+                float2 sc = a.scales[m.p0 + i];
+                if (!PAIR) sc.x = __int_as_float(plan_slot(a.slots, a.nslots, m.p0 + i));
+                bars->scale[i] = sc;
             }
-            epi_bar();
+            epi_bar<DRAIN>();
             if (!mbar_wait_or_abort(&bars->acc_full, (uint32_t)ti & 1u, abort_flag)) {
                 *abort_flag = 1;
                 break;
@@ -414,7 +511,7 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
                 if constexpr (CW == 32) tmem_ld_32x32b_x32(lane_addr + (uint32_t)cc, x);
                 else tmem_ld_32x32b_x16(lane_addr + (uint32_t)cc, x);
                 tmem_wait_ld();
-                if (cc + 2 * CW >= m.cnt) {
+                if (cc + STEP >= m.cnt) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars->acc_empty);
@@ -438,26 +535,27 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
                 } else if (in) {
                     float* out = a.y + n;
                     const int left = m.cnt - cc;
+                    auto put = [&](int i) {
+                        const float2 sc = bars->scale[cc + i];
+                        out[(int64_t)__float_as_int(sc.x) * a.N] = __uint_as_float(x[i]) * sc.y;
+                    };
                     if (left >= CW) {
 #pragma unroll
-                        for (int i = 0; i < CW; ++i)
-                            out[(int64_t)bars->row[cc + i] * a.N] = __uint_as_float(x[i]) * bars->scale[cc + i].y;
+                        for (int i = 0; i < CW; ++i) put(i);
                     } else {
 #pragma unroll
                         for (int i = 0; i < CW; ++i)
-                            if (i < left)
-                                out[(int64_t)bars->row[cc + i] * a.N] =
-                                    __uint_as_float(x[i]) * bars->scale[cc + i].y;
+                            if (i < left) put(i);
                     }
                 }
             };
             if (CW * b < m.cnt) read(v, CW * b);
-            for (int cc = CW * b; cc < m.cnt; cc += 4 * CW) {
-                if (cc + 2 * CW < m.cnt) read(w, cc + 2 * CW);
+            for (int cc = CW * b; cc < m.cnt; cc += 2 * STEP) {
+                if (cc + STEP < m.cnt) read(w, cc + STEP);
                 finish(v, cc);
-                if (cc + 2 * CW < m.cnt) {
-                    if (cc + 4 * CW < m.cnt) read(v, cc + 4 * CW);
-                    finish(w, cc + 2 * CW);
+                if (cc + STEP < m.cnt) {
+                    if (cc + 2 * STEP < m.cnt) read(v, cc + 2 * STEP);
+                    finish(w, cc + STEP);
                 }
             }
             if (held) {                                    // a narrow tile: no columns for this warp
@@ -574,11 +672,13 @@ moe_stage_kernel(const T* __restrict__ x, int64_t ldx, int vec, int D, const int
 }
 
 template <int G, bool PAIR, bool WIDE>
-cudaError_t launch_umma_moe(const MuMaps& maps, const MuArgs& a, cudaStream_t st) {
+cudaError_t launch_umma_moe(const MuMaps& maps, MuArgs a, cudaStream_t st) {
+    // more than 256 positions to a tile need a store of every decoder group in each tile (four stages)
+    a.bn = WIDE && a.nk > 6 ? MU_BN : 256;
     int dev = 0, sms = 152;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const size_t smem = 1024 + (size_t)MU_B * MU_B_SLOT + (size_t)MU_RAW * 8 * q4_block_bytes(G, a.zeros != 0) +
+    const size_t smem = 1024 + (size_t)MU_B + (size_t)MU_RAW * 8 * q4_block_bytes(G, a.zeros != 0) +
                         sizeof(MuBars) + (size_t)(a.E + 1) * 4;
     cudaError_t e = cudaFuncSetAttribute(moe_umma_kernel<G, PAIR, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
@@ -598,8 +698,9 @@ bool row_maps(MuMaps& m, __half* rows, int64_t inner, int64_t n) {
 
 template <bool PAIR>
 cudaError_t launch_by_group(int group, const MuMaps& maps, const MuArgs& a, cudaStream_t st) {
-    // wide tiles from 96 rows a matrix on average
-    const bool wide = a.nslots >= 96 * (int64_t)a.E;
+    // wide tiles from 120 rows a matrix on average (64 experts of 2048x1024, 96 / 128 rows each: narrow 130 / 146
+    // us, wide 137 / 144)
+    const bool wide = a.nslots >= 120 * (int64_t)a.E;
     if (group == 32)
         return wide ? launch_umma_moe<32, PAIR, true>(maps, a, st) : launch_umma_moe<32, PAIR, false>(maps, a, st);
     if (group == 64)

@@ -268,6 +268,36 @@ def test_experts_many_tokens_of_any_magnitude(lib, magnitude):
     assert np.all(np.abs(got - want) <= bound)
 
 
+@pytest.mark.parametrize("seed", [0, 1])
+def test_experts_tiles_of_every_width(lib, seed):
+    """Several tiles of very different widths one after the other in each CTA; positions beside the widths' limits
+    are compared (one expert a token, so that a token is a position)."""
+    rng = np.random.default_rng(30 + seed)
+    E, D, F, group = 40, 576, 832, 64
+    counts = [384, 385, 320, 321, 256, 257, 1, 0, 2, 31, 33, 64, 97, 128, 160, 255, 300, 352, 383, 511, 512, 513, 768, 769]
+    counts = rng.permutation(counts + list(rng.integers(200, 400, E - len(counts))))
+    mats, handles = [], []
+    for N, K in ((F, D), (F, D), (D, F)):
+        c, d, z = planes(rng, E, N, K, group, True)
+        mats.append(oq4.dequant(c, d.view(np.uint16), z, group))
+        handles.append(upload(lib, c, d, z, group))
+    ids = rng.permutation(np.repeat(np.arange(E), counts))[:, None]
+    T = len(ids)
+    weights = rng.random((T, 1)).astype(np.float32)
+    x, got = run_experts(lib, rng.normal(size=(T, D)) * 0.2, ids, weights, handles, "bfloat16", E)
+    pick = []
+    for e in range(E):
+        of = np.flatnonzero(ids[:, 0] == e)
+        pick += [of[p] for p in {0, len(of) // 2, len(of) - 1, 127, 255, 256, 319, 320, 383} if 0 <= p < len(of)]
+    x, got, ids, weights = x[pick], got[pick], ids[pick], weights[pick]
+    want = omoe.experts(x, ids, weights, *mats)
+    eps = 2.0 ** -11 + (F / 16 + 16) * 2.0 ** -22
+    bound = omoe.experts_bound(x, ids, weights, *mats, eps, eps, 2.0 ** -11)
+    bound = 1.02 * bound + (2.0 ** -8 + 2.0 ** -22) * np.abs(want) + 1e-7
+    bad = ~(np.abs(got - want) <= bound)
+    assert not bad.any(), f"{bad.sum()} off, worst {np.max(np.abs(got - want) / bound):.3g} of the bound"
+
+
 def test_experts_no_tokens_and_no_slots(lib):
     import torch
     rng = np.random.default_rng(4)
