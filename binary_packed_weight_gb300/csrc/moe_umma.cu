@@ -579,11 +579,13 @@ template <>
 struct Pair<__half> {
     using type = __half2;
     static __device__ __forceinline__ float2 f32(__half2 v) { return __half22float2(v); }
+    static __device__ __forceinline__ __half2 zero() { return __float2half2_rn(0.f); }
 };
 template <>
 struct Pair<__nv_bfloat16> {
     using type = __nv_bfloat162;
     static __device__ __forceinline__ float2 f32(__nv_bfloat162 v) { return __bfloat1622float2(v); }
+    static __device__ __forceinline__ __nv_bfloat162 zero() { return __float2bfloat162_rn(0.f); }
 };
 // Eight elements of a row.
 template <class T>
@@ -602,72 +604,102 @@ __device__ __forceinline__ void load8(const T* p, bool vec, typename Pair<T>::ty
     }
 }
 
-// A warp a position: its row of x as f16, scaled, and the scales.  Two passes
-// over the row, the second from L1; a token's rows share its lines in L2.
-template <class T>
+// Of each routed slot: its position and the product of its matrices' bounds.
 __global__ void __launch_bounds__(256)
-moe_stage_kernel(const T* __restrict__ x, int64_t ldx, int vec, int D, const int* __restrict__ offsets,
-                 const int* __restrict__ slots, int nslots, int k, int E, const float* __restrict__ bound0,
-                 const float* __restrict__ bound1, __half* __restrict__ xs, float2* __restrict__ first,
-                 float2* __restrict__ second) {
-    const int lane = threadIdx.x & 31;
+moe_where_kernel(const int* __restrict__ offsets, const int* __restrict__ slots, int nslots, int E,
+                 const float* __restrict__ bound0, const float* __restrict__ bound1, float2* __restrict__ where) {
     pdl_launch_dependents();
     pdl_wait();
-    const int end = plan_offset(offsets, nslots, E);
-    for (int p = blockIdx.x * 8 + (threadIdx.x >> 5); p < end; p += gridDim.x * 8) {
-        const T* row = x + (int64_t)(plan_slot(slots, nslots, p) / k) * ldx;
-        typename Pair<T>::type v[4], top[4];
-        float ss = 0.f;
-        load8(row + (lane * 8 < D ? lane * 8 : 0), vec != 0, v);
+    const int p = blockIdx.x * 256 + threadIdx.x;
+    if (p >= plan_offset(offsets, nslots, E)) return;
+    int lo = 0, hi = E;                                    // the position's matrix
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (plan_offset(offsets, nslots, mid) <= p) lo = mid; else hi = mid;
+    }
+    where[plan_slot(slots, nslots, p)] = make_float2(__int_as_float(p), bound0[lo] * bound1[lo]);
+}
+
+// A CTA a token: its row of x as f16, scaled, at each of its positions, and the
+// scales.  A row is converted once for all its positions (a warp a position took 745
+// instructions for each: 21 us for 16384 slots of 2048, now 15; the whole call of 2048
+// tokens of 64 experts 227 -> 221); what is left is bound by the writes of T*k*D halves.
+template <class T>
+__global__ void __launch_bounds__(256)
+moe_stage_kernel(const T* __restrict__ x, int64_t ldx, int vec, int D, const int* __restrict__ ids,
+                 const float2* __restrict__ where, int nslots, int k, __half* __restrict__ xs,
+                 float2* __restrict__ first, float2* __restrict__ second) {
+    __shared__ int to[32];                                 // positions, -1: none
+    __shared__ float red[9];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t t = blockIdx.x;
+    const T* row = x + t * ldx;
+    typename Pair<T>::type v[4], top[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top[i] = __habs2(v[i]);
+    for (int i = 0; i < 4; ++i) v[i] = top[i] = Pair<T>::zero();
+    float2 at = make_float2(0.f, 0.f);
+    int pos = -1;
+    if (tid < k && ids[t * k + tid] >= 0) {
+        at = where[t * k + tid];
+        pos = min(max(__float_as_int(at.x), 0), nslots - 1);
+    }
+    for (int c = tid * 8; c < D; c += 2048) {
+        load8(row + c, vec != 0, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top[i] = __hmax2(top[i], __habs2(v[i]));
+    }
+    top[0] = __hmax2(__hmax2(top[0], top[1]), __hmax2(top[2], top[3]));
+    float m = fmaxf(Pair<T>::f32(top[0]).x, Pair<T>::f32(top[0]).y);
+    m = __int_as_float(__reduce_max_sync(0xffffffffu, __float_as_int(m)));   // m >= 0: its bits have its order
+    if (lane == 0) red[warp] = m;
+    if (tid < 32) to[tid] = pos;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, red[i]);
+    const int be = (__float_as_int(m) >> 23) & 255;
+    int se = be == 0 ? 253 : 127 + 14 - (be - 127);
+    if (m == 0.f || be == 255) se = 127;
+    se = se > 253 ? 253 : se;
+    const float s = __int_as_float(se << 23);
+    float ss = 0.f;
+    for (int c = tid * 8; c < D; c += 2048) {
+        if (D > 2048) load8(row + c, vec != 0, v);         // (else they are at hand)
+        __half2 h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float2 f = Pair<T>::f32(v[i]);
+            f.x *= s;
+            f.y *= s;
+            ss = fmaf(f.x, f.x, ss);
+            ss = fmaf(f.y, f.y, ss);
+            h[i] = __float22half2_rn(f);
+        }
 #pragma unroll 4
-        for (int c = lane * 8 + 256; c < D; c += 256) {
-            load8(row + c, vec != 0, v);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top[i] = __hmax2(top[i], __habs2(v[i]));
+        for (int j = 0; j < k; ++j) {
+            const int p = to[j];
+            if (p >= 0) *reinterpret_cast<uint4*>(xs + (int64_t)p * D + c) = *reinterpret_cast<uint4*>(h);
         }
-        top[0] = __hmax2(__hmax2(top[0], top[1]), __hmax2(top[2], top[3]));
-        float m = fmaxf(Pair<T>::f32(top[0]).x, Pair<T>::f32(top[0]).y);
-        m = __int_as_float(__reduce_max_sync(0xffffffffu, __float_as_int(m)));   // m >= 0: its bits have its order
-        const int be = (__float_as_int(m) >> 23) & 255;
-        int se = be == 0 ? 253 : 127 + 14 - (be - 127);
-        if (m == 0.f || be == 255) se = 127;
-        se = se > 253 ? 253 : se;
-        const float s = __int_as_float(se << 23);
-#pragma unroll 4
-        for (int c = lane * 8; c < D; c += 256) {
-            load8(row + c, vec != 0, v);
-            __half2 h[4];
+    }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float2 f = Pair<T>::f32(v[i]);
-                f.x *= s;
-                f.y *= s;
-                ss = fmaf(f.x, f.x, ss);
-                ss = fmaf(f.y, f.y, ss);
-                h[i] = __float22half2_rn(f);
-            }
-            *reinterpret_cast<uint4*>(xs + (int64_t)p * D + c) = *reinterpret_cast<uint4*>(h);
-        }
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    __syncthreads();
+    if (lane == 0) red[warp] = ss;
+    __syncthreads();
+    if (pos >= 0) {
+        ss = 0.f;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (lane == 0) {
-            int lo = 0, hi = E;                            // the position's matrix
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (plan_offset(offsets, nslots, mid) <= p) lo = mid; else hi = mid;
-            }
-            // exponent of the hidden row's bound, x's own scale taken out
-            const float b = ss * bound0[lo] * bound1[lo];
-            const int e = ((__float_as_int(b) >> 23) & 255) - 127 - 2 * (se - 127);
-            int hs = 127 + 14 - e;
-            if (b == 0.f) hs = 127;
-            hs = hs < 1 ? 1 : hs > 253 ? 253 : hs;
-            const float inv = __int_as_float((254 - se) << 23);
-            first[p] = make_float2(inv, __int_as_float(hs << 23));
-            second[p] = make_float2(0.f, __int_as_float((254 - hs) << 23));
-        }
+        for (int i = 0; i < 8; ++i) ss += red[i];
+        // exponent of the hidden row's bound, x's own scale taken out
+        const float b = ss * at.y;
+        const int e = ((__float_as_int(b) >> 23) & 255) - 127 - 2 * (se - 127);
+        int hs = 127 + 14 - e;
+        if (b == 0.f) hs = 127;
+        hs = hs < 1 ? 1 : hs > 253 ? 253 : hs;
+        const float inv = __int_as_float((254 - se) << 23);
+        first[pos] = make_float2(inv, __int_as_float(hs << 23));
+        second[pos] = make_float2(0.f, __int_as_float((254 - hs) << 23));
     }
 }
 
@@ -712,9 +744,9 @@ size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
 
-// f16 rows of x and of the hidden values by position, and two scales each.
+// f16 rows of x and of the hidden values and two pairs of scales by position; a position and a bound by slot.
 size_t moe_tensor_scratch(int64_t nslots, int64_t D, int64_t F) {
-    return round256((size_t)nslots * D * 2) + round256((size_t)nslots * F * 2) + 2 * round256((size_t)nslots * 8);
+    return round256((size_t)nslots * D * 2) + round256((size_t)nslots * F * 2) + 3 * round256((size_t)nslots * 8);
 }
 
 cudaError_t launch_moe_tensor(const MoeTensor& m, void* scratch, cudaStream_t st) {
@@ -727,21 +759,22 @@ cudaError_t launch_moe_tensor(const MoeTensor& m, void* scratch, cudaStream_t st
     float2* first = reinterpret_cast<float2*>(at);
     at += round256((size_t)S * 8);
     float2* second = reinterpret_cast<float2*>(at);
-    int64_t grid = (S + 7) / 8;
-    if (grid > 152 * 16) grid = 152 * 16;
-    const int vec = (reinterpret_cast<uintptr_t>(m.x) & 15) == 0 && m.ldx % 8 == 0;
-    cudaError_t e;
+    at += round256((size_t)S * 8);
+    float2* where = reinterpret_cast<float2*>(at);
     const int E = (int)m.gate->E;
+    const unsigned T = (unsigned)(S / m.k);
+    const int vec = (reinterpret_cast<uintptr_t>(m.x) & 15) == 0 && m.ldx % 8 == 0;
+    cudaError_t e = launch_pdl(moe_where_kernel, dim3((unsigned)((S + 255) / 256)), dim3(256), 0, st, m.offsets,
+                               m.slots, (int)S, E, static_cast<const float*>(m.gate->bound),
+                               static_cast<const float*>(m.up->bound), where);
+    if (e != cudaSuccess) return e;
     if (m.dtype == TQ2_F16)
-        e = launch_pdl(moe_stage_kernel<__half>, dim3((unsigned)grid), dim3(256), 0, st,
-                       static_cast<const __half*>(m.x), m.ldx, vec, (int)D, m.offsets, m.slots, (int)S, m.k, E,
-                       static_cast<const float*>(m.gate->bound), static_cast<const float*>(m.up->bound), xs, first,
-                       second);
+        e = launch_pdl(moe_stage_kernel<__half>, dim3(T), dim3(256), 0, st, static_cast<const __half*>(m.x), m.ldx,
+                       vec, (int)D, m.ids, static_cast<const float2*>(where), (int)S, m.k, xs, first, second);
     else
-        e = launch_pdl(moe_stage_kernel<__nv_bfloat16>, dim3((unsigned)grid), dim3(256), 0, st,
-                       static_cast<const __nv_bfloat16*>(m.x), m.ldx, vec, (int)D, m.offsets, m.slots, (int)S, m.k, E,
-                       static_cast<const float*>(m.gate->bound), static_cast<const float*>(m.up->bound), xs, first,
-                       second);
+        e = launch_pdl(moe_stage_kernel<__nv_bfloat16>, dim3(T), dim3(256), 0, st,
+                       static_cast<const __nv_bfloat16*>(m.x), m.ldx, vec, (int)D, m.ids,
+                       static_cast<const float2*>(where), (int)S, m.k, xs, first, second);
     if (e != cudaSuccess) return e;
     MuMaps xmaps, hmaps;
     if (!row_maps(xmaps, xs, D, S) || !row_maps(hmaps, hid, F, S)) return cudaErrorInvalidValue;

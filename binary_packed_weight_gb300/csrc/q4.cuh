@@ -174,6 +174,7 @@ struct MoeTensor {
     const void* x;
     int64_t ldx;
     int dtype;
+    const int* ids;
     const int* offsets;
     const int* slots;
     int nslots, k;

@@ -342,7 +342,7 @@ tq2_status moe_experts(q4_handle gate, q4_handle up, q4_handle down, const void*
             mem.p = nullptr;
             return cuda_status(e, "moe_experts: scratch");
         }
-        const MoeTensor m{gate, up, down, x, ldx, dtype, offsets, slots, (int)S, k, static_cast<float*>(mem.p)};
+        const MoeTensor m{gate, up, down, x, ldx, dtype, ids, offsets, slots, (int)S, k, static_cast<float*>(mem.p)};
         e = launch_moe_tensor(m, static_cast<char*>(mem.p) + ybytes, st);
         if (e == cudaSuccess) e = combine(m.y);
         return cuda_status(e, "moe_experts: tensor path");
