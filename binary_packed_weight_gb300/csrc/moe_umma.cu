@@ -10,9 +10,10 @@
 //   * warps 0 and 2 stream the activations (B, 128-byte swizzle) by TMA, the first
 //     and the second 64 k of a stage (one warp takes ~650 cycles a slot);
 //   * warp 3 streams the packed blocks of 256 k by bulk copies;
-//   * two or three groups of four decoder warps, which take turns, decode a
-//     block's rows, one weight row a thread, and store them as the A operand in
-//     tensor memory (rounding (c - z) d to f16 is the only rounding of the weights);
+//   * two or three groups of four decoder warps, which take every second or third
+//     stage, decode a block's rows, one weight row a thread, and store them as the A
+//     operand in tensor memory (rounding (c - z) d to f16 is the only rounding of
+//     the weights);
 //   * warp 1 issues the MMAs; one barrier a stage covers both operands, and the
 //     next stage's is tested while this stage's MMAs run;
 //   * eight or sixteen epilogue warps drain the finished tile, some columns each in
@@ -167,7 +168,7 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
         }
         for (int r = 0; r < MU_RAW; ++r) {
             mbar_init(&bars->raw_full[r], 1);
-            mbar_init(&bars->raw_empty[r], 4 * MU_GROUPS); // every decoder warp
+            mbar_init(&bars->raw_empty[r], 8);             // the decoder warps of its two stages
         }
         mbar_init(&bars->acc_full, 1);
         mbar_init(&bars->acc_empty, DRAIN);                    // every epilogue warp
@@ -407,80 +408,94 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
         const int b = PAIR ? (lane >> 4) * 4 + q : q * 2 + (lane >> 4);
         const uint32_t expo = q4_exponent<false>();
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16) + MU_ACOL;
-        Ring<MU_RAW> r;
+        // The stage at hand: of tile i, `st` of its stages; its packed block is the CTA's item `item`, in slot rs.
         MuStages<WIDE> f;
-        int turn = (warp - 4) >> 2;                        // stages until this group's next one
-        uint32_t drains = 0;
-        bool ok = true;
-        for (int i = 0; i < mine && ok; ++i) {
-            bool owed = f.begin(tile_at(i).cnt) > f.lowest;   // a wait before this tile's first store
-            for (int kc = 0; kc * 4 < a.nk && ok; ++kc, r.next()) {
-                if (!mbar_wait_or_abort(&bars->raw_full[r.s], r.ph, abort_flag)) {
-                    *abort_flag = 1;
-                    ok = false;
-                    break;
-                }
-                const uint8_t* src = raw_ring + (size_t)r.s * 8 * blk + b * blk;
-                const uint8_t* sc = src + Q4_CODES + q4_scale_index(row, 0, NG) * 2;
-                const uint8_t* zp = src + Q4_CODES + 32 * NG + q4_scale_index(row, 0, NG);
-                for (int c2 = 0; c2 < 2 && kc * 4 + c2 * 2 < a.nk; ++c2, f.next()) {
-                    if (turn-- > 0) continue;
-                    turn = MU_GROUPS - 1;
-                    // (an odd last stage's second half is decoded from the block's padding and not used)
-                    uint2 w[2][4];
-#pragma unroll
-                    for (int at = 0; at < 2; ++at)
-#pragma unroll
-                        for (int tt = 0; tt < 4; ++tt)
-                            w[at][tt] = *reinterpret_cast<const uint2*>(src + (c2 * 2 + at) * 512 + (tt * 8 + g) * 16 +
-                                                                        hi * 8);
-#pragma unroll
-                    for (int at = 0; at < 2; ++at) {       // two chunks of 64 k
-                        const int c = c2 * 2 + at;
-                        uint32_t v[32];
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const int gi = (c * 2 + half) / (G / 32);
-                            const __half2 d = __half2half2(*reinterpret_cast<const __half*>(sc + gi * 4));
-                            const Q4Zero z = q4_zero<false>(a.zeros ? zp[gi * 2] : 8u);
-#pragma unroll
-                            for (int tt = 0; tt < 4; ++tt) {
-                                uint32_t p[4];
-                                q4_decode<false>(half ? w[at][tt].y : w[at][tt].x, expo, z, p);
-#pragma unroll
-                                for (int x = 0; x < 4; ++x) {
-                                    const __half2 m = __hmul2(*reinterpret_cast<const __half2*>(&p[x]), d);
-                                    v[16 * half + 4 * tt + x] = *reinterpret_cast<const uint32_t*>(&m);
-                                }
-                            }
-                        }
-                        if (at == 0) {
-                            if (owed) {
-                                ok = mbar_wait_or_abort(&bars->drained, drains & 1u, abort_flag);
-                                ++drains;
-                                owed = false;
-                            }
-                            // (passes at a stage's first use)
-                            if (!ok || !mbar_wait_or_abort(&bars->empty[f.s], f.parity() ^ 1u, abort_flag)) {
-                                *abort_flag = 1;
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                        }
-                        tmem_st_32x32b_x32(lane_addr + (uint32_t)(f.s * 64 + at * 32), v);
-                    }
-                    if (!ok) break;
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->full[f.s]);
-                }
-                // the values are used: the slot is refilled through the async proxy
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->raw_empty[r.s]);
+        int i = 0, st = 0, base = 0, item = 0, rs = 0;
+        uint32_t rph = 0, drains = 0;
+        bool ok = true, owed = false;                      // owed: a wait for `drained`
+        if (mine > 0) f.begin(tile_at(0).cnt);
+        auto advance = [&] {                               // by one stage
+            f.next();
+            if (++st == stages) {
+                st = 0;
+                base += (stages + 1) / 2;
+                ++i;
+                if (WIDE && i < mine) owed = f.begin(tile_at(i).cnt) > f.lowest || owed;
             }
+        };
+        auto settle = [&] {
+            const int now = base + (st >> 1);
+            rs += now - item;
+            item = now;
+            if (rs >= MU_RAW) {                            // (an item or two were the other groups')
+                rs -= MU_RAW;
+                rph ^= 1u;
+            }
+        };
+        for (int x = (warp - 4) >> 2; x > 0; --x) advance();
+        settle();
+        while (i < mine) {
+            // The stage first, then its packed block: MMAs of four stages ago are past the slot's last block, so
+            // that the parity waited for is the right one's.  (The first passes at a stage's first use.)
+            if (owed) {
+                ok = mbar_wait_or_abort(&bars->drained, drains & 1u, abort_flag);
+                ++drains;
+                owed = false;
+            }
+            if (!ok || !mbar_wait_or_abort(&bars->empty[f.s], f.parity() ^ 1u, abort_flag) ||
+                !mbar_wait_or_abort(&bars->raw_full[rs], rph, abort_flag)) {
+                *abort_flag = 1;
+                break;
+            }
+            tc_fence_after();
+            const int c2 = st & 1;
+            const uint8_t* src = raw_ring + (size_t)rs * 8 * blk + b * blk;
+            const uint8_t* sc = src + Q4_CODES + q4_scale_index(row, 0, NG) * 2;
+            const uint8_t* zp = src + Q4_CODES + 32 * NG + q4_scale_index(row, 0, NG);
+            // (an odd last stage's second half is decoded from the block's padding and not used)
+            uint2 w[2][4];
+#pragma unroll
+            for (int at = 0; at < 2; ++at)
+#pragma unroll
+                for (int tt = 0; tt < 4; ++tt)
+                    w[at][tt] = *reinterpret_cast<const uint2*>(src + (c2 * 2 + at) * 512 + (tt * 8 + g) * 16 +
+                                                                hi * 8);
+#pragma unroll
+            for (int at = 0; at < 2; ++at) {               // two chunks of 64 k
+                const int c = c2 * 2 + at;
+                uint32_t v[32];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int gi = (c * 2 + half) / (G / 32);
+                    const __half2 d = __half2half2(*reinterpret_cast<const __half*>(sc + gi * 4));
+                    const Q4Zero z = q4_zero<false>(a.zeros ? zp[gi * 2] : 8u);
+#pragma unroll
+                    for (int tt = 0; tt < 4; ++tt) {
+                        uint32_t p[4];
+                        q4_decode<false>(half ? w[at][tt].y : w[at][tt].x, expo, z, p);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const __half2 m = __hmul2(*reinterpret_cast<const __half2*>(&p[x]), d);
+                            v[16 * half + 4 * tt + x] = *reinterpret_cast<const uint32_t*>(&m);
+                        }
+                    }
+                }
+                tmem_st_32x32b_x32(lane_addr + (uint32_t)(f.s * 64 + at * 32), v);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            // the packed values are used: the slot is refilled through the async proxy
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars->full[f.s]);
+                mbar_arrive(&bars->raw_empty[rs]);
+                // (a last block of one stage has one group)
+                if ((stages & 1) && st == stages - 1) mbar_arrive(&bars->raw_empty[rs]);
+            }
+#pragma unroll
+            for (int x = 0; x < MU_GROUPS; ++x) advance();
+            settle();
         }
     } else if (warp >= MU_EPI) {                           // ---- epilogue: CW columns in turn
         const int q = warp & 3, b = (warp - MU_EPI) >> 2;
@@ -732,7 +747,8 @@ template <bool PAIR>
 cudaError_t launch_by_group(int group, const MuMaps& maps, const MuArgs& a, cudaStream_t st) {
     // wide tiles from 120 rows a matrix on average (64 experts of 2048x1024, 96 / 128 rows each: narrow 130 / 146
     // us, wide 137 / 144)
-    const bool wide = a.nslots >= 120 * (int64_t)a.E;
+    // (two groups of decoders need blocks of two stages: a slot's last block must have been theirs or the MMAs')
+    const bool wide = a.nslots >= 120 * (int64_t)a.E && a.nk > 2;
     if (group == 32)
         return wide ? launch_umma_moe<32, PAIR, true>(maps, a, st) : launch_umma_moe<32, PAIR, false>(maps, a, st);
     if (group == 64)
