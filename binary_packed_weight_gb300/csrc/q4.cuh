@@ -103,11 +103,12 @@ __device__ __forceinline__ void q4_decode(uint32_t w, uint32_t m, const Q4Zero& 
 }
 
 // A plan's values, kept inside their ranges whatever it holds.
+// (Read from L2: a kernel that starts before the one ahead of it has ended may read a plan.)
 __device__ __forceinline__ int plan_offset(const int* offsets, int nslots, int e) {
-    return min(max(offsets[e], 0), nslots);
+    return min(max(__ldcg(offsets + e), 0), nslots);
 }
 __device__ __forceinline__ int plan_slot(const int* slots, int nslots, int p) {
-    return min(max(slots[p], 0), nslots - 1);
+    return min(max(__ldcg(slots + p), 0), nslots - 1);
 }
 
 }  // namespace tq2
@@ -159,6 +160,7 @@ struct Q4Stream {
     int xdiv;                          // x row of position p: slots[p] / xdiv; 0: p itself
     int oslot;                         // out row of position p: slots[p]; 0: p itself
     int tokens;                        // rows expected of one matrix at most (sizes the column tiles)
+    int after;                         // the last kernel of the stream is a product over the same plan
 };
 cudaError_t launch_q4_stream(const Q4Stream& a, cudaStream_t st);
 cudaError_t launch_q4_stream_g32(const Q4Stream& a, cudaStream_t st);

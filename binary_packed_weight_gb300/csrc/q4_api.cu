@@ -387,6 +387,7 @@ tq2_status moe_experts(q4_handle gate, q4_handle up, q4_handle down, const void*
     b.slots = slots;
     b.nslots = (int)S;
     b.tokens = a.tokens;
+    b.after = 1;
     e = launch_q4_stream(b, st);
     if (e != cudaSuccess) return cuda_status(e, "moe_experts: down");
     e = combine(y);

@@ -287,13 +287,15 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
         fence_proxy_async_shared();
     }
     __syncthreads();
+    // The plan may be the last kernel's.  Where that is the product before this one, the plan is older and read at
+    // once: that product lets this one start only when it has waited for the plan itself.
+    if (PLAN && !a.after) pdl_wait();
     pdl_launch_dependents();
 
     // the CTA's tiles (whole units: a tile, or a pair of them)
     const int two = PLAN && a.pair ? 2 : 1;
     int u0, u1;
     if (PLAN) {
-        pdl_wait();                                        // the plan is an earlier kernel's
         int* offs = prefix + a.E + 1;
         for (int e = tid; e <= a.E; e += Q4_WARPS * 32) offs[e] = q4_offset(a, e);
         if (k.off_slots && tid < a.nslots) reinterpret_cast<int*>(smem + k.off_slots)[tid] = q4_slot(a, tid);
@@ -339,7 +341,10 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
         u0 = b * k.each + min(b, k.more);
         u1 = u0 + k.each + (b < k.more ? 1 : 0);
     }
-    if (u0 >= u1) return;                                  // uniform; the plan's wait is done
+    if (u0 >= u1) {                                        // uniform
+        if (PLAN && a.after) pdl_wait();                   // (a kernel never ends before the ones it follows)
+        return;
+    }
 
     // The tiles of one pass; warp w takes their blocks L*w/16 .. L*(w+1)/16.
     struct Batch {
@@ -374,7 +379,7 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_stream_kernel(const __gri
     Batch b = batch_at(u0);
     Q4Block<G> cur;
     if (b.i0 < b.i1) cur.load(first_ptr(b), lane, a.zeros);
-    if (!PLAN) pdl_wait();                                 // x is an earlier kernel's; the weights are not
+    if (!PLAN || a.after) pdl_wait();                      // x is the last kernel's; the weights are not
 
     const uint32_t expo = q4_exponent<BF>();
     uint32_t xphase = 0;
