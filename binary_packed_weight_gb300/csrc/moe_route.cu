@@ -170,15 +170,19 @@ __device__ __forceinline__ void merge_two(float& a1, float& a2, float b1, float 
 
 // Positions of this CTA's slots (n of them from slot s0, expert ids at
 // `ids`), CTA-size slots at a time; base[e] is the next position of expert e.
-// cnt: uint16 [warps][E] in shared memory.
+// cnt: uint16 [warps][E] in shared memory; ready: it is zero, and `first` is this
+// thread's id of the first round.
 __device__ __forceinline__ void place_slots(const int32_t* ids, int64_t s0, int n, int E, int* base, uint16_t* cnt,
-                                            int32_t* slots) {
+                                            int32_t* slots, bool ready, int first) {
     const int tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31, nw = nt >> 5;
     for (int i0 = 0; i0 < n; i0 += nt) {
-        for (int i = tid; i < (nw * E + 1) / 2; i += nt) reinterpret_cast<uint32_t*>(cnt)[i] = 0;
-        __syncthreads();
         const int i = i0 + tid;
-        const int e = i < n ? ids[i] : -1;
+        int e = first;
+        if (i0 > 0 || !ready) {
+            for (int x = tid; x < (nw * E + 1) / 2; x += nt) reinterpret_cast<uint32_t*>(cnt)[x] = 0;
+            __syncthreads();
+            e = i < n ? ids[i] : -1;
+        }
         const uint32_t same = __match_any_sync(0xffffffffu, e);
         const int rank = __popc(same & ((1u << lane) - 1u));
         if (e >= 0 && rank == 0) cnt[warp * E + e] = (uint16_t)__popc(same);
@@ -436,7 +440,7 @@ __global__ void __launch_bounds__(V <= 8 ? 1024 : 256) moe_route_kernel(const __
     for (int e = tid; e < a.E; e += nt) base[e] += before[e];
     __syncthreads();
     // the ids were written by this CTA's own warps (ordered by the barriers above)
-    if (t1 > t0) place_slots(a.ids + t0 * a.k, t0 * a.k, (int)((t1 - t0) * a.k), a.E, base, cnt, a.slots);
+    if (t1 > t0) place_slots(a.ids + t0 * a.k, t0 * a.k, (int)((t1 - t0) * a.k), a.E, base, cnt, a.slots, false, -1);
 }
 
 // Second kernel of the plan: CTA b places the slots of chunk b.  Shared
@@ -459,8 +463,12 @@ __global__ void __launch_bounds__(1024) moe_plan_kernel(const int32_t* __restric
         base[i] = 0;
         before[i] = 0;
     }
+    for (int i = tid; i < ((nt >> 5) * E + 1) / 2; i += nt) reinterpret_cast<uint32_t*>(cnt)[i] = 0;
     __syncthreads();
     pdl_wait();
+    const int64_t t0 = (int64_t)b * chunk, t1 = t0 + chunk < T ? t0 + chunk : T;
+    const int n = (int)((t1 - t0) * k);
+    const int first = tid < n ? ids[t0 * k + tid] : -1;
     // column sums of the counts, many loads in flight: as many threads to a column as fit
     const int rows = nt / words;
     if (tid < words * rows) {
@@ -497,8 +505,7 @@ __global__ void __launch_bounds__(1024) moe_plan_kernel(const int32_t* __restric
     __syncthreads();
     for (int i = tid; i < E; i += nt) base[i] += before[i];
     __syncthreads();
-    const int64_t t0 = (int64_t)b * chunk, t1 = t0 + chunk < T ? t0 + chunk : T;
-    place_slots(ids + t0 * k, t0 * k, (int)((t1 - t0) * k), E, base, cnt, slots);
+    place_slots(ids + t0 * k, t0 * k, n, E, base, cnt, slots, true, first);
 }
 
 struct RouteBackArgs {
