@@ -49,20 +49,24 @@ namespace {
 template <bool WIDE>
 struct MuShape {
     static constexpr int GROUPS = WIDE ? 2 : 3;
+    static constexpr int HALF = WIDE ? 1 : 2;              // chunks of 64 k in half a stage
+    static constexpr int STAGES = WIDE ? 4 : 3;            // stages of weights in tensor memory
+    static constexpr int BN = WIDE ? 384 : 128;            // positions of a tile at most
+    static constexpr int ACOL = WIDE ? 256 : 128;          // first tensor-memory column of the stages
+    static constexpr int BLOCK_STAGES = 2 / HALF;          // stages of a packed block
+    static constexpr int SLOTS = WIDE ? 5 : 4;             // activation slots (half a stage) of 32 KB
+    static __host__ __device__ constexpr int raw(int G) { return WIDE ? 3 : G == 32 ? 4 : 5; }   // packed blocks of 256 k in their ring
     static constexpr int EPI = 4 + 4 * GROUPS;             // first epilogue warp
     static constexpr int DRAIN = WIDE ? 16 : 8;            // epilogue warps
     static constexpr int THREADS = 32 * (EPI + DRAIN);
     static constexpr int CW = 16;
 };
-constexpr int MU_BN = 384;                 // positions of a tile at most
-constexpr int MU_B = 160 * 1024;           // bytes of the activation ring
-constexpr int MU_A = 4;                    // stages of 128 k: decoded weights (64 tensor-memory columns each)
-constexpr int MU_RAW = 3;                  // packed blocks of 256 k
-constexpr int MU_ACOL = 256;               // first tensor-memory column of the A stages
+constexpr int MU_A = 4;                    // stages of decoded weights at most
+constexpr int MU_RAW = 5;                  // packed blocks of 256 k in their ring at most
 constexpr int MU_LIST = 64;                // tiles of a CTA that are looked up ahead
 
-// Activation rows in boxes of 32, 64, 128 and 256: a tile is loaded in at most
-// three copies a slot.
+// Activation rows in boxes of 32, 64, 128 and 256 (at most three copies a slot of
+// a wide tile), or of 32, 64, 96 and 128 (one copy a chunk of a narrow one).
 struct MuMaps {
     CUtensorMap box[4];
 };
@@ -77,7 +81,7 @@ struct MuBars {
     uint32_t tmem_base;
     int abort;
     MuTile list[MU_LIST];
-    float2 scale[MU_BN];                   // epilogue: a tile's scales (or output rows and scales)
+    float2 scale[384];                     // epilogue: a tile's scales (or output rows and scales)
 };
 
 // The stage at hand and the parities of its barriers' phases.  A tile of more
@@ -102,11 +106,11 @@ struct MuStages {
     }
     __device__ __forceinline__ void next() {
         used ^= 1u << s;
-        s = s + 1 == MU_A ? (WIDE ? lowest : 0) : s + 1;
+        s = s + 1 == MuShape<WIDE>::STAGES ? (WIDE ? lowest : 0) : s + 1;
     }
     __device__ __forceinline__ uint32_t parity() const { return (used >> s) & 1u; }
-    // Activation slots of 64 k in the ring, and their bytes.
-    __device__ __forceinline__ int slots() const { return WIDE ? 5 - lowest : 5; }
+    // Activation slots (half a stage) in the ring, and their bytes.
+    __device__ __forceinline__ int slots() const { return WIDE ? MuShape<WIDE>::SLOTS - lowest : MuShape<WIDE>::SLOTS; }
     __device__ __forceinline__ uint32_t slot_bytes() const { return WIDE ? 32768u + 8192u * (uint32_t)lowest : 32768u; }
 };
 
@@ -132,7 +136,8 @@ struct MuArgs {
     int nkc, zeros, E, nslots;
     int N;                                 // output columns (F, or D)
     int row_tiles;                         // tiles along them
-    int nk;                                // 64-k slots of a tile
+    int K;
+    int nk;                                // slots (half stages) of a tile
     int bn;                                // positions of a tile at most
     const int* offsets;
     const int* slots;
@@ -150,13 +155,15 @@ __global__ void __launch_bounds__(MuShape<WIDE>::THREADS, 1)
 moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     constexpr int NG = Q4_K / G;
+    constexpr int HALF = MuShape<WIDE>::HALF, ACOL = MuShape<WIDE>::ACOL, BLOCK_STAGES = MuShape<WIDE>::BLOCK_STAGES;
     constexpr int MU_GROUPS = MuShape<WIDE>::GROUPS, MU_EPI = MuShape<WIDE>::EPI, MU_THREADS = MuShape<WIDE>::THREADS;
     constexpr int CW = MuShape<WIDE>::CW, DRAIN = MuShape<WIDE>::DRAIN;
     constexpr int STEP = CW * DRAIN / 4;                   // columns that the epilogue warps of a quarter take in turn
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int blk = q4_block_bytes(G, a.zeros != 0);
-    uint8_t* raw_ring = smem + MU_B;
-    MuBars* bars = reinterpret_cast<MuBars*>(raw_ring + MU_RAW * 8 * blk);
+    constexpr int RAW = MuShape<WIDE>::raw(G);
+    uint8_t* raw_ring = smem + MuShape<WIDE>::SLOTS * 32768;
+    MuBars* bars = reinterpret_cast<MuBars*>(raw_ring + RAW * 8 * blk);
     int* prefix = reinterpret_cast<int*>(bars + 1);        // token tiles before each matrix
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -166,9 +173,9 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
             mbar_init(&bars->empty[s], 1);                 // the MMA warp's commits: a stage, its first 64 k
             mbar_init(&bars->half_empty[s], 1);
         }
-        for (int r = 0; r < MU_RAW; ++r) {
+        for (int r = 0; r < RAW; ++r) {
             mbar_init(&bars->raw_full[r], 1);
-            mbar_init(&bars->raw_empty[r], 8);             // the decoder warps of its two stages
+            mbar_init(&bars->raw_empty[r], 4 * BLOCK_STAGES);   // the decoder warps of its stages
         }
         mbar_init(&bars->acc_full, 1);
         mbar_init(&bars->acc_empty, DRAIN);                    // every epilogue warp
@@ -234,7 +241,7 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
     for (int i = tid; i < min(mine, MU_LIST); i += MU_THREADS) bars->list[i] = find_tile(blockIdx.x + i * gridDim.x);
     __syncthreads();
     auto tile_at = [&](int i) { return i < MU_LIST ? bars->list[i] : find_tile(blockIdx.x + i * gridDim.x); };
-    const int stages = (a.nk + 1) / 2;                     // of 128 k, the last one maybe of 64
+    const int stages = (a.nk + 1) / 2;                     // the last one maybe a half
 
     if (warp == 0 || warp == 2) {                          // ---- activations
         pdl_wait();
@@ -279,17 +286,23 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
                     uint64_t* bar = &bars->full[f.s];
                     armed |= 1u << f.s;
                     parity = (parity & ~(1u << f.s)) | f.parity() << f.s;
-                    mbar_arrive_expect_tx(bar, there ? (uint32_t)boxes * 4096u : 0u);
+                    mbar_arrive_expect_tx(bar, there ? (uint32_t)boxes * (4096u * HALF) : 0u);
                     if (there) {
                         uint8_t* dst = smem + (uint32_t)slot * bytes;
-                        int row = m.p0;
+                        const int k0 = (2 * st + half) * (64 * HALF);
+                        if (WIDE) {
+                            int row = m.p0;
 #pragma unroll
-                        for (int x = 3; x >= 0; --x)
-                            if (boxes & (1 << x)) {
-                                tma_load_2d(dst, &maps.box[x], bar, (2 * st + half) * 64, row);
-                                dst += 4096 << x;
-                                row += 32 << x;
-                            }
+                            for (int x = 3; x >= 0; --x)
+                                if (boxes & (1 << x)) {
+                                    tma_load_2d(dst, &maps.box[x], bar, k0, row);
+                                    dst += 4096 << x;
+                                    row += 32 << x;
+                                }
+                        } else {                           // (a chunk past the row's end is zeros)
+                            tma_load_2d(dst, &maps.box[boxes - 1], bar, k0, m.p0);
+                            tma_load_2d(dst + boxes * 4096, &maps.box[boxes - 1], bar, k0 + 64, m.p0);
+                        }
                     }
                     slot += 2;
                     slot -= slot >= slots ? slots : 0;
@@ -309,7 +322,7 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
         __syncwarp();
     } else if (warp == 3) {
         if (elect_one()) {                                 // ---- packed blocks
-            Ring<MU_RAW> r;
+            Ring<RAW> r;
             bool ok = true;
             const uint32_t bytes = 8u * (uint32_t)blk;
             for (int i = 0; i < mine && ok; ++i) {
@@ -317,7 +330,7 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
                 // first of the tile's blocks of a chunk: 8 row tiles of one matrix, or 4 of each of two
                 const int rt = PAIR ? m.r * 4 : m.r * 8;
                 const int64_t first = (int64_t)m.e * a.mstride + q4_block_index(rt, 0, a.nkc) * blk;
-                for (int kc = 0; kc * 4 < a.nk; ++kc, r.next()) {
+                for (int kc = 0; kc < a.nkc; ++kc, r.next()) {
                     if (!r.first && !mbar_wait_or_abort(&bars->raw_empty[r.s], r.ph ^ 1u, abort_flag)) {
                         *abort_flag = 1;
                         ok = false;
@@ -335,7 +348,7 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
                 }
             }
             if (!ok)
-                for (int i = 0; i < MU_RAW; ++i)
+                for (int i = 0; i < RAW; ++i)
                     mbar_wait(&bars->raw_full[i], i < r.s ? r.ph : r.ph ^ 1u);
         }
     } else if (warp == 1) {                                // ---- MMA issuer
@@ -347,6 +360,7 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
             for (int i = 0; i < mine && ok; ++i) {
                 // more than 256 positions are two MMAs side by side
                 const int n16 = (cnt + 15) / 16 * 16, n1 = WIDE && cnt > 256 ? (n16 / 16 + 1) / 2 * 16 : n16, n2 = n16 - n1;
+                const int boxes = (cnt + 31) / 32;
                 const uint32_t idesc = idesc_f16_f32(128, (uint32_t)n1), idesc2 = idesc_f16_f32(128, (uint32_t)n2);
                 if (i > 0) {
                     if (!mbar_wait_or_abort(&bars->acc_empty, (uint32_t)(i - 1) & 1u, abort_flag, true)) {
@@ -372,15 +386,18 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
                     // (its latency hides under the MMAs below)
                     ready = st + 1 < stages && mbar_test_wait(&bars->full[g.s], g.parity());
                     tc_fence_after();
-                    const uint32_t acol = tmem + MU_ACOL + (uint32_t)(f.s * 64);
+                    const uint32_t acol = tmem + ACOL + (uint32_t)(f.s * 64 * HALF);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (h == 0 || 2 * st + 1 < a.nk) {
                             const uint64_t bdesc = sdesc_kmajor_sw128(smem_u32(smem + (uint32_t)slot * bytes));
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                umma_f16_ts(tmem, acol + (uint32_t)(h * 32 + j * 8), bdesc + (uint64_t)(2 * j), idesc,
-                                            (st > 0 || h > 0 || j > 0) ? 1u : 0u);
+                            for (int c = 0; c < HALF; ++c)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    umma_f16_ts(tmem, acol + (uint32_t)((h * HALF + c) * 32 + j * 8),
+                                                bdesc + (uint64_t)(2 * j) + (uint64_t)(c * boxes * 256), idesc,
+                                                (st > 0 || h > 0 || c > 0 || j > 0) ? 1u : 0u);
                             if (WIDE && n2) {
 #pragma unroll
                                 for (int j = 0; j < 4; ++j)
@@ -407,7 +424,7 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
         const int row = lane & 15, g = row & 7, hi = row >> 3;
         const int b = PAIR ? (lane >> 4) * 4 + q : q * 2 + (lane >> 4);
         const uint32_t expo = q4_exponent<false>();
-        const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16) + MU_ACOL;
+        const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16) + ACOL;
         // The stage at hand: of tile i, `st` of its stages; its packed block is the CTA's item `item`, in slot rs.
         MuStages<WIDE> f;
         int i = 0, st = 0, base = 0, item = 0, rs = 0;
@@ -418,24 +435,24 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
             f.next();
             if (++st == stages) {
                 st = 0;
-                base += (stages + 1) / 2;
+                base += a.nkc;
                 ++i;
                 if (WIDE && i < mine) owed = f.begin(tile_at(i).cnt) > f.lowest || owed;
             }
         };
         auto settle = [&] {
-            const int now = base + (st >> 1);
+            const int now = base + st / BLOCK_STAGES;
             rs += now - item;
             item = now;
-            if (rs >= MU_RAW) {                            // (an item or two were the other groups')
-                rs -= MU_RAW;
+            if (rs >= RAW) {                               // (an item or two were the other groups')
+                rs -= RAW;
                 rph ^= 1u;
             }
         };
         for (int x = (warp - 4) >> 2; x > 0; --x) advance();
         settle();
         while (i < mine) {
-            // The stage first, then its packed block: MMAs of four stages ago are past the slot's last block, so
+            // The stage first, then its packed block: the MMAs of its last use are past the slot's last block, so
             // that the parity waited for is the right one's.  (The first passes at a stage's first use.)
             if (owed) {
                 ok = mbar_wait_or_abort(&bars->drained, drains & 1u, abort_flag);
@@ -448,39 +465,41 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
                 break;
             }
             tc_fence_after();
-            const int c2 = st & 1;
             const uint8_t* src = raw_ring + (size_t)rs * 8 * blk + b * blk;
             const uint8_t* sc = src + Q4_CODES + q4_scale_index(row, 0, NG) * 2;
             const uint8_t* zp = src + Q4_CODES + 32 * NG + q4_scale_index(row, 0, NG);
-            // (an odd last stage's second half is decoded from the block's padding and not used)
-            uint2 w[2][4];
+            // (a last stage's missing second half is decoded from the block's padding and not used)
 #pragma unroll
-            for (int at = 0; at < 2; ++at)
+            for (int h = 0; h < HALF; ++h) {
+                const int c0 = 2 * h + (BLOCK_STAGES == 2 ? 2 * (st & 1) : 0);   // two chunks of 64 k
+                uint2 w[2][4];
 #pragma unroll
-                for (int tt = 0; tt < 4; ++tt)
-                    w[at][tt] = *reinterpret_cast<const uint2*>(src + (c2 * 2 + at) * 512 + (tt * 8 + g) * 16 +
-                                                                hi * 8);
+                for (int at = 0; at < 2; ++at)
 #pragma unroll
-            for (int at = 0; at < 2; ++at) {               // two chunks of 64 k
-                const int c = c2 * 2 + at;
-                uint32_t v[32];
+                    for (int tt = 0; tt < 4; ++tt)
+                        w[at][tt] = *reinterpret_cast<const uint2*>(src + (c0 + at) * 512 + (tt * 8 + g) * 16 + hi * 8);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int gi = (c * 2 + half) / (G / 32);
-                    const __half2 d = __half2half2(*reinterpret_cast<const __half*>(sc + gi * 4));
-                    const Q4Zero z = q4_zero<false>(a.zeros ? zp[gi * 2] : 8u);
+                for (int at = 0; at < 2; ++at) {
+                    const int c = c0 + at;
+                    uint32_t v[32];
 #pragma unroll
-                    for (int tt = 0; tt < 4; ++tt) {
-                        uint32_t p[4];
-                        q4_decode<false>(half ? w[at][tt].y : w[at][tt].x, expo, z, p);
+                    for (int half = 0; half < 2; ++half) {
+                        const int gi = (c * 2 + half) / (G / 32);
+                        const __half2 d = __half2half2(*reinterpret_cast<const __half*>(sc + gi * 4));
+                        const Q4Zero z = q4_zero<false>(a.zeros ? zp[gi * 2] : 8u);
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const __half2 m = __hmul2(*reinterpret_cast<const __half2*>(&p[x]), d);
-                            v[16 * half + 4 * tt + x] = *reinterpret_cast<const uint32_t*>(&m);
+                        for (int tt = 0; tt < 4; ++tt) {
+                            uint32_t p[4];
+                            q4_decode<false>(half ? w[at][tt].y : w[at][tt].x, expo, z, p);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const __half2 m = __hmul2(*reinterpret_cast<const __half2*>(&p[x]), d);
+                                v[16 * half + 4 * tt + x] = *reinterpret_cast<const uint32_t*>(&m);
+                            }
                         }
                     }
+                    tmem_st_32x32b_x32(lane_addr + (uint32_t)(f.s * 64 * HALF + (2 * h + at) * 32), v);
                 }
-                tmem_st_32x32b_x32(lane_addr + (uint32_t)(f.s * 64 + at * 32), v);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -491,7 +510,7 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
                 mbar_arrive(&bars->full[f.s]);
                 mbar_arrive(&bars->raw_empty[rs]);
                 // (a last block of one stage has one group)
-                if ((stages & 1) && st == stages - 1) mbar_arrive(&bars->raw_empty[rs]);
+                if (BLOCK_STAGES == 2 && (stages & 1) && st == stages - 1) mbar_arrive(&bars->raw_empty[rs]);
             }
 #pragma unroll
             for (int x = 0; x < MU_GROUPS; ++x) advance();
@@ -721,11 +740,12 @@ moe_stage_kernel(const T* __restrict__ x, int64_t ldx, int vec, int D, const int
 template <int G, bool PAIR, bool WIDE>
 cudaError_t launch_umma_moe(const MuMaps& maps, MuArgs a, cudaStream_t st) {
     // more than 256 positions to a tile need a store of every decoder group in each tile (four stages)
-    a.bn = WIDE && a.nk > 6 ? MU_BN : 256;
+    a.nk = (a.K + 64 * MuShape<WIDE>::HALF - 1) / (64 * MuShape<WIDE>::HALF);
+    a.bn = WIDE && a.nk <= 6 ? 256 : MuShape<WIDE>::BN;
     int dev = 0, sms = 152;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const size_t smem = 1024 + (size_t)MU_B + (size_t)MU_RAW * 8 * q4_block_bytes(G, a.zeros != 0) +
+    const size_t smem = 1024 + (size_t)MuShape<WIDE>::SLOTS * 32768 + (size_t)MuShape<WIDE>::raw(G) * 8 * q4_block_bytes(G, a.zeros != 0) +
                         sizeof(MuBars) + (size_t)(a.E + 1) * 4;
     cudaError_t e = cudaFuncSetAttribute(moe_umma_kernel<G, PAIR, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
@@ -735,20 +755,23 @@ cudaError_t launch_umma_moe(const MuMaps& maps, MuArgs a, cudaStream_t st) {
 }
 
 // f16 rows of length `inner`.
-bool row_maps(MuMaps& m, __half* rows, int64_t inner, int64_t n) {
+bool row_maps(MuMaps& m, __half* rows, int64_t inner, int64_t n, bool wide) {
     for (int i = 0; i < 4; ++i)
         if (!make_tensor_map_2d(&m.box[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rows, (uint64_t)inner, (uint64_t)n,
-                                (uint64_t)inner * 2, 64u, 32u << i, CU_TENSOR_MAP_SWIZZLE_128B))
+                                (uint64_t)inner * 2, 64u, wide ? 32u << i : 32u * (i + 1), CU_TENSOR_MAP_SWIZZLE_128B))
             return false;
     return true;
 }
 
+// Wide tiles from 120 rows a matrix on average.  (Two groups of decoders need
+// blocks of two stages: a slot's last block must have been theirs or the MMAs'.)
+bool wide_tiles(int64_t nslots, int64_t E, int64_t K) { return nslots >= 120 * E && K > 128; }
+
 template <bool PAIR>
-cudaError_t launch_by_group(int group, const MuMaps& maps, const MuArgs& a, cudaStream_t st) {
-    // wide tiles from 120 rows a matrix on average (64 experts of 2048x1024, 96 / 128 rows each: narrow 130 / 146
-    // us, wide 137 / 144)
-    // (two groups of decoders need blocks of two stages: a slot's last block must have been theirs or the MMAs')
-    const bool wide = a.nslots >= 120 * (int64_t)a.E && a.nk > 2;
+cudaError_t launch_by_group(int group, __half* rows, const MuArgs& a, cudaStream_t st) {
+    const bool wide = wide_tiles(a.nslots, a.E, a.K);
+    MuMaps maps;
+    if (!row_maps(maps, rows, a.K, a.nslots, wide)) return cudaErrorInvalidValue;
     if (group == 32)
         return wide ? launch_umma_moe<32, PAIR, true>(maps, a, st) : launch_umma_moe<32, PAIR, false>(maps, a, st);
     if (group == 64)
@@ -792,8 +815,6 @@ cudaError_t launch_moe_tensor(const MoeTensor& m, void* scratch, cudaStream_t st
                        static_cast<const __nv_bfloat16*>(m.x), m.ldx, vec, (int)D, m.ids,
                        static_cast<const float2*>(where), (int)S, m.k, xs, first, second);
     if (e != cudaSuccess) return e;
-    MuMaps xmaps, hmaps;
-    if (!row_maps(xmaps, xs, D, S) || !row_maps(hmaps, hid, F, S)) return cudaErrorInvalidValue;
     MuArgs a{};
     a.w0 = m.gate->blocks;
     a.w1 = m.up->blocks;
@@ -804,12 +825,12 @@ cudaError_t launch_moe_tensor(const MoeTensor& m, void* scratch, cudaStream_t st
     a.nslots = (int)S;
     a.N = (int)F;
     a.row_tiles = (int)((F + 63) / 64);
-    a.nk = (int)((D + 63) / 64);
+    a.K = (int)D;
     a.offsets = m.offsets;
     a.slots = m.slots;
     a.scales = first;
     a.hidden = hid;
-    e = launch_by_group<true>(m.gate->group, xmaps, a, st);
+    e = launch_by_group<true>(m.gate->group, xs, a, st);
     if (e != cudaSuccess) return e;
     MuArgs b = a;
     b.w0 = m.down->blocks;
@@ -819,11 +840,11 @@ cudaError_t launch_moe_tensor(const MoeTensor& m, void* scratch, cudaStream_t st
     b.zeros = m.down->zeros ? 1 : 0;
     b.N = (int)D;
     b.row_tiles = (int)((D + 127) / 128);
-    b.nk = (int)((F + 63) / 64);
+    b.K = (int)F;
     b.scales = second;
     b.hidden = nullptr;
     b.y = m.y;
-    return launch_by_group<false>(m.down->group, hmaps, b, st);
+    return launch_by_group<false>(m.down->group, hid, b, st);
 }
 
 unsigned int read_clear_dev_error_moe_umma(cudaStream_t st) {
