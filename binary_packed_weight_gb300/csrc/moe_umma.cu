@@ -3,13 +3,14 @@
 // Per matrix e of the plan, rows p of its positions, W = (c - z) d:
 //   hidden[p] = silu(Gate x[p]) * (Up x[p]),   y[slot(p)] = Down hidden[p]
 //
-// Both products are D[n, p] = sum_k W[n,k] act[p,k] with 128 weight rows and up
-// to 256 (wide tiles: 384) positions a tile, f16 operands and one f32 accumulator in
-// tensor memory, in stages of 128 k (what a stage costs besides its MMAs -- waits,
-// commits, the decoders' hand-offs, several hundred cycles -- does not grow with its k):
+// Both products are D[n, p] = sum_k W[n,k] act[p,k] with 128 weight rows and up to
+// 128 (wide tiles: 384) positions a tile, f16 operands and one f32 accumulator in
+// tensor memory, in stages of 256 (128) k (what a stage costs besides its MMAs --
+// waits, commits, hand-offs, several hundred cycles -- does not grow with its k):
 //   * warps 0 and 2 stream the activations (B, 128-byte swizzle) by TMA, the first
-//     and the second 64 k of a stage (one warp takes ~650 cycles a slot);
-//   * warp 3 streams the packed blocks of 256 k by bulk copies;
+//     and the second half of a stage (one warp takes ~650 cycles a slot);
+//   * warp 3 streams the packed blocks of 256 k by bulk copies; narrow tiles are a
+//     stream of weights, so they have five blocks (86 KB) in flight, wide ones three;
 //   * two or three groups of four decoder warps, which take every second or third
 //     stage, decode a block's rows, one weight row a thread, and store them as the A
 //     operand in tensor memory (rounding (c - z) d to f16 is the only rounding of
@@ -18,10 +19,13 @@
 //     next stage's is tested while this stage's MMAs run;
 //   * eight or sixteen epilogue warps drain the finished tile, some columns each in
 //     turn, while the next tile's operands fill their rings.
-// A matrix's weights are decoded once for each of its tiles, so tiles are as wide as
-// tensor memory allows: 256 columns of accumulator leave room for four stages of
-// weights, 320 for three, 384 for two.  (With 256 at most, experts of 257 rows were
-// two tiles, each bound by the decoders: 2048 tokens of 64 experts 243 us, now 219.)
+// A matrix's weights are decoded once for each of its tiles, so wide tiles are as
+// wide as tensor memory allows: 256 columns of accumulator leave room for four stages
+// of weights, 320 for three, 384 for two.  (With 256 at most, experts of 257 rows were
+// two tiles, each bound by the decoders: 2048 tokens of 64 experts 243 us, now 218.)
+// Bound: wide tiles by their MMAs (60 % of the time), the decoders and the epilogue,
+// which nothing overlaps; narrow ones by the decoders (of 256 k in ~2200 cycles a
+// group) and the blocks' latency: 213 MB of weights in 75 us from 40 to 128 tokens.
 // A tile of the first product holds 64 rows of Gate and the same 64 of Up: lanes
 // 0..15 of each quarter are Gate's, 16..31 Up's, so one shuffle meets the two.
 //
@@ -763,7 +767,8 @@ bool row_maps(MuMaps& m, __half* rows, int64_t inner, int64_t n, bool wide) {
     return true;
 }
 
-// Wide tiles from 120 rows a matrix on average.  (Two groups of decoders need
+// Wide tiles from 120 rows a matrix on average (64 experts of 2048x1024, 112 / 128
+// rows each: narrow 131 / 150 us, wide 136 / 140).  (Two groups of decoders need
 // blocks of two stages: a slot's last block must have been theirs or the MMAs'.)
 bool wide_tiles(int64_t nslots, int64_t E, int64_t K) { return nslots >= 120 * E && K > 128; }
 

@@ -154,8 +154,10 @@ cudaError_t launch_combine(const float* y, const int32_t* ids, const float* w, v
                       ldo, T_, D, k, D % 4 == 0 ? 1 : 0);
 }
 
-// Average rows of a matrix from which f16 and bf16 calls take the tensor-core path.
-constexpr int64_t MOE_TENSOR_ROWS = 10;
+// Average rows of a matrix above which f16 and bf16 calls take the tensor-core
+// path: beyond, the streaming products need a second tile of columns (64 experts of
+// 2048x1024 bf16, 4 / 4.9 rows each: streaming 66 / 85 us, tensor cores 75 / 75).
+constexpr int64_t MOE_TENSOR_ROWS = 4;
 
 // Scratch of one call, given back on the same stream whatever happens.
 struct Scratch {
@@ -336,7 +338,7 @@ tq2_status moe_experts(q4_handle gate, q4_handle up, q4_handle down, const void*
     };
     Scratch mem(st);
     const size_t ybytes = ((size_t)S * D * 4 + 255) / 256 * 256;
-    if (dtype != TQ2_F32 && S >= MOE_TENSOR_ROWS * E) {
+    if (dtype != TQ2_F32 && S > MOE_TENSOR_ROWS * E) {
         cudaError_t e = scratch_alloc(&mem.p, ybytes + moe_tensor_scratch(S, D, F), st);
         if (e != cudaSuccess) {
             mem.p = nullptr;

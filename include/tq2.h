@@ -586,8 +586,8 @@ TQ2_API tq2_status moe_route_backward(const void* logits, int64_t ld, int dtype,
  *   that fit each other: else TQ2_ESHAPE.  Pointers aligned to their elements:
  *   else TQ2_EINVAL.
  *
- * Calls of f32, and those of f16 and bf16 with fewer than 10 slots a matrix on
- * average (T*k < 10 E): Gate and Up take x as q4_gemm takes it; the gated product
+ * Calls of f32, and those of f16 and bf16 with at most 4 slots a matrix on
+ * average (T*k <= 4 E): Gate and Up take x as q4_gemm takes it; the gated product
  * is kept in f32 and enters Down as f32 activations do (for f16 and bf16 as its
  * first f16 part alone, within 2^-11 of its magnitude).
  * f16 and bf16 calls with more: the weights are rounded to f16, rows of x and of
