@@ -150,6 +150,13 @@ struct MuArgs {
     float* y;                              // else: [slot][N]
 };
 
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]) : "memory");
+}
+
 // Barrier of the eight epilogue warps.
 template <int WARPS>
 __device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory"); }
@@ -485,9 +492,9 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
 #pragma unroll
                 for (int at = 0; at < 2; ++at) {
                     const int c = c0 + at;
-                    uint32_t v[32];
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
+                        uint32_t v[16];
                         const int gi = (c * 2 + half) / (G / 32);
                         const __half2 d = __half2half2(*reinterpret_cast<const __half*>(sc + gi * 4));
                         const Q4Zero z = q4_zero<false>(a.zeros ? zp[gi * 2] : 8u);
@@ -498,11 +505,11 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {
                                 const __half2 m = __hmul2(*reinterpret_cast<const __half2*>(&p[x]), d);
-                                v[16 * half + 4 * tt + x] = *reinterpret_cast<const uint32_t*>(&m);
+                                v[4 * tt + x] = *reinterpret_cast<const uint32_t*>(&m);
                             }
                         }
+                        tmem_st_32x32b_x16(lane_addr + (uint32_t)(f.s * 64 * HALF + (2 * h + at) * 32 + 16 * half), v);
                     }
-                    tmem_st_32x32b_x32(lane_addr + (uint32_t)(f.s * 64 * HALF + (2 * h + at) * 32), v);
                 }
             }
             tmem_wait_st();
