@@ -17,6 +17,11 @@
 // the first) turns them into each chunk's first positions and writes the slots.
 // Within a chunk, warps count their 32 slots by match.any and a prefix over the
 // warps orders them, so there is no atomic whose order could matter.
+//
+// Bound: a few tokens by the call (1x64: 7 us) and the latency of the picks (300x160
+// in groups: 9.8); many by issue (16384x256, 4 of 8 groups, top 8: 26.5 us, 998 warp
+// instructions a token, a third of them the exact scores; the plan's kernel is 6 of
+// it).  The gradient's 16384x128 takes 6.2 us, the host's time for the call.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

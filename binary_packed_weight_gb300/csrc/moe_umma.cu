@@ -25,7 +25,7 @@
 // two tiles, each bound by the decoders: 2048 tokens of 64 experts 243 us, now 218.)
 // Bound: wide tiles by their MMAs (60 % of the time), the decoders and the epilogue,
 // which nothing overlaps; narrow ones by the decoders (of 256 k in ~2200 cycles a
-// group) and the blocks' latency: 213 MB of weights in 75 us from 40 to 128 tokens.
+// group) and the blocks' latency: 213 MB of weights in 74 us from 40 to 128 tokens.
 // A tile of the first product holds 64 rows of Gate and the same 64 of Up: lanes
 // 0..15 of each quarter are Gate's, 16..31 Up's, so one shuffle meets the two.
 //
