@@ -298,6 +298,55 @@ def test_experts_tiles_of_every_width(lib, seed):
     assert not bad.any(), f"{bad.sum()} off, worst {np.max(np.abs(got - want) / bound):.3g} of the bound"
 
 
+@pytest.mark.parametrize("E,T,F", [(4, 40000, 8192), (64, 1600, 12288)])
+def test_experts_many_tiles(lib, E, T, F):
+    """More tiles than a CTA looks up ahead, wide and narrow ones; sampled tokens of three experts."""
+    rng = np.random.default_rng(40 + E)
+    D, group = 128, 128
+    some = [0, E // 2, E - 1]
+    mats, handles = [], []
+    for N, K in ((F, D), (F, D), (D, F)):
+        c, d, z = planes(rng, E, N, K, group, False)
+        mats.append(oq4.dequant(c[some], d[some].view(np.uint16), z, group))
+        handles.append(upload(lib, c, d, z, group))
+    ids = rng.integers(0, E, (T, 1))
+    weights = rng.random((T, 1)).astype(np.float32)
+    x, got = run_experts(lib, rng.normal(size=(T, D)) * 0.2, ids, weights, handles, "bfloat16", E)
+    of = [np.flatnonzero(ids[:, 0] == e) for e in some]
+    pick = np.concatenate([p[[0, 1, len(p) // 2, -2, -1]] for p in of])
+    local = np.repeat(np.arange(3), 5)[:, None]
+    x, got, weights = x[pick], got[pick], weights[pick]
+    want = omoe.experts(x, local, weights, *mats)
+    eps = 2.0 ** -11 + (F / 16 + 16) * 2.0 ** -22
+    bound = omoe.experts_bound(x, local, weights, *mats, eps, eps, 2.0 ** -11)
+    bound = 1.02 * bound + (2.0 ** -8 + 2.0 ** -22) * np.abs(want) + 1e-7
+    assert np.all(np.isfinite(got)) and np.all(np.abs(got - want) <= bound)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("T,E,k,D,F,group,zeros", [(9, 2, 1, 32, 32, 32, True), (5, 3, 3, 64, 160, 32, False),
+                                                   (31, 7, 1, 416, 96, 32, True), (21, 4, 1, 320, 448, 64, False),
+                                                   (26, 5, 2, 640, 128, 128, True), (43, 1, 3, 192, 64, 64, True)])
+def test_experts_of_few_rows(lib, dtype, T, E, k, D, F, group, zeros):
+    """Between 4 and 130 rows an expert; some slots are not routed, and with one expert the rest of a token's."""
+    rng = np.random.default_rng(50 + T)
+    mats, handles = [], []
+    for N, K in ((F, D), (F, D), (D, F)):
+        c, d, z = planes(rng, E, N, K, group, zeros)
+        mats.append(oq4.dequant(c, d.view(np.uint16), z, group))
+        handles.append(upload(lib, c, d, z, group))
+    ids = rng.integers(0, E, (T, k))
+    ids[T // 3, 0] = -1
+    weights = rng.random((T, k)).astype(np.float32)
+    x, got = run_experts(lib, rng.normal(size=(T, D)) * 0.2, ids, weights, handles, dtype, E, pad=3)
+    want = omoe.experts(x, ids, weights, *mats)
+    eps = 2.0 ** -11 + (max(D, F) / 16 + 16) * 2.0 ** -22
+    bound = omoe.experts_bound(x, ids, weights, *mats, eps, eps, 2.0 ** -11)
+    bound = 1.02 * bound + (HALF_ULP[dtype] + k * 2.0 ** -22) * np.abs(want) + 1e-7
+    bad = ~(np.abs(got - want) <= bound)
+    assert not bad.any(), f"{bad.sum()} off, worst {np.max(np.abs(got - want) / bound):.3g} of the bound"
+
+
 def test_experts_no_tokens_and_no_slots(lib):
     import torch
     rng = np.random.default_rng(4)
