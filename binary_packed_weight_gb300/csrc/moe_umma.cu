@@ -201,7 +201,8 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
     }
     pdl_launch_dependents();
     if (warp == 1) {
-        pdl_wait();                                        // the plan is an earlier kernel's
+        // The plan is there: the kernel ahead lets this one start only when it has waited for it, and so for the
+        // first packed blocks; what that kernel writes is waited for below.
         int run = 0;
         bool down = false;                                 // ranges that go back are no plan: nothing is done
         for (int e0 = 0; e0 <= a.E; e0 += 32) {
@@ -677,8 +678,8 @@ moe_stage_kernel(const T* __restrict__ x, int64_t ldx, int vec, int D, const int
     __shared__ int to[32];                                 // positions, -1: none
     __shared__ float red[9];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();                               // (the products read the plan before they wait)
     const int64_t t = blockIdx.x;
     const T* row = x + t * ldx;
     typename Pair<T>::type v[4], top[4];
