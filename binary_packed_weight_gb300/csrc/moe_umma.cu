@@ -22,10 +22,11 @@
 // A matrix's weights are decoded once for each of its tiles, so wide tiles are as
 // wide as tensor memory allows: 256 columns of accumulator leave room for four stages
 // of weights, 320 for three, 384 for two.  (With 256 at most, experts of 257 rows were
-// two tiles, each bound by the decoders: 2048 tokens of 64 experts 243 us, now 218.)
+// two tiles, each bound by the decoders: 2048 tokens of 64 experts 243 us against 219.)
 // Bound: wide tiles by their MMAs (60 % of the time), the decoders and the epilogue,
 // which nothing overlaps; narrow ones by the decoders (of 256 k in ~2200 cycles a
-// group) and the blocks' latency: 213 MB of weights in 74 us from 40 to 128 tokens.
+// group) and the blocks' latency: 213 MB of weights in 68 us from 40 to 64 tokens.
+// Plan and first packed blocks are read while the kernel ahead ends (74 us without).
 // A tile of the first product holds 64 rows of Gate and the same 64 of Up: lanes
 // 0..15 of each quarter are Gate's, 16..31 Up's, so one shuffle meets the two.
 //
@@ -775,10 +776,10 @@ bool row_maps(MuMaps& m, __half* rows, int64_t inner, int64_t n, bool wide) {
     return true;
 }
 
-// Wide tiles from 120 rows a matrix on average (64 experts of 2048x1024, 112 / 128
-// rows each: narrow 131 / 150 us, wide 136 / 140).  (Two groups of decoders need
+// Wide tiles from 112 rows a matrix on average (64 experts of 2048x1024, 112 / 128
+// rows each: narrow 122 / 141 us, wide 121 / 127).  (Two groups of decoders need
 // blocks of two stages: a slot's last block must have been theirs or the MMAs'.)
-bool wide_tiles(int64_t nslots, int64_t E, int64_t K) { return nslots >= 120 * E && K > 128; }
+bool wide_tiles(int64_t nslots, int64_t E, int64_t K) { return nslots >= 112 * E && K > 128; }
 
 template <bool PAIR>
 cudaError_t launch_by_group(int group, __half* rows, const MuArgs& a, cudaStream_t st) {

@@ -157,7 +157,7 @@ cudaError_t launch_combine(const float* y, const int32_t* ids, const float* w, v
 
 // Average rows of a matrix above which f16 and bf16 calls take the tensor-core
 // path: beyond, the streaming products need a second tile of columns (64 experts of
-// 2048x1024 bf16, 4 / 4.9 rows each: streaming 66 / 85 us, tensor cores 75 / 75).
+// 2048x1024 bf16, 4 / 4.9 rows each: streaming 66 / 85 us, tensor cores 67 / 68).
 constexpr int64_t MOE_TENSOR_ROWS = 4;
 
 // Scratch of one call, given back on the same stream whatever happens.
