@@ -39,6 +39,7 @@
 #include <cuda_fp16.h>
 
 #include "../../include/tq2.h"
+#include "moe_stages.cuh"
 #include "q4.cuh"
 #include "tq2_internal.h"
 
@@ -46,26 +47,6 @@ namespace tq2 {
 
 namespace {
 
-// Decoder groups (of four warps), epilogue warps and the columns one of those takes
-// at a time.  Narrow tiles, whose MMAs are short, need three groups to feed them; the
-// epilogue of wide ones, which the next tile's MMAs wait for, needs sixteen warps
-// (64 experts of 2048x1024 bf16, top 8, 2048 tokens: 219 us with 2 groups and 16
-// warps, 227 with 2 and 12, 230 with 3 and 12, 248 with 3 and 8).
-template <bool WIDE>
-struct MuShape {
-    static constexpr int GROUPS = WIDE ? 2 : 3;
-    static constexpr int HALF = WIDE ? 1 : 2;              // chunks of 64 k in half a stage
-    static constexpr int STAGES = WIDE ? 4 : 3;            // stages of weights in tensor memory
-    static constexpr int BN = WIDE ? 384 : 128;            // positions of a tile at most
-    static constexpr int ACOL = WIDE ? 256 : 128;          // first tensor-memory column of the stages
-    static constexpr int BLOCK_STAGES = 2 / HALF;          // stages of a packed block
-    static constexpr int SLOTS = WIDE ? 5 : 4;             // activation slots (half a stage) of 32 KB
-    static __host__ __device__ constexpr int raw(int G) { return WIDE ? 3 : G == 32 ? 4 : 5; }   // packed blocks of 256 k in their ring
-    static constexpr int EPI = 4 + 4 * GROUPS;             // first epilogue warp
-    static constexpr int DRAIN = WIDE ? 16 : 8;            // epilogue warps
-    static constexpr int THREADS = 32 * (EPI + DRAIN);
-    static constexpr int CW = 16;
-};
 constexpr int MU_A = 4;                    // stages of decoded weights at most
 constexpr int MU_RAW = 5;                  // packed blocks of 256 k in their ring at most
 constexpr int MU_LIST = 64;                // tiles of a CTA that are looked up ahead
@@ -87,36 +68,6 @@ struct MuBars {
     int abort;
     MuTile list[MU_LIST];
     float2 scale[384];                     // epilogue: a tile's scales (or output rows and scales)
-};
-
-// The stage at hand and the parities of its barriers' phases.  A tile of more
-// than 256 (320) positions has its last accumulator columns where stage 0 (and
-// 1) would be, so it goes without; a later tile that takes such a stage up again
-// waits for `drained`, which the MMA warp completes then.  (Two groups of
-// decoders need two stages: a group's last wait must be past every older phase
-// of the stage that it waits for next.)
-template <bool WIDE>
-struct MuStages {
-    int s = 0;
-    int lowest = 0;                        // (stays 0 unless WIDE)
-    uint32_t used = 0;
-    // The next tile; returns the last one's lowest stage.
-    __device__ __forceinline__ int begin(int cnt) {
-        const int was = WIDE ? lowest : 0;
-        if (WIDE) {
-            lowest = cnt > 320 ? 2 : cnt > 256 ? 1 : 0;
-            s = s < lowest ? lowest : s;
-        }
-        return was;
-    }
-    __device__ __forceinline__ void next() {
-        used ^= 1u << s;
-        s = s + 1 == MuShape<WIDE>::STAGES ? (WIDE ? lowest : 0) : s + 1;
-    }
-    __device__ __forceinline__ uint32_t parity() const { return (used >> s) & 1u; }
-    // Activation slots (half a stage) in the ring, and their bytes.
-    __device__ __forceinline__ int slots() const { return WIDE ? MuShape<WIDE>::SLOTS - lowest : MuShape<WIDE>::SLOTS; }
-    __device__ __forceinline__ uint32_t slot_bytes() const { return WIDE ? 32768u + 8192u * (uint32_t)lowest : 32768u; }
 };
 
 // Slot and phase parity of a ring's next item.
@@ -272,7 +223,7 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
             for (int i = 0; i < mine && ok; ++i) {
                 const MuTile m = tile_at(i);
                 const int boxes = (m.cnt + 31) / 32;
-                if (f.begin(m.cnt) != f.lowest) {
+                if (f.begin(m.cnt) != 0) {
                     if (last && !mbar_wait_or_abort(last, last_parity, abort_flag)) {
                         ok = false;
                         break;
@@ -381,9 +332,9 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
                         break;
                     }
                 }
-                const int was = f.begin(cnt);
-                if (f.lowest < was) mbar_arrive(&bars->drained);
-                if (f.lowest != was) slot = 0;
+                const int again = f.begin(cnt);
+                if (again > 0) mbar_arrive(&bars->drained);
+                if (again != 0) slot = 0;
                 const int slots = f.slots();
                 const uint32_t bytes = f.slot_bytes();
                 bool ready = false;
@@ -450,7 +401,7 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
                 st = 0;
                 base += a.nkc;
                 ++i;
-                if (WIDE && i < mine) owed = f.begin(tile_at(i).cnt) > f.lowest || owed;
+                if (WIDE && i < mine) owed = f.begin(tile_at(i).cnt) > 0 || owed;
             }
         };
         auto settle = [&] {
