@@ -109,7 +109,7 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
         "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]) : "memory");
 }
 
-// Barrier of the eight epilogue warps.
+// Barrier of the epilogue warps.
 template <int WARPS>
 __device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory"); }
 
@@ -484,6 +484,7 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
         const int q = warp & 3, b = (warp - MU_EPI) >> 2;
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
         pdl_wait();
+        bool ok = true;
         for (int ti = 0; ti < mine; ++ti) {
             const MuTile m = tile_at(ti);
             epi_bar<DRAIN>();                                     // the last tile's scales and rows are done with
@@ -493,9 +494,11 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
                 bars->scale[i] = sc;
             }
             epi_bar<DRAIN>();
-            if (!mbar_wait_or_abort(&bars->acc_full, (uint32_t)ti & 1u, abort_flag)) {
+            // (after a wait that ran out a warp stays for the barriers: others may still be on their way to them)
+            if (!ok || !mbar_wait_or_abort(&bars->acc_full, (uint32_t)ti & 1u, abort_flag)) {
                 *abort_flag = 1;
-                break;
+                ok = false;
+                continue;
             }
             tc_fence_after();
             // pair: this lane finishes half of CW positions of its row, else all of them

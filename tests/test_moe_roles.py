@@ -81,3 +81,13 @@ def test_no_expression_holds_a_new_tile_and_what_it_changes():
     for name in sorted(os.listdir(CSRC)):
         for statement in re.split(r"[;{}]", source(name)):
             assert not ("begin(" in statement and "lowest" in statement), (name, statement)
+
+
+def test_epilogue_warps_meet_at_their_barrier_whatever_happens():
+    """The epilogue warps share a named barrier.  Of one wait that runs out some of them may see the end and others
+    not, so none may leave the loop early: the others would wait for it for good."""
+    text = source("moe_umma.cu")
+    start = text.index("warp >= MU_EPI) {")
+    role = text[start:text.index("tmem_dealloc(tmem", start)]
+    assert role.count("epi_bar<DRAIN>();") == 2
+    assert not re.search(r"\b(break|return|goto)\b", role)
