@@ -63,7 +63,7 @@ struct MuTile {
 
 struct MuBars {
     uint64_t full[MU_A], empty[MU_A], half_empty[MU_A], raw_full[MU_RAW], raw_empty[MU_RAW];
-    uint64_t acc_full, acc_empty, drained;
+    uint64_t acc_full, acc_empty, drained, idle;
     uint32_t tmem_base;
     int abort;
     MuTile list[MU_LIST];
@@ -143,6 +143,7 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
         mbar_init(&bars->acc_full, 1);
         mbar_init(&bars->acc_empty, DRAIN);                    // every epilogue warp
         mbar_init(&bars->drained, 1);                      // the MMA warp
+        mbar_init(&bars->idle, 1);                         // its last commit
         bars->abort = 0;
         fence_mbar_init();
         for (int i = 0; i < 4; ++i) tma_prefetch_desc(&maps.box[i]);
@@ -379,6 +380,10 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
                 umma_commit(&bars->acc_full);
                 if (i + 1 < mine) cnt = tile_at(i + 1).cnt;
             }
+            // Whatever the other roles gave up, the MMAs still in flight end before tensor memory is given back and
+            // the CTA exits.  (Without a timeout the epilogue waits for the same ones.)
+            umma_commit(&bars->idle);
+            mbar_wait(&bars->idle, 0u);
         }
         __syncwarp();
     } else if (warp >= 4 && warp < MU_EPI) {               // ---- decoders

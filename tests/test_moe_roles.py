@@ -91,3 +91,15 @@ def test_epilogue_warps_meet_at_their_barrier_whatever_happens():
     role = text[start:text.index("tmem_dealloc(tmem", start)]
     assert role.count("epi_bar<DRAIN>();") == 2
     assert not re.search(r"\b(break|return|goto)\b", role)
+
+
+def test_mmas_end_before_their_tensor_memory_is_given_back():
+    """A role that gives up leads every warp to the end of the kernel: the issuer waits for what it issued, on every
+    way out of its loop."""
+    text = source("moe_umma.cu")
+    start = text.index("} else if (warp == 1) {")
+    role = text[start:text.index("} else if (warp >= 4", start)]
+    assert not re.search(r"\b(return|goto)\b", role)
+    tail = role[role.rindex("umma_commit(&bars->acc_full);"):]
+    assert re.search(r"}\s*umma_commit\(&bars->idle\);\s*mbar_wait\(&bars->idle, 0u\);\s*}\s*__syncwarp\(\);\s*$", tail)
+    assert text.count("mbar_init(&bars->idle, 1);") == 1
