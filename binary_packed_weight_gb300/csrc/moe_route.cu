@@ -529,7 +529,9 @@ struct RouteBackArgs {
 // Lane j holds slot j.  Where only the selected logits matter (sigmoid;
 // renormalised softmax without a bias, whose selected scores sum to at least
 // 1/(2E), so that the common factor of the softmax cancels) they are gathered;
-// else the row is read.  The row is written dense, then the selected entries.
+// else the row is read.  A score is divided by the sum before anything is
+// multiplied by it: g / S alone may pass the largest f32, p / S is at most 1.
+// The row is written dense, then the selected entries.
 template <class T, int V>
 __global__ void __launch_bounds__(256) moe_route_backward_kernel(const __grid_constant__ RouteBackArgs a) {
     const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
@@ -541,7 +543,7 @@ __global__ void __launch_bounds__(256) moe_route_backward_kernel(const __grid_co
         T* drow = reinterpret_cast<T*>(a.dl) + t * a.ldd;
         const int id = lane < a.k ? a.ids[t * a.k + lane] : -1;
         const bool on = id >= 0 && id < a.E;
-        float g = on ? a.dw[t * a.k + lane] * a.scale : 0.f;
+        const float g = on ? a.dw[t * a.k + lane] * a.scale : 0.f;
         const float l = on ? available(to_f32(row[id]), a.bias ? a.bias[id] : 0.f) : -INFINITY;
         const bool live = l > -INFINITY;
         float out[V];
@@ -551,10 +553,11 @@ __global__ void __launch_bounds__(256) moe_route_backward_kernel(const __grid_co
         if (a.score == MOE_SIGMOID) {
             const float p = live ? sigmoid(l) : 0.f, q = live ? sigmoid(-l) : 0.f;   // q = 1 - p without cancellation
             if (a.renorm) {
-                const float S = fmaxf(warp_sum(p), ROUTE_TINY);
-                g = (g - warp_sum(g * p) / S) / S;
+                const float r = p / fmaxf(warp_sum(p), ROUTE_TINY);
+                mine = r * q * (g - warp_sum(g * r));
+            } else {
+                mine = p * q * g;
             }
-            mine = p * q * g;
         } else if (a.renorm && !a.bias) {
             const float m = warp_max(l);
             const float e = live ? expf(l - m) : 0.f;
@@ -575,15 +578,10 @@ __global__ void __launch_bounds__(256) moe_route_backward_kernel(const __grid_co
             for (int i = 0; i < V; ++i) x[i] = x[i] > -INFINITY ? expf(x[i] - m) : 0.f;
             const float s = tree_sum<V>(x);
             const float p = live ? expf(l - m) / s : 0.f;
-            float dot = 0.f;
-            if (a.renorm) {
-                const float S = fmaxf(warp_sum(p), ROUTE_TINY);
-                g = (g - warp_sum(g * p) / S) / S;
-            } else {
-                dot = warp_sum(g * p);
-            }
-            mine = p * (g - dot);
-            const float c = s > 0.f ? -dot / s : 0.f;
+            const float r = a.renorm ? p / fmaxf(warp_sum(p), ROUTE_TINY) : p;
+            const float dot = warp_sum(g * r);
+            mine = r * (g - dot);
+            const float c = !a.renorm && s > 0.f ? -dot / s : 0.f;
 #pragma unroll
             for (int i = 0; i < V; ++i) out[i] = x[i] * c;
         }
