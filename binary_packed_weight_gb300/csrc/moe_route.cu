@@ -531,6 +531,8 @@ struct RouteBackArgs {
 // 1/(2E), so that the common factor of the softmax cancels) they are gathered;
 // else the row is read.  A score is divided by the sum before anything is
 // multiplied by it: g / S alone may pass the largest f32, p / S is at most 1.
+// A sum below 2^-126 is not what the weights were divided by: they are p times
+// a constant there, and so is their gradient.
 // The row is written dense, then the selected entries.
 template <class T, int V>
 __global__ void __launch_bounds__(256) moe_route_backward_kernel(const __grid_constant__ RouteBackArgs a) {
@@ -553,8 +555,9 @@ __global__ void __launch_bounds__(256) moe_route_backward_kernel(const __grid_co
         if (a.score == MOE_SIGMOID) {
             const float p = live ? sigmoid(l) : 0.f, q = live ? sigmoid(-l) : 0.f;   // q = 1 - p without cancellation
             if (a.renorm) {
-                const float r = p / fmaxf(warp_sum(p), ROUTE_TINY);
-                mine = r * q * (g - warp_sum(g * r));
+                const float S = warp_sum(p), r = p / fmaxf(S, ROUTE_TINY);
+                const float dot = warp_sum(g * r);
+                mine = r * q * (S < ROUTE_TINY ? g : g - dot);
             } else {
                 mine = p * q * g;
             }
@@ -578,10 +581,12 @@ __global__ void __launch_bounds__(256) moe_route_backward_kernel(const __grid_co
             for (int i = 0; i < V; ++i) x[i] = x[i] > -INFINITY ? expf(x[i] - m) : 0.f;
             const float s = tree_sum<V>(x);
             const float p = live ? expf(l - m) / s : 0.f;
-            const float r = a.renorm ? p / fmaxf(warp_sum(p), ROUTE_TINY) : p;
+            const float S = warp_sum(p), r = a.renorm ? p / fmaxf(S, ROUTE_TINY) : p;
             const float dot = warp_sum(g * r);
-            mine = r * (g - dot);
-            const float c = !a.renorm && s > 0.f ? -dot / s : 0.f;
+            // the sum as divisor makes what flows to all experts vanish; a constant one does not
+            const bool clamped = a.renorm && S < ROUTE_TINY;
+            mine = clamped ? r * g - p * dot : r * (g - dot);
+            const float c = (clamped || !a.renorm) && s > 0.f ? -dot / s : 0.f;
 #pragma unroll
             for (int i = 0; i < V; ++i) out[i] = x[i] * c;
         }

@@ -555,10 +555,11 @@ TQ2_API tq2_status moe_route(const void* logits, int64_t ld, int dtype, const fl
 /*
  * moe_route_backward -- gradient of moe_route's weights to its logits (the
  * selection is piecewise constant and the bias takes no part in the weights).
- * With g_j = scale * dweights[j] and p as above, sums over the selected j:
- *   renorm:   q_j = (g_j - sum_i g_i p_i / S) / S,  S = max(sum_i p_i, 2^-126); else q_j = g_j
+ * With g_j = scale * dweights[j] and p as above, sums over the selected j, S = sum_i p_i:
+ *   q_j = g_j without renorm;  (g_j - sum_i g_i p_i / S) / S with renorm;  g_j / 2^-126 with
+ *   renorm where S < 2^-126 (the weights are divided by a constant there)
  *   softmax:  dlogits[e] = p_e (q_e - sum_j q_j p_j)      (q_e = 0 unless selected;
- *             with renorm the sum is 0 and only the selected get a gradient)
+ *             with renorm and S >= 2^-126 the sum is 0 and only the selected get a gradient)
  *   sigmoid:  dlogits[e] = p_e (1 - p_e) q_e
  * ids as moe_route returned them; a slot of -1 takes no part.  dlogits: DEVICE,
  * dtype, T rows of E, ldd >= E elements apart, overwritten.  Limits as

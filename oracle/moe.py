@@ -98,12 +98,12 @@ def route_backward(logits, ids, dw, bias=None, score="softmax", renorm=True, sca
         p, _ = scores(row, bias, score)
         on = [(e, g * scale) for e, g in zip(ids[t], np.asarray(dw[t], np.float64)) if e >= 0]
         q = np.zeros(len(row))
-        S = max(sum(p[e] for e, _ in on), TINY)
-        mean = sum(g * p[e] for e, g in on) / S
+        S = sum(p[e] for e, _ in on)
+        clamped = renorm and S < TINY                     # w = scale p / TINY: nothing is shared out
         for e, g in on:
-            q[e] = (g - mean) / S if renorm else g
+            q[e] = g if not renorm else g / TINY if clamped else (g - sum(h * p[i] for i, h in on) / S) / S
         if score == "softmax":
-            out[t] = p * (q - (0.0 if renorm else sum(q[e] * p[e] for e, _ in on)))
+            out[t] = p * (q - (0.0 if renorm and not clamped else sum(q[e] * p[e] for e, _ in on)))
         else:
             out[t] = p * (1 - p) * q
     return out

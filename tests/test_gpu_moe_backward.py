@@ -76,3 +76,21 @@ def test_backward_of_softmax_scores_that_underflow(lib, renorm):
     dw = (rng.normal(size=(12, k)) * 50).astype(np.float32)
     got = backward(lib, l, ids, dw, renorm=renorm, scale=2.5, bias=bias)
     check_backward(got, l, ids, dw, 2.5, bias, "softmax", renorm)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_backward_where_the_sum_is_clamped(lib, score):
+    """Below 2^-126 the divisor of the weights is a constant."""
+    rng = np.random.default_rng(62)
+    E, k = 12, 2
+    l = rng.uniform(-88.6, -87.4, (20, E)).astype(np.float32).astype(np.float64)
+    l[10:] -= 0.0 if score == "sigmoid" else 1.0
+    l[:, 0] = -1e4 if score == "sigmoid" else 0.0                      # (a softmax with a score of one)
+    ids = np.array([1 + rng.permutation(E - 1)[:k] for _ in range(20)])
+    ids[4:8, 1] = -1
+    p = np.array([omoe.scores(r, None, score)[0] for r in l])
+    assert np.sum(np.where(ids >= 0, np.take_along_axis(p, np.maximum(ids, 0), 1), 0).sum(1) < omoe.TINY) >= 4
+    bias = np.where(np.arange(E) > 0, 2.0, 0.0)                        # why they were selected
+    dw = rng.normal(size=(20, k)).astype(np.float32)
+    got = backward(lib, l, ids, dw, score=score, scale=2.5, bias=bias)
+    check_backward(got, l, ids, dw, 2.5, bias, score, True)

@@ -103,3 +103,20 @@ def test_experts_closed_forms():
     one = moe.experts(x, np.array([[1], [1]]), np.ones((2, 1)), 1e4 * np.abs(gate) * np.sign(x[0]), up, down)
     v = 1e4 * (np.abs(gate[1]) @ np.abs(x[0]))
     assert np.allclose(one[0], down[1] @ (v * (up[1] @ x[0])))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("logits", [(-87.5, -89.0, -88.0), (-88.0, -1e4, -90.0), (-87.2, -86.5, -91.0)])
+def test_route_gradient_where_the_sum_is_clamped(score, logits):
+    """Selected scores that sum to less than 2^-126 (and, last, to a little more): the weights' divisor is a constant."""
+    row = np.array(logits + (0.0, -0.5 if score == "softmax" else -1e4))
+    ids, dw = np.array([0, 1, 2]), np.array([0.7, -1.3, 0.4])
+    got = moe.route_backward(row[None], ids[None], dw[None], score=score, scale=1.5)[0]
+    h = 1e-5
+    for e in range(len(row)):
+        up, dn = row.copy(), row.copy()
+        up[e] += h
+        dn[e] -= h
+        diff = (moe.weights_of(up, ids, score=score, scale=1.5) - moe.weights_of(dn, ids, score=score, scale=1.5)) / (2 * h)
+        # central differences of functions of size 1.5: curvature h^2, rounding 2^-50 / h
+        assert abs(got[e] - diff @ dw) < 1e-9
