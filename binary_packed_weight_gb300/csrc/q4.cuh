@@ -122,6 +122,7 @@ struct q4_weight {
     int64_t mstride = 0;               // bytes of one matrix
     uint8_t* blocks = nullptr;
     float* bound = nullptr;            // [E] no row of W[e] has a larger 2-norm
+    float most = 0.f;                  // no weight is larger in magnitude (Inf or NaN where a scale is)
 };
 
 namespace tq2 {

@@ -160,6 +160,10 @@ cudaError_t launch_combine(const float* y, const int32_t* ids, const float* w, v
 // 2048x1024 bf16, 4 / 4.9 rows each: streaming 66 / 85 us, tensor cores 67 / 68).
 constexpr int64_t MOE_TENSOR_ROWS = 4;
 
+// Whether every weight is an f16 number, as the tensor-core path decodes them; the streaming products scale the
+// integers' sums in f32 and take any.  (A group's scale may be up to 65504, its weights 15 times that.)
+bool fits_f16(const q4_weight* w) { return w->most <= 65504.f; }
+
 // Scratch of one call, given back on the same stream whatever happens.
 struct Scratch {
     void* p = nullptr;
@@ -214,9 +218,9 @@ tq2_status q4_upload(const uint8_t* codes, const uint16_t* scales, const uint8_t
     const size_t ngroups = (size_t)E * N * (K / group);
     void* tmp[3] = {nullptr, nullptr, nullptr};
     const void* dev[3] = {nullptr, nullptr, nullptr};
-    // the bounds sit behind the blocks
+    // the bounds sit behind the blocks, the largest weight behind them
     const size_t blocks_bytes = ((size_t)E * w->mstride + 255) / 256 * 256;
-    cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&w->blocks), blocks_bytes + (size_t)E * 4);
+    cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&w->blocks), blocks_bytes + (size_t)(E + 1) * 4);
     if (e == cudaSuccess) w->bound = reinterpret_cast<float*>(w->blocks + blocks_bytes);
     if (e == cudaSuccess) e = to_device(codes, (size_t)E * N * (K / 2), &tmp[0], &dev[0], st);
     if (e == cudaSuccess) e = to_device(scales, ngroups * 2, &tmp[1], &dev[1], st);
@@ -226,6 +230,7 @@ tq2_status q4_upload(const uint8_t* codes, const uint16_t* scales, const uint8_t
                            static_cast<const uint8_t*>(dev[2]), w, st);
     if (e == cudaSuccess)
         e = launch_q4_bound(static_cast<const uint16_t*>(dev[1]), static_cast<const uint8_t*>(dev[2]), w, st);
+    if (e == cudaSuccess) e = cudaMemcpyAsync(&w->most, w->bound + E, 4, cudaMemcpyDeviceToHost, st);
     for (void* p : tmp)
         if (p) cudaFreeAsync(p, st);
     const cudaError_t done = cudaStreamSynchronize(st);        // the caller's planes are read, whatever happened
@@ -339,7 +344,7 @@ tq2_status moe_experts(q4_handle gate, q4_handle up, q4_handle down, const void*
     };
     Scratch mem(st);
     const size_t ybytes = ((size_t)S * D * 4 + 255) / 256 * 256;
-    if (dtype != TQ2_F32 && S > MOE_TENSOR_ROWS * E) {
+    if (dtype != TQ2_F32 && S > MOE_TENSOR_ROWS * E && fits_f16(gate) && fits_f16(up) && fits_f16(down)) {
         cudaError_t e = scratch_alloc(&mem.p, ybytes + moe_tensor_scratch(S, D, F), st);
         if (e != cudaSuccess) {
             mem.p = nullptr;

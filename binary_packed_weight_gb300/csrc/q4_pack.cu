@@ -58,25 +58,33 @@ q4_pack_kernel(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ s
 
 // A warp a row: its 2-norm is at most sqrt(G sum_g (d_g max|c - z_g|)^2); the
 // largest of a matrix, as the bits of a non-negative float (a maximum has no order).
+// Behind the E bounds: the largest |d_g| max|c - z_g| of all, which as bits keeps a NaN.
 __global__ void __launch_bounds__(256)
 q4_bound_kernel(const uint16_t* __restrict__ scales, const uint8_t* __restrict__ zeros, float* __restrict__ bound,
                 int64_t N, int64_t kg, int G) {
     const int lane = threadIdx.x & 31;
+    int* largest = reinterpret_cast<int*>(bound) + gridDim.y;
     scales += (int64_t)blockIdx.y * N * kg;
     if (zeros) zeros += (int64_t)blockIdx.y * N * kg;
     float most = 0.f;
+    int weight = 0;
     for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < N; r += (int64_t)gridDim.x * 8) {
         float s = 0.f;
         for (int64_t i = lane; i < kg; i += 32) {
             const int z = zeros ? zeros[r * kg + i] & 15 : 8;
             const float v = __half2float(__ushort_as_half(scales[r * kg + i])) * (float)(z > 15 - z ? z : 15 - z);
+            weight = max(weight, __float_as_int(v) & 0x7FFFFFFF);
             s = fmaf(v, v, s);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         most = fmaxf(most, sqrtf(s * (float)G));
     }
-    if (lane == 0) atomicMax(reinterpret_cast<int*>(bound) + blockIdx.y, __float_as_int(most));
+    weight = __reduce_max_sync(0xffffffffu, weight);
+    if (lane == 0) {
+        atomicMax(reinterpret_cast<int*>(bound) + blockIdx.y, __float_as_int(most));
+        atomicMax(largest, weight);
+    }
 }
 
 // One thread per (row, 8 k): out[e][row][k..k+7], exact in f32 (5 + 11 bits).
@@ -169,7 +177,7 @@ cudaError_t launch_q4_pack(const uint8_t* codes, const uint16_t* scales, const u
 }
 
 cudaError_t launch_q4_bound(const uint16_t* scales, const uint8_t* zeros, const q4_weight* w, cudaStream_t st) {
-    cudaError_t e = cudaMemsetAsync(w->bound, 0, (size_t)w->E * 4, st);
+    cudaError_t e = cudaMemsetAsync(w->bound, 0, (size_t)(w->E + 1) * 4, st);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((w->N + 7) / 8 < 256 ? (w->N + 7) / 8 : 256);
     q4_bound_kernel<<<dim3(grid, (unsigned)w->E), 256, 0, st>>>(scales, zeros, w->bound, w->N, w->K / w->group,

@@ -451,7 +451,7 @@ typedef struct q4_weight* q4_handle;
  *
  * The handle holds one copy in 16-row x 256-k blocks (codes, then the block's
  * scales and zero points), N padded to 128 rows and K to 256, and a bound of
- * each matrix's row norms (for moe_experts).
+ * each matrix's row norms and the weights' largest magnitude (for moe_experts).
  */
 TQ2_API tq2_status q4_upload(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, int64_t E,
                              int64_t N, int64_t K, int group, q4_handle* out, void* stream);
@@ -588,10 +588,12 @@ TQ2_API tq2_status moe_route_backward(const void* logits, int64_t ld, int dtype,
  *   else TQ2_EINVAL.
  *
  * Calls of f32, and those of f16 and bf16 with at most 4 slots a matrix on
- * average (T*k <= 4 E): Gate and Up take x as q4_gemm takes it; the gated product
- * is kept in f32 and enters Down as f32 activations do (for f16 and bf16 as its
- * first f16 part alone, within 2^-11 of its magnitude).
- * f16 and bf16 calls with more: the weights are rounded to f16, rows of x and of
+ * average (T*k <= 4 E) or with a weight that may exceed 65504, the largest of
+ * f16 (|d| max(z, 15-z) in any of the handles): Gate and Up take x as q4_gemm
+ * takes it; the gated product is kept in f32 and enters Down as f32 activations
+ * do (for f16 and bf16 as its first f16 part alone, within 2^-11 of its
+ * magnitude).
+ * Other f16 and bf16 calls: the weights are rounded to f16, rows of x and of
  * the gated product are f16 scaled by a power of two each (of x so that its
  * largest element is just below 2^15; of the gated product by a bound of it,
  * |x|^2 times the bounds of Gate's and Up's row norms, so that elements below
