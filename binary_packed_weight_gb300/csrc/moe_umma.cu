@@ -33,8 +33,10 @@
 // f16 holds the activations because each row is scaled by a power of two: a
 // row of x so that its largest magnitude is 2^14..2^15, a hidden row by its
 // bound |x|^2 bound(Gate) bound(Up) (Cauchy-Schwarz; silu(v) <= |v|), which
-// can only be too large, by about 2^16 for ordinary rows, and leaves 13 binades
-// of full precision below them.
+// can only be too large, for ordinary rows by about 2 D, and keeps every bit of
+// values down to 2^-28 of it.  Where the rows of a matrix differ so much that its
+// smallest might fall below, hidden rows are written in f32 and scaled by their own
+// maximum in a pass of their own (own_scale; the rule and its cost are in q4_api.cu).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -98,7 +100,8 @@ struct MuArgs {
     const int* offsets;
     const int* slots;
     const float2* scales;                  // [position] of a row of x: 1/scale; of the hidden row: scale
-    __half* hidden;                        // pair: [position][N]
+    void* hidden;                          // pair: [position][N], f16 or (own_scale) f32
+    int own_scale;
     float* y;                              // else: [slot][N]
 };
 
@@ -108,6 +111,9 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
         "%16};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
         "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]) : "memory");
 }
+
+__device__ __forceinline__ void put_hidden(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put_hidden(__half* p, float v) { *p = __float2half_rn(v); }
 
 // Barrier of the epilogue warps.
 template <int WARPS>
@@ -528,16 +534,20 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
                 if (PAIR) {
                     constexpr int H = CW / 2;
                     const int c0 = cc + (upper ? H : 0), left = in ? m.cnt - c0 : 0;
-                    __half* out = a.hidden + (int64_t)(m.p0 + c0) * a.N + n;
+                    const int64_t at = (int64_t)(m.p0 + c0) * a.N + n;
+                    auto store = [&](auto* out, bool scaled) {
 #pragma unroll
-                    for (int i = 0; i < H; ++i, out += a.N) {
-                        const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? x[i] : x[H + i], 16);
-                        const float2 sc = bars->scale[c0 + i];
-                        const float gt = __uint_as_float(upper ? other : x[i]) * sc.x;
-                        const float up = __uint_as_float(upper ? x[H + i] : other) * sc.x;
-                        const float hv = __fdividef(gt, 1.0f + __expf(-gt)) * up;
-                        if (i < left) *out = __float2half_rn(hv * sc.y);
-                    }
+                        for (int i = 0; i < H; ++i, out += a.N) {
+                            const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? x[i] : x[H + i], 16);
+                            const float2 sc = bars->scale[c0 + i];
+                            const float gt = __uint_as_float(upper ? other : x[i]) * sc.x;
+                            const float up = __uint_as_float(upper ? x[H + i] : other) * sc.x;
+                            const float hv = __fdividef(gt, 1.0f + __expf(-gt)) * up;
+                            if (i < left) put_hidden(out, scaled ? hv * sc.y : hv);
+                        }
+                    };
+                    if (a.own_scale) store(static_cast<float*>(a.hidden) + at, false);
+                    else store(static_cast<__half*>(a.hidden) + at, true);
                 } else if (in) {
                     float* out = a.y + n;
                     const int left = m.cnt - cc;
@@ -626,6 +636,14 @@ moe_where_kernel(const int* __restrict__ offsets, const int* __restrict__ slots,
     where[plan_slot(slots, nslots, p)] = make_float2(__int_as_float(p), bound0[lo] * bound1[lo]);
 }
 
+// Exponent bits of the power of two that takes a row of largest magnitude m to 2^14..2^15, kept a
+// normal number with a normal inverse; 1 for a row of zeros or one with infinities.
+__device__ __forceinline__ int scale_exponent(float m) {
+    const int be = (__float_as_int(m) >> 23) & 255;
+    const int se = be == 0 ? 253 : 127 + 14 - (be - 127);
+    return m == 0.f || be == 255 ? 127 : min(se, 253);
+}
+
 // A CTA a token: its row of x as f16, scaled, at each of its positions, and the
 // scales.  A row is converted once for all its positions (a warp a position took 745
 // instructions for each: 21 us for 16384 slots of 2048, now 15; the whole call of 2048
@@ -664,10 +682,7 @@ moe_stage_kernel(const T* __restrict__ x, int64_t ldx, int vec, int D, const int
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = fmaxf(m, red[i]);
-    const int be = (__float_as_int(m) >> 23) & 255;
-    int se = be == 0 ? 253 : 127 + 14 - (be - 127);
-    if (m == 0.f || be == 255) se = 127;
-    se = se > 253 ? 253 : se;
+    const int se = scale_exponent(m);
     const float s = __int_as_float(se << 23);
     float ss = 0.f;
     for (int c = tid * 8; c < D; c += 2048) {
@@ -707,6 +722,38 @@ moe_stage_kernel(const T* __restrict__ x, int64_t ldx, int vec, int D, const int
         first[pos] = make_float2(inv, __int_as_float(hs << 23));
         second[pos] = make_float2(0.f, __int_as_float((254 - hs) << 23));
     }
+}
+
+// A CTA a position: its f32 gated row as f16, scaled by its own maximum, and the
+// scale for the second product.  (That product reads the plan before it waits, so it may
+// start only when this kernel has waited.)
+__global__ void __launch_bounds__(256)
+moe_rescale_kernel(const float* __restrict__ rows, const int* __restrict__ offsets, int nslots, int E, int F,
+                   __half* __restrict__ out, float2* __restrict__ second) {
+    __shared__ float red[8];
+    const int tid = threadIdx.x, p = blockIdx.x;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (p >= plan_offset(offsets, nslots, E)) return;
+    const float4* row = reinterpret_cast<const float4*>(rows + (int64_t)p * F);
+    float m = 0.f;
+    for (int c = tid; c < F / 4; c += 256) {
+        const float4 v = row[c];
+        m = fmaxf(fmaxf(fmaxf(m, fabsf(v.x)), fmaxf(fabsf(v.y), fabsf(v.z))), fabsf(v.w));
+    }
+    m = __int_as_float(__reduce_max_sync(0xffffffffu, __float_as_int(m)));
+    if ((tid & 31) == 0) red[tid >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, red[i]);
+    const int se = scale_exponent(m);
+    const float s = __int_as_float(se << 23);
+    for (int c = tid; c < F / 4; c += 256) {
+        const float4 v = row[c];
+        const __half2 h[2] = {__floats2half2_rn(v.x * s, v.y * s), __floats2half2_rn(v.z * s, v.w * s)};
+        reinterpret_cast<uint2*>(out + (int64_t)p * F)[c] = *reinterpret_cast<const uint2*>(h);
+    }
+    if (tid == 0) second[p] = make_float2(0.f, __int_as_float((254 - se) << 23));
 }
 
 template <int G, bool PAIR, bool WIDE>
@@ -756,9 +803,11 @@ size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
 
-// f16 rows of x and of the hidden values and two pairs of scales by position; a position and a bound by slot.
-size_t moe_tensor_scratch(int64_t nslots, int64_t D, int64_t F) {
-    return round256((size_t)nslots * D * 2) + round256((size_t)nslots * F * 2) + 3 * round256((size_t)nslots * 8);
+// f16 rows of x and of the hidden values and two pairs of scales by position; a position and a bound by slot;
+// the hidden values in f32 where they are scaled afterwards.
+size_t moe_tensor_scratch(int64_t nslots, int64_t D, int64_t F, bool own_scale) {
+    return round256((size_t)nslots * D * 2) + round256((size_t)nslots * F * 2) + 3 * round256((size_t)nslots * 8) +
+           (own_scale ? (size_t)nslots * F * 4 : 0);
 }
 
 cudaError_t launch_moe_tensor(const MoeTensor& m, void* scratch, cudaStream_t st) {
@@ -773,6 +822,8 @@ cudaError_t launch_moe_tensor(const MoeTensor& m, void* scratch, cudaStream_t st
     float2* second = reinterpret_cast<float2*>(at);
     at += round256((size_t)S * 8);
     float2* where = reinterpret_cast<float2*>(at);
+    at += round256((size_t)S * 8);
+    float* hid32 = reinterpret_cast<float*>(at);
     const int E = (int)m.gate->E;
     const unsigned T = (unsigned)(S / m.k);
     const int vec = (reinterpret_cast<uintptr_t>(m.x) & 15) == 0 && m.ldx % 8 == 0;
@@ -802,8 +853,12 @@ cudaError_t launch_moe_tensor(const MoeTensor& m, void* scratch, cudaStream_t st
     a.offsets = m.offsets;
     a.slots = m.slots;
     a.scales = first;
-    a.hidden = hid;
+    a.hidden = m.own_scale ? static_cast<void*>(hid32) : hid;
+    a.own_scale = m.own_scale ? 1 : 0;
     e = launch_by_group<true>(m.gate->group, xs, a, st);
+    if (e == cudaSuccess && m.own_scale)
+        e = launch_pdl(moe_rescale_kernel, dim3((unsigned)S), dim3(256), 0, st, static_cast<const float*>(hid32),
+                       m.offsets, (int)S, E, (int)F, hid, second);
     if (e != cudaSuccess) return e;
     MuArgs b = a;
     b.w0 = m.down->blocks;

@@ -122,6 +122,7 @@ struct q4_weight {
     int64_t mstride = 0;               // bytes of one matrix
     uint8_t* blocks = nullptr;
     float* bound = nullptr;            // [E] no row of W[e] has a larger 2-norm
+    float spread = 1.f;                // within a matrix at most: largest row norm / smallest that is not 0
     float most = 0.f;                  // no weight is larger in magnitude (Inf or NaN where a scale is)
 };
 
@@ -130,7 +131,10 @@ namespace tq2 {
 // q4_pack.cu
 cudaError_t launch_q4_pack(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, const q4_weight* w,
                            cudaStream_t st);
-cudaError_t launch_q4_bound(const uint16_t* scales, const uint8_t* zeros, const q4_weight* w, cudaStream_t st);
+// bound[E], each matrix's smallest row norm that is not 0 [E] and the largest weight [1], one after the other
+constexpr size_t q4_bounds(int64_t E) { return (size_t)(2 * E + 1); }
+cudaError_t launch_q4_bound(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, const q4_weight* w,
+                            cudaStream_t st);
 cudaError_t launch_q4_dequant(const q4_weight* w, float* out, cudaStream_t st);
 cudaError_t launch_q4_quantize(const void* w, int dtype, int64_t rows, int64_t K, int group, uint8_t* codes,
                                uint16_t* scales, uint8_t* zeros, cudaStream_t st);
@@ -182,8 +186,9 @@ struct MoeTensor {
     const int* slots;
     int nslots, k;
     float* y;                          // [slot][D]
+    bool own_scale;                    // gated rows are scaled by their own maximum, in a pass of their own
 };
-size_t moe_tensor_scratch(int64_t nslots, int64_t D, int64_t F);
+size_t moe_tensor_scratch(int64_t nslots, int64_t D, int64_t F, bool own_scale);
 cudaError_t launch_moe_tensor(const MoeTensor& m, void* scratch, cudaStream_t st);
 unsigned int read_clear_dev_error_moe_umma(cudaStream_t st);
 

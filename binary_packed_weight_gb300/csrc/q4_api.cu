@@ -164,6 +164,18 @@ constexpr int64_t MOE_TENSOR_ROWS = 4;
 // integers' sums in f32 and take any.  (A group's scale may be up to 65504, its weights 15 times that.)
 bool fits_f16(const q4_weight* w) { return w->most <= 65504.f; }
 
+// Whether the gated rows need a scale of their own.  The tensor-core path scales them as it
+// makes them, by the bound |x|^2 |Gate row| |Up row| of the matrix's largest rows.  Products
+// are about 1/sqrt(D) of |x| |row|, so values of a matrix's smallest rows are spread_gate
+// spread_up D below the bound; f16 keeps 2^28 below it without losing bits, and four
+// of its binades are left to rows of x that meet the weights less than chance would.
+// (Of outputs to which all rows contribute alike, D = 7168: off by 2.1e-4 up to a spread
+// of 2^11, 6.7e-4 at 2^14, 4e-2 at 2^20.)  With a pass of its own the scale is the row's
+// maximum: 64 experts of 2048x1024 bf16, top 8, 2048 tokens 208 -> 241 us, 64 tokens 68 -> 72.
+bool own_scale(const q4_weight* gate, const q4_weight* up) {
+    return !((double)gate->spread * up->spread * (double)gate->K <= 0x1p24);
+}
+
 // Scratch of one call, given back on the same stream whatever happens.
 struct Scratch {
     void* p = nullptr;
@@ -218,9 +230,9 @@ tq2_status q4_upload(const uint8_t* codes, const uint16_t* scales, const uint8_t
     const size_t ngroups = (size_t)E * N * (K / group);
     void* tmp[3] = {nullptr, nullptr, nullptr};
     const void* dev[3] = {nullptr, nullptr, nullptr};
-    // the bounds sit behind the blocks, the largest weight behind them
+    // the bounds sit behind the blocks
     const size_t blocks_bytes = ((size_t)E * w->mstride + 255) / 256 * 256;
-    cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&w->blocks), blocks_bytes + (size_t)(E + 1) * 4);
+    cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&w->blocks), blocks_bytes + q4_bounds(E) * 4);
     if (e == cudaSuccess) w->bound = reinterpret_cast<float*>(w->blocks + blocks_bytes);
     if (e == cudaSuccess) e = to_device(codes, (size_t)E * N * (K / 2), &tmp[0], &dev[0], st);
     if (e == cudaSuccess) e = to_device(scales, ngroups * 2, &tmp[1], &dev[1], st);
@@ -229,8 +241,10 @@ tq2_status q4_upload(const uint8_t* codes, const uint16_t* scales, const uint8_t
         e = launch_q4_pack(static_cast<const uint8_t*>(dev[0]), static_cast<const uint16_t*>(dev[1]),
                            static_cast<const uint8_t*>(dev[2]), w, st);
     if (e == cudaSuccess)
-        e = launch_q4_bound(static_cast<const uint16_t*>(dev[1]), static_cast<const uint8_t*>(dev[2]), w, st);
-    if (e == cudaSuccess) e = cudaMemcpyAsync(&w->most, w->bound + E, 4, cudaMemcpyDeviceToHost, st);
+        e = launch_q4_bound(static_cast<const uint8_t*>(dev[0]), static_cast<const uint16_t*>(dev[1]),
+                            static_cast<const uint8_t*>(dev[2]), w, st);
+    float bounds[q4_bounds(1024)];
+    if (e == cudaSuccess) e = cudaMemcpyAsync(bounds, w->bound, q4_bounds(E) * 4, cudaMemcpyDeviceToHost, st);
     for (void* p : tmp)
         if (p) cudaFreeAsync(p, st);
     const cudaError_t done = cudaStreamSynchronize(st);        // the caller's planes are read, whatever happened
@@ -240,6 +254,9 @@ tq2_status q4_upload(const uint8_t* codes, const uint16_t* scales, const uint8_t
         delete w;
         return cuda_status(e, "q4_upload");
     }
+    for (int64_t i = 0; i < E; ++i)
+        if (bounds[i] > w->spread * bounds[E + i]) w->spread = bounds[i] / bounds[E + i];
+    w->most = bounds[2 * E];
     *out = w;
     return TQ2_OK;
 }
@@ -345,12 +362,14 @@ tq2_status moe_experts(q4_handle gate, q4_handle up, q4_handle down, const void*
     Scratch mem(st);
     const size_t ybytes = ((size_t)S * D * 4 + 255) / 256 * 256;
     if (dtype != TQ2_F32 && S > MOE_TENSOR_ROWS * E && fits_f16(gate) && fits_f16(up) && fits_f16(down)) {
-        cudaError_t e = scratch_alloc(&mem.p, ybytes + moe_tensor_scratch(S, D, F), st);
+        const bool own = own_scale(gate, up);
+        cudaError_t e = scratch_alloc(&mem.p, ybytes + moe_tensor_scratch(S, D, F, own), st);
         if (e != cudaSuccess) {
             mem.p = nullptr;
             return cuda_status(e, "moe_experts: scratch");
         }
-        const MoeTensor m{gate, up, down, x, ldx, dtype, ids, offsets, slots, (int)S, k, static_cast<float*>(mem.p)};
+        const MoeTensor m{gate, up, down, x, ldx, dtype, ids, offsets, slots, (int)S, k, static_cast<float*>(mem.p),
+                          own};
         e = launch_moe_tensor(m, static_cast<char*>(mem.p) + ybytes, st);
         if (e == cudaSuccess) e = combine(m.y);
         return cuda_status(e, "moe_experts: tensor path");

@@ -56,34 +56,48 @@ q4_pack_kernel(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ s
     }
 }
 
-// A warp a row: its 2-norm is at most sqrt(G sum_g (d_g max|c - z_g|)^2); the
-// largest of a matrix, as the bits of a non-negative float (a maximum has no order).
-// Behind the E bounds: the largest |d_g| max|c - z_g| of all, which as bits keeps a NaN.
+// A warp a row: its 2-norm from the integers' squares, which are exact, each eight of
+// them scaled by d^2; (1 + 2^-10) times that, so that no rounding makes a bound too small.
+// A matrix's largest and smallest (of rows that are not 0) and the largest |d| max|c - z|
+// of all are kept as the bits of non-negative floats: they have the floats' order,
+// extremes have none of their own, and a largest NaN stays.
 __global__ void __launch_bounds__(256)
-q4_bound_kernel(const uint16_t* __restrict__ scales, const uint8_t* __restrict__ zeros, float* __restrict__ bound,
-                int64_t N, int64_t kg, int G) {
+q4_bound_kernel(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ scales,
+                const uint8_t* __restrict__ zeros, float* __restrict__ bound, int64_t N, int64_t K, int G) {
     const int lane = threadIdx.x & 31;
-    int* largest = reinterpret_cast<int*>(bound) + gridDim.y;
+    int* of = reinterpret_cast<int*>(bound);
+    const int64_t kg = K / G;
+    codes += (int64_t)blockIdx.y * N * (K / 2);
     scales += (int64_t)blockIdx.y * N * kg;
     if (zeros) zeros += (int64_t)blockIdx.y * N * kg;
-    float most = 0.f;
-    int weight = 0;
+    int most = 0, least = 0x7F7F7F7F, weight = 0;
     for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < N; r += (int64_t)gridDim.x * 8) {
         float s = 0.f;
-        for (int64_t i = lane; i < kg; i += 32) {
-            const int z = zeros ? zeros[r * kg + i] & 15 : 8;
-            const float v = __half2float(__ushort_as_half(scales[r * kg + i])) * (float)(z > 15 - z ? z : 15 - z);
-            weight = max(weight, __float_as_int(v) & 0x7FFFFFFF);
-            s = fmaf(v, v, s);
+        for (int64_t k = lane * 8; k < K; k += 256) {
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(codes + r * (K / 2) + k / 2);
+            const uint32_t p = src[0] | ((uint32_t)src[1] << 16);
+            const int z = zeros ? zeros[r * kg + k / G] & 15 : 8;
+            const float d = __half2float(__ushort_as_half(scales[r * kg + k / G]));
+            int q = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = (int)((p >> (4 * i)) & 15u) - z;
+                q += c * c;
+            }
+            weight = max(weight, __float_as_int(d * (float)max(z, 15 - z)) & 0x7FFFFFFF);
+            s = fmaf(d * d, (float)q, s);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        most = fmaxf(most, sqrtf(s * (float)G));
+        const int norm = __float_as_int(sqrtf(s) * (1.f + 0x1p-10f)) & 0x7FFFFFFF;
+        most = max(most, norm);
+        if (norm > 0) least = min(least, norm);
     }
     weight = __reduce_max_sync(0xffffffffu, weight);
     if (lane == 0) {
-        atomicMax(reinterpret_cast<int*>(bound) + blockIdx.y, __float_as_int(most));
-        atomicMax(largest, weight);
+        atomicMax(of + blockIdx.y, most);
+        atomicMin(of + gridDim.y + blockIdx.y, least);
+        atomicMax(of + 2 * gridDim.y, weight);
     }
 }
 
@@ -176,12 +190,13 @@ cudaError_t launch_q4_pack(const uint8_t* codes, const uint16_t* scales, const u
     return cudaGetLastError();
 }
 
-cudaError_t launch_q4_bound(const uint16_t* scales, const uint8_t* zeros, const q4_weight* w, cudaStream_t st) {
-    cudaError_t e = cudaMemsetAsync(w->bound, 0, (size_t)(w->E + 1) * 4, st);
+cudaError_t launch_q4_bound(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, const q4_weight* w,
+                            cudaStream_t st) {
+    cudaError_t e = cudaMemsetAsync(w->bound, 0, q4_bounds(w->E) * 4, st);
+    if (e == cudaSuccess) e = cudaMemsetAsync(w->bound + w->E, 0x7F, (size_t)w->E * 4, st);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((w->N + 7) / 8 < 256 ? (w->N + 7) / 8 : 256);
-    q4_bound_kernel<<<dim3(grid, (unsigned)w->E), 256, 0, st>>>(scales, zeros, w->bound, w->N, w->K / w->group,
-                                                               w->group);
+    q4_bound_kernel<<<dim3(grid, (unsigned)w->E), 256, 0, st>>>(codes, scales, zeros, w->bound, w->N, w->K, w->group);
     return cudaGetLastError();
 }
 

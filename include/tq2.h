@@ -451,7 +451,8 @@ typedef struct q4_weight* q4_handle;
  *
  * The handle holds one copy in 16-row x 256-k blocks (codes, then the block's
  * scales and zero points), N padded to 128 rows and K to 256, and a bound of
- * each matrix's row norms and the weights' largest magnitude (for moe_experts).
+ * each matrix's row norms, the spread of those norms and the weights' largest
+ * magnitude (for moe_experts).
  */
 TQ2_API tq2_status q4_upload(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, int64_t E,
                              int64_t N, int64_t K, int group, q4_handle* out, void* stream);
@@ -596,12 +597,16 @@ TQ2_API tq2_status moe_route_backward(const void* logits, int64_t ld, int dtype,
  * Other f16 and bf16 calls: the weights are rounded to f16, rows of x and of
  * the gated product are f16 scaled by a power of two each (of x so that its
  * largest element is just below 2^15; of the gated product by a bound of it,
- * |x|^2 times the bounds of Gate's and Up's row norms, so that elements below
- * 2^-28 of that bound lose bits), and a product's sum over k runs in f32.
+ * |x|^2 times Gate's and Up's largest row norms in the matrix, so that elements
+ * below 2^-28 of that bound lose bits), and a product's sum over k runs in f32.
+ * Where Gate's largest row norm over its smallest (but 0) in some matrix, times
+ * Up's, times D is above 2^24, a row of the gated product is scaled by its own
+ * maximum instead, like a row of x.
  * Either way a token's sum over j runs in the order of j, in f32, and is
  * rounded once to dtype.
  * Scratch from the library's stream-ordered pool: T*k rows of D floats, and of F
- * floats (f16 and bf16 calls with many slots: of F and of D halves).  Asynchronous.
+ * floats (f16 and bf16 calls with many slots: of F and of D halves, and of F
+ * floats where gated rows are scaled by themselves).  Asynchronous.
  */
 TQ2_API tq2_status moe_experts(q4_handle gate, q4_handle up, q4_handle down, const void* x, int64_t ldx, int dtype,
                                const int32_t* ids, const float* weights, const int32_t* offsets,

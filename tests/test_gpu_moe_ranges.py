@@ -71,3 +71,22 @@ def test_experts_of_large_weights(lib, dtype, large, T):
     assert np.all(np.isfinite(got))
     # (f16 outputs in its subnormal range are off by 2^-25 at most)
     assert np.linalg.norm(got - want) < NORM[dtype][1] * np.linalg.norm(want) + 2.0 ** -25 * np.sqrt(want.size)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("T", [8, 40, 300])
+@pytest.mark.parametrize("factor", [30.0, 1000.0])
+def test_experts_with_a_few_large_rows(lib, dtype, T, factor):
+    """32 of Gate's and Up's rows are `factor` times the others and Down's columns that meet them as much smaller, so
+    that all gated values count alike, large and ordinary ones."""
+    rng = np.random.default_rng(72)
+    E, D, F = 2, 1024, 512
+    rows = np.ones((E, F, 1))
+    rows[:, 64:96] = factor
+    columns = np.full((E, 1, F // 32), 200.0)
+    columns[:, :, 2] /= factor ** 2
+    mats, handles = layer(lib, rng, E, D, F, gate=rows, up=rows, down=columns)
+    ids = (np.arange(T) % E)[:, None]
+    w = np.ones((T, 1), np.float32)
+    x, got = run_experts(lib, rng.normal(size=(T, D)) * 0.2, ids, w, handles, dtype, E)
+    assert norm_error(got, omoe.experts(x, ids, w, *mats)) < NORM[dtype][T > 4 * E]
