@@ -35,10 +35,16 @@ cudaError_t scratch_pool(cudaMemPool_t* pool) {
     props.allocType = cudaMemAllocationTypePinned;
     props.location.type = cudaMemLocationTypeDevice;
     props.location.id = dev;
-    e = cudaMemPoolCreate(pool, &props);
+    // The first call may be part of a capture.  Making a pool is no work of a stream, but this thread may
+    // not do it during one unless it says so.
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    e = cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) return e;
+    e = cudaMemPoolCreate(pool, &props);
     uint64_t keep = ~uint64_t(0);
-    e = cudaMemPoolSetAttribute(*pool, cudaMemPoolAttrReleaseThreshold, &keep);
+    if (e == cudaSuccess) e = cudaMemPoolSetAttribute(*pool, cudaMemPoolAttrReleaseThreshold, &keep);
+    const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e == cudaSuccess) e = back;
     if (e != cudaSuccess) return e;
     pools[dev].store(*pool, std::memory_order_release);
     return cudaSuccess;
