@@ -16,7 +16,7 @@ __all__ = [
     "load", "lib_path", "TQ2Error", "Weight", "tq2_upload", "tq2_gemm", "tq2_gemm_path", "tq2_gemm_tensor_tuned",
     "tq2_gemm_skinny_static", "tq2_gemm_grouped", "GroupedGemv", "tq2_unpack", "tq2_dequant_f16", "tq2_quantize", "blr_expand_bits", "blr_forward", "blr_backward", "blr_forward_paths", "blr_backward_paths", "blr_sign_grads",
     "Q4Weight", "q4_upload", "q4_dequant", "q4_quantize", "q4_gemm", "moe_route", "moe_route_backward", "moe_experts",
-    "device_status", "debug_wait_timeout", "PATH_AUTO", "PATH_SKINNY", "PATH_TENSOR",
+    "device_status", "release_scratch", "debug_wait_timeout", "PATH_AUTO", "PATH_SKINNY", "PATH_TENSOR",
 ]
 
 PATH_AUTO, PATH_SKINNY, PATH_TENSOR = 0, 1, 2
@@ -30,6 +30,7 @@ _SIGS = {
     "tq2_last_error": (ctypes.c_char_p, []),
     "tq2_version": (ctypes.c_char_p, []),
     "tq2_device_status": (_I, [_P]),
+    "tq2_release_scratch": (_I, []),
     "tq2_debug_wait_timeout": (_I, [ctypes.c_uint64, _P]),
     "tq2_upload": (_I, [_P, _I64, _I64, ctypes.POINTER(_P), _P]),
     "tq2_free": (_I, [_P]),
@@ -477,3 +478,8 @@ def debug_wait_timeout(limit_ns, stream=None):
 def device_status(stream=None):
     """Synchronize and raise if a kernel recorded a bounded-wait timeout."""
     _check(load().tq2_device_status(_stream(stream)), "tq2_device_status")
+
+
+def release_scratch():
+    """Give back the device memory that the library keeps for the scratch of later calls."""
+    _check(load().tq2_release_scratch(), "tq2_release_scratch")

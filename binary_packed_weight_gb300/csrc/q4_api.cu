@@ -14,13 +14,14 @@
 
 namespace tq2 {
 
+constexpr int MAX_DEVICES = 64;
+static std::atomic<cudaMemPool_t> pools[MAX_DEVICES];   // of scratch, by device
+
 // The library's stream-ordered pool of a device: like the device's default
 // pool, except that freed scratch stays reserved over synchronizations (the
 // default pool gives it back to the driver at each one, and the next call
 // pays for mapping it again).
 cudaError_t scratch_pool(cudaMemPool_t* pool) {
-    constexpr int MAX_DEVICES = 64;
-    static std::atomic<cudaMemPool_t> pools[MAX_DEVICES];
     static std::mutex lock;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -211,6 +212,16 @@ Q4Stream stream_of(const q4_weight* w) {
 using namespace tq2;
 
 extern "C" {
+
+tq2_status tq2_release_scratch(void) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev < MAX_DEVICES) {
+        cudaMemPool_t pool = pools[dev].load(std::memory_order_acquire);
+        if (pool) e = cudaMemPoolTrimTo(pool, 0);
+    }
+    return cuda_status(e, "tq2_release_scratch");
+}
 
 tq2_status q4_upload(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, int64_t E, int64_t N,
                      int64_t K, int group, q4_handle* out, void* stream) {

@@ -83,6 +83,16 @@ TQ2_API const char* tq2_version(void);
 TQ2_API tq2_status tq2_device_status(void* stream);
 
 /*
+ * Give back to the device what the library's memory pool of the current
+ * device holds and no call is using.  moe_route (plans of many tokens) and
+ * moe_experts take their scratch from that pool, and it keeps what they took
+ * (gigabytes after a call of many tokens) for the next call; the scratch of
+ * work still pending on a stream is in use.  The next call takes memory from
+ * the device again.  Not during a capture.
+ */
+TQ2_API tq2_status tq2_release_scratch(void);
+
+/*
  * tq2_debug_wait_timeout -- test export for the error path above: launches
  * one thread that waits, with a bound of limit_ns, on a shared-memory
  * barrier that nothing completes.  When the bound runs out it records the
@@ -604,7 +614,8 @@ TQ2_API tq2_status moe_route_backward(const void* logits, int64_t ld, int dtype,
  * maximum instead, like a row of x.
  * Either way a token's sum over j runs in the order of j, in f32, and is
  * rounded once to dtype.
- * Scratch from the library's stream-ordered pool: T*k rows of D floats, and of F
+ * Scratch from the library's stream-ordered pool, which keeps it
+ * (tq2_release_scratch): T*k rows of D floats, and of F
  * floats (f16 and bf16 calls with many slots: of F and of D halves, and of F
  * floats where gated rows are scaled by themselves).  Asynchronous.
  */

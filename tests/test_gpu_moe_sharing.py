@@ -94,3 +94,19 @@ def test_layers_on_two_streams(lib):
     for c, w in zip(calls, want):
         assert torch.equal(c[1], w)
     lib.device_status()
+
+
+def test_scratch_is_given_back_on_request(lib):
+    import torch
+    call, out, _, _ = moe_call(lib, np.random.default_rng(83), 20000, D=1024)
+    torch.cuda.synchronize()
+    lib.release_scratch()
+    before = torch.cuda.mem_get_info()[0]
+    call()
+    torch.cuda.synchronize()
+    held = before - torch.cuda.mem_get_info()[0]
+    assert held >= 20000 * 2 * 1024 * 4                                  # the slots' outputs, kept for the next call
+    lib.release_scratch()
+    assert before - torch.cuda.mem_get_info()[0] <= held // 8
+    want = out.clone()
+    assert torch.equal(call(), want)                                     # and taken again
