@@ -357,6 +357,13 @@ def _on(t, stream):
     return _raw_stream(t.get_device())
 
 
+def _group(group, where):
+    """A group size by which K can be divided (which ones there are the library says)."""
+    if group < 1:
+        raise ValueError(f"{where}: group must be 32, 64 or 128, got {group}")
+    return group
+
+
 def q4_upload(codes, scales, zeros=None, group=128, stream=None):
     """4-bit weights -> :class:`Q4Weight`.  ``codes`` uint8 [E, N, K/2] or [N, K/2] (even k in the low
     half byte), ``scales`` float16 and ``zeros`` uint8 (or None: 8) [.., N, K/group]; CPU or CUDA tensors."""
@@ -364,6 +371,7 @@ def q4_upload(codes, scales, zeros=None, group=128, stream=None):
     if len(shape) != 3:
         raise ValueError(f"q4_upload: codes must be [E, N, K/2] or [N, K/2], got {list(codes.shape)}")
     E, N, K = shape[0], shape[1], 2 * shape[2]
+    _group(group, "q4_upload")
     lead = tuple(codes.shape)[:-1]
     _plane(codes, lead + (K // 2,), "uint8", "q4_upload", "codes", host=True)
     _plane(scales, lead + (K // group,), "float16", "q4_upload", "scales", host=True)
@@ -385,7 +393,10 @@ def q4_dequant(w, out, stream=None):
 
 def q4_quantize(w, codes, scales, zeros=None, group=128, stream=None):
     """Plain weights [.., N, K] to the planes :func:`q4_upload` takes (see include/tq2.h)."""
+    if w.dim() < 1:
+        raise ValueError("q4_quantize: w must have rows of K weights, got a scalar")
     K = w.shape[-1]
+    _group(group, "q4_quantize")
     lead = tuple(w.shape)[:-1]
     if not (w.is_contiguous() and w.is_cuda):
         raise ValueError("q4_quantize: w must be contiguous and on the GPU")

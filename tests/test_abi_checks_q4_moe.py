@@ -133,3 +133,16 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(lib):
     with pytest.raises(ValueError, match="on the GPU"):
         bpw.moe_experts(w, w, w, x, ids, wt, torch.zeros(2, dtype=torch.int32), torch.zeros(8, dtype=torch.int32),
                         torch.zeros_like(x))
+
+
+def test_binding_refuses_groups_that_divide_nothing(lib):
+    import torch
+    import binary_packed_weight_gb300 as bpw
+    codes, scales = torch.zeros((2, 64), dtype=torch.uint8), torch.zeros((2, 1), dtype=torch.float16)
+    for group in (0, -32):
+        with pytest.raises(ValueError, match="group must be"):
+            bpw.q4_upload(codes, scales, group=group)
+        with pytest.raises(ValueError, match="group must be"):
+            bpw.q4_quantize(torch.zeros((2, 128)), codes, scales, group=group)
+    with pytest.raises(ValueError, match="scalar"):
+        bpw.q4_quantize(torch.zeros(()), codes, scales)
