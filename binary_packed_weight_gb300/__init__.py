@@ -118,8 +118,8 @@ class Weight:
 
     def free(self):
         if self._h:
-            _check(load().tq2_free(self._h), "tq2_free")
-            self._h = None
+            h, self._h = self._h, None                     # taken back even where an error is reported
+            _check(load().tq2_free(h), "tq2_free")
 
     def __del__(self):
         try:
@@ -290,8 +290,8 @@ class Q4Weight:
 
     def free(self):
         if self._h:
-            _check(load().q4_free(self._h), "q4_free")
-            self._h = None
+            h, self._h = self._h, None                     # taken back even where an error is reported
+            _check(load().q4_free(h), "q4_free")
 
     def __del__(self):
         try:

@@ -146,3 +146,23 @@ def test_binding_refuses_groups_that_divide_nothing(lib):
             bpw.q4_quantize(torch.zeros((2, 128)), codes, scales, group=group)
     with pytest.raises(ValueError, match="scalar"):
         bpw.q4_quantize(torch.zeros(()), codes, scales)
+
+
+@pytest.mark.parametrize("kind", ["q4", "tq2"])
+def test_a_handle_is_freed_once_whatever_the_library_reports(lib, monkeypatch, kind):
+    """The library deletes a handle before it reports that its memory could not be freed."""
+    import binary_packed_weight_gb300 as bpw
+    freed = []
+
+    class Failing:
+        tq2_last_error = staticmethod(lambda: b"planted")
+        tq2_status_string = staticmethod(lambda status: b"CUDA error")
+        q4_free = staticmethod(lambda h: freed.append(h) or 4)
+        tq2_free = q4_free
+    monkeypatch.setattr(bpw, "_lib", Failing)
+    w = bpw.Q4Weight(A, 1, 16, 128, 128) if kind == "q4" else bpw.Weight(A, 16, 128)
+    with pytest.raises(bpw.TQ2Error):
+        w.free()
+    w.free()
+    del w
+    assert freed == [A]
