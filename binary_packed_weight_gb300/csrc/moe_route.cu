@@ -590,6 +590,7 @@ __global__ void __launch_bounds__(256) moe_route_backward_kernel(const __grid_co
 #pragma unroll
             for (int i = 0; i < V; ++i) out[i] = x[i] * c;
         }
+        __syncwarp();                                      // dlogits may be the logits: every lane has read the row
         store_row<T, V>(drow, a.E, lane, a.vecd != 0, out);
         __syncwarp();
         if (on) drow[id] = from_f32<T>(mine);

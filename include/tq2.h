@@ -573,8 +573,9 @@ TQ2_API tq2_status moe_route(const void* logits, int64_t ld, int dtype, const fl
  *             with renorm and S >= 2^-126 the sum is 0 and only the selected get a gradient)
  *   sigmoid:  dlogits[e] = p_e (1 - p_e) q_e
  * ids as moe_route returned them; a slot of -1 takes no part.  dlogits: DEVICE,
- * dtype, T rows of E, ldd >= E elements apart, overwritten.  Limits as
- * moe_route.  Asynchronous, no scratch.
+ * dtype, T rows of E, ldd >= E elements apart, overwritten; may be logits itself
+ * (ldd = ld), else overlaps none of the inputs.  Limits as moe_route.
+ * Asynchronous, no scratch.
  */
 TQ2_API tq2_status moe_route_backward(const void* logits, int64_t ld, int dtype, const float* bias,
                                       const int32_t* ids, const float* dweights, void* dlogits, int64_t ldd,

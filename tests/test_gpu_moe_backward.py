@@ -94,3 +94,19 @@ def test_backward_where_the_sum_is_clamped(lib, score):
     dw = rng.normal(size=(20, k)).astype(np.float32)
     got = backward(lib, l, ids, dw, score=score, scale=2.5, bias=bias)
     check_backward(got, l, ids, dw, 2.5, bias, score, True)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("E", [60, 1000])
+def test_backward_in_place(lib, score, renorm, E):
+    """dlogits may be the logits' own memory."""
+    import torch
+    rng = np.random.default_rng(63)
+    l = torch.from_numpy(rng.normal(size=(700, E)).astype(np.float32)).cuda()
+    ids = torch.topk(l, 8).indices.int()
+    dw = torch.from_numpy(rng.normal(size=(700, 8)).astype(np.float32)).cuda()
+    want = lib.moe_route_backward(l, ids, dw, torch.empty_like(l), score=score, renorm=renorm)
+    got = l.clone()
+    lib.moe_route_backward(got, ids, dw, got, score=score, renorm=renorm)
+    assert torch.equal(got, want)
