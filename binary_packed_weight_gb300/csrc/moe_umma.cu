@@ -520,8 +520,7 @@ moe_umma_kernel(const __grid_constant__ MuMaps maps, const __grid_constant__ MuA
             uint32_t v[CW], w[CW];
             // the columns after the ones at hand are read ahead; with the last ones the accumulator is handed back
             auto read = [&](uint32_t (&x)[CW], int cc) {
-                if constexpr (CW == 32) tmem_ld_32x32b_x32(lane_addr + (uint32_t)cc, x);
-                else tmem_ld_32x32b_x16(lane_addr + (uint32_t)cc, x);
+                tmem_ld_32x32b_x16(lane_addr + (uint32_t)cc, x);
                 tmem_wait_ld();
                 if (cc + STEP >= m.cnt) {
                     tc_fence_before();

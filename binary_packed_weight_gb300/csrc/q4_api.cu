@@ -113,43 +113,36 @@ __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float v) { retu
 template <class T>
 __global__ void __launch_bounds__(256)
 moe_combine_kernel(const float* __restrict__ y, const int32_t* __restrict__ ids, const float* __restrict__ weights,
-                   T* __restrict__ out, int64_t ldo, int64_t T_, int D, int k, int vec) {
+                   T* __restrict__ out, int64_t ldo, int64_t T_, int D, int k) {
     pdl_launch_dependents();
     pdl_wait();
     const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 4;
-    if (c >= D) return;
+    if (c >= D) return;                                    // (D is a multiple of 32)
     for (int64_t t = blockIdx.x; t < T_; t += gridDim.x) {
         float s[4] = {0.f, 0.f, 0.f, 0.f};
         const float* p = y + t * k * D + c;
-        if (vec) {
-            for (int j0 = 0; j0 < k; j0 += 4) {
-                float4 v[4];
-                float w[4];
-                bool on[4];
+        for (int j0 = 0; j0 < k; j0 += 4) {
+            float4 v[4];
+            float w[4];
+            bool on[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = j0 + i;
-                    on[i] = j < k && ids[t * k + j] >= 0;
-                    w[i] = on[i] ? weights[t * k + j] : 0.f;
-                    if (on[i]) v[i] = __ldcs(reinterpret_cast<const float4*>(p + (int64_t)j * D));
+            for (int i = 0; i < 4; ++i) {
+                const int j = j0 + i;
+                on[i] = j < k && ids[t * k + j] >= 0;
+                w[i] = on[i] ? weights[t * k + j] : 0.f;
+                if (on[i]) v[i] = __ldcs(reinterpret_cast<const float4*>(p + (int64_t)j * D));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (on[i]) {
+                    s[0] = fmaf(w[i], v[i].x, s[0]);
+                    s[1] = fmaf(w[i], v[i].y, s[1]);
+                    s[2] = fmaf(w[i], v[i].z, s[2]);
+                    s[3] = fmaf(w[i], v[i].w, s[3]);
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (on[i]) {
-                        s[0] = fmaf(w[i], v[i].x, s[0]);
-                        s[1] = fmaf(w[i], v[i].y, s[1]);
-                        s[2] = fmaf(w[i], v[i].z, s[2]);
-                        s[3] = fmaf(w[i], v[i].w, s[3]);
-                    }
-            }
-        } else {
-            for (int j = 0; j < k; ++j) {
-                if (ids[t * k + j] < 0) continue;
-                const float w = weights[t * k + j];
-                for (int i = 0; i < 4 && c + i < D; ++i) s[i] = fmaf(w, p[(int64_t)j * D + i], s[i]);
-            }
         }
-        for (int i = 0; i < 4 && c + i < D; ++i) out[t * ldo + c + i] = round_to<T>(s[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[t * ldo + c + i] = round_to<T>(s[i]);
     }
 }
 
@@ -159,7 +152,7 @@ cudaError_t launch_combine(const float* y, const int32_t* ids, const float* w, v
     const unsigned gy = (unsigned)((D + 1023) / 1024);
     const unsigned gx = (unsigned)(T_ < 16384 ? T_ : 16384);
     return launch_pdl(moe_combine_kernel<T>, dim3(gx, gy), dim3(256), 0, st, y, ids, w, reinterpret_cast<T*>(out),
-                      ldo, T_, D, k, D % 4 == 0 ? 1 : 0);
+                      ldo, T_, D, k);
 }
 
 // Average rows of a matrix above which f16 and bf16 calls take the tensor-core

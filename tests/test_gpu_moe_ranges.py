@@ -53,7 +53,7 @@ def test_experts_on_both_sides_of_the_tensor_cores(lib, dtype, T):
 
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
 @pytest.mark.parametrize("large", ["gate", "up", "down"])
-@pytest.mark.parametrize("T", [8, 9, 300])
+@pytest.mark.parametrize("T", [8, 9, 12, 300])
 def test_experts_of_large_weights(lib, dtype, large, T):
     """Scales up to the largest of f16: a weight is up to 15 times as much, beyond f16 itself."""
     rng = np.random.default_rng(71)
