@@ -810,6 +810,7 @@ size_t moe_tensor_scratch(int64_t nslots, int64_t D, int64_t F, bool own_scale) 
 }
 
 cudaError_t launch_moe_tensor(const MoeTensor& m, void* scratch, cudaStream_t st) {
+    g_launched.store(true, std::memory_order_release);
     const int64_t S = m.nslots, D = m.gate->K, F = m.gate->N;
     char* at = static_cast<char*>(scratch);
     __half* xs = reinterpret_cast<__half*>(at);
@@ -874,12 +875,6 @@ cudaError_t launch_moe_tensor(const MoeTensor& m, void* scratch, cudaStream_t st
     return launch_by_group<false>(m.down->group, hid, b, st);
 }
 
-unsigned int read_clear_dev_error_moe_umma(cudaStream_t st) {
-    unsigned int v = 0, z = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, g_dev_error, sizeof(v), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess) return 0;
-    cudaMemcpyToSymbolAsync(g_dev_error, &z, sizeof(z), 0, cudaMemcpyHostToDevice, st);
-    cudaStreamSynchronize(st);
-    return v;
-}
+unsigned int read_clear_dev_error_moe_umma(cudaStream_t st) { return read_clear_record(st); }
 
 }  // namespace tq2

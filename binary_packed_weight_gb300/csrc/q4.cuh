@@ -23,6 +23,7 @@
 // of a lane: its B fragments of 32 k are 16 bytes of one activation row.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -100,6 +101,19 @@ __device__ __forceinline__ void q4_decode(uint32_t w, uint32_t m, const Q4Zero& 
             a[i] = *reinterpret_cast<const uint32_t*>(&r);
         }
     }
+}
+
+// This file's error record, read and cleared.  Until one of its kernels has been launched there is nothing
+// in it, and a program that uses other calls pays for no round trip (nor for loading the kernels).
+static std::atomic<bool> g_launched{false};
+[[maybe_unused]] static unsigned int read_clear_record(cudaStream_t st) {
+    if (!g_launched.load(std::memory_order_acquire)) return 0;
+    unsigned int v = 0;
+    const unsigned int none = 0;
+    if (cudaMemcpyFromSymbolAsync(&v, g_dev_error, sizeof(v), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess) return 0;
+    cudaStreamSynchronize(st);
+    if (v) cudaMemcpyToSymbolAsync(g_dev_error, &none, sizeof(none), 0, cudaMemcpyHostToDevice, st);
+    return v;
 }
 
 // A plan's values, kept inside their ranges whatever it holds.

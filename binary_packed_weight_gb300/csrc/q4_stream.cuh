@@ -739,6 +739,7 @@ cudaError_t q4_stream_pick(Q4Kernel& k, int tok, int split, const Q4Device& dev,
 // 4), and further while that gives idle SMs a CTA of at least 32 chunks a tile.
 template <int G>
 cudaError_t q4_stream_run(const Q4Stream& a, cudaStream_t st) {
+    g_launched.store(true, std::memory_order_release);
     Q4Kernel k{};
     k.a = a;
     k.parts = a.xmode == Q4_X_SPLIT ? 2 : 1;

@@ -5,12 +5,6 @@ namespace tq2 {
 
 cudaError_t launch_q4_stream_g32(const Q4Stream& a, cudaStream_t st) { return q4_stream_run<32>(a, st); }
 
-unsigned int read_clear_dev_error_q4_g32(cudaStream_t st) {
-    unsigned int v = 0, z = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, g_dev_error, sizeof(v), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess) return 0;
-    cudaMemcpyToSymbolAsync(g_dev_error, &z, sizeof(z), 0, cudaMemcpyHostToDevice, st);
-    cudaStreamSynchronize(st);
-    return v;
-}
+unsigned int read_clear_dev_error_q4_g32(cudaStream_t st) { return read_clear_record(st); }
 
 }  // namespace tq2
