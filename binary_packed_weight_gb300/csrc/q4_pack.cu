@@ -63,27 +63,30 @@ q4_pack_kernel(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ s
 // extremes have none of their own, and a largest NaN stays.
 __global__ void __launch_bounds__(256)
 q4_bound_kernel(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ scales,
-                const uint8_t* __restrict__ zeros, float* __restrict__ bound, int64_t N, int64_t K, int G) {
+                const uint8_t* __restrict__ zeros, float* __restrict__ bound, int64_t N, int64_t K, int gshift) {
+    __shared__ int cta[3];
     const int lane = threadIdx.x & 31;
     int* of = reinterpret_cast<int*>(bound);
-    const int64_t kg = K / G;
+    if (threadIdx.x < 3) cta[threadIdx.x] = threadIdx.x == 1 ? 0x7F7F7F7F : 0;
+    __syncthreads();
+    const int64_t kg = K >> gshift;
     codes += (int64_t)blockIdx.y * N * (K / 2);
     scales += (int64_t)blockIdx.y * N * kg;
     if (zeros) zeros += (int64_t)blockIdx.y * N * kg;
     int most = 0, least = 0x7F7F7F7F, weight = 0;
     for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < N; r += (int64_t)gridDim.x * 8) {
         float s = 0.f;
-        for (int64_t k = lane * 8; k < K; k += 256) {
-            const uint16_t* src = reinterpret_cast<const uint16_t*>(codes + r * (K / 2) + k / 2);
-            const uint32_t p = src[0] | ((uint32_t)src[1] << 16);
-            const int z = zeros ? zeros[r * kg + k / G] & 15 : 8;
-            const float d = __half2float(__ushort_as_half(scales[r * kg + k / G]));
-            int q = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int c = (int)((p >> (4 * i)) & 15u) - z;
-                q += c * c;
-            }
+        const uint16_t* row = reinterpret_cast<const uint16_t*>(codes + r * (K / 2));
+#pragma unroll 4
+        for (int k = lane * 8; k < (int)K; k += 256) {
+            const uint32_t p = row[k / 4] | ((uint32_t)row[k / 4 + 1] << 16);
+            const int64_t g = r * kg + (k >> gshift);
+            const int z = zeros ? zeros[g] & 15 : 8;
+            const float d = __half2float(__ushort_as_half(scales[g]));
+            // sum (c - z)^2 = sum c^2 - 2 z sum c + 8 z^2
+            const uint32_t lo = p & 0x0F0F0F0Fu, hi = (p >> 4) & 0x0F0F0F0Fu;
+            const int c1 = (int)__dp4a(lo, 0x01010101u, __dp4a(hi, 0x01010101u, 0u));
+            const int q = (int)__dp4a(lo, lo, __dp4a(hi, hi, 0u)) - 2 * z * c1 + 8 * z * z;
             weight = max(weight, __float_as_int(d * (float)max(z, 15 - z)) & 0x7FFFFFFF);
             s = fmaf(d * d, (float)q, s);
         }
@@ -95,9 +98,15 @@ q4_bound_kernel(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ 
     }
     weight = __reduce_max_sync(0xffffffffu, weight);
     if (lane == 0) {
-        atomicMax(of + blockIdx.y, most);
-        atomicMin(of + gridDim.y + blockIdx.y, least);
-        atomicMax(of + 2 * gridDim.y, weight);
+        atomicMax(cta, most);
+        atomicMin(cta + 1, least);
+        atomicMax(cta + 2, weight);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        atomicMax(of + blockIdx.y, cta[0]);
+        atomicMin(of + gridDim.y + blockIdx.y, cta[1]);
+        atomicMax(of + 2 * gridDim.y, cta[2]);
     }
 }
 
@@ -195,8 +204,9 @@ cudaError_t launch_q4_bound(const uint8_t* codes, const uint16_t* scales, const 
     cudaError_t e = cudaMemsetAsync(w->bound, 0, q4_bounds(w->E) * 4, st);
     if (e == cudaSuccess) e = cudaMemsetAsync(w->bound + w->E, 0x7F, (size_t)w->E * 4, st);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)((w->N + 7) / 8 < 256 ? (w->N + 7) / 8 : 256);
-    q4_bound_kernel<<<dim3(grid, (unsigned)w->E), 256, 0, st>>>(codes, scales, zeros, w->bound, w->N, w->K, w->group);
+    const unsigned grid = (unsigned)((w->N + 7) / 8 < 1024 ? (w->N + 7) / 8 : 1024);
+    q4_bound_kernel<<<dim3(grid, (unsigned)w->E), 256, 0, st>>>(codes, scales, zeros, w->bound, w->N, w->K,
+                                                               w->group == 32 ? 5 : w->group == 64 ? 6 : 7);
     return cudaGetLastError();
 }
 
