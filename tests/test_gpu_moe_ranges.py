@@ -90,3 +90,36 @@ def test_experts_with_a_few_large_rows(lib, dtype, T, factor):
     w = np.ones((T, 1), np.float32)
     x, got = run_experts(lib, rng.normal(size=(T, D)) * 0.2, ids, w, handles, dtype, E)
     assert norm_error(got, omoe.experts(x, ids, w, *mats)) < NORM[dtype][T > 4 * E]
+
+
+@pytest.mark.parametrize("tiny", [0.0, 2.0 ** -24])
+def test_experts_with_dead_rows(lib, tiny):
+    """Rows of Gate and Up whose scales are nothing, or next to it, and one expert all of them."""
+    rng = np.random.default_rng(73)
+    E, D, F, T = 3, 512, 256, 60
+    dead = np.where(rng.random((E, F, 1)) < 0.1, tiny / 0.01, 1.0)
+    dead[2] = tiny / 0.01
+    mats, handles = layer(lib, rng, E, D, F, gate=dead, up=dead)
+    ids = (np.arange(T) % E)[:, None]
+    w = np.ones((T, 1), np.float32)
+    x, got = run_experts(lib, rng.normal(size=(T, D)), ids, w, handles, "float16", E)
+    want = omoe.experts(x, ids, w, *mats)
+    assert norm_error(got[ids[:, 0] < 2], want[ids[:, 0] < 2]) < NORM["float16"][1]
+    assert np.abs(got[ids[:, 0] == 2] - want[ids[:, 0] == 2]).max() <= 2.0 ** -25       # outputs next to nothing
+
+
+@pytest.mark.parametrize("bad", [np.inf, np.nan])
+@pytest.mark.parametrize("T", [6, 60])
+def test_experts_beside_a_broken_one(lib, bad, T):
+    """A scale that is no number spoils its expert's tokens and no others."""
+    rng = np.random.default_rng(74)
+    E, D, F = 3, 256, 128
+    planted = np.ones((E, F, 1))
+    planted[1, 5] = bad
+    mats, handles = layer(lib, rng, E, D, F, gate=planted)
+    ids = (np.arange(T) % E)[:, None]
+    w = np.ones((T, 1), np.float32)
+    x, got = run_experts(lib, rng.normal(size=(T, D)), ids, w, handles, "float16", E)
+    sound = ids[:, 0] != 1
+    assert norm_error(got[sound], omoe.experts(x[sound], ids[sound], w[sound], *mats)) < NORM["float16"][T > 4 * E]
+    assert not np.isfinite(got[~sound]).any()
