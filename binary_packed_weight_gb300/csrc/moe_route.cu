@@ -529,8 +529,9 @@ struct RouteBackArgs {
 // Lane j holds slot j.  Where only the selected logits matter (sigmoid;
 // renormalised softmax without a bias, whose selected scores sum to at least
 // 1/(2E), so that the common factor of the softmax cancels) they are gathered;
-// else the row is read.  A score is divided by the sum before anything is
-// multiplied by it: g / S alone may pass the largest f32, p / S is at most 1.
+// else the row is read.  A score meets 1 / S before anything else does: g / S alone
+// may pass the largest f32, p / S is at most 1.  (A product with the reciprocal: most lanes
+// hold no score, and dividing their 0 is slow: 16384x128 sigmoid 5.1 us, now 4.4.)
 // A sum below 2^-126 is not what the weights were divided by: they are p times
 // a constant there, and so is their gradient.
 // The row is written dense, then the selected entries.
@@ -555,9 +556,10 @@ __global__ void __launch_bounds__(256) moe_route_backward_kernel(const __grid_co
         if (a.score == MOE_SIGMOID) {
             const float p = live ? sigmoid(l) : 0.f, q = live ? sigmoid(-l) : 0.f;   // q = 1 - p without cancellation
             if (a.renorm) {
-                const float S = warp_sum(p), r = p / fmaxf(S, ROUTE_TINY);
-                const float dot = warp_sum(g * r);
-                mine = r * q * (S < ROUTE_TINY ? g : g - dot);
+                // both sums at once, of scores times 2^32, so that g p keeps its bits down to the least p
+                const float P = p * 0x1p32f, S = warp_sum(P), gP = warp_sum(g * P);
+                const float d = fmaxf(S, ROUTE_TINY * 0x1p32f), one = 1.0f / d;
+                mine = P * one * q * (S < d ? g : g - gP * one);
             } else {
                 mine = p * q * g;
             }
@@ -581,7 +583,7 @@ __global__ void __launch_bounds__(256) moe_route_backward_kernel(const __grid_co
             for (int i = 0; i < V; ++i) x[i] = x[i] > -INFINITY ? expf(x[i] - m) : 0.f;
             const float s = tree_sum<V>(x);
             const float p = live ? expf(l - m) / s : 0.f;
-            const float S = warp_sum(p), r = a.renorm ? p / fmaxf(S, ROUTE_TINY) : p;
+            const float S = a.renorm ? warp_sum(p) : 1.f, r = a.renorm ? p * (1.0f / fmaxf(S, ROUTE_TINY)) : p;
             const float dot = warp_sum(g * r);
             // the sum as divisor makes what flows to all experts vanish; a constant one does not
             const bool clamped = a.renorm && S < ROUTE_TINY;
