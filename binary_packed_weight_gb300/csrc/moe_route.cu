@@ -19,9 +19,11 @@
 // warps orders them, so there is no atomic whose order could matter.
 //
 // Bound: a few tokens by the call (1x64: 7 us) and the latency of the picks (300x160
-// in groups: 9.8); many by issue (16384x256, 4 of 8 groups, top 8: 26.5 us, 998 warp
-// instructions a token, a third of them the exact scores; the plan's kernel is 6 of
-// it).  The gradient's 16384x128 takes 6.2 us, the host's time for the call.
+// in groups: 9.8).  Many (16384x256, 4 of 8 groups, top 8: 26.5 us): 998 warp instructions a
+// token, a third of them the exact scores, are about 14 us of issue; the slots are 65 % busy,
+// the rest waits in the chain of a pick (redux, ballot, shuffle) with one token a warp, and
+// the plan's kernel is 6 to 7 of it.  The gradient's 16384x128 takes 6.5 us, of which the
+// kernel 6.3 (in a replayed graph); 100x60 6.3 and 1.6.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -37,6 +37,10 @@
 // values down to 2^-28 of it.  Where the rows of a matrix differ so much that its
 // smallest might fall below, hidden rows are written in f32 and scaled by their own
 // maximum in a pass of their own (own_scale; the rule and its cost are in q4_api.cu).
+//
+// silu goes by the fast exponential and division: off by a few 2^-22 of a value (times
+// |v| for the exponential), far below the f16 that it is rounded to; v below -87, whose
+// silu is next to nothing, may give 0.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -782,7 +786,7 @@ bool row_maps(MuMaps& m, __half* rows, int64_t inner, int64_t n, bool wide) {
 }
 
 // Wide tiles from 112 rows a matrix on average (64 experts of 2048x1024, 112 / 128
-// rows each: narrow 122 / 141 us, wide 121 / 127).  (Two groups of decoders need
+// rows each: narrow 122 / 141 us, wide 121 / 127; the one shape that was measured).  (Two groups of decoders need
 // blocks of two stages: a slot's last block must have been theirs or the MMAs'.)
 bool wide_tiles(int64_t nslots, int64_t E, int64_t K) { return nslots >= 112 * E && K > 128; }
 

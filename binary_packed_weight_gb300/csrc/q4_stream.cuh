@@ -30,9 +30,15 @@
 // fit are further launches.
 //
 // Bound: one row by the launch and one pass of latency (1x4096x4096 f32 5.4 us a
-// call); from 8 rows by the issue of the decode and the MMAs (400 to 490 warp
-// instructions a block: 8x11008x4096 bf16 8.2 us, 2.9 TB/s; 16x14336x4096 bf16 12.7 us,
-// 2.5 TB/s, issue slots 80 to 90 % busy between start and end).
+// call).  8x11008x4096 bf16 takes 8.2 us (2.9 TB/s) and 16x14336x4096 bf16 12.7 (2.5 TB/s):
+// 400 to 490 warp instructions a block are 3.7 and 6.0 us of that, if every scheduler
+// issued in every cycle.  The rest is the start, rows of x that the first MMA waits for,
+// the one block of look-ahead and the closing sums; how it divides is not measured.
+//
+// With a plan the accumulators of two or four column tiles do not fit 128 registers
+// beside a pass's bookkeeping: those variants spill (four tiles, groups of 128: 284 bytes
+// stored, 340 loaded a thread).  f32 calls of more than 4 rows a pass use them, and
+// 16-bit ones of more than 8 whose weights pass f16.
 //
 // With a plan (offsets, slots; PLAN) matrix e multiplies the rows of positions
 // offsets[e]..offsets[e+1]; `pair` takes tiles of two matrices in turn over the

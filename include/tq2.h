@@ -24,7 +24,8 @@
  *     stream).  Compute calls are asynchronous on that stream unless stated.
  *   - "DEVICE" pointers are CUDA device memory owned by the caller (for
  *     instance torch tensors); "HOST" pointers are ordinary host memory.
- *   - All float data is IEEE binary32, row-major, densely packed.
+ *   - All float data is IEEE binary32, row-major, densely packed, but for the
+ *     calls that take a tq2_dtype and a row stride.
  *   - Device-side waits inside the kernels are bounded (about one second);
  *     when one runs out the kernel records TQ2_ETIMEOUT and returns early.
  *     tq2_device_status() reports (and clears) that record.
@@ -572,7 +573,10 @@ TQ2_API tq2_status moe_route(const void* logits, int64_t ld, int dtype, const fl
  *   softmax:  dlogits[e] = p_e (q_e - sum_j q_j p_j)      (q_e = 0 unless selected;
  *             with renorm and S >= 2^-126 the sum is 0 and only the selected get a gradient)
  *   sigmoid:  dlogits[e] = p_e (1 - p_e) q_e
- * ids as moe_route returned them; a slot of -1 takes no part.  dlogits: DEVICE,
+ * ids as moe_route returned them; a slot of -1 takes no part.  dweights: DEVICE
+ * float[T][k], the loss's gradient to the weights; for the output of moe_experts that
+ * is out's gradient times the slot's own expert output, which is the caller's to
+ * compute (moe_experts returns the weighted sum alone).  dlogits: DEVICE,
  * dtype, T rows of E, ldd >= E elements apart, overwritten; may be logits itself
  * (ldd = ld), else overlaps none of the inputs.  Limits as moe_route.
  * Asynchronous, no scratch.
