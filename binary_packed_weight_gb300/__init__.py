@@ -17,6 +17,7 @@ __all__ = [
     "load", "lib_path", "TQ2Error", "Weight", "tq2_upload", "tq2_gemm", "tq2_gemm_path", "tq2_gemm_tensor_tuned",
     "tq2_gemm_skinny_static", "tq2_gemm_grouped", "GroupedGemv", "tq2_unpack", "tq2_dequant_f16", "tq2_quantize", "blr_expand_bits", "blr_forward", "blr_backward", "blr_forward_paths", "blr_backward_paths", "blr_sign_grads",
     "Q4Weight", "q4_upload", "q4_dequant", "q4_quantize", "q4_gemm", "moe_route", "moe_route_backward", "moe_experts",
+    "KV8Cache", "KV8Batch", "kv8_write", "kv8_read", "kv8_attention",
     "device_status", "release_scratch", "debug_wait_timeout", "PATH_AUTO", "PATH_SKINNY", "PATH_TENSOR",
 ]
 
@@ -60,6 +61,9 @@ _SIGS = {
     "moe_route": (_I, [_P, _I64, _I, _P, _I64, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P]),
     "moe_route_backward": (_I, [_P, _I64, _I, _P, _P, _P, _P, _I64, _I64, _I, _I, _I, _I, _F, _P]),
     "moe_experts": (_I, [_P, _P, _P, _P, _I64, _I, _P, _P, _P, _P, _P, _I64, _I64, _I, _P]),
+    "kv8_write": (_I, [_P, _P, _P, _I64, _I64, _P, _I64, _I64, _I, _I64, _P]),
+    "kv8_read": (_I, [_P, _P, _P, _I64, _I64, _P, _I64, _I64, _I, _I64, _P]),
+    "kv8_attention": (_I, [_P, _P, _P, _I64, _I64, _P, _I64, _I64, _I, _P, _I64, _I, _F, _I, _I64, _I64, _P]),
 }
 
 
@@ -67,6 +71,16 @@ class BlrPath(ctypes.Structure):
     """``blr_path`` of include/tq2.h: device pointers of one path."""
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("bits_u", "bits_v", "h", "l", "g", "a_save", "c_save", "dh", "dl", "dg")]
+
+
+class _Kv8Cache(ctypes.Structure):
+    """``kv8_cache`` of include/tq2.h."""
+    _fields_ = [("codes", _P), ("scales", _P), ("blocks", _I64), ("heads", _I), ("tokens", _I), ("dim", _I)]
+
+
+class _Kv8Batch(ctypes.Structure):
+    """``kv8_batch`` of include/tq2.h."""
+    _fields_ = [("table", _P), ("ld", _I64), ("offsets", _P), ("lens", _P), ("width", _I), ("seqs", _I)]
 
 
 class TQ2Error(RuntimeError):
@@ -478,6 +492,85 @@ def moe_experts(gate, up, down, x, ids, weights, offsets, slots, out, stream=Non
         _plane(ids, (T, k), "int32", at, "ids"), _plane(weights, (T, k), "float32", at, "weights"),
         _plane(offsets, (gate.E + 1,), "int32", at, "offsets"), _plane(slots, (T * k,), "int32", at, "slots"),
         out.data_ptr(), _rows(out, T, D, at, "out"), T, k, _on(x, stream)), at)
+    return out
+
+
+class KV8Cache:
+    """A pool of blocks of 8-bit keys and values in the caller's memory (kept alive): ``codes`` uint8
+    [blocks, 2, heads, tokens, dim], ``scales`` float32 [blocks, 2, heads], marshalled once."""
+
+    def __init__(self, codes, scales):
+        if codes.dim() != 5 or codes.shape[1] != 2:
+            raise ValueError(f"KV8Cache: codes must be [blocks, 2, heads, tokens, dim], got {list(codes.shape)}")
+        self.blocks, _, self.heads, self.tokens, self.dim = codes.shape
+        self.codes, self.scales = codes, scales
+        self._c = _Kv8Cache(_plane(codes, tuple(codes.shape), "uint8", "KV8Cache", "codes"),
+                            _plane(scales, tuple(codes.shape)[:3], "float32", "KV8Cache", "scales"),
+                            self.blocks, self.heads, self.tokens, self.dim)
+        self._at = ctypes.addressof(self._c)
+
+
+class KV8Batch:
+    """The sequences of a call in the caller's memory (kept alive; what it holds may change between
+    calls): ``table`` int32 [seqs, width] with rows of any stride, ``offsets`` int32 [seqs + 1], ``lens`` int32 [seqs]."""
+
+    def __init__(self, table, offsets, lens):
+        if table.dim() != 2:
+            raise ValueError(f"KV8Batch: table must be [seqs, width], got {list(table.shape)}")
+        self.seqs, self.width = table.shape
+        ld = _rows(table, self.seqs, self.width, "KV8Batch", "table")
+        self.table, self.offsets, self.lens = table, offsets, lens
+        at = _plane(offsets, (self.seqs + 1,), "int32", "KV8Batch", "offsets")
+        if table.dtype is not _names["int32"]:
+            raise ValueError(f"KV8Batch: table must be int32, got {table.dtype}")
+        self._c = _Kv8Batch(table.data_ptr(), ld, at, _plane(lens, (self.seqs,), "int32", "KV8Batch", "lens"),
+                            self.width, self.seqs)
+        self._at = ctypes.addressof(self._c)
+
+
+def _heads(t, rows, heads, dim, where, name):
+    """Address and strides of a [rows, heads, dim] tensor whose heads' elements are neighbours."""
+    if t.shape != (rows, heads, dim):
+        raise ValueError(f"{where}: {name} must be [{rows}, {heads}, {dim}], got {list(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{where}: {name} must be on the GPU")
+    st, sh, inner = t.stride()
+    if inner != 1:
+        raise ValueError(f"{where}: the elements of a head of {name} must be neighbours")
+    return t.data_ptr(), st, sh
+
+
+def _kv8_move(fn, where, cache, batch, k, v, stream):
+    if v.dtype is not k.dtype:
+        raise TypeError(f"{where}: k and v must have the same dtype")
+    T = k.shape[0]
+    _check(fn(cache._at, batch._at, *_heads(k, T, cache.heads, cache.dim, where, "k"),
+              *_heads(v, T, cache.heads, cache.dim, where, "v"), _dtype(k, where), T, _on(k, stream)), where)
+    return k, v
+
+
+def kv8_write(cache, batch, k, v, stream=None):
+    """Quantise the sequences' last tokens ``k``, ``v`` [T, heads, dim] into their blocks (see include/tq2.h)."""
+    return _kv8_move((_lib or load()).kv8_write, "kv8_write", cache, batch, k, v, stream)
+
+
+def kv8_read(cache, batch, k, v, stream=None):
+    """The sequences' last tokens as values, into ``k`` and ``v`` [T, heads, dim]."""
+    return _kv8_move((_lib or load()).kv8_read, "kv8_read", cache, batch, k, v, stream)
+
+
+def kv8_attention(cache, batch, q, out, lse=None, scale=None, causal=True, window=0, max_q=None, stream=None):
+    """Attention of the sequences' last tokens ``q`` [T, Hq, dim] over the cache into ``out`` [T, Hq, dim] and,
+    unless None, ``lse`` float32 [T, Hq] (see include/tq2.h).  scale: dim ** -0.5 if None; max_q: a bound of a
+    sequence's rows, if one is known."""
+    at = "kv8_attention"
+    T, Hq, D = q.shape
+    if out.dtype is not q.dtype:
+        raise TypeError("kv8_attention: q and out must have the same dtype")
+    _check((_lib or load()).kv8_attention(
+        cache._at, batch._at, *_heads(q, T, Hq, cache.dim, at, "q"), *_heads(out, T, Hq, cache.dim, at, "out"),
+        _dtype(q, at), None if lse is None else _plane(lse, (T, Hq), "float32", at, "lse"), T, Hq,
+        D ** -0.5 if scale is None else scale, 1 if causal else 0, window, max_q or 0, _on(q, stream)), at)
     return out
 
 

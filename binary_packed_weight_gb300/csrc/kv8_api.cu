@@ -1,0 +1,134 @@
+// kv8_api.cu -- the C ABI of the 8-bit cache: argument checks, scratch, and
+// the choice of the attention's path.
+#include <cmath>
+
+#include "../../include/tq2.h"
+#include "kv8.cuh"
+
+namespace tq2 {
+namespace {
+
+tq2_status cuda_status(cudaError_t e, const char* what) {
+    if (e == cudaSuccess) return TQ2_OK;
+    return (tq2_status)set_error(e == cudaErrorMemoryAllocation ? TQ2_ENOMEM : TQ2_ECUDA, "%s: %s", what,
+                                 cudaGetErrorString(e));
+}
+
+// What the three calls have in common: the cache and the sequences as the kernels see them.
+tq2_status view(const kv8_cache* c, const kv8_batch* b, int dtype, int64_t T, const char* where, Kv8View* out) {
+    if (!c || !b || !c->codes || !c->scales || !b->table || !b->offsets || !b->lens)
+        return (tq2_status)set_error(TQ2_EINVAL, "%s: null pointer", where);
+    if (dtype != TQ2_F32 && dtype != TQ2_F16 && dtype != TQ2_BF16)
+        return (tq2_status)set_error(TQ2_EINVAL, "%s: unknown dtype %d", where, dtype);
+    int logB = 4;
+    while (logB < 7 && (1 << logB) < c->tokens) ++logB;
+    if ((1 << logB) != c->tokens || (c->dim != 64 && c->dim != 128) || c->heads < 1 || c->heads > 1024 ||
+        c->blocks < 1 || c->blocks > ((int64_t)1 << 30) || c->blocks * 2 * c->heads * c->tokens >= ((int64_t)1 << 31))
+        return (tq2_status)set_error(TQ2_ESHAPE,
+                                     "%s: need tokens 16, 32, 64 or 128, dim 64 or 128, 1 <= heads <= 1024, blocks >= 1 "
+                                     "and blocks*2*heads*tokens < 2^31 (blocks=%lld heads=%d tokens=%d dim=%d)",
+                                     where, (long long)c->blocks, c->heads, c->tokens, c->dim);
+    if (b->seqs < 1 || b->width < 1 || b->ld < b->width || (int64_t)b->width * c->tokens > ((int64_t)1 << 30))
+        return (tq2_status)set_error(TQ2_ESHAPE,
+                                     "%s: need seqs >= 1, 1 <= width <= ld, width*tokens <= 2^30 (seqs=%d width=%d ld=%lld)",
+                                     where, b->seqs, b->width, (long long)b->ld);
+    if (T < 0 || T >= ((int64_t)1 << 31))
+        return (tq2_status)set_error(TQ2_ESHAPE, "%s: bad T=%lld", where, (long long)T);
+    if (off_element(c->codes, 16) || off_element(c->scales, 4) || off_element(b->table, 4) ||
+        off_element(b->offsets, 4) || off_element(b->lens, 4))
+        return (tq2_status)set_error(TQ2_EINVAL, "%s: codes must be 16-byte aligned, the others to their elements", where);
+    *out = Kv8View{c->codes, c->scales, b->table, b->offsets, b->lens, b->ld, (int)c->blocks, c->heads, logB, c->dim,
+                   b->width, b->seqs, (int)T};
+    return TQ2_OK;
+}
+
+tq2_status move(const kv8_cache* c, const kv8_batch* b, void* k, int64_t kt, int64_t kh, void* v, int64_t vt,
+                int64_t vh, int dtype, int64_t T, void* stream, const char* where,
+                cudaError_t (*launch)(const Kv8View&, const Kv8Rows&, cudaStream_t)) {
+    Kv8View w;
+    const tq2_status st = view(c, b, dtype, T, where, &w);
+    if (st != TQ2_OK) return st;
+    if (T * c->heads * c->dim >= ((int64_t)1 << 40))
+        return (tq2_status)set_error(TQ2_ESHAPE, "%s: %lld rows are too many for one call", where, (long long)T);
+    if (T == 0) return TQ2_OK;
+    if (!k || !v) return (tq2_status)set_error(TQ2_EINVAL, "%s: null pointer", where);
+    if (off_element(k, element_size(dtype)) || off_element(v, element_size(dtype)))
+        return (tq2_status)set_error(TQ2_EINVAL, "%s: k and v must be element-aligned", where);
+    return cuda_status(launch(w, Kv8Rows{k, v, kt, kh, vt, vh, dtype}, reinterpret_cast<cudaStream_t>(stream)), where);
+}
+
+// Scratch of one call, given back on the same stream whatever happens.
+struct Scratch {
+    void* p = nullptr;
+    cudaStream_t st;
+    explicit Scratch(cudaStream_t s) : st(s) {}
+    ~Scratch() {
+        if (p) cudaFreeAsync(p, st);
+    }
+};
+
+}  // namespace
+}  // namespace tq2
+
+using namespace tq2;
+
+extern "C" {
+
+tq2_status kv8_write(const kv8_cache* c, const kv8_batch* b, const void* k, int64_t kt, int64_t kh, const void* v,
+                     int64_t vt, int64_t vh, int dtype, int64_t T, void* stream) {
+    return move(c, b, const_cast<void*>(k), kt, kh, const_cast<void*>(v), vt, vh, dtype, T, stream, "kv8_write",
+                launch_kv8_write);
+}
+
+tq2_status kv8_read(const kv8_cache* c, const kv8_batch* b, void* k, int64_t kt, int64_t kh, void* v, int64_t vt,
+                    int64_t vh, int dtype, int64_t T, void* stream) {
+    return move(c, b, k, kt, kh, v, vt, vh, dtype, T, stream, "kv8_read", launch_kv8_read);
+}
+
+tq2_status kv8_attention(const kv8_cache* c, const kv8_batch* b, const void* q, int64_t qt, int64_t qh, void* out,
+                         int64_t ot, int64_t oh, int dtype, float* lse, int64_t T, int Hq, float scale, int causal,
+                         int64_t window, int64_t max_q, void* stream) {
+    Kv8Attention a{};
+    const tq2_status bad = view(c, b, dtype, T, "kv8_attention", &a.c);
+    if (bad != TQ2_OK) return bad;
+    if (Hq < c->heads || Hq % c->heads || T * Hq >= ((int64_t)1 << 31))
+        return (tq2_status)set_error(TQ2_ESHAPE, "kv8_attention: Hq=%d must be a multiple of heads=%d with T*Hq < 2^31", Hq,
+                                     c->heads);
+    if (!std::isfinite(scale) || (causal != 0 && causal != 1) || window < 0 || (window && !causal) || max_q < 0)
+        return (tq2_status)set_error(TQ2_EINVAL,
+                                     "kv8_attention: need a finite scale, causal 0 or 1, window >= 0 (0 unless causal), "
+                                     "max_q >= 0 (scale=%g causal=%d window=%lld max_q=%lld)",
+                                     (double)scale, causal, (long long)window, (long long)max_q);
+    if (T == 0) return TQ2_OK;
+    if (!q || !out) return (tq2_status)set_error(TQ2_EINVAL, "kv8_attention: null pointer");
+    if (off_element(q, element_size(dtype)) || off_element(out, element_size(dtype)) || off_element(lse, 4))
+        return (tq2_status)set_error(TQ2_EINVAL, "kv8_attention: q, out and lse must be element-aligned");
+    const uint32_t rows = (uint32_t)(c->tokens < 64 ? c->tokens : 64);
+    if (!make_tensor_map_2d(&a.map, CU_TENSOR_MAP_DATA_TYPE_UINT8, c->codes, (uint64_t)c->dim,
+                            (uint64_t)c->blocks * 2 * c->heads * c->tokens, (uint64_t)c->dim, (uint32_t)c->dim, rows,
+                            c->dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+        return (tq2_status)set_error(TQ2_ECUDA, "kv8_attention: the cache cannot be mapped for TMA");
+    a.q = q;
+    a.out = out;
+    a.lse = lse;
+    a.qt = qt;
+    a.qh = qh;
+    a.ot = ot;
+    a.oh = oh;
+    a.dtype = dtype;
+    a.G = Hq / c->heads;
+    a.scale = scale * 1.4426950408889634f;                    // powers of 2 from here on
+    a.causal = causal;
+    a.window = window < ((int64_t)1 << 30) ? (int)window : 0;  // no sequence is longer
+    a.few = 0x7fffffff;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    Scratch mem(st);
+    cudaError_t e = scratch_alloc(&mem.p, kv8_stream_scratch(a), st);
+    if (e != cudaSuccess) {
+        mem.p = nullptr;
+        return cuda_status(e, "kv8_attention: scratch");
+    }
+    return cuda_status(launch_kv8_stream(a, mem.p, st), "kv8_attention");
+}
+
+}  // extern "C"

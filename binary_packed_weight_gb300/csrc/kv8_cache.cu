@@ -1,0 +1,192 @@
+// kv8_cache.cu -- new tokens into the 8-bit cache, and tokens out of it.
+//
+// A CTA takes a block of B tokens in one head, of the keys or of the values: all
+// that shares a scale.  Its new values stay in registers between the maximum
+// and the codes, so each is read once.  Both kernels move bytes and little else;
+// what bounds the write besides is one exchange of the maximum between a CTA's
+// loads and its stores, covered by other CTAs of the SM.
+#include "kv8.cuh"
+
+namespace tq2 {
+namespace {
+
+constexpr int CHUNK = 16;       // elements a thread takes at a time: 16 codes are one 16-byte store
+constexpr int MAX_CHUNKS = 4;   // of a thread: B * D / 16 codes over 64 to 256 threads
+
+int threads_of(const Kv8View& c) {
+    const int chunks = (c.D << c.logB) / CHUNK;
+    return chunks < 256 ? chunks : 256;
+}
+
+// Blocks of a sequence are dealt over gridDim.z CTAs: enough for a lone prompt to fill the
+// GPU, none that a decode step would launch in vain.
+dim3 grid_of(const Kv8View& c) {
+    const int64_t most = ((int64_t)c.T >> c.logB) + 2;
+    const int64_t want = (int64_t)(152 * 32) / ((int64_t)c.seqs * c.H * 2) + 1;
+    return dim3((unsigned)c.seqs, (unsigned)(c.H * 2), (unsigned)(c.T == c.seqs ? 1 : most < want ? most : want));
+}
+
+// Values below 2^-96 count as zeros, so that a scale and its reciprocal are normal numbers.
+constexpr float SMALLEST = 0x1p-96f;
+
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* shared) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    if (blockDim.x == 32) return v;
+    __syncthreads();                                         // the last block's maximum has been read
+    if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int warps = blockDim.x >> 5;
+    v = shared[0];
+    for (int i = 1; i < warps; ++i) v = max(v, shared[i]);
+    return v;
+}
+
+__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
+    // whole numbers of -127..127 above 1.5 * 2^23 have their value in the low byte
+    const float magic = 12583040.f;                          // 1.5 * 2^23 + 128
+    const uint32_t lo = __byte_perm(__float_as_uint(a + magic), __float_as_uint(b + magic), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(c + magic), __float_as_uint(d + magic), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
+}
+
+__device__ __forceinline__ float code_of(float x, float inverse) {
+    return fminf(fmaxf(rintf(__fmul_rn(x, inverse)), -127.f), 127.f);
+}
+
+template <class T>
+__global__ void __launch_bounds__(256)
+kv8_write_kernel(const Kv8View c, const T* k, const T* v, int64_t kt, int64_t kh, int64_t vt, int64_t vh, bool vec) {
+    __shared__ uint32_t shared[8];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int s = blockIdx.x, head = blockIdx.y >> 1, kv = blockIdx.y & 1;
+    const Kv8Seq q = kv8_seq(c, s);
+    if (q.n == 0 || q.len == 0) return;
+    const T* x = kv ? v : k;
+    const int64_t xt = kv ? vt : kt, xh = kv ? vh : kh;
+    const int B = 1 << c.logB, per_row = c.D / CHUNK, chunks = per_row << c.logB;
+    const int start = q.len - q.n;                           // below 0: tokens that no position is left for
+    const int first = max(start, 0);
+    for (int b = (first >> c.logB) + blockIdx.z; (b << c.logB) < q.len; b += gridDim.z) {
+        const int block = kv8_block(c, s, b << c.logB);
+        if (block < 0) continue;
+        const int base = b << c.logB;
+        const int lo = max(first - base, 0), hi = min(q.len - base, B);   // new tokens of the block
+        float y[MAX_CHUNKS][CHUNK];
+        uint32_t peak = 0;
+#pragma unroll
+        for (int i = 0; i < MAX_CHUNKS; ++i) {
+            const int at = threadIdx.x + i * blockDim.x, token = at / per_row;
+            if (at < chunks && token >= lo && token < hi) {
+                kv8_load16(x + (q.q0 + (base + token - start)) * xt + head * xh + (at % per_row) * CHUNK, vec, y[i]);
+#pragma unroll
+                for (int j = 0; j < CHUNK; ++j) peak = max(peak, __float_as_uint(y[i][j]) & 0x7fffffffu);
+            }
+        }
+        peak = block_max(peak, shared);
+        float* where = c.scales + ((int64_t)block * 2 + kv) * c.H + head;
+        const float before = lo > 0 ? *where : 0.f;
+        const float most = __uint_as_float(peak);
+        // a value that is no number leaves none in the block
+        const float fresh = peak >= 0x7f800000u ? __uint_as_float(0x7fffffffu)
+                                                : most >= SMALLEST ? __fdiv_rn(most, 127.f) : 0.f;
+        const bool bad = isnan(before) || isnan(fresh);
+        const float now = bad ? __uint_as_float(0x7fffffffu) : fmaxf(before, fresh);
+        const float inverse = now > 0.f ? __fdiv_rn(1.f, now) : 0.f;
+        const bool coarser = lo > 0 && now > before;
+        const float ratio = coarser ? __fdiv_rn(before, now) : 1.f;
+        uint4* codes = reinterpret_cast<uint4*>(c.codes + kv8_row(c, block, kv, head) * c.D);
+#pragma unroll
+        for (int i = 0; i < MAX_CHUNKS; ++i) {
+            const int at = threadIdx.x + i * blockDim.x, token = at / per_row;
+            if (at >= chunks || token >= hi) continue;
+            if (token >= lo) {
+                float z[CHUNK];
+#pragma unroll
+                for (int j = 0; j < CHUNK; ++j) z[j] = code_of(y[i][j], inverse);
+                codes[at] = make_uint4(pack4(z[0], z[1], z[2], z[3]), pack4(z[4], z[5], z[6], z[7]),
+                                       pack4(z[8], z[9], z[10], z[11]), pack4(z[12], z[13], z[14], z[15]));
+            } else if (coarser) {
+                uint4 w = codes[at];
+                uint32_t* e = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float z[4];
+#pragma unroll
+                    for (int l = 0; l < 4; ++l) z[l] = code_of((float)((int)(e[j] >> (8 * l) & 255u) - 128), ratio);
+                    e[j] = pack4(z[0], z[1], z[2], z[3]);
+                }
+                codes[at] = w;
+            }
+        }
+        __syncthreads();                                     // every thread has read the scale
+        if (threadIdx.x == 0 && (lo == 0 || now != before)) *where = now;
+    }
+}
+
+template <class T>
+__global__ void __launch_bounds__(256)
+kv8_read_kernel(const Kv8View c, T* k, T* v, int64_t kt, int64_t kh, int64_t vt, int64_t vh, bool vec) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int s = blockIdx.x, head = blockIdx.y >> 1, kv = blockIdx.y & 1;
+    const Kv8Seq q = kv8_seq(c, s);
+    if (q.n == 0 || q.len == 0) return;
+    T* x = kv ? v : k;
+    const int64_t xt = kv ? vt : kt, xh = kv ? vh : kh;
+    const int B = 1 << c.logB, per_row = c.D / CHUNK, chunks = per_row << c.logB;
+    const int start = q.len - q.n, first = max(start, 0);
+    for (int b = (first >> c.logB) + blockIdx.z; (b << c.logB) < q.len; b += gridDim.z) {
+        const int block = kv8_block(c, s, b << c.logB);
+        if (block < 0) continue;
+        const int base = b << c.logB;
+        const int lo = max(first - base, 0), hi = min(q.len - base, B);
+        const float scale = c.scales[((int64_t)block * 2 + kv) * c.H + head];
+        const uint4* codes = reinterpret_cast<const uint4*>(c.codes + kv8_row(c, block, kv, head) * c.D);
+#pragma unroll
+        for (int i = 0; i < MAX_CHUNKS; ++i) {
+            const int at = threadIdx.x + i * blockDim.x, token = at / per_row;
+            if (at >= chunks || token < lo || token >= hi) continue;
+            const uint4 w = codes[at];
+            const uint32_t* e = reinterpret_cast<const uint32_t*>(&w);
+            float y[CHUNK];
+#pragma unroll
+            for (int j = 0; j < CHUNK; ++j)
+                y[j] = __fmul_rn((float)((int)(e[j / 4] >> (8 * (j & 3)) & 255u) - 128), scale);
+            kv8_store16(x + (q.q0 + (base + token - start)) * xt + head * xh + (at % per_row) * CHUNK, vec, y);
+        }
+    }
+}
+
+bool vectors(const Kv8Rows& r) {
+    const int64_t size = (int64_t)element_size(r.dtype);
+    const int64_t all = (int64_t)(uintptr_t)r.k | (int64_t)(uintptr_t)r.v | r.kt * size | r.kh * size | r.vt * size | r.vh * size;
+    return (all & 15) == 0;
+}
+
+template <class T>
+cudaError_t write_as(const Kv8View& c, const Kv8Rows& r, cudaStream_t st) {
+    return launch_pdl(kv8_write_kernel<T>, grid_of(c), dim3(threads_of(c)), 0, st, c, static_cast<const T*>(r.k),
+                      static_cast<const T*>(r.v), r.kt, r.kh, r.vt, r.vh, vectors(r));
+}
+template <class T>
+cudaError_t read_as(const Kv8View& c, const Kv8Rows& r, cudaStream_t st) {
+    return launch_pdl(kv8_read_kernel<T>, grid_of(c), dim3(threads_of(c)), 0, st, c, static_cast<T*>(r.k),
+                      static_cast<T*>(r.v), r.kt, r.kh, r.vt, r.vh, vectors(r));
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_write(const Kv8View& c, const Kv8Rows& r, cudaStream_t st) {
+    if (r.dtype == TQ2_F32) return write_as<float>(c, r, st);
+    if (r.dtype == TQ2_F16) return write_as<__half>(c, r, st);
+    return write_as<__nv_bfloat16>(c, r, st);
+}
+
+cudaError_t launch_kv8_read(const Kv8View& c, const Kv8Rows& r, cudaStream_t st) {
+    if (r.dtype == TQ2_F32) return read_as<float>(c, r, st);
+    if (r.dtype == TQ2_F16) return read_as<__half>(c, r, st);
+    return read_as<__nv_bfloat16>(c, r, st);
+}
+
+}  // namespace tq2

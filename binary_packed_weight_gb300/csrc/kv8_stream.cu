@@ -1,0 +1,645 @@
+// kv8_stream.cu -- attention of few rows over the 8-bit cache: decoded and
+// drafted tokens.
+//
+// Mathematics, per row r (a query token and one of its heads) and token t, with the
+// scales ks and vs of the token's block:
+//     w_t = scale log2(e) ks (q_r . c_t) + x_t,   x_t the exponent of vs = 2^x_t f_t
+//     out = sum_t 2^(w_t - m) f_t c'_t / l,  l = sum_t 2^(w_t - m) 2^-x_t
+// so that what is rounded to f16 is the whole weight of a value code c': a block of large
+// values takes no bits from others that it does not outweigh.  m is a running reference
+// that follows the largest w in steps, so that few tokens rescale the sums.
+// The codes are whole numbers, exact in f16; f16 and bf16 queries, scaled by a power of
+// two a row, are exact as well, f32 ones are two f16 parts (and so are their
+// weights), of which an MMA takes both as rows r and r + 8.  Sums are f32.
+//
+// Bound: the bytes of the codes.  A CTA walks chunks of 64 tokens; all chunks of all
+// sequences and heads are cut evenly over the CTAs, so a ragged batch or one
+// long sequence fills the GPU alike.  What a cut divides is joined by a second kernel in the
+// order of the tokens.  TMA brings the chunks into a ring (keys and values of
+// a chunk are 128-byte-swizzled rows, so that fragments are read without
+// conflicts), four warps take 16 tokens of each.
+#include <type_traits>
+
+#include "kv8.cuh"
+#include "q4.cuh"
+
+namespace tq2 {
+namespace {
+
+constexpr int CT = 64;          // tokens of a chunk
+constexpr int WARPS = 4;        // that compute; one more feeds them
+constexpr int THREADS = WARPS * 32 + 32;
+constexpr int STAGES = 4;
+// The running reference m of a row: HEAD below the largest weight when it was set (so that f16 keeps
+// weights down to 2^-30 of it), set anew where a weight passes RAISE above it (2^15 is in f16's range).
+constexpr float HEAD = 6.f, RAISE = 14.f;
+constexpr int MIN_CHUNKS = 2;   // of a CTA, where there are fewer than the GPU's CTAs take
+
+template <int D>
+struct __align__(1024) Shared {
+    uint8_t k[STAGES][CT * D];
+    uint8_t v[STAGES][CT * D];
+    float acc[WARPS][16 * (D + 4)];
+    float m[WARPS][16], l[WARPS][16];
+    float2 scales[STAGES][4];   // of keys and of values, by piece; values' -1: nothing there
+    uint64_t full[STAGES], empty[STAGES];
+    long long sums[WARPS + 1], seq_start;
+    int seq;
+    volatile int abort;
+};
+
+struct Walk {
+    // a CTA's chunks [pos, end) of the whole list; the current sequence's begin at `base`
+    long long pos, end, base;
+    int s;
+    Kv8Seq q;
+    int tiles, first, count;    // row tiles of a head, first chunk, chunks of a tile
+};
+
+template <int RM>
+__device__ __forceinline__ long long open_seq(const Kv8Attention& a, int s, Walk& w) {
+    w.s = s;
+    w.q = kv8_seq(a.c, s);
+    const int rows = w.q.n * a.G;
+    w.tiles = rows > a.few ? 0 : (rows + RM - 1) / RM;
+    const int from = a.window ? max(w.q.len - w.q.n - a.window + 1, 0) : 0;
+    w.first = from / CT;
+    w.count = max((w.q.len + CT - 1) / CT - w.first, 1);
+    return (long long)w.tiles * a.c.H * w.count;
+}
+
+// CTA's share of `total` chunks: as even as can be, over as many CTAs as have two each.
+struct Cut {
+    long long base, more;
+    int ctas;
+    __device__ __forceinline__ Cut(long long total, int grid) {
+        const long long useful = (total + MIN_CHUNKS - 1) / MIN_CHUNKS;
+        ctas = useful < grid ? (int)useful : grid;
+        base = ctas ? total / ctas : 0;
+        more = ctas ? total - base * ctas : 0;
+    }
+    __device__ __forceinline__ long long begin(int c) const { return c * base + (c < more ? c : more); }
+    __device__ __forceinline__ int of(long long chunk) const {
+        const long long fat = more * (base + 1);
+        return (int)(chunk < fat ? chunk / (base + 1) : more + (chunk - fat) / base);
+    }
+};
+
+// What a cut divided: written by the CTA that has the first piece.
+struct Joint {
+    int s, head, tile, pieces;
+};
+
+__host__ __device__ constexpr size_t part_floats(int D) { return 16 * (size_t)(D + 2); }
+
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// What f16 left of a and b.
+__device__ __forceinline__ uint32_t rest_half2(float a, float b, uint32_t h) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return pack_half2(a - f.x, b - f.y);
+}
+// Barrier of the computing warps; the second tells all of them whether any gave up.
+__device__ __forceinline__ void named_sync() { asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory"); }
+__device__ __forceinline__ bool named_sync_or(bool any) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)any), "n"(WARPS * 32)
+        : "memory");
+    return r != 0;
+}
+
+// Row r's output and the logarithm of its sum.
+template <class T>
+__device__ __forceinline__ int64_t out_row(const Kv8Attention& a, const Kv8Seq& q, int head, int r, int64_t* lse) {
+    const int token = q.q0 + r / a.G, h = head * a.G + r % a.G;
+    *lse = (int64_t)token * a.c.H * a.G + h;
+    return token * a.ot + h * a.oh;
+}
+
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l > 0.f || isnan(l) ? (log2f(l) + m) * 0.69314718055994531f : __int_as_float(0xff800000);
+}
+
+template <class T, int D>
+__global__ void __launch_bounds__(THREADS, 2)
+kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Joint* joints) {
+    constexpr bool SPLIT = sizeof(T) == 4;
+    // weights of f16 outputs in two parts too: one part's rounding is as large as the output's own
+    constexpr bool TWO = std::is_same<T, __half>::value;
+    constexpr int RM = SPLIT ? 8 : 16;
+    constexpr int KS = D / 16;                               // k steps of q . c
+    constexpr int NT = D / 8;                                // column tiles of the output
+    extern __shared__ __align__(1024) uint8_t raw[];
+    Shared<D>& sm = *reinterpret_cast<Shared<D>*>(raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(&sm.full[i], 33);
+            mbar_init(&sm.empty[i], WARPS);
+        }
+        sm.abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&a.map);
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // the whole list's length, and where this CTA's share begins
+    const int S = a.c.seqs, per = (S + THREADS - 1) / THREADS;
+    Walk w;
+    long long mine = 0;
+    for (int s = tid * per; s < min((tid + 1) * per, S); ++s) mine += open_seq<RM>(a, s, w);
+    long long before = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, before, d);
+        if (lane >= d) before += u;
+    }
+    if (lane == 31) sm.sums[warp] = before;
+    before -= mine;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int i = 0; i <= WARPS; ++i) {
+        if (i < warp) before += sm.sums[i];
+        total += sm.sums[i];
+    }
+    const Cut cut(total, gridDim.x);
+    const int cta = blockIdx.x;
+    if (cta >= cut.ctas) {
+        if (tid == 0) joints[cta].pieces = 0;
+        return;
+    }
+    w.pos = cut.begin(cta);
+    w.end = cut.begin(cta + 1);
+    if (before <= w.pos && w.pos < before + mine) {
+        for (int s = tid * per;; ++s) {
+            const long long len = open_seq<RM>(a, s, w);
+            if (w.pos < before + len) {
+                sm.seq = s;
+                sm.seq_start = before;
+                break;
+            }
+            before += len;
+        }
+    }
+    __syncthreads();
+    w.base = sm.seq_start;
+    long long span = open_seq<RM>(a, sm.seq, w);
+    const int logB = a.c.logB;
+    const int rows_piece = min(1 << logB, CT), pieces = CT / rows_piece;
+
+    if (warp == WARPS) {
+        // ------------------------------------------------------- producer
+        int stage = 0, phase = 0;
+        bool issued = false;                                 // all stages have been
+        fence_proxy_async_shared();
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        while (w.pos < w.end) {
+            while (w.pos >= w.base + span) {
+                w.base += span;
+                span = open_seq<RM>(a, w.s + 1, w);
+            }
+            const long long in = w.pos - w.base;
+            const int item = (int)(in / w.count), ch = (int)(in % w.count);
+            const int head = item / w.tiles;
+            const long long run = min((long long)(w.count - ch), w.end - w.pos);
+            const int from = a.window ? max(w.q.len - w.q.n - a.window + 1, 0) : 0;
+            for (int i = 0; i < run; ++i) {
+                if (!mbar_wait_or_abort(&sm.empty[stage], phase ^ 1, &sm.abort)) {
+                    sm.abort = 1;
+                    // copies in flight end before the shared memory goes
+                    for (int u = 0; u < STAGES; ++u) {
+                        if (u < stage || issued) mbar_wait(&sm.full[u], u < stage ? phase : phase ^ 1);
+                    }
+                    return;
+                }
+                const int token = (w.first + ch + i) * CT + lane * rows_piece;
+                int block = -1;
+                if (lane < pieces) {
+                    if (token < w.q.len && token + rows_piece > from) block = kv8_block(a.c, w.s, token);
+                    if (block < 0) sm.scales[stage][lane] = make_float2(0.f, -1.f);
+                }
+                const uint32_t here = __ballot_sync(0xffffffffu, block >= 0);
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&sm.full[stage], __popc(here) * 2u * (uint32_t)(rows_piece * D));
+                if (block >= 0) {
+                    const int inside = token & ((1 << logB) - 1);
+                    const int64_t kr = kv8_row(a.c, block, 0, head) + inside, vr = kv8_row(a.c, block, 1, head) + inside;
+                    tma_load_2d(sm.k[stage] + lane * rows_piece * D, &a.map, &sm.full[stage], 0, (int)kr);
+                    tma_load_2d(sm.v[stage] + lane * rows_piece * D, &a.map, &sm.full[stage], 0, (int)vr);
+                    const float* sc = a.c.scales + (int64_t)block * 2 * a.c.H + head;
+                    cp_async4(&sm.scales[stage][lane].x, sc);
+                    cp_async4(&sm.scales[stage][lane].y, sc + a.c.H);
+                }
+                cp_async_arrive(&sm.full[stage]);
+                if (++stage == STAGES) stage = 0, phase ^= 1, issued = true;
+            }
+            w.pos += run;
+        }
+        return;
+    }
+
+    // ----------------------------------------------------------- consumers
+    const int g = lane >> 2, t4 = lane & 3;
+    int stage = 0, phase = 0;
+    Joint joint{0, 0, 0, 0};
+    bool ok = true;
+    while (w.pos < w.end) {
+        while (w.pos >= w.base + span) {
+            w.base += span;
+            span = open_seq<RM>(a, w.s + 1, w);
+        }
+        const long long in = w.pos - w.base;
+        const int item = (int)(in / w.count), ch = (int)(in % w.count);
+        const int head = item / w.tiles, tile = item % w.tiles;
+        const int run = (int)min((long long)(w.count - ch), w.end - w.pos);
+        const int rows = min(w.q.n * a.G - tile * RM, RM);
+
+        // the tile's queries as MMA operands: k step 4j+i of lane t4 takes elements D/4 t4 + 16j + 4i + {0,1}, {2,3}
+        uint32_t qf[KS][4];
+        float qa[2];
+        int hi[2], lo[2];
+        constexpr int HALVES = SPLIT ? 1 : 2;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int r = g + 8 * half;
+            if (half < HALVES) {
+                const bool live = r < rows;
+                const int rr = tile * RM + (live ? r : 0);
+                const int j = rr / a.G;
+                const T* p = static_cast<const T*>(a.q) + (int64_t)(w.q.q0 + j) * a.qt +
+                             (int64_t)(head * a.G + rr % a.G) * a.qh + t4 * (D / 4);
+                const bool vec = ((reinterpret_cast<uintptr_t>(p)) & 15) == 0;
+                float x[D / 4], most = 0.f;
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    float y[16];
+                    kv8_load16(p + 16 * c, vec, y);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        x[16 * c + e] = live ? y[e] : 0.f;
+                        most = fmaxf(most, fabsf(x[16 * c + e]));
+                    }
+                }
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                // a power of two that takes the row's largest element to 2^14 .. 2^15
+                const int e = min(max(141 - (int)(__float_as_uint(most) >> 23), -112), 126);
+                const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+                qa[half] = a.scale * __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const float u0 = x[4 * ks + 2 * b] * up, u1 = x[4 * ks + 2 * b + 1] * up;
+                        const __half h0 = __float2half_rn(u0), h1 = __float2half_rn(u1);
+                        qf[ks][half + 2 * b] = (uint32_t)__half_as_ushort(h0) | (uint32_t)__half_as_ushort(h1) << 16;
+                        if (SPLIT) qf[ks][1 + 2 * b] = pack_half2(u0 - __half2float(h0), u1 - __half2float(h1));
+                    }
+                const int pos = w.q.len - w.q.n + j;
+                hi[half] = a.causal ? min(w.q.len, pos + 1) : w.q.len;
+                lo[half] = a.window ? max(pos - a.window + 1, 0) : 0;
+            } else {
+                qa[1] = qa[0];
+                hi[1] = hi[0];
+                lo[1] = lo[0];
+            }
+        }
+        // tokens [safe_lo, safe_hi) are seen by all rows of the tile
+        const int j0 = tile * RM / a.G, j1 = (tile * RM + rows - 1) / a.G;
+        const int p0 = w.q.len - w.q.n + j0, p1 = w.q.len - w.q.n + j1;
+        const int safe_hi = a.causal ? min(w.q.len, p0 + 1) : w.q.len;
+        const int safe_lo = a.window ? max(p1 - a.window + 1, 0) : 0;
+        const int any_hi = a.causal ? min(w.q.len, p1 + 1) : w.q.len;
+        const int any_lo = a.window ? max(p0 - a.window + 1, 0) : 0;
+
+        float acc[NT][4];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+        const float NONE = __int_as_float(0xff800000);
+        float m[2] = {NONE, NONE}, l[2] = {0.f, 0.f};
+
+        for (int i = 0; i < run && ok; ++i) {
+            ok = mbar_wait_or_abort(&sm.full[stage], phase, &sm.abort);
+            if (!ok) {
+                sm.abort = 1;
+                break;
+            }
+            const int token = (w.first + ch + i) * CT + warp * 16;
+            const float2 sc = sm.scales[stage][(warp * 16) / rows_piece];
+            if (!(sc.y < 0.f) && token < any_hi && token + 16 > any_lo) {
+                // ---- scores of 16 tokens
+                float s[2][4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+                    const int row = warp * 16 + n * 8 + g;
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+                        const int col = D == 128 ? (2 * t4 + c) ^ (row & 7) : t4 ^ ((row >> 1) & 3);
+                        const uint4 kw = *reinterpret_cast<const uint4*>(sm.k[stage] + row * D + col * 16);
+                        const uint32_t* e = reinterpret_cast<const uint32_t*>(&kw);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            mma_16816_pure(s[n], qf[4 * c + x], kv8_pair<0>(e[x]), kv8_pair<2>(e[x]));
+                    }
+                }
+                // ---- weights
+                const uint32_t vb = __float_as_uint(fmaxf(sc.y, 0x1p-103f));
+                const int ex = min((int)(vb >> 23) - 127, 126);
+                const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+                const float frac = sc.y * down;              // (of a NaN scale NaN, of 0 zero)
+                const float a0 = sc.x * qa[0], a1 = sc.x * qa[1], fex = (float)ex;
+                float e0[4], e1[4];                          // rows g and g + 8 (SPLIT: e0 alone)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        e0[2 * n + x] = fmaf(SPLIT ? s[n][x] + s[n][2 + x] : s[n][x], a0, fex);
+                        if (!SPLIT) e1[2 * n + x] = fmaf(s[n][2 + x], a1, fex);
+                    }
+                const bool inside = token >= safe_lo && token + 16 <= safe_hi;
+                if (!inside) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int t = token + (x >> 1) * 8 + 2 * t4 + (x & 1);
+                        if (t < lo[0] || t >= hi[0]) e0[x] = NONE;
+                        if (!SPLIT && (t < lo[1] || t >= hi[1])) e1[x] = NONE;
+                    }
+                }
+                float t0 = fmaxf(fmaxf(e0[0], e0[1]), fmaxf(e0[2], e0[3]));
+                float t1 = SPLIT ? NONE : fmaxf(fmaxf(e1[0], e1[1]), fmaxf(e1[2], e1[3]));
+                if (__any_sync(0xffffffffu, t0 > m[0] + RAISE || t1 > m[1] + RAISE)) {
+#pragma unroll
+                    for (int half = 0; half < HALVES; ++half) {
+                        float t = half ? t1 : t0;
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+                        if (!(t > m[half] + RAISE)) continue;             // the same in a row's four lanes
+                        const float f = exp2_fast(m[half] - (t - HEAD));
+                        m[half] = t - HEAD;
+                        l[half] *= f;
+#pragma unroll
+                        for (int c = 0; c < NT; ++c) {
+                            acc[c][2 * half] *= f;
+                            acc[c][2 * half + 1] *= f;
+                            if (SPLIT) {
+                                acc[c][2] *= f;
+                                acc[c][3] *= f;
+                            }
+                        }
+                    }
+                }
+                uint32_t pf[4], pl[4];
+                {
+                    const float m0 = m[0] == NONE ? 0.f : m[0];
+                    float sum = 0.f;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const bool dead = !inside && e0[x] == NONE;
+                        const float e = exp2_fast(e0[x] - m0);
+                        sum += e;
+                        e0[x] = dead ? 0.f : e * frac;
+                    }
+                    l[0] = fmaf(sum, down, l[0]);
+                    pf[0] = pack_half2(e0[0], e0[1]);
+                    pf[2] = pack_half2(e0[2], e0[3]);
+                    if (SPLIT) {
+                        pf[1] = rest_half2(e0[0], e0[1], pf[0]);
+                        pf[3] = rest_half2(e0[2], e0[3], pf[2]);
+                    } else {
+                        const float m1 = m[1] == NONE ? 0.f : m[1];
+                        float sum1 = 0.f;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const bool dead = !inside && e1[x] == NONE;
+                            const float e = exp2_fast(e1[x] - m1);
+                            sum1 += e;
+                            e1[x] = dead ? 0.f : e * frac;
+                        }
+                        l[1] = fmaf(sum1, down, l[1]);
+                        pf[1] = pack_half2(e1[0], e1[1]);
+                        pf[3] = pack_half2(e1[2], e1[3]);
+                    }
+                    if (TWO) {
+                        pl[0] = rest_half2(e0[0], e0[1], pf[0]);
+                        pl[1] = rest_half2(e1[0], e1[1], pf[1]);
+                        pl[2] = rest_half2(e0[2], e0[3], pf[2]);
+                        pl[3] = rest_half2(e1[2], e1[3], pf[3]);
+                    }
+                }
+                // ---- values: lane's tokens 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4, columns D/8 g ..
+                uint32_t vw[4][D / 32];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int row = warp * 16 + (x >> 1) * 8 + 2 * t4 + (x & 1);
+                    if constexpr (D == 128) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(sm.v[stage] + row * D + (g ^ (row & 7)) * 16);
+                        vw[x][0] = u.x, vw[x][1] = u.y, vw[x][2] = u.z, vw[x][3] = u.w;
+                    } else {
+                        const uint2 u = *reinterpret_cast<const uint2*>(
+                            sm.v[stage] + row * D + ((g >> 1) ^ ((row >> 1) & 3)) * 16 + (g & 1) * 8);
+                        vw[x][0] = u.x, vw[x][1] = u.y;
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) {
+                    const uint32_t l01 = __byte_perm(vw[0][x], vw[1][x], 0x5140), h01 = __byte_perm(vw[0][x], vw[1][x], 0x7362);
+                    const uint32_t l23 = __byte_perm(vw[2][x], vw[3][x], 0x5140), h23 = __byte_perm(vw[2][x], vw[3][x], 0x7362);
+                    const uint32_t b0[4] = {kv8_pair<0>(l01), kv8_pair<2>(l01), kv8_pair<0>(h01), kv8_pair<2>(h01)};
+                    const uint32_t b1[4] = {kv8_pair<0>(l23), kv8_pair<2>(l23), kv8_pair<0>(h23), kv8_pair<2>(h23)};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        mma_16816_pure(acc[4 * x + y], pf, b0[y], b1[y]);
+                        if (TWO) mma_16816_pure(acc[4 * x + y], pl, b0[y], b1[y]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.empty[stage]);
+            if (++stage == STAGES) stage = 0, phase ^= 1;
+        }
+
+        // ---- the four warps' sums, in the order of the warps
+#pragma unroll
+        for (int half = 0; half < HALVES; ++half) {
+            l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
+            l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
+            if (t4 == 0) {
+                sm.m[warp][g + 8 * half] = m[half];
+                sm.l[warp][g + 8 * half] = l[half];
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float* dst = &sm.acc[warp][(g + 8 * half) * (D + 4) + (2 * t4 + x) * NT];
+#pragma unroll
+                for (int c = 0; c < NT; c += 4) {
+                    float4 o;
+                    float* po = reinterpret_cast<float*>(&o);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        po[y] = SPLIT ? acc[c + y][x] + acc[c + y][2 + x] : acc[c + y][2 * half + x];
+                    *reinterpret_cast<float4*>(dst + c) = o;
+                }
+            }
+        }
+        ok = !named_sync_or(!ok);
+        if (!ok) break;
+        const bool whole = run == w.count;
+        float* part = parts + ((size_t)cta * 2 + (ch == 0 ? 1 : 0)) * part_floats(D);
+        for (int at = tid; at < rows * (D / 4); at += WARPS * 32) {
+            const int r = at / (D / 4), col = at % (D / 4) * 4;
+            float top = sm.m[0][r];
+#pragma unroll
+            for (int i = 1; i < WARPS; ++i) top = fmaxf(top, sm.m[i][r]);
+            float sum = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < WARPS; ++i) {
+                const float f = sm.m[i][r] == NONE ? (sm.l[i][r] != 0.f ? 1.f : 0.f) : exp2_fast(sm.m[i][r] - top);
+                sum = fmaf(sm.l[i][r], f, sum);
+                const float4 u = *reinterpret_cast<const float4*>(&sm.acc[i][r * (D + 4) + col]);
+                o.x = fmaf(u.x, f, o.x);
+                o.y = fmaf(u.y, f, o.y);
+                o.z = fmaf(u.z, f, o.z);
+                o.w = fmaf(u.w, f, o.w);
+            }
+            if (whole) {
+                int64_t at_lse;
+                T* dst = static_cast<T*>(a.out) + out_row<T>(a, w.q, head, tile * RM + r, &at_lse) + col;
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                dst[0] = kv8_round<T>(o.x * inv);
+                dst[1] = kv8_round<T>(o.y * inv);
+                dst[2] = kv8_round<T>(o.z * inv);
+                dst[3] = kv8_round<T>(o.w * inv);
+                if (col == 0 && a.lse) a.lse[at_lse] = lse_of(top, sum);
+            } else {
+                *reinterpret_cast<float4*>(part + 32 + r * D + col) = o;
+                if (col == 0) part[r] = top, part[16 + r] = sum;
+            }
+        }
+        if (!whole && ch == 0) {
+            const long long last = w.pos + w.count - 1;
+            joint = Joint{w.s, head, tile, cut.of(last) - cta + 1};
+        }
+        named_sync();
+        w.pos += run;
+    }
+    if (tid == 0) joints[cta] = ok ? joint : Joint{0, 0, 0, 0};
+}
+
+// Rows that a cut divided: the pieces' sums in the order of the tokens.  A warp takes a row.
+template <class T, int D>
+__global__ void __launch_bounds__(256)
+kv8_join_kernel(const __grid_constant__ Kv8Attention a, const float* parts, const Joint* joints) {
+    constexpr int RM = sizeof(T) == 4 ? 8 : 16;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int cta = blockIdx.x, lane = threadIdx.x & 31;
+    const Joint j = joints[cta];
+    if (j.pieces == 0) return;
+    const Kv8Seq q = kv8_seq(a.c, j.s);
+    const int rows = min(q.n * a.G - j.tile * RM, RM);
+    const float NONE = __int_as_float(0xff800000);
+    constexpr int PER = D / 32;
+    for (int r = threadIdx.x >> 5; r < rows; r += blockDim.x >> 5) {
+        // piece 0 is this CTA's last, the others are their CTAs' first
+        const float* first = parts + ((size_t)cta * 2 + 1) * part_floats(D);
+        const float* rest = parts + (size_t)cta * 2 * part_floats(D);
+        float top = NONE;
+        for (int i = lane; i < j.pieces; i += 32)
+            top = fmaxf(top, (i ? rest + i * 2 * part_floats(D) : first)[r]);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        float sum = 0.f, o[PER];
+#pragma unroll
+        for (int c = 0; c < PER; ++c) o[c] = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < j.pieces; ++i) {
+            const float* p = i ? rest + i * 2 * part_floats(D) : first;
+            const float m = p[r], l = p[16 + r];
+            const float f = m == NONE ? (l != 0.f ? 1.f : 0.f) : exp2_fast(m - top);
+            sum = fmaf(l, f, sum);
+#pragma unroll
+            for (int c = 0; c < PER; ++c) o[c] = fmaf(p[32 + r * D + lane + 32 * c], f, o[c]);
+        }
+        int64_t at_lse;
+        T* dst = static_cast<T*>(a.out) + out_row<T>(a, q, j.head, j.tile * RM + r, &at_lse);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int c = 0; c < PER; ++c) dst[lane + 32 * c] = kv8_round<T>(o[c] * inv);
+        if (lane == 0 && a.lse) a.lse[at_lse] = lse_of(top, sum);
+    }
+}
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 152;
+    return n;
+}
+
+// Two CTAs a SM, and none that could never have a chunk.
+int grid_of(const Kv8Attention& a) {
+    const int64_t most = (int64_t)a.c.seqs * a.c.H * (((int64_t)a.c.width << a.c.logB) / CT + 1) *
+                         (((int64_t)a.c.T * a.G + 7) / 8);
+    const int64_t full = 2 * sm_count();
+    return (int)(most < full ? most : full);
+}
+
+template <class T, int D>
+cudaError_t run(const Kv8Attention& a, void* scratch, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(kv8_stream_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)sizeof(Shared<D>));
+    if (e != cudaSuccess) return e;
+    const int grid = grid_of(a);
+    float* parts = static_cast<float*>(scratch);
+    Joint* joints = reinterpret_cast<Joint*>(parts + (size_t)grid * 2 * part_floats(D));
+    g_launched.store(true, std::memory_order_release);
+    e = launch_pdl(kv8_stream_kernel<T, D>, dim3(grid), dim3(THREADS), sizeof(Shared<D>), st, a, parts, joints);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kv8_join_kernel<T, D>, dim3(grid), dim3(256), 0, st, a, (const float*)parts, (const Joint*)joints);
+}
+
+template <class T>
+cudaError_t run_d(const Kv8Attention& a, void* scratch, cudaStream_t st) {
+    return a.c.D == 64 ? run<T, 64>(a, scratch, st) : run<T, 128>(a, scratch, st);
+}
+
+}  // namespace
+
+int kv8_few_rows(int dtype) { return dtype == TQ2_F32 ? 8 : 16; }
+
+size_t kv8_stream_scratch(const Kv8Attention& a) {
+    return (size_t)grid_of(a) * (2 * part_floats(a.c.D) * sizeof(float) + sizeof(Joint));
+}
+
+cudaError_t launch_kv8_stream(const Kv8Attention& a, void* scratch, cudaStream_t st) {
+    if (a.dtype == TQ2_F32) return run_d<float>(a, scratch, st);
+    if (a.dtype == TQ2_F16) return run_d<__half>(a, scratch, st);
+    return run_d<__nv_bfloat16>(a, scratch, st);
+}
+
+unsigned int read_clear_dev_error_kv8_stream(cudaStream_t st) { return read_clear_record(st); }
+
+}  // namespace tq2

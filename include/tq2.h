@@ -628,6 +628,111 @@ TQ2_API tq2_status moe_experts(q4_handle gate, q4_handle up, q4_handle down, con
                                const int32_t* ids, const float* weights, const int32_t* offsets,
                                const int32_t* slots, void* out, int64_t ldo, int64_t T, int k, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* 8-bit cache of keys and values                                            */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * The cache: a pool of blocks of `tokens` tokens, in the caller's DEVICE memory.
+ *   codes   uint8[blocks][2][heads][tokens][dim] (keys, then values), 16-byte aligned.
+ *   scales  float[blocks][2][heads]: one scale for a block's tokens in a head, >= 0 or NaN.
+ * A code c stands for (c - 128) * scale.
+ *   tokens 16, 32, 64 or 128;  dim 64 or 128;  1 <= heads <= 1024;  blocks >= 1 with
+ *   blocks * 2 * heads * tokens < 2^31.  Else TQ2_ESHAPE.
+ */
+typedef struct {
+    uint8_t* codes;
+    float* scales;
+    int64_t blocks;
+    int heads, tokens, dim;
+} kv8_cache;
+
+/*
+ * Sequences of a call (the arrays in DEVICE memory, read when the kernels run, so a captured
+ * call follows what they hold at its replay):
+ *   table    int32, a row of `width` block numbers a sequence, rows `ld` >= width elements
+ *            apart: token t of sequence s lies in block table[s*ld + t/tokens], at t % tokens.
+ *   offsets  int32[seqs+1], ascending: rows offsets[s] .. offsets[s+1]-1 of the call's other
+ *            arrays are sequence s's last tokens.
+ *   lens     int32[seqs]: tokens of each sequence, those n = offsets[s+1]-offsets[s] among
+ *            them; row offsets[s]+j is at position lens[s]-n+j.
+ *   1 <= seqs, 1 <= width, width * tokens <= 2^30.  Else TQ2_ESHAPE.
+ * Entries of any contents are safe: offsets outside the rows and lengths outside the table are
+ * clamped to them, ranges that go back are empty, and a block number outside the pool names
+ * no block.  Entries past a sequence's tokens are not read.
+ */
+typedef struct {
+    const int32_t* table;
+    int64_t ld;
+    const int32_t* offsets;
+    const int32_t* lens;
+    int width, seqs;
+} kv8_batch;
+
+/*
+ * kv8_write -- quantise the sequences' last tokens as they enter their blocks.
+ *
+ * Per block, head, and keys or values, each operation rounded to f32, halves to even: with
+ * M the largest magnitude of the new tokens, d0 the block's scale where it holds
+ * tokens of the sequence before the new ones (0 where not),
+ *     d = max(d0, M / 127)   (M below 2^-96 counts as 0)
+ *     c = 128 + clamp(rint(x * (1 / d)), -127, 127)          of the new tokens
+ *     c = 128 + rint((c - 128) * (d0 / d))                   of those before, where d > d0
+ * (d = 0: c = 128).  Codes past the new tokens keep what they hold, which nothing reads.
+ * A NaN or Inf among the new tokens leaves the block's scale NaN: every value of that
+ * block and head reads as NaN until a write begins the block anew.
+ *
+ *   c, b    HOST structs, read during the call.
+ *   k, v    DEVICE, dtype (tq2_dtype), T rows of `heads` heads of dim neighbouring elements;
+ *           kt, kh and vt, vh: elements from row to row and from head to head.  Fetched
+ *           faster where 16-byte aligned throughout.
+ *   0 <= T, T * heads * dim < 2^40.
+ * Tokens without a position (n > lens[s]) or without a block are not written.  What a
+ * block of two sequences (shared, or named twice) holds after both were written into it
+ * is unspecified.  Asynchronous, no scratch.
+ */
+TQ2_API tq2_status kv8_write(const kv8_cache* c, const kv8_batch* b, const void* k, int64_t kt, int64_t kh,
+                             const void* v, int64_t vt, int64_t vh, int dtype, int64_t T, void* stream);
+
+/*
+ * kv8_read -- the sequences' last tokens as values: k[offsets[s]+j][head] = (c - 128) * scale, rounded
+ * to f32 and then to dtype.  Arguments as kv8_write's; k and v are written, and keep what they
+ * hold in rows without a position, without a block, or of no sequence.  Asynchronous, no scratch.
+ */
+TQ2_API tq2_status kv8_read(const kv8_cache* c, const kv8_batch* b, void* k, int64_t kt, int64_t kh, void* v,
+                            int64_t vt, int64_t vh, int dtype, int64_t T, void* stream);
+
+/*
+ * kv8_attention -- attention of the sequences' last tokens over the cache.
+ *
+ * Query head h of a row reads head h / (Hq / heads) of the cache:
+ *     s_t = scale * sum_d q[row][h][d] k_t[d],   p = softmax of s over the seen tokens t,
+ *     out[row][h] = sum_t p_t v_t,   lse[row][h] = ln sum_t exp(s_t).
+ * Of tokens 0 .. lens[s]-1, those with a block, a row at position i sees
+ *     causal:  t <= i, and t > i - window where window > 0;      else all.
+ * A row that sees none has out 0 and lse -Inf.
+ *
+ *   q, out  DEVICE, dtype, T rows of Hq heads of dim neighbouring elements; qt, qh and ot, oh:
+ *           elements from row to row and from head to head.  out must not overlap q. Rows of no
+ *           sequence are left as they are, in lse too.
+ *   lse     DEVICE float[T][Hq] or NULL.
+ *   Hq      a multiple of heads, T * Hq < 2^31.  Else TQ2_ESHAPE.
+ *   scale   finite;  causal 0 or 1;  window >= 0, 0 unless causal.  Else TQ2_EINVAL.
+ *   max_q   a bound of the sequences' rows that the choice of kernels goes by (0: T); results
+ *           of longer ones are right too, but slower.
+ * f16 and bf16 queries and the codes enter the products exactly (elements below 2^-29 of their
+ * row's largest lose bits), f32 queries within 2^-22 of each element and 2^-39 of the row's
+ * largest.  A token's weight times its block's scale is rounded to f16 for bf16 results (2^-11), to two
+ * f16 parts for f16 and f32 ones (2^-22), and to 2^-30 of the row's largest at the least.  Sums
+ * are f32, results rounded once.  A row of q with NaN or Inf gives NaN in its own row alone; a NaN scale reaches the rows
+ * that see a token of its block.  The order of additions depends on lengths, shapes and the
+ * GPU alone, so results are the same from run to run.  Asynchronous; scratch from the
+ * library's stream-ordered pool.
+ */
+TQ2_API tq2_status kv8_attention(const kv8_cache* c, const kv8_batch* b, const void* q, int64_t qt, int64_t qh,
+                                 void* out, int64_t ot, int64_t oh, int dtype, float* lse, int64_t T, int Hq,
+                                 float scale, int causal, int64_t window, int64_t max_q, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
