@@ -117,7 +117,8 @@ tq2_status tq2_device_status(void* stream) {
                              tq2::read_clear_dev_error_q4_g64(S(stream)) |
                              tq2::read_clear_dev_error_q4_g128(S(stream)) |
                              tq2::read_clear_dev_error_moe_umma(S(stream)) |
-                             tq2::read_clear_dev_error_kv8_stream(S(stream));
+                             tq2::read_clear_dev_error_kv8_stream(S(stream)) |
+                             tq2::read_clear_dev_error_kv8_umma(S(stream));
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "tq2_device_status");
     if (err) return fail(TQ2_ETIMEOUT, "a bounded device-side wait ran out (record 0x%x)", err);

@@ -133,11 +133,14 @@ struct Kv8Attention {
     int dtype, G;               // query heads a head of the cache
     float scale;                // softmax scale * log2(e)
     int causal, window;
-    int few;                    // sequences of more rows (queries * G) are left to the other path
+    int few;                    // sequences of at most so many rows (queries * G) are the streaming path's
 };
 int kv8_few_rows(int dtype);    // most rows of a sequence that the streaming path takes in one pass
 size_t kv8_stream_scratch(const Kv8Attention& a);
 cudaError_t launch_kv8_stream(const Kv8Attention& a, void* scratch, cudaStream_t st);
 unsigned int read_clear_dev_error_kv8_stream(cudaStream_t st);
+size_t kv8_umma_scratch(const Kv8Attention& a);
+cudaError_t launch_kv8_umma(const Kv8Attention& a, void* scratch, cudaStream_t st);
+unsigned int read_clear_dev_error_kv8_umma(cudaStream_t st);
 
 }  // namespace tq2

@@ -103,9 +103,9 @@ tq2_status kv8_attention(const kv8_cache* c, const kv8_batch* b, const void* q, 
     if (!q || !out) return (tq2_status)set_error(TQ2_EINVAL, "kv8_attention: null pointer");
     if (off_element(q, element_size(dtype)) || off_element(out, element_size(dtype)) || off_element(lse, 4))
         return (tq2_status)set_error(TQ2_EINVAL, "kv8_attention: q, out and lse must be element-aligned");
-    const uint32_t rows = (uint32_t)(c->tokens < 64 ? c->tokens : 64);
+    const uint32_t box = (uint32_t)(c->tokens < 64 ? c->tokens : 64);
     if (!make_tensor_map_2d(&a.map, CU_TENSOR_MAP_DATA_TYPE_UINT8, c->codes, (uint64_t)c->dim,
-                            (uint64_t)c->blocks * 2 * c->heads * c->tokens, (uint64_t)c->dim, (uint32_t)c->dim, rows,
+                            (uint64_t)c->blocks * 2 * c->heads * c->tokens, (uint64_t)c->dim, (uint32_t)c->dim, box,
                             c->dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
         return (tq2_status)set_error(TQ2_ECUDA, "kv8_attention: the cache cannot be mapped for TMA");
     a.q = q;
@@ -120,15 +120,22 @@ tq2_status kv8_attention(const kv8_cache* c, const kv8_batch* b, const void* q, 
     a.scale = scale * 1.4426950408889634f;                    // powers of 2 from here on
     a.causal = causal;
     a.window = window < ((int64_t)1 << 30) ? (int)window : 0;  // no sequence is longer
-    a.few = 0x7fffffff;
+    // Rows of a sequence: few go the streaming way, many the tensor cores'.  Which sequences have how many
+    // the host does not know, so where both may be there both kernels are launched, each for its own.
+    const int64_t rows = (max_q && max_q < T ? max_q : T) * a.G;
+    const bool few = rows <= kv8_few_rows(dtype);
+    a.few = few ? 0x7fffffff : b->seqs == 1 ? 0 : kv8_few_rows(dtype);
+    const size_t stream_bytes = (kv8_stream_scratch(a) + 255) / 256 * 256;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     Scratch mem(st);
-    cudaError_t e = scratch_alloc(&mem.p, kv8_stream_scratch(a), st);
+    cudaError_t e = scratch_alloc(&mem.p, stream_bytes + (few ? 0 : kv8_umma_scratch(a)), st);
     if (e != cudaSuccess) {
         mem.p = nullptr;
         return cuda_status(e, "kv8_attention: scratch");
     }
-    return cuda_status(launch_kv8_stream(a, mem.p, st), "kv8_attention");
+    if (!few) e = launch_kv8_umma(a, static_cast<char*>(mem.p) + stream_bytes, st);
+    if (e == cudaSuccess && a.few) e = launch_kv8_stream(a, mem.p, st);
+    return cuda_status(e, "kv8_attention");
 }
 
 }  // extern "C"

@@ -1,0 +1,121 @@
+// kv8_join.cuh -- what both attention paths of the 8-bit cache share: the even cut of
+// their work over the CTAs, and the kernel that joins what a cut divided.
+#pragma once
+
+#include "kv8.cuh"
+
+namespace tq2 {
+
+// CTAs' shares of `total` units: as even as can be, over as many CTAs as have `least` each.
+struct Kv8Cut {
+    long long base, more;
+    int ctas;
+    __device__ __forceinline__ Kv8Cut(long long total, int grid, int least) {
+        const long long useful = (total + least - 1) / least;
+        ctas = useful < grid ? (int)useful : grid;
+        base = ctas ? total / ctas : 0;
+        more = ctas ? total - base * ctas : 0;
+    }
+    __device__ __forceinline__ long long begin(int c) const { return c * base + (c < more ? c : more); }
+    __device__ __forceinline__ int of(long long unit) const {
+        const long long fat = more * (base + 1);
+        return (int)(unit < fat ? unit / (base + 1) : more + (unit - fat) / base);
+    }
+};
+
+// A tile of rows that a cut divided, noted by the CTA that has the first piece: that CTA's last
+// piece (part 2 cta + 1), and the first ones (parts 2 (cta + i)) of the pieces-1 CTAs behind it.
+struct Kv8Joint {
+    int s, head, tile, pieces;
+};
+
+// A part: R references m, R sums l, R rows of D sums.
+__host__ __device__ constexpr size_t kv8_part_floats(int rows, int D) { return (size_t)rows * (D + 2); }
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// What f16 left of a and b.
+__device__ __forceinline__ uint32_t rest_half2(float a, float b, uint32_t h) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return pack_half2(a - f.x, b - f.y);
+}
+
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// One of the barrier's arrivals, when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ float kv8_none() { return __int_as_float(0xff800000); }
+
+// Where row r of a sequence's head goes in out; its place in lse.
+__device__ __forceinline__ int64_t kv8_out_row(const Kv8Attention& a, const Kv8Seq& q, int head, int r, int64_t* lse) {
+    const int token = q.q0 + r / a.G, h = head * a.G + r % a.G;
+    *lse = (int64_t)token * a.c.H * a.G + h;
+    return token * a.ot + h * a.oh;
+}
+__device__ __forceinline__ float kv8_lse(float m, float l) {
+    return l > 0.f || isnan(l) ? (log2f(l) + m) * 0.69314718055994531f : kv8_none();
+}
+// Factor that takes sums of reference m to those of reference top; sums without a reference are 0 or NaN.
+__device__ __forceinline__ float kv8_factor(float m, float l, float top) {
+    return m == kv8_none() ? (l != 0.f ? 1.f : 0.f) : exp2_fast(m - top);
+}
+
+// The pieces' sums in the order of the tokens.  A warp takes a row.
+template <class T, int D, int RM>
+__global__ void __launch_bounds__(256)
+kv8_join_kernel(const __grid_constant__ Kv8Attention a, const float* parts, const Kv8Joint* joints) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int cta = blockIdx.x, lane = threadIdx.x & 31;
+    const Kv8Joint j = joints[cta];
+    if (j.pieces == 0) return;
+    const Kv8Seq q = kv8_seq(a.c, j.s);
+    const int rows = min(q.n * a.G - j.tile * RM, RM);
+    constexpr int PER = D / 32;
+    constexpr size_t PART = kv8_part_floats(RM, D);
+    const float* first = parts + ((size_t)cta * 2 + 1) * PART;
+    const float* rest = parts + (size_t)cta * 2 * PART;
+    for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8) {
+        float top = kv8_none();
+        for (int i = lane; i < j.pieces; i += 32) top = fmaxf(top, (i ? rest + i * 2 * PART : first)[r]);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        float sum = 0.f, o[PER];
+#pragma unroll
+        for (int c = 0; c < PER; ++c) o[c] = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < j.pieces; ++i) {
+            const float* p = i ? rest + i * 2 * PART : first;
+            const float l = p[RM + r], f = kv8_factor(p[r], l, top);
+            sum = fmaf(l, f, sum);
+#pragma unroll
+            for (int c = 0; c < PER; ++c) o[c] = fmaf(p[2 * RM + r * D + lane + 32 * c], f, o[c]);
+        }
+        int64_t at_lse;
+        T* dst = static_cast<T*>(a.out) + kv8_out_row(a, q, j.head, j.tile * RM + r, &at_lse);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int c = 0; c < PER; ++c) dst[lane + 32 * c] = kv8_round<T>(o[c] * inv);
+        if (lane == 0 && a.lse) a.lse[at_lse] = kv8_lse(top, sum);
+    }
+}
+
+inline int kv8_sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 152;
+    return n;
+}
+
+}  // namespace tq2

@@ -20,7 +20,7 @@
 // conflicts), four warps take 16 tokens of each.
 #include <type_traits>
 
-#include "kv8.cuh"
+#include "kv8_join.cuh"
 #include "q4.cuh"
 
 namespace tq2 {
@@ -68,50 +68,6 @@ __device__ __forceinline__ long long open_seq(const Kv8Attention& a, int s, Walk
     return (long long)w.tiles * a.c.H * w.count;
 }
 
-// CTA's share of `total` chunks: as even as can be, over as many CTAs as have two each.
-struct Cut {
-    long long base, more;
-    int ctas;
-    __device__ __forceinline__ Cut(long long total, int grid) {
-        const long long useful = (total + MIN_CHUNKS - 1) / MIN_CHUNKS;
-        ctas = useful < grid ? (int)useful : grid;
-        base = ctas ? total / ctas : 0;
-        more = ctas ? total - base * ctas : 0;
-    }
-    __device__ __forceinline__ long long begin(int c) const { return c * base + (c < more ? c : more); }
-    __device__ __forceinline__ int of(long long chunk) const {
-        const long long fat = more * (base + 1);
-        return (int)(chunk < fat ? chunk / (base + 1) : more + (chunk - fat) / base);
-    }
-};
-
-// What a cut divided: written by the CTA that has the first piece.
-struct Joint {
-    int s, head, tile, pieces;
-};
-
-__host__ __device__ constexpr size_t part_floats(int D) { return 16 * (size_t)(D + 2); }
-
-__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-// What f16 left of a and b.
-__device__ __forceinline__ uint32_t rest_half2(float a, float b, uint32_t h) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    return pack_half2(a - f.x, b - f.y);
-}
 // Barrier of the computing warps; the second tells all of them whether any gave up.
 __device__ __forceinline__ void named_sync() { asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory"); }
 __device__ __forceinline__ bool named_sync_or(bool any) {
@@ -127,21 +83,9 @@ __device__ __forceinline__ bool named_sync_or(bool any) {
     return r != 0;
 }
 
-// Row r's output and the logarithm of its sum.
-template <class T>
-__device__ __forceinline__ int64_t out_row(const Kv8Attention& a, const Kv8Seq& q, int head, int r, int64_t* lse) {
-    const int token = q.q0 + r / a.G, h = head * a.G + r % a.G;
-    *lse = (int64_t)token * a.c.H * a.G + h;
-    return token * a.ot + h * a.oh;
-}
-
-__device__ __forceinline__ float lse_of(float m, float l) {
-    return l > 0.f || isnan(l) ? (log2f(l) + m) * 0.69314718055994531f : __int_as_float(0xff800000);
-}
-
 template <class T, int D>
 __global__ void __launch_bounds__(THREADS, 2)
-kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Joint* joints) {
+kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* joints) {
     constexpr bool SPLIT = sizeof(T) == 4;
     // weights of f16 outputs in two parts too: one part's rounding is as large as the output's own
     constexpr bool TWO = std::is_same<T, __half>::value;
@@ -183,7 +127,7 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Joint* j
         if (i < warp) before += sm.sums[i];
         total += sm.sums[i];
     }
-    const Cut cut(total, gridDim.x);
+    const Kv8Cut cut(total, gridDim.x, MIN_CHUNKS);
     const int cta = blockIdx.x;
     if (cta >= cut.ctas) {
         if (tid == 0) joints[cta].pieces = 0;
@@ -262,7 +206,7 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Joint* j
     // ----------------------------------------------------------- consumers
     const int g = lane >> 2, t4 = lane & 3;
     int stage = 0, phase = 0;
-    Joint joint{0, 0, 0, 0};
+    Kv8Joint joint{0, 0, 0, 0};
     bool ok = true;
     while (w.pos < w.end) {
         while (w.pos >= w.base + span) {
@@ -336,7 +280,7 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Joint* j
         float acc[NT][4];
 #pragma unroll
         for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-        const float NONE = __int_as_float(0xff800000);
+        const float NONE = kv8_none();
         float m[2] = {NONE, NONE}, l[2] = {0.f, 0.f};
 
         for (int i = 0; i < run && ok; ++i) {
@@ -506,7 +450,7 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Joint* j
         ok = !named_sync_or(!ok);
         if (!ok) break;
         const bool whole = run == w.count;
-        float* part = parts + ((size_t)cta * 2 + (ch == 0 ? 1 : 0)) * part_floats(D);
+        float* part = parts + ((size_t)cta * 2 + (ch == 0 ? 1 : 0)) * kv8_part_floats(RM, D);
         for (int at = tid; at < rows * (D / 4); at += WARPS * 32) {
             const int r = at / (D / 4), col = at % (D / 4) * 4;
             float top = sm.m[0][r];
@@ -516,7 +460,7 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Joint* j
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < WARPS; ++i) {
-                const float f = sm.m[i][r] == NONE ? (sm.l[i][r] != 0.f ? 1.f : 0.f) : exp2_fast(sm.m[i][r] - top);
+                const float f = kv8_factor(sm.m[i][r], sm.l[i][r], top);
                 sum = fmaf(sm.l[i][r], f, sum);
                 const float4 u = *reinterpret_cast<const float4*>(&sm.acc[i][r * (D + 4) + col]);
                 o.x = fmaf(u.x, f, o.x);
@@ -526,84 +470,33 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Joint* j
             }
             if (whole) {
                 int64_t at_lse;
-                T* dst = static_cast<T*>(a.out) + out_row<T>(a, w.q, head, tile * RM + r, &at_lse) + col;
+                T* dst = static_cast<T*>(a.out) + kv8_out_row(a, w.q, head, tile * RM + r, &at_lse) + col;
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 dst[0] = kv8_round<T>(o.x * inv);
                 dst[1] = kv8_round<T>(o.y * inv);
                 dst[2] = kv8_round<T>(o.z * inv);
                 dst[3] = kv8_round<T>(o.w * inv);
-                if (col == 0 && a.lse) a.lse[at_lse] = lse_of(top, sum);
+                if (col == 0 && a.lse) a.lse[at_lse] = kv8_lse(top, sum);
             } else {
-                *reinterpret_cast<float4*>(part + 32 + r * D + col) = o;
-                if (col == 0) part[r] = top, part[16 + r] = sum;
+                *reinterpret_cast<float4*>(part + 2 * RM + r * D + col) = o;
+                if (col == 0) part[r] = top, part[RM + r] = sum;
             }
         }
         if (!whole && ch == 0) {
             const long long last = w.pos + w.count - 1;
-            joint = Joint{w.s, head, tile, cut.of(last) - cta + 1};
+            joint = Kv8Joint{w.s, head, tile, cut.of(last) - cta + 1};
         }
         named_sync();
         w.pos += run;
     }
-    if (tid == 0) joints[cta] = ok ? joint : Joint{0, 0, 0, 0};
-}
-
-// Rows that a cut divided: the pieces' sums in the order of the tokens.  A warp takes a row.
-template <class T, int D>
-__global__ void __launch_bounds__(256)
-kv8_join_kernel(const __grid_constant__ Kv8Attention a, const float* parts, const Joint* joints) {
-    constexpr int RM = sizeof(T) == 4 ? 8 : 16;
-    pdl_launch_dependents();
-    pdl_wait();
-    const int cta = blockIdx.x, lane = threadIdx.x & 31;
-    const Joint j = joints[cta];
-    if (j.pieces == 0) return;
-    const Kv8Seq q = kv8_seq(a.c, j.s);
-    const int rows = min(q.n * a.G - j.tile * RM, RM);
-    const float NONE = __int_as_float(0xff800000);
-    constexpr int PER = D / 32;
-    for (int r = threadIdx.x >> 5; r < rows; r += blockDim.x >> 5) {
-        // piece 0 is this CTA's last, the others are their CTAs' first
-        const float* first = parts + ((size_t)cta * 2 + 1) * part_floats(D);
-        const float* rest = parts + (size_t)cta * 2 * part_floats(D);
-        float top = NONE;
-        for (int i = lane; i < j.pieces; i += 32)
-            top = fmaxf(top, (i ? rest + i * 2 * part_floats(D) : first)[r]);
-#pragma unroll
-        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        float sum = 0.f, o[PER];
-#pragma unroll
-        for (int c = 0; c < PER; ++c) o[c] = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < j.pieces; ++i) {
-            const float* p = i ? rest + i * 2 * part_floats(D) : first;
-            const float m = p[r], l = p[16 + r];
-            const float f = m == NONE ? (l != 0.f ? 1.f : 0.f) : exp2_fast(m - top);
-            sum = fmaf(l, f, sum);
-#pragma unroll
-            for (int c = 0; c < PER; ++c) o[c] = fmaf(p[32 + r * D + lane + 32 * c], f, o[c]);
-        }
-        int64_t at_lse;
-        T* dst = static_cast<T*>(a.out) + out_row<T>(a, q, j.head, j.tile * RM + r, &at_lse);
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-        for (int c = 0; c < PER; ++c) dst[lane + 32 * c] = kv8_round<T>(o[c] * inv);
-        if (lane == 0 && a.lse) a.lse[at_lse] = lse_of(top, sum);
-    }
-}
-
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 152;
-    return n;
+    if (tid == 0) joints[cta] = ok ? joint : Kv8Joint{0, 0, 0, 0};
 }
 
 // Two CTAs a SM, and none that could never have a chunk.
 int grid_of(const Kv8Attention& a) {
     const int64_t most = (int64_t)a.c.seqs * a.c.H * (((int64_t)a.c.width << a.c.logB) / CT + 1) *
                          (((int64_t)a.c.T * a.G + 7) / 8);
-    const int64_t full = 2 * sm_count();
+    const int64_t full = 2 * kv8_sm_count();
     return (int)(most < full ? most : full);
 }
 
@@ -612,13 +505,14 @@ cudaError_t run(const Kv8Attention& a, void* scratch, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kv8_stream_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)sizeof(Shared<D>));
     if (e != cudaSuccess) return e;
+    constexpr int RM = sizeof(T) == 4 ? 8 : 16;
     const int grid = grid_of(a);
     float* parts = static_cast<float*>(scratch);
-    Joint* joints = reinterpret_cast<Joint*>(parts + (size_t)grid * 2 * part_floats(D));
+    Kv8Joint* joints = reinterpret_cast<Kv8Joint*>(parts + (size_t)grid * 2 * kv8_part_floats(RM, D));
     g_launched.store(true, std::memory_order_release);
     e = launch_pdl(kv8_stream_kernel<T, D>, dim3(grid), dim3(THREADS), sizeof(Shared<D>), st, a, parts, joints);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kv8_join_kernel<T, D>, dim3(grid), dim3(256), 0, st, a, (const float*)parts, (const Joint*)joints);
+    return launch_pdl(kv8_join_kernel<T, D, RM>, dim3(grid), dim3(256), 0, st, a, (const float*)parts, (const Kv8Joint*)joints);
 }
 
 template <class T>
@@ -631,7 +525,7 @@ cudaError_t run_d(const Kv8Attention& a, void* scratch, cudaStream_t st) {
 int kv8_few_rows(int dtype) { return dtype == TQ2_F32 ? 8 : 16; }
 
 size_t kv8_stream_scratch(const Kv8Attention& a) {
-    return (size_t)grid_of(a) * (2 * part_floats(a.c.D) * sizeof(float) + sizeof(Joint));
+    return (size_t)grid_of(a) * (2 * kv8_part_floats(16, a.c.D) * sizeof(float) + sizeof(Kv8Joint));
 }
 
 cudaError_t launch_kv8_stream(const Kv8Attention& a, void* scratch, cudaStream_t st) {

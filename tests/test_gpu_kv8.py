@@ -159,7 +159,7 @@ def test_attention(lib, dtype, D, B, case):
     for beside, pad in (((2, 0), 0), ((0, 1), 3)):
         q, out, lse = c.attend(queries(rng, c.T, H * G, D), dtype, pad=pad, beside=beside, **options)
         check_attention(out, lse, attention_of(c, q, **options), dtype, D, max(lens), f"{case} {beside}")
-    assert np.array_equal(c.attend(q, dtype, lse=False, **options)[1], out)
+    assert np.array_equal(c.attend(q, dtype, pad=pad, beside=beside, lse=False, **options)[1], out)
 
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
