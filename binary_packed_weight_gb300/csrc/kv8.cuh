@@ -131,6 +131,7 @@ struct Kv8Attention {
     float* lse;                 // [T][Hq] or NULL
     int64_t qt, qh, ot, oh;     // strides in elements
     int dtype, G;               // query heads a head of the cache
+    int qvec;                   // rows of q are 16-byte aligned
     float scale;                // softmax scale * log2(e)
     int causal, window;
     int few;                    // sequences of at most so many rows (queries * G) are the streaming path's

@@ -117,6 +117,8 @@ tq2_status kv8_attention(const kv8_cache* c, const kv8_batch* b, const void* q, 
     a.oh = oh;
     a.dtype = dtype;
     a.G = Hq / c->heads;
+    const int64_t size = (int64_t)element_size(dtype);
+    a.qvec = (((int64_t)(uintptr_t)q | qt * size | qh * size) & 15) == 0;
     a.scale = scale * 1.4426950408889634f;                    // powers of 2 from here on
     a.causal = causal;
     a.window = window < ((int64_t)1 << 30) ? (int)window : 0;  // no sequence is longer

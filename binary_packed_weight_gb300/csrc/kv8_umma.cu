@@ -165,6 +165,158 @@ __device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
     return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float max16(const uint32_t* v) {
+    auto f = [&](int i) { return __uint_as_float(v[i]); };
+    const float a = max3(f(0), f(1), f(2)), b = max3(f(3), f(4), f(5)), c = max3(f(6), f(7), f(8));
+    const float d = max3(f(9), f(10), f(11)), e = max3(f(12), f(13), f(14));
+    return max3(max3(a, b, c), max3(d, e, f(15)), kv8_none());
+}
+
+// Scores are read from tensor memory twice (64 columns take 50 cycles) rather than held: the loops stay short, which
+// the instruction caches of warps in four different roles ask for.
+
+// The largest exponent of a row's 128 weights.  ALL: the row sees all tokens, else those of columns lo .. hi-1.
+template <bool ALL>
+__device__ __forceinline__ float tile_top(uint32_t s_addr, const float4* cons, float qa, int lo, int hi) {
+    float t = kv8_none();
+#pragma unroll 1
+    for (int c = 0; c < KT; c += 64) {
+        uint32_t v[2][32];
+        tmem_ld_32x32b_x32(s_addr + c, v[0]);
+        tmem_ld_32x32b_x32(s_addr + c + 32, v[1]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            const float4 k = cons[c / 16 + h];
+            const float ks = k.x * qa;
+            uint32_t* x = &v[h >> 1][16 * (h & 1)];
+            if (ALL) {
+                t = fmaxf(t, fmaf(max16(x), ks, k.y));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int col = c + 16 * h + e;
+                    t = fmaxf(t, col >= lo && col < hi ? fmaf(__uint_as_float(x[e]), ks, k.y) : kv8_none());
+                }
+            }
+        }
+    }
+    return t;
+}
+
+// The row's weights relative to ref, in place of its scores: 32 tokens' are 16 columns (and 16 of second
+// parts).  Returns l with their sum.
+template <bool TWO, bool ALL>
+__device__ __forceinline__ float tile_weights(uint32_t s_addr, const float4* cons, float qa, float ref, float l, int lo,
+                                              int hi) {
+#pragma unroll 1
+    for (int c = 0; c < KT; c += 64) {
+        uint32_t v[2][32];
+        tmem_ld_32x32b_x32(s_addr + c, v[0]);
+        tmem_ld_32x32b_x32(s_addr + c + 32, v[1]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            uint32_t ph[16], pl[16];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 k = cons[c / 16 + 2 * g + h];
+                const float ks = k.x * qa, off = k.y - ref;
+                const F2 ks2 = f2(ks, ks), off2 = f2(off, off);
+                F2 sum = f2(0.f, 0.f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t* at = &v[g][16 * h + 2 * e];
+                    const float2 x = f2_parts(f2_fma(f2(__uint_as_float(at[0]), __uint_as_float(at[1])), ks2, off2));
+                    float e0 = exp2_fast(x.x), e1 = exp2_fast(x.y);
+                    if (!ALL) {
+                        const int col = c + 32 * g + 16 * h + 2 * e;
+                        e0 = col >= lo && col < hi ? e0 : 0.f;
+                        e1 = col + 1 >= lo && col + 1 < hi ? e1 : 0.f;
+                    }
+                    sum = f2_add(sum, f2(e0, e1));
+                    ph[8 * h + e] = pack_half2(e0, e1);
+                    if (TWO) pl[8 * h + e] = rest_half2(e0, e1, ph[8 * h + e]);
+                }
+                const float2 both = f2_parts(sum);
+                l = fmaf(both.x + both.y, k.z, l);
+            }
+            tmem_st_32x32b_x16(s_addr + c + 32 * g, ph);
+            if (TWO) tmem_st_32x32b_x16(s_addr + c + 32 * g + 16, pl);
+        }
+    }
+    return l;
+}
+
+// A warp's 32 rows of queries, scaled by a power of two to 2^14 .. 2^15, into the layout of an MMA operand (the scores of
+// the rows before are there, so nobody reads those any more).  Returns the power of the lane's row.
+template <class T, int D>
+__device__ __forceinline__ int load_queries(const Kv8Attention& a, Shared<T, D>& sm, const Walk<Form<T, D>::ROWS>& w, int qi,
+                                            int warp, int lane) {
+    using F = Form<T, D>;
+    constexpr int EL = 16 / (int)sizeof(T), LPR = D / EL, RPP = 32 / LPR;   // a lane's elements, lanes a row, rows a pass
+    constexpr int DEEP = 8;                     // passes whose loads are in flight
+    const int in_row = lane % LPR, el = in_row * EL;
+    int power = 0;
+#pragma unroll 1
+    for (int p0 = 0; p0 < 32 / RPP; p0 += DEEP) {
+        uint4 raw[DEEP];
+#pragma unroll
+        for (int d = 0; d < DEEP; ++d) {
+            const int r = w.tile * F::ROWS + qi * 128 + warp * 32 + (p0 + d) * RPP + lane / LPR;
+            const int token = min(r, w.q.rows - 1) / a.G, h = min(r, w.q.rows - 1) - token * a.G;
+            const T* p = static_cast<const T*>(a.q) + (int64_t)(w.q.q.q0 + token) * a.qt + (int64_t)(w.head * a.G + h) * a.qh + el;
+            if (a.qvec) {
+                raw[d] = *reinterpret_cast<const uint4*>(p);
+            } else {
+                T* e = reinterpret_cast<T*>(&raw[d]);
+#pragma unroll
+                for (int k = 0; k < EL; ++k) e[k] = p[k];
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < DEEP; ++d) {
+            const int i = warp * 32 + (p0 + d) * RPP + lane / LPR;          // of the group
+            const bool live = w.tile * F::ROWS + qi * 128 + i < w.q.rows;
+            const T* u = reinterpret_cast<const T*>(&raw[d]);
+            float x[EL], most = 0.f;
+#pragma unroll
+            for (int k = 0; k < EL; ++k) {
+                x[k] = live ? kv8_wide(u[k]) : 0.f;
+                most = fmaxf(most, fabsf(x[k]));
+            }
+#pragma unroll
+            for (int k = 1; k < LPR; k <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, k));
+            const int e = min(max(141 - (int)(__float_as_uint(most) >> 23), -112), 126);
+            const float up = copysignf(__uint_as_float((uint32_t)(e + 127) << 23), a.scale);
+            const int of = __shfl_sync(0xffffffffu, e, (lane - (p0 + d) * RPP) * LPR & 31);
+            if (lane / RPP == p0 + d) power = of;
+            uint32_t h[EL / 2], l[EL / 2];
+#pragma unroll
+            for (int k = 0; k < EL / 2; ++k) {
+                h[k] = pack_half2(x[2 * k] * up, x[2 * k + 1] * up);
+                if (F::SPLIT) l[k] = rest_half2(x[2 * k] * up, x[2 * k + 1] * up, h[k]);
+            }
+            const int off = (el / 64) * F::SLAB + i * 128 + (el % 64 / 8 ^ (i & 7)) * 16 + el % 8 * 2;
+            if constexpr (F::SPLIT) {
+                *reinterpret_cast<uint2*>(sm.q[0] + off) = make_uint2(h[0], h[1]);
+                *reinterpret_cast<uint2*>(sm.q[1] + off) = make_uint2(l[0], l[1]);
+            } else {
+                *reinterpret_cast<uint4*>(sm.q[qi] + off) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+        }
+    }
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.q_full[qi]);
+    return power;
+}
+
 template <class T, int D>
 __global__ void __launch_bounds__(THREADS, 1)
 kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* joints) {
@@ -185,7 +337,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
         }
         for (int i = 0; i < CONS; ++i) mbar_init(&sm.cons_full[i], 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.q_full[i], 128);
+            mbar_init(&sm.q_full[i], 4);
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.p_full[i], 128);
             mbar_init(&sm.o_full[i], 1);
@@ -293,7 +445,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                 const int inside = token & ((1 << logB) - 1);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    if (!mbar_wait_or_abort(&sm.raw_empty[st], ph ^ 1, abort_flag)) {
+                    if (!mbar_wait_or_abort(&sm.raw_empty[st], ph ^ 1, abort_flag, true)) {
                         sm.abort = 1;
                         ok = false;
                         break;
@@ -413,8 +565,8 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
 #pragma unroll 1
             for (int kv = 0; kv < 2; ++kv) {
                 const int buf = ((int)(2 * g) & 3) + kv;
-                if (!mbar_wait_or_abort(&sm.raw_full[st], ph, abort_flag) ||
-                    !mbar_wait_or_abort(&sm.kv_empty[buf], ((uint32_t)(g >> 1) & 1) ^ 1, abort_flag)) {
+                if (!mbar_wait_or_abort(&sm.raw_full[st], ph, abort_flag, true) ||
+                    !mbar_wait_or_abort(&sm.kv_empty[buf], ((uint32_t)(g >> 1) & 1) ^ 1, abort_flag, true)) {
                     sm.abort = 1;
                     ok = false;
                     break;
@@ -430,28 +582,40 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.cons_full[slot]);
+                } else if (kv && !mbar_wait_or_abort(&sm.cons_full[slot], (uint32_t)(g / CONS) & 1, abort_flag, true)) {
+                    sm.abort = 1;
+                    ok = false;
+                    break;
                 }
                 const uint8_t* src = sm.raw[st];
                 uint8_t* dst = sm.kv[buf];
-                constexpr int CH = D / 16;                   // 16-byte pieces of a row
-                constexpr int STEP = 32 / CH;                // rows a warp takes at a time
-                const int pos = lane % CH;
+                // Eight rows of 64 packed bytes a step.  Lanes 0..3 and 4..7 of a phase take rows r and r ^ 5: their swizzled
+                // 16-byte pieces lie in different halves of a line, and those of f16 in its even and odd pieces.
+                constexpr int DEEP = 4;                      // steps whose loads are in flight
+                const int in8 = (lane >> 3) ^ ((lane >> 2 & 1) * 5), c = lane & 3;
+                const int row0 = dw * 32 + in8;
+                const int from = row0 * D + (D == 128 ? c ^ in8 : c ^ (in8 >> 1 & 3)) * 16;
+                const int to = row0 * 128 + (2 * c ^ in8) * 16;
+                const bool any_zero = kv && __any_sync(0xffffffffu, lane < 2 && sm.cons[slot][dw * 2 + (lane & 1)].w == 0.f);
+#pragma unroll 1
+                for (int x0 = 0; x0 < D / 16; x0 += DEEP) {
+                    uint4 u[DEEP];
 #pragma unroll
-                for (int x = 0; x < 32 / STEP; ++x) {
-                    const int row = dw * 32 + x * STEP + lane / CH;
-                    const int c = D == 128 ? pos ^ (row & 7) : pos ^ ((row >> 1) & 3);
-                    uint4 u = *reinterpret_cast<const uint4*>(src + row * D + pos * 16);
-                    if (kv && sm.scales[slot][(dw * 32 + x * STEP) / rows_piece].y < TINY)
-                        u = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-                    // two 16-byte pieces of f16; neighbouring lanes write other banks' first
-                    const bool swap = D == 128 && (c & 4);
-                    const uint32_t e0 = swap ? u.z : u.x, e1 = swap ? u.w : u.y, e2 = swap ? u.x : u.z, e3 = swap ? u.y : u.w;
-                    uint8_t* to = dst + (c >> 2) * F::SLAB + row * 128;
-                    const int p0 = 2 * (c & 3) + (swap ? 1 : 0);
-                    *reinterpret_cast<uint4*>(to + (p0 ^ (row & 7)) * 16) =
-                        make_uint4(kv8_pair<0>(e0), kv8_pair<2>(e0), kv8_pair<0>(e1), kv8_pair<2>(e1));
-                    *reinterpret_cast<uint4*>(to + ((p0 ^ 1) ^ (row & 7)) * 16) =
-                        make_uint4(kv8_pair<0>(e2), kv8_pair<2>(e2), kv8_pair<0>(e3), kv8_pair<2>(e3));
+                    for (int x = 0; x < DEEP; ++x) {
+                        const int block = (x0 + x) & 3, slab = (x0 + x) >> 2;      // of 8 rows, of 64 columns
+                        u[x] = *reinterpret_cast<const uint4*>(src + (from ^ (slab * 64)) + block * 8 * D);
+                        if (any_zero && sm.cons[slot][dw * 2 + (block >> 1)].w == 0.f)
+                            u[x] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+                    }
+#pragma unroll
+                    for (int x = 0; x < DEEP; ++x) {
+                        const int block = (x0 + x) & 3, slab = (x0 + x) >> 2;
+                        uint8_t* p = dst + slab * F::SLAB + block * 1024;
+                        *reinterpret_cast<uint4*>(p + to) =
+                            make_uint4(kv8_pair<0>(u[x].x), kv8_pair<2>(u[x].x), kv8_pair<0>(u[x].y), kv8_pair<2>(u[x].y));
+                        *reinterpret_cast<uint4*>(p + (to ^ 16)) =
+                            make_uint4(kv8_pair<0>(u[x].z), kv8_pair<2>(u[x].z), kv8_pair<0>(u[x].w), kv8_pair<2>(u[x].w));
+                    }
                 }
                 fence_proxy_async_shared();
                 __syncwarp();
@@ -471,59 +635,23 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
         bool ok = true;
         const float NONE = kv8_none();
         Kv8Joint joint{0, 0, 0, 0};
-        for (; ok && w.left; w.next(a)) {
-            if (w.q.rows - w.tile * ROWS <= 128 * qi) {      // no rows for this group
+        // pieces that have rows for this group
+        auto skip = [&] {
+            while (w.left && w.q.rows - w.tile * ROWS <= 128 * qi) {
                 g += w.run;
-                continue;
+                w.next(a);
             }
-            // ---- the row's query: scaled to 2^14 .. 2^15, into the layout of an MMA operand
+        };
+        skip();
+        int power = 0;
+        if (w.left) power = load_queries<T, D>(a, sm, w, qi, warp & 3, lane);
+        while (w.left) {
             const int r = w.tile * ROWS + qi * 128 + row;
             const bool live = r < w.q.rows;
-            const int token = (live ? r : w.tile * ROWS) / a.G, pos = w.q.q.len - w.q.q.n + token;
+            const int pos = w.q.q.len - w.q.q.n + (live ? r : w.tile * ROWS) / a.G;
             const int row_hi = a.causal ? min(w.q.q.len, pos + 1) : w.q.q.len;
             const int row_lo = a.window ? max(pos - a.window + 1, 0) : 0;
-            float qa;
-            {
-                const T* p = static_cast<const T*>(a.q) + (int64_t)(w.q.q.q0 + token) * a.qt +
-                             (int64_t)(w.head * a.G + (live ? r : 0) % a.G) * a.qh;
-                const bool vec = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
-                float most = 0.f;
-                if (live) {
-#pragma unroll 4
-                    for (int c = 0; c < D / 16; ++c) {
-                        float x[16];
-                        kv8_load16(p + 16 * c, vec, x);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(x[e]));
-                    }
-                }
-                const int e = min(max(141 - (int)(__float_as_uint(most) >> 23), -112), 126);
-                const float up = copysignf(__uint_as_float((uint32_t)(e + 127) << 23), a.scale);
-                qa = fabsf(a.scale) * __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll 2
-                for (int c = 0; c < D / 16; ++c) {
-                    float x[16];
-                    if (live) kv8_load16(p + 16 * c, vec, x);
-                    uint32_t h[8], l[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float u0 = live ? x[2 * i] * up : 0.f, u1 = live ? x[2 * i + 1] * up : 0.f;
-                        h[i] = pack_half2(u0, u1);
-                        l[i] = rest_half2(u0, u1, h[i]);
-                    }
-                    const int off = (c >> 2) * F::SLAB + row * 128, p0 = 2 * (c & 3);
-                    uint8_t* to = sm.q[F::SPLIT ? 0 : qi] + off;
-                    *reinterpret_cast<uint4*>(to + (p0 ^ (row & 7)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
-                    *reinterpret_cast<uint4*>(to + ((p0 + 1) ^ (row & 7)) * 16) = make_uint4(h[4], h[5], h[6], h[7]);
-                    if (F::SPLIT) {
-                        to = sm.q[1] + off;
-                        *reinterpret_cast<uint4*>(to + (p0 ^ (row & 7)) * 16) = make_uint4(l[0], l[1], l[2], l[3]);
-                        *reinterpret_cast<uint4*>(to + ((p0 + 1) ^ (row & 7)) * 16) = make_uint4(l[4], l[5], l[6], l[7]);
-                    }
-                }
-                fence_proxy_async_shared();
-                mbar_arrive(&sm.q_full[qi]);
-            }
+            const float qa = fabsf(a.scale) * __uint_as_float((uint32_t)(127 - power) << 23);
             // tokens [safe_lo, safe_hi) are seen by all of the warp's rows
             const int safe_hi = __reduce_min_sync(0xffffffffu, live ? row_hi : 0x7fffffff);
             const int safe_lo = __reduce_max_sync(0xffffffffu, live ? row_lo : 0);
@@ -532,8 +660,8 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
             for (int i = 0; i < w.run; ++i, ++g) {
                 const int base = (w.span.x + w.at + i) * KT, slot = (int)g & (CONS - 1);
                 // (scores that are there mean that the slot's phase is this tile's)
-                if (!mbar_wait_or_abort(&sm.s_full[qi], s_ph, abort_flag) ||
-                    !mbar_wait_or_abort(&sm.cons_full[slot], (uint32_t)(g / CONS) & 1, abort_flag)) {
+                if (!mbar_wait_or_abort(&sm.s_full[qi], s_ph, abort_flag, true) ||
+                    !mbar_wait_or_abort(&sm.cons_full[slot], (uint32_t)(g / CONS) & 1, abort_flag, true)) {
                     sm.abort = 1;
                     ok = false;
                     break;
@@ -543,32 +671,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                 const float4* cons = sm.cons[slot];
                 const bool inside = base >= safe_lo && base + KT <= safe_hi;
                 const int lo = row_lo - base, hi = row_hi - base;
-                // ---- the largest weight
-                float t = NONE;
-#pragma unroll
-                for (int c = 0; c < KT / 32; ++c) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(s_addr + 32 * c, v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float4 k = cons[2 * c + h];
-                        const float ks = k.x * qa;
-                        if (inside) {
-                            float x = __uint_as_float(v[16 * h]);
-#pragma unroll
-                            for (int e = 1; e < 16; ++e) x = fmaxf(x, __uint_as_float(v[16 * h + e]));
-                            t = fmaxf(t, fmaf(x, ks, k.y));
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const int col = 32 * c + 16 * h + e;
-                                const float x = fmaf(__uint_as_float(v[16 * h + e]), ks, k.y);
-                                t = fmaxf(t, col >= lo && col < hi ? x : NONE);
-                            }
-                        }
-                    }
-                }
+                float t = inside ? tile_top<true>(s_addr, cons, qa, lo, hi) : tile_top<false>(s_addr, cons, qa, lo, hi);
                 const bool raise = t > m + RAISE;
                 if (__any_sync(0xffffffffu, raise)) {
                     const float now = raise ? t - HEAD : m;
@@ -577,66 +680,45 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                     l *= f;
                     if (i > 0) {
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t v[32];
-                            tmem_ld_32x32b_x32(o_addr + 32 * c, v);
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld_32x32b_x16(o_addr + 16 * c, o);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-                            tmem_st_32x32b_x32(o_addr + 32 * c, v);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st_32x32b_x16(o_addr + 16 * c, o);
                         }
                     }
                 }
-                // ---- weights over the scores' columns: 32 tokens' are 16 columns (and 16 of second parts)
                 const float ref = m == NONE ? 0.f : m;
-#pragma unroll
-                for (int c = 0; c < KT / 32; ++c) {
-                    uint32_t v[32], ph[16], pl[16];
-                    tmem_ld_32x32b_x32(s_addr + 32 * c, v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float4 k = cons[2 * c + h];
-                        const float ks = k.x * qa, off = k.y - ref;
-                        const F2 ks2 = f2(ks, ks), off2 = f2(off, off);
-                        F2 sum = f2(0.f, 0.f);
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const float2 x = f2_parts(f2_fma(f2(__uint_as_float(v[16 * h + e]), __uint_as_float(v[16 * h + e + 1])), ks2, off2));
-                            float e0 = exp2_fast(x.x), e1 = exp2_fast(x.y);
-                            if (!inside) {
-                                const int col = 32 * c + 16 * h + e;
-                                e0 = col >= lo && col < hi ? e0 : 0.f;
-                                e1 = col + 1 >= lo && col + 1 < hi ? e1 : 0.f;
-                            }
-                            sum = f2_add(sum, f2(e0, e1));
-                            ph[8 * h + e / 2] = pack_half2(e0, e1);
-                            if (F::TWO) pl[8 * h + e / 2] = rest_half2(e0, e1, ph[8 * h + e / 2]);
-                        }
-                        const float2 both = f2_parts(sum);
-                        l = fmaf(both.x + both.y, k.z, l);
-                    }
-                    tmem_st_32x32b_x16(s_addr + 32 * c, ph);
-                    if (F::TWO) tmem_st_32x32b_x16(s_addr + 32 * c + 16, pl);
-                }
+                l = inside ? tile_weights<F::TWO, true>(s_addr, cons, qa, ref, l, lo, hi)
+                           : tile_weights<F::TWO, false>(s_addr, cons, qa, ref, l, lo, hi);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&sm.p_full[qi]);
             }
             if (!ok) break;
-            // ---- the row's result, or its part of one
-            if (!mbar_wait_or_abort(&sm.o_full[qi], o_ph, abort_flag)) {
+            // ---- where the row's result goes, or its part of one; the next rows' queries meanwhile
+            const bool whole = w.run == w.span.y;
+            int64_t at_lse = 0;
+            T* out = static_cast<T*>(a.out) + kv8_out_row(a, w.q.q, w.head, live ? r : 0, &at_lse);
+            float* part = parts + ((size_t)cta * 2 + (w.at == 0 ? 1 : 0)) * kv8_part_floats(ROWS, D);
+            if (!whole && w.at == 0) {
+                // the rows' other pieces: as many CTAs as the rest of their tiles reaches into
+                const long long from = cut.begin(cta + 1) - w.run;
+                joint = Kv8Joint{w.s, w.head, w.tile, cut.of(from + w.span.y - 1) - cta + 1};
+            }
+            w.next(a);
+            skip();
+            if (w.left) power = load_queries<T, D>(a, sm, w, qi, warp & 3, lane);
+            if (!mbar_wait_or_abort(&sm.o_full[qi], o_ph, abort_flag, true)) {
                 sm.abort = 1;
                 ok = false;
                 break;
             }
             o_ph ^= 1;
             tc_fence_after();
-            const bool whole = w.run == w.span.y;
-            int64_t at_lse = 0;
-            T* out = static_cast<T*>(a.out) + kv8_out_row(a, w.q.q, w.head, live ? r : 0, &at_lse);
             const bool vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-            float* part = parts + ((size_t)cta * 2 + (w.at == 0 ? 1 : 0)) * kv8_part_floats(ROWS, D);
             const int pr = qi * 128 + row;
             const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
@@ -658,11 +740,6 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
             }
             if (live && whole && a.lse) a.lse[at_lse] = kv8_lse(m, l);
             if (live && !whole) part[pr] = m, part[ROWS + pr] = l;
-            if (!whole && w.at == 0) {
-                // the rows' other pieces: as many CTAs as the rest of their tiles reaches into
-                const long long from = cut.begin(cta + 1) - w.run;
-                joint = Kv8Joint{w.s, w.head, w.tile, cut.of(from + w.span.y - 1) - cta + 1};
-            }
             tc_fence_before();
         }
         if (warp == 4 && lane == 0) joints[cta] = ok ? joint : Kv8Joint{0, 0, 0, 0};
