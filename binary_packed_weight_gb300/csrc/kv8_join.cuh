@@ -50,6 +50,10 @@ __device__ __forceinline__ uint32_t rest_half2(float a, float b, uint32_t h) {
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // One of the barrier's arrivals, when this thread's copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -58,8 +62,8 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 __device__ __forceinline__ float kv8_none() { return __int_as_float(0xff800000); }
 
 // Where row r of a sequence's head goes in out; its place in lse.
-__device__ __forceinline__ int64_t kv8_out_row(const Kv8Attention& a, const Kv8Seq& q, int head, int r, int64_t* lse) {
-    const int token = q.q0 + r / a.G, h = head * a.G + r % a.G;
+__device__ __forceinline__ int64_t kv8_out_row(const Kv8Attention& a, int q0, int head, int r, int64_t* lse) {
+    const int token = q0 + r / a.G, h = head * a.G + r % a.G;
     *lse = (int64_t)token * a.c.H * a.G + h;
     return token * a.ot + h * a.oh;
 }
@@ -103,7 +107,7 @@ kv8_join_kernel(const __grid_constant__ Kv8Attention a, const float* parts, cons
             for (int c = 0; c < PER; ++c) o[c] = fmaf(p[2 * RM + r * D + lane + 32 * c], f, o[c]);
         }
         int64_t at_lse;
-        T* dst = static_cast<T*>(a.out) + kv8_out_row(a, q, j.head, j.tile * RM + r, &at_lse);
+        T* dst = static_cast<T*>(a.out) + kv8_out_row(a, q.q0, j.head, j.tile * RM + r, &at_lse);
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
         for (int c = 0; c < PER; ++c) dst[lane + 32 * c] = kv8_round<T>(o[c] * inv);

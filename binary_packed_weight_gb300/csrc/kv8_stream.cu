@@ -470,7 +470,7 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
             }
             if (whole) {
                 int64_t at_lse;
-                T* dst = static_cast<T*>(a.out) + kv8_out_row(a, w.q, head, tile * RM + r, &at_lse) + col;
+                T* dst = static_cast<T*>(a.out) + kv8_out_row(a, w.q.q0, head, tile * RM + r, &at_lse) + col;
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 dst[0] = kv8_round<T>(o.x * inv);
                 dst[1] = kv8_round<T>(o.y * inv);

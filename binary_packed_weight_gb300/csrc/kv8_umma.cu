@@ -46,6 +46,16 @@ struct Form {
     static constexpr int TILE = SLAB * (D / 64);             // 128 rows of D f16
 };
 
+// Tiles of one tile of rows in a row: what a CTA's roles work on between two results.  (One warp walks the list and says
+// what is next, so that the others hold no more than this.)
+struct Piece {
+    int s, head, tile, rows;    // rows: of the sequence's head
+    int q0, n, len, first;      // first tile of 128 tokens
+    int run, whole, part;       // tiles; whether they are all of the rows'; else the part that takes the sums
+    int pad;
+};
+constexpr int PIECES = 4;
+
 template <class T, int D>
 struct __align__(1024) Shared {
     uint8_t q[2][Form<T, D>::TILE];                          // by group (f32: by part)
@@ -56,7 +66,9 @@ struct __align__(1024) Shared {
     uint64_t raw_full[Form<T, D>::RAW], raw_empty[Form<T, D>::RAW];
     uint64_t kv_full[BUFS], kv_empty[BUFS], cons_full[CONS];
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2], idle;
-    long long sums[THREADS / 32], rest;
+    Piece pieces[PIECES];                                    // run 0: no more
+    uint64_t piece_full[PIECES], piece_empty[PIECES];
+    long long sums[THREADS / 32];
     uint32_t tmem;
     int seq, head, tile, at;
     volatile int abort;
@@ -85,34 +97,6 @@ __device__ __forceinline__ int2 span_of(const Kv8Attention& a, const Seq& s, int
     return make_int2(first, max((hi + KT - 1) / KT - first, 1));
 }
 
-// A CTA's way through its share: pieces of `run` tiles of one tile of rows.
-template <int ROWS>
-struct Walk {
-    long long left;
-    int s, head, tile, at;      // at: tiles of the current rows that are behind
-    Seq q;
-    int2 span;
-    int run;
-    __device__ __forceinline__ void open(const Kv8Attention& a) {
-        span = span_of<ROWS>(a, q, tile);
-        run = (int)min((long long)(span.y - at), left);
-    }
-    __device__ __forceinline__ void next(const Kv8Attention& a) {
-        left -= run;
-        if (left == 0) return;
-        at = 0;                                              // the piece ended its rows
-        if (++tile == q.tiles) {
-            tile = 0;
-            if (++head == a.c.H) {
-                head = 0;
-                do q = seq_of<ROWS>(a, ++s);
-                while (q.tiles == 0);
-            }
-        }
-        open(a);
-    }
-};
-
 // KV tiles of one head of the warp's sequences s0 + lane (a lane's own; 0 where there is none).
 template <int ROWS>
 __device__ __forceinline__ long long lane_units(const Kv8Attention& a, int s, int end, Seq& q, int lane) {
@@ -121,11 +105,14 @@ __device__ __forceinline__ long long lane_units(const Kv8Attention& a, int s, in
     if (s < end) q = seq_of<ROWS>(a, s);
     const bool many = q.tiles > 4;
     if (!many)
+#pragma unroll 1
         for (int t = 0; t < q.tiles; ++t) u += span_of<ROWS>(a, q, t).y;
+#pragma unroll 1
     for (uint32_t rest = __ballot_sync(0xffffffffu, many); rest; rest &= rest - 1) {
         const int owner = __ffs(rest) - 1;
         const Seq o = seq_of<ROWS>(a, __shfl_sync(0xffffffffu, s, owner));
         long long sum = 0;
+#pragma unroll 1
         for (int t = lane; t < o.tiles; t += 32) sum += span_of<ROWS>(a, o, t).y;
 #pragma unroll
         for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -180,9 +167,8 @@ __device__ __forceinline__ float max16(const uint32_t* v) {
 // Scores are read from tensor memory twice (64 columns take 50 cycles) rather than held: the loops stay short, which
 // the instruction caches of warps in four different roles ask for.
 
-// The largest exponent of a row's 128 weights.  ALL: the row sees all tokens, else those of columns lo .. hi-1.
-template <bool ALL>
-__device__ __forceinline__ float tile_top(uint32_t s_addr, const float4* cons, float qa, int lo, int hi) {
+// The largest exponent of a row's 128 weights, all of them seen.
+__device__ __forceinline__ float tile_top(uint32_t s_addr, const float4* cons, float qa) {
     float t = kv8_none();
 #pragma unroll 1
     for (int c = 0; c < KT; c += 64) {
@@ -193,27 +179,31 @@ __device__ __forceinline__ float tile_top(uint32_t s_addr, const float4* cons, f
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
             const float4 k = cons[c / 16 + h];
-            const float ks = k.x * qa;
-            uint32_t* x = &v[h >> 1][16 * (h & 1)];
-            if (ALL) {
-                t = fmaxf(t, fmaf(max16(x), ks, k.y));
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int col = c + 16 * h + e;
-                    t = fmaxf(t, col >= lo && col < hi ? fmaf(__uint_as_float(x[e]), ks, k.y) : kv8_none());
-                }
-            }
+            t = fmaxf(t, fmaf(max16(&v[h >> 1][16 * (h & 1)]), k.x * qa, k.y));
         }
     }
     return t;
 }
 
+// Weights of 2 N tokens relative to a reference: f16 pairs (and what those leave), added to sum.
+template <bool TWO, int N>
+__device__ __forceinline__ F2 weights_of(const uint32_t* v, F2 ks, F2 off, uint32_t* ph, uint32_t* pl) {
+    F2 sum = f2(0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const float2 x = f2_parts(f2_fma(f2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), ks, off));
+        const float e0 = exp2_fast(x.x), e1 = exp2_fast(x.y);
+        sum = f2_add(sum, f2(e0, e1));
+        ph[e] = pack_half2(e0, e1);
+        if (TWO) pl[e] = rest_half2(e0, e1, ph[e]);
+    }
+    return sum;
+}
+
 // The row's weights relative to ref, in place of its scores: 32 tokens' are 16 columns (and 16 of second
 // parts).  Returns l with their sum.
-template <bool TWO, bool ALL>
-__device__ __forceinline__ float tile_weights(uint32_t s_addr, const float4* cons, float qa, float ref, float l, int lo,
-                                              int hi) {
+template <bool TWO>
+__device__ __forceinline__ float tile_weights(uint32_t s_addr, const float4* cons, float qa, float ref, float l) {
 #pragma unroll 1
     for (int c = 0; c < KT; c += 64) {
         uint32_t v[2][32];
@@ -227,23 +217,7 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, const float4* con
             for (int h = 0; h < 2; ++h) {
                 const float4 k = cons[c / 16 + 2 * g + h];
                 const float ks = k.x * qa, off = k.y - ref;
-                const F2 ks2 = f2(ks, ks), off2 = f2(off, off);
-                F2 sum = f2(0.f, 0.f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t* at = &v[g][16 * h + 2 * e];
-                    const float2 x = f2_parts(f2_fma(f2(__uint_as_float(at[0]), __uint_as_float(at[1])), ks2, off2));
-                    float e0 = exp2_fast(x.x), e1 = exp2_fast(x.y);
-                    if (!ALL) {
-                        const int col = c + 32 * g + 16 * h + 2 * e;
-                        e0 = col >= lo && col < hi ? e0 : 0.f;
-                        e1 = col + 1 >= lo && col + 1 < hi ? e1 : 0.f;
-                    }
-                    sum = f2_add(sum, f2(e0, e1));
-                    ph[8 * h + e] = pack_half2(e0, e1);
-                    if (TWO) pl[8 * h + e] = rest_half2(e0, e1, ph[8 * h + e]);
-                }
-                const float2 both = f2_parts(sum);
+                const float2 both = f2_parts(weights_of<TWO, 8>(&v[g][16 * h], f2(ks, ks), f2(off, off), ph + 8 * h, pl + 8 * h));
                 l = fmaf(both.x + both.y, k.z, l);
             }
             tmem_st_32x32b_x16(s_addr + c + 32 * g, ph);
@@ -253,68 +227,167 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, const float4* con
     return l;
 }
 
-// A warp's 32 rows of queries, scaled by a power of two to 2^14 .. 2^15, into the layout of an MMA operand (the scores of
-// the rows before are there, so nobody reads those any more).  Returns the power of the lane's row.
+// Both for tiles of which the row sees columns lo .. hi-1 alone.  (Scores become exponents in their place first.)
+__device__ __forceinline__ float tile_top_some(uint32_t s_addr, const float4* cons, float qa, int lo, int hi) {
+    float t = kv8_none();
+#pragma unroll 1
+    for (int c = 0; c < KT; c += 16) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(s_addr + c, v);
+        tmem_wait_ld();
+        const float4 k = cons[c / 16];
+        const float ks = k.x * qa;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            v[e] = __float_as_uint(c + e >= lo && c + e < hi ? fmaf(__uint_as_float(v[e]), ks, k.y) : kv8_none());
+        t = fmaxf(t, max16(v));
+        tmem_st_32x32b_x16(s_addr + c, v);
+    }
+    tmem_wait_st();
+    return t;
+}
+template <bool TWO>
+__device__ __forceinline__ float tile_weights_some(uint32_t s_addr, const float4* cons, float ref, float l) {
+#pragma unroll 1
+    for (int c = 0; c < KT; c += 32) {
+        uint32_t v[32], ph[16], pl[16];
+        tmem_ld_32x32b_x32(s_addr + c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float2 both = f2_parts(weights_of<TWO, 8>(v + 16 * h, f2(1.f, 1.f), f2(-ref, -ref), ph + 8 * h, pl + 8 * h));
+            l = fmaf(both.x + both.y, cons[c / 16 + h].z, l);
+        }
+        tmem_st_32x32b_x16(s_addr + c, ph);
+        if (TWO) tmem_st_32x32b_x16(s_addr + c + 16, pl);
+    }
+    return l;
+}
+
+// tile_weights for weights of one part, on the chance that none passes ref by much: whether that held (most tiles
+// raise nothing, and this saves them the pass for the largest).  If not, nothing has changed.
+__device__ __forceinline__ bool tile_weights_if(uint32_t s_addr, const float4* cons, float qa, float ref, float& l) {
+    uint32_t p[KT / 32][16];
+    float most = 0.f, now = l;
+#pragma unroll
+    for (int c = 0; c < KT / 32; ++c) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(s_addr + 32 * c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 k = cons[2 * c + h];
+            const float ks = k.x * qa, off = k.y - ref;
+            const float2 both = f2_parts(weights_of<false, 8>(v + 16 * h, f2(ks, ks), f2(off, off), p[c] + 8 * h, nullptr));
+            const float one = both.x + both.y;
+            most = fmaxf(most, one);                         // (NaN weights are none the other way either)
+            now = fmaf(one, k.z, now);
+        }
+    }
+    if (!__all_sync(0xffffffffu, most <= 0x1p15f && ref != kv8_none())) return false;
+    l = now;
+#pragma unroll
+    for (int c = 0; c < KT / 32; ++c) tmem_st_32x32b_x16(s_addr + 32 * c, p[c]);
+    return true;
+}
+
+// A warp's 32 rows of queries, scaled by a power of two to 2^14 .. 2^15, in the layout of an MMA operand (the scores of
+// the rows before are there, so nobody reads those any more).  Returns the power of the lane's row.  Raw pieces
+// of 8 elements are copied to where their f16 values (f32: first and second parts) go, and converted in place.
+// (Not inlined and in short loops, as whatever runs once a piece: code that the instruction cache does not
+// hold costs more than it does.)
 template <class T, int D>
-__device__ __forceinline__ int load_queries(const Kv8Attention& a, Shared<T, D>& sm, const Walk<Form<T, D>::ROWS>& w, int qi,
+__device__ __forceinline__ int load_queries(const Kv8Attention& a, Shared<T, D>& sm, const Piece& w, int qi,
                                             int warp, int lane) {
     using F = Form<T, D>;
-    constexpr int EL = 16 / (int)sizeof(T), LPR = D / EL, RPP = 32 / LPR;   // a lane's elements, lanes a row, rows a pass
-    constexpr int DEEP = 8;                     // passes whose loads are in flight
-    const int in_row = lane % LPR, el = in_row * EL;
-    int power = 0;
+    constexpr int LPR = D / 8, RPP = 32 / LPR;               // lanes a row, rows a pass
+    const int el = lane % LPR * 8, r0 = w.tile * F::ROWS + qi * 128 + warp * 32;
+    const int i0 = warp * 32 + lane / LPR;                   // of the group
+    uint8_t* const to0 = sm.q[F::SPLIT ? 0 : qi] + (el / 64) * F::SLAB;
+    auto place = [&](int i) { return to0 + i * 128 + (el % 64 / 8 ^ (i & 7)) * 16; };
+    const T* const q = static_cast<const T*>(a.q) + (int64_t)w.q0 * a.qt + (int64_t)w.head * a.G * a.qh + el;
+    auto row_of = [&](int pass) {                            // (rows that are none: the last one, cleared below)
+        const int r = min(r0 + lane / LPR + pass * RPP, w.rows - 1), token = r / a.G;
+        return q + token * a.qt + (r - token * a.G) * a.qh;
+    };
+    if (a.qvec) {
+#pragma unroll 4
+        for (int pass = 0; pass < LPR; ++pass) {
+            const T* p = row_of(pass);
+            uint8_t* to = place(i0 + pass * RPP);
+            cp_async16(to, p);
+            if (F::SPLIT) cp_async16(to + F::TILE, p + 4);
+        }
+    } else {
 #pragma unroll 1
-    for (int p0 = 0; p0 < 32 / RPP; p0 += DEEP) {
-        uint4 raw[DEEP];
+        for (int pass = 0; pass < LPR; ++pass) {
+            const T* p = row_of(pass);
+            uint8_t* to = place(i0 + pass * RPP);
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<T*>(to + (F::SPLIT ? k / 4 * F::TILE + k % 4 * 4 : k * 2)) = p[k];
+        }
+    }
+    cp_async_wait_all();
+    int power = 0;
+#pragma unroll 4
+    for (int pass = 0; pass < LPR; ++pass) {
+        uint8_t* to = place(i0 + pass * RPP);
+        const bool live = r0 + lane / LPR + pass * RPP < w.rows;
+        uint4 raw[F::SPLIT ? 2 : 1];
+        raw[0] = *reinterpret_cast<const uint4*>(to);
+        if constexpr (F::SPLIT) raw[1] = *reinterpret_cast<const uint4*>(to + F::TILE);
+        const T* u = reinterpret_cast<const T*>(raw);
+        float x[8], most = 0.f;
 #pragma unroll
-        for (int d = 0; d < DEEP; ++d) {
-            const int r = w.tile * F::ROWS + qi * 128 + warp * 32 + (p0 + d) * RPP + lane / LPR;
-            const int token = min(r, w.q.rows - 1) / a.G, h = min(r, w.q.rows - 1) - token * a.G;
-            const T* p = static_cast<const T*>(a.q) + (int64_t)(w.q.q.q0 + token) * a.qt + (int64_t)(w.head * a.G + h) * a.qh + el;
-            if (a.qvec) {
-                raw[d] = *reinterpret_cast<const uint4*>(p);
-            } else {
-                T* e = reinterpret_cast<T*>(&raw[d]);
-#pragma unroll
-                for (int k = 0; k < EL; ++k) e[k] = p[k];
-            }
+        for (int k = 0; k < 8; ++k) {
+            x[k] = live ? kv8_wide(u[k]) : 0.f;
+            most = fmaxf(most, fabsf(x[k]));
         }
 #pragma unroll
-        for (int d = 0; d < DEEP; ++d) {
-            const int i = warp * 32 + (p0 + d) * RPP + lane / LPR;          // of the group
-            const bool live = w.tile * F::ROWS + qi * 128 + i < w.q.rows;
-            const T* u = reinterpret_cast<const T*>(&raw[d]);
-            float x[EL], most = 0.f;
+        for (int k = 1; k < LPR; k <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, k));
+        const int e = min(max(141 - (int)(__float_as_uint(most) >> 23), -112), 126);
+        const float up = copysignf(__uint_as_float((uint32_t)(e + 127) << 23), a.scale);
+        const int of = __shfl_sync(0xffffffffu, e, (lane - pass * RPP) * LPR & 31);
+        if (lane / RPP == pass) power = of;
+        uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int k = 0; k < EL; ++k) {
-                x[k] = live ? kv8_wide(u[k]) : 0.f;
-                most = fmaxf(most, fabsf(x[k]));
-            }
-#pragma unroll
-            for (int k = 1; k < LPR; k <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, k));
-            const int e = min(max(141 - (int)(__float_as_uint(most) >> 23), -112), 126);
-            const float up = copysignf(__uint_as_float((uint32_t)(e + 127) << 23), a.scale);
-            const int of = __shfl_sync(0xffffffffu, e, (lane - (p0 + d) * RPP) * LPR & 31);
-            if (lane / RPP == p0 + d) power = of;
-            uint32_t h[EL / 2], l[EL / 2];
-#pragma unroll
-            for (int k = 0; k < EL / 2; ++k) {
-                h[k] = pack_half2(x[2 * k] * up, x[2 * k + 1] * up);
-                if (F::SPLIT) l[k] = rest_half2(x[2 * k] * up, x[2 * k + 1] * up, h[k]);
-            }
-            const int off = (el / 64) * F::SLAB + i * 128 + (el % 64 / 8 ^ (i & 7)) * 16 + el % 8 * 2;
-            if constexpr (F::SPLIT) {
-                *reinterpret_cast<uint2*>(sm.q[0] + off) = make_uint2(h[0], h[1]);
-                *reinterpret_cast<uint2*>(sm.q[1] + off) = make_uint2(l[0], l[1]);
-            } else {
-                *reinterpret_cast<uint4*>(sm.q[qi] + off) = make_uint4(h[0], h[1], h[2], h[3]);
-            }
+        for (int k = 0; k < 4; ++k) {
+            hi[k] = pack_half2(x[2 * k] * up, x[2 * k + 1] * up);
+            if (F::SPLIT) lo[k] = rest_half2(x[2 * k] * up, x[2 * k + 1] * up, hi[k]);
         }
+        *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if constexpr (F::SPLIT) *reinterpret_cast<uint4*>(to + F::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
     fence_proxy_async_shared();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.q_full[qi]);
     return power;
+}
+
+// A row of O times inv to its place in global memory.
+template <class T, int D>
+__device__ __forceinline__ void store_row(uint32_t o_addr, bool live, float inv, T* out) {
+    if (__any_sync(0xffffffffu, reinterpret_cast<uintptr_t>(out) & 15)) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 2) {
+            uint32_t v[2];
+            tmem_ld_32x32b_x2(o_addr + c, v);
+            tmem_wait_ld();
+            if (live) out[c] = kv8_round<T>(__uint_as_float(v[0]) * inv), out[c + 1] = kv8_round<T>(__uint_as_float(v[1]) * inv);
+        }
+        return;
+    }
+#pragma unroll 1
+    for (int c = 0; c < D; c += 16) {
+        uint32_t v[16];
+        float y[16];
+        tmem_ld_32x32b_x16(o_addr + c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(v[e]) * inv;
+        if (live) kv8_store16(out + c, true, y);
+    }
 }
 
 template <class T, int D>
@@ -342,6 +415,10 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
             mbar_init(&sm.p_full[i], 128);
             mbar_init(&sm.o_full[i], 1);
         }
+        for (int i = 0; i < PIECES; ++i) {
+            mbar_init(&sm.piece_full[i], 1);
+            mbar_init(&sm.piece_empty[i], 2 + 4 * F::NQ);
+        }
         mbar_init(&sm.idle, 1);
         sm.abort = 0;
         fence_mbar_init();
@@ -355,6 +432,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
     const int slice_end = min((warp + 1) * per, S);
     long long mine = 0;
     Seq q;
+#pragma unroll 1
     for (int s = warp * per; s < slice_end; s += 32) mine += lane_units<ROWS>(a, s + lane, slice_end, q, lane);
 #pragma unroll
     for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
@@ -374,6 +452,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
     }
     const long long begin = cut.begin(cta);
     if (before <= begin && begin < before + mine) {
+#pragma unroll 1
         for (int s = warp * per; s < slice_end; s += 32) {
             const long long u = lane_units<ROWS>(a, s + lane, slice_end, q, lane);
             const long long incl = warp_scan(u * a.c.H, lane);
@@ -387,6 +466,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
             const long long uh = __shfl_sync(0xffffffffu, u, owner);
             q = seq_of<ROWS>(a, s + owner);
             long long left = in % uh;
+#pragma unroll 1
             for (int t = 0;; t += 32) {
                 const long long c = t + lane < q.tiles ? span_of<ROWS>(a, q, t + lane).y : 0;
                 const long long sum = warp_scan(c, lane);
@@ -416,31 +496,76 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    Walk<ROWS> w;
-    w.left = cut.begin(cta + 1) - begin;
-    const long long units = w.left;
-    w.s = sm.seq;
-    w.head = sm.head;
-    w.tile = sm.tile;
-    w.at = sm.at;
-    w.q = seq_of<ROWS>(a, w.s);
-    w.open(a);
+    const uint32_t units = (uint32_t)(cut.begin(cta + 1) - begin);   // (a CTA's: below 2^31 rows / 128 * 2^23 tiles / CTAs)
     volatile int* abort_flag = &sm.abort;
     const int logB = a.c.logB, rows_piece = min(1 << logB, KT / 2), pieces = KT / rows_piece;
 
-    if (warp == 0) {                                         // ---- packed tiles
+    // a role's next piece, and its leave of it
+    uint32_t pieces_seen = 0;
+    auto next_piece = [&](Piece& w) {
+        const int slot = pieces_seen & (PIECES - 1);
+        if (!mbar_wait_or_abort(&sm.piece_full[slot], pieces_seen / PIECES & 1, abort_flag, true)) {
+            sm.abort = 1;
+            return false;
+        }
+        w = sm.pieces[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.piece_empty[slot]);
+        ++pieces_seen;
+        return w.run > 0;
+    };
+
+    if (warp == 3) {                                         // ---- the list
+        int s = sm.seq, head = sm.head, tile = sm.tile, at = sm.at;
+        uint32_t left = units;
+        Seq q = seq_of<ROWS>(a, s);
+        Kv8Joint joint{0, 0, 0, 0};
+        for (uint32_t i = 0;; ++i) {
+            const int slot = i & (PIECES - 1);
+            if (!mbar_wait_or_abort(&sm.piece_empty[slot], (i / PIECES & 1) ^ 1, abort_flag, true)) {
+                sm.abort = 1;
+                joint.pieces = 0;
+                break;
+            }
+            const int2 span = span_of<ROWS>(a, q, tile);
+            const int run = (int)min((uint32_t)(span.y - at), left);
+            if (lane == 0) {
+                sm.pieces[slot] = Piece{s, head, tile, q.rows, q.q.q0, q.q.n, q.q.len, span.x + at, run, run == span.y,
+                                        at == 0 ? 1 : 0, 0};
+                mbar_arrive(&sm.piece_full[slot]);
+            }
+            if (left == 0) break;
+            if (run < span.y && at == 0)
+                // the rows' other pieces: as many CTAs as the rest of their tiles reaches into
+                joint = Kv8Joint{s, head, tile, cut.of(cut.begin(cta + 1) - run + span.y - 1) - cta + 1};
+            left -= run;
+            if (left) {                                      // so the piece ended its rows
+                at = 0;
+                if (++tile == q.tiles) {
+                    tile = 0;
+                    if (++head == a.c.H) {
+                        head = 0;
+                        do q = seq_of<ROWS>(a, ++s);
+                        while (q.tiles == 0);
+                    }
+                }
+            }
+        }
+        if (lane == 0) joints[cta] = joint;
+    } else if (warp == 0) {                                  // ---- packed tiles
+        Piece w;
         int st = 0;
         uint32_t ph = 0;
-        long long g = 0;
+        uint32_t g = 0;
         bool wrapped = false, ok = true;
         fence_proxy_async_shared();
         asm volatile("fence.proxy.async.global;" ::: "memory");
-        for (; ok && w.left; w.next(a)) {
-            const int from = a.window ? max(w.q.q.len - w.q.q.n - a.window + 1, 0) : 0;
+        while (ok && next_piece(w)) {
+            const int from = a.window ? max(w.len - w.n - a.window + 1, 0) : 0;
             for (int i = 0; ok && i < w.run; ++i, ++g) {
-                const int token = (w.span.x + w.at + i) * KT + lane * rows_piece;
+                const int token = (w.first + i) * KT + lane * rows_piece;
                 int block = -1;
-                if (lane < pieces && token < w.q.q.len && token + rows_piece > from) block = kv8_block(a.c, w.s, token);
+                if (lane < pieces && token < w.len && token + rows_piece > from) block = kv8_block(a.c, w.s, token);
                 const uint32_t here = __ballot_sync(0xffffffffu, block >= 0);
                 const int inside = token & ((1 << logB) - 1);
 #pragma unroll
@@ -474,40 +599,11 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                 if (u < st || wrapped) mbar_wait(&sm.raw_full[u], u < st ? ph : ph ^ 1);
     } else if (warp == 1) {                                  // ---- MMA issuer
         constexpr uint32_t s_idesc = idesc_f16_f32(128, KT), o_idesc = idesc_f16_f32_bmn(128, D);
-        uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0};
-        long long g = 0;
+        const uint64_t q0_desc = sdesc_kmajor_sw128(smem_u32(sm.q[0])), k0_desc = sdesc_kmajor_sw128(smem_u32(sm.kv[0]));
+        const uint64_t v0_desc = sdesc_mnmajor_sw128(smem_u32(sm.kv[0]), F::SLAB, 1024);
+        uint32_t q_ph = 0, p_ph = 0;                         // a bit a group
+        uint32_t g = 0;                                      // tiles
         bool ok = true;
-        auto scores = [&](int qi, int buf) {
-            if (elect_one()) {
-                const uint32_t qb = smem_u32(sm.q[F::SPLIT ? 0 : qi]), kb = smem_u32(sm.kv[buf]);
-#pragma unroll
-                for (int part = 0; part < (F::SPLIT ? 2 : 1); ++part)
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = (k >> 2) * F::SLAB + (k & 3) * 32;
-                        umma_f16_ss(tmem + S_COL + 128 * qi, sdesc_kmajor_sw128(qb + part * F::TILE + off),
-                                    sdesc_kmajor_sw128(kb + off), s_idesc, part || k);
-                    }
-                umma_commit(&sm.s_full[qi]);
-            }
-            __syncwarp();
-        };
-        auto values = [&](int qi, int buf, bool more) {
-            if (elect_one()) {
-                const uint32_t vb = smem_u32(sm.kv[buf]);
-#pragma unroll
-                for (int k = 0; k < KT / 16; ++k)
-#pragma unroll
-                    for (int part = 0; part < (F::TWO ? 2 : 1); ++part)
-                        umma_f16_ts(tmem + O_COL + D * qi, tmem + S_COL + 128 * qi + 32 * (k >> 1) + 16 * part + 8 * (k & 1),
-                                    sdesc_mnmajor_sw128(vb + k * 2048, F::SLAB, 1024), o_idesc, more || k || part);
-            }
-            __syncwarp();
-        };
-        auto done = [&](uint64_t* bar) {
-            if (elect_one()) umma_commit(bar);
-            __syncwarp();
-        };
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             if (ok && !mbar_wait_or_abort(bar, parity, abort_flag, true)) {
                 sm.abort = 1;
@@ -515,44 +611,64 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
             }
             return ok;
         };
-        for (; ok && w.left; w.next(a)) {
-            const int nq = w.q.rows - w.tile * ROWS > 128 ? F::NQ : 1;
-            for (int i = 0; ok && i < w.run; ++i, ++g) {
-                const int kb = (int)(2 * g) & 3, vb = kb + 1;
-                const uint32_t ph = (uint32_t)(g >> 1) & 1;
-                if (i == 0) {
-                    for (int qi = 0; qi < nq && ok; ++qi) {
-                        if (!wait(&sm.q_full[qi], q_ph[qi])) break;
-                        q_ph[qi] ^= 1;
-                        if (qi == 0 && !wait(&sm.kv_full[kb], ph)) break;
+        Piece w;
+        while (ok && next_piece(w)) {
+            const int nq = w.rows - w.tile * ROWS > 128 ? F::NQ : 1;
+            // step i: the values of tile i, and of each group right behind them the scores of tile i + 1
+#pragma unroll 1
+            for (int i = -1; ok && i < w.run; ++i) {
+                const bool more = i + 1 < w.run;
+                const int vb = (2 * g - 1) & 3, kb = 2 * g & 3;              // (g: tile i + 1 of all)
+                const uint32_t v_ph = (g - 1) >> 1 & 1, k_ph = g >> 1 & 1;
+#pragma unroll 1
+                for (int qi = 0; qi < nq; ++qi) {
+                    if (i >= 0) {
+                        if (!wait(&sm.p_full[qi], p_ph >> qi & 1)) break;
+                        p_ph ^= 1 << qi;
+                        if (qi == 0 && !wait(&sm.kv_full[vb], v_ph)) break;
                         tc_fence_after();
-                        scores(qi, kb);
-                    }
-                    if (!ok) break;
-                    done(&sm.kv_empty[kb]);
-                }
-                const int kn = kb ^ 2;
-                const uint32_t phn = (uint32_t)((g + 1) >> 1) & 1;
-                for (int qi = 0; qi < nq && ok; ++qi) {
-                    if (!wait(&sm.p_full[qi], p_ph[qi])) break;
-                    p_ph[qi] ^= 1;
-                    if (qi == 0 && !wait(&sm.kv_full[vb], ph)) break;
-                    tc_fence_after();
-                    values(qi, vb, i > 0);
-                    if (qi == nq - 1) done(&sm.kv_empty[vb]);
-                    if (i + 1 < w.run) {
-                        if (qi == 0 && !wait(&sm.kv_full[kn], phn)) break;
-                        tc_fence_after();
-                        scores(qi, kn);
-                        if (qi == nq - 1) done(&sm.kv_empty[kn]);
+                        if (elect_one()) {
+                            const uint64_t vd = v0_desc + (uint32_t)vb * (F::TILE >> 4);
+                            const uint32_t o = tmem + O_COL + D * qi, pcol = tmem + S_COL + 128 * qi;
+#pragma unroll
+                            for (int k = 0; k < KT / 16; ++k)
+#pragma unroll
+                                for (int part = 0; part < (F::TWO ? 2 : 1); ++part)
+                                    umma_f16_ts(o, pcol + 32 * (k >> 1) + 16 * part + 8 * (k & 1), vd + k * (2048 >> 4),
+                                                o_idesc, k || part ? 1u : (uint32_t)(i > 0));
+                            if (qi == nq - 1) umma_commit(&sm.kv_empty[vb]);
+                            if (!more) umma_commit(&sm.o_full[qi]);
+                        }
+                        __syncwarp();
                     } else {
-                        done(&sm.o_full[qi]);
+                        if (!wait(&sm.q_full[qi], q_ph >> qi & 1)) break;
+                        q_ph ^= 1 << qi;
+                    }
+                    if (more) {
+                        if (qi == 0 && !wait(&sm.kv_full[kb], k_ph)) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t qd = q0_desc + (uint32_t)qi * (F::TILE >> 4), kd = k0_desc + (uint32_t)kb * (F::TILE >> 4);
+                            const uint32_t s = tmem + S_COL + 128 * qi;
+#pragma unroll
+                            for (int part = 0; part < (F::SPLIT ? 2 : 1); ++part)
+#pragma unroll
+                                for (int k = 0; k < D / 16; ++k) {
+                                    const uint32_t off = ((k >> 2) * F::SLAB + (k & 3) * 32) >> 4;
+                                    umma_f16_ss(s, qd + part * (F::TILE >> 4) + off, kd + off, s_idesc, part || k);
+                                }
+                            umma_commit(&sm.s_full[qi]);
+                            if (qi == nq - 1) umma_commit(&sm.kv_empty[kb]);
+                        }
+                        __syncwarp();
                     }
                 }
+                if (more) ++g;
             }
         }
         if (!ok) {                                           // MMAs in flight end before their operands go
-            done(&sm.idle);
+            if (elect_one()) umma_commit(&sm.idle);
+            __syncwarp();
             mbar_wait(&sm.idle, 0);
         }
     } else if (warp >= 12) {                                 // ---- decoders: 32 tokens of a tile each
@@ -560,13 +676,13 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
         int st = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (long long g = 0; ok && g < units; ++g) {
-            const int slot = (int)g & (CONS - 1);
+        for (uint32_t g = 0; ok && g < units; ++g) {
+            const int slot = g & (CONS - 1);
 #pragma unroll 1
             for (int kv = 0; kv < 2; ++kv) {
-                const int buf = ((int)(2 * g) & 3) + kv;
+                const int buf = (2 * g & 3) + kv;
                 if (!mbar_wait_or_abort(&sm.raw_full[st], ph, abort_flag, true) ||
-                    !mbar_wait_or_abort(&sm.kv_empty[buf], ((uint32_t)(g >> 1) & 1) ^ 1, abort_flag, true)) {
+                    !mbar_wait_or_abort(&sm.kv_empty[buf], (g >> 1 & 1) ^ 1, abort_flag, true)) {
                     sm.abort = 1;
                     ok = false;
                     break;
@@ -582,7 +698,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.cons_full[slot]);
-                } else if (kv && !mbar_wait_or_abort(&sm.cons_full[slot], (uint32_t)(g / CONS) & 1, abort_flag, true)) {
+                } else if (kv && !mbar_wait_or_abort(&sm.cons_full[slot], g / CONS & 1, abort_flag, true)) {
                     sm.abort = 1;
                     ok = false;
                     break;
@@ -630,38 +746,63 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
         const int qi = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t s_addr = tmem + S_COL + 128 * qi + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t o_addr = tmem + O_COL + D * qi + ((uint32_t)((warp & 3) * 32) << 16);
-        uint32_t s_ph = 0, o_ph = 0;
-        long long g = 0;
-        bool ok = true;
+        uint32_t s_ph = 0, o_ph = 0, g = 0, skipped = 0;
+        bool ok = true, have = false;
         const float NONE = kv8_none();
-        Kv8Joint joint{0, 0, 0, 0};
-        // pieces that have rows for this group
-        auto skip = [&] {
-            while (w.left && w.q.rows - w.tile * ROWS <= 128 * qi) {
-                g += w.run;
-                w.next(a);
+        // of the piece at hand
+        float m = NONE, l = 0.f;
+        bool whole = false, live = false;
+        T* out = nullptr;
+        float* part = nullptr;
+        int64_t at_lse = 0;
+        while (true) {
+            Piece w;
+            bool more;
+            skipped = 0;
+            while ((more = next_piece(w)) && w.rows - w.tile * ROWS <= 128 * qi) skipped += w.run;   // no rows for this group
+            int power = 0;
+            if (more) power = load_queries<T, D>(a, sm, w, qi, warp & 3, lane);
+            if (have) {
+                // ---- a row's result, or its part of one
+                if (!mbar_wait_or_abort(&sm.o_full[qi], o_ph, abort_flag, true)) {
+                    sm.abort = 1;
+                    break;
+                }
+                o_ph ^= 1;
+                tc_fence_after();
+                const int pr = qi * 128 + row;
+                if (whole) {
+                    store_row<T, D>(o_addr, live, l == 0.f ? 0.f : 1.f / l, out);
+                    if (live && a.lse) a.lse[at_lse] = kv8_lse(m, l);
+                } else {
+                    store_row<float, D>(o_addr, live, 1.f, part + 2 * ROWS + (size_t)pr * D);
+                    if (live) part[pr] = m, part[ROWS + pr] = l;
+                }
+                tc_fence_before();
             }
-        };
-        skip();
-        int power = 0;
-        if (w.left) power = load_queries<T, D>(a, sm, w, qi, warp & 3, lane);
-        while (w.left) {
+            if (!more) break;
+            have = true;
+            g += skipped;
             const int r = w.tile * ROWS + qi * 128 + row;
-            const bool live = r < w.q.rows;
-            const int pos = w.q.q.len - w.q.q.n + (live ? r : w.tile * ROWS) / a.G;
-            const int row_hi = a.causal ? min(w.q.q.len, pos + 1) : w.q.q.len;
+            live = r < w.rows;
+            const int pos = w.len - w.n + (live ? r : w.tile * ROWS) / a.G;
+            const int row_hi = a.causal ? min(w.len, pos + 1) : w.len;
             const int row_lo = a.window ? max(pos - a.window + 1, 0) : 0;
             const float qa = fabsf(a.scale) * __uint_as_float((uint32_t)(127 - power) << 23);
+            whole = w.whole;
+            out = static_cast<T*>(a.out) + kv8_out_row(a, w.q0, w.head, live ? r : 0, &at_lse);
+            part = parts + ((size_t)cta * 2 + w.part) * kv8_part_floats(ROWS, D);
+            m = NONE;
+            l = 0.f;
             // tokens [safe_lo, safe_hi) are seen by all of the warp's rows
             const int safe_hi = __reduce_min_sync(0xffffffffu, live ? row_hi : 0x7fffffff);
             const int safe_lo = __reduce_max_sync(0xffffffffu, live ? row_lo : 0);
 
-            float m = NONE, l = 0.f;
             for (int i = 0; i < w.run; ++i, ++g) {
-                const int base = (w.span.x + w.at + i) * KT, slot = (int)g & (CONS - 1);
+                const int base = (w.first + i) * KT, slot = g & (CONS - 1);
                 // (scores that are there mean that the slot's phase is this tile's)
                 if (!mbar_wait_or_abort(&sm.s_full[qi], s_ph, abort_flag, true) ||
-                    !mbar_wait_or_abort(&sm.cons_full[slot], (uint32_t)(g / CONS) & 1, abort_flag, true)) {
+                    !mbar_wait_or_abort(&sm.cons_full[slot], g / CONS & 1, abort_flag, true)) {
                     sm.abort = 1;
                     ok = false;
                     break;
@@ -671,78 +812,35 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                 const float4* cons = sm.cons[slot];
                 const bool inside = base >= safe_lo && base + KT <= safe_hi;
                 const int lo = row_lo - base, hi = row_hi - base;
-                float t = inside ? tile_top<true>(s_addr, cons, qa, lo, hi) : tile_top<false>(s_addr, cons, qa, lo, hi);
-                const bool raise = t > m + RAISE;
-                if (__any_sync(0xffffffffu, raise)) {
-                    const float now = raise ? t - HEAD : m;
-                    const float f = raise ? exp2_fast(m - now) : 1.f;
-                    m = now;
-                    l *= f;
-                    if (i > 0) {
+                if (F::TWO || i == 0 || !inside || !tile_weights_if(s_addr, cons, qa, m, l)) {
+                    const float t = inside ? tile_top(s_addr, cons, qa) : tile_top_some(s_addr, cons, qa, lo, hi);
+                    const bool raise = t > m + RAISE;
+                    if (__any_sync(0xffffffffu, raise)) {
+                        const float now = raise ? t - HEAD : m;
+                        const float f = raise ? exp2_fast(m - now) : 1.f;
+                        m = now;
+                        l *= f;
+                        if (i > 0) {
 #pragma unroll 1
-                        for (int c = 0; c < D / 16; ++c) {
-                            uint32_t o[16];
-                            tmem_ld_32x32b_x16(o_addr + 16 * c, o);
-                            tmem_wait_ld();
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint32_t o[16];
+                                tmem_ld_32x32b_x16(o_addr + 16 * c, o);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st_32x32b_x16(o_addr + 16 * c, o);
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st_32x32b_x16(o_addr + 16 * c, o);
+                            }
                         }
                     }
+                    const float ref = m == NONE ? 0.f : m;
+                    l = inside ? tile_weights<F::TWO>(s_addr, cons, qa, ref, l) : tile_weights_some<F::TWO>(s_addr, cons, ref, l);
                 }
-                const float ref = m == NONE ? 0.f : m;
-                l = inside ? tile_weights<F::TWO, true>(s_addr, cons, qa, ref, l, lo, hi)
-                           : tile_weights<F::TWO, false>(s_addr, cons, qa, ref, l, lo, hi);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&sm.p_full[qi]);
             }
             if (!ok) break;
-            // ---- where the row's result goes, or its part of one; the next rows' queries meanwhile
-            const bool whole = w.run == w.span.y;
-            int64_t at_lse = 0;
-            T* out = static_cast<T*>(a.out) + kv8_out_row(a, w.q.q, w.head, live ? r : 0, &at_lse);
-            float* part = parts + ((size_t)cta * 2 + (w.at == 0 ? 1 : 0)) * kv8_part_floats(ROWS, D);
-            if (!whole && w.at == 0) {
-                // the rows' other pieces: as many CTAs as the rest of their tiles reaches into
-                const long long from = cut.begin(cta + 1) - w.run;
-                joint = Kv8Joint{w.s, w.head, w.tile, cut.of(from + w.span.y - 1) - cta + 1};
-            }
-            w.next(a);
-            skip();
-            if (w.left) power = load_queries<T, D>(a, sm, w, qi, warp & 3, lane);
-            if (!mbar_wait_or_abort(&sm.o_full[qi], o_ph, abort_flag, true)) {
-                sm.abort = 1;
-                ok = false;
-                break;
-            }
-            o_ph ^= 1;
-            tc_fence_after();
-            const bool vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-            const int pr = qi * 128 + row;
-            const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(o_addr + 32 * c, v);
-                tmem_wait_ld();
-                float y[2][16];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) y[e >> 4][e & 15] = __uint_as_float(v[e]) * inv;
-                if (live && whole) {
-                    kv8_store16(out + 32 * c, vec, y[0]);
-                    kv8_store16(out + 32 * c + 16, vec, y[1]);
-                } else if (live) {
-                    float* to = part + 2 * ROWS + (size_t)pr * D + 32 * c;
-                    kv8_store16(to, true, y[0]);
-                    kv8_store16(to + 16, true, y[1]);
-                }
-            }
-            if (live && whole && a.lse) a.lse[at_lse] = kv8_lse(m, l);
-            if (live && !whole) part[pr] = m, part[ROWS + pr] = l;
-            tc_fence_before();
         }
-        if (warp == 4 && lane == 0) joints[cta] = ok ? joint : Kv8Joint{0, 0, 0, 0};
     }
     tc_fence_before();
     __syncthreads();
