@@ -11,7 +11,7 @@ struct Kv8Cut {
     long long base, more;
     int ctas;
     __device__ __forceinline__ Kv8Cut(long long total, int grid, int least) {
-        const long long useful = (total + least - 1) / least;
+        const long long useful = total < least ? total > 0 : total / least;
         ctas = useful < grid ? (int)useful : grid;
         base = ctas ? total / ctas : 0;
         more = ctas ? total - base * ctas : 0;

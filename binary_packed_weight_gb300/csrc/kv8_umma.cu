@@ -18,6 +18,7 @@
 // The MMAs are issued in the order Q K^T, P V, Q K^T .. of a group, and execute in that order: P V
 // reads P before the next scores take its place, and scores that are there mean that the
 // last P V is done, so the group may rescale O.
+#include <cstddef>
 #include <type_traits>
 
 #include "kv8_join.cuh"
@@ -31,9 +32,13 @@ constexpr int THREADS = 512;
 constexpr int DECODERS = 4;     // warps
 constexpr int BUFS = 4;         // decoded tiles: keys and values in turn
 constexpr int CONS = 4;         // tiles whose scales are at hand
-constexpr int LEAST = 2;        // tiles of a CTA, where there are fewer than all CTAs take
+// The cut counts a tile of rows as its tiles of tokens and so many more, which is about what queries, masked tiles and
+// the result cost.  A cut through those is one at their start.
+constexpr int EXTRA = 4;
+constexpr int LEAST = EXTRA + 1;                             // units of a CTA: no two cuts through the same EXTRA
 constexpr float HEAD = 6.f, RAISE = 14.f;                    // as kv8_stream.cu
 constexpr float TINY = 0x1p-103f;
+constexpr uint32_t S_COL = 0, O_COL = 256;                  // columns of tensor memory: scores, sums
 
 template <class T, int D>
 struct Form {
@@ -97,7 +102,7 @@ __device__ __forceinline__ int2 span_of(const Kv8Attention& a, const Seq& s, int
     return make_int2(first, max((hi + KT - 1) / KT - first, 1));
 }
 
-// KV tiles of one head of the warp's sequences s0 + lane (a lane's own; 0 where there is none).
+// Units of one head of a lane's own sequence s (0 where there is none).
 template <int ROWS>
 __device__ __forceinline__ long long lane_units(const Kv8Attention& a, int s, int end, Seq& q, int lane) {
     long long u = 0;
@@ -106,14 +111,14 @@ __device__ __forceinline__ long long lane_units(const Kv8Attention& a, int s, in
     const bool many = q.tiles > 4;
     if (!many)
 #pragma unroll 1
-        for (int t = 0; t < q.tiles; ++t) u += span_of<ROWS>(a, q, t).y;
+        for (int t = 0; t < q.tiles; ++t) u += span_of<ROWS>(a, q, t).y + EXTRA;
 #pragma unroll 1
     for (uint32_t rest = __ballot_sync(0xffffffffu, many); rest; rest &= rest - 1) {
         const int owner = __ffs(rest) - 1;
         const Seq o = seq_of<ROWS>(a, __shfl_sync(0xffffffffu, s, owner));
         long long sum = 0;
 #pragma unroll 1
-        for (int t = lane; t < o.tiles; t += 32) sum += span_of<ROWS>(a, o, t).y;
+        for (int t = lane; t < o.tiles; t += 32) sum += span_of<ROWS>(a, o, t).y + EXTRA;
 #pragma unroll
         for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         if (lane == owner) u = sum;
@@ -230,18 +235,23 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, const float4* con
 // Both for tiles of which the row sees columns lo .. hi-1 alone.  (Scores become exponents in their place first.)
 __device__ __forceinline__ float tile_top_some(uint32_t s_addr, const float4* cons, float qa, int lo, int hi) {
     float t = kv8_none();
+    lo = max(lo, 0);
 #pragma unroll 1
-    for (int c = 0; c < KT; c += 16) {
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(s_addr + c, v);
+    for (int c = 0; c < KT; c += 32) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(s_addr + c, v);
         tmem_wait_ld();
-        const float4 k = cons[c / 16];
-        const float ks = k.x * qa;
+        const uint32_t from = lo - c, count = max(hi - lo, 0);       // column e is seen: e - from < count
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-            v[e] = __float_as_uint(c + e >= lo && c + e < hi ? fmaf(__uint_as_float(v[e]), ks, k.y) : kv8_none());
-        t = fmaxf(t, max16(v));
-        tmem_st_32x32b_x16(s_addr + c, v);
+        for (int h = 0; h < 2; ++h) {
+            const float4 k = cons[c / 16 + h];
+            const float ks = k.x * qa;
+#pragma unroll
+            for (int e = 16 * h; e < 16 * h + 16; ++e)
+                v[e] = __float_as_uint(e - from < count ? fmaf(__uint_as_float(v[e]), ks, k.y) : kv8_none());
+            t = fmaxf(t, max16(v + 16 * h));
+        }
+        tmem_st_32x32b_x32(s_addr + c, v);
     }
     tmem_wait_st();
     return t;
@@ -330,34 +340,51 @@ __device__ __forceinline__ int load_queries(const Kv8Attention& a, Shared<T, D>&
     }
     cp_async_wait_all();
     int power = 0;
-#pragma unroll 4
-    for (int pass = 0; pass < LPR; ++pass) {
-        uint8_t* to = place(i0 + pass * RPP);
-        const bool live = r0 + lane / LPR + pass * RPP < w.rows;
-        uint4 raw[F::SPLIT ? 2 : 1];
-        raw[0] = *reinterpret_cast<const uint4*>(to);
-        if constexpr (F::SPLIT) raw[1] = *reinterpret_cast<const uint4*>(to + F::TILE);
-        const T* u = reinterpret_cast<const T*>(raw);
-        float x[8], most = 0.f;
+    constexpr int DEEP = 4;                                  // passes side by side
+#pragma unroll 1
+    for (int p0 = 0; p0 < LPR; p0 += DEEP) {
+        uint4 raw[DEEP][F::SPLIT ? 2 : 1];
+        float most[DEEP];
+        int e[DEEP];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            x[k] = live ? kv8_wide(u[k]) : 0.f;
-            most = fmaxf(most, fabsf(x[k]));
+        for (int d = 0; d < DEEP; ++d) {
+            uint8_t* to = place(i0 + (p0 + d) * RPP);
+            const bool live = r0 + lane / LPR + (p0 + d) * RPP < w.rows;
+            raw[d][0] = live ? *reinterpret_cast<const uint4*>(to) : make_uint4(0, 0, 0, 0);
+            if constexpr (F::SPLIT) raw[d][1] = live ? *reinterpret_cast<const uint4*>(to + F::TILE) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int k = 1; k < LPR; k <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, k));
-        const int e = min(max(141 - (int)(__float_as_uint(most) >> 23), -112), 126);
-        const float up = copysignf(__uint_as_float((uint32_t)(e + 127) << 23), a.scale);
-        const int of = __shfl_sync(0xffffffffu, e, (lane - pass * RPP) * LPR & 31);
-        if (lane / RPP == pass) power = of;
-        uint32_t hi[4], lo[4];
+        for (int d = 0; d < DEEP; ++d) {
+            const T* u = reinterpret_cast<const T*>(raw[d]);
+            most[d] = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            hi[k] = pack_half2(x[2 * k] * up, x[2 * k + 1] * up);
-            if (F::SPLIT) lo[k] = rest_half2(x[2 * k] * up, x[2 * k + 1] * up, hi[k]);
+            for (int k = 0; k < 8; ++k) most[d] = fmaxf(most[d], fabsf(kv8_wide(u[k])));
         }
-        *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if constexpr (F::SPLIT) *reinterpret_cast<uint4*>(to + F::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+        for (int k = 1; k < LPR; k <<= 1)
+#pragma unroll
+            for (int d = 0; d < DEEP; ++d) most[d] = fmaxf(most[d], __shfl_xor_sync(0xffffffffu, most[d], k));
+#pragma unroll
+        for (int d = 0; d < DEEP; ++d) {
+            e[d] = min(max(141 - (int)(__float_as_uint(most[d]) >> 23), -112), 126);
+            const int of = __shfl_sync(0xffffffffu, e[d], (lane - (p0 + d) * RPP) * LPR & 31);
+            if (lane / RPP == p0 + d) power = of;
+        }
+#pragma unroll
+        for (int d = 0; d < DEEP; ++d) {
+            const T* u = reinterpret_cast<const T*>(raw[d]);
+            const float up = copysignf(__uint_as_float((uint32_t)(e[d] + 127) << 23), a.scale);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float x0 = kv8_wide(u[2 * k]) * up, x1 = kv8_wide(u[2 * k + 1]) * up;
+                hi[k] = pack_half2(x0, x1);
+                if (F::SPLIT) lo[k] = rest_half2(x0, x1, hi[k]);
+            }
+            uint8_t* to = place(i0 + (p0 + d) * RPP);
+            *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if constexpr (F::SPLIT) *reinterpret_cast<uint4*>(to + F::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
     }
     fence_proxy_async_shared();
     __syncwarp();
@@ -390,12 +417,38 @@ __device__ __forceinline__ void store_row(uint32_t o_addr, bool live, float inv,
     }
 }
 
+// The MMAs of one group: scores S = Q K^T from decoded tile KB, and values O (+)= P V with VB = KB + 1.  Buffers and
+// groups are constants, and so all operands of the instructions but the first's flag: computed ones would be
+// moved into uniform registers one by one (120 cycles an MMA).  All of tensor memory is this CTA's: it begins at 0.
+template <class F, int D, int QI, int KB>
+__device__ __forceinline__ void issue_scores(uint32_t q, uint32_t kv) {
+    constexpr uint32_t idesc = idesc_f16_f32(128, KT);
+#pragma unroll
+    for (int part = 0; part < (F::SPLIT ? 2 : 1); ++part)
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k >> 2) * F::SLAB + (k & 3) * 32;
+            umma_f16_ss(S_COL + 128 * QI, sdesc_kmajor_sw128(q + (QI + part) * F::TILE + off),
+                        sdesc_kmajor_sw128(kv + KB * F::TILE + off), idesc, part || k);
+        }
+}
+template <class F, int D, int QI, int KB>
+__device__ __forceinline__ void issue_values(uint32_t kv, bool add) {
+    constexpr uint32_t idesc = idesc_f16_f32_bmn(128, D);
+#pragma unroll
+    for (int k = 0; k < KT / 16; ++k)
+#pragma unroll
+        for (int part = 0; part < (F::TWO ? 2 : 1); ++part)
+            umma_f16_ts(O_COL + D * QI, S_COL + 128 * QI + 32 * (k >> 1) + 16 * part + 8 * (k & 1),
+                        sdesc_mnmajor_sw128(kv + (KB + 1) * F::TILE + k * 2048, F::SLAB, 1024), idesc,
+                        k || part ? 1u : (uint32_t)add);
+}
+
 template <class T, int D>
 __global__ void __launch_bounds__(THREADS, 1)
 kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* joints) {
     using F = Form<T, D>;
     constexpr int ROWS = F::ROWS;
-    constexpr uint32_t S_COL = 0, O_COL = 256;
     extern __shared__ __align__(1024) uint8_t raw_shared[];
     Shared<T, D>& sm = *reinterpret_cast<Shared<T, D>*>(raw_shared);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -412,12 +465,12 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.q_full[i], 4);
             mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i], 128);
+            mbar_init(&sm.p_full[i], 4);
             mbar_init(&sm.o_full[i], 1);
         }
         for (int i = 0; i < PIECES; ++i) {
             mbar_init(&sm.piece_full[i], 1);
-            mbar_init(&sm.piece_empty[i], 2 + 4 * F::NQ);
+            mbar_init(&sm.piece_empty[i], 2 + DECODERS + 4 * F::NQ);
         }
         mbar_init(&sm.idle, 1);
         sm.abort = 0;
@@ -468,7 +521,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
             long long left = in % uh;
 #pragma unroll 1
             for (int t = 0;; t += 32) {
-                const long long c = t + lane < q.tiles ? span_of<ROWS>(a, q, t + lane).y : 0;
+                const long long c = t + lane < q.tiles ? span_of<ROWS>(a, q, t + lane).y + EXTRA : 0;
                 const long long sum = warp_scan(c, lane);
                 const uint32_t there = __ballot_sync(0xffffffffu, sum > left);
                 if (!there) {
@@ -495,8 +548,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sm.tmem;
-    const uint32_t units = (uint32_t)(cut.begin(cta + 1) - begin);   // (a CTA's: below 2^31 rows / 128 * 2^23 tiles / CTAs)
+    const uint32_t tmem = 0;
     volatile int* abort_flag = &sm.abort;
     const int logB = a.c.logB, rows_piece = min(1 << logB, KT / 2), pieces = KT / rows_piece;
 
@@ -516,8 +568,10 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
     };
 
     if (warp == 3) {                                         // ---- the list
-        int s = sm.seq, head = sm.head, tile = sm.tile, at = sm.at;
-        uint32_t left = units;
+        int s = sm.seq, head = sm.head, tile = sm.tile, at = sm.at;      // at: units of the rows that are behind
+        long long pos = begin;
+        const long long end = cut.begin(cta + 1);
+        if (at <= EXTRA) pos -= at, at = 0;
         Seq q = seq_of<ROWS>(a, s);
         Kv8Joint joint{0, 0, 0, 0};
         for (uint32_t i = 0;; ++i) {
@@ -528,26 +582,25 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                 break;
             }
             const int2 span = span_of<ROWS>(a, q, tile);
-            const int run = (int)min((uint32_t)(span.y - at), left);
+            const int take = (int)min((long long)(span.y + EXTRA - at), end - pos);
+            const int behind = max(at - EXTRA, 0), run = max(take - (at ? 0 : EXTRA), 0);
             if (lane == 0) {
-                sm.pieces[slot] = Piece{s, head, tile, q.rows, q.q.q0, q.q.n, q.q.len, span.x + at, run, run == span.y,
+                sm.pieces[slot] = Piece{s, head, tile, q.rows, q.q.q0, q.q.n, q.q.len, span.x + behind, run, run == span.y,
                                         at == 0 ? 1 : 0, 0};
                 mbar_arrive(&sm.piece_full[slot]);
             }
-            if (left == 0) break;
+            if (run == 0) break;
             if (run < span.y && at == 0)
                 // the rows' other pieces: as many CTAs as the rest of their tiles reaches into
-                joint = Kv8Joint{s, head, tile, cut.of(cut.begin(cta + 1) - run + span.y - 1) - cta + 1};
-            left -= run;
-            if (left) {                                      // so the piece ended its rows
-                at = 0;
-                if (++tile == q.tiles) {
-                    tile = 0;
-                    if (++head == a.c.H) {
-                        head = 0;
-                        do q = seq_of<ROWS>(a, ++s);
-                        while (q.tiles == 0);
-                    }
+                joint = Kv8Joint{s, head, tile, cut.of(pos + EXTRA + span.y - 1) - cta + 1};
+            pos += take;
+            at = 0;                                          // (unless nothing is left, the piece ended its rows)
+            if (pos < end && ++tile == q.tiles) {
+                tile = 0;
+                if (++head == a.c.H) {
+                    head = 0;
+                    do q = seq_of<ROWS>(a, ++s);
+                    while (q.tiles == 0);
                 }
             }
         }
@@ -598,9 +651,9 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
             for (int u = 0; u < F::RAW; ++u)
                 if (u < st || wrapped) mbar_wait(&sm.raw_full[u], u < st ? ph : ph ^ 1);
     } else if (warp == 1) {                                  // ---- MMA issuer
-        constexpr uint32_t s_idesc = idesc_f16_f32(128, KT), o_idesc = idesc_f16_f32_bmn(128, D);
-        const uint64_t q0_desc = sdesc_kmajor_sw128(smem_u32(sm.q[0])), k0_desc = sdesc_kmajor_sw128(smem_u32(sm.kv[0]));
-        const uint64_t v0_desc = sdesc_mnmajor_sw128(smem_u32(sm.kv[0]), F::SLAB, 1024);
+        using Sh = Shared<T, D>;
+        static_assert(offsetof(Sh, q) == 0 && offsetof(Sh, kv) == 2 * F::TILE, "operands lead");
+        const uint32_t q_at = smem_u32(raw_shared), kv_at = q_at + 2 * F::TILE;
         uint32_t q_ph = 0, p_ph = 0;                         // a bit a group
         uint32_t g = 0;                                      // tiles
         bool ok = true;
@@ -628,14 +681,10 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                         if (qi == 0 && !wait(&sm.kv_full[vb], v_ph)) break;
                         tc_fence_after();
                         if (elect_one()) {
-                            const uint64_t vd = v0_desc + (uint32_t)vb * (F::TILE >> 4);
-                            const uint32_t o = tmem + O_COL + D * qi, pcol = tmem + S_COL + 128 * qi;
-#pragma unroll
-                            for (int k = 0; k < KT / 16; ++k)
-#pragma unroll
-                                for (int part = 0; part < (F::TWO ? 2 : 1); ++part)
-                                    umma_f16_ts(o, pcol + 32 * (k >> 1) + 16 * part + 8 * (k & 1), vd + k * (2048 >> 4),
-                                                o_idesc, k || part ? 1u : (uint32_t)(i > 0));
+                            if (vb == 1)
+                                qi ? issue_values<F, D, F::NQ - 1, 0>(kv_at, i > 0) : issue_values<F, D, 0, 0>(kv_at, i > 0);
+                            else
+                                qi ? issue_values<F, D, F::NQ - 1, 2>(kv_at, i > 0) : issue_values<F, D, 0, 2>(kv_at, i > 0);
                             if (qi == nq - 1) umma_commit(&sm.kv_empty[vb]);
                             if (!more) umma_commit(&sm.o_full[qi]);
                         }
@@ -648,15 +697,10 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                         if (qi == 0 && !wait(&sm.kv_full[kb], k_ph)) break;
                         tc_fence_after();
                         if (elect_one()) {
-                            const uint64_t qd = q0_desc + (uint32_t)qi * (F::TILE >> 4), kd = k0_desc + (uint32_t)kb * (F::TILE >> 4);
-                            const uint32_t s = tmem + S_COL + 128 * qi;
-#pragma unroll
-                            for (int part = 0; part < (F::SPLIT ? 2 : 1); ++part)
-#pragma unroll
-                                for (int k = 0; k < D / 16; ++k) {
-                                    const uint32_t off = ((k >> 2) * F::SLAB + (k & 3) * 32) >> 4;
-                                    umma_f16_ss(s, qd + part * (F::TILE >> 4) + off, kd + off, s_idesc, part || k);
-                                }
+                            if (kb == 0)
+                                qi ? issue_scores<F, D, F::NQ - 1, 0>(q_at, kv_at) : issue_scores<F, D, 0, 0>(q_at, kv_at);
+                            else
+                                qi ? issue_scores<F, D, F::NQ - 1, 2>(q_at, kv_at) : issue_scores<F, D, 0, 2>(q_at, kv_at);
                             umma_commit(&sm.s_full[qi]);
                             if (qi == nq - 1) umma_commit(&sm.kv_empty[kb]);
                         }
@@ -676,7 +720,10 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
         int st = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (uint32_t g = 0; ok && g < units; ++g) {
+        uint32_t g = 0;
+        Piece w;
+        while (ok && next_piece(w))
+        for (int i = 0; ok && i < w.run; ++i, ++g) {
             const int slot = g & (CONS - 1);
 #pragma unroll 1
             for (int kv = 0; kv < 2; ++kv) {
@@ -837,7 +884,8 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&sm.p_full[qi]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_full[qi]);
             }
             if (!ok) break;
         }
