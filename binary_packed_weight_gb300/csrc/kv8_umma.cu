@@ -18,7 +18,6 @@
 // The MMAs are issued in the order Q K^T, P V, Q K^T .. of a group, and execute in that order: P V
 // reads P before the next scores take its place, and scores that are there mean that the
 // last P V is done, so the group may rescale O.
-#include <cstddef>
 #include <type_traits>
 
 #include "kv8_join.cuh"
@@ -274,33 +273,6 @@ __device__ __forceinline__ float tile_weights_some(uint32_t s_addr, const float4
     return l;
 }
 
-// tile_weights for weights of one part, on the chance that none passes ref by much: whether that held (most tiles
-// raise nothing, and this saves them the pass for the largest).  If not, nothing has changed.
-__device__ __forceinline__ bool tile_weights_if(uint32_t s_addr, const float4* cons, float qa, float ref, float& l) {
-    uint32_t p[KT / 32][16];
-    float most = 0.f, now = l;
-#pragma unroll
-    for (int c = 0; c < KT / 32; ++c) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(s_addr + 32 * c, v);
-        tmem_wait_ld();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float4 k = cons[2 * c + h];
-            const float ks = k.x * qa, off = k.y - ref;
-            const float2 both = f2_parts(weights_of<false, 8>(v + 16 * h, f2(ks, ks), f2(off, off), p[c] + 8 * h, nullptr));
-            const float one = both.x + both.y;
-            most = fmaxf(most, one);                         // (NaN weights are none the other way either)
-            now = fmaf(one, k.z, now);
-        }
-    }
-    if (!__all_sync(0xffffffffu, most <= 0x1p15f && ref != kv8_none())) return false;
-    l = now;
-#pragma unroll
-    for (int c = 0; c < KT / 32; ++c) tmem_st_32x32b_x16(s_addr + 32 * c, p[c]);
-    return true;
-}
-
 // A warp's 32 rows of queries, scaled by a power of two to 2^14 .. 2^15, in the layout of an MMA operand (the scores of
 // the rows before are there, so nobody reads those any more).  Returns the power of the lane's row.  Raw pieces
 // of 8 elements are copied to where their f16 values (f32: first and second parts) go, and converted in place.
@@ -417,31 +389,26 @@ __device__ __forceinline__ void store_row(uint32_t o_addr, bool live, float inv,
     }
 }
 
-// The MMAs of one group: scores S = Q K^T from decoded tile KB, and values O (+)= P V with VB = KB + 1.  Buffers and
-// groups are constants, and so all operands of the instructions but the first's flag: computed ones would be
-// moved into uniform registers one by one (120 cycles an MMA).  All of tensor memory is this CTA's: it begins at 0.
-template <class F, int D, int QI, int KB>
-__device__ __forceinline__ void issue_scores(uint32_t q, uint32_t kv) {
+// The MMAs of one group: scores S = Q K^T, and values O (+)= P V.
+template <class F, int D>
+__device__ __forceinline__ void issue_scores(uint32_t s, uint64_t q, uint64_t k) {
     constexpr uint32_t idesc = idesc_f16_f32(128, KT);
 #pragma unroll
     for (int part = 0; part < (F::SPLIT ? 2 : 1); ++part)
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k >> 2) * F::SLAB + (k & 3) * 32;
-            umma_f16_ss(S_COL + 128 * QI, sdesc_kmajor_sw128(q + (QI + part) * F::TILE + off),
-                        sdesc_kmajor_sw128(kv + KB * F::TILE + off), idesc, part || k);
+        for (int i = 0; i < D / 16; ++i) {
+            const uint32_t off = ((i >> 2) * F::SLAB + (i & 3) * 32) >> 4;
+            umma_f16_ss(s, q + (part * F::TILE >> 4) + off, k + off, idesc, part || i);
         }
 }
-template <class F, int D, int QI, int KB>
-__device__ __forceinline__ void issue_values(uint32_t kv, bool add) {
+template <class F, int D>
+__device__ __forceinline__ void issue_values(uint32_t o, uint32_t p, uint64_t v, uint32_t add) {
     constexpr uint32_t idesc = idesc_f16_f32_bmn(128, D);
 #pragma unroll
-    for (int k = 0; k < KT / 16; ++k)
+    for (int i = 0; i < KT / 16; ++i)
 #pragma unroll
         for (int part = 0; part < (F::TWO ? 2 : 1); ++part)
-            umma_f16_ts(O_COL + D * QI, S_COL + 128 * QI + 32 * (k >> 1) + 16 * part + 8 * (k & 1),
-                        sdesc_mnmajor_sw128(kv + (KB + 1) * F::TILE + k * 2048, F::SLAB, 1024), idesc,
-                        k || part ? 1u : (uint32_t)add);
+            umma_f16_ts(o, p + 32 * (i >> 1) + 16 * part + 8 * (i & 1), v + (i * 2048 >> 4), idesc, i || part ? 1u : add);
 }
 
 template <class T, int D>
@@ -651,26 +618,25 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
             for (int u = 0; u < F::RAW; ++u)
                 if (u < st || wrapped) mbar_wait(&sm.raw_full[u], u < st ? ph : ph ^ 1);
     } else if (warp == 1) {                                  // ---- MMA issuer
-        using Sh = Shared<T, D>;
-        static_assert(offsetof(Sh, q) == 0 && offsetof(Sh, kv) == 2 * F::TILE, "operands lead");
-        const uint32_t q_at = smem_u32(raw_shared), kv_at = q_at + 2 * F::TILE;
+        const uint64_t q0_desc = sdesc_kmajor_sw128(smem_u32(sm.q[0])), k0_desc = sdesc_kmajor_sw128(smem_u32(sm.kv[0]));
+        const uint64_t v0_desc = sdesc_mnmajor_sw128(smem_u32(sm.kv[0]), F::SLAB, 1024);
         uint32_t q_ph = 0, p_ph = 0;                         // a bit a group
         uint32_t g = 0;                                      // tiles
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-            if (ok && !mbar_wait_or_abort(bar, parity, abort_flag, true)) {
-                sm.abort = 1;
-                ok = false;
-            }
+            // (a vote: what follows is the same in the whole warp, and known to be)
+            ok = __all_sync(0xffffffffu, ok && mbar_wait_or_abort(bar, parity, abort_flag, true));
+            if (!ok) sm.abort = 1;
             return ok;
         };
         Piece w;
-        while (ok && next_piece(w)) {
-            const int nq = w.rows - w.tile * ROWS > 128 ? F::NQ : 1;
+        while (ok && __any_sync(0xffffffffu, next_piece(w))) {
+            const int nq = __shfl_sync(0xffffffffu, w.rows - w.tile * ROWS > 128 ? F::NQ : 1, 0);
+            const int run = __shfl_sync(0xffffffffu, w.run, 0);
             // step i: the values of tile i, and of each group right behind them the scores of tile i + 1
 #pragma unroll 1
-            for (int i = -1; ok && i < w.run; ++i) {
-                const bool more = i + 1 < w.run;
+            for (int i = -1; ok && i < run; ++i) {
+                const bool more = i + 1 < run;
                 const int vb = (2 * g - 1) & 3, kb = 2 * g & 3;              // (g: tile i + 1 of all)
                 const uint32_t v_ph = (g - 1) >> 1 & 1, k_ph = g >> 1 & 1;
 #pragma unroll 1
@@ -681,10 +647,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                         if (qi == 0 && !wait(&sm.kv_full[vb], v_ph)) break;
                         tc_fence_after();
                         if (elect_one()) {
-                            if (vb == 1)
-                                qi ? issue_values<F, D, F::NQ - 1, 0>(kv_at, i > 0) : issue_values<F, D, 0, 0>(kv_at, i > 0);
-                            else
-                                qi ? issue_values<F, D, F::NQ - 1, 2>(kv_at, i > 0) : issue_values<F, D, 0, 2>(kv_at, i > 0);
+                            issue_values<F, D>(O_COL + D * qi, S_COL + 128 * qi, v0_desc + (uint32_t)vb * (F::TILE >> 4), i > 0);
                             if (qi == nq - 1) umma_commit(&sm.kv_empty[vb]);
                             if (!more) umma_commit(&sm.o_full[qi]);
                         }
@@ -697,10 +660,8 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                         if (qi == 0 && !wait(&sm.kv_full[kb], k_ph)) break;
                         tc_fence_after();
                         if (elect_one()) {
-                            if (kb == 0)
-                                qi ? issue_scores<F, D, F::NQ - 1, 0>(q_at, kv_at) : issue_scores<F, D, 0, 0>(q_at, kv_at);
-                            else
-                                qi ? issue_scores<F, D, F::NQ - 1, 2>(q_at, kv_at) : issue_scores<F, D, 0, 2>(q_at, kv_at);
+                            issue_scores<F, D>(S_COL + 128 * qi, q0_desc + (uint32_t)qi * (F::TILE >> 4),
+                                               k0_desc + (uint32_t)kb * (F::TILE >> 4));
                             umma_commit(&sm.s_full[qi]);
                             if (qi == nq - 1) umma_commit(&sm.kv_empty[kb]);
                         }
@@ -754,7 +715,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                 uint8_t* dst = sm.kv[buf];
                 // Eight rows of 64 packed bytes a step.  Lanes 0..3 and 4..7 of a phase take rows r and r ^ 5: their swizzled
                 // 16-byte pieces lie in different halves of a line, and those of f16 in its even and odd pieces.
-                constexpr int DEEP = 4;                      // steps whose loads are in flight
+                constexpr int DEEP = 2;                      // steps whose loads are in flight
                 const int in8 = (lane >> 3) ^ ((lane >> 2 & 1) * 5), c = lane & 3;
                 const int row0 = dw * 32 + in8;
                 const int from = row0 * D + (D == 128 ? c ^ in8 : c ^ (in8 >> 1 & 3)) * 16;
@@ -859,29 +820,27 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                 const float4* cons = sm.cons[slot];
                 const bool inside = base >= safe_lo && base + KT <= safe_hi;
                 const int lo = row_lo - base, hi = row_hi - base;
-                if (F::TWO || i == 0 || !inside || !tile_weights_if(s_addr, cons, qa, m, l)) {
-                    const float t = inside ? tile_top(s_addr, cons, qa) : tile_top_some(s_addr, cons, qa, lo, hi);
-                    const bool raise = t > m + RAISE;
-                    if (__any_sync(0xffffffffu, raise)) {
-                        const float now = raise ? t - HEAD : m;
-                        const float f = raise ? exp2_fast(m - now) : 1.f;
-                        m = now;
-                        l *= f;
-                        if (i > 0) {
+                const float t = inside ? tile_top(s_addr, cons, qa) : tile_top_some(s_addr, cons, qa, lo, hi);
+                const bool raise = t > m + RAISE;
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float now = raise ? t - HEAD : m;
+                    const float f = raise ? exp2_fast(m - now) : 1.f;
+                    m = now;
+                    l *= f;
+                    if (i > 0) {
 #pragma unroll 1
-                            for (int c = 0; c < D / 16; ++c) {
-                                uint32_t o[16];
-                                tmem_ld_32x32b_x16(o_addr + 16 * c, o);
-                                tmem_wait_ld();
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld_32x32b_x16(o_addr + 16 * c, o);
+                            tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st_32x32b_x16(o_addr + 16 * c, o);
-                            }
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st_32x32b_x16(o_addr + 16 * c, o);
                         }
                     }
-                    const float ref = m == NONE ? 0.f : m;
-                    l = inside ? tile_weights<F::TWO>(s_addr, cons, qa, ref, l) : tile_weights_some<F::TWO>(s_addr, cons, ref, l);
                 }
+                const float ref = m == NONE ? 0.f : m;
+                l = inside ? tile_weights<F::TWO>(s_addr, cons, qa, ref, l) : tile_weights_some<F::TWO>(s_addr, cons, ref, l);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
