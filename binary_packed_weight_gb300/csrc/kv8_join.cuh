@@ -75,43 +75,66 @@ __device__ __forceinline__ float kv8_factor(float m, float l, float top) {
     return m == kv8_none() ? (l != 0.f ? 1.f : 0.f) : exp2_fast(m - top);
 }
 
-// The pieces' sums in the order of the tokens.  A warp takes a row.
-template <class T, int D, int RM>
-__global__ void __launch_bounds__(256)
+// The pieces' sums, each warp's in the order of the tokens and then those of the WPR warps that share a row: one
+// where a row has few pieces and there are many rows, several where one sequence was cut over the whole GPU.
+constexpr int KV8_JOIN_WARPS = 8;
+template <class T, int D, int RM, int WPR>
+__global__ void __launch_bounds__(KV8_JOIN_WARPS * 32)
 kv8_join_kernel(const __grid_constant__ Kv8Attention a, const float* parts, const Kv8Joint* joints) {
+    constexpr int RPB = KV8_JOIN_WARPS / WPR, PER = D / 32;  // rows a block at a time; a lane's columns
+    constexpr size_t PART = kv8_part_floats(RM, D);
+    __shared__ float os[KV8_JOIN_WARPS][D], ls[KV8_JOIN_WARPS];
     pdl_launch_dependents();
     pdl_wait();
-    const int cta = blockIdx.x, lane = threadIdx.x & 31;
+    const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = warp % WPR;
     const Kv8Joint j = joints[cta];
     if (j.pieces == 0) return;
     const Kv8Seq q = kv8_seq(a.c, j.s);
     const int rows = min(q.n * a.G - j.tile * RM, RM);
-    constexpr int PER = D / 32;
-    constexpr size_t PART = kv8_part_floats(RM, D);
     const float* first = parts + ((size_t)cta * 2 + 1) * PART;
     const float* rest = parts + (size_t)cta * 2 * PART;
-    for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8) {
-        float top = kv8_none();
-        for (int i = lane; i < j.pieces; i += 32) top = fmaxf(top, (i ? rest + i * 2 * PART : first)[r]);
-#pragma unroll
-        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        float sum = 0.f, o[PER];
+    for (int r0 = blockIdx.y * RPB; r0 < rows; r0 += gridDim.y * RPB) {
+        const int r = r0 + warp / WPR;
+        const bool live = r < rows;
+        float top = kv8_none(), sum = 0.f, o[PER];
 #pragma unroll
         for (int c = 0; c < PER; ++c) o[c] = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < j.pieces; ++i) {
-            const float* p = i ? rest + i * 2 * PART : first;
-            const float l = p[RM + r], f = kv8_factor(p[r], l, top);
-            sum = fmaf(l, f, sum);
+        if (live) {
+            for (int i = lane; i < j.pieces; i += 32) top = fmaxf(top, (i ? rest + i * 2 * PART : first)[r]);
 #pragma unroll
-            for (int c = 0; c < PER; ++c) o[c] = fmaf(p[2 * RM + r * D + lane + 32 * c], f, o[c]);
+            for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+#pragma unroll 8
+            for (int i = share; i < j.pieces; i += WPR) {
+                const float* p = i ? rest + i * 2 * PART : first;
+                const float l = p[RM + r], f = kv8_factor(p[r], l, top);
+                sum = fmaf(l, f, sum);
+#pragma unroll
+                for (int c = 0; c < PER; ++c) o[c] = fmaf(p[2 * RM + r * D + lane + 32 * c], f, o[c]);
+            }
         }
-        int64_t at_lse;
-        T* dst = static_cast<T*>(a.out) + kv8_out_row(a, q.q0, j.head, j.tile * RM + r, &at_lse);
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        if (WPR > 1) {
 #pragma unroll
-        for (int c = 0; c < PER; ++c) dst[lane + 32 * c] = kv8_round<T>(o[c] * inv);
-        if (lane == 0 && a.lse) a.lse[at_lse] = kv8_lse(top, sum);
+            for (int c = 0; c < PER; ++c) os[warp][lane + 32 * c] = o[c];
+            if (lane == 0) ls[warp] = sum;
+            __syncthreads();
+            if (share == 0) {
+#pragma unroll
+                for (int k = 1; k < WPR; ++k) {
+                    sum += ls[warp + k];
+#pragma unroll
+                    for (int c = 0; c < PER; ++c) o[c] += os[warp + k][lane + 32 * c];
+                }
+            }
+            __syncthreads();
+        }
+        if (live && share == 0) {
+            int64_t at_lse;
+            T* dst = static_cast<T*>(a.out) + kv8_out_row(a, q.q0, j.head, j.tile * RM + r, &at_lse);
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+            for (int c = 0; c < PER; ++c) dst[lane + 32 * c] = kv8_round<T>(o[c] * inv);
+            if (lane == 0 && a.lse) a.lse[at_lse] = kv8_lse(top, sum);
+        }
     }
 }
 

@@ -30,17 +30,23 @@ constexpr int CT = 64;          // tokens of a chunk
 constexpr int WARPS = 4;        // that compute; one more feeds them
 constexpr int THREADS = WARPS * 32 + 32;
 constexpr int STAGES = 4;
+constexpr int CTAS = 2;         // a SM
 // The running reference m of a row: HEAD below the largest weight when it was set (so that f16 keeps
 // weights down to 2^-30 of it), set anew where a weight passes RAISE above it (2^15 is in f16's range).
 constexpr float HEAD = 6.f, RAISE = 14.f;
-constexpr int MIN_CHUNKS = 2;   // of a CTA, where there are fewer than the GPU's CTAs take
+// The cut counts a tile of rows as its chunks and so many more, which is about what queries and the closing sums
+// cost.  A cut through those is one at their start.
+constexpr int EXTRA = 2;
+constexpr int LEAST = EXTRA + 1;                             // units of a CTA: no two cuts through the same EXTRA
 
 template <int D>
 struct __align__(1024) Shared {
     uint8_t k[STAGES][CT * D];
     uint8_t v[STAGES][CT * D];
-    float acc[WARPS][16 * (D + 4)];
+    uint4 q[D / 16][32];        // queries as MMA operands, by k step and lane
+    float acc[WARPS][16 * (D / 2 + 4)];
     float m[WARPS][16], l[WARPS][16];
+    float qa[16];               // what undoes a row's power of two
     float2 scales[STAGES][4];   // of keys and of values, by piece; values' -1: nothing there
     uint64_t full[STAGES], empty[STAGES];
     long long sums[WARPS + 1], seq_start;
@@ -65,7 +71,7 @@ __device__ __forceinline__ long long open_seq(const Kv8Attention& a, int s, Walk
     const int from = a.window ? max(w.q.len - w.q.n - a.window + 1, 0) : 0;
     w.first = from / CT;
     w.count = max((w.q.len + CT - 1) / CT - w.first, 1);
-    return (long long)w.tiles * a.c.H * w.count;
+    return (long long)w.tiles * a.c.H * (w.count + EXTRA);
 }
 
 // Barrier of the computing warps; the second tells all of them whether any gave up.
@@ -84,7 +90,7 @@ __device__ __forceinline__ bool named_sync_or(bool any) {
 }
 
 template <class T, int D>
-__global__ void __launch_bounds__(THREADS, 2)
+__global__ void __launch_bounds__(THREADS, CTAS)
 kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* joints) {
     constexpr bool SPLIT = sizeof(T) == 4;
     // weights of f16 outputs in two parts too: one part's rounding is as large as the output's own
@@ -127,7 +133,7 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
         if (i < warp) before += sm.sums[i];
         total += sm.sums[i];
     }
-    const Kv8Cut cut(total, gridDim.x, MIN_CHUNKS);
+    const Kv8Cut cut(total, gridDim.x, LEAST);
     const int cta = blockIdx.x;
     if (cta >= cut.ctas) {
         if (tid == 0) joints[cta].pieces = 0;
@@ -149,6 +155,10 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
     __syncthreads();
     w.base = sm.seq_start;
     long long span = open_seq<RM>(a, sm.seq, w);
+    {
+        const int at = (int)((w.pos - w.base) % (w.count + EXTRA));
+        if (at <= EXTRA) w.pos -= at;
+    }
     const int logB = a.c.logB;
     const int rows_piece = min(1 << logB, CT), pieces = CT / rows_piece;
 
@@ -164,9 +174,10 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
                 span = open_seq<RM>(a, w.s + 1, w);
             }
             const long long in = w.pos - w.base;
-            const int item = (int)(in / w.count), ch = (int)(in % w.count);
+            const int item = (int)(in / (w.count + EXTRA)), at = (int)(in % (w.count + EXTRA));
             const int head = item / w.tiles;
-            const long long run = min((long long)(w.count - ch), w.end - w.pos);
+            const int take = (int)min((long long)(w.count + EXTRA - at), w.end - w.pos);
+            const int run = take - (at ? 0 : EXTRA), ch = at ? at - EXTRA : 0;
             const int from = a.window ? max(w.q.len - w.q.n - a.window + 1, 0) : 0;
             for (int i = 0; i < run; ++i) {
                 if (!mbar_wait_or_abort(&sm.empty[stage], phase ^ 1, &sm.abort)) {
@@ -198,7 +209,7 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
                 cp_async_arrive(&sm.full[stage]);
                 if (++stage == STAGES) stage = 0, phase ^= 1, issued = true;
             }
-            w.pos += run;
+            w.pos += take;
         }
         return;
     }
@@ -214,60 +225,69 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
             span = open_seq<RM>(a, w.s + 1, w);
         }
         const long long in = w.pos - w.base;
-        const int item = (int)(in / w.count), ch = (int)(in % w.count);
+        const int item = (int)(in / (w.count + EXTRA)), at = (int)(in % (w.count + EXTRA));
         const int head = item / w.tiles, tile = item % w.tiles;
-        const int run = (int)min((long long)(w.count - ch), w.end - w.pos);
+        const int take = (int)min((long long)(w.count + EXTRA - at), w.end - w.pos);
+        const int run = take - (at ? 0 : EXTRA), ch = at ? at - EXTRA : 0;
+        if (run <= 0) break;                                 // the next CTA begins with these rows
         const int rows = min(w.q.n * a.G - tile * RM, RM);
 
-        // the tile's queries as MMA operands: k step 4j+i of lane t4 takes elements D/4 t4 + 16j + 4i + {0,1}, {2,3}
-        uint32_t qf[KS][4];
+        // The tile's queries as MMA operands: k step 4j+i of lane 4g+t takes elements D/4 t + 16j + 4i + {0,1}, {2,3}
+        // of rows g and g + 8 (SPLIT: of row g, first parts and second).  Eight lanes read a row.
+        {
+            constexpr int EL = D / 8;
+            const int r = warp * (RM / WARPS) + (lane >> 3);
+            const bool mine = lane >> 3 < RM / WARPS, live = mine && r < rows;
+            const int rr = tile * RM + (live ? r : 0), j = rr / a.G;
+            const int d0 = (lane & 7) * EL;
+            const T* p = static_cast<const T*>(a.q) + (int64_t)(w.q.q0 + j) * a.qt + (int64_t)(head * a.G + rr % a.G) * a.qh + d0;
+            float x[EL], most = 0.f;
+            if (a.qvec) {
+                constexpr int N = 16 / (int)sizeof(T);
+#pragma unroll
+                for (int e = 0; e < EL; e += N) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(p + e);
+#pragma unroll
+                    for (int k = 0; k < N; ++k) x[e + k] = kv8_wide(reinterpret_cast<const T*>(&u)[k]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < EL; ++e) x[e] = kv8_wide(p[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < EL; ++e) {
+                x[e] = live ? x[e] : 0.f;
+                most = fmaxf(most, fabsf(x[e]));
+            }
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+            // a power of two that takes the row's largest element to 2^14 .. 2^15
+            const int e = min(max(141 - (int)(__float_as_uint(most) >> 23), -112), 126);
+            const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+            if (mine) {
+                if ((lane & 7) == 0) sm.qa[r] = a.scale * __uint_as_float((uint32_t)(127 - e) << 23);
+                const int half = SPLIT ? 0 : r >> 3, to = (r & 7) * 4 + d0 / (D / 4), in_quarter = d0 % (D / 4);
+#pragma unroll
+                for (int i = 0; i < EL; i += 2) {
+                    const float u0 = x[i] * up, u1 = x[i + 1] * up;
+                    const uint32_t h = pack_half2(u0, u1);
+                    uint32_t* dst = reinterpret_cast<uint32_t*>(&sm.q[(in_quarter + i) / 4][to]) + (i % 4 / 2) * 2;
+                    dst[half] = h;
+                    if (SPLIT) dst[1] = rest_half2(u0, u1, h);
+                }
+            }
+        }
+        named_sync();
         float qa[2];
         int hi[2], lo[2];
         constexpr int HALVES = SPLIT ? 1 : 2;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const int r = g + 8 * half;
-            if (half < HALVES) {
-                const bool live = r < rows;
-                const int rr = tile * RM + (live ? r : 0);
-                const int j = rr / a.G;
-                const T* p = static_cast<const T*>(a.q) + (int64_t)(w.q.q0 + j) * a.qt +
-                             (int64_t)(head * a.G + rr % a.G) * a.qh + t4 * (D / 4);
-                const bool vec = ((reinterpret_cast<uintptr_t>(p)) & 15) == 0;
-                float x[D / 4], most = 0.f;
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    float y[16];
-                    kv8_load16(p + 16 * c, vec, y);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        x[16 * c + e] = live ? y[e] : 0.f;
-                        most = fmaxf(most, fabsf(x[16 * c + e]));
-                    }
-                }
-                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-                // a power of two that takes the row's largest element to 2^14 .. 2^15
-                const int e = min(max(141 - (int)(__float_as_uint(most) >> 23), -112), 126);
-                const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-                qa[half] = a.scale * __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const float u0 = x[4 * ks + 2 * b] * up, u1 = x[4 * ks + 2 * b + 1] * up;
-                        const __half h0 = __float2half_rn(u0), h1 = __float2half_rn(u1);
-                        qf[ks][half + 2 * b] = (uint32_t)__half_as_ushort(h0) | (uint32_t)__half_as_ushort(h1) << 16;
-                        if (SPLIT) qf[ks][1 + 2 * b] = pack_half2(u0 - __half2float(h0), u1 - __half2float(h1));
-                    }
-                const int pos = w.q.len - w.q.n + j;
-                hi[half] = a.causal ? min(w.q.len, pos + 1) : w.q.len;
-                lo[half] = a.window ? max(pos - a.window + 1, 0) : 0;
-            } else {
-                qa[1] = qa[0];
-                hi[1] = hi[0];
-                lo[1] = lo[0];
-            }
+            const int r = g + 8 * (SPLIT ? 0 : half);
+            const int pos = w.q.len - w.q.n + (tile * RM + (r < rows ? r : 0)) / a.G;
+            qa[half] = sm.qa[r];
+            hi[half] = a.causal ? min(w.q.len, pos + 1) : w.q.len;
+            lo[half] = a.window ? max(pos - a.window + 1, 0) : 0;
         }
         // tokens [safe_lo, safe_hi) are seen by all rows of the tile
         const int j0 = tile * RM / a.G, j1 = (tile * RM + rows - 1) / a.G;
@@ -293,19 +313,25 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
             const float2 sc = sm.scales[stage][(warp * 16) / rows_piece];
             if (!(sc.y < 0.f) && token < any_hi && token + 16 > any_lo) {
                 // ---- scores of 16 tokens
-                float s[2][4];
+                float s[2][4] = {};
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-                    const int row = warp * 16 + n * 8 + g;
+                for (int c = 0; c < D / 64; ++c) {
+                    uint4 kw[2];
 #pragma unroll
-                    for (int c = 0; c < D / 64; ++c) {
+                    for (int n = 0; n < 2; ++n) {
+                        const int row = warp * 16 + n * 8 + g;
                         const int col = D == 128 ? (2 * t4 + c) ^ (row & 7) : t4 ^ ((row >> 1) & 3);
-                        const uint4 kw = *reinterpret_cast<const uint4*>(sm.k[stage] + row * D + col * 16);
-                        const uint32_t* e = reinterpret_cast<const uint32_t*>(&kw);
+                        kw[n] = *reinterpret_cast<const uint4*>(sm.k[stage] + row * D + col * 16);
+                    }
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            mma_16816_pure(s[n], qf[4 * c + x], kv8_pair<0>(e[x]), kv8_pair<2>(e[x]));
+                    for (int x = 0; x < 4; ++x) {
+                        const uint4 u = sm.q[4 * c + x][lane];
+                        const uint32_t qf[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const uint32_t e = reinterpret_cast<const uint32_t*>(&kw[n])[x];
+                            mma_16816_pure(s[n], qf, kv8_pair<0>(e), kv8_pair<2>(e));
+                        }
                     }
                 }
                 // ---- weights
@@ -424,7 +450,7 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
             if (++stage == STAGES) stage = 0, phase ^= 1;
         }
 
-        // ---- the four warps' sums, in the order of the warps
+        // ---- the four warps' sums, in the order of the warps; columns NT n + c, c < NT / 2, then the others
 #pragma unroll
         for (int half = 0; half < HALVES; ++half) {
             l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
@@ -433,61 +459,71 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
                 sm.m[warp][g + 8 * half] = m[half];
                 sm.l[warp][g + 8 * half] = l[half];
             }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float* dst = &sm.acc[warp][(g + 8 * half) * (D + 4) + (2 * t4 + x) * NT];
-#pragma unroll
-                for (int c = 0; c < NT; c += 4) {
-                    float4 o;
-                    float* po = reinterpret_cast<float*>(&o);
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        po[y] = SPLIT ? acc[c + y][x] + acc[c + y][2 + x] : acc[c + y][2 * half + x];
-                    *reinterpret_cast<float4*>(dst + c) = o;
-                }
-            }
         }
-        ok = !named_sync_or(!ok);
-        if (!ok) break;
         const bool whole = run == w.count;
         float* part = parts + ((size_t)cta * 2 + (ch == 0 ? 1 : 0)) * kv8_part_floats(RM, D);
-        for (int at = tid; at < rows * (D / 4); at += WARPS * 32) {
-            const int r = at / (D / 4), col = at % (D / 4) * 4;
-            float top = sm.m[0][r];
+        constexpr int HN = NT / 2, LD = D / 2 + 4;
 #pragma unroll
-            for (int i = 1; i < WARPS; ++i) top = fmaxf(top, sm.m[i][r]);
-            float sum = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int cols = 0; cols < 2; ++cols) {
 #pragma unroll
-            for (int i = 0; i < WARPS; ++i) {
-                const float f = kv8_factor(sm.m[i][r], sm.l[i][r], top);
-                sum = fmaf(sm.l[i][r], f, sum);
-                const float4 u = *reinterpret_cast<const float4*>(&sm.acc[i][r * (D + 4) + col]);
-                o.x = fmaf(u.x, f, o.x);
-                o.y = fmaf(u.y, f, o.y);
-                o.z = fmaf(u.z, f, o.z);
-                o.w = fmaf(u.w, f, o.w);
-            }
-            if (whole) {
-                int64_t at_lse;
-                T* dst = static_cast<T*>(a.out) + kv8_out_row(a, w.q.q0, head, tile * RM + r, &at_lse) + col;
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                dst[0] = kv8_round<T>(o.x * inv);
-                dst[1] = kv8_round<T>(o.y * inv);
-                dst[2] = kv8_round<T>(o.z * inv);
-                dst[3] = kv8_round<T>(o.w * inv);
-                if (col == 0 && a.lse) a.lse[at_lse] = kv8_lse(top, sum);
+            for (int half = 0; half < HALVES; ++half)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int c = 0; c < HN; c += 4) {
+                        float4 o;
+                        float* po = reinterpret_cast<float*>(&o);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const float* v = acc[cols * HN + c + y];
+                            po[y] = SPLIT ? v[x] + v[2 + x] : v[2 * half + x];
+                        }
+                        *reinterpret_cast<float4*>(&sm.acc[warp][(g + 8 * half) * LD + (2 * t4 + x) * HN + c]) = o;
+                    }
+            if (cols == 0) {
+                ok = !named_sync_or(!ok);
+                if (!ok) break;
             } else {
-                *reinterpret_cast<float4*>(part + 2 * RM + r * D + col) = o;
-                if (col == 0) part[r] = top, part[RM + r] = sum;
+                named_sync();
             }
+            for (int i = tid; i < rows * (D / 8); i += WARPS * 32) {
+                const int r = i / (D / 8), c = i % (D / 8) * 4, col = c / HN * NT + cols * HN + c % HN;
+                float top = sm.m[0][r];
+#pragma unroll
+                for (int k = 1; k < WARPS; ++k) top = fmaxf(top, sm.m[k][r]);
+                float sum = 0.f;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < WARPS; ++k) {
+                    const float f = kv8_factor(sm.m[k][r], sm.l[k][r], top);
+                    sum = fmaf(sm.l[k][r], f, sum);
+                    const float4 u = *reinterpret_cast<const float4*>(&sm.acc[k][r * LD + c]);
+                    o.x = fmaf(u.x, f, o.x);
+                    o.y = fmaf(u.y, f, o.y);
+                    o.z = fmaf(u.z, f, o.z);
+                    o.w = fmaf(u.w, f, o.w);
+                }
+                if (whole) {
+                    int64_t at_lse;
+                    T* dst = static_cast<T*>(a.out) + kv8_out_row(a, w.q.q0, head, tile * RM + r, &at_lse) + col;
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    dst[0] = kv8_round<T>(o.x * inv);
+                    dst[1] = kv8_round<T>(o.y * inv);
+                    dst[2] = kv8_round<T>(o.z * inv);
+                    dst[3] = kv8_round<T>(o.w * inv);
+                    if (col == 0 && a.lse) a.lse[at_lse] = kv8_lse(top, sum);
+                } else {
+                    *reinterpret_cast<float4*>(part + 2 * RM + r * D + col) = o;
+                    if (col == 0) part[r] = top, part[RM + r] = sum;
+                }
+            }
+            named_sync();
         }
-        if (!whole && ch == 0) {
-            const long long last = w.pos + w.count - 1;
-            joint = Kv8Joint{w.s, head, tile, cut.of(last) - cta + 1};
-        }
-        named_sync();
-        w.pos += run;
+        if (!ok) break;
+        if (!whole && at == 0)
+            // the rows' other pieces: as many CTAs as the rest of their chunks reaches into
+            joint = Kv8Joint{w.s, head, tile, cut.of(w.pos + EXTRA + w.count - 1) - cta + 1};
+        w.pos += take;
     }
     if (tid == 0) joints[cta] = ok ? joint : Kv8Joint{0, 0, 0, 0};
 }
@@ -496,7 +532,7 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
 int grid_of(const Kv8Attention& a) {
     const int64_t most = (int64_t)a.c.seqs * a.c.H * (((int64_t)a.c.width << a.c.logB) / CT + 1) *
                          (((int64_t)a.c.T * a.G + 7) / 8);
-    const int64_t full = 2 * kv8_sm_count();
+    const int64_t full = CTAS * kv8_sm_count();
     return (int)(most < full ? most : full);
 }
 
@@ -512,7 +548,7 @@ cudaError_t run(const Kv8Attention& a, void* scratch, cudaStream_t st) {
     g_launched.store(true, std::memory_order_release);
     e = launch_pdl(kv8_stream_kernel<T, D>, dim3(grid), dim3(THREADS), sizeof(Shared<D>), st, a, parts, joints);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kv8_join_kernel<T, D, RM>, dim3(grid), dim3(256), 0, st, a, (const float*)parts, (const Kv8Joint*)joints);
+    return launch_pdl(kv8_join_kernel<T, D, RM, 4>, dim3(grid, RM / 2), dim3(KV8_JOIN_WARPS * 32), 0, st, a, (const float*)parts, (const Kv8Joint*)joints);
 }
 
 template <class T>

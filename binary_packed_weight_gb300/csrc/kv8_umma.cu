@@ -876,7 +876,7 @@ cudaError_t run(const Kv8Attention& a, void* scratch, cudaStream_t st) {
     g_launched.store(true, std::memory_order_release);
     e = launch_pdl(kv8_umma_kernel<T, D>, dim3(grid), dim3(THREADS), sizeof(Shared<T, D>), st, a, parts, joints);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kv8_join_kernel<T, D, ROWS>, dim3(grid, ROWS / 32), dim3(256), 0, st, a, (const float*)parts,
+    return launch_pdl(kv8_join_kernel<T, D, ROWS, 1>, dim3(grid, ROWS / 32), dim3(KV8_JOIN_WARPS * 32), 0, st, a, (const float*)parts,
                       (const Kv8Joint*)joints);
 }
 
