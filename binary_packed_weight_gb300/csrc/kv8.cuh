@@ -132,11 +132,12 @@ struct Kv8Attention {
     int64_t qt, qh, ot, oh;     // strides in elements
     int dtype, G;               // query heads a head of the cache
     int qvec;                   // rows of q are 16-byte aligned
+    int narrow;                 // no sequence has more than 8 rows
     float scale;                // softmax scale * log2(e)
     int causal, window;
     int few;                    // sequences of at most so many rows (queries * G) are the streaming path's
 };
-int kv8_few_rows(int dtype);    // most rows of a sequence that the streaming path takes in one pass
+constexpr int KV8_FEW_ROWS = 32;  // of a sequence: where there are no more, the streaming path is faster
 size_t kv8_stream_scratch(const Kv8Attention& a);
 cudaError_t launch_kv8_stream(const Kv8Attention& a, void* scratch, cudaStream_t st);
 unsigned int read_clear_dev_error_kv8_stream(cudaStream_t st);

@@ -99,6 +99,10 @@ tq2_status kv8_attention(const kv8_cache* c, const kv8_batch* b, const void* q, 
                                      "kv8_attention: need a finite scale, causal 0 or 1, window >= 0 (0 unless causal), "
                                      "max_q >= 0 (scale=%g causal=%d window=%lld max_q=%lld)",
                                      (double)scale, causal, (long long)window, (long long)max_q);
+    // tiles of 128 rows by 128 tokens are counted in 32 bits a CTA
+    if ((T * (Hq / c->heads) / 128 + b->seqs) * c->heads * ((int64_t)b->width * c->tokens / 128 + 1) >= ((int64_t)1 << 38))
+        return (tq2_status)set_error(TQ2_ESHAPE, "kv8_attention: T=%lld rows over tables of %lld tokens are too many for one call",
+                                     (long long)T, (long long)b->width * c->tokens);
     if (T == 0) return TQ2_OK;
     if (!q || !out) return (tq2_status)set_error(TQ2_EINVAL, "kv8_attention: null pointer");
     if (off_element(q, element_size(dtype)) || off_element(out, element_size(dtype)) || off_element(lse, 4))
@@ -122,11 +126,17 @@ tq2_status kv8_attention(const kv8_cache* c, const kv8_batch* b, const void* q, 
     a.scale = scale * 1.4426950408889634f;                    // powers of 2 from here on
     a.causal = causal;
     a.window = window < ((int64_t)1 << 30) ? (int)window : 0;  // no sequence is longer
-    // Rows of a sequence: few go the streaming way, many the tensor cores'.  Which sequences have how many
-    // the host does not know, so where both may be there both kernels are launched, each for its own.
+    // Rows of a sequence (queries * G): few go the streaming way, many the tensor cores'.  Which sequences have how
+    // many the host does not know, so where both may be there both kernels are launched, each for its own; but where the
+    // tables hold little, all go one way.  (8 sequences of 4096 tokens, 8 heads of 128, G = 4, bf16: 16 rows 25 us
+    // streaming and 42 on the tensor cores, 32 rows 37 / 43, 64 rows 62 / 44.  f32, passes of 8 rows: 34 / 61, 57 / 61,
+    // 103 / 63.  The second pair of kernels costs 7 us; few rows' codes stream at 5 TB/s and pass the tensor
+    // cores at half of that, so 32 MB are worth it.)
     const int64_t rows = (max_q && max_q < T ? max_q : T) * a.G;
-    const bool few = rows <= kv8_few_rows(dtype);
-    a.few = few ? 0x7fffffff : b->seqs == 1 ? 0 : kv8_few_rows(dtype);
+    const int64_t held = (int64_t)b->seqs * b->width * c->tokens * c->heads * c->dim * 2;
+    const bool few = rows <= KV8_FEW_ROWS;
+    a.few = few ? 0x7fffffff : b->seqs == 1 || held <= ((int64_t)32 << 20) ? 0 : KV8_FEW_ROWS;
+    a.narrow = rows <= 8;
     const size_t stream_bytes = (kv8_stream_scratch(a) + 255) / 256 * 256;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     Scratch mem(st);

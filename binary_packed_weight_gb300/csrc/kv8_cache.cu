@@ -31,7 +31,6 @@ constexpr float SMALLEST = 0x1p-96f;
 
 __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* shared) {
     v = __reduce_max_sync(0xffffffffu, v);
-    if (blockDim.x == 32) return v;
     __syncthreads();                                         // the last block's maximum has been read
     if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
     __syncthreads();
@@ -64,28 +63,45 @@ kv8_write_kernel(const Kv8View c, const T* k, const T* v, int64_t kt, int64_t kh
     if (q.n == 0 || q.len == 0) return;
     const T* x = kv ? v : k;
     const int64_t xt = kv ? vt : kt, xh = kv ? vh : kh;
-    const int B = 1 << c.logB, per_row = c.D / CHUNK, chunks = per_row << c.logB;
+    const int B = 1 << c.logB, logR = c.D == 128 ? 3 : 2, chunks = 1 << (logR + c.logB);   // a row's chunks, a block's
     const int start = q.len - q.n;                           // below 0: tokens that no position is left for
     const int first = max(start, 0);
+    constexpr int W = CHUNK * (int)sizeof(T) / 16;
     for (int b = (first >> c.logB) + blockIdx.z; (b << c.logB) < q.len; b += gridDim.z) {
-        const int block = kv8_block(c, s, b << c.logB);
-        if (block < 0) continue;
         const int base = b << c.logB;
         const int lo = max(first - base, 0), hi = min(q.len - base, B);   // new tokens of the block
-        float y[MAX_CHUNKS][CHUNK];
+        // the values stay as they came between the maximum and the codes
+        uint4 raw[MAX_CHUNKS][W];
+        const T* from = x + (q.q0 + (base - start)) * xt + head * xh;
+#pragma unroll
+        for (int i = 0; i < MAX_CHUNKS; ++i) {
+            const int at = threadIdx.x + i * blockDim.x, token = at >> logR;
+#pragma unroll
+            for (int k = 0; k < W; ++k) raw[i][k] = make_uint4(0, 0, 0, 0);
+            if (at < chunks && token >= lo && token < hi) {
+                const T* p = from + token * xt + (at & ((1 << logR) - 1)) * CHUNK;
+                if (vec) {
+#pragma unroll
+                    for (int k = 0; k < W; ++k) raw[i][k] = __ldcs(reinterpret_cast<const uint4*>(p) + k);
+                } else {
+                    T* e = reinterpret_cast<T*>(raw[i]);
+#pragma unroll
+                    for (int k = 0; k < CHUNK; ++k) e[k] = p[k];
+                }
+            }
+        }
+        const int block = kv8_block(c, s, base);
+        float* where = c.scales + ((int64_t)max(block, 0) * 2 + kv) * c.H + head;
+        const float before = lo > 0 && block >= 0 ? *where : 0.f;
         uint32_t peak = 0;
 #pragma unroll
         for (int i = 0; i < MAX_CHUNKS; ++i) {
-            const int at = threadIdx.x + i * blockDim.x, token = at / per_row;
-            if (at < chunks && token >= lo && token < hi) {
-                kv8_load16(x + (q.q0 + (base + token - start)) * xt + head * xh + (at % per_row) * CHUNK, vec, y[i]);
+            const T* e = reinterpret_cast<const T*>(raw[i]);
 #pragma unroll
-                for (int j = 0; j < CHUNK; ++j) peak = max(peak, __float_as_uint(y[i][j]) & 0x7fffffffu);
-            }
+            for (int k = 0; k < CHUNK; ++k) peak = max(peak, __float_as_uint(kv8_wide(e[k])) & 0x7fffffffu);
         }
-        peak = block_max(peak, shared);
-        float* where = c.scales + ((int64_t)block * 2 + kv) * c.H + head;
-        const float before = lo > 0 ? *where : 0.f;
+        peak = block_max(peak, shared);                      // (behind it, every thread has read the scale)
+        if (block < 0) continue;
         const float most = __uint_as_float(peak);
         // a value that is no number leaves none in the block
         const float fresh = peak >= 0x7f800000u ? __uint_as_float(0x7fffffffu)
@@ -95,17 +111,21 @@ kv8_write_kernel(const Kv8View c, const T* k, const T* v, int64_t kt, int64_t kh
         const float inverse = now > 0.f ? __fdiv_rn(1.f, now) : 0.f;
         const bool coarser = lo > 0 && now > before;
         const float ratio = coarser ? __fdiv_rn(before, now) : 1.f;
+        if (threadIdx.x == 0 && (lo == 0 || bad || coarser)) *where = now;
         uint4* codes = reinterpret_cast<uint4*>(c.codes + kv8_row(c, block, kv, head) * c.D);
 #pragma unroll
         for (int i = 0; i < MAX_CHUNKS; ++i) {
-            const int at = threadIdx.x + i * blockDim.x, token = at / per_row;
+            const int at = threadIdx.x + i * blockDim.x, token = at >> logR;
             if (at >= chunks || token >= hi) continue;
             if (token >= lo) {
-                float z[CHUNK];
+                const T* e = reinterpret_cast<const T*>(raw[i]);
+                uint4 w;
+                uint32_t* o = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
-                for (int j = 0; j < CHUNK; ++j) z[j] = code_of(y[i][j], inverse);
-                codes[at] = make_uint4(pack4(z[0], z[1], z[2], z[3]), pack4(z[4], z[5], z[6], z[7]),
-                                       pack4(z[8], z[9], z[10], z[11]), pack4(z[12], z[13], z[14], z[15]));
+                for (int j = 0; j < 4; ++j)
+                    o[j] = pack4(code_of(kv8_wide(e[4 * j]), inverse), code_of(kv8_wide(e[4 * j + 1]), inverse),
+                                 code_of(kv8_wide(e[4 * j + 2]), inverse), code_of(kv8_wide(e[4 * j + 3]), inverse));
+                codes[at] = w;
             } else if (coarser) {
                 uint4 w = codes[at];
                 uint32_t* e = reinterpret_cast<uint32_t*>(&w);
@@ -119,8 +139,6 @@ kv8_write_kernel(const Kv8View c, const T* k, const T* v, int64_t kt, int64_t kh
                 codes[at] = w;
             }
         }
-        __syncthreads();                                     // every thread has read the scale
-        if (threadIdx.x == 0 && (lo == 0 || now != before)) *where = now;
     }
 }
 

@@ -89,12 +89,13 @@ __device__ __forceinline__ bool named_sync_or(bool any) {
     return r != 0;
 }
 
-template <class T, int D>
+// SPLIT: tiles of 8 rows, an MMA's rows r + 8 hold second parts: of f32 queries and weights, and of f16 results' weights
+// where there are no more than 8 rows (with more, those take MMAs of their own: TWO).
+template <class T, int D, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, CTAS)
 kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* joints) {
-    constexpr bool SPLIT = sizeof(T) == 4;
     // weights of f16 outputs in two parts too: one part's rounding is as large as the output's own
-    constexpr bool TWO = std::is_same<T, __half>::value;
+    constexpr bool TWO = !SPLIT && std::is_same<T, __half>::value;
     constexpr int RM = SPLIT ? 8 : 16;
     constexpr int KS = D / 16;                               // k steps of q . c
     constexpr int NT = D / 8;                                // column tiles of the output
@@ -536,38 +537,36 @@ int grid_of(const Kv8Attention& a) {
     return (int)(most < full ? most : full);
 }
 
-template <class T, int D>
+template <class T, int D, bool SPLIT>
 cudaError_t run(const Kv8Attention& a, void* scratch, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(kv8_stream_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(kv8_stream_kernel<T, D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)sizeof(Shared<D>));
     if (e != cudaSuccess) return e;
-    constexpr int RM = sizeof(T) == 4 ? 8 : 16;
+    constexpr int RM = SPLIT ? 8 : 16;
     const int grid = grid_of(a);
     float* parts = static_cast<float*>(scratch);
     Kv8Joint* joints = reinterpret_cast<Kv8Joint*>(parts + (size_t)grid * 2 * kv8_part_floats(RM, D));
     g_launched.store(true, std::memory_order_release);
-    e = launch_pdl(kv8_stream_kernel<T, D>, dim3(grid), dim3(THREADS), sizeof(Shared<D>), st, a, parts, joints);
+    e = launch_pdl(kv8_stream_kernel<T, D, SPLIT>, dim3(grid), dim3(THREADS), sizeof(Shared<D>), st, a, parts, joints);
     if (e != cudaSuccess) return e;
     return launch_pdl(kv8_join_kernel<T, D, RM, 4>, dim3(grid, RM / 2), dim3(KV8_JOIN_WARPS * 32), 0, st, a, (const float*)parts, (const Kv8Joint*)joints);
 }
 
-template <class T>
+template <class T, bool SPLIT>
 cudaError_t run_d(const Kv8Attention& a, void* scratch, cudaStream_t st) {
-    return a.c.D == 64 ? run<T, 64>(a, scratch, st) : run<T, 128>(a, scratch, st);
+    return a.c.D == 64 ? run<T, 64, SPLIT>(a, scratch, st) : run<T, 128, SPLIT>(a, scratch, st);
 }
 
 }  // namespace
-
-int kv8_few_rows(int dtype) { return dtype == TQ2_F32 ? 8 : 16; }
 
 size_t kv8_stream_scratch(const Kv8Attention& a) {
     return (size_t)grid_of(a) * (2 * kv8_part_floats(16, a.c.D) * sizeof(float) + sizeof(Kv8Joint));
 }
 
 cudaError_t launch_kv8_stream(const Kv8Attention& a, void* scratch, cudaStream_t st) {
-    if (a.dtype == TQ2_F32) return run_d<float>(a, scratch, st);
-    if (a.dtype == TQ2_F16) return run_d<__half>(a, scratch, st);
-    return run_d<__nv_bfloat16>(a, scratch, st);
+    if (a.dtype == TQ2_F32) return run_d<float, true>(a, scratch, st);
+    if (a.dtype == TQ2_F16) return a.narrow ? run_d<__half, true>(a, scratch, st) : run_d<__half, false>(a, scratch, st);
+    return run_d<__nv_bfloat16, false>(a, scratch, st);
 }
 
 unsigned int read_clear_dev_error_kv8_stream(cudaStream_t st) { return read_clear_record(st); }
