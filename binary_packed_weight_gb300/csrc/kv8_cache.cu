@@ -11,19 +11,23 @@ namespace tq2 {
 namespace {
 
 constexpr int CHUNK = 16;       // elements a thread takes at a time: 16 codes are one 16-byte store
-constexpr int MAX_CHUNKS = 4;   // of a thread: B * D / 16 codes over 64 to 256 threads
+constexpr int MAX_THREADS = 256;
 
-int threads_of(const Kv8View& c) {
-    const int chunks = (c.D << c.logB) / CHUNK;
-    return chunks < 256 ? chunks : 256;
-}
+// A block's chunks, one, two or four a thread.
+int chunks_of(const Kv8View& c) { return (c.D << c.logB) / CHUNK; }
+int threads_of(const Kv8View& c) { return chunks_of(c) < MAX_THREADS ? chunks_of(c) : MAX_THREADS; }
 
-// Blocks of a sequence are dealt over gridDim.z CTAs: enough for a lone prompt to fill the
-// GPU, none that a decode step would launch in vain.
+// CTAs of a writing SM: what bounds it is a CTA's chain of loads, maximum and stores, so as many as hold their values.
+template <class T, int PER>
+constexpr int ctas() { return PER * sizeof(T) <= 4 ? 5 : PER * sizeof(T) <= 8 ? 3 : 2; }
+
+// Blocks of a sequence are dealt over gridDim.z CTAs: enough for a lone prompt to fill the GPU, and no more than twice
+// the average sequence's blocks (10 sequences of 1500 tokens in blocks of 16, with a CTA for every block there could be:
+// 5.6 us, so 4.1).
 dim3 grid_of(const Kv8View& c) {
-    const int64_t most = ((int64_t)c.T >> c.logB) + 2;
-    const int64_t want = (int64_t)(152 * 32) / ((int64_t)c.seqs * c.H * 2) + 1;
-    return dim3((unsigned)c.seqs, (unsigned)(c.H * 2), (unsigned)(c.T == c.seqs ? 1 : most < want ? most : want));
+    const int64_t most = 2 * (int64_t)c.T / ((int64_t)c.seqs << c.logB) + 1;
+    const int64_t fill = (int64_t)(152 * 32) / ((int64_t)c.seqs * c.H * 2) + 1;
+    return dim3((unsigned)c.seqs, (unsigned)(c.H * 2), (unsigned)(most < fill ? most : fill));
 }
 
 // Values below 2^-96 count as zeros, so that a scale and its reciprocal are normal numbers.
@@ -52,10 +56,10 @@ __device__ __forceinline__ float code_of(float x, float inverse) {
     return fminf(fmaxf(rintf(__fmul_rn(x, inverse)), -127.f), 127.f);
 }
 
-template <class T>
-__global__ void __launch_bounds__(256)
+template <class T, int PER>
+__global__ void __launch_bounds__(MAX_THREADS, ctas<T, PER>())
 kv8_write_kernel(const Kv8View c, const T* k, const T* v, int64_t kt, int64_t kh, int64_t vt, int64_t vh, bool vec) {
-    __shared__ uint32_t shared[8];
+    __shared__ uint32_t shared[MAX_THREADS / 32];
     pdl_launch_dependents();
     pdl_wait();
     const int s = blockIdx.x, head = blockIdx.y >> 1, kv = blockIdx.y & 1;
@@ -71,10 +75,10 @@ kv8_write_kernel(const Kv8View c, const T* k, const T* v, int64_t kt, int64_t kh
         const int base = b << c.logB;
         const int lo = max(first - base, 0), hi = min(q.len - base, B);   // new tokens of the block
         // the values stay as they came between the maximum and the codes
-        uint4 raw[MAX_CHUNKS][W];
+        uint4 raw[PER][W];
         const T* from = x + (q.q0 + (base - start)) * xt + head * xh;
 #pragma unroll
-        for (int i = 0; i < MAX_CHUNKS; ++i) {
+        for (int i = 0; i < PER; ++i) {
             const int at = threadIdx.x + i * blockDim.x, token = at >> logR;
 #pragma unroll
             for (int k = 0; k < W; ++k) raw[i][k] = make_uint4(0, 0, 0, 0);
@@ -95,7 +99,7 @@ kv8_write_kernel(const Kv8View c, const T* k, const T* v, int64_t kt, int64_t kh
         const float before = lo > 0 && block >= 0 ? *where : 0.f;
         uint32_t peak = 0;
 #pragma unroll
-        for (int i = 0; i < MAX_CHUNKS; ++i) {
+        for (int i = 0; i < PER; ++i) {
             const T* e = reinterpret_cast<const T*>(raw[i]);
 #pragma unroll
             for (int k = 0; k < CHUNK; ++k) peak = max(peak, __float_as_uint(kv8_wide(e[k])) & 0x7fffffffu);
@@ -114,7 +118,7 @@ kv8_write_kernel(const Kv8View c, const T* k, const T* v, int64_t kt, int64_t kh
         if (threadIdx.x == 0 && (lo == 0 || bad || coarser)) *where = now;
         uint4* codes = reinterpret_cast<uint4*>(c.codes + kv8_row(c, block, kv, head) * c.D);
 #pragma unroll
-        for (int i = 0; i < MAX_CHUNKS; ++i) {
+        for (int i = 0; i < PER; ++i) {
             const int at = threadIdx.x + i * blockDim.x, token = at >> logR;
             if (at >= chunks || token >= hi) continue;
             if (token >= lo) {
@@ -143,7 +147,7 @@ kv8_write_kernel(const Kv8View c, const T* k, const T* v, int64_t kt, int64_t kh
 }
 
 template <class T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(MAX_THREADS)
 kv8_read_kernel(const Kv8View c, T* k, T* v, int64_t kt, int64_t kh, int64_t vt, int64_t vh, bool vec) {
     pdl_launch_dependents();
     pdl_wait();
@@ -162,7 +166,7 @@ kv8_read_kernel(const Kv8View c, T* k, T* v, int64_t kt, int64_t kh, int64_t vt,
         const float scale = c.scales[((int64_t)block * 2 + kv) * c.H + head];
         const uint4* codes = reinterpret_cast<const uint4*>(c.codes + kv8_row(c, block, kv, head) * c.D);
 #pragma unroll
-        for (int i = 0; i < MAX_CHUNKS; ++i) {
+        for (int i = 0; i < 4; ++i) {
             const int at = threadIdx.x + i * blockDim.x, token = at / per_row;
             if (at >= chunks || token < lo || token >= hi) continue;
             const uint4 w = codes[at];
@@ -184,7 +188,9 @@ bool vectors(const Kv8Rows& r) {
 
 template <class T>
 cudaError_t write_as(const Kv8View& c, const Kv8Rows& r, cudaStream_t st) {
-    return launch_pdl(kv8_write_kernel<T>, grid_of(c), dim3(threads_of(c)), 0, st, c, static_cast<const T*>(r.k),
+    auto kernel = chunks_of(c) > 2 * MAX_THREADS ? kv8_write_kernel<T, 4>
+                  : chunks_of(c) > MAX_THREADS ? kv8_write_kernel<T, 2> : kv8_write_kernel<T, 1>;
+    return launch_pdl(kernel, grid_of(c), dim3(threads_of(c)), 0, st, c, static_cast<const T*>(r.k),
                       static_cast<const T*>(r.v), r.kt, r.kh, r.vt, r.vh, vectors(r));
 }
 template <class T>
