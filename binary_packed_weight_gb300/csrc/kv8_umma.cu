@@ -389,11 +389,6 @@ __device__ __forceinline__ void store_row(uint32_t o_addr, bool live, float inv,
     }
 }
 
-// The rest of a wait that did not end at once (out of line: it is not what the issuer's loop is short of).
-__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    return mbar_wait_or_abort(bar, parity, abort_flag, true);
-}
-
 // The MMAs of one group: scores S = Q K^T, and values O (+)= P V.
 template <class F, int D>
 __device__ __forceinline__ void issue_scores(uint32_t s, uint64_t q, uint64_t k) {
@@ -623,59 +618,64 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
             for (int u = 0; u < F::RAW; ++u)
                 if (u < st || wrapped) mbar_wait(&sm.raw_full[u], u < st ? ph : ph ^ 1);
     } else if (warp == 1) {                                  // ---- MMA issuer
-        // One lane runs all of it, in as little code as can be: what the instruction cache next to the
-        // scheduler does not hold takes longer to fetch than the MMAs to issue.
-        if (elect_one()) {
-            const uint64_t q0_desc = sdesc_kmajor_sw128(smem_u32(sm.q[0])), k0_desc = sdesc_kmajor_sw128(smem_u32(sm.kv[0]));
-            const uint64_t v0_desc = sdesc_mnmajor_sw128(smem_u32(sm.kv[0]), F::SLAB, 1024);
-            uint32_t q_ph = 0, p_ph = 0;                     // a bit a group
-            uint32_t g = 0;                                  // tiles whose scores have been issued
-            bool ok = true;
-            auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag); };
-            for (uint32_t n = 0;; ++n) {
-                const int slot = n & (PIECES - 1);
-                if (!wait(&sm.piece_full[slot], n / PIECES & 1)) break;
-                const int run = sm.pieces[slot].run, nq = sm.pieces[slot].rows - sm.pieces[slot].tile * ROWS > 128 ? F::NQ : 1;
-                mbar_arrive(&sm.piece_empty[slot]);
-                if (run == 0) break;
-                // step i: the values of tile i, and of each group right behind them the scores of tile i + 1
+        const uint64_t q0_desc = sdesc_kmajor_sw128(smem_u32(sm.q[0])), k0_desc = sdesc_kmajor_sw128(smem_u32(sm.kv[0]));
+        const uint64_t v0_desc = sdesc_mnmajor_sw128(smem_u32(sm.kv[0]), F::SLAB, 1024);
+        uint32_t q_ph = 0, p_ph = 0;                         // a bit a group
+        uint32_t g = 0;                                      // tiles
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            // (a vote: what follows is the same in the whole warp, and known to be)
+            ok = __all_sync(0xffffffffu, ok && mbar_wait_or_abort(bar, parity, abort_flag, true));
+            if (!ok) sm.abort = 1;
+            return ok;
+        };
+        Piece w;
+        while (ok && __any_sync(0xffffffffu, next_piece(w))) {
+            const int nq = __shfl_sync(0xffffffffu, w.rows - w.tile * ROWS > 128 ? F::NQ : 1, 0);
+            const int run = __shfl_sync(0xffffffffu, w.run, 0);
+            // step i: the values of tile i, and of each group right behind them the scores of tile i + 1
 #pragma unroll 1
-                for (int i = -1; ok && i < run; ++i) {
-                    const bool more = i + 1 < run;
-                    const int vb = (2 * g - 1) & 3, kb = 2 * g & 3;              // (g: tile i + 1 of all)
+            for (int i = -1; ok && i < run; ++i) {
+                const bool more = i + 1 < run;
+                const int vb = (2 * g - 1) & 3, kb = 2 * g & 3;              // (g: tile i + 1 of all)
+                const uint32_t v_ph = (g - 1) >> 1 & 1, k_ph = g >> 1 & 1;
 #pragma unroll 1
-                    for (int qi = 0; qi < nq; ++qi) {
-                        if (i >= 0) {
-                            if (!wait(&sm.p_full[qi], p_ph >> qi & 1) || !wait(&sm.kv_full[vb], (g - 1) >> 1 & 1)) break;
-                            p_ph ^= 1 << qi;
-                            tc_fence_after();
+                for (int qi = 0; qi < nq; ++qi) {
+                    if (i >= 0) {
+                        if (!wait(&sm.p_full[qi], p_ph >> qi & 1)) break;
+                        p_ph ^= 1 << qi;
+                        if (qi == 0 && !wait(&sm.kv_full[vb], v_ph)) break;
+                        tc_fence_after();
+                        if (elect_one()) {
                             issue_values<F, D>(O_COL + D * qi, S_COL + 128 * qi, v0_desc + (uint32_t)vb * (F::TILE >> 4), i > 0);
                             if (qi == nq - 1) umma_commit(&sm.kv_empty[vb]);
                             if (!more) umma_commit(&sm.o_full[qi]);
-                        } else {
-                            if (!wait(&sm.q_full[qi], q_ph >> qi & 1)) break;
-                            q_ph ^= 1 << qi;
                         }
-                        if (more) {
-                            if (!wait(&sm.kv_full[kb], g >> 1 & 1)) break;
-                            tc_fence_after();
+                        __syncwarp();
+                    } else {
+                        if (!wait(&sm.q_full[qi], q_ph >> qi & 1)) break;
+                        q_ph ^= 1 << qi;
+                    }
+                    if (more) {
+                        if (qi == 0 && !wait(&sm.kv_full[kb], k_ph)) break;
+                        tc_fence_after();
+                        if (elect_one()) {
                             issue_scores<F, D>(S_COL + 128 * qi, q0_desc + (uint32_t)qi * (F::TILE >> 4),
                                                k0_desc + (uint32_t)kb * (F::TILE >> 4));
                             umma_commit(&sm.s_full[qi]);
                             if (qi == nq - 1) umma_commit(&sm.kv_empty[kb]);
                         }
+                        __syncwarp();
                     }
-                    if (more) ++g;
                 }
-                if (!ok) break;
-            }
-            if (!ok) {                                       // MMAs in flight end before their operands go
-                sm.abort = 1;
-                umma_commit(&sm.idle);
-                mbar_wait(&sm.idle, 0);
+                if (more) ++g;
             }
         }
-        __syncwarp();
+        if (!ok) {                                           // MMAs in flight end before their operands go
+            if (elect_one()) umma_commit(&sm.idle);
+            __syncwarp();
+            mbar_wait(&sm.idle, 0);
+        }
     } else if (warp >= 12) {                                 // ---- decoders: 32 tokens of a tile each
         const int dw = warp - 12;
         int st = 0;
