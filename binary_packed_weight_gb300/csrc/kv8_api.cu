@@ -100,7 +100,7 @@ tq2_status kv8_attention(const kv8_cache* c, const kv8_batch* b, const void* q, 
                                      "max_q >= 0 (scale=%g causal=%d window=%lld max_q=%lld)",
                                      (double)scale, causal, (long long)window, (long long)max_q);
     // tiles of 128 rows by 128 tokens are counted in 32 bits a CTA
-    if ((T * (Hq / c->heads) / 128 + b->seqs) * c->heads * ((int64_t)b->width * c->tokens / 128 + 1) >= ((int64_t)1 << 38))
+    if (((double)T * (Hq / c->heads) / 128 + b->seqs) * c->heads * ((double)b->width * c->tokens / 128 + 1) >= 0x1p38)
         return (tq2_status)set_error(TQ2_ESHAPE, "kv8_attention: T=%lld rows over tables of %lld tokens are too many for one call",
                                      (long long)T, (long long)b->width * c->tokens);
     if (T == 0) return TQ2_OK;
@@ -133,9 +133,9 @@ tq2_status kv8_attention(const kv8_cache* c, const kv8_batch* b, const void* q, 
     // 103 / 63.  The second pair of kernels costs 7 us; few rows' codes stream at 5 TB/s and pass the tensor
     // cores at half of that, so 32 MB are worth it.)
     const int64_t rows = (max_q && max_q < T ? max_q : T) * a.G;
-    const int64_t held = (int64_t)b->seqs * b->width * c->tokens * c->heads * c->dim * 2;
+    const double held = 2.0 * b->seqs * b->width * c->tokens * c->heads * c->dim;
     const bool few = rows <= KV8_FEW_ROWS;
-    a.few = few ? 0x7fffffff : b->seqs == 1 || held <= ((int64_t)32 << 20) ? 0 : KV8_FEW_ROWS;
+    a.few = few ? 0x7fffffff : b->seqs == 1 || held <= 32 << 20 ? 0 : KV8_FEW_ROWS;
     a.narrow = rows <= 8;
     const size_t stream_bytes = (kv8_stream_scratch(a) + 255) / 256 * 256;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -10,14 +10,22 @@
 // that share a head of the cache, over tiles of 128 tokens.  Warps: one brings packed
 // tiles by TMA, four decode them (code - 128, exact in f16) into the swizzled layout of the MMAs'
 // operands, one issues S = Q K^T (both from shared memory) and O += P V (P from tensor
-// memory, over S's columns), and a group of four for every 128 rows does the softmax, a
-// thread a row, while the MMAs work for the other group.  f32 queries are two f16 parts, f32
-// and f16 results' weights too (twice the MMAs of that product).  All tiles of
-// all rows are cut evenly over the CTAs; what a cut divides is joined afterwards.
+// memory, over S's columns), a group of four for every 128 rows does the softmax, a
+// thread a row, while the MMAs work for the other group, and one walks the list of what is to be
+// done.  f32 queries are two f16 parts, f32 and f16 results' weights too (twice the MMAs of that
+// product: with one part, a weight's rounding is as large as an f16 result's own).  All tiles of
+// all rows are cut over the CTAs by what they cost; what a cut divides is joined afterwards.
 //
 // The MMAs are issued in the order Q K^T, P V, Q K^T .. of a group, and execute in that order: P V
 // reads P before the next scores take its place, and scores that are there mean that the
 // last P V is done, so the group may rescale O.
+//
+// Bound: 8192 causal tokens, 8 heads of 128, G = 4, bf16: 514 us, 1.07 PFLOP/s (55 % of the measured
+// peak; tensor pipe 49 %, issue slots 53 %).  A tile of 128 x 256 takes 4000 cycles, its MMAs 2048.  A group's
+// scores, softmax and values follow one another (2 x 512 cycles of MMAs, 600 until their completion is seen,
+// 1700 of softmax beside the other group's and the decoders), and the operands' reads, the decoders' and the copies
+// want shared memory for 2500 of the 4000.  What the instruction cache does not hold costs time in every
+// role, so code that runs once a tile is kept in short loops, and what runs once a piece is read from one list.
 #include <type_traits>
 
 #include "kv8_join.cuh"
@@ -276,8 +284,6 @@ __device__ __forceinline__ float tile_weights_some(uint32_t s_addr, const float4
 // A warp's 32 rows of queries, scaled by a power of two to 2^14 .. 2^15, in the layout of an MMA operand (the scores of
 // the rows before are there, so nobody reads those any more).  Returns the power of the lane's row.  Raw pieces
 // of 8 elements are copied to where their f16 values (f32: first and second parts) go, and converted in place.
-// (Not inlined and in short loops, as whatever runs once a piece: code that the instruction cache does not
-// hold costs more than it does.)
 template <class T, int D>
 __device__ __forceinline__ int load_queries(const Kv8Attention& a, Shared<T, D>& sm, const Piece& w, int qi,
                                             int warp, int lane) {
@@ -857,10 +863,10 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
 
 // One CTA a SM, and none that could never have a tile.
 int grid_of(const Kv8Attention& a) {
-    const int64_t rows = (int64_t)a.c.T * a.G;
-    const int64_t most = (rows / 128 + a.c.seqs) * a.c.H * ((((int64_t)a.c.width << a.c.logB) + KT - 1) / KT);
-    const int64_t full = kv8_sm_count();
-    return (int)(most < full ? most : full);
+    const double rows = (double)a.c.T * a.G;
+    const double most = (rows / 128 + a.c.seqs) * a.c.H * ((((int64_t)a.c.width << a.c.logB) + KT - 1) / KT);
+    const int full = kv8_sm_count();
+    return most < full ? (int)most : full;
 }
 
 template <class T, int D>

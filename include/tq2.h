@@ -635,7 +635,8 @@ TQ2_API tq2_status moe_experts(q4_handle gate, q4_handle up, q4_handle down, con
 /*
  * The cache: a pool of blocks of `tokens` tokens, in the caller's DEVICE memory.
  *   codes   uint8[blocks][2][heads][tokens][dim] (keys, then values), 16-byte aligned.
- *   scales  float[blocks][2][heads]: one scale for a block's tokens in a head, >= 0 or NaN.
+ *   scales  float[blocks][2][heads]: one scale for a block's tokens in a head, >= 0 or NaN
+ *           (attention may take one below 2^-103, less than kv8_write makes, for 0).
  * A code c stands for (c - 128) * scale.
  *   tokens 16, 32, 64 or 128;  dim 64 or 128;  1 <= heads <= 1024;  blocks >= 1 with
  *   blocks * 2 * heads * tokens < 2^31.  Else TQ2_ESHAPE.
@@ -716,7 +717,8 @@ TQ2_API tq2_status kv8_read(const kv8_cache* c, const kv8_batch* b, void* k, int
  *           elements from row to row and from head to head.  out must not overlap q. Rows of no
  *           sequence are left as they are, in lse too.
  *   lse     DEVICE float[T][Hq] or NULL.
- *   Hq      a multiple of heads, T * Hq < 2^31.  Else TQ2_ESHAPE.
+ *   Hq      a multiple of heads, T * Hq < 2^31, and fewer than 2^38 tiles of 128 rows (T * Hq / heads)
+ *           by 128 tokens of the tables.  Else TQ2_ESHAPE.
  *   scale   finite;  causal 0 or 1;  window >= 0, 0 unless causal.  Else TQ2_EINVAL.
  *   max_q   a bound of the sequences' rows that the choice of kernels goes by (0: T); results
  *           of longer ones are right too, but slower.

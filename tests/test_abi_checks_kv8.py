@@ -97,3 +97,10 @@ def test_binding_refuses_what_does_not_fit(bpw):
         bpw.KV8Batch(table[0], offsets, lens)
     with pytest.raises(ValueError, match="on the GPU"):
         bpw.KV8Batch(table, offsets, lens)
+
+
+def test_sizes_whose_products_pass_64_bits_are_refused(bpw):
+    """Tables of 2^30 tokens for 2^31 - 1 sequences, and rows near 2^31."""
+    c, b = structs(bpw, heads=1024, blocks=1, tokens=16, width=1 << 26, ld=1 << 26, seqs=(1 << 31) - 1)
+    assert call(bpw, "attention", c, b, T=(1 << 20) - 1, Hq=2048) == TQ2_ESHAPE
+    assert "too many" in bpw.load().tq2_last_error().decode()
