@@ -14,7 +14,7 @@
 //
 // Bound: the bytes of the codes (64 tokens of up to 8192, 8 heads of 128, G = 4, bf16: 104 us, 5.0 TB/s or 75 % of the
 // measured copy; 400 warp instructions for 16 tokens' 4 KB keep the issue slots 42 % busy).  One sequence of
-// 131072 tokens, 4 heads: 41 us, 31 of them here and the rest in the join of 76 pieces a head.
+// 131072 tokens, 4 heads: 38 us, 31 of them here and the rest in the join of 76 pieces a head.
 // A CTA walks chunks of 64 tokens; all chunks of all sequences and heads are cut over the CTAs by what they cost, so a
 // ragged batch or one long sequence fills the GPU alike.  What a cut divides is joined by a second
 // kernel in the order of the tokens.  TMA brings the chunks into a ring (keys and values of
@@ -551,7 +551,14 @@ cudaError_t run(const Kv8Attention& a, void* scratch, cudaStream_t st) {
     g_launched.store(true, std::memory_order_release);
     e = launch_pdl(kv8_stream_kernel<T, D, SPLIT>, dim3(grid), dim3(THREADS), sizeof(Shared<D>), st, a, parts, joints);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kv8_join_kernel<T, D, RM, 4>, dim3(grid, RM / 2), dim3(KV8_JOIN_WARPS * 32), 0, st, a, (const float*)parts, (const Kv8Joint*)joints);
+    // Few tiles of rows leave each of them many pieces: eight warps a row (one sequence of 131072 tokens, 4 heads: 45 us
+    // with four, 41 with eight; 64 sequences of up to 8192, 8 heads: 105 and 108).
+    const int64_t tiles = (int64_t)a.c.seqs * a.c.H * (((int64_t)a.c.T * a.G + RM - 1) / RM);
+    const Kv8Joint* j = joints;
+    const float* p = parts;
+    if (tiles <= grid / 16)
+        return launch_pdl(kv8_join_kernel<T, D, RM, 8>, dim3(grid, RM), dim3(KV8_JOIN_WARPS * 32), 0, st, a, p, j);
+    return launch_pdl(kv8_join_kernel<T, D, RM, 4>, dim3(grid, RM / 2), dim3(KV8_JOIN_WARPS * 32), 0, st, a, p, j);
 }
 
 template <class T, bool SPLIT>
