@@ -7,7 +7,7 @@ library is missing or fails to load, every call raises.
 
 Tensors must live on the current CUDA device, be contiguous and have the
 dtype the C ABI states (float32 for activations and outputs, uint8 / int16
-bit patterns for packed data).  The ``q4_`` and ``moe_`` calls also take
+bit patterns for packed data).  The ``q4_``, ``moe_`` and ``kv8_`` calls also take
 float16 and bfloat16 activations, and rows with a stride.
 """
 import ctypes
