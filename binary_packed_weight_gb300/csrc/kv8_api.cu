@@ -128,8 +128,8 @@ tq2_status kv8_attention(const kv8_cache* c, const kv8_batch* b, const void* q, 
     a.window = window < ((int64_t)1 << 30) ? (int)window : 0;  // no sequence is longer
     // Rows of a sequence (queries * G): few go the streaming way, many the tensor cores'.  Which sequences have how
     // many the host does not know, so where both may be there both kernels are launched, each for its own; but where the
-    // tables hold little, all go one way.  (8 sequences of 4096 tokens, 8 heads of 128, G = 4, bf16: 16 rows 25 us
-    // streaming and 42 on the tensor cores, 32 rows 37 / 43, 64 rows 62 / 44.  f32, passes of 8 rows: 34 / 61, 57 / 61,
+    // tables hold little, all go one way.  (8 sequences of 4096 tokens, 8 heads of 128, G = 4, bf16: 16 rows 24 us
+    // streaming and 42 on the tensor cores, 32 rows 37 / 43, 64 rows 62 / 44.  f32, passes of 8 rows: 34 / 60, 58 / 61,
     // 103 / 63.  The second pair of kernels costs 7 us; few rows' codes stream at 5 TB/s and pass the tensor
     // cores at half of that, so 32 MB are worth it.)
     const int64_t rows = (max_q && max_q < T ? max_q : T) * a.G;

@@ -12,14 +12,15 @@
 // two a row, are exact as well, f32 ones are two f16 parts (and so are their
 // weights), of which an MMA takes both as rows r and r + 8.  Sums are f32.
 //
-// Bound: the bytes of the codes (64 tokens of up to 8192, 8 heads of 128, G = 4, bf16: 104 us, 5.0 TB/s or 75 % of the
+// Bound: the bytes of the codes (64 tokens of up to 8192, 8 heads of 128, G = 4, bf16: 102.5 us, 5.1 TB/s or 76 % of the
 // measured copy; 400 warp instructions for 16 tokens' 4 KB keep the issue slots 42 % busy).  One sequence of
-// 131072 tokens, 4 heads: 38 us, 31 of them here and the rest in the join of 76 pieces a head.
+// 131072 tokens, 4 heads: 37 us, 31 of them here and the rest in the join of 76 pieces a head.
 // A CTA walks chunks of 64 tokens; all chunks of all sequences and heads are cut over the CTAs by what they cost, so a
 // ragged batch or one long sequence fills the GPU alike.  What a cut divides is joined by a second
 // kernel in the order of the tokens.  TMA brings the chunks into a ring (keys and values of
 // a chunk are swizzled rows, so that fragments are read without conflicts), four warps take 16
-// tokens of each; two CTAs an SM with four chunks ahead (three with three, and 128 registers: 107 us and 64).
+// tokens of each; two CTAs an SM with four chunks ahead (104 us and 53 when both were
+// measured; three with three, and 128 registers, 107 and 65, the first 149 where calls overlap).
 // The codes go from bytes into f16 pairs by a permutation under the exponent of 1024 and one subtraction.
 #include <type_traits>
 
@@ -38,8 +39,9 @@ constexpr int CTAS = 2;         // a SM
 // weights down to 2^-30 of it), set anew where a weight passes RAISE above it (2^15 is in f16's range).
 constexpr float HEAD = 6.f, RAISE = 14.f;
 // The cut counts a tile of rows as its chunks and so many more, which is about what queries and the closing sums
-// cost.  A cut through those is one at their start.
-constexpr int EXTRA = 2;
+// cost.  A cut through those is one at their start.  (1, 2, 3, 4: 64 sequences of up to 8192 tokens, 8 heads, G = 4, 110,
+// 105, 103, 103.5 us; 256 of 1024 91, 82, 78, 78; one of 131072 alike.)
+constexpr int EXTRA = 3;
 constexpr int LEAST = EXTRA + 1;                             // units of a CTA: no two cuts through the same EXTRA
 
 template <int D>
@@ -551,12 +553,14 @@ cudaError_t run(const Kv8Attention& a, void* scratch, cudaStream_t st) {
     g_launched.store(true, std::memory_order_release);
     e = launch_pdl(kv8_stream_kernel<T, D, SPLIT>, dim3(grid), dim3(THREADS), sizeof(Shared<D>), st, a, parts, joints);
     if (e != cudaSuccess) return e;
-    // Few tiles of rows leave each of them many pieces: eight warps a row (one sequence of 131072 tokens, 4 heads: 45 us
-    // with four, 41 with eight; 64 sequences of up to 8192, 8 heads: 105 and 108).
-    const int64_t tiles = (int64_t)a.c.seqs * a.c.H * (((int64_t)a.c.T * a.G + RM - 1) / RM);
+    // Few tiles of rows leave each of them many pieces: eight warps a row where a tile has twelve or more (4 heads of
+    // 128, G = 8, us with eight and four: 1 sequence of 131072 tokens 38 and 41, 4 of 32768 16 and 18.5, 8 of 16384
+    // 21 and 20; 64 of up to 8192, 8 heads, 108 and 105).  T counts the tokens of all sequences, each of which adds at
+    // most one tile that is part full.
+    const int64_t tiles = (int64_t)a.c.H * ((int64_t)a.c.T * a.G / RM + a.c.seqs);
     const Kv8Joint* j = joints;
     const float* p = parts;
-    if (tiles <= grid / 16)
+    if (tiles <= grid / 12)
         return launch_pdl(kv8_join_kernel<T, D, RM, 8>, dim3(grid, RM), dim3(KV8_JOIN_WARPS * 32), 0, st, a, p, j);
     return launch_pdl(kv8_join_kernel<T, D, RM, 4>, dim3(grid, RM / 2), dim3(KV8_JOIN_WARPS * 32), 0, st, a, p, j);
 }
