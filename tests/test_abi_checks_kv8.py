@@ -75,6 +75,9 @@ def test_attention_options(bpw):
     for Hq in (0, 1, 3, -2):
         assert call(bpw, "attention", c, b, Hq=Hq) == TQ2_ESHAPE, Hq
     assert call(bpw, "attention", c, b, T=1 << 29, Hq=4) == TQ2_ESHAPE
+    one = structs(bpw, heads=1)                              # rows whose positions less a window pass 32 bits
+    assert call(bpw, "attention", *one, T=(1 << 30) + 1, Hq=1, window=(1 << 30) - 1) == TQ2_ESHAPE
+    assert "2^30" in bpw.load().tq2_last_error().decode()
     for options in (dict(scale=float("nan")), dict(scale=float("inf")), dict(causal=2), dict(causal=-1), dict(window=-1),
                     dict(window=3, causal=0), dict(max_q=-1)):
         assert call(bpw, "attention", c, b, **options) == TQ2_EINVAL, options
