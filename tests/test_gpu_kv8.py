@@ -296,6 +296,37 @@ def test_one_long_sequence(lib, dtype, D, G, L):
     assert np.array_equal(again[1], out) and np.array_equal(again[2], lse)
 
 
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("repeats", [1 << 17, (1 << 17) + 1])
+def test_tens_of_millions_of_tokens(lib, dtype, repeats):
+    """Tables of 2^24 tokens and one block more, all of them the same 128: their mean is the block's, the sum
+    `repeats` times it.  The longest chain of f32 additions is a CTA's: 3 tiles of rows (f32: 6) of 2^18 chunks over
+    300 CTAs, 5300, and the pieces, 300."""
+    import torch
+    rng = np.random.default_rng(50)
+    c = Cache(lib, rng, [128], [3], H=1, D=64, B=128)
+    table = torch.full((1, repeats), int(c.table[0, 0]), dtype=torch.int32, device="cuda")
+    c.batch = lib.KV8Batch(table, c.d["offsets"], torch.tensor([repeats * 128], dtype=torch.int32, device="cuda"))
+    q, out, lse = c.attend(queries(rng, 3, 16, 64), dtype, causal=False)
+    check_attention(out, lse - np.log(repeats), attention_of(c, q, causal=False), dtype, 64, 16 * 5600)
+
+
+def test_rows_far_apart_in_a_long_list(lib):
+    """Two prompts with 2^18 sequences without rows between them."""
+    import torch
+    rng = np.random.default_rng(51)
+    S = (1 << 18) + 2
+    c = Cache(lib, rng, [90, 70], [40, 50], H=1, D=64, B=16)
+    table = torch.full((S, c.table.shape[1]), -1, dtype=torch.int32, device="cuda")
+    table[0], table[-1] = c.d["table"][0], c.d["table"][1]
+    offsets = torch.full((S + 1,), 40, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(S, dtype=torch.int32, device="cuda")
+    offsets[0], offsets[-1], lens[0], lens[-1] = 0, 90, 90, 70
+    c.batch = lib.KV8Batch(table, offsets, lens)
+    q, out, lse = c.attend(queries(rng, c.T, 2, 64), "bfloat16")
+    check_attention(out, lse, attention_of(c, q), "bfloat16", 64, 90)
+
+
 @pytest.mark.parametrize("n", [100, 257, 1000])
 def test_prompt_rows_match_decoded_ones(lib, n):
     """Row i of a prompt is what a lone token at its position gets, within both results' bounds."""
