@@ -446,11 +446,13 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
                     const uint32_t b1[4] = {kv8_pair<0>(l23), kv8_pair<2>(l23), kv8_pair<0>(h23), kv8_pair<2>(h23)};
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
-                        mma_16816_pure(acc[4 * x + y], pf, b0[y], b1[y]);
-                        if (TWO) mma_16816_pure(acc[4 * x + y], pl, b0[y], b1[y]);
+                        // (volatile, as the fence is: the values are used up before their stage goes)
+                        mma_16816(acc[4 * x + y], pf, b0[y], b1[y], acc[4 * x + y]);
+                        if (TWO) mma_16816(acc[4 * x + y], pl, b0[y], b1[y], acc[4 * x + y]);
                     }
                 }
             }
+            fence_proxy_async_shared();                      // the stage is refilled through the async proxy
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.empty[stage]);
             if (++stage == STAGES) stage = 0, phase ^= 1;
