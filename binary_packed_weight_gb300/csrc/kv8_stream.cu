@@ -201,6 +201,7 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
                     if (block < 0) sm.scales[stage][lane] = make_float2(0.f, -1.f);
                 }
                 const uint32_t here = __ballot_sync(0xffffffffu, block >= 0);
+                __syncwarp();                                // the ordinary stores are lane 0's to release
                 if (lane == 0)
                     mbar_arrive_expect_tx(&sm.full[stage], __popc(here) * 2u * (uint32_t)(rows_piece * D));
                 if (block >= 0) {

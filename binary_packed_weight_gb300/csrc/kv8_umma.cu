@@ -601,10 +601,6 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                         ok = false;
                         break;
                     }
-                    if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[st], __popc(here) * (uint32_t)(rows_piece * D));
-                    if (block >= 0)
-                        tma_load_2d(sm.raw[st] + lane * rows_piece * D, &a.map, &sm.raw_full[st], 0,
-                                    (int)(kv8_row(a.c, block, kv, w.head) + inside));
                     if (kv == 0) {
                         float2* sc = &sm.scales[g & (CONS - 1)][lane & 7];
                         if (block >= 0) {
@@ -615,6 +611,11 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                             *sc = make_float2(0.f, -1.f);
                         }
                     }
+                    __syncwarp();                            // the ordinary stores are lane 0's to release
+                    if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[st], __popc(here) * (uint32_t)(rows_piece * D));
+                    if (block >= 0)
+                        tma_load_2d(sm.raw[st] + lane * rows_piece * D, &a.map, &sm.raw_full[st], 0,
+                                    (int)(kv8_row(a.c, block, kv, w.head) + inside));
                     cp_async_arrive(&sm.raw_full[st]);
                     if (++st == F::RAW) st = 0, ph ^= 1, wrapped = true;
                 }

@@ -31,3 +31,18 @@ def test_rings_that_go_round_many_times(lib, dtype, n, D, B):
     for _ in range(8):
         again = c.attend(q, dtype, max_q=n)
         assert np.array_equal(again[1], out) and np.array_equal(again[2], lse)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("n", [1, 90])
+def test_blocks_that_come_and_go(lib, dtype, n):
+    """Slots of the rings hold a block, then none, then one again: what is not there is never taken for what was."""
+    rng = np.random.default_rng(71)
+    c = Cache(lib, rng, [3000, 2000, 2500], [n] * 3, H=2, D=64, B=16)
+    c.table[rng.random(c.table.shape) < 0.4] = -1
+    c.upload()
+    q, out, lse = c.attend(queries(rng, c.T, 4, 64), dtype)
+    check_attention(out, lse, attention_of(c, q), dtype, 64, 3000)
+    for _ in range(8):
+        again = c.attend(q, dtype)
+        assert np.array_equal(again[1], out) and np.array_equal(again[2], lse)
