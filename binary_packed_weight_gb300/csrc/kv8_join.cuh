@@ -59,6 +59,13 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// A wait of a whole warp: where it runs out, or another role has given up, all lanes learn so and the other roles are told.
+__device__ __forceinline__ bool kv8_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, bool spin) {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, abort_flag, spin));
+    if (!ok) *abort_flag = 1;
+    return ok;
+}
+
 __device__ __forceinline__ float kv8_none() { return __int_as_float(0xff800000); }
 
 // Where row r of a sequence's head goes in out; its place in lse.

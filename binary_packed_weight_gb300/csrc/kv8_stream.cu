@@ -186,8 +186,7 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
             const int run = take - (at ? 0 : EXTRA), ch = at ? at - EXTRA : 0;
             const int from = a.window ? max(w.q.len - w.q.n - a.window + 1, 0) : 0;
             for (int i = 0; i < run; ++i) {
-                if (!mbar_wait_or_abort(&sm.empty[stage], phase ^ 1, &sm.abort)) {
-                    sm.abort = 1;
+                if (!kv8_wait(&sm.empty[stage], phase ^ 1, &sm.abort, false)) {
                     // copies in flight end before the shared memory goes
                     for (int u = 0; u < STAGES; ++u) {
                         if (u < stage || issued) mbar_wait(&sm.full[u], u < stage ? phase : phase ^ 1);
@@ -311,11 +310,8 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
         float m[2] = {NONE, NONE}, l[2] = {0.f, 0.f};
 
         for (int i = 0; i < run && ok; ++i) {
-            ok = mbar_wait_or_abort(&sm.full[stage], phase, &sm.abort);
-            if (!ok) {
-                sm.abort = 1;
-                break;
-            }
+            ok = kv8_wait(&sm.full[stage], phase, &sm.abort, false);
+            if (!ok) break;
             const int token = (w.first + ch + i) * CT + warp * 16;
             const float2 sc = sm.scales[stage][(warp * 16) / rows_piece];
             if (!(sc.y < 0.f) && token < any_hi && token + 16 > any_lo) {

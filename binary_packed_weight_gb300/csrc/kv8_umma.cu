@@ -529,10 +529,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
     uint32_t pieces_seen = 0;
     auto next_piece = [&](Piece& w) {
         const int slot = pieces_seen & (PIECES - 1);
-        if (!mbar_wait_or_abort(&sm.piece_full[slot], pieces_seen / PIECES & 1, abort_flag, true)) {
-            sm.abort = 1;
-            return false;
-        }
+        if (!kv8_wait(&sm.piece_full[slot], pieces_seen / PIECES & 1, abort_flag, true)) return false;
         w = sm.pieces[slot];
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.piece_empty[slot]);
@@ -549,8 +546,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
         Kv8Joint joint{0, 0, 0, 0};
         for (uint32_t i = 0;; ++i) {
             const int slot = i & (PIECES - 1);
-            if (!mbar_wait_or_abort(&sm.piece_empty[slot], (i / PIECES & 1) ^ 1, abort_flag, true)) {
-                sm.abort = 1;
+            if (!kv8_wait(&sm.piece_empty[slot], (i / PIECES & 1) ^ 1, abort_flag, true)) {
                 joint.pieces = 0;
                 break;
             }
@@ -596,8 +592,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                 const int inside = token & ((1 << logB) - 1);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    if (!mbar_wait_or_abort(&sm.raw_empty[st], ph ^ 1, abort_flag, true)) {
-                        sm.abort = 1;
+                    if (!kv8_wait(&sm.raw_empty[st], ph ^ 1, abort_flag, true)) {
                         ok = false;
                         break;
                     }
@@ -630,12 +625,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
         uint32_t q_ph = 0, p_ph = 0;                         // a bit a group
         uint32_t g = 0;                                      // tiles
         bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-            // (a vote: what follows is the same in the whole warp, and known to be)
-            ok = __all_sync(0xffffffffu, ok && mbar_wait_or_abort(bar, parity, abort_flag, true));
-            if (!ok) sm.abort = 1;
-            return ok;
-        };
+        auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = ok && kv8_wait(bar, parity, abort_flag, true); };
         Piece w;
         while (ok && __any_sync(0xffffffffu, next_piece(w))) {
             const int nq = __shfl_sync(0xffffffffu, w.rows - w.tile * ROWS > 128 ? F::NQ : 1, 0);
@@ -696,9 +686,8 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
 #pragma unroll 1
             for (int kv = 0; kv < 2; ++kv) {
                 const int buf = (2 * g & 3) + kv;
-                if (!mbar_wait_or_abort(&sm.raw_full[st], ph, abort_flag, true) ||
-                    !mbar_wait_or_abort(&sm.kv_empty[buf], (g >> 1 & 1) ^ 1, abort_flag, true)) {
-                    sm.abort = 1;
+                if (!kv8_wait(&sm.raw_full[st], ph, abort_flag, true) ||
+                    !kv8_wait(&sm.kv_empty[buf], (g >> 1 & 1) ^ 1, abort_flag, true)) {
                     ok = false;
                     break;
                 }
@@ -713,8 +702,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.cons_full[slot]);
-                } else if (kv && !mbar_wait_or_abort(&sm.cons_full[slot], g / CONS & 1, abort_flag, true)) {
-                    sm.abort = 1;
+                } else if (kv && !kv8_wait(&sm.cons_full[slot], g / CONS & 1, abort_flag, true)) {
                     ok = false;
                     break;
                 }
@@ -779,10 +767,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
             if (more) power = load_queries<T, D>(a, sm, w, qi, warp & 3, lane);
             if (have) {
                 // ---- a row's result, or its part of one
-                if (!mbar_wait_or_abort(&sm.o_full[qi], o_ph, abort_flag, true)) {
-                    sm.abort = 1;
-                    break;
-                }
+                if (!kv8_wait(&sm.o_full[qi], o_ph, abort_flag, true)) break;
                 o_ph ^= 1;
                 tc_fence_after();
                 const int pr = qi * 128 + row;
@@ -816,9 +801,8 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
             for (int i = 0; i < w.run; ++i, ++g) {
                 const int base = (w.first + i) * KT, slot = g & (CONS - 1);
                 // (scores that are there mean that the slot's phase is this tile's)
-                if (!mbar_wait_or_abort(&sm.s_full[qi], s_ph, abort_flag, true) ||
-                    !mbar_wait_or_abort(&sm.cons_full[slot], g / CONS & 1, abort_flag, true)) {
-                    sm.abort = 1;
+                if (!kv8_wait(&sm.s_full[qi], s_ph, abort_flag, true) ||
+                    !kv8_wait(&sm.cons_full[slot], g / CONS & 1, abort_flag, true)) {
                     ok = false;
                     break;
                 }
