@@ -29,8 +29,15 @@ struct Kv8Joint {
     int s, head, tile, pieces;
 };
 
-// A part: R references m, R sums l, R rows of D sums.
-__host__ __device__ constexpr size_t kv8_part_floats(int rows, int D) { return (size_t)rows * (D + 2); }
+// A part: R references m of the values' sums, R sums l of the weights, R references n of those, R rows of D values' sums.
+__host__ __device__ constexpr size_t kv8_part_floats(int rows, int D) { return (size_t)rows * (D + 3); }
+
+// A row's values' sums, of 2^(s_t - m) v_t, and its weights' sum, of 2^(s_t - n), have references of their own: the first
+// follows the largest weight times scale, and what is far below it is dropped there, but not from the second,
+// whatever the scales are (blocks of zeros among large values; nothing but zeros, for a million tokens).  Where the
+// scales at hand are at least 2^(m - n - NEAR), one exponential serves both: what it flushes to
+// zero is below 2^(NEAR - 126) in the second, and it adds 2^(NEAR + RAISE) there at most.  Elsewhere the second has its own.
+constexpr float KV8_NEAR = 40.f, KV8_FAR = 0x1p40f;          // an exponent, and the factor
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -74,13 +81,13 @@ __device__ __forceinline__ int64_t kv8_out_row(const Kv8Attention& a, int q0, in
     *lse = (int64_t)token * a.c.H * a.G + h;
     return token * a.ot + h * a.oh;
 }
-__device__ __forceinline__ float kv8_lse(float m, float l) {
-    return l > 0.f || isnan(l) ? (log2f(l) + m) * 0.69314718055994531f : kv8_none();
+__device__ __forceinline__ float kv8_lse(float n, float l) {
+    return l > 0.f || isnan(l) ? (log2f(l) + n) * 0.69314718055994531f : kv8_none();
 }
 // Factor that takes sums of reference m to those of reference top; sums without a reference are 0 or NaN.
-__device__ __forceinline__ float kv8_factor(float m, float l, float top) {
-    return m == kv8_none() ? (l != 0.f ? 1.f : 0.f) : exp2_fast(m - top);
-}
+__device__ __forceinline__ float kv8_factor(float m, float top) { return m == kv8_none() ? 1.f : exp2_fast(m - top); }
+// What takes a row's values' sums to its result.
+__device__ __forceinline__ float kv8_inverse(float m, float n, float l) { return l == 0.f ? 0.f : exp2_fast(m - n) / l; }
 
 // The pieces' sums, each warp's in the order of the tokens and then those of the WPR warps that share a row: one
 // where a row has few pieces and there are many rows, several where one sequence was cut over the whole GPU.
@@ -103,20 +110,27 @@ kv8_join_kernel(const __grid_constant__ Kv8Attention a, const float* parts, cons
     for (int r0 = blockIdx.y * RPB; r0 < rows; r0 += gridDim.y * RPB) {
         const int r = r0 + warp / WPR;
         const bool live = r < rows;
-        float top = kv8_none(), sum = 0.f, o[PER];
+        float top = kv8_none(), top_n = kv8_none(), sum = 0.f, o[PER];
 #pragma unroll
         for (int c = 0; c < PER; ++c) o[c] = 0.f;
         if (live) {
-            for (int i = lane; i < j.pieces; i += 32) top = fmaxf(top, (i ? rest + i * 2 * PART : first)[r]);
+            for (int i = lane; i < j.pieces; i += 32) {
+                const float* p = i ? rest + i * 2 * PART : first;
+                top = fmaxf(top, p[r]);
+                top_n = fmaxf(top_n, p[2 * RM + r]);
+            }
 #pragma unroll
-            for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            for (int d = 16; d; d >>= 1) {
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                top_n = fmaxf(top_n, __shfl_xor_sync(0xffffffffu, top_n, d));
+            }
 #pragma unroll 8
             for (int i = share; i < j.pieces; i += WPR) {
                 const float* p = i ? rest + i * 2 * PART : first;
-                const float l = p[RM + r], f = kv8_factor(p[r], l, top);
-                sum = fmaf(l, f, sum);
+                const float f = kv8_factor(p[r], top);
+                sum = fmaf(p[RM + r], kv8_factor(p[2 * RM + r], top_n), sum);
 #pragma unroll
-                for (int c = 0; c < PER; ++c) o[c] = fmaf(p[2 * RM + r * D + lane + 32 * c], f, o[c]);
+                for (int c = 0; c < PER; ++c) o[c] = fmaf(p[3 * RM + r * D + lane + 32 * c], f, o[c]);
             }
         }
         if (WPR > 1) {
@@ -137,10 +151,10 @@ kv8_join_kernel(const __grid_constant__ Kv8Attention a, const float* parts, cons
         if (live && share == 0) {
             int64_t at_lse;
             T* dst = static_cast<T*>(a.out) + kv8_out_row(a, q.q0, j.head, j.tile * RM + r, &at_lse);
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const float inv = kv8_inverse(top, top_n, sum);
 #pragma unroll
             for (int c = 0; c < PER; ++c) dst[lane + 32 * c] = kv8_round<T>(o[c] * inv);
-            if (lane == 0 && a.lse) a.lse[at_lse] = kv8_lse(top, sum);
+            if (lane == 0 && a.lse) a.lse[at_lse] = kv8_lse(top_n, sum);
         }
     }
 }

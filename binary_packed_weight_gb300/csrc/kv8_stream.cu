@@ -4,10 +4,10 @@
 // Mathematics, per row r (a query token and one of its heads) and token t, with the
 // scales ks and vs of the token's block:
 //     w_t = scale log2(e) ks (q_r . c_t) + x_t,   x_t the exponent of vs = 2^x_t f_t
-//     out = sum_t 2^(w_t - m) f_t c'_t / l,  l = sum_t 2^(w_t - m) 2^-x_t
+//     out = 2^(m - n) sum_t 2^(w_t - m) f_t c'_t / l,  l = sum_t 2^(w_t - m) 2^(m - n - x_t)
 // so that what is rounded to f16 is the whole weight of a value code c': a block of large
-// values takes no bits from others that it does not outweigh.  m is a running reference
-// that follows the largest w in steps, so that few tokens rescale the sums.
+// values takes no bits from others that it does not outweigh.  m and n are running references
+// that follow the largest w and w - x in steps, so that few tokens rescale the sums.
 // The codes are whole numbers, exact in f16; f16 and bf16 queries, scaled by a power of
 // two a row, are exact as well, f32 ones are two f16 parts (and so are their
 // weights), of which an MMA takes both as rows r and r + 8.  Sums are f32.
@@ -50,7 +50,7 @@ struct __align__(1024) Shared {
     uint8_t v[STAGES][CT * D];
     uint4 q[D / 16][32];        // queries as MMA operands, by k step and lane
     float acc[WARPS][16 * (D / 2 + 4)];
-    float m[WARPS][16], l[WARPS][16];
+    float m[WARPS][16], l[WARPS][16], n[WARPS][16];
     float qa[16];               // what undoes a row's power of two
     float2 scales[STAGES][4];   // of keys and of values, by piece; values' -1: nothing there
     uint64_t full[STAGES], empty[STAGES];
@@ -307,7 +307,8 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
 #pragma unroll
         for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
         const float NONE = kv8_none();
-        float m[2] = {NONE, NONE}, l[2] = {0.f, 0.f};
+        float m[2] = {NONE, NONE}, l[2] = {0.f, 0.f}, n[2] = {NONE, NONE};
+        float ratio[2] = {0.f, 0.f};                         // 2^(m - n)
 
         for (int i = 0; i < run && ok; ++i) {
             ok = kv8_wait(&sm.full[stage], phase, &sm.abort, false);
@@ -362,31 +363,55 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
                 }
                 float t0 = fmaxf(fmaxf(e0[0], e0[1]), fmaxf(e0[2], e0[3]));
                 float t1 = SPLIT ? NONE : fmaxf(fmaxf(e1[0], e1[1]), fmaxf(e1[2], e1[3]));
-                if (__any_sync(0xffffffffu, t0 > m[0] + RAISE || t1 > m[1] + RAISE)) {
+                float unit[2] = {ratio[0] * down, ratio[1] * down};          // of a weight in l
+                if (__any_sync(0xffffffffu, t0 > m[0] + RAISE || t1 > m[1] + RAISE || fmaxf(unit[0], unit[1]) > KV8_FAR)) {
 #pragma unroll
                     for (int half = 0; half < HALVES; ++half) {
-                        float t = half ? t1 : t0;
-                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-                        if (!(t > m[half] + RAISE)) continue;             // the same in a row's four lanes
-                        const float f = exp2_fast(m[half] - (t - HEAD));
-                        m[half] = t - HEAD;
-                        l[half] *= f;
+                        const auto top_of_row = [](float t) {             // the same in a row's four lanes
+                            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+                            return fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+                        };
+                        const auto follow = [&](float to) {
+                            if (to > n[half]) l[half] *= exp2_fast(n[half] - to), n[half] = to;
+                        };
+                        const float t = top_of_row(half ? t1 : t0);
+                        if (t > m[half] + RAISE) {
+                            const float f = exp2_fast(m[half] - (t - HEAD));
+                            m[half] = t - HEAD;
+                            follow(m[half] - fex);
 #pragma unroll
-                        for (int c = 0; c < NT; ++c) {
-                            acc[c][2 * half] *= f;
-                            acc[c][2 * half + 1] *= f;
-                            if (SPLIT) {
-                                acc[c][2] *= f;
-                                acc[c][3] *= f;
+                            for (int c = 0; c < NT; ++c) {
+                                acc[c][2 * half] *= f;
+                                acc[c][2 * half + 1] *= f;
+                                if (SPLIT) {
+                                    acc[c][2] *= f;
+                                    acc[c][3] *= f;
+                                }
                             }
                         }
+                        unit[half] = m[half] == NONE ? 0.f : exp2_fast(m[half] - n[half]) * down;
+                        if (__any_sync(0xffffffffu, unit[half] > KV8_FAR)) {
+                            float z[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const float* u = s[x >> 1];
+                                z[x] = SPLIT ? (u[x & 1] + u[2 + (x & 1)]) * a0 : u[2 * half + (x & 1)] * (half ? a1 : a0);
+                                if (!inside && (half ? e1 : e0)[x] == NONE) z[x] = NONE;
+                            }
+                            const float most = top_of_row(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
+                            if (most > n[half] + RAISE) follow(most - HEAD);
+                            const float ref = n[half] == NONE ? 0.f : n[half];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) l[half] += exp2_fast(z[x] - ref);
+                            unit[half] = 0.f;
+                        }
+                        ratio[half] = m[half] == NONE ? 0.f : exp2_fast(m[half] - n[half]);
                     }
                 }
                 uint32_t pf[4], pl[4];
                 {
                     const float m0 = m[0] == NONE ? 0.f : m[0];
-                    float sum = 0.f;
+                    float sum = 0.f;                         // (without a reference 0 or NaN)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         const bool dead = !inside && e0[x] == NONE;
@@ -394,7 +419,7 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
                         sum += e;
                         e0[x] = dead ? 0.f : e * frac;
                     }
-                    l[0] = fmaf(sum, down, l[0]);
+                    l[0] = fmaf(sum, unit[0], l[0]);
                     pf[0] = pack_half2(e0[0], e0[1]);
                     pf[2] = pack_half2(e0[2], e0[3]);
                     if (SPLIT) {
@@ -410,7 +435,7 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
                             sum1 += e;
                             e1[x] = dead ? 0.f : e * frac;
                         }
-                        l[1] = fmaf(sum1, down, l[1]);
+                        l[1] = fmaf(sum1, unit[1], l[1]);
                         pf[1] = pack_half2(e1[0], e1[1]);
                         pf[3] = pack_half2(e1[2], e1[3]);
                     }
@@ -463,6 +488,7 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
             if (t4 == 0) {
                 sm.m[warp][g + 8 * half] = m[half];
                 sm.l[warp][g + 8 * half] = l[half];
+                sm.n[warp][g + 8 * half] = n[half];
             }
         }
         const bool whole = run == w.count;
@@ -493,15 +519,15 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
             }
             for (int i = tid; i < rows * (D / 8); i += WARPS * 32) {
                 const int r = i / (D / 8), c = i % (D / 8) * 4, col = c / HN * NT + cols * HN + c % HN;
-                float top = sm.m[0][r];
+                float top = sm.m[0][r], top_n = sm.n[0][r];
 #pragma unroll
-                for (int k = 1; k < WARPS; ++k) top = fmaxf(top, sm.m[k][r]);
+                for (int k = 1; k < WARPS; ++k) top = fmaxf(top, sm.m[k][r]), top_n = fmaxf(top_n, sm.n[k][r]);
                 float sum = 0.f;
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < WARPS; ++k) {
-                    const float f = kv8_factor(sm.m[k][r], sm.l[k][r], top);
-                    sum = fmaf(sm.l[k][r], f, sum);
+                    const float f = kv8_factor(sm.m[k][r], top);
+                    sum = fmaf(sm.l[k][r], kv8_factor(sm.n[k][r], top_n), sum);
                     const float4 u = *reinterpret_cast<const float4*>(&sm.acc[k][r * LD + c]);
                     o.x = fmaf(u.x, f, o.x);
                     o.y = fmaf(u.y, f, o.y);
@@ -511,15 +537,15 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
                 if (whole) {
                     int64_t at_lse;
                     T* dst = static_cast<T*>(a.out) + kv8_out_row(a, w.q.q0, head, tile * RM + r, &at_lse) + col;
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    const float inv = kv8_inverse(top, top_n, sum);
                     dst[0] = kv8_round<T>(o.x * inv);
                     dst[1] = kv8_round<T>(o.y * inv);
                     dst[2] = kv8_round<T>(o.z * inv);
                     dst[3] = kv8_round<T>(o.w * inv);
-                    if (col == 0 && a.lse) a.lse[at_lse] = kv8_lse(top, sum);
+                    if (col == 0 && a.lse) a.lse[at_lse] = kv8_lse(top_n, sum);
                 } else {
-                    *reinterpret_cast<float4*>(part + 2 * RM + r * D + col) = o;
-                    if (col == 0) part[r] = top, part[RM + r] = sum;
+                    *reinterpret_cast<float4*>(part + 3 * RM + r * D + col) = o;
+                    if (col == 0) part[r] = top, part[RM + r] = sum, part[2 * RM + r] = top_n;
                 }
             }
             named_sync();

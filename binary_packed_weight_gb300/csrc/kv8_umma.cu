@@ -3,8 +3,9 @@
 //
 // Mathematics: as the streaming path (kv8_stream.cu), with the whole weight
 // 2^(w_t - m), w_t = (scale log2(e) ks) (q . c) + log2 vs, in f16, and
-// l = sum 2^(w_t - m) / vs.  ks and vs are constant over 16 columns, so per score that is
-// half a packed multiply-add, one exponential and half a packed sum.
+// l = sum 2^(w_t - m) 2^x / vs, x the exponent of the first vs.  ks and vs are constant over 16 columns, so per score that is
+// half a packed multiply-add, one exponential and half a packed sum.  Where a vs is too far from 2^x for
+// that, a piece's weights have a sum (and exponentials) of their own from there on.
 //
 // A CTA takes 256 rows (f32: 128), a row being a query token and one of the heads
 // that share a head of the cache, over tiles of 128 tokens.  Warps: one brings packed
@@ -73,7 +74,8 @@ struct __align__(1024) Shared {
     uint8_t q[2][Form<T, D>::TILE];                          // by group (f32: by part)
     uint8_t kv[BUFS][Form<T, D>::TILE];
     uint8_t raw[Form<T, D>::RAW][KT * D];
-    float4 cons[CONS][KT / 16];                              // ks, log2 vs, 1 / vs; w: values count
+    float4 cons[CONS][KT / 16];                              // ks, log2 vs, 2^x / vs; w: values count
+    int near[CONS];                                          // 4 x, and 0: all vs of the piece so far are near it, 1: now not, 2: no more
     float2 scales[CONS][8];                                  // of keys and values, by piece; -1: nothing there
     uint64_t raw_full[Form<T, D>::RAW], raw_empty[Form<T, D>::RAW];
     uint64_t kv_full[BUFS], kv_empty[BUFS], cons_full[CONS];
@@ -195,6 +197,36 @@ __device__ __forceinline__ float tile_top(uint32_t s_addr, const float4* cons, f
         }
     }
     return t;
+}
+
+// The sum of a row's weights, with a reference n of their own.  The scores are as they came (raw), or the weights' exponents
+// with -Inf in columns that the row does not see.
+__device__ __forceinline__ void tile_sum(uint32_t s_addr, const float4* cons, float qa, bool raw, float& l, float& n) {
+    float top = kv8_none();
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {                   // their largest, then their sum
+        const float ref = n == kv8_none() ? 0.f : n;
+#pragma unroll 1
+        for (int c = 0; c < KT; c += 16) {
+            const float4 k = cons[c / 16];
+            if (k.y == kv8_none()) continue;
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(s_addr + c, v);
+            tmem_wait_ld();
+            const float ks = raw ? k.x * qa : 1.f, off = raw ? 0.f : -k.y;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float z = fmaf(__uint_as_float(v[e]), ks, off);
+                if (pass) l += exp2_fast(z - ref);
+                else top = fmaxf(top, z);
+            }
+        }
+        if (!pass && top > n + RAISE) {
+            l *= exp2_fast(n - (top - HEAD));
+            n = top - HEAD;
+        }
+        __syncwarp();
+    }
 }
 
 // Weights of 2 N tokens relative to a reference: f16 pairs (and what those leave), added to sum.
@@ -679,6 +711,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
         uint32_t ph = 0;
         bool ok = true;
         uint32_t g = 0;
+        int x = 0, far = 0;
         Piece w;
         while (ok && next_piece(w))
         for (int i = 0; ok && i < w.run; ++i, ++g) {
@@ -692,14 +725,23 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                     break;
                 }
                 if (kv == 0 && dw == 0) {
-                    if (lane < KT / 16) {
-                        const float2 sc = sm.scales[slot][lane * 16 / rows_piece];
-                        float4 c = make_float4(sc.x, log2f(sc.y), 1.f / sc.y, 1.f);
-                        if (isnan(sc.y)) c.z = 1.f;
-                        if (sc.y < TINY) c = make_float4(sc.x, -103.f, 0x1p103f, 0.f);   // values that are all zeros
-                        if (sc.y < 0.f) c = make_float4(0.f, kv8_none(), 1.f, 0.f);      // no block: nobody sees it
-                        sm.cons[slot][lane] = c;
+                    const int group = lane & (KT / 16 - 1);
+                    const float2 sc = sm.scales[slot][group * 16 / rows_piece];
+                    float4 c = make_float4(sc.x, log2f(sc.y), 1.f / sc.y, 1.f);
+                    if (isnan(sc.y)) c.z = 1.f;
+                    if (sc.y < TINY) c = make_float4(sc.x, -103.f, 0x1p103f, 0.f);       // values that are all zeros
+                    if (sc.y < 0.f) c = make_float4(0.f, kv8_none(), 1.f, 0.f);          // no block: nobody sees it
+                    if (i == 0) {
+                        float most = c.y;
+#pragma unroll
+                        for (int d = 1; d < KT / 16; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+                        x = most == kv8_none() ? 0 : (int)fminf(floorf(most), 127.f);
+                        far = 0;
                     }
+                    far = far ? 2 : __any_sync(0xffffffffu, c.y != kv8_none() && fabsf(c.y - x) > KV8_NEAR);
+                    c.z *= exp2_fast((float)x);
+                    if (lane < KT / 16) sm.cons[slot][lane] = c;
+                    if (lane == 0) sm.near[slot] = 4 * x + far;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.cons_full[slot]);
                 } else if (kv && !kv8_wait(&sm.cons_full[slot], g / CONS & 1, abort_flag, true)) {
@@ -754,6 +796,8 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
         const float NONE = kv8_none();
         // of the piece at hand
         float m = NONE, l = 0.f;
+        float own[2] = {0.f, 0.f};                           // l and n once they are apart
+        int near = 0;
         bool whole = false, live = false;
         T* out = nullptr;
         float* part = nullptr;
@@ -771,12 +815,14 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                 o_ph ^= 1;
                 tc_fence_after();
                 const int pr = qi * 128 + row;
+                float n = m - (near >> 2);
+                if (near & 3) l = own[0], n = own[1];
                 if (whole) {
-                    store_row<T, D>(o_addr, live, l == 0.f ? 0.f : 1.f / l, out);
-                    if (live && a.lse) a.lse[at_lse] = kv8_lse(m, l);
+                    store_row<T, D>(o_addr, live, kv8_inverse(m, n, l), out);
+                    if (live && a.lse) a.lse[at_lse] = kv8_lse(n, l);
                 } else {
-                    store_row<float, D>(o_addr, live, 1.f, part + 2 * ROWS + (size_t)pr * D);
-                    if (live) part[pr] = m, part[ROWS + pr] = l;
+                    store_row<float, D>(o_addr, live, 1.f, part + 3 * ROWS + (size_t)pr * D);
+                    if (live) part[pr] = m, part[ROWS + pr] = l, part[2 * ROWS + pr] = n;
                 }
                 tc_fence_before();
             }
@@ -809,11 +855,17 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                 s_ph ^= 1;
                 tc_fence_after();
                 const float4* cons = sm.cons[slot];
+                near = sm.near[slot];
                 const bool inside = base >= safe_lo && base + KT <= safe_hi;
                 const int lo = row_lo - base, hi = row_hi - base;
                 const float t = inside ? tile_top(s_addr, cons, qa) : tile_top_some(s_addr, cons, qa, lo, hi);
                 const bool raise = t > m + RAISE;
-                if (__any_sync(0xffffffffu, raise)) {
+                if (__builtin_expect(__any_sync(0xffffffffu, raise || near & 3), 0)) {
+                    if (__builtin_expect(near & 3, 0)) {
+                        float sum = near & 1 ? l : own[0], n = near & 1 ? m - (near >> 2) : own[1];
+                        tile_sum(s_addr, cons, qa, inside, sum, n);
+                        own[0] = sum, own[1] = n;            // (l is of no use from here on)
+                    }
                     const float now = raise ? t - HEAD : m;
                     const float f = raise ? exp2_fast(m - now) : 1.f;
                     m = now;

@@ -46,3 +46,88 @@ def test_blocks_that_come_and_go(lib, dtype, n):
     for _ in range(8):
         again = c.attend(q, dtype)
         assert np.array_equal(again[1], out) and np.array_equal(again[2], lse)
+
+
+# -------------------------------------------------- scales of values at the ends ----
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("n", [1, 12])
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -103, 2.0 ** -60])
+def test_values_of_zeros_at_length(lib, dtype, n, scale):
+    """A million tokens whose values are (about) zeros: their weights add up like any others'.  The longest chain of
+    additions is that of test_tens_of_millions_of_tokens, 16 times shorter."""
+    import torch
+    rng = np.random.default_rng(72)
+    c = Cache(lib, rng, [128], [n], H=1, D=64, B=128)
+    c.scales[:, 1] = scale
+    c.upload()
+    blocks = 1 << 13                                          # all of them the same 128 tokens
+    c.batch = lib.KV8Batch(c.d["table"].repeat(1, blocks), c.d["offsets"], c.d["lens"] * blocks)
+    q, out, lse = c.attend(queries(rng, n, 4, 64) * 0.01, dtype, causal=False)    # of about the same weight
+    check_attention(out, lse - np.log(blocks), attention_of(c, q, causal=False), dtype, 64, 16 * 5600)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("G", [1, 40])
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -103, 2.0 ** -20])
+def test_weights_that_rise_within_one_piece(lib, dtype, G, scale):
+    """Sequences of 12800 tokens, one for every place that works at once; the first 128 tokens weigh 2^7.8 times less."""
+    import torch
+    rng = np.random.default_rng(73)
+    S, blocks, D = 304, 100, 64
+    c = Cache(lib, rng, [256], [1], H=1, D=D, B=128)
+    first, rest = c.table[0]
+    c.codes[:] = 128
+    c.codes[rest, 0, 0, :, 0] = 228
+    c.codes[:, 1] = rng.integers(1, 256, c.codes[:, 1].shape)
+    c.scales[:, 0], c.scales[:, 1] = 0.054, scale
+    c.upload()
+    table = torch.full((S, blocks), int(rest), dtype=torch.int32, device="cuda")
+    table[:, 0] = int(first)
+    c.batch = lib.KV8Batch(table, torch.arange(S + 1, dtype=torch.int32, device="cuda"),
+                           torch.full((S,), 128 * blocks, dtype=torch.int32, device="cuda"))
+    q = np.zeros((S, G, D))
+    q[:, :, 0] = 1.0
+    q, out, lse = c.attend(q, dtype, scale=1.0)
+    c.table, c.lens = table[:1].cpu().numpy(), np.array([128 * blocks], np.int32)
+    c.offsets = np.array([0, 1], np.int32)
+    want = attention_of(c, q[:1], scale=1.0)
+    for s in (0, 150, 303):
+        check_attention(out[s:s + 1], lse[s:s + 1], want, dtype, D, 128 * blocks)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("small,large", [(0.0, 28), (0.0, 31), (0.0, 60), (0.0, 100), (-60, 60), (-100, 100), (-103, 120)])
+def test_value_scales_at_both_ends(lib, dtype, n, small, large):
+    """Blocks of the smallest and of the largest values in one row, in every order: a weight counts in the sum whatever
+    its value's scale is."""
+    rng = np.random.default_rng(74)
+    lens = [96 + n] * 4
+    c = Cache(lib, rng, lens, [n] * 4, H=1, D=64, B=16)
+    c.scales[:, 0] = 0.01
+    for s, blocks in enumerate(([0, 1, 4], [3, 5], [5], [1, 2, 3, 4, 5])):   # those of large values
+        c.scales[c.table[s], 1] = small and 2.0 ** small
+        c.scales[c.table[s, blocks], 1] = 2.0 ** large
+    c.upload()
+    q, out, lse = c.attend(queries(rng, c.T, 2, 64), dtype)
+    check_attention(out, lse, attention_of(c, q), dtype, 64, max(lens))
+    for options in ({"window": 40}, {"causal": False}):
+        q, out, lse = c.attend(queries(rng, c.T, 2, 64), dtype, **options)
+        check_attention(out, lse, attention_of(c, q, **options), dtype, 64, max(lens))
+
+
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("n", [1, 70])
+@pytest.mark.parametrize("exponents", [(None, 0), (None, 0, 45), (None, 0, -60, -90)])
+def test_blocks_of_zeros_among_others_at_length(lib, dtype, n, exponents):
+    """Long sequences over many pieces in which blocks of zeros, small and large values follow in no order."""
+    rng = np.random.default_rng(80)
+    c = Cache(lib, rng, [3000, 2500, 129], [n] * 3, H=2, D=64, B=16)
+    kind = rng.integers(0, len(exponents), c.scales[:, 1].shape)
+    c.scales[:, 1] *= np.array([0.0 if e is None else 2.0 ** e for e in exponents], np.float32)[kind]
+    if dtype == "float16":
+        c.scales[:, 1] = np.minimum(c.scales[:, 1], 400.0)    # (results within the type)
+    c.upload()
+    for options in ({}, {"window": 700}):
+        q, out, lse = c.attend(queries(rng, c.T, 4, 64), dtype, **options)
+        check_attention(out, lse, attention_of(c, q, **options), dtype, 64, 3000)
