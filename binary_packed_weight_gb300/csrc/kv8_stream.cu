@@ -22,6 +22,7 @@
 // tokens of each; two CTAs an SM with four chunks ahead (104 us and 53 when both were
 // measured; three with three, and 128 registers, 107 and 65, the first 149 where calls overlap).
 // The codes go from bytes into f16 pairs by a permutation under the exponent of 1024 and one subtraction.
+#include <cfloat>
 #include <type_traits>
 
 #include "kv8_join.cuh"
@@ -339,10 +340,11 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
                     }
                 }
                 // ---- weights
-                const uint32_t vb = __float_as_uint(fmaxf(sc.y, 0x1p-103f));
+                const bool number = sc.y <= FLT_MAX;         // (values that are none leave NaN in the sums of values alone)
+                const uint32_t vb = __float_as_uint(number ? fmaxf(sc.y, 0x1p-103f) : 1.f);
                 const int ex = min((int)(vb >> 23) - 127, 126);
                 const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-                const float frac = sc.y * down;              // (of a NaN scale NaN, of 0 zero)
+                const float frac = number ? sc.y * down : __int_as_float(0x7fffffff);
                 const float a0 = sc.x * qa[0], a1 = sc.x * qa[1], fex = (float)ex;
                 float e0[4], e1[4];                          // rows g and g + 8 (SPLIT: e0 alone)
 #pragma unroll

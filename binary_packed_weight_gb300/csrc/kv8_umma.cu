@@ -27,6 +27,7 @@
 // 1700 of softmax beside the other group's and the decoders), and the operands' reads, the decoders' and the copies
 // want shared memory for 2500 of the 4000.  What the instruction cache does not hold costs time in every
 // role, so code that runs once a tile is kept in short loops, and what runs once a piece is read from one list.
+#include <cfloat>
 #include <type_traits>
 
 #include "kv8_join.cuh"
@@ -74,7 +75,7 @@ struct __align__(1024) Shared {
     uint8_t q[2][Form<T, D>::TILE];                          // by group (f32: by part)
     uint8_t kv[BUFS][Form<T, D>::TILE];
     uint8_t raw[Form<T, D>::RAW][KT * D];
-    float4 cons[CONS][KT / 16];                              // ks, log2 vs, 2^x / vs; w: values count
+    float4 cons[CONS][KT / 16];                              // ks, log2 vs, 2^x / vs; w: values count (NaN: are no numbers)
     int near[CONS];                                          // 4 x, and 0: all vs of the piece so far are near it, 1: now not, 2: no more
     float2 scales[CONS][8];                                  // of keys and values, by piece; -1: nothing there
     uint64_t raw_full[Form<T, D>::RAW], raw_empty[Form<T, D>::RAW];
@@ -227,6 +228,22 @@ __device__ __forceinline__ void tile_sum(uint32_t s_addr, const float4* cons, fl
         }
         __syncwarp();
     }
+}
+
+// NaN in place of the weights' exponents of seen tokens whose values are no numbers (raw: of all of them).
+__device__ __forceinline__ void tile_poison(uint32_t s_addr, const float4* cons, bool raw) {
+#pragma unroll 1
+    for (int c = 0; c < KT; c += 16) {
+        if (!isnan(cons[c / 16].w)) continue;
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(s_addr + c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (raw || __uint_as_float(v[e]) != kv8_none()) v[e] = 0x7fffffffu;
+        tmem_st_32x32b_x16(s_addr + c, v);
+    }
+    tmem_wait_st();
 }
 
 // Weights of 2 N tokens relative to a reference: f16 pairs (and what those leave), added to sum.
@@ -728,7 +745,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                     const int group = lane & (KT / 16 - 1);
                     const float2 sc = sm.scales[slot][group * 16 / rows_piece];
                     float4 c = make_float4(sc.x, log2f(sc.y), 1.f / sc.y, 1.f);
-                    if (isnan(sc.y)) c.z = 1.f;
+                    if (!(sc.y <= FLT_MAX)) c = make_float4(sc.x, 0.f, 1.f, __int_as_float(0x7fffffff));   // NaN, Inf
                     if (sc.y < TINY) c = make_float4(sc.x, -103.f, 0x1p103f, 0.f);       // values that are all zeros
                     if (sc.y < 0.f) c = make_float4(0.f, kv8_none(), 1.f, 0.f);          // no block: nobody sees it
                     if (i == 0) {
@@ -738,7 +755,8 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                         x = most == kv8_none() ? 0 : (int)fminf(floorf(most), 127.f);
                         far = 0;
                     }
-                    far = far ? 2 : __any_sync(0xffffffffu, c.y != kv8_none() && fabsf(c.y - x) > KV8_NEAR);
+                    // (the sums of a tile with values that are no numbers go apart too)
+                    far = far ? 2 : __any_sync(0xffffffffu, c.y != kv8_none() && !(fabsf(c.y - x) <= KV8_NEAR && c.w <= 1.f));
                     c.z *= exp2_fast((float)x);
                     if (lane < KT / 16) sm.cons[slot][lane] = c;
                     if (lane == 0) sm.near[slot] = 4 * x + far;
@@ -865,6 +883,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                         float sum = near & 1 ? l : own[0], n = near & 1 ? m - (near >> 2) : own[1];
                         tile_sum(s_addr, cons, qa, inside, sum, n);
                         own[0] = sum, own[1] = n;            // (l is of no use from here on)
+                        tile_poison(s_addr, cons, inside);
                     }
                     const float now = raise ? t - HEAD : m;
                     const float f = raise ? exp2_fast(m - now) : 1.f;

@@ -636,7 +636,7 @@ TQ2_API tq2_status moe_experts(q4_handle gate, q4_handle up, q4_handle down, con
  * The cache: a pool of blocks of `tokens` tokens, in the caller's DEVICE memory.
  *   codes   uint8[blocks][2][heads][tokens][dim] (keys, then values), 16-byte aligned.
  *   scales  float[blocks][2][heads]: one scale for a block's tokens in a head, >= 0 or NaN
- *           (attention may take one below 2^-103, less than kv8_write makes, for 0).
+ *           (attention may take one below 2^-103, less than kv8_write makes, for 0, and takes Inf for NaN).
  * A code c stands for (c - 128) * scale.
  *   tokens 16, 32, 64 or 128;  dim 64 or 128;  1 <= heads <= 1024;  blocks >= 1 with
  *   blocks * 2 * heads * tokens < 2^31.  Else TQ2_ESHAPE.
@@ -727,7 +727,7 @@ TQ2_API tq2_status kv8_read(const kv8_cache* c, const kv8_batch* b, void* k, int
  * largest.  A token's weight times its block's scale is rounded to f16 for bf16 results (2^-11), to two
  * f16 parts for f16 and f32 ones (2^-22), and to 2^-30 of the row's largest at the least.  Sums
  * are f32, results rounded once.  A row of q with NaN or Inf gives NaN in its own row alone; a NaN scale reaches the rows
- * that see a token of its block.  The order of additions depends on lengths, shapes and the
+ * that see a token of its block: out, and lse where it is the keys'.  The order of additions depends on lengths, shapes and the
  * GPU alone, so results are the same from run to run.  Asynchronous; scratch from the
  * library's stream-ordered pool.
  */

@@ -131,3 +131,30 @@ def test_blocks_of_zeros_among_others_at_length(lib, dtype, n, exponents):
     for options in ({}, {"window": 700}):
         q, out, lse = c.attend(queries(rng, c.T, 4, 64), dtype, **options)
         check_attention(out, lse, attention_of(c, q, **options), dtype, 64, 3000)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("n", [1, 3, 150])
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_values_that_are_no_numbers_leave_the_sum(lib, dtype, n, bad):
+    """A scale of the values alone that is no number (Inf counts as none): rows that see a token of its block have NaN
+    in out; lse does not depend on values."""
+    rng = np.random.default_rng(75)
+    c = Cache(lib, rng, [400, 390], [n, n], H=2, D=64, B=16)
+    clean = c.scales.copy()
+    for at in ([399 // 16], [2, 7], list(range(25))):
+        c.scales = clean.copy()
+        c.scales[c.table[0, at], 1] = bad
+        c.upload()
+        for options in ({}, {"window": 150}, {"causal": False}):
+            q, out, lse = c.attend(queries(rng, c.T, 4, 64), dtype, **options)
+            keep, c.scales = c.scales, clean
+            want = attention_of(c, q, **options)
+            c.scales = keep
+            i = 400 - n + np.arange(n)[:, None]
+            first = np.array(at)[None, :] * 16
+            sees = np.zeros(c.T, bool)
+            window = options.get("window", 1 << 20)
+            sees[:n] = ((first <= i) & (first + 15 > i - window)).any(1) if options.get("causal", True) else True
+            assert np.isnan(out[sees]).all(), (at, options)
+            check_attention(np.where(sees[:, None, None], want["out"], out), lse, want, dtype, 64, 400, f"{at} {options}")
