@@ -342,8 +342,8 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
                 // ---- weights
                 const bool number = sc.y <= FLT_MAX;         // (values that are none leave NaN in the sums of values alone)
                 const uint32_t vb = __float_as_uint(number ? fmaxf(sc.y, 0x1p-103f) : 1.f);
-                const int ex = min((int)(vb >> 23) - 127, 126);
-                const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+                const int ex = (int)(vb >> 23) - 127;
+                const float down = __uint_as_float(max((uint32_t)(127 - ex) << 23, 0x400000u));   // (2^-127 is a subnormal)
                 const float frac = number ? sc.y * down : __int_as_float(0x7fffffff);
                 const float a0 = sc.x * qa[0], a1 = sc.x * qa[1], fex = (float)ex;
                 float e0[4], e1[4];                          // rows g and g + 8 (SPLIT: e0 alone)

@@ -133,6 +133,22 @@ def test_blocks_of_zeros_among_others_at_length(lib, dtype, n, exponents):
         check_attention(out, lse, attention_of(c, q, **options), dtype, 64, 3000)
 
 
+@pytest.mark.parametrize("G", [1, 40])
+def test_value_scales_up_to_the_largest_number(lib, G):
+    """Values of 0 and the largest f32, with weights that come close to where the running reference moves."""
+    rng = np.random.default_rng(81)
+    c = Cache(lib, rng, [512], [1], H=1, D=64, B=128)
+    c.codes[:] = 128
+    c.codes[c.table[0, 1:], 0, 0, :, 0] = 228
+    c.codes[:, 1] = rng.integers(128, 130, c.codes[:, 1].shape)
+    c.scales[:, 0], c.scales[:, 1] = 7.9999 / 100 / np.log2(np.e), np.finfo(np.float32).max
+    c.upload()
+    q = np.zeros((1, G, 64))
+    q[:, :, 0] = 1.0
+    q, out, lse = c.attend(q, "float32", scale=1.0)
+    check_attention(out, lse, attention_of(c, q, scale=1.0), "float32", 64, 512)
+
+
 @pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
 @pytest.mark.parametrize("n", [1, 3, 150])
 @pytest.mark.parametrize("bad", [np.nan, np.inf])
