@@ -75,6 +75,9 @@ __device__ __forceinline__ bool kv8_wait(uint64_t* bar, uint32_t parity, volatil
 
 __device__ __forceinline__ float kv8_none() { return __int_as_float(0xff800000); }
 
+// The power of two that takes a row of queries' largest element to 2^14 .. 2^15, in f16's range (below 2^-112: less far).
+__device__ __forceinline__ int kv8_power(float most) { return min(max(141 - (int)(__float_as_uint(most) >> 23), -113), 126); }
+
 // Where row r of a sequence's head goes in out; its place in lse.
 __device__ __forceinline__ int64_t kv8_out_row(const Kv8Attention& a, int q0, int head, int r, int64_t* lse) {
     const int token = q0 + r / a.G, h = head * a.G + r % a.G;

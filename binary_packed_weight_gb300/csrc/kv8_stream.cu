@@ -268,8 +268,7 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
             }
 #pragma unroll
             for (int d = 1; d < 8; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-            // a power of two that takes the row's largest element to 2^14 .. 2^15
-            const int e = min(max(141 - (int)(__float_as_uint(most) >> 23), -112), 126);
+            const int e = kv8_power(most);
             const float up = __uint_as_float((uint32_t)(e + 127) << 23);
             if (mine) {
                 if ((lane & 7) == 0) sm.qa[r] = a.scale * __uint_as_float((uint32_t)(127 - e) << 23);

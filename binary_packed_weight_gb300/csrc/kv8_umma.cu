@@ -393,7 +393,7 @@ __device__ __forceinline__ int load_queries(const Kv8Attention& a, Shared<T, D>&
             for (int d = 0; d < DEEP; ++d) most[d] = fmaxf(most[d], __shfl_xor_sync(0xffffffffu, most[d], k));
 #pragma unroll
         for (int d = 0; d < DEEP; ++d) {
-            e[d] = min(max(141 - (int)(__float_as_uint(most[d]) >> 23), -112), 126);
+            e[d] = kv8_power(most[d]);
             const int of = __shfl_sync(0xffffffffu, e[d], (lane - (p0 + d) * RPP) * LPR & 31);
             if (lane / RPP == p0 + d) power = of;
         }

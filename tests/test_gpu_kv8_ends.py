@@ -174,3 +174,19 @@ def test_values_that_are_no_numbers_leave_the_sum(lib, dtype, n, bad):
             sees[:n] = ((first <= i) & (first + 15 > i - window)).any(1) if options.get("causal", True) else True
             assert np.isnan(out[sees]).all(), (at, options)
             check_attention(np.where(sees[:, None, None], want["out"], out), lse, want, dtype, 64, 400, f"{at} {options}")
+
+
+# ----------------------------------------------------------- queries at the ends ----
+@pytest.mark.parametrize("n", [1, 40])
+def test_queries_up_to_the_largest_number(lib, n):
+    """Rows whose largest element is the largest f32; the keys' scales and the factor keep the scores small."""
+    rng = np.random.default_rng(76)
+    c = Cache(lib, rng, [100], [n], H=1, D=64, B=16)
+    c.scales[:, 0] *= np.float32(2.0 ** -60)
+    c.upload()
+    q = np.clip(queries(rng, n, 2, 64), -6, 6)
+    q[:, :, 7], q[:, 1, 9] = 6.0, -6.0
+    q = q / 6.0 * float(np.finfo(np.float32).max)
+    scale = float(np.float32(0.75 * 2.0 ** -67))
+    q, out, lse = c.attend(q, "float32", scale=scale)
+    check_attention(out, lse, attention_of(c, q, scale=scale), "float32", 64, 100)
