@@ -271,7 +271,9 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
             const int e = kv8_power(most);
             const float up = __uint_as_float((uint32_t)(e + 127) << 23);
             if (mine) {
-                if ((lane & 7) == 0) sm.qa[r] = a.scale * __uint_as_float((uint32_t)(127 - e) << 23);
+                // (a row that has an Inf is none of numbers: its scores might all be -Inf, as if it saw no token)
+                if ((lane & 7) == 0)
+                    sm.qa[r] = most <= FLT_MAX ? a.scale * __uint_as_float((uint32_t)(127 - e) << 23) : __int_as_float(0x7fffffff);
                 const int half = SPLIT ? 0 : r >> 3, to = (r & 7) * 4 + d0 / (D / 4), in_quarter = d0 % (D / 4);
 #pragma unroll
                 for (int i = 0; i < EL; i += 2) {

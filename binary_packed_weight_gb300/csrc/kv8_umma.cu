@@ -333,6 +333,8 @@ __device__ __forceinline__ float tile_weights_some(uint32_t s_addr, const float4
 // A warp's 32 rows of queries, scaled by a power of two to 2^14 .. 2^15, in the layout of an MMA operand (the scores of
 // the rows before are there, so nobody reads those any more).  Returns the power of the lane's row.  Raw pieces
 // of 8 elements are copied to where their f16 values (f32: first and second parts) go, and converted in place.
+// A row that has a NaN or Inf becomes zeros, and its power NO_NUMBERS: it is NaN at the end if it saw a token.
+constexpr int NO_NUMBERS = 1 << 20;
 template <class T, int D>
 __device__ __forceinline__ int load_queries(const Kv8Attention& a, Shared<T, D>& sm, const Piece& w, int qi,
                                             int warp, int lane) {
@@ -371,7 +373,7 @@ __device__ __forceinline__ int load_queries(const Kv8Attention& a, Shared<T, D>&
 #pragma unroll 1
     for (int p0 = 0; p0 < LPR; p0 += DEEP) {
         uint4 raw[DEEP][F::SPLIT ? 2 : 1];
-        float most[DEEP];
+        uint32_t most[DEEP];
         int e[DEEP];
 #pragma unroll
         for (int d = 0; d < DEEP; ++d) {
@@ -383,28 +385,29 @@ __device__ __forceinline__ int load_queries(const Kv8Attention& a, Shared<T, D>&
 #pragma unroll
         for (int d = 0; d < DEEP; ++d) {
             const T* u = reinterpret_cast<const T*>(raw[d]);
-            most[d] = 0.f;
+            most[d] = 0;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) most[d] = fmaxf(most[d], fabsf(kv8_wide(u[k])));
+            for (int k = 0; k < 8; ++k) most[d] = max(most[d], __float_as_uint(kv8_wide(u[k])) & 0x7fffffffu);
         }
 #pragma unroll
         for (int k = 1; k < LPR; k <<= 1)
 #pragma unroll
-            for (int d = 0; d < DEEP; ++d) most[d] = fmaxf(most[d], __shfl_xor_sync(0xffffffffu, most[d], k));
+            for (int d = 0; d < DEEP; ++d) most[d] = max(most[d], __shfl_xor_sync(0xffffffffu, most[d], k));
 #pragma unroll
         for (int d = 0; d < DEEP; ++d) {
-            e[d] = kv8_power(most[d]);
+            e[d] = most[d] < 0x7f800000u ? kv8_power(__uint_as_float(most[d])) : NO_NUMBERS;
             const int of = __shfl_sync(0xffffffffu, e[d], (lane - (p0 + d) * RPP) * LPR & 31);
             if (lane / RPP == p0 + d) power = of;
         }
 #pragma unroll
         for (int d = 0; d < DEEP; ++d) {
             const T* u = reinterpret_cast<const T*>(raw[d]);
+            const bool numbers = e[d] != NO_NUMBERS;
             const float up = copysignf(__uint_as_float((uint32_t)(e[d] + 127) << 23), a.scale);
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float x0 = kv8_wide(u[2 * k]) * up, x1 = kv8_wide(u[2 * k + 1]) * up;
+                const float x0 = numbers ? kv8_wide(u[2 * k]) * up : 0.f, x1 = numbers ? kv8_wide(u[2 * k + 1]) * up : 0.f;
                 hi[k] = pack_half2(x0, x1);
                 if (F::SPLIT) lo[k] = rest_half2(x0, x1, hi[k]);
             }
@@ -852,7 +855,7 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
             const int pos = w.len - w.n + (live ? r : w.tile * ROWS) / a.G;
             const int row_hi = a.causal ? min(w.len, pos + 1) : w.len;
             const int row_lo = a.window ? max(pos - a.window + 1, 0) : 0;
-            const float qa = fabsf(a.scale) * __uint_as_float((uint32_t)(127 - power) << 23);
+            const float qa = power == NO_NUMBERS ? -1.f : fabsf(a.scale) * __uint_as_float((uint32_t)(127 - power) << 23);
             whole = w.whole;
             out = static_cast<T*>(a.out) + kv8_out_row(a, w.q0, w.head, live ? r : 0, &at_lse);
             part = parts + ((size_t)cta * 2 + w.part) * kv8_part_floats(ROWS, D);
@@ -909,6 +912,10 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                 if (lane == 0) mbar_arrive(&sm.p_full[qi]);
             }
             if (!ok) break;
+            if (qa < 0.f) {                                  // (a row of zeros, of no numbers)
+                if (l != 0.f) l = __int_as_float(0x7fffffff);
+                if (own[0] != 0.f) own[0] = __int_as_float(0x7fffffff);
+            }
         }
     }
     tc_fence_before();

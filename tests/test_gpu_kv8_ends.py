@@ -190,3 +190,44 @@ def test_queries_up_to_the_largest_number(lib, n):
     scale = float(np.float32(0.75 * 2.0 ** -67))
     q, out, lse = c.attend(q, "float32", scale=scale)
     check_attention(out, lse, attention_of(c, q, scale=scale), "float32", 64, 100)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("G", [1, 5, 40])
+def test_queries_that_are_no_numbers_and_see_no_token(lib, dtype, G):
+    """A row that sees no token (of a table without blocks, of a length of zero) has 0 and -Inf whatever it holds."""
+    rng = np.random.default_rng(82)
+    c = Cache(lib, rng, [300, 0, 300], [1] * 3, H=1, D=64, B=16)
+    c.table[0] = -1
+    c.table[2, 3:7] = len(c.codes)
+    c.upload()
+    q = queries(rng, 3, G, 64)
+    q[:2, -1] = np.nan
+    got, out, lse = c.attend(q, dtype)
+    assert (out[:2] == 0).all() and np.isneginf(lse[:2]).all()
+    check_attention(out, lse, attention_of(c, np.nan_to_num(got)), dtype, 64, 300)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("G", [1, 5, 40])
+@pytest.mark.parametrize("scale", [0.1, -0.1, 0.0])
+def test_infinite_queries_are_no_numbers(lib, dtype, G, scale):
+    """An Inf in q leaves NaN in its row whatever signs the codes have, and 0 where the row sees no token."""
+    rng = np.random.default_rng(77)
+    lens = [1, 1, 1, 40, 0, 33]
+    c = Cache(lib, rng, lens, [1] * 6, H=1, D=64, B=16)
+    c.codes[c.table[0, 0], 0, 0, 0, 5] = 1                    # of a sign each, and none
+    c.codes[c.table[1, 0], 0, 0, 0, 5] = 255
+    c.codes[c.table[2, 0], 0, 0, 0, 5] = 128
+    c.codes[c.table[3], 0, 0, :, 5] = 90                      # one sign in all tokens
+    c.table[5] = -1
+    c.upload()
+    for bad in (np.inf, -np.inf):
+        q = queries(rng, 6, G, 64)
+        q[:, -1, 5] = bad
+        got, out, lse = c.attend(q, dtype, scale=scale)
+        assert np.isnan(out[:4, -1]).all() and np.isnan(lse[:4, -1]).all()
+        assert (out[4:, -1] == 0).all() and np.isneginf(lse[4:, -1]).all()
+        if G > 1:
+            want = attention_of(c, got[:, :-1], scale=scale)
+            check_attention(out[:, :-1], lse[:, :-1], want, dtype, 64, 40)
