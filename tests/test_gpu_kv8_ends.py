@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 
 from kv8_util import Cache, attention_of, check_attention, queries
+from oracle import kv8
 
 pytestmark = pytest.mark.gpu
 
@@ -231,3 +232,82 @@ def test_infinite_queries_are_no_numbers(lib, dtype, G, scale):
         if G > 1:
             want = attention_of(c, got[:, :-1], scale=scale)
             check_attention(out[:, :-1], lse[:, :-1], want, dtype, 64, 40)
+
+
+# ------------------------------------------------------- offsets that move or lie ----
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_captured_writes_follow_the_offsets(lib, dtype):
+    """Captured once; offsets and lengths move on the GPU between replays."""
+    import torch
+    from test_gpu_kv8 import host, tokens
+    rng = np.random.default_rng(78)
+    c = Cache(lib, rng, [80, 80, 80], [30, 20, 10], H=2, D=64, B=16)
+    k, v = tokens(rng, 60, 2, 64, dtype), tokens(rng, 60, 2, 64, dtype)
+    x = np.stack((host(k), host(v)))
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+
+    def step():
+        lib.kv8_write(c.cache, c.batch, k, v)
+        lib.kv8_read(c.cache, c.batch, ko, vo)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for offsets, lens in (([0, 30, 50, 60], [80, 80, 80]), ([0, 1, 2, 3], [33, 80, 1]), ([5, 5, 40, 57], [10, 70, 17]),
+                          ([0, 60, 60, 60], [64, 3, 0])):
+        c.upload()
+        c.d["offsets"].copy_(torch.tensor(offsets, dtype=torch.int32))
+        c.d["lens"].copy_(torch.tensor(lens, dtype=torch.int32))
+        ko.fill_(9.0), vo.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = kv8.write(c.codes, c.scales, c.table, np.array(offsets), np.array(lens), x)
+        codes, scales = c.on_gpu()
+        assert np.array_equal(codes, want[0]) and np.array_equal(scales, want[1])
+        values = kv8.values(codes, scales)
+        back = np.full((2, 60, 2, 64), 9.0)
+        for s in range(3):
+            for row, _, b, at in kv8.tokens_of(c.table, offsets, lens, len(codes), 16, s):
+                back[:, row] = values[b, :, :, at]
+        for got, w in zip((ko, vo), back):
+            assert torch.equal(got.cpu(), torch.from_numpy(w).float().to(got.dtype))
+    lib.device_status()
+
+
+def test_offsets_and_lengths_out_of_range_touch_their_own_blocks_alone(lib):
+    """Clamped to the rows and the table; what that leaves is written and read, and nothing else."""
+    import torch
+    from test_gpu_kv8 import host, tokens
+    rng = np.random.default_rng(79)
+    c = Cache(lib, rng, [48] * 5, [8] * 5, H=2, D=64, B=16, spare=4)
+    T = c.T
+    k, v = tokens(rng, T, 2, 64, "float32"), tokens(rng, T, 2, 64, "float32")
+    x = np.stack((host(k), host(v)))
+    offsets, lens = [-7, 9, 4, 12, 1 << 30, -(1 << 31)], [1 << 30, 48, 5, (1 << 31) - 1, 48]
+    c.d["offsets"].copy_(torch.tensor(offsets, dtype=torch.int32))
+    c.d["lens"].copy_(torch.tensor(lens, dtype=torch.int32))
+    codes, scales = c.codes, c.scales
+    back = np.full((2, T, 2, 64), 9.0)
+    some = []
+    for s in range(5):
+        a = min(max(offsets[s], 0), T)
+        o, l = np.array([a, min(max(offsets[s + 1], a), T)]), np.array([min(max(lens[s], 0), 48)])
+        some.append((s, o, l))
+        codes, scales = kv8.write(codes, scales, c.table[s:s + 1], o, l, x)
+    assert sum(o[1] - o[0] for _, o, _ in some) == 9 + 8 + T - 12
+    lib.kv8_write(c.cache, c.batch, k, v)
+    got = c.on_gpu()
+    assert np.array_equal(got[0], codes) and np.array_equal(got[1], scales)
+    values = kv8.values(codes, scales)
+    taken = {}
+    for s, o, l in some:
+        for row, t, b, at in kv8.tokens_of(c.table[s:s + 1], o, l, len(codes), 16, 0):
+            taken.setdefault(row, []).append(values[b, :, :, at])
+    ko, vo = torch.full_like(k, 9.0), torch.full_like(v, 9.0)
+    lib.kv8_read(c.cache, c.batch, ko, vo)
+    lib.device_status()
+    for kv, got in enumerate((host(ko), host(vo))):
+        for row in range(T):                                  # (an element of two ranges' row is either's)
+            allowed = [w[kv].astype(np.float32) for w in taken.get(row, [np.full((2, 2, 64), 9.0)])]
+            assert np.any([got[row] == w for w in allowed], 0).all(), (kv, row)
