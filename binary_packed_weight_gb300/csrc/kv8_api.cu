@@ -92,9 +92,10 @@ tq2_status kv8_attention(const kv8_cache* c, const kv8_batch* b, const void* q, 
     const tq2_status bad = view(c, b, dtype, T, "kv8_attention", &a.c);
     if (bad != TQ2_OK) return bad;
     // (a row's position less the window, each of 2^30 at most, is a number of 32 bits)
-    if (Hq < c->heads || Hq % c->heads || T > ((int64_t)1 << 30) || T * Hq >= ((int64_t)1 << 31))
+    // (and so is the end of the last, part-full tile of rows)
+    if (Hq < c->heads || Hq % c->heads || T > ((int64_t)1 << 30) || T * Hq > ((int64_t)1 << 31) - 512)
         return (tq2_status)set_error(TQ2_ESHAPE,
-                                     "kv8_attention: Hq=%d must be a multiple of heads=%d with T <= 2^30 and T*Hq < 2^31", Hq,
+                                     "kv8_attention: Hq=%d must be a multiple of heads=%d with T <= 2^30 and T*Hq <= 2^31 - 512", Hq,
                                      c->heads);
     if (!std::isfinite(scale) || (causal != 0 && causal != 1) || window < 0 || (window && !causal) || max_q < 0)
         return (tq2_status)set_error(TQ2_EINVAL,

@@ -1,0 +1,16 @@
+"""Host-side refusals of the 8-bit cache at the ends of the ranges, through the C ABI and the binding.
+
+As in test_abi_checks_kv8.py, the made-up addresses are never dereferenced and the cases run only on
+machines without a GPU.
+"""
+import pytest
+
+from test_abi_checks_kv8 import TQ2_EINVAL, TQ2_ESHAPE, bpw, call, structs  # noqa: F401 (bpw is a fixture)
+
+
+def test_rows_whose_last_tile_ends_past_32_bits(bpw):  # noqa: F811
+    one = structs(bpw, heads=1)
+    for T, Hq in (((1 << 30) - 128, 2), ((1 << 30) - 255, 2), ((1 << 31) // 64 - 4, 64)):
+        assert (1 << 31) - 512 < T * Hq < 1 << 31
+        assert call(bpw, "attention", *one, T=T, Hq=Hq) == TQ2_ESHAPE
+        assert "2^31" in bpw.load().tq2_last_error().decode()
