@@ -106,6 +106,9 @@ tq2_status kv8_attention(const kv8_cache* c, const kv8_batch* b, const void* q, 
     if (((double)T * (Hq / c->heads) / 128 + b->seqs) * c->heads * ((double)b->width * c->tokens / 128 + 1) >= 0x1p38)
         return (tq2_status)set_error(TQ2_ESHAPE, "kv8_attention: T=%lld rows over tables of %lld tokens are too many for one call",
                                      (long long)T, (long long)b->width * c->tokens);
+    // each of a CTA's warps walks sequences without rows by itself, and none may be a second ahead of the others
+    if (b->seqs > 1 << 24)
+        return (tq2_status)set_error(TQ2_ESHAPE, "kv8_attention: %d sequences are too many for one call", b->seqs);
     if (T == 0) return TQ2_OK;
     if (!q || !out) return (tq2_status)set_error(TQ2_EINVAL, "kv8_attention: null pointer");
     if (off_element(q, element_size(dtype)) || off_element(out, element_size(dtype)) || off_element(lse, 4))

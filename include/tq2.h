@@ -718,7 +718,7 @@ TQ2_API tq2_status kv8_read(const kv8_cache* c, const kv8_batch* b, void* k, int
  *           sequence are left as they are, in lse too.
  *   lse     DEVICE float[T][Hq] or NULL.
  *   Hq      a multiple of heads, T <= 2^30, T * Hq <= 2^31 - 512, and fewer than 2^38 tiles of 128 rows (T * Hq / heads)
- *           by 128 tokens of the tables.  Else TQ2_ESHAPE.
+ *           by 128 tokens of the tables; seqs <= 2^24.  Else TQ2_ESHAPE.
  *   scale   finite;  causal 0 or 1;  window >= 0, 0 unless causal.  Else TQ2_EINVAL.
  *   max_q   a bound of the sequences' rows that the choice of kernels goes by (0: T); results
  *           of longer ones are right too, but slower.

@@ -14,3 +14,9 @@ def test_rows_whose_last_tile_ends_past_32_bits(bpw):  # noqa: F811
         assert (1 << 31) - 512 < T * Hq < 1 << 31
         assert call(bpw, "attention", *one, T=T, Hq=Hq) == TQ2_ESHAPE
         assert "2^31" in bpw.load().tq2_last_error().decode()
+
+
+def test_more_sequences_than_one_call_walks(bpw):  # noqa: F811
+    for seqs in ((1 << 24) + 1, (1 << 31) - 1):
+        assert call(bpw, "attention", *structs(bpw, seqs=seqs)) == TQ2_ESHAPE
+        assert "sequences are too many" in bpw.load().tq2_last_error().decode()
