@@ -97,9 +97,10 @@ tq2_status kv8_attention(const kv8_cache* c, const kv8_batch* b, const void* q, 
         return (tq2_status)set_error(TQ2_ESHAPE,
                                      "kv8_attention: Hq=%d must be a multiple of heads=%d with T <= 2^30 and T*Hq <= 2^31 - 512", Hq,
                                      c->heads);
-    if (!std::isfinite(scale) || (causal != 0 && causal != 1) || window < 0 || (window && !causal) || max_q < 0)
+    const float scale2 = scale * 1.4426950408889634f;        // powers of 2 from here on
+    if (!std::isfinite(scale2) || (causal != 0 && causal != 1) || window < 0 || (window && !causal) || max_q < 0)
         return (tq2_status)set_error(TQ2_EINVAL,
-                                     "kv8_attention: need a finite scale, causal 0 or 1, window >= 0 (0 unless causal), "
+                                     "kv8_attention: need a finite scale (times log2(e) too), causal 0 or 1, window >= 0 (0 unless causal), "
                                      "max_q >= 0 (scale=%g causal=%d window=%lld max_q=%lld)",
                                      (double)scale, causal, (long long)window, (long long)max_q);
     // tiles of 128 rows by 128 tokens are counted in 32 bits a CTA
@@ -129,7 +130,7 @@ tq2_status kv8_attention(const kv8_cache* c, const kv8_batch* b, const void* q, 
     a.G = Hq / c->heads;
     const int64_t size = (int64_t)element_size(dtype);
     a.qvec = (((int64_t)(uintptr_t)q | qt * size | qh * size) & 15) == 0;
-    a.scale = scale * 1.4426950408889634f;                    // powers of 2 from here on
+    a.scale = scale2;
     a.causal = causal;
     a.window = window < ((int64_t)1 << 30) ? (int)window : 0;  // no sequence is longer
     // Rows of a sequence (queries * G): few go the streaming way, many the tensor cores'.  Which sequences have how

@@ -719,7 +719,7 @@ TQ2_API tq2_status kv8_read(const kv8_cache* c, const kv8_batch* b, void* k, int
  *   lse     DEVICE float[T][Hq] or NULL.
  *   Hq      a multiple of heads, T <= 2^30, T * Hq <= 2^31 - 512, and fewer than 2^38 tiles of 128 rows (T * Hq / heads)
  *           by 128 tokens of the tables; seqs <= 2^24.  Else TQ2_ESHAPE.
- *   scale   finite;  causal 0 or 1;  window >= 0, 0 unless causal.  Else TQ2_EINVAL.
+ *   scale   finite, and times log2(e) too;  causal 0 or 1;  window >= 0, 0 unless causal.  Else TQ2_EINVAL.
  *   max_q   a bound of the sequences' rows that the choice of kernels goes by (0: T); results
  *           of longer ones are right too, but slower.
  * f16 and bf16 queries and the codes enter the products exactly (elements below 2^-29 of their

@@ -20,3 +20,9 @@ def test_more_sequences_than_one_call_walks(bpw):  # noqa: F811
     for seqs in ((1 << 24) + 1, (1 << 31) - 1):
         assert call(bpw, "attention", *structs(bpw, seqs=seqs)) == TQ2_ESHAPE
         assert "sequences are too many" in bpw.load().tq2_last_error().decode()
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -3.4e38])
+def test_scales_that_no_power_of_two_has(bpw, scale):  # noqa: F811
+    assert call(bpw, "attention", *structs(bpw), scale=scale) == TQ2_EINVAL
+    assert "finite scale" in bpw.load().tq2_last_error().decode()
