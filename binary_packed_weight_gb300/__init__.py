@@ -347,7 +347,7 @@ def _rows(t, rows, cols, where, name):
     ld, inner = t.stride()
     if inner != 1 and cols > 1:
         raise ValueError(f"{where}: the rows of {name} must be contiguous")
-    return ld if rows > 1 and cols > 1 else max(ld, cols)
+    return ld if rows > 1 else max(ld, cols)               # (a lone row's stride says nothing)
 
 
 def _plane(t, shape, dtype, where, name, host=False):

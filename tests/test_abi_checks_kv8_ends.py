@@ -26,3 +26,27 @@ def test_more_sequences_than_one_call_walks(bpw):  # noqa: F811
 def test_scales_that_no_power_of_two_has(bpw, scale):  # noqa: F811
     assert call(bpw, "attention", *structs(bpw), scale=scale) == TQ2_EINVAL
     assert "finite scale" in bpw.load().tq2_last_error().decode()
+
+
+class OnGpu:
+    """What the binding asks of a tensor, of a tensor that is on no GPU."""
+
+    def __init__(self, t):
+        self.t, self.shape, self.dtype, self.is_cuda = t, t.shape, t.dtype, True
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_rows_of_one_element_that_are_one_and_the_same(bpw):  # noqa: F811
+    """A table of one block a sequence, the same for all: its rows' stride of 0 is refused like any that is below the width."""
+    import torch
+    table, offsets, lens = torch.zeros((1, 1), dtype=torch.int32), torch.zeros(6, dtype=torch.int32), torch.zeros(5, dtype=torch.int32)
+    b = bpw.KV8Batch(*(OnGpu(t) for t in (table.expand(5, 1), offsets, lens)))
+    assert b._c.ld == 0
+    c, _ = structs(bpw)
+    assert call(bpw, "attention", c, b._at) == TQ2_ESHAPE
+    wide = torch.zeros((5, 7), dtype=torch.int32)
+    assert bpw.KV8Batch(*(OnGpu(t) for t in (wide[:, 2:3], offsets, lens)))._c.ld == 7
+    assert bpw.KV8Batch(*(OnGpu(t) for t in (wide[:1, 2:3], offsets[:2], lens[:1])))._c.ld == 7
+    assert bpw.KV8Batch(*(OnGpu(t) for t in (table.expand(1, 1), offsets[:2], lens[:1])))._c.ld == 1
