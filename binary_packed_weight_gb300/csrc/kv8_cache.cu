@@ -7,6 +7,8 @@
 // has one exchange of the maximum between a CTA's loads and its stores, which the SM's other CTAs
 // cover in part, and 18 instructions a value: 16384 tokens at 3.8 TB/s (22 us, issue slots 74 % busy).
 // A decoded token: 4.4 us, launch and four dependent reads.
+#include <cfloat>
+
 #include "kv8.cuh"
 
 namespace tq2 {
@@ -114,7 +116,7 @@ kv8_write_kernel(const Kv8View c, const T* k, const T* v, int64_t kt, int64_t kh
                                                 : most >= SMALLEST ? __fdiv_rn(most, 127.f) : 0.f;
         const bool bad = isnan(before) || isnan(fresh);
         const float now = bad ? __uint_as_float(0x7fffffffu) : fmaxf(before, fresh);
-        const float inverse = now > 0.f ? __fdiv_rn(1.f, now) : 0.f;
+        const float inverse = now > 0.f ? fminf(__fdiv_rn(1.f, now), FLT_MAX) : 0.f;
         const bool coarser = lo > 0 && now > before;
         const float ratio = coarser ? __fdiv_rn(before, now) : 1.f;
         if (threadIdx.x == 0 && (lo == 0 || bad || coarser)) *where = now;

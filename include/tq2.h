@@ -679,7 +679,7 @@ typedef struct {
  *     d = max(d0, M / 127)   (M below 2^-96 counts as 0)
  *     c = 128 + clamp(rint(x * (1 / d)), -127, 127)          of the new tokens
  *     c = 128 + rint((c - 128) * (d0 / d))                   of those before, where d > d0
- * (d = 0: c = 128).  Codes past the new tokens keep what they hold, which nothing reads.
+ * (d = 0: c = 128; 1 / d is the largest f32 at most).  Codes past the new tokens keep what they hold, which nothing reads.
  * A NaN or Inf among the new tokens leaves the block's scale NaN: every value of that
  * block and head reads as NaN until a write begins the block anew.
  *

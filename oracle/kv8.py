@@ -45,7 +45,8 @@ def write(codes, scales, table, offsets, lens, x):
                     if at[0] > 0 and d > d0:
                         old = codes[b, kv, h, :at[0]].astype(F) - F(128)
                         codes[b, kv, h, :at[0]] = np.rint(old * F(d0 / d)) + F(128)
-                    inv = F(F(1) / d) if d > 0 else F(0)
+                    with np.errstate(over="ignore"):
+                        inv = min(F(F(1) / d), np.finfo(F).max) if d > 0 else F(0)
                     codes[b, kv, h, at] = np.clip(np.rint(new * inv), -127, 127) + F(128)
                     scales[b, kv, h] = d
     return codes, scales

@@ -234,6 +234,22 @@ def test_infinite_queries_are_no_numbers(lib, dtype, G, scale):
             check_attention(out[:, :-1], lse[:, :-1], want, dtype, 64, 40)
 
 
+# ----------------------------------------------------------------- small scales ----
+def test_tokens_behind_others_of_the_smallest_scales(lib):
+    """A block whose scale is a subnormal number (no write makes one): zeros stay zeros beside its tokens."""
+    from test_gpu_kv8 import tokens, write_and_check
+    rng = np.random.default_rng(83)
+    c = Cache(lib, rng, [20, 20, 20], [3, 3, 3], H=2, D=64, B=32)
+    c.scales[c.table[:, 0]] = np.array([1e-40, 1e-45, 2.0 ** -126], np.float32)[:, None, None]
+    c.upload()
+    k, v = tokens(rng, 9, 2, 64, "float32"), tokens(rng, 9, 2, 64, "float32")
+    k.zero_()
+    v *= 2.0 ** -110
+    v[:, :, ::3] = 0.0
+    write_and_check(lib, c, k, v)
+    assert (c.codes[c.table[:, 0], 0][:, :, 17:20] == 128).all()
+
+
 # ------------------------------------------------------- offsets that move or lie ----
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 def test_captured_writes_follow_the_offsets(lib, dtype):
