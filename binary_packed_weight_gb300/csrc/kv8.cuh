@@ -114,6 +114,13 @@ __device__ __forceinline__ uint32_t kv8_pair(uint32_t w) {
 }
 
 // ------------------------------------------------------------ launches ----
+inline int kv8_sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 152;
+    return n;
+}
+
 // Keys and values of a write or a read: strides in elements.
 struct Kv8Rows {
     void *k, *v;

@@ -30,7 +30,7 @@ constexpr int ctas() { return PER * sizeof(T) <= 4 ? 5 : PER * sizeof(T) <= 8 ? 
 // 5.6 us, so 4.1).
 dim3 grid_of(const Kv8View& c) {
     const int64_t most = 2 * (int64_t)c.T / ((int64_t)c.seqs << c.logB) + 1;
-    const int64_t fill = (int64_t)(152 * 32) / ((int64_t)c.seqs * c.H * 2) + 1;
+    const int64_t fill = (int64_t)kv8_sm_count() * 32 / ((int64_t)c.seqs * c.H * 2) + 1;
     return dim3((unsigned)c.seqs, (unsigned)(c.H * 2), (unsigned)(most < fill ? most : fill));
 }
 

@@ -162,11 +162,4 @@ kv8_join_kernel(const __grid_constant__ Kv8Attention a, const float* parts, cons
     }
 }
 
-inline int kv8_sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 152;
-    return n;
-}
-
 }  // namespace tq2
