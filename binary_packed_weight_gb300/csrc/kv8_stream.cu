@@ -103,7 +103,6 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
     // weights of f16 outputs in two parts too: one part's rounding is as large as the output's own
     constexpr bool TWO = !SPLIT && std::is_same<T, __half>::value;
     constexpr int RM = SPLIT ? 8 : 16;
-    constexpr int KS = D / 16;                               // k steps of q . c
     constexpr int NT = D / 8;                                // column tiles of the output
     extern __shared__ __align__(1024) uint8_t raw[];
     Shared<D>& sm = *reinterpret_cast<Shared<D>*>(raw);
@@ -581,10 +580,10 @@ cudaError_t run(const Kv8Attention& a, void* scratch, cudaStream_t st) {
     g_launched.store(true, std::memory_order_release);
     e = launch_pdl(kv8_stream_kernel<T, D, SPLIT>, dim3(grid), dim3(THREADS), sizeof(Shared<D>), st, a, parts, joints);
     if (e != cudaSuccess) return e;
-    // Few tiles of rows leave each of them many pieces: eight warps a row where a tile has twelve or more (4 heads of
-    // 128, G = 8, us with eight and four: 1 sequence of 131072 tokens 38 and 41, 4 of 32768 16 and 18.5, 8 of 16384
-    // 21 and 20; 64 of up to 8192, 8 heads, 108 and 105).  T counts the tokens of all sequences, each of which adds at
-    // most one tile that is part full.
+    // Few tiles of rows leave each of them many pieces: eight warps a row where there are at most a twelfth as many tiles
+    // as CTAs (4 heads of 128, G = 8, bf16, us with eight and four: 1 sequence of 131072 tokens 38 and 41, 4 of 32768 16
+    // and 18.5, 8 of 16384 21 and 20; 64 of up to 8192, 8 heads, 108 and 105).  What is counted is a bound, the
+    // tokens of all sequences and a part-full tile of each: one decoded token a sequence with G >= RM counts twice.
     const int64_t tiles = (int64_t)a.c.H * ((int64_t)a.c.T * a.G / RM + a.c.seqs);
     const Kv8Joint* j = joints;
     const float* p = parts;
