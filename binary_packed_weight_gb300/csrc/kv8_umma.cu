@@ -3,7 +3,7 @@
 //
 // Mathematics: as the streaming path (kv8_stream.cu), with the whole weight
 // 2^(w_t - m), w_t = (scale log2(e) ks) (q . c) + log2 vs, in f16, and
-// l = sum 2^(w_t - m) 2^x / vs, x the exponent of the first vs.  ks and vs are constant over 16 columns, so per score that is
+// l = sum 2^(w_t - m) 2^x / vs, x the exponent of the first vs (blocks of zeros: vs 2^(x - 40) in both).  ks and vs are constant over 16 columns, so per score that is
 // half a packed multiply-add, one exponential and half a packed sum.  Where a vs is too far from 2^x for
 // that, a piece's weights have a sum (and exponentials) of their own from there on.
 //
@@ -747,20 +747,20 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                 if (kv == 0 && dw == 0) {
                     const int group = lane & (KT / 16 - 1);
                     const float2 sc = sm.scales[slot][group * 16 / rows_piece];
-                    float4 c = make_float4(sc.x, log2f(sc.y), 1.f / sc.y, 1.f);
-                    if (!(sc.y <= FLT_MAX)) c = make_float4(sc.x, 0.f, 1.f, __int_as_float(0x7fffffff));   // NaN, Inf
-                    if (sc.y < TINY) c = make_float4(sc.x, -103.f, 0x1p103f, 0.f);       // values that are all zeros
-                    if (sc.y < 0.f) c = make_float4(0.f, kv8_none(), 1.f, 0.f);          // no block: nobody sees it
+                    const bool number = sc.y <= FLT_MAX, some = number && sc.y >= TINY;      // (values that are not all zeros)
+                    const float y = some ? log2f(sc.y) : kv8_none();
                     if (i == 0) {
-                        float most = c.y;
+                        float most = y;
 #pragma unroll
                         for (int d = 1; d < KT / 16; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
                         x = most == kv8_none() ? 0 : (int)fminf(floorf(most), 127.f);
                         far = 0;
                     }
-                    // (the sums of a tile with values that are no numbers go apart too)
-                    far = far ? 2 : __any_sync(0xffffffffu, c.y != kv8_none() && !(fabsf(c.y - x) <= KV8_NEAR && c.w <= 1.f));
-                    c.z *= exp2_fast((float)x);
+                    far = far ? 2 : __any_sync(0xffffffffu, !number || (some && fabsf(y - x) > KV8_NEAR));
+                    float4 c = make_float4(sc.x, y, exp2_fast((float)x) / sc.y, 1.f);
+                    if (!some) c = make_float4(sc.x, x - KV8_NEAR, KV8_FAR, 0.f);        // zeros weigh, as little as counts
+                    if (!number) c = make_float4(sc.x, (float)x, 1.f, __int_as_float(0x7fffffff));
+                    if (sc.y < 0.f) c = make_float4(0.f, kv8_none(), 1.f, 0.f);          // no block: nobody sees it
                     if (lane < KT / 16) sm.cons[slot][lane] = c;
                     if (lane == 0) sm.near[slot] = 4 * x + far;
                     __syncwarp();

@@ -725,7 +725,8 @@ TQ2_API tq2_status kv8_read(const kv8_cache* c, const kv8_batch* b, void* k, int
  * f16 and bf16 queries and the codes enter the products exactly (elements below 2^-29 of their
  * row's largest lose bits), f32 queries within 2^-22 of each element and 2^-39 of the row's
  * largest (both: of 2^-112 where that is larger).  Scores have to be in f32's range.  A token's weight times its block's scale is rounded to f16 for bf16 results (2^-11), to two
- * f16 parts for f16 and f32 ones (2^-22), and to 2^-30 of the row's largest at the least.  Sums
+ * f16 parts for f16 and f32 ones (2^-22), and to 2^-30 of the row's largest at the least (where values are
+ * all zeros, a weight times 2^-40 of a neighbour's scale may be the largest).  Sums
  * are f32, results rounded once.  A row of q with NaN or Inf gives NaN in its own row alone; a NaN scale reaches the rows
  * that see a token of its block: out, and lse where it is the keys'.  The order of additions depends on lengths, shapes and the
  * GPU alone, so results are the same from run to run.  Asynchronous; scratch from the

@@ -134,6 +134,26 @@ def test_blocks_of_zeros_among_others_at_length(lib, dtype, n, exponents):
         check_attention(out, lse, attention_of(c, q, **options), dtype, 64, 3000)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("G", [1, 40])
+@pytest.mark.parametrize("gap", [10, 30])
+def test_zeros_that_outweigh_all_others(lib, dtype, G, gap):
+    """A block of zeros whose tokens weigh 2^gap times the others (a first token that draws all attention): what is
+    left of the others is as precise as ever."""
+    rng = np.random.default_rng(84)
+    c = Cache(lib, rng, [512], [1], H=1, D=64, B=128)
+    c.codes[:] = 128
+    c.codes[c.table[0, 0], 0, 0, :, 0] = 228
+    c.codes[:, 1] = rng.integers(1, 256, c.codes[:, 1].shape)
+    c.scales[:, 0], c.scales[:, 1] = gap / 100 / np.log2(np.e), 0.02
+    c.scales[c.table[0, 0], 1] = 0.0
+    c.upload()
+    q = np.zeros((1, G, 64))
+    q[:, :, 0] = 1.0
+    q, out, lse = c.attend(q, dtype, scale=1.0)
+    check_attention(out, lse, attention_of(c, q, scale=1.0), dtype, 64, 512)
+
+
 @pytest.mark.parametrize("G", [1, 40])
 def test_value_scales_up_to_the_largest_number(lib, G):
     """Values of 0 and the largest f32, with weights that come close to where the running reference moves."""
