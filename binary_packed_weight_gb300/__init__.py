@@ -562,7 +562,7 @@ def kv8_read(cache, batch, k, v, stream=None):
 def kv8_attention(cache, batch, q, out, lse=None, scale=None, causal=True, window=0, max_q=None, stream=None):
     """Attention of the sequences' last tokens ``q`` [T, Hq, dim] over the cache into ``out`` [T, Hq, dim] and,
     unless None, ``lse`` float32 [T, Hq] (see include/tq2.h).  scale: dim ** -0.5 if None; max_q: a bound of a
-    sequence's rows, if one is known."""
+    sequence's rows, 1 when decoding (without one, a batch of more than 32 rows in all counts as a prompt, and is slower)."""
     at = "kv8_attention"
     T, Hq, D = q.shape
     if out.dtype is not q.dtype:

@@ -142,8 +142,8 @@ tq2_status kv8_attention(const kv8_cache* c, const kv8_batch* b, const void* q, 
     const int64_t rows = (max_q && max_q < T ? max_q : T) * a.G;
     const double held = 2.0 * b->seqs * b->width * c->tokens * c->heads * c->dim;
     // Warps of the tensor path that a piece of work leaves idle wait for the next one, and no wait may last a second: a
-    // piece of 2^24 tokens takes 0.3 s (f32 0.5), a walk over 2^18 sequences without rows as long.  Beyond those, all
-    // stream, where nothing waits for more than a chunk.
+    // piece of 2^24 tokens takes 0.3 to 0.4 s (where scales are 2^40 apart 0.65, f32 0.7), a walk over 2^18 sequences
+    // without rows as long.  Beyond those, all stream, where nothing waits for more than a chunk.
     const bool longest = (int64_t)b->width * c->tokens > 1 << 24 || b->seqs > 1 << 18;
     const bool few = rows <= KV8_FEW_ROWS || longest;
     a.few = few ? 0x7fffffff : b->seqs == 1 || held <= 32 << 20 ? 0 : KV8_FEW_ROWS;

@@ -5,8 +5,8 @@
 // and the codes, so each is read once.  Both kernels move bytes and little else: 65536 tokens
 // of 8 heads of 128 are read as bf16 at 6.4 TB/s (63 us; 96 % of the measured copy).  The write
 // has one exchange of the maximum between a CTA's loads and its stores, which the SM's other CTAs
-// cover in part, and 18 instructions a value: 16384 tokens at 3.8 TB/s (22 us, issue slots 74 % busy).
-// A decoded token: 4.4 us, launch and four dependent reads.
+// cover in part, and 21 instructions a value: 13518 tokens as bf16 at 3.9 TB/s (21.4 us, issue slots 73 % busy).
+// A decoded token: 4.1 us, launch and four dependent reads.  f32 is read back at 4.1 TB/s (163 us for the tokens above).
 #include <cfloat>
 
 #include "kv8.cuh"

@@ -12,9 +12,10 @@
 // two a row, are exact as well, f32 ones are two f16 parts (and so are their
 // weights), of which an MMA takes both as rows r and r + 8.  Sums are f32.
 //
-// Bound: the bytes of the codes (64 tokens of up to 8192, 8 heads of 128, G = 4, bf16: 102.5 us, 5.1 TB/s or 76 % of the
-// measured copy; 400 warp instructions for 16 tokens' 4 KB keep the issue slots 42 % busy).  One sequence of
-// 131072 tokens, 4 heads: 37 us, 31 of them here and the rest in the join of 76 pieces a head.
+// Bound: the bytes of the codes (64 tokens of up to 8192, 8 heads of 128, G = 4, bf16: 103 us, 5.1 TB/s or 76 % of the
+// measured copy; 400 warp instructions for 16 tokens' 4 KB keep the issue slots 45 % busy).  One sequence of
+// 131072 tokens, 4 heads: 37.6 us, 32 of them here and the rest in the join of 76 pieces a head.  The fence before a stage
+// goes back costs 1 to 2 %.
 // A CTA walks chunks of 64 tokens; all chunks of all sequences and heads are cut over the CTAs by what they cost, so a
 // ragged batch or one long sequence fills the GPU alike.  What a cut divides is joined by a second
 // kernel in the order of the tokens.  TMA brings the chunks into a ring (keys and values of

@@ -21,12 +21,15 @@
 // reads P before the next scores take its place, and scores that are there mean that the
 // last P V is done, so the group may rescale O.
 //
-// Bound: 8192 causal tokens, 8 heads of 128, G = 4, bf16: 514 us, 1.07 PFLOP/s (55 % of the measured
-// peak; tensor pipe 49 %, issue slots 53 %).  A tile of 128 x 256 takes 4000 cycles, its MMAs 2048.  A group's
+// Bound: 8192 causal tokens, 8 heads of 128, G = 4, bf16: 533 us, 1.03 PFLOP/s (53 % of the measured
+// peak; tensor pipe 46 %, issue slots 52 %; f16, with two parts of each weight, 672, f32, with two of queries too and half
+// the rows a CTA, 1326).  A tile of 128 x 256 takes 4100 cycles, its MMAs 2048.  A group's
 // scores, softmax and values follow one another (2 x 512 cycles of MMAs, 600 until their completion is seen,
 // 1700 of softmax beside the other group's and the decoders), and the operands' reads, the decoders' and the copies
-// want shared memory for 2500 of the 4000.  What the instruction cache does not hold costs time in every
-// role, so code that runs once a tile is kept in short loops, and what runs once a piece is read from one list.
+// want shared memory for 2500 of the 4100.  Sums of their own, where scales are 2^40 apart, take twice the time (1110).
+// What the instruction cache does not hold costs time in every role, so code that runs once a tile is kept in short loops,
+// and what runs once a piece is read from one list.  (The code of sums of their own, which such calls never run, costs 2 %;
+// a reference of its own for every row's sum cost 5 to 9.)
 #include <cfloat>
 #include <type_traits>
 

@@ -721,7 +721,8 @@ TQ2_API tq2_status kv8_read(const kv8_cache* c, const kv8_batch* b, void* k, int
  *           by 128 tokens of the tables; seqs <= 2^24.  Else TQ2_ESHAPE.
  *   scale   finite, and times log2(e) too;  causal 0 or 1;  window >= 0, 0 unless causal.  Else TQ2_EINVAL.
  *   max_q   a bound of the sequences' rows that the choice of kernels goes by (0: T); results
- *           of longer ones are right too, but slower.
+ *           of longer ones are right too, but slower.  Give it where it is known: without one, decoded tokens whose
+ *           rows (T * Hq / heads) are more than 32 in all count as a prompt, and run or launch its kernels too.
  * f16 and bf16 queries and the codes enter the products exactly (elements below 2^-29 of their
  * row's largest lose bits), f32 queries within 2^-22 of each element and 2^-39 of the row's
  * largest (both: of 2^-112 where that is larger).  Scores have to be in f32's range.  A token's weight times its block's scale is rounded to f16 for bf16 results (2^-11), to two
