@@ -346,7 +346,8 @@ kv8_stream_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint
                 const int ex = (int)(vb >> 23) - 127;
                 const float down = __uint_as_float(max((uint32_t)(127 - ex) << 23, 0x400000u));   // (2^-127 is a subnormal)
                 const float frac = number ? sc.y * down : __int_as_float(0x7fffffff);
-                const float a0 = sc.x * qa[0], a1 = sc.x * qa[1], fex = (float)ex;
+                const float ks = sc.x <= FLT_MAX ? sc.x : __int_as_float(0x7fffffff);
+                const float a0 = ks * qa[0], a1 = ks * qa[1], fex = (float)ex;
                 float e0[4], e1[4];                          // rows g and g + 8 (SPLIT: e0 alone)
 #pragma unroll
                 for (int n = 0; n < 2; ++n)

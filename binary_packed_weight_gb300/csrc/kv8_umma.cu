@@ -749,7 +749,8 @@ kv8_umma_kernel(const __grid_constant__ Kv8Attention a, float* parts, Kv8Joint* 
                 }
                 if (kv == 0 && dw == 0) {
                     const int group = lane & (KT / 16 - 1);
-                    const float2 sc = sm.scales[slot][group * 16 / rows_piece];
+                    float2 sc = sm.scales[slot][group * 16 / rows_piece];
+                    if (!(sc.x <= FLT_MAX)) sc.x = __int_as_float(0x7fffffff);
                     const bool number = sc.y <= FLT_MAX, some = number && sc.y >= TINY;      // (values that are not all zeros)
                     const float y = some ? log2f(sc.y) : kv8_none();
                     if (i == 0) {

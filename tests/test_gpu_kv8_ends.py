@@ -197,6 +197,25 @@ def test_values_that_are_no_numbers_leave_the_sum(lib, dtype, n, bad):
             check_attention(np.where(sees[:, None, None], want["out"], out), lse, want, dtype, 64, 400, f"{at} {options}")
 
 
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("G", [1, 5, 40])
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_keys_that_are_no_numbers(lib, dtype, G, bad):
+    """A scale of the keys that is no number (Inf counts as none), whatever signs the scores would have."""
+    rng = np.random.default_rng(85)
+    c = Cache(lib, rng, [1, 1, 30, 40], [1] * 4, H=1, D=64, B=16)
+    for s, code in enumerate((1, 255, 90)):                   # scores of one sign alone
+        own = c.table[s][c.table[s] >= 0]
+        c.codes[own, 0], c.scales[own, 0] = code, bad
+    c.upload()
+    q = np.abs(queries(rng, 4, G, 64))
+    q, out, lse = c.attend(q, dtype)
+    assert np.isnan(out[:3]).all() and np.isnan(lse[:3]).all()
+    c.scales[:, 0] = np.where(np.isfinite(c.scales[:, 0]), c.scales[:, 0], 0)
+    want = {k: v[3:] for k, v in attention_of(c, q).items()}
+    check_attention(out[3:], lse[3:], want, dtype, 64, 40)
+
+
 # ----------------------------------------------------------- queries at the ends ----
 @pytest.mark.parametrize("n", [1, 40])
 def test_queries_up_to_the_largest_number(lib, n):
